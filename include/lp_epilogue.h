@@ -87,7 +87,7 @@ extern "C" {
 #define LP_UNUSED_LP_BITS 0x7FC00000u /* lp bits of an unused pair (a quiet NaN) */
 
 /* Element type of the logit block. */
-typedef enum { LP_F32 = 0, LP_BF16 = 1 } lp_dtype;
+typedef enum { LP_F32 = 0, LP_BF16 = 1, LP_F16 = 2 /* attention plans only */ } lp_dtype;
 
 /* Host error codes. */
 enum {
@@ -109,6 +109,9 @@ enum {
 #define LP_STATUS_BAD_GROUP 0x8u /* group_indptr malformed: the run reads and writes nothing else */
 #define LP_STATUS_TIMEOUT 0x10u  /* a bounded device wait expired: outputs are incomplete */
 #define LP_STATUS_BAD_TEMPERATURE 0x20u /* lp_chain_verify: a temperature not in (0, inf): group skipped */
+#define LP_STATUS_BAD_POSITION 0x40u /* lp_norm_rope, lp_kv_append: a position past the rotation table: row skipped */
+#define LP_STATUS_BAD_PAGE 0x80u     /* a page id outside [0, num_pages): not written, read as zeros */
+#define LP_STATUS_BAD_PREFIX 0x100u  /* lp_attend: a malformed prefix: taken as absent */
 
 /* Plan flags. */
 #define LP_PLAN_HOST_STAGING 0x1u     /* also allocate device staging so lp_run_host can be used */
@@ -418,6 +421,161 @@ int lp_plan_tiles_per_row(lp_plan_t plan);
  * LP_EDTYPE, LP_ECAPACITY, LP_ESCRATCH, LP_ECUDA. */
 #define LP_STATIC_SCRATCH_BYTES (4u << 20)
 int lp_run_static(const lp_plan_desc* desc, const lp_io* io, void* stream);
+
+/* ---- Attention of the verify forward ----
+ *
+ * No counterpart in the design pages: the operators that run on the same
+ * verify groups just before the epilogue, in every attention layer of the
+ * target model, with the K and V state that a round reads and commits.
+ *
+ *   lp_norm_rope   each query and key head's RMS norm and position rotation;
+ *   lp_kv_append   the same, with the keys and values going to a paged cache;
+ *   lp_attend      attention of the verify rows over that cache, prefixes that
+ *                  several groups share read and computed once for all.
+ *
+ * State.  Group g owns rows group_indptr[g] .. group_indptr[g+1]-1, as in
+ * lp_bind.  lens[g] counts its committed tokens; row j of the group is token
+ * lens[g] + j.  lp_kv_append writes those tokens and lp_attend reads them;
+ * neither changes lens.  After the epilogue the caller commits the round with
+ * lens[g] += accepted[g] + 1: tokens past lens are never read as committed,
+ * and the next append overwrites them.  lens[g] < 0 marks an idle group (a
+ * slot of a captured batch without a request).
+ *
+ * Cache.  k_cache and v_cache are [num_pages, kv_heads, page_size, head_dim]
+ * each; token t of group g is slot t % page_size of page
+ * block_tables[g][t / page_size].  A shared prefix has a page table of its
+ * own in the same caches; the groups behind it count their own tokens from 0.
+ * Nothing is read from slots past a group's or prefix's tokens that reaches a
+ * result, whatever they hold.
+ *
+ * Status.  These calls OR their LP_STATUS_* bits into *status and do not
+ * reset it (a forward makes them once per layer; the caller clears the word
+ * when it reads it).
+ *
+ * Strides are in elements between rows; the heads of a row are dense (q may
+ * be the columns of a fused projection).  Device pointers throughout; every
+ * call only enqueues, allocates nothing and can be captured in a CUDA graph.
+ * One plan serves one stream at a time.  Host errors: LP_EINVAL, LP_ESHAPE,
+ * LP_EALIGN (a tensor not 16-byte aligned, or a stride that is no multiple of
+ * 8 elements), LP_ECAPACITY, LP_EDTYPE, LP_ECUDA. */
+#define LP_ATTN_MAX_GROUP_ROWS 32 /* largest verify group lp_attend accepts (bits of a row mask) */
+
+typedef struct {
+    int32_t max_rows;         /* capacity: rows per call (>= 1) */
+    int32_t max_groups;       /* capacity: groups per call (>= 1) */
+    int32_t max_group_rows;   /* lp_attend: largest group, 1..LP_ATTN_MAX_GROUP_ROWS */
+    int32_t q_heads;          /* a multiple of kv_heads, at most 128 times it */
+    int32_t kv_heads;
+    int32_t head_dim;         /* 64 or 128 */
+    int32_t page_size;        /* tokens per page: a power of two, 8..256 */
+    int32_t max_pages;        /* columns of block_tables (>= 1) */
+    int32_t max_prefixes;     /* capacity: shared prefixes per call (>= 0) */
+    int32_t max_prefix_pages; /* columns of prefix_tables */
+    int32_t dtype;            /* LP_BF16 or LP_F16: q, k, v, caches, out and norm weights */
+    int32_t device;
+    int64_t num_pages;        /* pages of each cache (>= 1) */
+    uint32_t flags;           /* LP_PLAN_DEBUG_FORCE_TIMEOUT or 0 */
+    int64_t timeout_ns;       /* limit of every device-side wait, from kernel start; 0 = 1 s */
+} lp_attn_desc;
+
+typedef struct lp_attn_s* lp_attn_t;
+
+/* Creates an attention plan and allocates its device scratch (once). */
+int lp_attn_create(lp_attn_t* out, const lp_attn_desc* desc);
+
+/* Frees the plan's scratch.  The caller must have drained work queued with it. */
+int lp_attn_destroy(lp_attn_t plan);
+
+/* Device bytes lp_attn_create allocates for desc (0 if desc is invalid). */
+size_t lp_attn_scratch_bytes(const lp_attn_desc* desc);
+
+/* For each row with 0 <= positions[row] < max_positions and each head x of q and k:
+ *   y = x / sqrt(mean(x^2) + eps) * (weight_offset + w)       (w given; else y = x)
+ *   pairs (a, b) of the first rot_dim lanes, pair i = lanes (i, i + rot_dim/2),
+ *   or (2i, 2i+1) when interleaved:  (a cos - b sin, b cos + a sin)
+ * with cos = cos_sin[position][i], sin = cos_sin[position][rot_dim/2 + i], in
+ * FP32 throughout, rounded once to the output.  A row with a negative
+ * position (padding) is skipped: nothing is written for it.  Outputs may be
+ * the inputs themselves (same pointer and stride), and must not overlap them
+ * otherwise.  q or k may be NULL (then its output is not used).  rot_dim is a
+ * multiple of 16, 0..head_dim; cos_sin may be NULL when it is 0. */
+typedef struct {
+    const void* q;             /* [rows, q_heads, head_dim] or NULL */
+    const void* k;             /* [rows, kv_heads, head_dim] or NULL */
+    void* q_out;
+    void* k_out;
+    int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+    const void* q_weight;      /* [head_dim] or NULL: no norm of q */
+    const void* k_weight;      /* [head_dim] or NULL: no norm of k */
+    const float* cos_sin;      /* [max_positions, rot_dim] */
+    const int32_t* positions;  /* [rows] */
+    uint32_t* status;          /* [1] */
+    float eps;                 /* >= 0 */
+    float weight_offset;       /* 0, or 1 for weights stored about zero */
+    int32_t max_positions;
+    int32_t rot_dim;
+    int32_t interleaved;
+    int32_t rows;
+} lp_rope_io;
+
+int lp_norm_rope(lp_attn_t plan, const lp_rope_io* io, void* stream);
+
+/* lp_norm_rope, and the keys and values of every row of a live group go to
+ * its token's slot of the caches (the values unchanged).  Groups may be of
+ * any size here (a prompt).  rope.k is required; rope.q may be NULL, and
+ * rope.k_out may be NULL (keys to the cache only).  Rows outside every group
+ * and rows of idle groups reach q_out and k_out but no cache; so do the rows
+ * of a malformed group (LP_STATUS_BAD_GROUP: rows out of range, or tokens past
+ * max_pages pages).  No two rows may name the same slot. */
+typedef struct {
+    lp_rope_io rope;
+    const void* v;               /* [rows, kv_heads, head_dim] */
+    int64_t v_stride;
+    const int32_t* group_indptr; /* [groups + 1] */
+    const int32_t* lens;         /* [groups] */
+    const int32_t* block_tables; /* [groups, max_pages] */
+    void* k_cache;
+    void* v_cache;
+    int32_t groups;
+} lp_append_io;
+
+int lp_kv_append(lp_attn_t plan, const lp_append_io* io, void* stream);
+
+/* Row j of group g attends to: every token of its prefix, the group's
+ * committed tokens 0..lens[g]-1, and of the round's own rows those whose bit
+ * is set in row_masks[row] (bit i = row i of the group; NULL: rows 0..j):
+ *   s_t = scale * (q . k_t);  out = sum_t softmax(s)_t v_t;  lse = log sum_t exp(s_t)
+ * with FP32 scores, statistics and sums (the probabilities that multiply v
+ * are rounded to the plan's type).  A row that sees nothing, and every row of
+ * an idle or malformed group, gets out 0 and lse -inf; rows outside every
+ * group are not written.  A malformed group (LP_STATUS_BAD_GROUP) has rows out
+ * of range, more than max_group_rows of them, or tokens past max_pages pages;
+ * rows that two entries of group_indptr claim are not written.
+ * Prefix p serves groups prefix_indptr[p] .. prefix_indptr[p+1]-1 and holds
+ * prefix_lens[p] tokens in the pages prefix_tables[p]. */
+typedef struct {
+    const void* q;                 /* [rows, q_heads, head_dim] */
+    int64_t q_stride;
+    const void* k_cache;
+    const void* v_cache;
+    const int32_t* group_indptr;   /* [groups + 1] */
+    const int32_t* lens;           /* [groups] */
+    const int32_t* block_tables;   /* [groups, max_pages] */
+    const uint32_t* row_masks;     /* [rows] or NULL */
+    const int32_t* prefix_indptr;  /* [prefixes + 1]; NULL when prefixes is 0 */
+    const int32_t* prefix_lens;    /* [prefixes] */
+    const int32_t* prefix_tables;  /* [prefixes, max_prefix_pages] */
+    void* out;                     /* [rows, q_heads, head_dim] */
+    int64_t out_stride;
+    float* lse_out;                /* [rows, q_heads] or NULL */
+    uint32_t* status;              /* [1] */
+    float scale;                   /* > 0 */
+    int32_t rows;
+    int32_t groups;
+    int32_t prefixes;
+} lp_attend_io;
+
+int lp_attend(lp_attn_t plan, const lp_attend_io* io, void* stream);
 
 /* Message of an LP_E* code. */
 const char* lp_strerror(int code);

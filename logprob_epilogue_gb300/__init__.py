@@ -23,12 +23,16 @@ MAX_IDS = 128
 UNUSED_LP_BITS = 0x7FC00000
 TILE_BYTES = 32768  # vocabulary tile: 16384 BF16 or 8192 FP32 logits
 
-LP_F32, LP_BF16 = 0, 1
+LP_F32, LP_BF16, LP_F16 = 0, 1, 2  # LP_F16: attention plans only
 STATUS_BAD_ID = 0x1
 STATUS_BAD_TOKEN = 0x2
 STATUS_BAD_COUNT = 0x4
 STATUS_BAD_GROUP = 0x8
 STATUS_TIMEOUT = 0x10
+STATUS_BAD_TEMPERATURE = 0x20
+STATUS_BAD_POSITION = 0x40
+STATUS_BAD_PAGE = 0x80
+STATUS_BAD_PREFIX = 0x100
 PLAN_HOST_STAGING = 0x1
 PLAN_READ_AHEAD = 0x2
 PLAN_VOCAB_SHARDS = 0x4
@@ -44,6 +48,7 @@ EXPORTS = ("lp_plan_create", "lp_plan_destroy", "lp_plan_scratch_bytes", "lp_bin
            "lp_run_host_bytes", "lp_debug_tiles_read", "lp_debug_poison_scratch", "lp_debug_trace",
            "lp_plan_tiles_per_row", "lp_run_static", "lp_score", "lp_bind_clip", "lp_debug_occupy",
            "lp_chain_verify", "lp_run_sharded",
+           "lp_attn_create", "lp_attn_destroy", "lp_attn_scratch_bytes", "lp_norm_rope", "lp_kv_append", "lp_attend",
            "lp_strerror", "lp_last_cuda_error")
 
 
@@ -150,11 +155,17 @@ def lib() -> ctypes.CDLL:
         L.lp_run_static.argtypes = [ctypes.POINTER(PlanDesc), ctypes.POINTER(IO), P]
         L.lp_score.argtypes = [P, ctypes.POINTER(ScoreIO), P]
         L.lp_bind_clip.argtypes = [P, P, P]
+        L.lp_attn_create.argtypes = [ctypes.POINTER(P), P]
+        L.lp_attn_destroy.argtypes = [P]
+        L.lp_attn_scratch_bytes.argtypes = [P]
+        L.lp_attn_scratch_bytes.restype = ctypes.c_size_t
+        for name in ("lp_norm_rope", "lp_kv_append", "lp_attend"):
+            getattr(L, name).argtypes = [P, P, P]
         L.lp_strerror.argtypes = [ctypes.c_int]
         L.lp_strerror.restype = ctypes.c_char_p
         L.lp_last_cuda_error.argtypes = []
         for name in EXPORTS:
-            if name not in ("lp_plan_scratch_bytes", "lp_strerror"):
+            if name not in ("lp_plan_scratch_bytes", "lp_attn_scratch_bytes", "lp_strerror"):
                 getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -470,3 +481,6 @@ def run_static(desc: PlanDesc, *, logits, group_indptr, draft_tokens, sampled_to
         stream = torch.cuda.current_stream(logits.device)
     handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     _check(lib().lp_run_static(ctypes.byref(desc), ctypes.byref(io), ctypes.c_void_p(handle)), "lp_run_static")
+
+
+from .attn import AttnPlan, attn_scratch_bytes, make_attn_desc  # noqa: E402,F401  (after the names it imports from here)

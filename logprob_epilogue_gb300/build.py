@@ -11,7 +11,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "liblp_epilogue.so")
-SOURCES = ["lp_plan.cu", "lp_kernels.cu", "lp_chain.cu"]
+SOURCES = ["lp_plan.cu", "lp_kernels.cu", "lp_chain.cu", "lp_attn.cu", "lp_rope.cu", "lp_attend.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 # Optional extra nvcc flags (e.g. -DLP_BF16_CTAS=2) for tuning builds.
@@ -25,7 +25,8 @@ def _nvcc() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES]
-    files += [os.path.join(CSRC, "lp_internal.h"), os.path.join(INCLUDE, "lp_epilogue.h")]
+    files += [os.path.join(CSRC, h) for h in ("lp_internal.h", "lp_host.h", "lp_attn.h")]
+    files += [os.path.join(INCLUDE, "lp_epilogue.h")]
     return files
 
 

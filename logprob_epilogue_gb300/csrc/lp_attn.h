@@ -1,0 +1,95 @@
+// lp_attn.h -- shared between the attention plan's host code and its kernels.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace lp {
+
+constexpr int kAttnMaxGroupRows = 32;
+constexpr unsigned kStatusAttnBadGroup = 0x8u, kStatusAttnTimeout = 0x10u, kStatusBadPosition = 0x40u,
+                   kStatusBadPage = 0x80u, kStatusBadPrefix = 0x100u;
+
+struct RopeParams {
+    const void *q, *k, *v;                 // [rows, heads, D]; v: append only
+    void *q_out, *k_out;
+    long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride;  // elements
+    const void *q_weight, *k_weight;       // [D] or null
+    const float* cos_sin;                  // [max_pos, rot]
+    const int* positions;
+    unsigned int* status;
+    float eps, weight_offset;
+    int max_pos, rot, interleaved;
+    int rows, q_heads, kv_heads;           // q_heads 0: no q; kv_heads 0: no k
+    // append (k_cache != nullptr)
+    const int *indptr, *lens, *tables;
+    void *k_cache, *v_cache;
+    int G, max_pages, page_shift;
+    long long num_pages;
+};
+
+struct AttendParams {
+    const void* q;
+    long long q_stride, out_stride;
+    const void *k_cache, *v_cache;
+    const int *indptr, *lens, *tables;
+    const unsigned int* row_masks;
+    const int *prefix_indptr, *prefix_lens, *prefix_tables;
+    void* out;
+    float* lse_out;
+    unsigned int* status;
+    float scale;
+    int rows, G, P;
+    int q_heads, kv_heads, share;          // share = q_heads / kv_heads
+    int max_group_rows, max_pages, max_prefix_pages, page_shift;
+    long long num_pages;
+};
+
+cudaError_t launch_rope(const RopeParams& p, int dtype, int head_dim, cudaStream_t stream);
+cudaError_t launch_attend(const AttendParams& p, int dtype, int head_dim, cudaStream_t stream);
+
+#ifdef __CUDACC__
+// Element type of an attention plan.
+template <bool kBf16>
+struct Half;
+template <>
+struct Half<true> {
+    using T = __nv_bfloat16;
+    using T2 = __nv_bfloat162;
+    static __device__ __forceinline__ float2 unpack(uint32_t w) {
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    }
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        const T2 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+};
+template <>
+struct Half<false> {
+    using T = __half;
+    using T2 = __half2;
+    static __device__ __forceinline__ float2 unpack(uint32_t w) {
+        return __half22float2(*reinterpret_cast<const T2*>(&w));
+    }
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        const T2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+};
+
+// The number of entries of indptr[0..G] that are <= row, less one: the group
+// of `row` when indptr ascends (the caller checks the answer).  All threads of
+// the block take part and get the answer.
+__device__ __forceinline__ int block_find_group(const int* indptr, int G, int row) {
+    int n = 0;
+    for (int b = 0; b <= G; b += blockDim.x) {
+        const int i = b + (int)threadIdx.x;
+        n += __syncthreads_count(i <= G && __ldg(&indptr[i <= G ? i : G]) <= row);
+    }
+    return n - 1;
+}
+#endif
+
+}  // namespace lp

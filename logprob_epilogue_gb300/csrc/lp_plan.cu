@@ -14,6 +14,7 @@
 #include <new>
 
 #include "lp_epilogue.h"
+#include "lp_host.h"
 #include "lp_internal.h"
 
 struct lp_plan_s {
@@ -54,17 +55,13 @@ struct lp_plan_s {
 
 namespace {
 
+using lp::align_up;
+using lp::aligned;
+using lp::cuda_fail;
+using lp::DeviceGuard;
+using lp::kDefaultTimeoutNs;
+
 thread_local int g_last_cuda_error = 0;
-
-constexpr size_t kAlign = 256;
-constexpr int64_t kDefaultTimeoutNs = 1000000000LL;  // 1 s
-
-size_t align_up(size_t v) { return (v + kAlign - 1) & ~(kAlign - 1); }
-
-int cuda_fail(cudaError_t e) {
-    g_last_cuda_error = (int)e;
-    return LP_ECUDA;
-}
 
 int elt_of(int dtype) { return dtype == LP_BF16 ? 2 : (dtype == LP_F32 ? 4 : 0); }
 
@@ -158,8 +155,6 @@ StageLayout stage_layout_of(const lp_plan_desc* d) {
     return S;
 }
 
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
 int check_io(const lp_plan_s* plan, const lp_io* io) {
     if (!io) return LP_EINVAL;
     if (io->rows < 0 || io->groups < 0) return LP_ESHAPE;
@@ -223,24 +218,14 @@ lp::Params make_params(const lp_plan_s* plan, const lp_io& io) {
     return p;
 }
 
-// Makes the plan's device current for the scope; restores the caller's.
-struct DeviceGuard {
-    int prev = -1;
-    bool ok = true;
-    explicit DeviceGuard(int dev) {
-        if (cudaGetDevice(&prev) != cudaSuccess) {
-            ok = false;
-            return;
-        }
-        if (prev != dev && cudaSetDevice(dev) != cudaSuccess) ok = false;
-    }
-    ~DeviceGuard() {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-    }
-};
-
 }  // namespace
+
+namespace lp {
+int cuda_fail(cudaError_t e) {
+    g_last_cuda_error = (int)e;
+    return LP_ECUDA;
+}
+}  // namespace lp
 
 extern "C" {
 

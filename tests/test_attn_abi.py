@@ -1,0 +1,137 @@
+"""CPU checks of the attention entries: what the host refuses before any CUDA call."""
+import ctypes
+
+import pytest
+
+import logprob_epilogue_gb300 as lpe
+from logprob_epilogue_gb300 import attn as A
+from logprob_epilogue_gb300 import build as B
+
+EINVAL, ESHAPE, EALIGN, ECAPACITY, EDTYPE, ECUDA = -1, -2, -3, -4, -5, -6
+
+
+@pytest.fixture(scope="module")
+def L():
+    B.build()
+    return lpe.lib()
+
+
+BASE = dict(max_rows=64, max_groups=8, q_heads=8, kv_heads=2, head_dim=128, page_size=16, num_pages=100, max_pages=10)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(max_rows=0), ESHAPE), (dict(max_groups=0), ESHAPE), (dict(max_pages=0), ESHAPE), (dict(num_pages=0), ESHAPE),
+    (dict(q_heads=7), ESHAPE), (dict(kv_heads=0), ESHAPE), (dict(q_heads=1), ESHAPE), (dict(head_dim=96), ESHAPE),
+    (dict(page_size=24), ESHAPE), (dict(page_size=4), ESHAPE), (dict(page_size=512), ESHAPE),
+    (dict(max_prefixes=1), ESHAPE), (dict(max_prefixes=-1), ESHAPE),
+    (dict(max_group_rows=0), ECAPACITY), (dict(max_group_rows=33), ECAPACITY), (dict(q_heads=516, kv_heads=4), ECAPACITY),
+    (dict(num_pages=1 << 31), ECAPACITY), (dict(max_pages=1 << 27), ECAPACITY),
+    (dict(dtype="f32"), EDTYPE), (dict(timeout_ns=-1), EINVAL),
+])
+def test_create_refuses(L, kw, code):
+    d = A.make_attn_desc(**{**BASE, **kw})
+    h = ctypes.c_void_p()
+    assert L.lp_attn_create(ctypes.byref(h), ctypes.byref(d)) == code
+    assert not h.value
+    assert L.lp_attn_scratch_bytes(ctypes.byref(d)) == 0
+
+
+def test_scratch_bytes_and_null_arguments(L):
+    assert A.attn_scratch_bytes(**BASE) > 0
+    assert L.lp_attn_create(None, None) == EINVAL
+    assert L.lp_attn_destroy(None) == EINVAL
+    assert L.lp_norm_rope(None, None, None) == EINVAL
+    assert L.lp_kv_append(None, None, None) == EINVAL
+    assert L.lp_attend(None, None, None) == EINVAL
+
+
+def test_struct_sizes_match_the_header(L, tmp_path):
+    import os
+    import subprocess
+    src = tmp_path / "s.c"
+    src.write_text('#include <stdio.h>\n#include "lp_epilogue.h"\nint main(void) { printf("%zu %zu %zu %zu\\n", '
+                   "sizeof(lp_attn_desc), sizeof(lp_rope_io), sizeof(lp_append_io), sizeof(lp_attend_io)); return 0; }\n")
+    exe = tmp_path / "s"
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run(["gcc", "-I", os.path.join(root, "include"), str(src), "-o", str(exe)], check=True)
+    sizes = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
+    assert sizes == [ctypes.sizeof(t) for t in (A.AttnDesc, A.RopeIO, A.AppendIO, A.AttendIO)]
+
+
+@pytest.mark.gpu
+class TestRefusals:
+    """Argument errors of the three calls (a plan needs a device)."""
+
+    def plan(self):
+        return lpe.AttnPlan(**BASE, max_prefixes=1, max_prefix_pages=2)
+
+    def rope(self, **kw):
+        io = A.RopeIO()
+        io.q = io.k = io.q_out = io.k_out = io.cos_sin = io.positions = io.status = 1 << 20  # never followed: refused first
+        io.q_stride = io.q_out_stride = 8 * 128
+        io.k_stride = io.k_out_stride = 2 * 128
+        io.eps, io.max_positions, io.rot_dim, io.rows = 1e-6, 10, 128, 4
+        for k, v in kw.items():
+            setattr(io, k, v)
+        return io
+
+    @pytest.mark.parametrize("kw,code", [
+        (dict(rows=65), ESHAPE), (dict(rows=-1), ESHAPE), (dict(rot_dim=8), ESHAPE), (dict(rot_dim=144), ESHAPE),
+        (dict(rot_dim=-16), ESHAPE), (dict(max_positions=-1), ESHAPE), (dict(eps=-1.0), EINVAL), (dict(eps=float("nan")), EINVAL),
+        (dict(status=None), EINVAL), (dict(positions=None), EINVAL), (dict(cos_sin=None), EINVAL), (dict(q=None, k=None), EINVAL),
+        (dict(q_out=None), EINVAL), (dict(k_out=None), EINVAL), (dict(q=(1 << 20) + 2), EALIGN), (dict(q_stride=8 * 128 + 4), EALIGN),
+        (dict(k_stride=128), ESHAPE), (dict(q_weight=(1 << 20) + 4), EALIGN), (dict(positions=(1 << 20) + 1), EALIGN),
+        (dict(weight_offset=float("inf")), EINVAL),
+    ])
+    def test_norm_rope(self, kw, code):
+        p = self.plan()
+        assert lpe.lib().lp_norm_rope(p._h, ctypes.byref(self.rope(**kw)), None) == code
+
+    @pytest.mark.parametrize("kw,code", [
+        (dict(groups=9), ESHAPE), (dict(groups=-1), ESHAPE), (dict(v=None), EINVAL), (dict(v_stride=8), ESHAPE), (dict(k_cache=None), EINVAL),
+        (dict(v_cache=(1 << 20) + 8), EALIGN), (dict(group_indptr=None), EINVAL), (dict(lens=None), EINVAL),
+        (dict(block_tables=(1 << 20) + 2), EALIGN), (dict(rope=dict(k=None)), EINVAL),
+    ])
+    def test_append(self, kw, code):
+        p = self.plan()
+        io = A.AppendIO()
+        io.rope = self.rope(**kw.pop("rope", {}))
+        io.v = io.group_indptr = io.lens = io.block_tables = io.k_cache = io.v_cache = 1 << 20
+        io.v_stride, io.groups = 2 * 128, 2
+        for k, v in kw.items():
+            setattr(io, k, v)
+        assert lpe.lib().lp_kv_append(p._h, ctypes.byref(io), None) == code
+
+    @pytest.mark.parametrize("kw,code", [
+        (dict(rows=65), ESHAPE), (dict(groups=9), ESHAPE), (dict(prefixes=2), ESHAPE), (dict(prefixes=-1), ESHAPE), (dict(scale=0.0), EINVAL),
+        (dict(scale=float("nan")), EINVAL), (dict(scale=float("inf")), EINVAL), (dict(scale=-1.0), EINVAL), (dict(status=None), EINVAL),
+        (dict(q=None), EINVAL), (dict(out=None), EINVAL), (dict(k_cache=None), EINVAL), (dict(lens=None), EINVAL),
+        (dict(prefix_tables=None), EINVAL), (dict(q=(1 << 20) + 8), EALIGN), (dict(out_stride=1028), EALIGN),
+        (dict(q_stride=512), ESHAPE), (dict(lse_out=(1 << 20) + 2), EALIGN), (dict(row_masks=(1 << 20) + 1), EALIGN),
+    ])
+    def test_attend(self, kw, code):
+        p = self.plan()
+        io = A.AttendIO()
+        for n in ("q", "k_cache", "v_cache", "group_indptr", "lens", "block_tables", "prefix_indptr", "prefix_lens", "prefix_tables", "out", "status"):
+            setattr(io, n, 1 << 20)
+        io.q_stride = io.out_stride = 8 * 128
+        io.scale, io.rows, io.groups, io.prefixes = 0.1, 4, 2, 1
+        for k, v in kw.items():
+            setattr(io, k, v)
+        assert lpe.lib().lp_attend(p._h, ctypes.byref(io), None) == code
+
+    def test_python_checks(self):
+        import torch
+        p = self.plan()
+        dev = torch.device("cuda", 0)
+        q = torch.zeros(4, 8, 128, dtype=torch.bfloat16, device=dev)
+        ok = dict(q=q, q_out=torch.zeros_like(q), cos_sin=torch.zeros(4, 128, device=dev),
+                  positions=torch.zeros(4, dtype=torch.int32, device=dev), status=torch.zeros(1, dtype=torch.int32, device=dev))
+        p.norm_rope(**ok)
+        for kw in (dict(q=q.half()), dict(q=q.cpu()), dict(q=q[:, :7]), dict(q=q.transpose(1, 2).contiguous().transpose(1, 2)),
+                   dict(q_out=q[:3]), dict(cos_sin=torch.zeros(4, 128, dtype=torch.float64, device=dev)),
+                   dict(positions=torch.zeros(3, dtype=torch.int32, device=dev)), dict(positions=torch.zeros(4, device=dev)),
+                   dict(cos_sin=torch.zeros(128, 4, device=dev).t()), dict(q=None, q_out=None)):
+            with pytest.raises(ValueError):
+                p.norm_rope(**{**ok, **kw})
+        torch.cuda.synchronize()

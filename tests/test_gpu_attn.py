@@ -1,0 +1,584 @@
+"""The attention operators on the GPU against their 64-bit reference."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+
+import attn_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+def dev():
+    import torch
+    return torch.device("cuda", 0)
+
+
+def rand(gen, *shape, dtype):
+    import torch
+    return torch.randn(*shape, generator=gen, device=dev(), dtype=torch.float32).to(R.DTYPE[dtype])
+
+
+def generator(seed):
+    import torch
+    g = torch.Generator(device=dev())
+    g.manual_seed(seed)
+    return g
+
+
+def i32(a):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(np.asarray(a), np.int32)).to(dev())
+
+
+def table(rot, positions=600, theta=1e4):
+    import torch
+    ang = torch.arange(positions, dtype=torch.float64)[:, None] * theta ** (-torch.arange(rot // 2, dtype=torch.float64) / max(rot // 2, 1))
+    return torch.cat([ang.cos(), ang.sin()], 1).float().to(dev()).contiguous()
+
+
+def status_word():
+    import torch
+    return torch.zeros(1, dtype=torch.int32, device=dev())
+
+
+def plan_of(**kw):
+    import logprob_epilogue_gb300 as lpe
+    base = dict(max_rows=1, max_groups=1, q_heads=4, kv_heads=2, head_dim=128, page_size=16, num_pages=1, max_pages=1)
+    base.update(kw)
+    return lpe.AttnPlan(**base)
+
+
+# ---- norm and rotation
+
+
+@pytest.mark.parametrize("dtype,d,hq,hk,rows,rot,inter,norm,offset", [
+    ("bf16", 128, 32, 8, 4, 128, False, True, 0.0),
+    ("bf16", 128, 3, 1, 1, 64, False, True, 1.0),
+    ("f16", 64, 5, 5, 129, 64, False, True, 0.0),
+    ("f16", 64, 24, 4, 77, 32, True, False, 0.0),
+    ("bf16", 64, 1, 1, 513, 16, True, True, 1.0),
+    ("bf16", 128, 7, 7, 33, 0, False, True, 0.0),
+    ("f16", 128, 16, 2, 250, 112, False, False, 0.0),
+    ("bf16", 128, 6, 2, 31, 48, True, True, 0.0),
+])
+@pytest.mark.parametrize("layout", ["dense", "fused", "inplace"])
+def test_norm_rope(dtype, d, hq, hk, rows, rot, inter, norm, offset, layout):
+    import torch
+    gen = generator(rows + rot)
+    if layout == "dense":
+        q, k = rand(gen, rows, hq, d, dtype=dtype), rand(gen, rows, hk, d, dtype=dtype)
+    else:
+        both = rand(gen, rows, (hq + hk) * d + 8, dtype=dtype)
+        q, k = both[:, :hq * d].unflatten(1, (hq, d)), both[:, hq * d:(hq + hk) * d].unflatten(1, (hk, d))
+    qw, kw = ((0.3 * rand(gen, d, dtype=dtype) + (1 - offset)).to(R.DTYPE[dtype]) if norm else None for _ in range(2))
+    cs = table(rot)
+    pos = torch.randint(0, 600, (rows,), generator=gen, device=dev(), dtype=torch.int32)
+    kw_ref = dict(eps=1e-5, offset=offset, interleaved=inter)
+    rq, rk = R.heads(q, qw, cs, pos, **kw_ref), R.heads(k, kw, cs, pos, **kw_ref)
+    if layout == "inplace":
+        qo, ko = q, k
+    else:
+        qo, ko = torch.full_like(q, 7.0).contiguous(), torch.full_like(k, 7.0).contiguous()
+    st = status_word()
+    p = plan_of(max_rows=rows, q_heads=hq, kv_heads=hk, head_dim=d, dtype=dtype)
+    p.norm_rope(q=q, k=k, q_out=qo, k_out=ko, q_weight=qw, k_weight=kw, eps=1e-5, weight_offset=offset, cos_sin=cs,
+                interleaved=inter, positions=pos, status=st)
+    torch.cuda.synchronize()
+    assert int(st[0]) == 0
+    R.check_heads(qo, *rq, dtype)
+    R.check_heads(ko, *rk, dtype)
+    if layout == "inplace":
+        # the columns of no head are untouched
+        again = rand(generator(rows + rot), rows, (hq + hk) * d + 8, dtype=dtype)
+        assert torch.equal(both[:, -8:], again[:, -8:])
+
+
+def test_norm_rope_skips_padding_and_reports_positions_past_the_table():
+    import torch
+    gen = generator(3)
+    q = rand(gen, 5, 4, 128, dtype="bf16")
+    out = torch.full_like(q, 7.0)
+    st = status_word()
+    p = plan_of(max_rows=5)
+    cs = table(128, positions=10)
+    p.norm_rope(q=q, q_out=out, cos_sin=cs, positions=i32([0, -1, 9, 10, -2147483648]), status=st)
+    torch.cuda.synchronize()
+    import logprob_epilogue_gb300 as lpe
+    assert int(st[0]) == lpe.STATUS_BAD_POSITION
+    assert bool((out[[1, 3, 4]] == 7.0).all())
+    ref = R.heads(q, None, cs, i32([0, 0, 9, 0, 0]), eps=1e-6, offset=0.0, interleaved=False)
+    R.check_heads(out[[0, 2]], ref[0][[0, 2]], ref[1][[0, 2]], "bf16")
+
+
+def test_norm_of_zero_and_huge_heads():
+    import torch
+    x = torch.zeros(3, 4, 128, dtype=torch.bfloat16, device=dev())
+    x[1] = 2.0 ** 60  # squares within FP32
+    x[2, 0, 5] = float("nan")
+    w = torch.ones(128, dtype=torch.bfloat16, device=dev())
+    out = torch.empty_like(x)
+    plan_of(max_rows=3).norm_rope(q=x, q_out=out, q_weight=w, cos_sin=table(0), positions=i32([0, 0, 0]), status=status_word())
+    assert bool((out[0] == 0).all()) and bool((out[1] == 1).all())
+    assert bool(out[2, 0].isnan().all()) and bool((out[2, 1:] == 0).all())
+
+
+# ---- append
+
+
+def batch(n, lens, page, seed, spare=3, extra_pages=0):
+    """indptr, tables (host lists) and the number of pages of a paged batch, pages in random order."""
+    r = np.random.RandomState(seed)
+    need = [(-(-(max(l, 0) + m) // page) if l >= 0 else 0) for l, m in zip(lens, n)]
+    total = sum(need) + spare + extra_pages
+    order = r.permutation(total)
+    width = max(1, max(need))
+    tables, used = np.full((len(n), width), -1, np.int64), 0
+    for g, m in enumerate(need):
+        tables[g, :m] = order[used:used + m]
+        used += m
+    return [0] + list(np.cumsum(n)), tables, total, order[used:]
+
+
+@pytest.mark.parametrize("dtype,d,hq,hk,page,n,lens,with_q,k_out,norm", [
+    ("bf16", 128, 32, 8, 16, [1], [1000], True, False, True),
+    ("bf16", 128, 8, 8, 64, [4] * 9, [0, 5, 63, 64, 65, -1, 127, 200, 60], True, False, True),
+    ("f16", 64, 6, 2, 8, [3, 0, 17, 1, 250], [5, 9, 7, -1, 3], False, True, False),
+    ("f16", 128, 5, 1, 256, [300, 1, 1], [10, 255, 256], True, True, True),
+    ("bf16", 64, 12, 4, 32, [2] * 300, [i % 71 - 1 for i in range(300)], True, False, False),
+])
+def test_append(dtype, d, hq, hk, page, n, lens, with_q, k_out, norm):
+    import torch
+    gen = generator(len(n) + page)
+    indptr, tables, pages, _ = batch(n, lens, page, seed=page)
+    rows = indptr[-1] + 2  # the last two rows belong to no group
+    both = rand(gen, rows, (hq + 2 * hk) * d, dtype=dtype)
+    q, k, v = (both[:, a * d:b * d].unflatten(1, (b - a, d)) for a, b in ((0, hq), (hq, hq + hk), (hq + hk, hq + 2 * hk)))
+    qw, kw = ((1 + 0.3 * rand(gen, d, dtype=dtype)).to(R.DTYPE[dtype]) if norm else None for _ in range(2))
+    cs = table(d, positions=700)
+    pos = torch.randint(0, 700, (rows,), generator=gen, device=dev(), dtype=torch.int32)
+    pos[-1] = -1
+    kc, vc = (torch.full((pages, hk, page, d), float("nan"), dtype=R.DTYPE[dtype], device=dev()) for _ in range(2))
+    qo = torch.full((rows, hq, d), 7.0, dtype=R.DTYPE[dtype], device=dev())
+    ko = torch.full((rows, hk, d), 7.0, dtype=R.DTYPE[dtype], device=dev())
+    st = status_word()
+    p = plan_of(max_rows=rows, max_groups=len(n), q_heads=hq, kv_heads=hk, head_dim=d, page_size=page, num_pages=pages,
+                max_pages=tables.shape[1], dtype=dtype)
+    p.append(q=q if with_q else None, q_out=qo if with_q else None, k=k, v=v, k_out=ko if k_out else None, q_weight=qw, k_weight=kw,
+             cos_sin=cs, positions=pos, group_indptr=i32(indptr), lens=i32(lens), block_tables=i32(tables), k_cache=kc, v_cache=vc,
+             status=st)
+    torch.cuda.synchronize()
+    assert int(st[0]) == 0
+    kw_ref = dict(eps=1e-6, offset=0.0, interleaved=False)
+    rk, mk = R.heads(k, kw, cs, pos, **kw_ref)
+    if with_q:
+        rq, mq = R.heads(q, qw, cs, pos, **kw_ref)
+        R.check_heads(qo[:-1], rq[:-1], mq[:-1], dtype)
+        assert bool((qo[-1] == 7.0).all())
+    if k_out:
+        R.check_heads(ko[:-1], rk[:-1], mk[:-1], dtype)
+        assert bool((ko[-1] == 7.0).all())
+    hit = torch.zeros(pages, page, dtype=torch.bool, device=dev())
+    rowsof, at, off = [], [], []
+    for g in range(len(n)):
+        for j in range(n[g] if lens[g] >= 0 else 0):
+            t = lens[g] + j
+            rowsof.append(indptr[g] + j), at.append(int(tables[g, t // page])), off.append(t % page)
+    hit[at, off] = True
+    R.check_heads(kc[at, :, off], rk[rowsof], mk[rowsof], dtype)
+    assert torch.equal(vc[at, :, off], v[rowsof])
+    if k_out:
+        assert torch.equal(kc[at, :, off], ko[rowsof])
+    # every other slot is untouched
+    for c in (kc, vc):
+        assert bool(c.transpose(1, 2)[~hit].isnan().all())
+
+
+def test_append_malformed_groups_and_pages_write_nothing():
+    import torch
+    import logprob_epilogue_gb300 as lpe
+    gen = generator(9)
+    rows = 8
+    k, v = (rand(gen, rows, 2, 128, dtype="bf16") for _ in range(2))
+    cs, pos = table(128), i32([1] * rows)
+
+    def call(indptr, lens, tables):
+        kc, vc = (torch.full((4, 2, 16, 128), 7.0, dtype=torch.bfloat16, device=dev()) for _ in range(2))
+        st = status_word()
+        p = plan_of(max_rows=rows, max_groups=len(lens), num_pages=4, max_pages=len(tables[0]))
+        p.append(k=k, v=v, cos_sin=cs, positions=pos, group_indptr=i32(indptr), lens=i32(lens), block_tables=i32(tables),
+                 k_cache=kc, v_cache=vc, status=st)
+        torch.cuda.synchronize()
+        return int(st[0]), int((vc != 7.0).any(-1).any(1).sum())
+
+    assert call([0, 8], [24], [[0, 1]]) == (0, 8)
+    assert call([0, 8], [25], [[0, 1]]) == (lpe.STATUS_BAD_GROUP, 0)           # tokens past the table
+    assert call([0, 9], [0], [[0, 1]]) == (lpe.STATUS_BAD_GROUP, 0)            # rows past the block
+    assert call([-3, 5], [0], [[0, 1]]) == (lpe.STATUS_BAD_GROUP, 0)
+    assert call([0, 8], [2147483647], [[0, 1]]) == (lpe.STATUS_BAD_GROUP, 0)
+    assert call([0, 8], [12], [[0, 4]]) == (lpe.STATUS_BAD_PAGE, 4)            # the second page does not exist
+    assert call([0, 8], [12], [[-1, 3]]) == (lpe.STATUS_BAD_PAGE, 4)
+    assert call([0, 4, 4, 8], [0, 0, -1], [[0], [1], [2]]) == (0, 4)           # an empty and an idle group
+    assert call([6, 2, 8], [0, 0], [[0], [1]])[1] <= 8                         # not ascending: in bounds
+
+
+# ---- attention
+
+
+class Case:
+    def __init__(self, *, dtype="bf16", d=128, hq=4, hk=2, page=16, n=(1,), lens=(0,), prefixes=(), prefix_indptr=None,
+                 masks=None, seed=1, width=3.0, pad_rows=0, fill=float("nan"), extra_pages=0, at_end=False, max_group_rows=32):
+        import torch
+        gen = generator(seed)
+        self.dtype, self.d, self.hq, self.hk, self.page, self.n, self.lens = dtype, d, hq, hk, page, list(n), list(lens)
+        ppages = [-(-x // page) for x in prefixes]
+        self.indptr, self.tables, self.pages, free = batch(self.n, self.lens, page, seed, spare=2 + sum(ppages), extra_pages=extra_pages)
+        if at_end and extra_pages:  # the batch in the cache's last pages
+            self.tables = np.where(self.tables >= 0, self.pages - 1 - np.argsort(np.argsort(self.tables.ravel())).reshape(self.tables.shape), -1)
+            used = set(self.tables[self.tables >= 0].tolist())
+            assert len(used) == int((self.tables >= 0).sum())
+            free = np.array([x for x in range(self.pages - 1, self.pages - 1 - len(used) - sum(ppages) - 2, -1) if x not in used])
+        self.rows = self.indptr[-1] + pad_rows
+        self.prefix_lens = list(prefixes)
+        self.prefix_indptr = list(prefix_indptr) if prefix_indptr is not None else ([0, len(self.n)] if prefixes else None)
+        self.prefix_tables = np.full((len(prefixes), max(ppages, default=1) or 1), -1, np.int64)
+        used = 0
+        for i, m in enumerate(ppages):
+            self.prefix_tables[i, :m] = free[used:used + m]
+            used += m
+        self.q = (rand(gen, self.rows, hq, d, dtype="bf16").float() * (0.2 + width * torch.rand(1, hq, 1, generator=gen, device=dev()))).to(R.DTYPE[dtype])
+        shape = (self.pages, hk, page, d)
+        self.kc, self.vc = (torch.full(shape, fill, dtype=R.DTYPE[dtype], device=dev()) for _ in range(2))
+        for tabs, counts in ((self.tables, [l + m if l >= 0 else 0 for l, m in zip(self.lens, self.n)]), (self.prefix_tables, self.prefix_lens)):
+            for tab, c in zip(tabs, counts):
+                if c == 0:
+                    continue
+                t = torch.arange(c, device=dev())
+                at, off = torch.from_numpy(tab).to(dev())[t // page], t % page
+                self.kc[at, :, off] = rand(gen, c, hk, d, dtype=dtype)
+                self.vc[at, :, off] = rand(gen, c, hk, d, dtype=dtype)
+        self.masks = masks
+        self.max_group_rows = max_group_rows
+        self.scale = 1.0 / math.sqrt(d)
+
+    def plan(self, **kw):
+        return plan_of(max_rows=max(self.rows, 1), max_groups=len(self.n), q_heads=self.hq, kv_heads=self.hk, head_dim=self.d,
+                       page_size=self.page, num_pages=self.pages, max_pages=self.tables.shape[1], max_prefixes=len(self.prefix_lens),
+                       max_prefix_pages=self.prefix_tables.shape[1] if self.prefix_lens else 0, max_group_rows=self.max_group_rows,
+                       dtype=self.dtype, **kw)
+
+    def tensors(self):
+        t = dict(q=self.q, k_cache=self.kc, v_cache=self.vc, group_indptr=i32(self.indptr), lens=i32(self.lens),
+                 block_tables=i32(self.tables), scale=self.scale)
+        if self.masks is not None:
+            t["row_masks"] = i32(np.array(self.masks, np.uint32).view(np.int32))
+        if self.prefix_lens:
+            t.update(prefix_indptr=i32(self.prefix_indptr), prefix_lens=i32(self.prefix_lens), prefix_tables=i32(self.prefix_tables))
+        return t
+
+    def run(self, plan=None, stream=None, **more):
+        import torch
+        out = torch.full((self.rows, self.hq, self.d), 7.0, dtype=R.DTYPE[self.dtype], device=dev())
+        lse = torch.full((self.rows, self.hq), 7.0, device=dev())
+        st = status_word()
+        plan = plan or self.plan()
+        plan.attend(**{**self.tensors(), **more}, out=out, lse_out=lse, status=st, stream=stream)
+        torch.cuda.synchronize()
+        return out, lse, int(st[0])
+
+    def ref(self):
+        return R.attend(self.q, self.kc, self.vc, self.indptr, self.lens, self.tables, scale=self.scale, masks=self.masks,
+                        prefix_indptr=self.prefix_indptr, prefix_lens=self.prefix_lens, prefix_tables=self.prefix_tables)
+
+    def check(self, **kw):
+        out, lse, st = self.run(**kw)
+        assert st == 0, hex(st)
+        R.check_attend(out, lse, self.ref(), self.dtype, slice(0, self.indptr[-1]))
+        return out, lse
+
+
+EDGES = [0, 1, 2, 15, 16, 17, 63, 64, 127, 128, 129, 255, 256, 257, 383, 640]
+
+
+@pytest.mark.parametrize("dtype,d,hq,hk,page", [
+    ("bf16", 128, 4, 1, 16), ("f16", 64, 6, 2, 8), ("bf16", 64, 2, 2, 256), ("f16", 128, 12, 1, 64), ("bf16", 128, 10, 2, 128),
+    ("f16", 128, 5, 1, 32), ("bf16", 64, 128, 1, 64),
+])
+def test_attend_lengths(dtype, d, hq, hk, page):
+    """Every length about a page's and a tile's end, groups of one to five rows, unused slots NaN."""
+    n = [1 + i % 5 for i in range(len(EDGES))]
+    Case(dtype=dtype, d=d, hq=hq, hk=hk, page=page, n=n, lens=EDGES, pad_rows=2).check()
+
+
+@pytest.mark.parametrize("prefix", [1, 7, 64, 127, 128, 129, 300, 1025])
+@pytest.mark.parametrize("dtype,d,hq,hk,page,n,lens", [
+    ("bf16", 128, 4, 1, 16, [1], [0]),
+    ("bf16", 128, 8, 2, 64, [4] * 11, [0, 1, 2, 130, 5, 64, 9, 31, 256, 77, 3]),
+    ("f16", 64, 3, 3, 32, [32, 1, 9, 31, 32], [5, 0, 700, 1, 128]),
+    ("f16", 128, 24, 2, 8, [16, 16, 16], [1, 0, 140]),
+])
+def test_attend_shared_prefix(prefix, dtype, d, hq, hk, page, n, lens):
+    Case(dtype=dtype, d=d, hq=hq, hk=hk, page=page, n=n, lens=lens, prefixes=[prefix]).check()
+
+
+def test_attend_several_prefixes_and_groups_without_one():
+    n = [2, 3, 1, 4, 1, 1, 5, 2, 2]
+    lens = [10, 0, 300, 5, -1, 129, 0, 64, 1]
+    Case(n=n, lens=lens, prefixes=[200, 5, 400], prefix_indptr=[1, 3, 3, 8], hq=6, hk=3).check()
+    Case(n=n, lens=lens, prefixes=[200, 0], prefix_indptr=[0, 4, 9], hq=6, hk=3, dtype="f16", d=64).check()
+
+
+def test_attend_many_rows_behind_a_prefix():
+    """More query rows than one tile: 66 groups of 1..8 rows, five heads sharing."""
+    n = [1 + i % 8 for i in range(66)]
+    lens = [(37 * i) % 150 - 1 for i in range(66)]
+    Case(n=n, lens=lens, prefixes=[517], hq=10, hk=2).check()
+    Case(n=n, lens=lens, prefixes=[517], hq=10, hk=2, d=64, dtype="f16", page=64).check()
+
+
+def test_attend_trees_and_empty_rows():
+    r = np.random.RandomState(0)
+    n, lens = [7, 32, 1, 16, 3], [0, 50, 0, 131, 0]
+    masks = []
+    for m in n:
+        rows = [1]
+        for j in range(1, m):
+            rows.append(rows[r.randint(j)] | 1 << j)
+        masks += rows
+    masks[3] = 0                 # no context, no row: nothing to see
+    masks[39] = 0                # a single row that does not see itself
+    masks[8] = 0xFFFFFFFF        # rows after its own, too
+    masks[-1] = 0xFFFFFFF8       # bits past the group's rows name nothing
+    c = Case(n=n, lens=lens, masks=masks)
+    out, lse = c.check()
+    for row in (3, 39, c.rows - 1):
+        assert bool((out[row] == 0).all()) and bool((lse[row] == -math.inf).all())
+    Case(n=n, lens=lens, masks=masks, prefixes=[33], d=64).check()
+
+
+def test_attend_idle_and_malformed_groups():
+    import torch
+    import logprob_epilogue_gb300 as lpe
+    c = Case(n=[2, 3, 2, 1], lens=[20, -1, 40, -7], prefixes=[30])
+    out, lse = c.check()
+    assert bool((out[2:5] == 0).all()) and bool((lse[2:5] == -math.inf).all())
+    ref = c.ref()
+    t = c.tensors()
+    good = list(range(0, 2)) + [7]
+    # more tokens than the table holds
+    out, lse, st = c.run(lens=i32([20, -1, c.tables.shape[1] * c.page - 1, -7]))
+    assert st == lpe.STATUS_BAD_GROUP
+    assert bool((out[5:7] == 0).all()) and bool((lse[5:7] == -math.inf).all())
+    R.check_attend(out, lse, ref, c.dtype, good)
+    # more rows than the plan takes, rows out of range, not ascending: in bounds, reported
+    small = Case(n=[2, 3, 2, 1], lens=[20, -1, 40, -7], prefixes=[30], max_group_rows=2)
+    out, lse, st = small.run(lens=i32([20, 3, 40, -7]))
+    assert st == lpe.STATUS_BAD_GROUP and bool((out[2:5] == 0).all())
+    R.check_attend(out, lse, ref, c.dtype, good)
+    for indptr in ([0, 2, 5, 7, 9], [-2, 2, 5, 7, 8], [0, 5, 2, 7, 8], [0, 2, 5, 2147483647, 8]):
+        _, _, st = c.run(group_indptr=i32(indptr))
+        assert st & lpe.STATUS_BAD_GROUP, indptr
+    # prefixes: out of range, not ascending, longer than their table
+    for bad in (dict(prefix_indptr=i32([0, 5])), dict(prefix_indptr=i32([3, 2])), dict(prefix_indptr=i32([-1, 4])),
+                dict(prefix_lens=i32([-1])), dict(prefix_lens=i32([c.prefix_tables.shape[1] * c.page + 1]))):
+        out, lse, st = c.run(**bad)
+        assert st == lpe.STATUS_BAD_PREFIX, bad
+        alone = R.attend(c.q, c.kc, c.vc, c.indptr, c.lens, c.tables, scale=c.scale)
+        R.check_attend(out, lse, alone, c.dtype, slice(0, c.rows))
+    assert torch.equal(t["lens"], i32(c.lens))
+
+
+def test_attend_pages_out_of_range_read_as_zeros():
+    import logprob_epilogue_gb300 as lpe
+    c = Case(n=[1, 2], lens=[40, 300], fill=0.0)
+    for bad in (-1, -2147483648, c.pages, 2147483647):
+        tab = c.tables.copy()
+        tab[1, 3] = bad
+        out, lse, st = c.run(block_tables=i32(tab))
+        assert st == lpe.STATUS_BAD_PAGE
+        kc, vc = c.kc.clone(), c.vc.clone()
+        kc[int(c.tables[1, 3])] = 0
+        vc[int(c.tables[1, 3])] = 0
+        ref = R.attend(c.q, kc, vc, c.indptr, c.lens, c.tables, scale=c.scale)
+        R.check_attend(out, lse, ref, c.dtype)
+
+
+def test_attend_infinities_and_nan_stay_with_the_rows_that_see_them():
+    import torch
+    c = Case(n=[4, 4], lens=[200, 129], hq=4, hk=2)
+    clean, clean_lse = c.check()
+    # the last draft's key and value of group 0: only row 3 sees them
+    t = 203
+    page, off = int(c.tables[0, t // c.page]), t % c.page
+    for cache in (c.kc, c.vc):
+        for bad in (float("nan"), float("inf"), -float("inf")):
+            keep = cache[page, :, off].clone()
+            cache[page, :, off] = bad
+            out, lse, st = c.run()
+            cache[page, :, off] = keep
+            assert st == 0
+            rows = [0, 1, 2, 4, 5, 6, 7]
+            assert torch.equal(out[rows], clean[rows]) and torch.equal(lse[rows], clean_lse[rows])
+            assert not bool(out[3].isfinite().all())
+    # a value of -inf scores (the type's lowest and below) weighs nothing: keys of one committed token very far away
+    t = 60
+    page, off = int(c.tables[0, t // c.page]), t % c.page
+    c.kc[page, :, off] = (-1e30 * c.q[0, ::2].float().sign()).to(R.DTYPE[c.dtype])
+    out, lse, st = c.run()
+    assert st == 0
+    R.check_attend(out[:1, ::2], lse[:1, ::2], [x[:1, ::2] for x in c.ref()], c.dtype)
+
+
+def test_attend_extreme_scores():
+    """Scores of magnitude 1e3, rising and falling along the context: the running maximum moves often."""
+    import torch
+    c = Case(n=[3, 1], lens=[900, 513], hq=4, hk=1, width=0.0)
+    c.q = torch.full_like(c.q, 8.0)
+    t = torch.arange(903, device=dev())
+    for g, count in ((0, 903), (1, 514)):
+        at, off = torch.from_numpy(c.tables[g]).to(dev())[t[:count] // c.page], t[:count] % c.page
+        ramp = (t[:count].float() - 300.0) * (1 if g == 0 else -1) / 64.0
+        c.kc[at, :, off] = ramp[:, None, None].expand(count, 1, 128).to(c.kc.dtype)
+    c.check()
+
+
+def test_attend_offsets_past_32_bits():
+    """A cache of more than 2^32 elements, the batch in its last pages."""
+    import torch
+    if torch.cuda.get_device_properties(0).total_memory < 60e9:
+        pytest.skip("needs a large card")
+    c = Case(n=[1, 3], lens=[300, 77], hq=4, hk=4, page=256, prefixes=[200], fill=0.0, extra_pages=33_000, at_end=True)
+    assert c.kc.numel() > 2 ** 32 and c.tables.max() > 33_000
+    c.check()
+    # and the append that reaches them
+    rows = c.rows
+    k, v = (rand(generator(5), rows, 4, 128, dtype="bf16") for _ in range(2))
+    c.plan().append(k=k, v=v, cos_sin=table(0), positions=i32([0] * rows), group_indptr=i32(c.indptr), lens=i32(c.lens),
+                    block_tables=i32(c.tables), k_cache=c.kc, v_cache=c.vc, status=status_word())
+    t = c.lens[1] + 2
+    assert torch.equal(c.kc[int(c.tables[1, t // 256]), :, t % 256], k[-1])
+    assert torch.equal(c.vc[int(c.tables[1, t // 256]), :, t % 256], v[-1])
+
+
+def test_attend_strided_tensors_other_streams_and_graphs():
+    import torch
+    c = Case(n=[4, 2, 1], lens=[100, 333, 0], prefixes=[150])
+    ref = c.ref()
+    wide = torch.zeros(c.rows, (c.hq + 3) * c.d, dtype=c.q.dtype, device=dev())
+    wide[:, c.d:(c.hq + 1) * c.d] = c.q.flatten(1)
+    q = wide[:, c.d:(c.hq + 1) * c.d].unflatten(1, (c.hq, c.d))
+    outs = torch.full((c.rows, (c.hq + 1) * c.d), 7.0, dtype=c.q.dtype, device=dev())
+    out = outs[:, :c.hq * c.d].unflatten(1, (c.hq, c.d))
+    plan, st, t = c.plan(), status_word(), c.tensors()
+    t["q"] = q
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    plan.attend(**t, out=out, status=st, stream=side)
+    side.synchronize()
+    R.check_attend(out, None, ref, c.dtype)
+    assert bool((outs[:, c.hq * c.d:] == 7.0).all())
+    # captured once, replayed on new lengths and queries
+    lse = torch.zeros(c.rows, c.hq, device=dev())
+    t["q"] = c.q
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plan.attend(**t, out=out, lse_out=lse, status=st)
+    for lens in ([100, 333, 0], [3, -1, 0], [0, 0, 0], [100, 12, 0]):
+        t["lens"].copy_(i32(lens))
+        c.lens = lens
+        # each row's own keys follow the length: the reference reads the cache as it is
+        for g, l in enumerate(lens):
+            for j in range(c.n[g] if l >= 0 else 0):
+                at, off = int(c.tables[g, (l + j) // c.page]), (l + j) % c.page
+                c.kc[at, :, off], c.vc[at, :, off] = 0.25 * (j + 1), 0.5 * j
+        graph.replay()
+        torch.cuda.synchronize()
+        R.check_attend(out, lse, c.ref(), c.dtype)
+    assert int(st[0]) == 0
+
+
+def test_attend_repeats_bit_for_bit_after_other_calls():
+    import torch
+    a = Case(n=[4] * 30, lens=[(97 * i) % 500 for i in range(30)], prefixes=[700])
+    b = Case(n=[2] * 30, lens=[(31 * i) % 300 for i in range(30)], prefixes=[20], seed=9)
+    plan = plan_of(max_rows=120, max_groups=30, num_pages=a.pages, max_pages=a.tables.shape[1], max_prefixes=1,
+                   max_prefix_pages=a.prefix_tables.shape[1], max_group_rows=4)
+    first = a.run(plan)
+    wide = np.full((30, a.tables.shape[1]), -1)
+    wide[:, :b.tables.shape[1]] = b.tables
+    ptab = np.full((1, a.prefix_tables.shape[1]), -1)
+    ptab[:, :b.prefix_tables.shape[1]] = b.prefix_tables
+    kc, vc = a.kc.clone(), a.vc.clone()
+    kc[:b.pages], vc[:b.pages] = b.kc, b.vc
+    out, lse, st = b.run(plan, block_tables=i32(wide), prefix_tables=i32(ptab), k_cache=kc, v_cache=vc)
+    assert st == 0
+    R.check_attend(out, lse, b.ref(), b.dtype)
+    again = a.run(plan)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_one_group_matches_the_batch():
+    """A group's rows do not depend on what else is in the batch (to rounding)."""
+    c = Case(n=[4, 1, 3], lens=[1000, 31, 400], prefixes=[250])
+    out, lse = c.check()
+    alone_out, alone_lse, _ = c.run(lens=i32([-1, -1, 400]))
+    R.check_attend(alone_out, alone_lse, c.ref(), c.dtype, slice(5, 8))
+    assert bool((alone_out[:5] == 0).all())
+
+
+def test_zero_rows_and_zero_groups():
+    import torch
+    c = Case(n=[1], lens=[5])
+    plan = c.plan()
+    empty = torch.empty(0, c.hq, c.d, dtype=c.q.dtype, device=dev())
+    t = c.tensors()
+    t["q"] = empty
+    t["group_indptr"], t["lens"], t["block_tables"] = i32([0]), i32([]), i32(np.zeros((0, c.tables.shape[1])))
+    plan.attend(**t, out=empty, status=status_word())
+    t["q"] = c.q
+    out = torch.full_like(c.q, 7.0)
+    plan.attend(**t, out=out, status=status_word())
+    torch.cuda.synchronize()
+    assert bool((out == 7.0).all())
+
+
+# ---- a verify round
+
+
+def test_rounds_of_append_attend_commit():
+    """Three rounds: append, attend, commit what was accepted; rejected tokens are overwritten by the next round."""
+    import torch
+    gen = generator(11)
+    hq, hk, d, page, groups, rows_g = 8, 2, 128, 16, 6, 4
+    rows, width = groups * rows_g, 12
+    pages = groups * width + 5
+    plan = plan_of(max_rows=rows, max_groups=groups, q_heads=hq, kv_heads=hk, head_dim=d, page_size=page, num_pages=pages,
+                   max_pages=width, max_group_rows=rows_g, max_prefixes=1, max_prefix_pages=5)
+    order = np.random.RandomState(1).permutation(pages)
+    tables, ptab = order[:groups * width].reshape(groups, width), order[groups * width:].reshape(1, 5)
+    kc, vc = (rand(gen, pages, hk, page, d, dtype="bf16") for _ in range(2))
+    lens = i32([0, 5, 16, 100, 31, -1])
+    st, cs = status_word(), table(d)
+    indptr = i32(np.arange(groups + 1) * rows_g)
+    for step in range(3):
+        qkv = rand(gen, rows, (hq + 2 * hk) * d, dtype="bf16")
+        q, k, v = (qkv[:, a * d:b * d].unflatten(1, (b - a, d)) for a, b in ((0, hq), (hq, hq + hk), (hq + hk, hq + 2 * hk)))
+        pos = (70 + lens.clamp(min=0)[:, None] + torch.arange(rows_g, device=dev(), dtype=torch.int32)).flatten().contiguous()
+        qo, out = (torch.empty(rows, hq, d, dtype=torch.bfloat16, device=dev()) for _ in range(2))
+        lse = torch.empty(rows, hq, device=dev())
+        plan.append(q=q, k=k, v=v, q_out=qo, cos_sin=cs, positions=pos, group_indptr=indptr, lens=lens, block_tables=i32(tables),
+                    k_cache=kc, v_cache=vc, status=st)
+        plan.attend(q=qo, k_cache=kc, v_cache=vc, group_indptr=indptr, lens=lens, block_tables=i32(tables), out=out, lse_out=lse,
+                    status=st, prefix_indptr=i32([0, groups]), prefix_lens=i32([70]), prefix_tables=i32(ptab))
+        ref = R.attend(qo, kc, vc, indptr.tolist(), lens.tolist(), tables, scale=d ** -0.5, prefix_indptr=[0, groups], prefix_lens=[70],
+                       prefix_tables=ptab)
+        R.check_attend(out, lse, ref, "bf16")
+        # the appended keys are the rotated ones
+        rk, mk = R.heads(k, None, cs, pos, eps=1e-6, offset=0.0, interleaved=False)
+        g, j = 3, 2
+        t = int(lens[g]) + j
+        R.check_heads(kc[int(tables[g, t // page]), :, t % page], rk[g * rows_g + j], mk[g * rows_g + j], "bf16")
+        accepted = torch.tensor([0, 3, 1, 2, 0, -1], dtype=torch.int32, device=dev())
+        lens = torch.where(lens >= 0, lens + accepted + 1, lens).int()
+    assert int(st[0]) == 0
