@@ -25,7 +25,7 @@ def _nvcc() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES]
-    files += [os.path.join(CSRC, h) for h in ("lp_internal.h", "lp_host.h", "lp_attn.h")]
+    files += [os.path.join(CSRC, h) for h in ("lp_internal.h", "lp_host.h", "lp_attn.h", "lp_tc.h")]
     files += [os.path.join(INCLUDE, "lp_epilogue.h")]
     return files
 

@@ -1,6 +1,7 @@
 // lp_attn.cu -- host side of the attention plan: descriptor and argument
 // checks, scratch, and the launches of lp_norm_rope, lp_kv_append and
 // lp_attend.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -12,9 +13,17 @@
 #include "lp_epilogue.h"
 #include "lp_host.h"
 
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
 struct lp_attn_s {
     lp_attn_desc d;
     int page_shift;
+    int grid;
+    unsigned char* scratch;
+    lp::AttendScratch sc;
+    EncodeTiled encode;
 };
 
 namespace {
@@ -52,6 +61,51 @@ int check_desc(const lp_attn_desc* d) {
     if (((int64_t)d->max_prefix_pages + 1) * d->page_size > 0x3FFFFFFF) return LP_ECAPACITY;
     if ((d->flags & ~(uint32_t)LP_PLAN_DEBUG_FORCE_TIMEOUT) != 0 || d->timeout_ns < 0) return LP_EINVAL;
     return LP_OK;
+}
+
+struct Layout {
+    size_t seg_tiles, seg_units, part_o, part_ml, total;
+    long long prefix_slots, group_slots;
+    int group_rows;
+};
+
+// Pieces of a kind: every unit starts one and every block boundary one more.
+Layout layout_of(const lp_attn_desc* d, int grid) {
+    Layout L{};
+    const int share = d->q_heads / d->kv_heads, per_tile = lp::kQTile / share;
+    const long long group_units = (long long)d->max_groups * ((d->max_group_rows + 2 * per_tile - 1) / (2 * per_tile));
+    const long long prefix_units = d->max_prefixes == 0 ? 0 : d->max_rows / (2 * per_tile) + d->max_prefixes;
+    L.group_rows = (d->max_group_rows < per_tile ? d->max_group_rows : per_tile) * share;
+    L.group_slots = group_units * d->kv_heads + grid;
+    L.prefix_slots = d->max_prefixes == 0 ? 0 : prefix_units * d->kv_heads + grid;
+    const size_t segs = (size_t)d->max_prefixes + (size_t)d->max_groups;
+    const size_t part_rows = 2 * ((size_t)L.prefix_slots * lp::kQTile + (size_t)L.group_slots * (size_t)L.group_rows);
+    size_t off = 0;
+    L.seg_tiles = off;
+    off = lp::align_up(off + (segs + 1) * 8);
+    L.seg_units = off;
+    off = lp::align_up(off + segs * 4);
+    L.part_ml = off;
+    off = lp::align_up(off + part_rows * 8);
+    L.part_o = off;
+    off = lp::align_up(off + part_rows * (size_t)d->head_dim * 4);
+    L.total = off;
+    return L;
+}
+
+// The 4-D map of a cache: lanes, slots of a page, heads, pages; boxes of 64
+// lanes (128 bytes, the swizzle's span) by a page's slots.
+bool encode_cache(const lp_attn_s* plan, CUtensorMap* map, const void* cache) {
+    const lp_attn_desc& d = plan->d;
+    const cuuint64_t row = (cuuint64_t)d.head_dim * 2;
+    const cuuint64_t dims[4] = {(cuuint64_t)d.head_dim, (cuuint64_t)d.page_size, (cuuint64_t)d.kv_heads, (cuuint64_t)d.num_pages};
+    const cuuint64_t strides[3] = {row, row * d.page_size, row * d.page_size * d.kv_heads};
+    const cuuint32_t box[4] = {64, (cuuint32_t)lp::cache_box_rows(d.page_size), 1, 1};
+    const cuuint32_t step[4] = {1, 1, 1, 1};
+    return plan->encode(map, d.dtype == LP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                        const_cast<void*>(cache), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // A [rows, heads, D] tensor: present, 16-byte aligned, rows a multiple of 16
@@ -120,7 +174,12 @@ extern "C" {
 
 size_t lp_attn_scratch_bytes(const lp_attn_desc* desc) {
     if (check_desc(desc) != LP_OK) return 0;
-    return 256;
+    int sms = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, desc->device) != cudaSuccess || sms < 1) {
+        (void)cudaGetLastError();
+        sms = 152;  // no such device here: a GB300's
+    }
+    return layout_of(desc, sms).total;
 }
 
 int lp_attn_create(lp_attn_t* out, const lp_attn_desc* desc) {
@@ -134,14 +193,40 @@ int lp_attn_create(lp_attn_t* out, const lp_attn_desc* desc) {
     if (!plan) return LP_EINVAL;
     plan->d = *desc;
     plan->page_shift = page_shift_of(desc->page_size);
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+    cudaError_t e = cudaDeviceGetAttribute(&plan->grid, cudaDevAttrMultiProcessorCount, desc->device);
+    if (e == cudaSuccess) e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
+    if (e == cudaSuccess && (found != cudaDriverEntryPointSuccess || !fn)) e = cudaErrorNotSupported;
+    if (e == cudaSuccess) e = lp::prepare_attend(desc->dtype, desc->head_dim);
+    Layout L{};
+    if (e == cudaSuccess) {
+        plan->encode = reinterpret_cast<EncodeTiled>(fn);
+        L = layout_of(desc, plan->grid);
+        e = cudaMalloc(&plan->scratch, L.total);
+    }
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        delete plan;
+        return cuda_fail(e);
+    }
+    plan->sc.seg_tiles = reinterpret_cast<unsigned long long*>(plan->scratch + L.seg_tiles);
+    plan->sc.seg_units = reinterpret_cast<int*>(plan->scratch + L.seg_units);
+    plan->sc.part_ml = reinterpret_cast<float2*>(plan->scratch + L.part_ml);
+    plan->sc.part_o = reinterpret_cast<float*>(plan->scratch + L.part_o);
+    plan->sc.prefix_slots = L.prefix_slots;
+    plan->sc.group_slots = L.group_slots;
+    plan->sc.group_rows = L.group_rows;
     *out = plan;
     return LP_OK;
 }
 
 int lp_attn_destroy(lp_attn_t plan) {
     if (!plan) return LP_EINVAL;
+    DeviceGuard guard(plan->d.device);
+    const cudaError_t e = cudaFree(plan->scratch);
     delete plan;
-    return LP_OK;
+    return e == cudaSuccess ? LP_OK : cuda_fail(e);
 }
 
 int lp_norm_rope(lp_attn_t plan, const lp_rope_io* io, void* stream) {
@@ -234,7 +319,15 @@ int lp_attend(lp_attn_t plan, const lp_attend_io* io, void* stream) {
     p.max_prefix_pages = d.max_prefix_pages;
     p.page_shift = plan->page_shift;
     p.num_pages = d.num_pages;
-    const cudaError_t e = lp::launch_attend(p, d.dtype, d.head_dim, static_cast<cudaStream_t>(stream));
+    p.rows_per_tile = lp::kQTile / p.share;
+    p.grid = plan->grid;
+    p.sc = plan->sc;
+    p.timeout_ns = (unsigned long long)(d.timeout_ns > 0 ? d.timeout_ns : lp::kDefaultTimeoutNs);
+    p.force_timeout = (d.flags & LP_PLAN_DEBUG_FORCE_TIMEOUT) != 0;
+    CUtensorMap k_map, v_map;
+    if (!encode_cache(plan, &k_map, io->k_cache) || !encode_cache(plan, &v_map, io->v_cache))
+        return cuda_fail(cudaErrorInvalidValue);
+    const cudaError_t e = lp::launch_attend(p, k_map, v_map, d.dtype, d.head_dim, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? LP_OK : cuda_fail(e);
 }
 

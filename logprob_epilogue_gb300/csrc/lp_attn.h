@@ -1,6 +1,7 @@
 // lp_attn.h -- shared between the attention plan's host code and its kernels.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -30,6 +31,21 @@ struct RopeParams {
     long long num_pages;
 };
 
+constexpr int kQTile = 128;    // query rows (row, head) of one tensor-core tile
+constexpr int kKTile = 128;    // tokens of one tile
+
+// Scratch of lp_attend.  A segment is a prefix or a group's committed tokens;
+// a unit is at most two tiles of its query rows for one key-value head; a
+// piece is the run of a unit's token tiles that one block takes.
+struct AttendScratch {
+    unsigned long long* seg_tiles;  // [P + G + 1] tiles before the segment
+    int* seg_units;                 // [P + G] units before it, among prefixes or among groups
+    float* part_o;                  // pieces of prefixes, then of groups: unnormalised results [2][rows][D]
+    float2* part_ml;                // (maximum in base 2, sum) [2][rows]
+    long long prefix_slots, group_slots;
+    int group_rows;                 // rows per tile in a group slot (prefix slots: kQTile)
+};
+
 struct AttendParams {
     const void* q;
     long long q_stride, out_stride;
@@ -45,10 +61,20 @@ struct AttendParams {
     int q_heads, kv_heads, share;          // share = q_heads / kv_heads
     int max_group_rows, max_pages, max_prefix_pages, page_shift;
     long long num_pages;
+    int rows_per_tile;                     // kQTile / share
+    int grid;                              // blocks of the attention kernel
+    AttendScratch sc;
+    unsigned long long timeout_ns;
+    int force_timeout;
 };
 
+// Token columns of a box of the caches' tensor maps: a page, or a tile of it.
+inline int cache_box_rows(int page_size) { return page_size < kKTile ? page_size : kKTile; }
+
 cudaError_t launch_rope(const RopeParams& p, int dtype, int head_dim, cudaStream_t stream);
-cudaError_t launch_attend(const AttendParams& p, int dtype, int head_dim, cudaStream_t stream);
+cudaError_t prepare_attend(int dtype, int head_dim);  // once per plan: kernel attributes
+cudaError_t launch_attend(const AttendParams& p, const CUtensorMap& k_map, const CUtensorMap& v_map, int dtype,
+                          int head_dim, cudaStream_t stream);
 
 #ifdef __CUDACC__
 // Element type of an attention plan.

@@ -582,3 +582,12 @@ def test_rounds_of_append_attend_commit():
         accepted = torch.tensor([0, 3, 1, 2, 0, -1], dtype=torch.int32, device=dev())
         lens = torch.where(lens >= 0, lens + accepted + 1, lens).int()
     assert int(st[0]) == 0
+
+
+def test_attend_reports_a_wait_that_runs_out():
+    """A wait on a barrier that nothing arrives at ends after the plan's limit: status, and the next call works."""
+    import logprob_epilogue_gb300 as lpe
+    c = Case(n=[2, 3], lens=[300, 40], prefixes=[150])
+    _, _, st = c.run(c.plan(debug_force_timeout=True, timeout_ns=2_000_000))
+    assert st == lpe.STATUS_TIMEOUT
+    c.check()
