@@ -49,7 +49,12 @@ constexpr float kNegInf = -__builtin_huge_valf();
 constexpr int kThreads = 384;
 constexpr int kWarps = kThreads / 32;
 constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr float kRescale = 8.0f;  // growth of the maximum (log2) that moves it
+// Registers: the softmax warpgroups hold 128 scores per thread.  The split's
+// sum is what the block is launched with, 384 x 168.
+constexpr int kRegsLaunch = 168, kRegsSoftmax = 200, kRegsOther = 104;
+static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * kRegsLaunch, "register split");
 
 // Tensor memory columns: two score tiles, two accumulators.
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256, kColStep = 128;
@@ -131,25 +136,62 @@ __device__ __forceinline__ Seg load_seg(const AttendParams& p, int s) {
     return x;
 }
 
-// First tile of block c's run of `total` tiles over n blocks.
-__device__ __forceinline__ unsigned long long run_start(unsigned long long total, int c, int n) {
-    return total * (unsigned)c / (unsigned)n;
+// `total` tiles cut into one run per block: blocks 0..more-1 take per + 1
+// tiles, the others per.
+struct Runs {
+    unsigned long long total, per;
+    int blocks, more;
+    __device__ __forceinline__ unsigned long long start(int c) const { return per * c + (c < more ? c : more); }
+    __device__ __forceinline__ int block_of(unsigned long long t) const {
+        const unsigned long long big = (per + 1) * more;
+        return t < big ? (int)quotient(t, per + 1) : more + (int)quotient(t - big, per);
+    }
+    static __device__ __forceinline__ unsigned long long quotient(unsigned long long a, unsigned long long b) {
+        return ((a | b) >> 32) == 0 ? (unsigned)a / (unsigned)b : a / b;  // the 64-bit division is slow
+    }
+};
+
+__device__ __forceinline__ Runs make_runs(unsigned long long total, int grid) {
+    Runs r;
+    r.total = total;
+    r.blocks = total < (unsigned long long)grid ? (int)total : grid;
+    r.per = r.blocks > 0 ? Runs::quotient(total, r.blocks) : 0;
+    r.more = (int)(total - r.per * r.blocks);
+    return r;
+}
+
+// Index of row 0 of a piece's part (tile or warpgroup `set`); -1: past the
+// scratch (only overlapping prefixes can ask for that).
+__device__ __forceinline__ long long part_row(const AttendParams& p, bool prefix, long long slot, int set) {
+    if (prefix) return slot < p.sc.prefix_slots ? (slot * 2 + set) * kQTile : -1;
+    if (slot >= p.sc.group_slots) return -1;
+    return p.sc.prefix_slots * 2 * kQTile + (slot * 2 + set) * p.sc.group_rows;
+}
+
+// A part's results lie chunk by chunk, four lanes of the head of every row
+// side by side (a warp's stores are whole lines): index of a float4, `base`
+// the part's first row and `cap` the rows it has room for.
+template <int D>
+__device__ __forceinline__ long long part_chunk(long long base, int cap, int row, int chunk) {
+    return base * (D / 4) + (long long)chunk * cap + row;
 }
 
 // A block's share of one unit.
 struct Piece {
-    bool prefix;
-    int row, rows;       // first row and rows of the unit
-    int kvh, t0, t1, len;
-    const int* table;
-    long long slot;      // of its part, within prefixes or groups
+    int row, rows;      // first row and rows of the unit; rows = 0: the run is done
+    int kvh, tiles;
+    int left;           // tokens from its first tile to the segment's end
+    int part_stride;    // rows between the parts of its two tiles (or warpgroups)
+    long long part;     // row 0 of its first part; -1: past the scratch (only overlapping prefixes can ask for that)
 };
 
-// Walks the pieces of a run of tiles; every role of a block walks its own.
+// Walks the pieces of a run of tiles.
 struct Walk {
     unsigned long long pos, end, off;  // off: tiles before the segment
     int seg, units, cta;               // units: before the segment, of its kind
     Seg s;
+    const int* table;                  // pages of the piece, and its first token
+    long long token;
     __device__ __forceinline__ bool next(const AttendParams& p, Piece& x) {
         while (pos < end) {
             const unsigned long long work = s.work(p);
@@ -157,54 +199,56 @@ struct Walk {
                 off += work;
                 units += s.tiles > 0 ? s.units * p.kv_heads : 0;
                 if (++seg == p.P) units = 0;
-                if (seg >= p.P + p.G) return false;
+                if (seg >= p.P + p.G) break;
                 s = load_seg(p, seg);
                 continue;
             }
-            const unsigned long long rel = pos - off;
-            const int unit = (int)(rel / (unsigned)s.tiles);
-            x.t0 = (int)(rel % (unsigned)s.tiles);
-            const unsigned long long left = end - pos;
-            x.t1 = left < (unsigned long long)(s.tiles - x.t0) ? x.t0 + (int)left : s.tiles;
+            const unsigned long long rel = pos - off, rest = end - pos;
+            const int unit = (int)Runs::quotient(rel, s.tiles);
+            const int t0 = (int)(rel - (unsigned long long)unit * s.tiles);
+            x.tiles = rest < (unsigned long long)(s.tiles - t0) ? (int)rest : s.tiles - t0;
             x.kvh = unit / s.units;
-            const int first = (unit % s.units) * 2 * p.rows_per_tile;
+            const int first = (unit - x.kvh * s.units) * 2 * p.rows_per_tile;
             x.row = s.r0 + first;
             x.rows = s.n - first < 2 * p.rows_per_tile ? s.n - first : 2 * p.rows_per_tile;
-            x.len = s.len;
-            x.prefix = seg < p.P;
-            x.table = x.prefix ? p.prefix_tables + (long long)seg * p.max_prefix_pages
-                               : p.tables + (long long)(seg - p.P) * p.max_pages;
-            x.slot = (long long)units + unit + cta;
-            pos += x.t1 - x.t0;
+            x.left = s.len - t0 * kKTile;
+            const bool prefix = seg < p.P;
+            table = prefix ? p.prefix_tables + (long long)seg * p.max_prefix_pages : p.tables + (long long)(seg - p.P) * p.max_pages;
+            token = (long long)t0 * kKTile;
+            x.part = part_row(p, prefix, (long long)units + unit + cta, 0);
+            x.part_stride = prefix ? kQTile : p.sc.group_rows;
+            pos += x.tiles;
             return true;
         }
+        x.rows = 0;
         return false;
     }
 };
 
-// Index of row 0 of a piece's part (tile or warpgroup `set`); -1: past the
-// scratch (only tables of overlapping prefixes can ask for it).
-__device__ __forceinline__ long long part_row(const AttendParams& p, bool prefix, long long slot, int set) {
-    if (prefix) return slot < p.sc.prefix_slots ? (slot * 2 + set) * kQTile : -1;
-    if (slot >= p.sc.group_slots) return -1;
-    return p.sc.prefix_slots * 2 * kQTile + (slot * 2 + set) * p.sc.group_rows;
-}
+constexpr int kPieces = 8;        // pieces the fetching warp may be ahead
+constexpr int kPieceReaders = 11; // warps that read each: products, two that load queries, eight of softmax
+
+template <int kValue>
+struct Int {
+    static constexpr int value = kValue;
+};
 
 struct Ctl {
-    uint64_t full[10], empty[10];
-    uint64_t q_ready, q_free, s_full[2], p_ready[2], pv_done[2], o_free[2], drain;
+    uint64_t full[10], empty[10], piece_full[kPieces], piece_empty[kPieces];
+    Piece piece[kPieces];
+    uint64_t q_full[2], q_free[2], s_full[2], p_ready[2][2], pv_done[2], o_free[2], drain;
     unsigned long long sum[kWarps][2];
     unsigned long long start_off;
     int start_seg, start_units;
+    Seg start;
     uint32_t tmem;
     int abort;
 };
 
 // The call's tiles and units: every thread sums its share of the segments,
 // the block scans the sums, and the thread that holds the block's first tile
-// names its segment.  Block 0 leaves the offsets for the join.  Returns the
-// total.
-__device__ __forceinline__ unsigned long long plan_run(const AttendParams& p, Ctl* ctl, int& blocks) {
+// names its segment.  Block 0 leaves the offsets for the join.
+__device__ __forceinline__ Runs plan_run(const AttendParams& p, Ctl* ctl) {
     const int S = p.P + p.G, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (S + kThreads - 1) / kThreads;
     const int s0 = tid * per < S ? tid * per : S, s1 = s0 + per < S ? s0 + per : S;
@@ -231,22 +275,141 @@ __device__ __forceinline__ unsigned long long plan_run(const AttendParams& p, Ct
         total += ctl->sum[w][0];
     }
     unsigned long long off = bt + it - tiles, u = bu + iu - units;
-    blocks = total < (unsigned long long)gridDim.x ? (int)total : (int)gridDim.x;
-    const bool mine = (int)blockIdx.x < blocks;
-    const unsigned long long lo = mine ? run_start(total, blockIdx.x, blocks) : ~0ull;
+    const Runs runs = make_runs(total, gridDim.x);
+    const unsigned long long lo = (int)blockIdx.x < runs.blocks ? runs.start(blockIdx.x) : ~0ull;
     if (blockIdx.x == 0 || (lo >= off && lo < off + tiles)) {
         for (int s = s0; s < s1; ++s) {
             const Seg x = load_seg(p, s);
             const unsigned long long work = x.work(p);
             const int before = (int)(s < p.P ? u >> 32 : u & 0xFFFFFFFFull);
             if (blockIdx.x == 0) p.sc.seg_tiles[s] = off, p.sc.seg_units[s] = before;
-            if (lo >= off && lo < off + work) ctl->start_seg = s, ctl->start_units = before, ctl->start_off = off;
+            if (lo >= off && lo < off + work) ctl->start_seg = s, ctl->start_units = before, ctl->start_off = off, ctl->start = x;
             off += work;
             if (x.tiles > 0) u += (unsigned long long)(x.units * p.kv_heads) << (s < p.P ? 32 : 0);
         }
     }
     if (blockIdx.x == 0 && tid == 0) p.sc.seg_tiles[S] = total;
-    return total;
+    return runs;
+}
+
+__device__ __forceinline__ unsigned long long pack2(uint32_t a, uint32_t b) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(unsigned long long v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// One row's running softmax: the maximum, what is subtracted in base 2, the sum.
+struct Row {
+    float m, base, l;
+};
+
+// Softmax of one score tile by one warp, a row per thread; `valid` of the 128
+// tokens exist.  Writes the row's probabilities over the scores and announces
+// the first half of them at p_ready.  False: a wait ran out.
+template <bool kBf16, int D>
+__device__ __forceinline__ bool softmax_tile(uint32_t s_col, uint32_t o_col, int valid, bool first, float c, Row& row, uint64_t* p_ready,
+                                             uint64_t* pv_done, uint32_t pv_parity, unsigned long long limit, volatile int* abort) {
+    using H = Half<kBf16>;
+    // F16 keeps probabilities down to 2^-24: lifting them by 2^6 (at most 2^14 then) keeps those above 2^-30
+    constexpr float kBias = kBf16 ? 0.0f : 6.0f;
+    uint32_t r[4][32];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) tc::tmem_ld32(s_col + b * 32, r[b]);
+    tc::wait_ld();
+#pragma unroll
+    for (int b = 0; b < 4; ++b) tc::tie(r[b]);
+    if (valid < kKTile) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if (b * 32 + e >= valid) r[b][e] = __float_as_uint(kNegInf);
+    }
+    float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int e = 0; e < 32; e += 2)
+            mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(r[b][e]), __uint_as_float(r[b][e + 1]));
+    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+    if (first) {
+        row.m = top;
+        row.base = top == kNegInf ? 0.0f : top * c - kBias;
+        row.l = 0.0f;
+    } else {
+        const bool grow = row.m == kNegInf ? top > row.m : top * c > row.m * c + kRescale;
+        if (__any_sync(kFull, grow)) {
+            float f = 1.0f;
+            if (grow) {
+                const float next = top * c - kBias;
+                if (row.m != kNegInf) f = ex2(row.base - next);
+                row.m = top;
+                row.base = next;
+                row.l *= f;
+            }
+            // the accumulator is this warp's to change once the products so far are in
+            if (!tc::warp_wait(pv_done, pv_parity, limit, abort)) return false;
+            tc::fence_after();
+#pragma unroll 1
+            for (int b = 0; b < D / 32; ++b) {
+                uint32_t o[32];
+                tc::tmem_ld32(o_col + b * 32, o);
+                tc::wait_ld();
+                tc::tie(o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tc::tmem_st32(o_col + b * 32, o);
+            }
+        }
+    }
+    const unsigned long long c2 = pack2(__float_as_uint(c), __float_as_uint(c));
+    const unsigned long long nb2 = pack2(__float_as_uint(-row.base), __float_as_uint(-row.base));
+    unsigned long long sum[2] = {0, 0};
+    // 32 columns at a time: 16 words of probabilities
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            float x, y;
+            unpack2(fma2(pack2(r[b][2 * e], r[b][2 * e + 1]), c2, nb2), x, y);
+            x = ex2(x);
+            y = ex2(y);
+            sum[e & 1] = add2(sum[e & 1], pack2(__float_as_uint(x), __float_as_uint(y)));
+            w[e] = H::pack(x, y);
+        }
+        tc::tmem_st16(s_col + b * 16, w);
+        if (b == 1) {
+            // the first half: its products start while the second is computed
+            tc::wait_st();
+            tc::fence_before();
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) tc::mbar_arrive(p_ready);
+        }
+    }
+    float x, y;
+    unpack2(add2(sum[0], sum[1]), x, y);
+    row.l += x + y;
+    tc::wait_st();
+    return true;
 }
 
 template <bool kBf16, int D>
@@ -261,18 +424,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;");  // the join waits for this grid's end by itself
     const unsigned long long limit = p.timeout_ns;
-    int blocks;
-    const unsigned long long total = plan_run(p, ctl, blocks);
-    if ((int)blockIdx.x >= blocks) return;
+    const Runs runs = plan_run(p, ctl);
+    if ((int)blockIdx.x >= runs.blocks) return;
 
     if (tid == 0) {
         for (int i = 0; i < C::kSlots; ++i) tc::mbar_init(&ctl->full[i], 1), tc::mbar_init(&ctl->empty[i], 1);
-        tc::mbar_init(&ctl->q_ready, 8);
-        tc::mbar_init(&ctl->q_free, 1);
         tc::mbar_init(&ctl->drain, 1);
+        for (int i = 0; i < kPieces; ++i) tc::mbar_init(&ctl->piece_full[i], 1), tc::mbar_init(&ctl->piece_empty[i], kPieceReaders);
         for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&ctl->q_full[i], 2);
+            tc::mbar_init(&ctl->q_free[i], 1);
             tc::mbar_init(&ctl->s_full[i], 1);
-            tc::mbar_init(&ctl->p_ready[i], 4);
+            tc::mbar_init(&ctl->p_ready[i][0], 4);
+            tc::mbar_init(&ctl->p_ready[i][1], 4);
             tc::mbar_init(&ctl->pv_done[i], 1);
             tc::mbar_init(&ctl->o_free[i], 4);
         }
@@ -288,303 +452,348 @@ __global__ void __launch_bounds__(kThreads, 1)
     // test hook: nothing arrives on `drain` before the end, so this wait runs out
     if (p.force_timeout) tc::warp_wait(&ctl->drain, 0, limit, abort);
 
-    Walk walk;
-    walk.cta = blockIdx.x;
-    walk.pos = run_start(total, blockIdx.x, blocks);
-    walk.end = run_start(total, blockIdx.x + 1, blocks);
-    walk.off = ctl->start_off;
-    walk.seg = ctl->start_seg;
-    walk.units = ctl->start_units;
-    walk.s = load_seg(p, walk.seg);
     Piece x;
     bool ok = !p.force_timeout;
-    uint32_t it = 0;  // ring position: K and V tiles fetched (warp 0) or taken (warp 1)
-
-    if (warp == 0) {
-        // ---- pages into the ring
-        constexpr int kHalves = D / 64;
-        const int step = p.page_shift < 7 ? 1 << p.page_shift : kKTile;  // tokens per box
-        while (ok && walk.next(p, x)) {
-            for (int t = x.t0; ok && t < x.t1; ++t) {
-                const int left = x.len - t * kKTile, valid = left < kKTile ? left : kKTile;
-                const int boxes = (valid + step - 1) / step * kHalves;
-                const int tok = lane / kHalves * step, half = lane % kHalves;
-                long long page = 0;
-                int y = 0;
-                if (lane < boxes) {
-                    const long long at = (long long)t * kKTile + tok;
-                    y = (int)(at & ((1 << p.page_shift) - 1));
-                    page = __ldg(&x.table[at >> p.page_shift]);
-                    if (page < 0 || page >= p.num_pages) {
-                        page = p.num_pages;  // outside the map: zeros
-                        atomicOr(p.status, kStatusBadPage);
-                    }
-                }
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv, ++it) {
-                    const uint32_t slot = it % C::kSlots;
-                    ok = tc::warp_wait(&ctl->empty[slot], (it / C::kSlots & 1u) ^ 1u, limit, abort);
-                    if (!ok) break;
-                    if (lane == 0) tc::mbar_expect(&ctl->full[slot], (uint32_t)boxes * step * 128u);
-                    __syncwarp();
-                    if (lane < boxes)
-                        tc::tma_load_4d(ring + slot * C::kTileBytes + half * (kKTile * 128) + tok * 128, kv == 0 ? &k_map : &v_map,
-                                        &ctl->full[slot], half * 64, y, x.kvh, (int)page);
-                }
-            }
-        }
-        // no copy outlives the block, whatever its readers did
-        int none = 0;
-        for (uint32_t i = it > C::kSlots ? it - C::kSlots : 0; i < it; ++i)
-            tc::mbar_wait(&ctl->full[i % C::kSlots], i / C::kSlots & 1u, limit, &none);
-    } else if (warp == 1) {
-        // ---- the products
-        constexpr uint32_t kIdescS = tc::make_idesc(kBf16, false, kQTile, kKTile), kIdescO = tc::make_idesc(kBf16, true, kQTile, D);
-        const uint32_t q_addr = tc::smem_addr(smem), ring_addr = tc::smem_addr(ring);
-        uint32_t pieces = 0, p_phase[2] = {0, 0}, o_phase[2] = {1, 1};
-        auto wait_full = [&](uint32_t i) {
-            return tc::warp_wait(&ctl->full[i % C::kSlots], i / C::kSlots & 1u, limit, abort);
-        };
-        auto scores = [&](int s, int q, uint32_t i) {  // S_s = Q_q K^T
-            if (lane == 0) {
-                const uint64_t a = tc::make_desc(q_addr + q * C::kTileBytes, 16, 1024);
-                const uint64_t b = tc::make_desc(ring_addr + i % C::kSlots * C::kTileBytes, 16, 1024);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint64_t o = (uint64_t)(((k / 4) * (kKTile * 128) + (k % 4) * 32) >> 4);
-                    tc::mma_ss(tmem + kColS + s * kColStep, a + o, b + o, kIdescS, k > 0);
-                }
-                tc::commit(&ctl->s_full[s]);
-            }
-        };
-        // O_s += P_s V; the first product of a piece waits for the accumulator to be read
-        auto values = [&](int s, uint32_t i, bool first, int valid) {
-            if (!tc::warp_wait(&ctl->p_ready[s], p_phase[s], limit, abort)) return false;
-            p_phase[s] ^= 1u;
-            if (first) {
-                if (!tc::warp_wait(&ctl->o_free[s], o_phase[s], limit, abort)) return false;
-                o_phase[s] ^= 1u;
-            }
-            if (valid > 0 && valid < kKTile) {
-                // slots past the length hold anything: zero them, so that 0 * v stays 0
-                unsigned char* v = ring + i % C::kSlots * C::kTileBytes;
-                const int chunks = (kKTile - valid) * 8;
-                for (int c = lane; c < chunks * (D / 64); c += 32) {
-                    const int half = c / chunks, r = c % chunks;
-                    *reinterpret_cast<uint4*>(v + half * (kKTile * 128) + (valid * 8 + r) * 16) = make_uint4(0, 0, 0, 0);
-                }
-                tc::fence_async_shared();
-                __syncwarp();
-            }
-            tc::fence_after();
-            if (lane == 0) {
-                const uint64_t b = tc::make_desc(ring_addr + i % C::kSlots * C::kTileBytes, kKTile * 128, 1024);
-#pragma unroll
-                for (int k = 0; k < kKTile / 16; ++k)
-                    tc::mma_ts(tmem + kColO + s * kColStep, tmem + kColS + s * kColStep + k * 8, b + (uint64_t)(k * 2048 >> 4), kIdescO,
-                               !(first && k == 0));
-                tc::commit(&ctl->pv_done[s]);
-            }
-            return true;
-        };
-        auto release = [&](uint32_t i) {
-            if (lane == 0) tc::commit(&ctl->empty[i % C::kSlots]);
-        };
-        while (ok && walk.next(p, x)) {
-            const int n = x.t1 - x.t0;
-            const bool two = x.rows > p.rows_per_tile;
-            auto valid = [&](int i) { return x.len - (x.t0 + i) * kKTile; };  // V tokens of tile i, if fewer than a tile
-            ok = tc::warp_wait(&ctl->q_ready, pieces++ & 1u, limit, abort);
-            tc::fence_after();
-            if (two) {
-                for (int i = 0; ok && i <= n; ++i) {
-                    const uint32_t k = it + 2 * i, v = it + 2 * i - 1;  // K of tile i, V of tile i - 1
-                    if (i < n) ok = wait_full(k);
-                    if (ok && i > 0) ok = wait_full(v);
-                    for (int s = 0; ok && s < 2; ++s) {
-                        if (i > 0) ok = values(s, v, i == 1, s == 0 ? valid(i - 1) : 0);
-                        if (ok && i < n) scores(s, s, k);
-                    }
-                    if (ok && i > 0) release(v);
-                    if (ok && i < n) release(k);
-                    if (ok && i == n - 1 && lane == 0) tc::commit(&ctl->q_free);
-                }
-            } else {
-                for (int i = 0; ok && i < n + 2; ++i) {
-                    const int s = i & 1;
-                    if (i >= 2) {
-                        const uint32_t v = it + 2 * (i - 2) + 1;
-                        if (i - 2 < n) {
-                            ok = wait_full(v) && values(s, v, i - 2 < 2, valid(i - 2));
-                            if (ok) release(v);
-                        }
-                    }
-                    if (ok && i < n) {
-                        const uint32_t k = it + 2 * i;
-                        ok = wait_full(k);
-                        if (ok) {
-                            tc::fence_after();
-                            scores(s, 0, k);
-                            release(k);
-                        }
-                    }
-                    if (ok && i == n - 1 && lane == 0) tc::commit(&ctl->q_free);
-                }
-            }
-            it += 2 * n;
-        }
-        if (lane == 0) {  // nor does a product
-            int none = 0;
-            tc::commit(&ctl->drain);
-            tc::mbar_wait(&ctl->drain, 0, limit, &none);
-        }
+    uint32_t n_piece = 0;
+    // the next piece, from the fetching warp; false at the end of the run
+    auto next_piece = [&]() {
+        const uint32_t i = n_piece % kPieces;
+        ok = tc::warp_wait(&ctl->piece_full[i], n_piece / kPieces & 1u, limit, abort);
+        if (!ok) return false;
+        x = ctl->piece[i];
         __syncwarp();
-    } else if (warp >= 4) {
+        if (lane == 0) tc::mbar_arrive(&ctl->piece_empty[i]);
+        ++n_piece;
+        return x.rows > 0;
+    };
+
+    // Order of the ring: a tile's K, then its V; among the tiles of one-tile units
+    // V follows the next tile's K, as the products take them.
+    uint32_t it = 0;  // ring position of the next fetch
+
+    // Each role sets its registers inside its own branch: code that both counts reach is held to the smaller.
+    if (warp >= 4) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         // ---- softmax
-        const int wg = (warp - 4) >> 2;             // warpgroup: query tile, or parity of token tiles
-        const int row = (warp & 3) * 32 + lane;     // tile row of this thread
-        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        const int wg = (warp - 4) >> 2, quarter = warp & 3;  // tensor tile; lanes 32 * quarter of tensor memory
+        const uint32_t lanes = (uint32_t)quarter << 21;
         const uint32_t s_col = tmem + lanes + kColS + wg * kColStep, o_col = tmem + lanes + kColO + wg * kColStep;
         const float c = p.scale * kLog2e;
-        // F16 keeps probabilities down to 2^-24: lifting them by 2^6 (at most 2^14 then) keeps those above 2^-30
-        constexpr float kBias = kBf16 ? 0.0f : 6.0f;
-        uint32_t pieces = 0, s_phase = 0, pv = 0;
-        while (ok && walk.next(p, x)) {
+        uint32_t s_phase = 0, pv = 0;
+        int turn = 0;
+        while (ok && next_piece()) {
             const bool two = x.rows > p.rows_per_tile;
-            const int n = x.t1 - x.t0, rt = p.rows_per_tile;
-            const int rows = two ? (wg == 0 ? rt : x.rows - rt) : x.rows;
-            const int valid_rows = rows * p.share;
-            // the query tile: both warpgroups fill half of it when there is one
-            if (pieces > 0) ok = tc::warp_wait(&ctl->q_free, (pieces - 1) & 1u, limit, abort);
-            if (!ok) break;
-            ++pieces;
-            {
-                const int per = row < valid_rows ? row / p.share : 0, head = x.kvh * p.share + (row < valid_rows ? row % p.share : 0);
-                const T* src = reinterpret_cast<const T*>(p.q) + (long long)(x.row + (two ? wg * rt : 0) + per) * p.q_stride + (long long)head * D;
-                unsigned char* dst = smem + (two ? wg * C::kTileBytes : 0) + row * 128;
-                constexpr int kChunks = D / 8;
-                const int c0 = two ? 0 : wg * (kChunks / 2), cn = two ? kChunks : kChunks / 2;
-#pragma unroll 8
-                for (int i = 0; i < cn; ++i) {
-                    const int ch = c0 + i;
-                    uint4 w = make_uint4(0, 0, 0, 0);
-                    if (row < valid_rows) w = __ldg(reinterpret_cast<const uint4*>(src + ch * 8));
-                    *reinterpret_cast<uint4*>(dst + (ch >> 3) * (kKTile * 128) + (((ch & 7) ^ (row & 7)) << 4)) = w;
-                }
-            }
-            tc::fence_async_shared();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&ctl->q_ready);
-
-            const bool live = (warp & 3) * 32 < valid_rows;  // any row of this warp
-            float m = kNegInf, base = 0.0f, l = 0.0f;        // maximum; what is subtracted in base 2; sum
-            const int first = two ? 0 : wg, stride = two ? 1 : 2;
+            const int n = x.tiles, rt = p.rows_per_tile, row = quarter * 32 + lane;  // row of the query tile
+            const int valid_rows = (two ? (wg == 0 ? rt : x.rows - rt) : x.rows) * p.share;
+            const bool live = quarter * 32 < valid_rows;  // any row of this warp
+            const int first = two ? 0 : wg ^ turn, stride = two ? 1 : 2;
+            if (!two) turn ^= n & 1;
+            Row st = {kNegInf, 0.0f, 0.0f};
             for (int i = first; i < n; i += stride) {
                 ok = tc::warp_wait(&ctl->s_full[wg], s_phase, limit, abort);
                 if (!ok) break;
                 s_phase ^= 1u;
-                tc::fence_after();
+                uint64_t* ready = ctl->p_ready[wg];
                 if (live) {
-                    uint32_t r[4][32];
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) tc::tmem_ld32(s_col + b * 32, r[b]);
-                    tc::wait_ld();
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) tc::tie(r[b]);
-                    const int valid = x.len - (x.t0 + i) * kKTile;
-                    if (valid < kKTile) {
-#pragma unroll
-                        for (int b = 0; b < 4; ++b)
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (b * 32 + e >= valid) r[b][e] = __float_as_uint(kNegInf);
-                    }
-                    float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-#pragma unroll
-                    for (int b = 0; b < 4; ++b)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(r[b][e]));
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    if (i == first) {
-                        m = top;
-                        base = m == kNegInf ? 0.0f : m * c - kBias;
-                    } else {
-                        const bool grow = m == kNegInf ? top > m : top * c > m * c + kRescale;
-                        if (__any_sync(kFull, grow)) {
-                            float f = 1.0f;
-                            if (grow) {
-                                const float next = top * c - kBias;
-                                if (m != kNegInf) f = ex2(base - next);
-                                m = top;
-                                base = next;
-                                l *= f;
-                            }
-                            // the accumulator is this warp's to change once the products so far are in
-                            ok = tc::warp_wait(&ctl->pv_done[wg], (pv - 1) & 1u, limit, abort);
-                            if (!ok) break;
-                            tc::fence_after();
-#pragma unroll
-                            for (int b = 0; b < D / 32; ++b) {
-                                uint32_t o[32];
-                                tc::tmem_ld32(o_col + b * 32, o);
-                                tc::wait_ld();
-                                tc::tie(o);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tc::tmem_st32(o_col + b * 32, o);
-                            }
-                            tc::wait_st();
-                        }
-                    }
-                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int b = 0; b < 4; b += 2) {
-                        uint32_t w[32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float a0 = ex2(fmaf(__uint_as_float(r[b + e / 16][2 * (e % 16)]), c, -base));
-                            const float a1 = ex2(fmaf(__uint_as_float(r[b + e / 16][2 * (e % 16) + 1]), c, -base));
-                            sum[(2 * e) & 3] += a0;
-                            sum[(2 * e + 1) & 3] += a1;
-                            w[e] = H::pack(a0, a1);
-                        }
-                        tc::tmem_st32(s_col + b * 16, w);
-                    }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    tc::wait_st();
+                    tc::fence_after();
+                    ok = softmax_tile<kBf16, D>(s_col, o_col, x.left - i * kKTile, i == first, c, st, &ready[0], &ctl->pv_done[wg],
+                                                (pv - 1) & 1u, limit, abort);
+                    if (!ok) break;
+                    tc::fence_before();
+                    __syncwarp();
+                } else if (lane == 0) {
+                    tc::mbar_arrive(&ready[0]);
                 }
+                if (lane == 0) tc::mbar_arrive(&ready[1]);
                 ++pv;
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&ctl->p_ready[wg]);
             }
             if (!ok) break;
-            if (first < n) {
-                ok = tc::warp_wait(&ctl->pv_done[wg], (pv - 1) & 1u, limit, abort);
-                if (!ok) break;
+            const long long part = x.part + wg * x.part_stride;
+            const bool store = row < valid_rows && x.part >= 0;
+            if (first >= n) {  // no tile of this piece was this warpgroup's
+                if (store) p.sc.part_ml[part + row] = make_float2(kNegInf, 0.0f);
+                continue;
+            }
+            ok = tc::warp_wait(&ctl->pv_done[wg], (pv - 1) & 1u, limit, abort);
+            if (!ok) break;
+            if (live) {
                 tc::fence_after();
-                if (live) {
-                    const long long at = part_row(p, x.prefix, x.slot, wg) + row;
-                    const bool store = row < valid_rows && at >= row;
-                    if (store) p.sc.part_ml[at] = make_float2(m == kNegInf ? kNegInf : base, l);
-                    float4* dst = reinterpret_cast<float4*>(p.sc.part_o + (store ? at : 0) * D);
+                if (store) p.sc.part_ml[part + row] = make_float2(st.m == kNegInf ? kNegInf : st.base, st.l);
+                float4* dst = reinterpret_cast<float4*>(p.sc.part_o) + part_chunk<D>(part, x.part_stride, row, 0);
 #pragma unroll
-                    for (int b = 0; b < D / 32; ++b) {
-                        uint32_t o[32];
-                        tc::tmem_ld32(o_col + b * 32, o);
-                        tc::wait_ld();
-                        tc::tie(o);
-                        if (store) {
+                for (int b = 0; b < D / 32; ++b) {
+                    uint32_t o[32];
+                    tc::tmem_ld32(o_col + b * 32, o);
+                    tc::wait_ld();
+                    tc::tie(o);
+                    if (store) {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                dst[b * 8 + e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                                             __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
-                        }
+                        for (int e = 0; e < 8; ++e)
+                            dst[(b * 8 + e) * x.part_stride] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                                           __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
                     }
                 }
                 tc::fence_before();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&ctl->o_free[wg]);
+            }
+            if (lane == 0) tc::mbar_arrive(&ctl->o_free[wg]);
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        if (warp == 0) {
+            // ---- pages into the ring
+            constexpr int kHalves = D / 64;
+            const int step = p.page_shift < 7 ? 1 << p.page_shift : kKTile;  // tokens per box
+            const int tok = lane / kHalves * step, half = lane % kHalves;
+            Walk walk;
+            walk.cta = blockIdx.x;
+            walk.pos = runs.start(blockIdx.x);
+            walk.end = runs.start(blockIdx.x + 1);
+            walk.off = ctl->start_off;
+            walk.seg = ctl->start_seg;
+            walk.units = ctl->start_units;
+            walk.s = ctl->start;
+            int late_boxes = 0, late_y = 0, late_kvh = 0, late_page = 0;  // of the tile whose V is still to come
+            auto fetch = [&](const CUtensorMap* map, int n, int fy, int fh, int fp) {
+                const uint32_t slot = it % C::kSlots;
+                if (!tc::warp_wait(&ctl->empty[slot], (it / C::kSlots & 1u) ^ 1u, limit, abort)) return false;
+                if (lane == 0) tc::mbar_expect(&ctl->full[slot], (uint32_t)n * step * 128u);
+                __syncwarp();
+                if (lane < n)
+                    tc::tma_load_4d(ring + slot * C::kTileBytes + half * (kKTile * 128) + tok * 128, map, &ctl->full[slot], half * 64, fy, fh, fp);
+                ++it;
+                return true;
+            };
+            for (bool more = ok; ok && more;) {
+                more = walk.next(p, x);
+                const uint32_t pi = n_piece % kPieces;
+                ok = tc::warp_wait(&ctl->piece_empty[pi], (n_piece / kPieces & 1u) ^ 1u, limit, abort);
+                if (!ok) break;
+                if (lane == 0) {
+                    ctl->piece[pi] = x;
+                    tc::mbar_arrive(&ctl->piece_full[pi]);
+                }
+                ++n_piece;
+                if (!more) break;
+                const bool two = x.rows > p.rows_per_tile;
+                // the pages of the next tile are read before this tile's waits
+                auto page_of = [&](int i) {
+                    const long long at = walk.token + i * kKTile + tok;
+                    return i < x.tiles && i * kKTile + tok < x.left ? __ldg(&walk.table[at >> p.page_shift]) : 0;
+                };
+                int next_page = page_of(0);
+                for (int i = 0; ok && i < x.tiles; ++i) {
+                    const int left = x.left - i * kKTile, valid = left < kKTile ? left : kKTile;
+                    const int boxes = (valid + step - 1) / step * kHalves, kvh = x.kvh;
+                    const int y = (int)((walk.token + i * kKTile + tok) & ((1 << p.page_shift) - 1));
+                    int page = next_page;
+                    next_page = page_of(i + 1);
+                    if (lane < boxes && (page < 0 || page >= p.num_pages)) {
+                        page = (int)p.num_pages;  // outside the map: zeros
+                        atomicOr(p.status, kStatusBadPage);
+                    }
+                    if (two) {
+                        if (late_boxes > 0) ok = fetch(&v_map, late_boxes, late_y, late_kvh, late_page);
+                        late_boxes = 0;
+                        ok = ok && fetch(&k_map, boxes, y, kvh, page) && fetch(&v_map, boxes, y, kvh, page);
+                    } else {
+                        ok = fetch(&k_map, boxes, y, kvh, page);
+                        if (ok && late_boxes > 0) ok = fetch(&v_map, late_boxes, late_y, late_kvh, late_page);
+                        late_boxes = boxes, late_y = y, late_kvh = kvh, late_page = page;
+                    }
+                }
+            }
+            if (ok && late_boxes > 0) fetch(&v_map, late_boxes, late_y, late_kvh, late_page);
+            // no copy outlives the block, whatever its readers did
+            int none = 0;
+            for (uint32_t i = it > C::kSlots ? it - C::kSlots : 0; i < it; ++i)
+                tc::mbar_wait(&ctl->full[i % C::kSlots], i / C::kSlots & 1u, limit, &none);
+        } else if (warp == 1) {
+            // ---- the products, issued by one thread
+            if (lane == 0) {
+                constexpr uint32_t kIdescS = tc::make_idesc(kBf16, false, kQTile, kKTile), kIdescO = tc::make_idesc(kBf16, true, kQTile, D);
+                // This thread's own instructions must hide behind the products (64 cycles each, few in the queue), so ring
+                // positions step without divisions and everything about a tensor tile is in registers of its own.
+                const uint64_t q_desc = tc::make_desc(tc::smem_addr(smem), 16, 1024);
+                const uint64_t k_desc = tc::make_desc(tc::smem_addr(ring), 16, 1024), v_desc = tc::make_desc(tc::smem_addr(ring), kKTile * 128, 1024);
+                constexpr uint32_t kTileStep = C::kTileBytes >> 4;
+                uint32_t q_pos = 0, slot = 0, phase = 0;  // the next ring position
+                uint32_t p_phase[2] = {0, 0}, o_phase[2] = {1, 1};
+                // The tiles whose scores are in S_s and whose values are still to be multiplied: tokens (0: none), ring
+                // position of V, whether the piece's first, the first and the last to use V.
+                int valid[2] = {0, 0};
+                uint32_t v_slot[2] = {0, 0}, v_phase[2] = {0, 0};
+                bool begins[2] = {}, cleans[2] = {}, releases[2] = {};
+                int turn = 0, late = -1;  // tensor tile of the next one-tile unit's tile; the one whose V has no ring position yet
+                auto wait = [&](uint64_t* bar, uint32_t parity) { return tc::mbar_wait(bar, parity, limit, abort); };
+                auto advance = [&]() {
+                    if (++slot == C::kSlots) slot = 0, phase ^= 1u;
+                };
+                auto place_late = [&]() {  // V of the late tile takes the next ring position
+                    if (late == 0) v_slot[0] = slot, v_phase[0] = phase;
+                    else v_slot[1] = slot, v_phase[1] = phase;
+                    advance();
+                };
+                auto scores = [&](auto tile, uint32_t q, uint32_t k_slot) {  // S_s = Q K^T
+                    constexpr int s = decltype(tile)::value;
+                    const uint64_t a = q_desc + q * kTileStep, b = k_desc + k_slot * kTileStep;
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint64_t o = (uint64_t)(((k / 4) * (kKTile * 128) + (k % 4) * 32) >> 4);
+                        tc::mma_ss(tmem + kColS + s * kColStep, a + o, b + o, kIdescS, k > 0);
+                    }
+                    tc::commit(&ctl->s_full[s]);
+                };
+                // O_s += P_s V, half of the tokens at a time; the first product of a piece waits for the accumulator to be read
+                auto values = [&](auto tile) {
+                    constexpr int s = decltype(tile)::value;
+                    if (valid[s] == 0) return true;
+                    const int have = valid[s];
+                    valid[s] = 0;
+                    if (cleans[s]) {  // the first to use V
+                        if (!wait(&ctl->full[v_slot[s]], v_phase[s])) return false;
+                        if ((have & 15) != 0) {
+                            // slots past the length hold anything: zero those that the last 16 rows of V take in, so that 0 * v stays 0
+                            unsigned char* v = ring + v_slot[s] * C::kTileBytes;
+                            for (int r = have; r < ((have + 15) & ~15); ++r)
+#pragma unroll
+                                for (int h = 0; h < D / 8; ++h)
+                                    *reinterpret_cast<uint4*>(v + (h >> 3) * (kKTile * 128) + r * 128 + (h & 7) * 16) = make_uint4(0, 0, 0, 0);
+                            tc::fence_async_shared();
+                        }
+                    }
+                    if (begins[s]) {
+                        if (!wait(&ctl->o_free[s], o_phase[s])) return false;
+                        o_phase[s] ^= 1u;
+                    }
+                    const uint64_t b = v_desc + v_slot[s] * kTileStep;
+                    const uint32_t o_t = tmem + kColO + s * kColStep, p_t = tmem + kColS + s * kColStep;
+                    if (!wait(&ctl->p_ready[s][0], p_phase[s])) return false;
+                    tc::fence_after();
+                    if (have > kKTile - 16) {
+#pragma unroll
+                        for (int k = 0; k < kKTile / 32; ++k)
+                            tc::mma_ts(o_t, p_t + k * 8, b + (uint64_t)(k * 2048 >> 4), kIdescO, k > 0 || !begins[s]);
+                        if (!wait(&ctl->p_ready[s][1], p_phase[s])) return false;
+                        tc::fence_after();
+#pragma unroll
+                        for (int k = kKTile / 32; k < kKTile / 16; ++k)
+                            tc::mma_ts(o_t, p_t + k * 8, b + (uint64_t)(k * 2048 >> 4), kIdescO, true);
+                    } else {
+                        if (!wait(&ctl->p_ready[s][1], p_phase[s])) return false;
+                        tc::fence_after();
+                        for (int k = 0; k < (have + 15) >> 4; ++k)
+                            tc::mma_ts(o_t, p_t + k * 8, b + (uint64_t)(k * 2048 >> 4), kIdescO, k > 0 || !begins[s]);
+                    }
+                    p_phase[s] ^= 1u;
+                    tc::commit(&ctl->pv_done[s]);
+                    if (releases[s]) tc::commit(&ctl->empty[v_slot[s]]);
+                    return true;
+                };
+                constexpr Int<0> kTile0{};
+                constexpr Int<1> kTile1{};
+                while (ok) {
+                    const uint32_t pi = n_piece % kPieces;
+                    ok = wait(&ctl->piece_full[pi], n_piece / kPieces & 1u);
+                    if (!ok) break;
+                    x = ctl->piece[pi];
+                    tc::mbar_arrive(&ctl->piece_empty[pi]);
+                    ++n_piece;
+                    if (x.rows == 0) break;
+                    const bool two = x.rows > p.rows_per_tile;
+                    if (two && late >= 0) {
+                        place_late();
+                        late = -1;
+                    }
+                    for (int j = 0; ok && j <= (two ? 1 : 0); ++j) ok = wait(&ctl->q_full[(q_pos + j) & 1u], (q_pos + j) >> 1 & 1u);
+                    if (!ok) break;
+                    const uint32_t q0 = q_pos & 1u;
+                    int left = x.left;
+                    if (two) {
+                        auto step = [&](auto tile, uint32_t k_slot, uint32_t k_phase, bool first) {
+                            constexpr int s = decltype(tile)::value;
+                            if (!values(tile)) return false;
+                            if (s == 0 && !wait(&ctl->full[k_slot], k_phase)) return false;
+                            tc::fence_after();
+                            scores(tile, q0 ^ s, k_slot);
+                            valid[s] = left < kKTile ? left : kKTile;
+                            v_slot[s] = slot, v_phase[s] = phase;
+                            begins[s] = first, cleans[s] = s == 0, releases[s] = s == 1;
+                            return true;
+                        };
+                        for (int i = 0; i < x.tiles; ++i) {
+                            const uint32_t k_slot = slot, k_phase = phase;
+                            advance();
+                            ok = step(kTile0, k_slot, k_phase, i == 0) && step(kTile1, k_slot, k_phase, i == 0);
+                            if (!ok) break;
+                            tc::commit(&ctl->empty[k_slot]);
+                            advance();
+                            left -= kKTile;
+                        }
+                    } else {
+                        auto step = [&](auto tile, bool first) {
+                            constexpr int s = decltype(tile)::value;
+                            const uint32_t k_slot = slot, k_phase = phase;
+                            advance();
+                            if (late >= 0) place_late();
+                            if (!values(tile) || !wait(&ctl->full[k_slot], k_phase)) return false;
+                            tc::fence_after();
+                            scores(tile, q0, k_slot);
+                            tc::commit(&ctl->empty[k_slot]);
+                            valid[s] = left < kKTile ? left : kKTile;
+                            begins[s] = first, cleans[s] = releases[s] = true;
+                            late = s;
+                            return true;
+                        };
+                        for (int i = 0; i < x.tiles; ++i) {
+                            ok = turn == 0 ? step(kTile0, i < 2) : step(kTile1, i < 2);
+                            if (!ok) break;
+                            turn ^= 1;
+                            left -= kKTile;
+                        }
+                    }
+                    if (ok) {
+                        tc::commit(&ctl->q_free[q0]);
+                        if (two) tc::commit(&ctl->q_free[q0 ^ 1u]);
+                    }
+                    q_pos += two ? 2 : 1;
+                }
+                if (late >= 0) place_late();
+                // in the order of their V
+                if (ok) ok = late == 0 ? values(kTile1) && values(kTile0) : values(kTile0) && values(kTile1);
+                int none = 0;  // no product outlives the block
+                tc::commit(&ctl->drain);
+                tc::mbar_wait(&ctl->drain, 0, limit, &none);
+            }
+            __syncwarp();
+        } else if (warp < 4) {
+            // ---- query tiles into shared memory, ahead of the products
+            const int t64 = tid - 64;
+            uint32_t q_pos = 0;
+            while (ok && next_piece()) {
+                const bool two = x.rows > p.rows_per_tile;
+                for (int j = 0; ok && j <= (two ? 1 : 0); ++j, ++q_pos) {
+                    const uint32_t b = q_pos & 1u;
+                    ok = tc::warp_wait(&ctl->q_free[b], (q_pos >> 1 & 1u) ^ 1u, limit, abort);
+                    if (!ok) break;
+                    const int rows = two ? (j == 0 ? p.rows_per_tile : x.rows - p.rows_per_tile) : x.rows;
+                    const int valid = rows * p.share;
+                    constexpr int kChunks = D / 8;
+                    const T* src = reinterpret_cast<const T*>(p.q) + (long long)(x.row + j * p.rows_per_tile) * p.q_stride + (long long)x.kvh * p.share * D;
+                    // straight into shared memory, all in flight; rows past the last are zeros
+                    const uint32_t at0 = tc::smem_addr(smem + b * C::kTileBytes);
+                    for (int i = t64; i < kQTile * kChunks; i += 64) {
+                        const int row = i / kChunks, ch = i % kChunks;
+                        const int per = row < valid ? (row * p.share_inv) >> 16 : 0, head = row < valid ? row - per * p.share : 0;
+                        const T* from = src + per * p.q_stride + head * D + ch * 8;
+                        const uint32_t at = at0 + (ch >> 3) * (kQTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+                        tc::copy16(at, from, row < valid ? 16 : 0);
+                    }
+                    tc::copies_done();
+                    tc::fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&ctl->q_full[b]);
+                }
             }
         }
     }
@@ -614,6 +823,11 @@ __device__ __forceinline__ void load_lane(const void* base, long long elem, floa
 template <int D>
 struct Acc {
     float o[D / 32], m, l;
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) o[e] = 0.0f;
+        m = kNegInf, l = 0.0f;
+    }
     __device__ __forceinline__ void add(float s, float w, const float (&v)[D / 32]) {  // a part: maximum s, sum w, result v
         const float top = fmaxf(m, s), base = top == kNegInf ? 0.0f : top;
         const float f = ex2(m - base), g = ex2(s - base);
@@ -624,100 +838,150 @@ struct Acc {
     }
 };
 
-// Joins the parts of one segment for tile-row `row` of the unit that holds row
-// `rel` of the segment.
 template <int D>
-__device__ __forceinline__ void join_parts(const AttendParams& p, Acc<D>& a, int seg, int rel, int head, int lane,
-                                           unsigned long long total, int blocks) {
+__device__ __forceinline__ void load_part(const float* parts, long long base, int cap, int row, int lane, float (&v)[D / 32]) {
+    if constexpr (D == 128) {
+        const float4 w = reinterpret_cast<const float4*>(parts)[part_chunk<D>(base, cap, row, lane)];
+        v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+    } else {
+        const float2 w = reinterpret_cast<const float2*>(parts)[part_chunk<D>(base, cap, row, lane >> 1) * 2 + (lane & 1)];
+        v[0] = w.x, v[1] = w.y;
+    }
+}
+
+constexpr int kBatch = 4;  // parts or tokens in flight per warp
+
+// Joins the parts of one segment for the unit row of query head `head` of the
+// segment's row `rel`; warp `sub` of `warps` takes every warps-th part.
+template <int D>
+__device__ __forceinline__ void join_parts(const AttendParams& p, Acc<D>& a, int seg, int rel, int head, int lane, int sub, int warps,
+                                           const Runs& runs) {
     const Seg s = load_seg(p, seg);
     if (s.tiles == 0) return;
     const bool prefix = seg < p.P;
     const int rt = p.rows_per_tile, u = rel / (2 * rt), left = s.n - u * 2 * rt;
     const bool two = left > rt;
     const int in = rel - u * 2 * rt, kvh = head / p.share;
+    const int sets = two ? 1 : 2;  // a unit of one tile: a part of each warpgroup
     const int row = (two ? in % rt : in) * p.share + head % p.share;
-    const unsigned long long begin = p.sc.seg_tiles[seg] + (unsigned long long)(kvh * s.units + u) * s.tiles, end = begin + s.tiles;
+    const unsigned long long begin = p.sc.seg_tiles[seg] + (unsigned long long)(kvh * s.units + u) * s.tiles;
     const long long slot = (long long)p.sc.seg_units[seg] + kvh * s.units + u;
     // the blocks whose runs hold the unit's first and last tile
-    const int c0 = (int)(((begin + 1) * (unsigned)blocks - 1) / total), c1 = (int)((end * (unsigned)blocks - 1) / total);
-    const int sets = two ? 1 : 2;
-    for (int k = 0; k < (c1 - c0 + 1) * sets; ++k) {
-        const int c = c0 + k / sets, set = two ? in / rt : k % sets;
-        if (!two && set == 1) {  // the second warpgroup had a tile only in a run of two or more
-            const unsigned long long lo = run_start(total, c, blocks), hi = run_start(total, c + 1, blocks);
-            if ((hi < end ? hi : end) - (lo > begin ? lo : begin) < 2) continue;
+    const int c0 = runs.block_of(begin), c1 = runs.block_of(begin + s.tiles - 1);
+    const int count = (c1 - c0 + 1) * sets;
+    for (int k0 = sub; k0 < count; k0 += warps * kBatch) {
+        float2 ml[kBatch];
+        float v[kBatch][D / 32];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int k = k0 + b * warps;
+            ml[b] = make_float2(kNegInf, 0.0f);
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) v[b][e] = 0.0f;
+            if (k < count) {
+                const int piece = k / sets, set = k - piece * sets;
+                const long long base = part_row(p, prefix, slot + c0 + piece, two ? in / rt : set);
+                if (base >= 0) {
+                    ml[b] = p.sc.part_ml[base + row];
+                    load_part<D>(p.sc.part_o, base, prefix ? kQTile : p.sc.group_rows, row, lane, v[b]);
+                }
+            }
         }
-        const long long at = part_row(p, prefix, slot + c, set);
-        if (at < 0) continue;
-        const float2 ml = p.sc.part_ml[at + row];
-        float v[D / 32];
-        const float* src = p.sc.part_o + (at + row) * D + lane * (D / 32);
-        if constexpr (D == 128) {
-            const float4 w = *reinterpret_cast<const float4*>(src);
-            v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
-        } else {
-            const float2 w = *reinterpret_cast<const float2*>(src);
-            v[0] = w.x, v[1] = w.y;
-        }
-        a.add(ml.x, ml.y, v);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+            if (ml[b].x != kNegInf || ml[b].y != 0.0f) a.add(ml[b].x, ml[b].y, v[b]);  // else nothing was written
     }
 }
 
-// One warp per (row, query head): the parts of the row's prefix and of its
-// group's committed tokens, then the round's own tokens that the row sees.
-template <bool kBf16, int D>
+// kSub warps per (row, query head): the round's own tokens that the row sees,
+// then the parts of the row's prefix and of its group's committed tokens.
+template <bool kBf16, int D, int kSub>
 __global__ void __launch_bounds__(kJoinThreads) lp_attend_join_kernel(const AttendParams p) {
     using H = Half<kBf16>;
     using T = typename H::T;
     constexpr int kE = D / 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int row = blockIdx.x, head = blockIdx.y * (kJoinThreads / 32) + warp;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % kSub;
+    const int row = blockIdx.x, head = blockIdx.y * (kJoinWarps / kSub) + warp / kSub;
     const int g = block_find_group(p.indptr, p.G, row);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (g < 0 || g >= p.G || head >= p.q_heads) return;
-    if (row < __ldg(&p.indptr[g]) || row >= __ldg(&p.indptr[g + 1])) return;  // two entries claim the row
-    const Group grp = load_group(p, g);
+    bool mine = g >= 0 && g < p.G && head < p.q_heads;
+    mine = mine && row >= __ldg(&p.indptr[g]) && row < __ldg(&p.indptr[g + 1]);  // else two entries claim the row
     Acc<D> a;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) a.o[e] = 0.0f;
-    a.m = kNegInf, a.l = 0.0f;
+    a.clear();
+    Group grp = {0, 0, 0, false};
+    if (mine) grp = load_group(p, g);
     if (grp.n > 0) {
-        const unsigned long long total = p.sc.seg_tiles[p.P + p.G];
-        const int blocks = total < (unsigned long long)p.grid ? (int)total : p.grid;
-        for (int i = 0; i < p.P; ++i) {
-            const Prefix x = load_prefix(p, i);
-            if (x.bad || g < x.g0 || g >= x.g1) continue;
-            join_parts<D>(p, a, i, row - x.r0, head, lane, total, blocks);
-            break;
-        }
-        join_parts<D>(p, a, p.P + g, row - grp.r0, head, lane, total, blocks);
         float q[kE];
         load_lane<kBf16, D>(p.q, row * p.q_stride + (long long)head * D + lane * kE, q);
         const float c = p.scale * kLog2e;
         const int* table = p.tables + (long long)g * p.max_pages;
         const int j = row - grp.r0, kvh = head / p.share;
         const unsigned mask = p.row_masks != nullptr ? __ldg(&p.row_masks[row]) : (2u << j) - 1u;
-        for (int i = 0; i < grp.n; ++i) {
-            if (!(mask >> i & 1u)) continue;
-            const int t = grp.len + i;
-            const int page = __ldg(&table[t >> p.page_shift]);
-            float k[kE] = {}, v[kE] = {};
-            if (page >= 0 && page < p.num_pages) {
-                const long long at =
-                    (((((long long)page * p.kv_heads + kvh) << p.page_shift) + (t & ((1 << p.page_shift) - 1))) * D) + lane * kE;
-                load_lane<kBf16, D>(p.k_cache, at, k);
-                load_lane<kBf16, D>(p.v_cache, at, v);
-            } else if (lane == 0) {
-                atomicOr(p.status, kStatusBadPage);
+        for (int i0 = sub; i0 < grp.n; i0 += kSub * kBatch) {
+            float k[kBatch][kE], v[kBatch][kE], s[kBatch];
+            bool sees[kBatch];
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                const int i = i0 + b * kSub;
+                sees[b] = i < grp.n && (mask >> i & 1u);
+#pragma unroll
+                for (int e = 0; e < kE; ++e) k[b][e] = v[b][e] = 0.0f;
+                if (sees[b]) {
+                    const int t = grp.len + i;
+                    const int page = __ldg(&table[t >> p.page_shift]);
+                    if (page >= 0 && page < p.num_pages) {
+                        const long long at =
+                            (((((long long)page * p.kv_heads + kvh) << p.page_shift) + (t & ((1 << p.page_shift) - 1))) * D) + lane * kE;
+                        load_lane<kBf16, D>(p.k_cache, at, k[b]);
+                        load_lane<kBf16, D>(p.v_cache, at, v[b]);
+                    } else if (lane == 0) {
+                        atomicOr(p.status, kStatusBadPage);
+                    }
+                }
             }
-            float s = 0.0f;
 #pragma unroll
-            for (int e = 0; e < kE; ++e) s = fmaf(q[e], k[e], s);
+            for (int b = 0; b < kBatch; ++b) {
+                s[b] = 0.0f;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-            a.add(s * c, 1.0f, v);
+                for (int e = 0; e < kE; ++e) s[b] = fmaf(q[e], k[b][e], s[b]);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) s[b] += __shfl_xor_sync(kFull, s[b], o);
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b)
+                if (sees[b]) a.add(s[b] * c, 1.0f, v[b]);
         }
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (grp.n > 0) {
+        const Runs runs = make_runs(p.sc.seg_tiles[p.P + p.G], p.grid);
+        for (int i = 0; i < p.P; ++i) {
+            const Prefix x = load_prefix(p, i);
+            if (x.bad || g < x.g0 || g >= x.g1) continue;
+            join_parts<D>(p, a, i, row - x.r0, head, lane, sub, kSub, runs);
+            break;
+        }
+        join_parts<D>(p, a, p.P + g, row - grp.r0, head, lane, sub, kSub, runs);
+    }
+    if constexpr (kSub > 1) {  // the warps' sums, in the order of the warps
+        __shared__ float4 part[kJoinWarps][32];
+        __shared__ float2 part_ml[kJoinWarps];
+        part[warp][lane] = make_float4(a.o[0], a.o[1], kE > 2 ? a.o[kE - 2] : 0.0f, kE > 2 ? a.o[kE - 1] : 0.0f);
+        if (lane == 0) part_ml[warp] = make_float2(a.m, a.l);
+        __syncthreads();
+        if (sub != 0) return;
+#pragma unroll
+        for (int w = 1; w < kSub; ++w) {
+            const float4 o = part[warp + w][lane];
+            const float2 ml = part_ml[warp + w];
+            float v[kE];
+            v[0] = o.x, v[1] = o.y;
+            if constexpr (kE > 2) v[2] = o.z, v[3] = o.w;
+            if (ml.x != kNegInf || ml.y != 0.0f) a.add(ml.x, ml.y, v);
+        }
+    }
+    if (!mine) return;
     const float inv = a.l > 0.0f ? 1.0f / a.l : (a.l == 0.0f ? 0.0f : a.l);
     T* dst = reinterpret_cast<T*>(p.out) + row * p.out_stride + (long long)head * D + lane * kE;
     if constexpr (D == 128) {
@@ -746,16 +1010,21 @@ cudaError_t launch(const AttendParams& p, const CUtensorMap& k_map, const CUtens
     lp_attend_kernel<kBf16, D><<<p.grid, kThreads, smem_bytes<D>(), stream>>>(p, k_map, v_map);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    // few rows: several warps share a row's parts
+    const long long heads = (long long)p.rows * p.q_heads;
+    const int sub = heads <= 8 * p.grid ? 8 : (heads <= 32 * p.grid ? 2 : 1);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3((unsigned)p.rows, (unsigned)((p.q_heads + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
+    lc.gridDim = dim3((unsigned)p.rows, (unsigned)((p.q_heads * sub + kJoinWarps - 1) / kJoinWarps));
     lc.blockDim = dim3(kJoinThreads);
     lc.stream = stream;
     lc.attrs = attr;
     lc.numAttrs = 1;
-    return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D>, p);
+    if (sub == 8) return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 8>, p);
+    if (sub == 2) return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 2>, p);
+    return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 1>, p);
 }
 
 }  // namespace

@@ -320,6 +320,7 @@ int lp_attend(lp_attn_t plan, const lp_attend_io* io, void* stream) {
     p.page_shift = plan->page_shift;
     p.num_pages = d.num_pages;
     p.rows_per_tile = lp::kQTile / p.share;
+    p.share_inv = (65536 + p.share - 1) / p.share;
     p.grid = plan->grid;
     p.sc = plan->sc;
     p.timeout_ns = (unsigned long long)(d.timeout_ns > 0 ? d.timeout_ns : lp::kDefaultTimeoutNs);

@@ -62,6 +62,7 @@ struct AttendParams {
     int max_group_rows, max_pages, max_prefix_pages, page_shift;
     long long num_pages;
     int rows_per_tile;                     // kQTile / share
+    int share_inv;                         // row / share = row * share_inv >> 16 for rows of a tile
     int grid;                              // blocks of the attention kernel
     AttendScratch sc;
     unsigned long long timeout_ns;
