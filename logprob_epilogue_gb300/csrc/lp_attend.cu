@@ -226,22 +226,17 @@ struct Walk {
 };
 
 constexpr int kPieces = 8;        // pieces the fetching warp may be ahead
-constexpr int kPieceReaders = 11; // warps that read each: products, two that load queries, eight of softmax
-
-template <int kValue>
-struct Int {
-    static constexpr int value = kValue;
-};
+constexpr int kPieceReaders = 11; // warps that read each: two of the products, one that loads queries, eight of softmax
 
 struct Ctl {
     uint64_t full[10], empty[10], piece_full[kPieces], piece_empty[kPieces];
     Piece piece[kPieces];
-    uint64_t q_full[2], q_free[2], s_full[2], p_ready[2][2], pv_done[2], o_free[2], drain;
+    uint64_t q_full[2], q_free[2], s_full[2], p_ready[2][2], pv_done[2], o_free[2], clean, drain;
     unsigned long long sum[kWarps][2];
     unsigned long long start_off;
     int start_seg, start_units;
     Seg start;
-    uint32_t tmem;
+    uint32_t tmem, issued;  // issued: ring fills under way or done
     int abort;
 };
 
@@ -428,12 +423,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if ((int)blockIdx.x >= runs.blocks) return;
 
     if (tid == 0) {
-        for (int i = 0; i < C::kSlots; ++i) tc::mbar_init(&ctl->full[i], 1), tc::mbar_init(&ctl->empty[i], 1);
-        tc::mbar_init(&ctl->drain, 1);
+        for (int i = 0; i < C::kSlots; ++i) tc::mbar_init(&ctl->full[i], 1), tc::mbar_init(&ctl->empty[i], 2);
+        tc::mbar_init(&ctl->clean, 1);
+        tc::mbar_init(&ctl->drain, 2);
         for (int i = 0; i < kPieces; ++i) tc::mbar_init(&ctl->piece_full[i], 1), tc::mbar_init(&ctl->piece_empty[i], kPieceReaders);
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&ctl->q_full[i], 2);
-            tc::mbar_init(&ctl->q_free[i], 1);
+            tc::mbar_init(&ctl->q_full[i], 1);
+            tc::mbar_init(&ctl->q_free[i], 2);
             tc::mbar_init(&ctl->s_full[i], 1);
             tc::mbar_init(&ctl->p_ready[i][0], 4);
             tc::mbar_init(&ctl->p_ready[i][1], 4);
@@ -441,6 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mbar_init(&ctl->o_free[i], 4);
         }
         ctl->abort = 0;
+        ctl->issued = 0;
         tc::fence_async_shared();
     }
     if (warp == 2) tc::tmem_alloc(&ctl->tmem, kTmemCols);
@@ -467,9 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return x.rows > 0;
     };
 
-    // Order of the ring: a tile's K, then its V; among the tiles of one-tile units
-    // V follows the next tile's K, as the products take them.
-    uint32_t it = 0;  // ring position of the next fetch
+    uint32_t it = 0;  // ring position: a tile's K, then its V
 
     // Each role sets its registers inside its own branch: code that both counts reach is held to the smaller.
     if (warp >= 4) {
@@ -553,11 +548,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             walk.seg = ctl->start_seg;
             walk.units = ctl->start_units;
             walk.s = ctl->start;
-            int late_boxes = 0, late_y = 0, late_kvh = 0, late_page = 0;  // of the tile whose V is still to come
             auto fetch = [&](const CUtensorMap* map, int n, int fy, int fh, int fp) {
                 const uint32_t slot = it % C::kSlots;
                 if (!tc::warp_wait(&ctl->empty[slot], (it / C::kSlots & 1u) ^ 1u, limit, abort)) return false;
-                if (lane == 0) tc::mbar_expect(&ctl->full[slot], (uint32_t)n * step * 128u);
+                if (lane == 0) {
+                    tc::mbar_expect(&ctl->full[slot], (uint32_t)n * step * 128u);
+                    tc::store_release(&ctl->issued, it + 1);
+                }
                 __syncwarp();
                 if (lane < n)
                     tc::tma_load_4d(ring + slot * C::kTileBytes + half * (kKTile * 128) + tok * 128, map, &ctl->full[slot], half * 64, fy, fh, fp);
@@ -575,7 +572,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ++n_piece;
                 if (!more) break;
-                const bool two = x.rows > p.rows_per_tile;
                 // the pages of the next tile are read before this tile's waits
                 auto page_of = [&](int i) {
                     const long long at = walk.token + i * kKTile + tok;
@@ -592,106 +588,82 @@ __global__ void __launch_bounds__(kThreads, 1)
                         page = (int)p.num_pages;  // outside the map: zeros
                         atomicOr(p.status, kStatusBadPage);
                     }
-                    if (two) {
-                        if (late_boxes > 0) ok = fetch(&v_map, late_boxes, late_y, late_kvh, late_page);
-                        late_boxes = 0;
-                        ok = ok && fetch(&k_map, boxes, y, kvh, page) && fetch(&v_map, boxes, y, kvh, page);
-                    } else {
-                        ok = fetch(&k_map, boxes, y, kvh, page);
-                        if (ok && late_boxes > 0) ok = fetch(&v_map, late_boxes, late_y, late_kvh, late_page);
-                        late_boxes = boxes, late_y = y, late_kvh = kvh, late_page = page;
-                    }
+                    ok = fetch(&k_map, boxes, y, kvh, page) && fetch(&v_map, boxes, y, kvh, page);
                 }
             }
-            if (ok && late_boxes > 0) fetch(&v_map, late_boxes, late_y, late_kvh, late_page);
             // no copy outlives the block, whatever its readers did
             int none = 0;
             for (uint32_t i = it > C::kSlots ? it - C::kSlots : 0; i < it; ++i)
                 tc::mbar_wait(&ctl->full[i % C::kSlots], i / C::kSlots & 1u, limit, &none);
-        } else if (warp == 1) {
-            // ---- the products, issued by one thread
+        } else if (warp <= 2) {
+            // ---- the products of tensor tile s, issued by one thread; the other tile's run while this thread waits and commits
             if (lane == 0) {
                 constexpr uint32_t kIdescS = tc::make_idesc(kBf16, false, kQTile, kKTile), kIdescO = tc::make_idesc(kBf16, true, kQTile, D);
-                // This thread's own instructions must hide behind the products (64 cycles each, few in the queue), so ring
-                // positions step without divisions and everything about a tensor tile is in registers of its own.
+                constexpr uint32_t kTileStep = C::kTileBytes >> 4;
+                const int s = warp - 1;
                 const uint64_t q_desc = tc::make_desc(tc::smem_addr(smem), 16, 1024);
                 const uint64_t k_desc = tc::make_desc(tc::smem_addr(ring), 16, 1024), v_desc = tc::make_desc(tc::smem_addr(ring), kKTile * 128, 1024);
-                constexpr uint32_t kTileStep = C::kTileBytes >> 4;
-                uint32_t q_pos = 0, slot = 0, phase = 0;  // the next ring position
-                uint32_t p_phase[2] = {0, 0}, o_phase[2] = {1, 1};
-                // The tiles whose scores are in S_s and whose values are still to be multiplied: tokens (0: none), ring
-                // position of V, whether the piece's first, the first and the last to use V.
-                int valid[2] = {0, 0};
-                uint32_t v_slot[2] = {0, 0}, v_phase[2] = {0, 0};
-                bool begins[2] = {}, cleans[2] = {}, releases[2] = {};
-                int turn = 0, late = -1;  // tensor tile of the next one-tile unit's tile; the one whose V has no ring position yet
+                const uint32_t s_t = tmem + kColS + s * kColStep, o_t = tmem + kColO + s * kColStep;
+                uint64_t *s_full = &ctl->s_full[s], *p_ready = ctl->p_ready[s], *pv_done = &ctl->pv_done[s], *o_free = &ctl->o_free[s];
+                uint32_t q_pos = 0, pos = 0, slot = 0, phase = 0, p_phase = 0, o_phase = 1, clean_phase = 0;  // pos, slot, phase: the next ring position
+                int turn = 0;  // whose the next tile of a one-tile unit is
                 auto wait = [&](uint64_t* bar, uint32_t parity) { return tc::mbar_wait(bar, parity, limit, abort); };
                 auto advance = [&]() {
+                    ++pos;
                     if (++slot == C::kSlots) slot = 0, phase ^= 1u;
                 };
-                auto place_late = [&]() {  // V of the late tile takes the next ring position
-                    if (late == 0) v_slot[0] = slot, v_phase[0] = phase;
-                    else v_slot[1] = slot, v_phase[1] = phase;
-                    advance();
+                // A position's fill.  This thread passes over the other's tiles, so it may look at a slot before the fill
+                // ahead of its own has ended, and the parity of that older phase would let it through: it first waits
+                // until its own fill is under way (which the older one's release comes before).
+                auto wait_fill = [&](uint32_t at, uint32_t fill_slot, uint32_t fill_phase) {
+                    return tc::wait_count(&ctl->issued, at, limit, abort) && wait(&ctl->full[fill_slot], fill_phase);
                 };
-                auto scores = [&](auto tile, uint32_t q, uint32_t k_slot) {  // S_s = Q K^T
-                    constexpr int s = decltype(tile)::value;
-                    const uint64_t a = q_desc + q * kTileStep, b = k_desc + k_slot * kTileStep;
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint64_t o = (uint64_t)(((k / 4) * (kKTile * 128) + (k % 4) * 32) >> 4);
-                        tc::mma_ss(tmem + kColS + s * kColStep, a + o, b + o, kIdescS, k > 0);
-                    }
-                    tc::commit(&ctl->s_full[s]);
+                auto release = [&](uint64_t* bar, bool shared) {  // two arrivals: one of each thread, or both of the only user
+                    tc::commit(bar);
+                    if (!shared) tc::commit(bar);
                 };
-                // O_s += P_s V, half of the tokens at a time; the first product of a piece waits for the accumulator to be read
-                auto values = [&](auto tile) {
-                    constexpr int s = decltype(tile)::value;
-                    if (valid[s] == 0) return true;
-                    const int have = valid[s];
-                    valid[s] = 0;
-                    if (cleans[s]) {  // the first to use V
-                        if (!wait(&ctl->full[v_slot[s]], v_phase[s])) return false;
-                        if ((have & 15) != 0) {
-                            // slots past the length hold anything: zero those that the last 16 rows of V take in, so that 0 * v stays 0
-                            unsigned char* v = ring + v_slot[s] * C::kTileBytes;
+                // O += P V, half of the tokens at a time; the first product of a piece waits for the accumulator to be read
+                auto values = [&](uint32_t v_pos, uint32_t v_slot, uint32_t v_phase, int have, bool first, bool two) {
+                    if (!wait_fill(v_pos, v_slot, v_phase)) return false;
+                    if ((have & 15) != 0 && have < kKTile) {
+                        // slots past the length hold anything: zero those that the last 16 rows of V take in, so that 0 * v stays 0
+                        if (!two || s == 0) {
+                            unsigned char* v = ring + v_slot * C::kTileBytes;
                             for (int r = have; r < ((have + 15) & ~15); ++r)
 #pragma unroll
                                 for (int h = 0; h < D / 8; ++h)
                                     *reinterpret_cast<uint4*>(v + (h >> 3) * (kKTile * 128) + r * 128 + (h & 7) * 16) = make_uint4(0, 0, 0, 0);
                             tc::fence_async_shared();
+                            if (two) tc::mbar_arrive(&ctl->clean);
+                        } else {
+                            if (!wait(&ctl->clean, clean_phase)) return false;
+                            clean_phase ^= 1u;
                         }
                     }
-                    if (begins[s]) {
-                        if (!wait(&ctl->o_free[s], o_phase[s])) return false;
-                        o_phase[s] ^= 1u;
+                    if (first) {
+                        if (!wait(o_free, o_phase)) return false;
+                        o_phase ^= 1u;
                     }
-                    const uint64_t b = v_desc + v_slot[s] * kTileStep;
-                    const uint32_t o_t = tmem + kColO + s * kColStep, p_t = tmem + kColS + s * kColStep;
-                    if (!wait(&ctl->p_ready[s][0], p_phase[s])) return false;
+                    const uint64_t b = v_desc + v_slot * kTileStep;
+                    if (!wait(&p_ready[0], p_phase)) return false;
                     tc::fence_after();
                     if (have > kKTile - 16) {
 #pragma unroll
-                        for (int k = 0; k < kKTile / 32; ++k)
-                            tc::mma_ts(o_t, p_t + k * 8, b + (uint64_t)(k * 2048 >> 4), kIdescO, k > 0 || !begins[s]);
-                        if (!wait(&ctl->p_ready[s][1], p_phase[s])) return false;
+                        for (int k = 0; k < kKTile / 32; ++k) tc::mma_ts(o_t, s_t + k * 8, b + (uint64_t)(k * 2048 >> 4), kIdescO, k > 0 || !first);
+                        if (!wait(&p_ready[1], p_phase)) return false;
                         tc::fence_after();
 #pragma unroll
-                        for (int k = kKTile / 32; k < kKTile / 16; ++k)
-                            tc::mma_ts(o_t, p_t + k * 8, b + (uint64_t)(k * 2048 >> 4), kIdescO, true);
+                        for (int k = kKTile / 32; k < kKTile / 16; ++k) tc::mma_ts(o_t, s_t + k * 8, b + (uint64_t)(k * 2048 >> 4), kIdescO, true);
                     } else {
-                        if (!wait(&ctl->p_ready[s][1], p_phase[s])) return false;
+                        if (!wait(&p_ready[1], p_phase)) return false;
                         tc::fence_after();
-                        for (int k = 0; k < (have + 15) >> 4; ++k)
-                            tc::mma_ts(o_t, p_t + k * 8, b + (uint64_t)(k * 2048 >> 4), kIdescO, k > 0 || !begins[s]);
+                        for (int k = 0; k < (have + 15) >> 4; ++k) tc::mma_ts(o_t, s_t + k * 8, b + (uint64_t)(k * 2048 >> 4), kIdescO, k > 0 || !first);
                     }
-                    p_phase[s] ^= 1u;
-                    tc::commit(&ctl->pv_done[s]);
-                    if (releases[s]) tc::commit(&ctl->empty[v_slot[s]]);
+                    p_phase ^= 1u;
+                    tc::commit(pv_done);
+                    release(&ctl->empty[v_slot], two);
                     return true;
                 };
-                constexpr Int<0> kTile0{};
-                constexpr Int<1> kTile1{};
                 while (ok) {
                     const uint32_t pi = n_piece % kPieces;
                     ok = wait(&ctl->piece_full[pi], n_piece / kPieces & 1u);
@@ -701,74 +673,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++n_piece;
                     if (x.rows == 0) break;
                     const bool two = x.rows > p.rows_per_tile;
-                    if (two && late >= 0) {
-                        place_late();
-                        late = -1;
-                    }
-                    for (int j = 0; ok && j <= (two ? 1 : 0); ++j) ok = wait(&ctl->q_full[(q_pos + j) & 1u], (q_pos + j) >> 1 & 1u);
-                    if (!ok) break;
-                    const uint32_t q0 = q_pos & 1u;
+                    // Both threads see every fill of every query buffer and both free it, used or not: neither gets a phase ahead.
+                    const uint32_t q = q_pos + (two ? s : 0);
+                    ok = wait(&ctl->q_full[q_pos & 1u], q_pos >> 1 & 1u) && (!two || wait(&ctl->q_full[(q_pos + 1) & 1u], (q_pos + 1) >> 1 & 1u));
+                    const uint64_t a = q_desc + (q & 1u) * kTileStep;
                     int left = x.left;
-                    if (two) {
-                        auto step = [&](auto tile, uint32_t k_slot, uint32_t k_phase, bool first) {
-                            constexpr int s = decltype(tile)::value;
-                            if (!values(tile)) return false;
-                            if (s == 0 && !wait(&ctl->full[k_slot], k_phase)) return false;
-                            tc::fence_after();
-                            scores(tile, q0 ^ s, k_slot);
-                            valid[s] = left < kKTile ? left : kKTile;
-                            v_slot[s] = slot, v_phase[s] = phase;
-                            begins[s] = first, cleans[s] = s == 0, releases[s] = s == 1;
-                            return true;
-                        };
-                        for (int i = 0; i < x.tiles; ++i) {
-                            const uint32_t k_slot = slot, k_phase = phase;
-                            advance();
-                            ok = step(kTile0, k_slot, k_phase, i == 0) && step(kTile1, k_slot, k_phase, i == 0);
+                    bool begun = false;
+                    for (int i = 0; ok && i < x.tiles; ++i, left -= kKTile) {
+                        const uint32_t k_pos = pos, k_slot = slot, k_phase = phase;
+                        advance();
+                        if (two || turn == s) {
+                            ok = wait_fill(k_pos, k_slot, k_phase);
                             if (!ok) break;
-                            tc::commit(&ctl->empty[k_slot]);
-                            advance();
-                            left -= kKTile;
-                        }
-                    } else {
-                        auto step = [&](auto tile, bool first) {
-                            constexpr int s = decltype(tile)::value;
-                            const uint32_t k_slot = slot, k_phase = phase;
-                            advance();
-                            if (late >= 0) place_late();
-                            if (!values(tile) || !wait(&ctl->full[k_slot], k_phase)) return false;
                             tc::fence_after();
-                            scores(tile, q0, k_slot);
-                            tc::commit(&ctl->empty[k_slot]);
-                            valid[s] = left < kKTile ? left : kKTile;
-                            begins[s] = first, cleans[s] = releases[s] = true;
-                            late = s;
-                            return true;
-                        };
-                        for (int i = 0; i < x.tiles; ++i) {
-                            ok = turn == 0 ? step(kTile0, i < 2) : step(kTile1, i < 2);
-                            if (!ok) break;
-                            turn ^= 1;
-                            left -= kKTile;
+                            const uint64_t b = k_desc + k_slot * kTileStep;
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k) {  // S = Q K^T
+                                const uint64_t o = (uint64_t)(((k / 4) * (kKTile * 128) + (k % 4) * 32) >> 4);
+                                tc::mma_ss(s_t, a + o, b + o, kIdescS, k > 0);
+                            }
+                            tc::commit(s_full);
+                            release(&ctl->empty[k_slot], two);
+                            ok = values(pos, slot, phase, left, !begun, two);
+                            begun = true;
                         }
+                        if (!two) turn ^= 1;
+                        advance();
                     }
                     if (ok) {
-                        tc::commit(&ctl->q_free[q0]);
-                        if (two) tc::commit(&ctl->q_free[q0 ^ 1u]);
+                        tc::commit(&ctl->q_free[q & 1u]);
+                        if (two) tc::mbar_arrive(&ctl->q_free[(q + 1) & 1u]);
                     }
                     q_pos += two ? 2 : 1;
                 }
-                if (late >= 0) place_late();
-                // in the order of their V
-                if (ok) ok = late == 0 ? values(kTile1) && values(kTile0) : values(kTile0) && values(kTile1);
                 int none = 0;  // no product outlives the block
                 tc::commit(&ctl->drain);
                 tc::mbar_wait(&ctl->drain, 0, limit, &none);
             }
             __syncwarp();
-        } else if (warp < 4) {
+        } else {
             // ---- query tiles into shared memory, ahead of the products
-            const int t64 = tid - 64;
             uint32_t q_pos = 0;
             while (ok && next_piece()) {
                 const bool two = x.rows > p.rows_per_tile;
@@ -782,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const T* src = reinterpret_cast<const T*>(p.q) + (long long)(x.row + j * p.rows_per_tile) * p.q_stride + (long long)x.kvh * p.share * D;
                     // straight into shared memory, all in flight; rows past the last are zeros
                     const uint32_t at0 = tc::smem_addr(smem + b * C::kTileBytes);
-                    for (int i = t64; i < kQTile * kChunks; i += 64) {
+                    for (int i = lane; i < kQTile * kChunks; i += 32) {
                         const int row = i / kChunks, ch = i % kChunks;
                         const int per = row < valid ? (row * p.share_inv) >> 16 : 0, head = row < valid ? row - per * p.share : 0;
                         const T* from = src + per * p.q_stride + head * D + ch * 8;

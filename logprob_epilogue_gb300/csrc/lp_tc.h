@@ -68,6 +68,30 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsign
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit, abort));
 }
 
+// A counter in shared memory that one thread raises: waits until it is past
+// `n` (differences modulo 2^32).  False as for mbar_wait.
+__device__ __forceinline__ void store_release(uint32_t* at, uint32_t v) {
+    asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(smem_addr(at)), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ bool wait_count(const uint32_t* at, uint32_t n, unsigned long long limit, volatile int* abort) {
+    unsigned long long start = 0;
+    for (uint32_t i = 1;; ++i) {
+        uint32_t v;
+        asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(smem_addr(at)) : "memory");
+        if ((int32_t)(v - n) > 0) return true;
+        if ((i & 63u) == 0u) {
+            if (*abort != 0) return false;
+            const unsigned long long now = globaltimer();
+            if (start == 0) start = now;
+            if (now - start > limit) {
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
 // ---- TMA
 
 // One box of a 4-D map into shared memory; x * element size is a multiple of 16 bytes.
