@@ -20,7 +20,10 @@
 // 128.  All token tiles of the call, unit after unit, are cut into one equal
 // run per block, wherever that falls: one request at a long context and
 // hundreds of short ones fill the machine alike, and no block waits on
-// another.  A unit of two query tiles reads each K and V tile once for both; a
+// another.  Before that, a prefix with more units than blocks deals them out
+// whole, one to every block at a time: the blocks of a head then go through
+// its tokens side by side, and a tile that one of them fetched is still in L2
+// for the others.  A unit of two query tiles reads each K and V tile once for both; a
 // unit of one tile gives its even token tiles to one warpgroup and its odd ones
 // to the other, each with its own maximum, sum and accumulator.
 //
@@ -51,6 +54,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr float kRescale = 8.0f;  // growth of the maximum (log2) that moves it
+constexpr int kUnitCost = 2;      // what a unit costs a block beside its tiles, in tiles
 // Registers: the softmax warpgroups hold 128 scores per thread.  The split's
 // sum is what the block is launched with, 384 x 168.
 constexpr int kRegsLaunch = 168, kRegsSoftmax = 200, kRegsOther = 104;
@@ -115,11 +119,12 @@ __device__ __forceinline__ Prefix load_prefix(const AttendParams& p, int i) {
 // Segment s: prefixes 0..P-1, then the groups' committed tokens.
 struct Seg {
     int r0, n, len;
-    int tiles, units;  // token tiles, units per key-value head; tiles = 0: no work
+    int tiles, units;  // token tiles; units per key-value head; tiles = 0: no work
+    int dealt;         // of all heads' units, those that go round the blocks whole
     bool bad;
-    __device__ __forceinline__ unsigned long long work(const AttendParams& p) const {
-        return (unsigned long long)tiles * units * p.kv_heads;
-    }
+    __device__ __forceinline__ int left(const AttendParams& p) const { return tiles > 0 ? units * p.kv_heads - dealt : 0; }
+    __device__ __forceinline__ int span() const { return tiles + kUnitCost; }  // of a unit in a run
+    __device__ __forceinline__ unsigned long long work(const AttendParams& p) const { return (unsigned long long)span() * left(p); }
 };
 
 __device__ __forceinline__ Seg load_seg(const AttendParams& p, int s) {
@@ -133,11 +138,12 @@ __device__ __forceinline__ Seg load_seg(const AttendParams& p, int s) {
     }
     x.units = (x.n + 2 * p.rows_per_tile - 1) / (2 * p.rows_per_tile);
     x.tiles = x.n > 0 ? (x.len + kKTile - 1) / kKTile : 0;
+    x.dealt = s < p.P && x.tiles > 0 ? x.units * p.kv_heads / p.grid * p.grid : 0;
     return x;
 }
 
-// `total` tiles cut into one run per block: blocks 0..more-1 take per + 1
-// tiles, the others per.
+// `total` tiles (with the units' cost) cut into one run per block: blocks
+// 0..more-1 take per + 1, the others per.
 struct Runs {
     unsigned long long total, per;
     int blocks, more;
@@ -185,39 +191,59 @@ struct Piece {
     long long part;     // row 0 of its first part; -1: past the scratch (only overlapping prefixes can ask for that)
 };
 
-// Walks the pieces of a run of tiles.
+// Walks a block's pieces: its share of the units that go round whole, then its
+// run of the other units' tiles.
 struct Walk {
+    int deal, deal_end, round, dealt;  // segments with units that go round; rounds dealt; units of earlier segments
     unsigned long long pos, end, off;  // off: tiles before the segment
-    int seg, units, cta;               // units: before the segment, of its kind
+    int seg, units, cta;               // units: the segment's first slot less cta
     Seg s;
     const int* table;                  // pages of the piece, and its first token
     long long token;
+    __device__ __forceinline__ void fill(const AttendParams& p, Piece& x, int sg, const Seg& y, int unit, int t0, int tiles, long long slot) {
+        const bool prefix = sg < p.P;
+        x.tiles = tiles;
+        x.kvh = unit / y.units;
+        const int first = (unit - x.kvh * y.units) * 2 * p.rows_per_tile;
+        x.row = y.r0 + first;
+        x.rows = y.n - first < 2 * p.rows_per_tile ? y.n - first : 2 * p.rows_per_tile;
+        x.left = y.len - t0 * kKTile;
+        table = prefix ? p.prefix_tables + (long long)sg * p.max_prefix_pages : p.tables + (long long)(sg - p.P) * p.max_pages;
+        token = (long long)t0 * kKTile;
+        x.part = part_row(p, prefix, slot, 0);
+        x.part_stride = prefix ? kQTile : p.sc.group_rows;
+    }
     __device__ __forceinline__ bool next(const AttendParams& p, Piece& x) {
+        while (deal < deal_end) {
+            const Seg y = load_seg(p, deal);
+            const int unit = round * p.grid + cta;
+            if (unit < y.dealt) {
+                ++round;
+                fill(p, x, deal, y, unit, 0, y.tiles, dealt + unit);
+                return true;
+            }
+            dealt += y.dealt;
+            ++deal;
+            round = 0;
+        }
         while (pos < end) {
             const unsigned long long work = s.work(p);
             if (pos >= off + work) {
                 off += work;
-                units += s.tiles > 0 ? s.units * p.kv_heads : 0;
-                if (++seg == p.P) units = 0;
-                if (seg >= p.P + p.G) break;
+                if (++seg >= p.P + p.G) break;
+                units = seg == p.P ? 0 : units + s.left(p);
                 s = load_seg(p, seg);
                 continue;
             }
+            // the unit's cost lies before its tiles; a run may hold that alone
             const unsigned long long rel = pos - off, rest = end - pos;
-            const int unit = (int)Runs::quotient(rel, s.tiles);
-            const int t0 = (int)(rel - (unsigned long long)unit * s.tiles);
-            x.tiles = rest < (unsigned long long)(s.tiles - t0) ? (int)rest : s.tiles - t0;
-            x.kvh = unit / s.units;
-            const int first = (unit - x.kvh * s.units) * 2 * p.rows_per_tile;
-            x.row = s.r0 + first;
-            x.rows = s.n - first < 2 * p.rows_per_tile ? s.n - first : 2 * p.rows_per_tile;
-            x.left = s.len - t0 * kKTile;
-            const bool prefix = seg < p.P;
-            table = prefix ? p.prefix_tables + (long long)seg * p.max_prefix_pages : p.tables + (long long)(seg - p.P) * p.max_pages;
-            token = (long long)t0 * kKTile;
-            x.part = part_row(p, prefix, (long long)units + unit + cta, 0);
-            x.part_stride = prefix ? kQTile : p.sc.group_rows;
-            pos += x.tiles;
+            const int unit = (int)Runs::quotient(rel, s.span());
+            const int u0 = (int)(rel - (unsigned long long)unit * s.span());
+            const int u1 = rest < (unsigned long long)(s.span() - u0) ? u0 + (int)rest : s.span();
+            pos += u1 - u0;
+            const int t0 = u0 > kUnitCost ? u0 - kUnitCost : 0, t1 = u1 - kUnitCost;
+            if (t1 <= t0) continue;
+            fill(p, x, seg, s, s.dealt + unit, t0, t1 - t0, (long long)units + unit + cta);
             return true;
         }
         x.rows = 0;
@@ -231,60 +257,77 @@ constexpr int kPieceReaders = 11; // warps that read each: two of the products, 
 struct Ctl {
     uint64_t full[10], empty[10], piece_full[kPieces], piece_empty[kPieces];
     Piece piece[kPieces];
-    uint64_t q_full[2], q_free[2], s_full[2], p_ready[2][2], pv_done[2], o_free[2], clean, drain;
+    uint64_t q_full[2], q_free[2], s_full[2], p_ready[2], pv_done[2], o_free[2], clean, drain;
     unsigned long long sum[kWarps][2];
+    int sum_dealt[kWarps], deal_first, deal_last;
     unsigned long long start_off;
     int start_seg, start_units;
     Seg start;
-    uint32_t tmem, issued;  // issued: ring fills under way or done
+    uint32_t tmem, issued, batches[2];  // ring fills under way or done; see take_turn
     int abort;
 };
 
 // The call's tiles and units: every thread sums its share of the segments,
 // the block scans the sums, and the thread that holds the block's first tile
-// names its segment.  Block 0 leaves the offsets for the join.
-__device__ __forceinline__ Runs plan_run(const AttendParams& p, Ctl* ctl) {
+// names its segment.  Block 0 leaves the offsets for the join.  False: the
+// block has no work.
+__device__ __forceinline__ bool plan_run(const AttendParams& p, Ctl* ctl, Runs& runs) {
     const int S = p.P + p.G, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (S + kThreads - 1) / kThreads;
     const int s0 = tid * per < S ? tid * per : S, s1 = s0 + per < S ? s0 + per : S;
-    unsigned long long tiles = 0, units = 0;  // units: of prefixes in the high half, of groups in the low
+    // units: slots of units that do not go round, of prefixes in the high half, of groups in the low
+    unsigned long long tiles = 0, units = 0;
+    int dealt = 0, first = S, last = -1;
     for (int s = s0; s < s1; ++s) {
         const Seg x = load_seg(p, s);
         tiles += x.work(p);
-        if (x.tiles > 0) units += (unsigned long long)(x.units * p.kv_heads) << (s < p.P ? 32 : 0);
+        units += (unsigned long long)x.left(p) << (s < p.P ? 32 : 0);
+        dealt += x.dealt;
+        if (x.dealt > 0) {
+            if (last < 0) first = s;
+            last = s;
+        }
         if (x.bad && blockIdx.x == 0) atomicOr(p.status, s < p.P ? kStatusBadPrefix : kStatusAttnBadGroup);
     }
     unsigned long long it = tiles, iu = units;
+    int id = dealt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const unsigned long long a = __shfl_up_sync(kFull, it, o), b = __shfl_up_sync(kFull, iu, o);
-        if (lane >= o) it += a, iu += b;
+        const int d = __shfl_up_sync(kFull, id, o);
+        if (lane >= o) it += a, iu += b, id += d;
     }
-    if (lane == 31) ctl->sum[warp][0] = it, ctl->sum[warp][1] = iu;
+    if (lane == 31) ctl->sum[warp][0] = it, ctl->sum[warp][1] = iu, ctl->sum_dealt[warp] = id;
+    if (tid == 0) ctl->deal_first = S, ctl->deal_last = -1;
     __syncthreads();
+    if (last >= 0) atomicMin(&ctl->deal_first, first), atomicMax(&ctl->deal_last, last);
     unsigned long long bt = 0, bu = 0, total = 0;
+    int bd = 0, all_dealt = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-        if (w == warp) bt = total;
+        if (w == warp) bt = total, bd = all_dealt;
         if (w < warp) bu += ctl->sum[w][1];
         total += ctl->sum[w][0];
+        all_dealt += ctl->sum_dealt[w];
     }
     unsigned long long off = bt + it - tiles, u = bu + iu - units;
-    const Runs runs = make_runs(total, gridDim.x);
+    int d = bd + id - dealt;
+    runs = make_runs(total, gridDim.x);
     const unsigned long long lo = (int)blockIdx.x < runs.blocks ? runs.start(blockIdx.x) : ~0ull;
     if (blockIdx.x == 0 || (lo >= off && lo < off + tiles)) {
         for (int s = s0; s < s1; ++s) {
             const Seg x = load_seg(p, s);
             const unsigned long long work = x.work(p);
-            const int before = (int)(s < p.P ? u >> 32 : u & 0xFFFFFFFFull);
-            if (blockIdx.x == 0) p.sc.seg_tiles[s] = off, p.sc.seg_units[s] = before;
+            const int before = (int)(s < p.P ? (u >> 32) + all_dealt : u & 0xFFFFFFFFull);  // slots: the dealt units', then the others'
+            if (blockIdx.x == 0) p.sc.seg_tiles[s] = off, p.sc.seg_units[s] = make_int2(before, d);
             if (lo >= off && lo < off + work) ctl->start_seg = s, ctl->start_units = before, ctl->start_off = off, ctl->start = x;
             off += work;
-            if (x.tiles > 0) u += (unsigned long long)(x.units * p.kv_heads) << (s < p.P ? 32 : 0);
+            u += (unsigned long long)x.left(p) << (s < p.P ? 32 : 0);
+            d += x.dealt;
         }
     }
     if (blockIdx.x == 0 && tid == 0) p.sc.seg_tiles[S] = total;
-    return runs;
+    return all_dealt > 0 || (int)blockIdx.x < runs.blocks;
 }
 
 __device__ __forceinline__ unsigned long long pack2(uint32_t a, uint32_t b) {
@@ -317,11 +360,9 @@ struct Row {
 };
 
 // Softmax of one score tile by one warp, a row per thread; `valid` of the 128
-// tokens exist.  Writes the row's probabilities over the scores and announces
-// the first half of them at p_ready.  False: a wait ran out.
+// tokens exist.  Writes the row's probabilities over the scores.
 template <bool kBf16, int D>
-__device__ __forceinline__ bool softmax_tile(uint32_t s_col, uint32_t o_col, int valid, bool first, float c, Row& row, uint64_t* p_ready,
-                                             uint64_t* pv_done, uint32_t pv_parity, unsigned long long limit, volatile int* abort) {
+__device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, int valid, bool first, float c, Row& row) {
     using H = Half<kBf16>;
     // F16 keeps probabilities down to 2^-24: lifting them by 2^6 (at most 2^14 then) keeps those above 2^-30
     constexpr float kBias = kBf16 ? 0.0f : 6.0f;
@@ -360,9 +401,7 @@ __device__ __forceinline__ bool softmax_tile(uint32_t s_col, uint32_t o_col, int
                 row.base = next;
                 row.l *= f;
             }
-            // the accumulator is this warp's to change once the products so far are in
-            if (!tc::warp_wait(pv_done, pv_parity, limit, abort)) return false;
-            tc::fence_after();
+            // the scores came after the products before them, so the accumulator is this warp's to change
 #pragma unroll 1
             for (int b = 0; b < D / 32; ++b) {
                 uint32_t o[32];
@@ -392,19 +431,11 @@ __device__ __forceinline__ bool softmax_tile(uint32_t s_col, uint32_t o_col, int
             w[e] = H::pack(x, y);
         }
         tc::tmem_st16(s_col + b * 16, w);
-        if (b == 1) {
-            // the first half: its products start while the second is computed
-            tc::wait_st();
-            tc::fence_before();
-            __syncwarp();
-            if ((threadIdx.x & 31) == 0) tc::mbar_arrive(p_ready);
-        }
     }
     float x, y;
     unpack2(add2(sum[0], sum[1]), x, y);
     row.l += x + y;
     tc::wait_st();
-    return true;
 }
 
 template <bool kBf16, int D>
@@ -419,8 +450,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;");  // the join waits for this grid's end by itself
     const unsigned long long limit = p.timeout_ns;
-    const Runs runs = plan_run(p, ctl);
-    if ((int)blockIdx.x >= runs.blocks) return;
+    Runs runs;
+    if (!plan_run(p, ctl, runs)) return;
 
     if (tid == 0) {
         for (int i = 0; i < C::kSlots; ++i) tc::mbar_init(&ctl->full[i], 1), tc::mbar_init(&ctl->empty[i], 2);
@@ -431,13 +462,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mbar_init(&ctl->q_full[i], 1);
             tc::mbar_init(&ctl->q_free[i], 2);
             tc::mbar_init(&ctl->s_full[i], 1);
-            tc::mbar_init(&ctl->p_ready[i][0], 4);
-            tc::mbar_init(&ctl->p_ready[i][1], 4);
+            tc::mbar_init(&ctl->p_ready[i], 4);
             tc::mbar_init(&ctl->pv_done[i], 1);
             tc::mbar_init(&ctl->o_free[i], 4);
         }
         ctl->abort = 0;
-        ctl->issued = 0;
+        ctl->issued = ctl->batches[0] = ctl->batches[1] = 0;
         tc::fence_async_shared();
     }
     if (warp == 2) tc::tmem_alloc(&ctl->tmem, kTmemCols);
@@ -474,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)quarter << 21;
         const uint32_t s_col = tmem + lanes + kColS + wg * kColStep, o_col = tmem + lanes + kColO + wg * kColStep;
         const float c = p.scale * kLog2e;
-        uint32_t s_phase = 0, pv = 0;
+        uint32_t s_phase = 0, pv_phase = 0, tile = 0;  // tile: tiles of the run before the piece
         int turn = 0;
         while (ok && next_piece()) {
             const bool two = x.rows > p.rows_per_tile;
@@ -488,20 +518,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = tc::warp_wait(&ctl->s_full[wg], s_phase, limit, abort);
                 if (!ok) break;
                 s_phase ^= 1u;
-                uint64_t* ready = ctl->p_ready[wg];
+                if (two && wg == 0 && quarter == 0 && lane == 0) {  // thread 0's products have read K of this tile and V of the one before
+                    tc::mbar_arrive(&ctl->empty[(tile + i) * 2 % C::kSlots]);
+                    if (i > 0) tc::mbar_arrive(&ctl->empty[((tile + i) * 2 - 1) % C::kSlots]);
+                }
                 if (live) {
                     tc::fence_after();
-                    ok = softmax_tile<kBf16, D>(s_col, o_col, x.left - i * kKTile, i == first, c, st, &ready[0], &ctl->pv_done[wg],
-                                                (pv - 1) & 1u, limit, abort);
-                    if (!ok) break;
+                    softmax_tile<kBf16, D>(s_col, o_col, x.left - i * kKTile, i == first, c, st);
                     tc::fence_before();
                     __syncwarp();
-                } else if (lane == 0) {
-                    tc::mbar_arrive(&ready[0]);
                 }
-                if (lane == 0) tc::mbar_arrive(&ready[1]);
-                ++pv;
+                if (lane == 0) tc::mbar_arrive(&ctl->p_ready[wg]);
             }
+            tile += n;
             if (!ok) break;
             const long long part = x.part + wg * x.part_stride;
             const bool store = row < valid_rows && x.part >= 0;
@@ -509,8 +538,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (store) p.sc.part_ml[part + row] = make_float2(kNegInf, 0.0f);
                 continue;
             }
-            ok = tc::warp_wait(&ctl->pv_done[wg], (pv - 1) & 1u, limit, abort);
+            ok = tc::warp_wait(&ctl->pv_done[wg], pv_phase, limit, abort);
             if (!ok) break;
+            pv_phase ^= 1u;
+            if (two && wg == 0 && quarter == 0 && lane == 0) tc::mbar_arrive(&ctl->empty[(tile * 2 - 1) % C::kSlots]);
             if (live) {
                 tc::fence_after();
                 if (store) p.sc.part_ml[part + row] = make_float2(st.m == kNegInf ? kNegInf : st.base, st.l);
@@ -542,8 +573,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int tok = lane / kHalves * step, half = lane % kHalves;
             Walk walk;
             walk.cta = blockIdx.x;
-            walk.pos = runs.start(blockIdx.x);
-            walk.end = runs.start(blockIdx.x + 1);
+            walk.deal = ctl->deal_first;
+            walk.deal_end = ctl->deal_last + 1;
+            walk.round = walk.dealt = 0;
+            walk.pos = walk.end = 0;
+            if ((int)blockIdx.x < runs.blocks) {
+                walk.pos = runs.start(blockIdx.x);
+                walk.end = runs.start(blockIdx.x + 1);
+            }
             walk.off = ctl->start_off;
             walk.seg = ctl->start_seg;
             walk.units = ctl->start_units;
@@ -561,6 +598,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++it;
                 return true;
             };
+            auto page_of = [&](int i) {
+                const long long at = walk.token + i * kKTile + tok;
+                return i < x.tiles && i * kKTile + tok < x.left ? __ldg(&walk.table[at >> p.page_shift]) : -1;
+            };
             for (bool more = ok; ok && more;) {
                 more = walk.next(p, x);
                 const uint32_t pi = n_piece % kPieces;
@@ -573,10 +614,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++n_piece;
                 if (!more) break;
                 // the pages of the next tile are read before this tile's waits
-                auto page_of = [&](int i) {
-                    const long long at = walk.token + i * kKTile + tok;
-                    return i < x.tiles && i * kKTile + tok < x.left ? __ldg(&walk.table[at >> p.page_shift]) : 0;
-                };
                 int next_page = page_of(0);
                 for (int i = 0; ok && i < x.tiles; ++i) {
                     const int left = x.left - i * kKTile, valid = left < kKTile ? left : kKTile;
@@ -604,29 +641,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t q_desc = tc::make_desc(tc::smem_addr(smem), 16, 1024);
                 const uint64_t k_desc = tc::make_desc(tc::smem_addr(ring), 16, 1024), v_desc = tc::make_desc(tc::smem_addr(ring), kKTile * 128, 1024);
                 const uint32_t s_t = tmem + kColS + s * kColStep, o_t = tmem + kColO + s * kColStep;
-                uint64_t *s_full = &ctl->s_full[s], *p_ready = ctl->p_ready[s], *pv_done = &ctl->pv_done[s], *o_free = &ctl->o_free[s];
+                uint64_t *s_full = &ctl->s_full[s], *p_ready = &ctl->p_ready[s], *pv_done = &ctl->pv_done[s], *o_free = &ctl->o_free[s];
                 uint32_t q_pos = 0, pos = 0, slot = 0, phase = 0, p_phase = 0, o_phase = 1, clean_phase = 0;  // pos, slot, phase: the next ring position
+                uint32_t batch = 0;
                 int turn = 0;  // whose the next tile of a one-tile unit is
                 auto wait = [&](uint64_t* bar, uint32_t parity) { return tc::mbar_wait(bar, parity, limit, abort); };
                 auto advance = [&]() {
                     ++pos;
                     if (++slot == C::kSlots) slot = 0, phase ^= 1u;
                 };
-                // A position's fill.  This thread passes over the other's tiles, so it may look at a slot before the fill
-                // ahead of its own has ended, and the parity of that older phase would let it through: it first waits
-                // until its own fill is under way (which the older one's release comes before).
-                auto wait_fill = [&](uint32_t at, uint32_t fill_slot, uint32_t fill_phase) {
-                    return tc::wait_count(&ctl->issued, at, limit, abort) && wait(&ctl->full[fill_slot], fill_phase);
+                // A position's fill.  In units of one tile this thread passes over the other's tiles, so it may look at a slot
+                // before the fill ahead of its own has ended, and the parity of that older phase would let it through: it
+                // first waits until its own fill is under way (which the older one's release comes before).
+                auto wait_fill = [&](uint32_t at, uint32_t fill_slot, uint32_t fill_phase, bool two) {
+                    return (two || tc::wait_count(&ctl->issued, at, limit, abort)) && wait(&ctl->full[fill_slot], fill_phase);
                 };
-                auto release = [&](uint64_t* bar, bool shared) {  // two arrivals: one of each thread, or both of the only user
-                    tc::commit(bar);
-                    if (!shared) tc::commit(bar);
+                // A slot comes free after two arrivals.  In units of two tiles thread 1, the last to use it, makes one as soon
+                // as its products are in, and warpgroup 0 the other when it sees the scores that followed thread 0's; in
+                // units of one tile the only user makes both.
+                auto release = [&](uint64_t* bar, bool two) {
+                    if (!two || s == 1) tc::commit(bar);
+                    if (!two) tc::commit(bar);
                 };
-                // O += P V, half of the tokens at a time; the first product of a piece waits for the accumulator to be read
-                auto values = [&](uint32_t v_pos, uint32_t v_slot, uint32_t v_phase, int have, bool first, bool two) {
-                    if (!wait_fill(v_pos, v_slot, v_phase)) return false;
-                    if ((have & 15) != 0 && have < kKTile) {
-                        // slots past the length hold anything: zero those that the last 16 rows of V take in, so that 0 * v stays 0
+                // In units of two tiles the threads take turns with the tensor core: P V and the next Q K^T of one tile, then of
+                // the other.  Left alone the two fall into step: both warpgroups in softmax, then both tiles' products, each
+                // idle during the other.
+                auto take_turn = [&]() { return tc::wait_count(&ctl->batches[s ^ 1], batch - (s ^ 1), limit, abort); };
+                auto pass_turn = [&]() { tc::store_release(&ctl->batches[s], ++batch); };
+                auto scores = [&](uint64_t a, uint32_t k_slot) {  // S = Q K^T
+                    const uint64_t b = k_desc + k_slot * kTileStep;
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint64_t o = (uint64_t)(((k / 4) * (kKTile * 128) + (k % 4) * 32) >> 4);
+                        tc::mma_ss(s_t, a + o, b + o, kIdescS, k > 0);
+                    }
+                };
+                // what O += P V needs besides P: V's fill, with the slots past the length zeroed (they hold anything, and 0 * v
+                // has to stay 0), and before a piece's first product the accumulator read
+                auto ready = [&](uint32_t v_pos, uint32_t v_slot, uint32_t v_phase, int have, bool first, bool two) {
+                    if (!wait_fill(v_pos, v_slot, v_phase, two)) return false;
+                    if ((have & 15) != 0 && have < kKTile) {  // the rows that the last 16 of V take in
                         if (!two || s == 0) {
                             unsigned char* v = ring + v_slot * C::kTileBytes;
                             for (int r = have; r < ((have + 15) & ~15); ++r)
@@ -644,25 +698,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!wait(o_free, o_phase)) return false;
                         o_phase ^= 1u;
                     }
-                    const uint64_t b = v_desc + v_slot * kTileStep;
-                    if (!wait(&p_ready[0], p_phase)) return false;
-                    tc::fence_after();
+                    return true;
+                };
+                auto values = [&](uint64_t b, int have, bool first) {  // O += P V
                     if (have > kKTile - 16) {
 #pragma unroll
-                        for (int k = 0; k < kKTile / 32; ++k) tc::mma_ts(o_t, s_t + k * 8, b + (uint64_t)(k * 2048 >> 4), kIdescO, k > 0 || !first);
-                        if (!wait(&p_ready[1], p_phase)) return false;
-                        tc::fence_after();
-#pragma unroll
-                        for (int k = kKTile / 32; k < kKTile / 16; ++k) tc::mma_ts(o_t, s_t + k * 8, b + (uint64_t)(k * 2048 >> 4), kIdescO, true);
+                        for (int k = 0; k < kKTile / 16; ++k) tc::mma_ts(o_t, s_t + k * 8, b + (uint64_t)(k * 2048 >> 4), kIdescO, k > 0 || !first);
                     } else {
-                        if (!wait(&p_ready[1], p_phase)) return false;
-                        tc::fence_after();
                         for (int k = 0; k < (have + 15) >> 4; ++k) tc::mma_ts(o_t, s_t + k * 8, b + (uint64_t)(k * 2048 >> 4), kIdescO, k > 0 || !first);
                     }
-                    p_phase ^= 1u;
-                    tc::commit(pv_done);
-                    release(&ctl->empty[v_slot], two);
-                    return true;
                 };
                 while (ok) {
                     const uint32_t pi = n_piece % kPieces;
@@ -678,28 +722,57 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = wait(&ctl->q_full[q_pos & 1u], q_pos >> 1 & 1u) && (!two || wait(&ctl->q_full[(q_pos + 1) & 1u], (q_pos + 1) >> 1 & 1u));
                     const uint64_t a = q_desc + (q & 1u) * kTileStep;
                     int left = x.left;
-                    bool begun = false;
-                    for (int i = 0; ok && i < x.tiles; ++i, left -= kKTile) {
-                        const uint32_t k_pos = pos, k_slot = slot, k_phase = phase;
-                        advance();
-                        if (two || turn == s) {
-                            ok = wait_fill(k_pos, k_slot, k_phase);
-                            if (!ok) break;
+                    if (two || turn == s || x.tiles > 1) {
+                        // this thread's tiles: all of them, or every other one
+                        const int step = two ? 1 : 2, skip = two || turn == s ? 0 : 1;
+                        if (skip) advance(), advance(), left -= kKTile;
+                        uint32_t k_slot = slot;
+                        ok = wait_fill(pos, slot, phase, two) && (!two || take_turn());
+                        if (ok) {
                             tc::fence_after();
-                            const uint64_t b = k_desc + k_slot * kTileStep;
-#pragma unroll
-                            for (int k = 0; k < D / 16; ++k) {  // S = Q K^T
-                                const uint64_t o = (uint64_t)(((k / 4) * (kKTile * 128) + (k % 4) * 32) >> 4);
-                                tc::mma_ss(s_t, a + o, b + o, kIdescS, k > 0);
-                            }
+                            scores(a, k_slot);
+                            if (two) pass_turn();
                             tc::commit(s_full);
                             release(&ctl->empty[k_slot], two);
-                            ok = values(pos, slot, phase, left, !begun, two);
-                            begun = true;
                         }
-                        if (!two) turn ^= 1;
-                        advance();
+                        for (int i = skip; ok && i < x.tiles; i += step, left -= step * kKTile) {
+                            advance();
+                            const uint32_t v_pos = pos, v_slot = slot, v_phase = phase;
+                            advance();
+                            const bool last = i + step >= x.tiles;
+                            if (!two && i + 1 < x.tiles) advance(), advance();
+                            k_slot = slot;
+                            ok = ready(v_pos, v_slot, v_phase, left, i == skip, two);
+                            ok = ok && (!two || last || wait_fill(pos, slot, phase, two));
+                            ok = ok && wait(p_ready, p_phase);
+                            p_phase ^= 1u;
+                            ok = ok && (!two || take_turn());
+                            if (!ok) break;
+                            tc::fence_after();
+                            values(v_desc + v_slot * kTileStep, left, i == skip);
+                            if (two) {
+                                // P V and the next Q K^T without a pause
+                                if (!last) scores(a, k_slot);
+                                pass_turn();
+                                tc::commit(last ? pv_done : s_full);
+                                release(&ctl->empty[v_slot], two);
+                                if (!last) release(&ctl->empty[k_slot], two);
+                            } else {
+                                if (last) tc::commit(pv_done);
+                                release(&ctl->empty[v_slot], two);
+                                if (last) break;
+                                ok = wait_fill(pos, slot, phase, two);
+                                if (!ok) break;
+                                tc::fence_after();
+                                scores(a, k_slot);
+                                tc::commit(s_full);
+                                release(&ctl->empty[k_slot], two);
+                            }
+                        }
+                    } else {
+                        advance(), advance();
                     }
+                    if (!two) turn ^= x.tiles & 1;
                     if (ok) {
                         tc::commit(&ctl->q_free[q & 1u]);
                         if (two) tc::mbar_arrive(&ctl->q_free[(q + 1) & 1u]);
@@ -793,75 +866,98 @@ __device__ __forceinline__ void load_part(const float* parts, long long base, in
     }
 }
 
-constexpr int kBatch = 4;  // parts or tokens in flight per warp
+constexpr int kBatch = 2;      // parts or tokens in flight per warp and head
+constexpr int kJoinHeads = 4;  // query heads of one key-value head per warp: its keys and values are loaded once for them
 
-// Joins the parts of one segment for the unit row of query head `head` of the
-// segment's row `rel`; warp `sub` of `warps` takes every warps-th part.
+// Joins the parts of one segment for the unit rows of query heads `head` ..
+// head + n - 1 of the segment's row `rel`; warp `sub` of `warps` takes every
+// warps-th part.
 template <int D>
-__device__ __forceinline__ void join_parts(const AttendParams& p, Acc<D>& a, int seg, int rel, int head, int lane, int sub, int warps,
-                                           const Runs& runs) {
+__device__ __forceinline__ void join_parts(const AttendParams& p, Acc<D> (&a)[kJoinHeads], int n, int seg, int rel, int head, int lane,
+                                           int sub, int warps, const Runs& runs) {
     const Seg s = load_seg(p, seg);
     if (s.tiles == 0) return;
     const bool prefix = seg < p.P;
     const int rt = p.rows_per_tile, u = rel / (2 * rt), left = s.n - u * 2 * rt;
     const bool two = left > rt;
-    const int in = rel - u * 2 * rt, kvh = head / p.share;
+    const int in = rel - u * 2 * rt, kvh = head / p.share, tile = two && in >= rt ? 1 : 0;
     const int sets = two ? 1 : 2;  // a unit of one tile: a part of each warpgroup
-    const int row = (two ? in % rt : in) * p.share + head % p.share;
-    const unsigned long long begin = p.sc.seg_tiles[seg] + (unsigned long long)(kvh * s.units + u) * s.tiles;
-    const long long slot = (long long)p.sc.seg_units[seg] + kvh * s.units + u;
-    // the blocks whose runs hold the unit's first and last tile
-    const int c0 = runs.block_of(begin), c1 = runs.block_of(begin + s.tiles - 1);
-    const int count = (c1 - c0 + 1) * sets;
+    const int row = (in - tile * rt) * p.share + head - kvh * p.share;
+    const int unit = kvh * s.units + u;
+    const int2 slots = p.sc.seg_units[seg];
+    long long slot;  // of the unit's first piece
+    int pieces = 1;
+    if (unit < s.dealt) {
+        slot = (long long)slots.y + unit;
+    } else {
+        // the blocks whose runs hold the unit's first and last tile
+        const unsigned long long begin = p.sc.seg_tiles[seg] + (unsigned long long)(unit - s.dealt) * s.span() + kUnitCost;
+        const int c0 = runs.block_of(begin);
+        pieces = runs.block_of(begin + s.tiles - 1) - c0 + 1;
+        slot = (long long)slots.x + (unit - s.dealt) + c0;
+    }
+    const int count = pieces * sets, cap = prefix ? kQTile : p.sc.group_rows;
     for (int k0 = sub; k0 < count; k0 += warps * kBatch) {
-        float2 ml[kBatch];
-        float v[kBatch][D / 32];
+        float2 ml[kBatch][kJoinHeads];
+        float v[kBatch][kJoinHeads][D / 32];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             const int k = k0 + b * warps;
-            ml[b] = make_float2(kNegInf, 0.0f);
+            const long long base = k < count ? part_row(p, prefix, slot + (two ? k : k >> 1), two ? tile : k & 1) : -1;
 #pragma unroll
-            for (int e = 0; e < D / 32; ++e) v[b][e] = 0.0f;
-            if (k < count) {
-                const int piece = k / sets, set = k - piece * sets;
-                const long long base = part_row(p, prefix, slot + c0 + piece, two ? in / rt : set);
-                if (base >= 0) {
-                    ml[b] = p.sc.part_ml[base + row];
-                    load_part<D>(p.sc.part_o, base, prefix ? kQTile : p.sc.group_rows, row, lane, v[b]);
+            for (int h = 0; h < kJoinHeads; ++h) {
+                ml[b][h] = make_float2(kNegInf, 0.0f);
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e) v[b][h][e] = 0.0f;
+                if (base >= 0 && h < n) {
+                    ml[b][h] = p.sc.part_ml[base + row + h];
+                    load_part<D>(p.sc.part_o, base, cap, row + h, lane, v[b][h]);
                 }
             }
         }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b)
-            if (ml[b].x != kNegInf || ml[b].y != 0.0f) a.add(ml[b].x, ml[b].y, v[b]);  // else nothing was written
+#pragma unroll
+            for (int h = 0; h < kJoinHeads; ++h)
+                if (ml[b][h].x != kNegInf || ml[b][h].y != 0.0f) a[h].add(ml[b][h].x, ml[b][h].y, v[b][h]);  // else nothing was written
     }
 }
 
-// kSub warps per (row, query head): the round's own tokens that the row sees,
-// then the parts of the row's prefix and of its group's committed tokens.
+// kSub warps per row and kJoinHeads query heads: the round's own tokens that
+// the row sees, then the parts of the row's prefix and of its group's committed
+// tokens.
 template <bool kBf16, int D, int kSub>
 __global__ void __launch_bounds__(kJoinThreads) lp_attend_join_kernel(const AttendParams p) {
     using H = Half<kBf16>;
     using T = typename H::T;
     constexpr int kE = D / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % kSub;
-    const int row = blockIdx.x, head = blockIdx.y * (kJoinWarps / kSub) + warp / kSub;
+    const int chunks = (p.share + kJoinHeads - 1) / kJoinHeads;
+    const int row = blockIdx.x, chunk = blockIdx.y * (kJoinWarps / kSub) + warp / kSub;
+    const int kvh = chunk / chunks, first = (chunk - kvh * chunks) * kJoinHeads, head = kvh * p.share + first;
+    const int n = p.share - first < kJoinHeads ? p.share - first : kJoinHeads;  // this warp's heads
     const int g = block_find_group(p.indptr, p.G, row);
-    bool mine = g >= 0 && g < p.G && head < p.q_heads;
+    bool mine = g >= 0 && g < p.G && kvh < p.kv_heads;
     mine = mine && row >= __ldg(&p.indptr[g]) && row < __ldg(&p.indptr[g + 1]);  // else two entries claim the row
-    Acc<D> a;
-    a.clear();
+    Acc<D> a[kJoinHeads];
+#pragma unroll
+    for (int h = 0; h < kJoinHeads; ++h) a[h].clear();
     Group grp = {0, 0, 0, false};
     if (mine) grp = load_group(p, g);
     if (grp.n > 0) {
-        float q[kE];
-        load_lane<kBf16, D>(p.q, row * p.q_stride + (long long)head * D + lane * kE, q);
+        float q[kJoinHeads][kE];
+#pragma unroll
+        for (int h = 0; h < kJoinHeads; ++h) {
+#pragma unroll
+            for (int e = 0; e < kE; ++e) q[h][e] = 0.0f;
+            if (h < n) load_lane<kBf16, D>(p.q, row * p.q_stride + (long long)(head + h) * D + lane * kE, q[h]);
+        }
         const float c = p.scale * kLog2e;
         const int* table = p.tables + (long long)g * p.max_pages;
-        const int j = row - grp.r0, kvh = head / p.share;
+        const int j = row - grp.r0;
         const unsigned mask = p.row_masks != nullptr ? __ldg(&p.row_masks[row]) : (2u << j) - 1u;
         for (int i0 = sub; i0 < grp.n; i0 += kSub * kBatch) {
-            float k[kBatch][kE], v[kBatch][kE], s[kBatch];
+            float k[kBatch][kE], v[kBatch][kE], s[kBatch][kJoinHeads];
             bool sees[kBatch];
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
@@ -883,18 +979,24 @@ __global__ void __launch_bounds__(kJoinThreads) lp_attend_join_kernel(const Atte
                 }
             }
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-                s[b] = 0.0f;
+            for (int b = 0; b < kBatch; ++b)
 #pragma unroll
-                for (int e = 0; e < kE; ++e) s[b] = fmaf(q[e], k[b][e], s[b]);
-            }
+                for (int h = 0; h < kJoinHeads; ++h) {
+                    s[b][h] = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) s[b][h] = fmaf(q[h][e], k[b][e], s[b][h]);
+                }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-                for (int b = 0; b < kBatch; ++b) s[b] += __shfl_xor_sync(kFull, s[b], o);
+                for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+                    for (int h = 0; h < kJoinHeads; ++h) s[b][h] += __shfl_xor_sync(kFull, s[b][h], o);
 #pragma unroll
             for (int b = 0; b < kBatch; ++b)
-                if (sees[b]) a.add(s[b] * c, 1.0f, v[b]);
+#pragma unroll
+                for (int h = 0; h < kJoinHeads; ++h)
+                    if (sees[b] && h < n) a[h].add(s[b][h] * c, 1.0f, v[b]);
         }
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -903,41 +1005,50 @@ __global__ void __launch_bounds__(kJoinThreads) lp_attend_join_kernel(const Atte
         for (int i = 0; i < p.P; ++i) {
             const Prefix x = load_prefix(p, i);
             if (x.bad || g < x.g0 || g >= x.g1) continue;
-            join_parts<D>(p, a, i, row - x.r0, head, lane, sub, kSub, runs);
+            join_parts<D>(p, a, n, i, row - x.r0, head, lane, sub, kSub, runs);
             break;
         }
-        join_parts<D>(p, a, p.P + g, row - grp.r0, head, lane, sub, kSub, runs);
+        join_parts<D>(p, a, n, p.P + g, row - grp.r0, head, lane, sub, kSub, runs);
     }
     if constexpr (kSub > 1) {  // the warps' sums, in the order of the warps
-        __shared__ float4 part[kJoinWarps][32];
-        __shared__ float2 part_ml[kJoinWarps];
-        part[warp][lane] = make_float4(a.o[0], a.o[1], kE > 2 ? a.o[kE - 2] : 0.0f, kE > 2 ? a.o[kE - 1] : 0.0f);
-        if (lane == 0) part_ml[warp] = make_float2(a.m, a.l);
+        __shared__ float4 part[kJoinWarps][kJoinHeads][32];
+        __shared__ float2 part_ml[kJoinWarps][kJoinHeads];
+#pragma unroll
+        for (int h = 0; h < kJoinHeads; ++h) {
+            part[warp][h][lane] = make_float4(a[h].o[0], a[h].o[1], kE > 2 ? a[h].o[kE - 2] : 0.0f, kE > 2 ? a[h].o[kE - 1] : 0.0f);
+            if (lane == 0) part_ml[warp][h] = make_float2(a[h].m, a[h].l);
+        }
         __syncthreads();
         if (sub != 0) return;
 #pragma unroll
-        for (int w = 1; w < kSub; ++w) {
-            const float4 o = part[warp + w][lane];
-            const float2 ml = part_ml[warp + w];
-            float v[kE];
-            v[0] = o.x, v[1] = o.y;
-            if constexpr (kE > 2) v[2] = o.z, v[3] = o.w;
-            if (ml.x != kNegInf || ml.y != 0.0f) a.add(ml.x, ml.y, v);
-        }
+        for (int w = 1; w < kSub; ++w)
+#pragma unroll
+            for (int h = 0; h < kJoinHeads; ++h) {
+                const float4 o = part[warp + w][h][lane];
+                const float2 ml = part_ml[warp + w][h];
+                float v[kE];
+                v[0] = o.x, v[1] = o.y;
+                if constexpr (kE > 2) v[2] = o.z, v[3] = o.w;
+                if (ml.x != kNegInf || ml.y != 0.0f) a[h].add(ml.x, ml.y, v);
+            }
     }
     if (!mine) return;
-    const float inv = a.l > 0.0f ? 1.0f / a.l : (a.l == 0.0f ? 0.0f : a.l);
-    T* dst = reinterpret_cast<T*>(p.out) + row * p.out_stride + (long long)head * D + lane * kE;
-    if constexpr (D == 128) {
-        uint2 w;
-        w.x = H::pack(a.o[0] * inv, a.o[1] * inv);
-        w.y = H::pack(a.o[2] * inv, a.o[3] * inv);
-        *reinterpret_cast<uint2*>(dst) = w;
-    } else {
-        *reinterpret_cast<uint32_t*>(dst) = H::pack(a.o[0] * inv, a.o[1] * inv);
+#pragma unroll
+    for (int h = 0; h < kJoinHeads; ++h) {
+        if (h >= n) break;
+        const float inv = a[h].l > 0.0f ? 1.0f / a[h].l : (a[h].l == 0.0f ? 0.0f : a[h].l);
+        T* dst = reinterpret_cast<T*>(p.out) + row * p.out_stride + (long long)(head + h) * D + lane * kE;
+        if constexpr (D == 128) {
+            uint2 w;
+            w.x = H::pack(a[h].o[0] * inv, a[h].o[1] * inv);
+            w.y = H::pack(a[h].o[2] * inv, a[h].o[3] * inv);
+            *reinterpret_cast<uint2*>(dst) = w;
+        } else {
+            *reinterpret_cast<uint32_t*>(dst) = H::pack(a[h].o[0] * inv, a[h].o[1] * inv);
+        }
+        if (p.lse_out != nullptr && lane == 0)
+            p.lse_out[(long long)row * p.q_heads + head + h] = a[h].l == 0.0f ? kNegInf : a[h].m * kLn2 + logf(a[h].l);
     }
-    if (p.lse_out != nullptr && lane == 0)
-        p.lse_out[(long long)row * p.q_heads + head] = a.l == 0.0f ? kNegInf : a.m * kLn2 + logf(a.l);
 }
 
 template <int D>
@@ -955,13 +1066,14 @@ cudaError_t launch(const AttendParams& p, const CUtensorMap& k_map, const CUtens
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     // few rows: several warps share a row's parts
-    const long long heads = (long long)p.rows * p.q_heads;
-    const int sub = heads <= 8 * p.grid ? 8 : (heads <= 32 * p.grid ? 2 : 1);
+    const int chunks = (p.share + kJoinHeads - 1) / kJoinHeads * p.kv_heads;
+    const long long tasks = (long long)p.rows * chunks;
+    const int sub = tasks <= 4 * p.grid ? 8 : (tasks <= 16 * p.grid ? 2 : 1);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3((unsigned)p.rows, (unsigned)((p.q_heads * sub + kJoinWarps - 1) / kJoinWarps));
+    lc.gridDim = dim3((unsigned)p.rows, (unsigned)((chunks * sub + kJoinWarps - 1) / kJoinWarps));
     lc.blockDim = dim3(kJoinThreads);
     lc.stream = stream;
     lc.attrs = attr;

@@ -84,7 +84,7 @@ Layout layout_of(const lp_attn_desc* d, int grid) {
     L.seg_tiles = off;
     off = lp::align_up(off + (segs + 1) * 8);
     L.seg_units = off;
-    off = lp::align_up(off + segs * 4);
+    off = lp::align_up(off + segs * 8);
     L.part_ml = off;
     off = lp::align_up(off + part_rows * 8);
     L.part_o = off;
@@ -211,7 +211,7 @@ int lp_attn_create(lp_attn_t* out, const lp_attn_desc* desc) {
         return cuda_fail(e);
     }
     plan->sc.seg_tiles = reinterpret_cast<unsigned long long*>(plan->scratch + L.seg_tiles);
-    plan->sc.seg_units = reinterpret_cast<int*>(plan->scratch + L.seg_units);
+    plan->sc.seg_units = reinterpret_cast<int2*>(plan->scratch + L.seg_units);
     plan->sc.part_ml = reinterpret_cast<float2*>(plan->scratch + L.part_ml);
     plan->sc.part_o = reinterpret_cast<float*>(plan->scratch + L.part_o);
     plan->sc.prefix_slots = L.prefix_slots;

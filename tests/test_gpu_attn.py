@@ -337,6 +337,14 @@ def test_attend_many_rows_behind_a_prefix():
     Case(n=n, lens=lens, prefixes=[517], hq=10, hk=2, d=64, dtype="f16", page=64).check()
 
 
+def test_attend_more_units_than_blocks():
+    """Prefixes whose query tiles go round the blocks whole, some once and some twice, and a rest that is cut."""
+    n = [20, 31, 7, 32, 32, 28, 12]
+    c = Case(n=n, lens=[0, 140, -1, 3, 0, 128, 9], prefixes=[260, 129], prefix_indptr=[0, 5, 7], hq=32 * 12, hk=32, d=64)
+    c.check()
+    Case(n=n, lens=[0, 140, -1, 3, 0, 128, 9], prefixes=[140], hq=16 * 40, hk=16, dtype="f16").check()
+
+
 def test_attend_trees_and_empty_rows():
     r = np.random.RandomState(0)
     n, lens = [7, 32, 1, 16, 3], [0, 50, 0, 131, 0]
