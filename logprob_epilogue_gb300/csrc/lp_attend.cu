@@ -17,9 +17,10 @@
 //
 // The query rows of a segment and key-value head (a row's `share` heads side
 // by side) form units of up to two tiles of 128; a unit's tokens form tiles of
-// 128.  All token tiles of the call, unit after unit, are cut into one equal
-// run per block, wherever that falls: one request at a long context and
-// hundreds of short ones fill the machine alike, and no block waits on
+// 128.  The prefixes' token tiles, unit after unit, are cut into one equal run
+// per block, wherever that falls, and after them the groups': one request at a
+// long context and hundreds of short ones fill the machine alike, the blocks
+// are all at the arithmetic or all at the memory at a time, and none waits on
 // another.  Before that, a prefix with more units than blocks deals them out
 // whole, one to every block at a time: the blocks of a head then go through
 // its tokens side by side, and a tile that one of them fetched is still in L2
@@ -54,7 +55,12 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr float kRescale = 8.0f;  // growth of the maximum (log2) that moves it
-constexpr int kUnitCost = 2;      // what a unit costs a block beside its tiles, in tiles
+// What a run is measured in: a token tile of a one-tile unit is 2, of a two-tile
+// unit 3, and every unit 4 more (its queries, first loads and results).  No run
+// is shorter than a tile, nor one of prefixes than four (every run of a unit
+// leaves a part for the join to read).
+constexpr int kTileCost = 2, kPairCost = 3, kUnitCost = 4;
+constexpr int kLeastPrefix = 4 * kPairCost, kLeastGroup = kPairCost;
 // Registers: the softmax warpgroups hold 128 scores per thread.  The split's
 // sum is what the block is launched with, 384 x 168.
 constexpr int kRegsLaunch = 168, kRegsSoftmax = 200, kRegsOther = 104;
@@ -123,8 +129,9 @@ struct Seg {
     int dealt;         // of all heads' units, those that go round the blocks whole
     bool bad;
     __device__ __forceinline__ int left(const AttendParams& p) const { return tiles > 0 ? units * p.kv_heads - dealt : 0; }
-    __device__ __forceinline__ int span() const { return tiles + kUnitCost; }  // of a unit in a run
-    __device__ __forceinline__ unsigned long long work(const AttendParams& p) const { return (unsigned long long)span() * left(p); }
+    int cost;          // of a token tile
+    __device__ __forceinline__ long long span() const { return (long long)tiles * cost + kUnitCost; }  // of a unit in a run
+    __device__ __forceinline__ unsigned long long work(const AttendParams& p) const { return (unsigned long long)(span() * left(p)); }
 };
 
 __device__ __forceinline__ Seg load_seg(const AttendParams& p, int s) {
@@ -138,11 +145,12 @@ __device__ __forceinline__ Seg load_seg(const AttendParams& p, int s) {
     }
     x.units = (x.n + 2 * p.rows_per_tile - 1) / (2 * p.rows_per_tile);
     x.tiles = x.n > 0 ? (x.len + kKTile - 1) / kKTile : 0;
+    x.cost = x.n > p.rows_per_tile ? kPairCost : kTileCost;
     x.dealt = s < p.P && x.tiles > 0 ? x.units * p.kv_heads / p.grid * p.grid : 0;
     return x;
 }
 
-// `total` tiles (with the units' cost) cut into one run per block: blocks
+// The units' cost, `total` in all, cut into one run per block: blocks
 // 0..more-1 take per + 1, the others per.
 struct Runs {
     unsigned long long total, per;
@@ -157,10 +165,13 @@ struct Runs {
     }
 };
 
-__device__ __forceinline__ Runs make_runs(unsigned long long total, int grid) {
+__device__ __forceinline__ Runs make_runs(unsigned long long total, int grid, int kind) {
     Runs r;
     r.total = total;
-    r.blocks = total < (unsigned long long)grid ? (int)total : grid;
+    // a run as long as a tile holds the start of one, wherever it lies among a unit's tiles
+    const unsigned long long most = Runs::quotient(total, kind == 0 ? kLeastPrefix : kLeastGroup);
+    r.blocks = most < (unsigned long long)grid ? (int)most : grid;
+    if (r.blocks == 0 && total > 0) r.blocks = 1;
     r.per = r.blocks > 0 ? Runs::quotient(total, r.blocks) : 0;
     r.more = (int)(total - r.per * r.blocks);
     return r;
@@ -191,13 +202,28 @@ struct Piece {
     long long part;     // row 0 of its first part; -1: past the scratch (only overlapping prefixes can ask for that)
 };
 
+// Where a block's run begins: its first segment, the tiles and units before it.
+struct Start {
+    unsigned long long off;
+    int seg, units;
+    Seg s;
+};
+
 // Walks a block's pieces: its share of the units that go round whole, then its
-// run of the other units' tiles.
+// run of the other prefix units' tiles, then of the groups'.
 struct Walk {
+    unsigned long long begin[2], finish[2];  // the runs
+    const Start* start;
+    int kind;
     int deal, deal_end, round, dealt;  // segments with units that go round; rounds dealt; units of earlier segments
     unsigned long long pos, end, off;  // off: tiles before the segment
     int seg, units, cta;               // units: the segment's first slot less cta
     Seg s;
+    __device__ __forceinline__ void enter(int k) {
+        kind = k;
+        pos = begin[k], end = finish[k];
+        off = start[k].off, seg = start[k].seg, units = start[k].units, s = start[k].s;
+    }
     const int* table;                  // pages of the piece, and its first token
     long long token;
     __device__ __forceinline__ void fill(const AttendParams& p, Piece& x, int sg, const Seg& y, int unit, int t0, int tiles, long long slot) {
@@ -226,22 +252,25 @@ struct Walk {
             ++deal;
             round = 0;
         }
-        while (pos < end) {
+        while (pos < end || kind == 0) {
+            if (pos >= end) {
+                enter(1);
+                continue;
+            }
             const unsigned long long work = s.work(p);
             if (pos >= off + work) {
                 off += work;
-                if (++seg >= p.P + p.G) break;
-                units = seg == p.P ? 0 : units + s.left(p);
-                s = load_seg(p, seg);
+                units += s.left(p);
+                s = load_seg(p, ++seg);
                 continue;
             }
-            // the unit's cost lies before its tiles; a run may hold that alone
-            const unsigned long long rel = pos - off, rest = end - pos;
-            const int unit = (int)Runs::quotient(rel, s.span());
-            const int u0 = (int)(rel - (unsigned long long)unit * s.span());
-            const int u1 = rest < (unsigned long long)(s.span() - u0) ? u0 + (int)rest : s.span();
+            // the unit's cost lies before its tiles, and a tile belongs to the run that its start lies in
+            const unsigned long long rel = pos - off, rest = end - pos, span = s.span();
+            const int unit = (int)Runs::quotient(rel, span);
+            const long long u0 = (long long)(rel - unit * span), u1 = rest < span - u0 ? u0 + (long long)rest : (long long)span;
             pos += u1 - u0;
-            const int t0 = u0 > kUnitCost ? u0 - kUnitCost : 0, t1 = u1 - kUnitCost;
+            const int t0 = u0 > kUnitCost ? (int)((u0 - kUnitCost + s.cost - 1) / s.cost) : 0;
+            const int t1 = u1 > kUnitCost ? (int)((u1 - kUnitCost + s.cost - 1) / s.cost) : 0;
             if (t1 <= t0) continue;
             fill(p, x, seg, s, s.dealt + unit, t0, t1 - t0, (long long)units + unit + cta);
             return true;
@@ -258,11 +287,9 @@ struct Ctl {
     uint64_t full[10], empty[10], piece_full[kPieces], piece_empty[kPieces];
     Piece piece[kPieces];
     uint64_t q_full[2], q_free[2], s_full[2], p_ready[2], pv_done[2], o_free[2], clean, drain;
-    unsigned long long sum[kWarps][2];
+    unsigned long long sum[kWarps][3];
     int sum_dealt[kWarps], deal_first, deal_last;
-    unsigned long long start_off;
-    int start_seg, start_units;
-    Seg start;
+    Start start[2];
     uint32_t tmem, issued, batches[2];  // ring fills under way or done; see take_turn
     int abort;
 };
@@ -271,16 +298,16 @@ struct Ctl {
 // the block scans the sums, and the thread that holds the block's first tile
 // names its segment.  Block 0 leaves the offsets for the join.  False: the
 // block has no work.
-__device__ __forceinline__ bool plan_run(const AttendParams& p, Ctl* ctl, Runs& runs) {
+__device__ __forceinline__ bool plan_run(const AttendParams& p, Ctl* ctl, Runs (&runs)[2]) {
     const int S = p.P + p.G, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (S + kThreads - 1) / kThreads;
     const int s0 = tid * per < S ? tid * per : S, s1 = s0 + per < S ? s0 + per : S;
-    // units: slots of units that do not go round, of prefixes in the high half, of groups in the low
-    unsigned long long tiles = 0, units = 0;
+    // of prefixes and of groups; units: slots of units that do not go round, of prefixes in the high half
+    unsigned long long cost0 = 0, cost1 = 0, units = 0;
     int dealt = 0, first = S, last = -1;
     for (int s = s0; s < s1; ++s) {
         const Seg x = load_seg(p, s);
-        tiles += x.work(p);
+        (s < p.P ? cost0 : cost1) += x.work(p);
         units += (unsigned long long)x.left(p) << (s < p.P ? 32 : 0);
         dealt += x.dealt;
         if (x.dealt > 0) {
@@ -289,45 +316,49 @@ __device__ __forceinline__ bool plan_run(const AttendParams& p, Ctl* ctl, Runs& 
         }
         if (x.bad && blockIdx.x == 0) atomicOr(p.status, s < p.P ? kStatusBadPrefix : kStatusAttnBadGroup);
     }
-    unsigned long long it = tiles, iu = units;
+    unsigned long long i0 = cost0, i1 = cost1, iu = units;
     int id = dealt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long a = __shfl_up_sync(kFull, it, o), b = __shfl_up_sync(kFull, iu, o);
+        const unsigned long long a = __shfl_up_sync(kFull, i0, o), b = __shfl_up_sync(kFull, i1, o), c = __shfl_up_sync(kFull, iu, o);
         const int d = __shfl_up_sync(kFull, id, o);
-        if (lane >= o) it += a, iu += b, id += d;
+        if (lane >= o) i0 += a, i1 += b, iu += c, id += d;
     }
-    if (lane == 31) ctl->sum[warp][0] = it, ctl->sum[warp][1] = iu, ctl->sum_dealt[warp] = id;
+    if (lane == 31) ctl->sum[warp][0] = i0, ctl->sum[warp][1] = i1, ctl->sum[warp][2] = iu, ctl->sum_dealt[warp] = id;
     if (tid == 0) ctl->deal_first = S, ctl->deal_last = -1;
     __syncthreads();
     if (last >= 0) atomicMin(&ctl->deal_first, first), atomicMax(&ctl->deal_last, last);
-    unsigned long long bt = 0, bu = 0, total = 0;
+    unsigned long long b0 = 0, b1 = 0, bu = 0, total0 = 0, total1 = 0;
     int bd = 0, all_dealt = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-        if (w == warp) bt = total, bd = all_dealt;
-        if (w < warp) bu += ctl->sum[w][1];
-        total += ctl->sum[w][0];
+        if (w == warp) b0 = total0, b1 = total1, bd = all_dealt;
+        if (w < warp) bu += ctl->sum[w][2];
+        total0 += ctl->sum[w][0];
+        total1 += ctl->sum[w][1];
         all_dealt += ctl->sum_dealt[w];
     }
-    unsigned long long off = bt + it - tiles, u = bu + iu - units;
+    unsigned long long at0 = b0 + i0 - cost0, at1 = b1 + i1 - cost1, u = bu + iu - units;
     int d = bd + id - dealt;
-    runs = make_runs(total, gridDim.x);
-    const unsigned long long lo = (int)blockIdx.x < runs.blocks ? runs.start(blockIdx.x) : ~0ull;
-    if (blockIdx.x == 0 || (lo >= off && lo < off + tiles)) {
+    runs[0] = make_runs(total0, gridDim.x, 0);
+    runs[1] = make_runs(total1, gridDim.x, 1);
+    const int cta = blockIdx.x;
+    const unsigned long long lo0 = cta < runs[0].blocks ? runs[0].start(cta) : ~0ull, lo1 = cta < runs[1].blocks ? runs[1].start(cta) : ~0ull;
+    if (cta == 0 || (lo0 >= at0 && lo0 < at0 + cost0) || (lo1 >= at1 && lo1 < at1 + cost1)) {
         for (int s = s0; s < s1; ++s) {
             const Seg x = load_seg(p, s);
-            const unsigned long long work = x.work(p);
-            const int before = (int)(s < p.P ? (u >> 32) + all_dealt : u & 0xFFFFFFFFull);  // slots: the dealt units', then the others'
-            if (blockIdx.x == 0) p.sc.seg_tiles[s] = off, p.sc.seg_units[s] = make_int2(before, d);
-            if (lo >= off && lo < off + work) ctl->start_seg = s, ctl->start_units = before, ctl->start_off = off, ctl->start = x;
-            off += work;
-            u += (unsigned long long)x.left(p) << (s < p.P ? 32 : 0);
+            const int kind = s < p.P ? 0 : 1;
+            const unsigned long long work = x.work(p), off = kind == 0 ? at0 : at1, lo = kind == 0 ? lo0 : lo1;
+            const int before = (int)(kind == 0 ? (u >> 32) + all_dealt : u & 0xFFFFFFFFull);  // slots: the dealt units', then the others'
+            if (cta == 0) p.sc.seg_tiles[s] = off, p.sc.seg_units[s] = make_int2(before, d);
+            if (lo >= off && lo < off + work) ctl->start[kind].off = off, ctl->start[kind].seg = s, ctl->start[kind].units = before, ctl->start[kind].s = x;
+            (kind == 0 ? at0 : at1) += work;
+            u += (unsigned long long)x.left(p) << (kind == 0 ? 32 : 0);
             d += x.dealt;
         }
     }
-    if (blockIdx.x == 0 && tid == 0) p.sc.seg_tiles[S] = total;
-    return all_dealt > 0 || (int)blockIdx.x < runs.blocks;
+    if (cta == 0 && tid == 0) p.sc.seg_tiles[S] = total0, p.sc.seg_tiles[S + 1] = total1;
+    return all_dealt > 0 || cta < runs[0].blocks || cta < runs[1].blocks;
 }
 
 __device__ __forceinline__ unsigned long long pack2(uint32_t a, uint32_t b) {
@@ -359,78 +390,139 @@ struct Row {
     float m, base, l;
 };
 
-// Softmax of one score tile by one warp, a row per thread; `valid` of the 128
-// tokens exist.  Writes the row's probabilities over the scores.
-template <bool kBf16, int D>
-__device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, int valid, bool first, float c, Row& row) {
-    using H = Half<kBf16>;
+// The maximum after scores up to `top`; f: what sums so far are worth under it.
+// The first tile sets it; later it moves only where it grew by 2^kRescale
+// (`used`: the row exists), so that most tiles leave the accumulator alone.
+template <bool kBf16>
+__device__ __forceinline__ bool raise(Row& row, float top, bool first, bool used, float c, float& f) {
     // F16 keeps probabilities down to 2^-24: lifting them by 2^6 (at most 2^14 then) keeps those above 2^-30
     constexpr float kBias = kBf16 ? 0.0f : 6.0f;
-    uint32_t r[4][32];
-#pragma unroll
-    for (int b = 0; b < 4; ++b) tc::tmem_ld32(s_col + b * 32, r[b]);
-    tc::wait_ld();
-#pragma unroll
-    for (int b = 0; b < 4; ++b) tc::tie(r[b]);
-    if (valid < kKTile) {
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-                if (b * 32 + e >= valid) r[b][e] = __float_as_uint(kNegInf);
-    }
-    float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
-#pragma unroll
-        for (int e = 0; e < 32; e += 2)
-            mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(r[b][e]), __uint_as_float(r[b][e + 1]));
-    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+    f = 1.0f;
     if (first) {
         row.m = top;
         row.base = top == kNegInf ? 0.0f : top * c - kBias;
         row.l = 0.0f;
-    } else {
-        const bool grow = row.m == kNegInf ? top > row.m : top * c > row.m * c + kRescale;
-        if (__any_sync(kFull, grow)) {
-            float f = 1.0f;
-            if (grow) {
-                const float next = top * c - kBias;
-                if (row.m != kNegInf) f = ex2(row.base - next);
-                row.m = top;
-                row.base = next;
-                row.l *= f;
-            }
-            // the scores came after the products before them, so the accumulator is this warp's to change
-#pragma unroll 1
-            for (int b = 0; b < D / 32; ++b) {
-                uint32_t o[32];
-                tc::tmem_ld32(o_col + b * 32, o);
-                tc::wait_ld();
-                tc::tie(o);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tc::tmem_st32(o_col + b * 32, o);
-            }
-        }
+        return false;
     }
-    const unsigned long long c2 = pack2(__float_as_uint(c), __float_as_uint(c));
-    const unsigned long long nb2 = pack2(__float_as_uint(-row.base), __float_as_uint(-row.base));
+    const bool grow = used && (row.m == kNegInf ? top > row.m : top * c > row.m * c + kRescale);
+    if (grow) {
+        const float next = top * c - kBias;
+        if (row.m != kNegInf) f = ex2(row.base - next);
+        row.m = top;
+        row.base = next;
+        row.l *= f;
+    }
+    return __any_sync(kFull, grow);
+}
+
+// O *= f: the scores came after the products before them, so the accumulator
+// is this warp's to change.
+template <int D>
+__device__ __forceinline__ void rescale(uint32_t o_col, float f) {
+#pragma unroll 1
+    for (int b = 0; b < D / 32; ++b) {
+        uint32_t o[32];
+        tc::tmem_ld32(o_col + b * 32, o);
+        tc::wait_ld();
+        tc::tie(o);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+        tc::tmem_st32(o_col + b * 32, o);
+    }
+}
+
+__device__ __forceinline__ float max32(const uint32_t (&r)[32], float top) {
+    float a = top, b = kNegInf;
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+        a = max3(a, __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+        b = max3(b, __uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]));
+    }
+    return fmaxf(a, b);
+}
+
+__device__ __forceinline__ void mask32(uint32_t (&r)[32], int valid) {
+    if (valid < 32) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if (e >= valid) r[e] = __float_as_uint(kNegInf);
+    }
+}
+
+// 32 scores to 16 words of probabilities, and their sums in pairs.
+template <bool kBf16>
+__device__ __forceinline__ void exp32(const uint32_t (&r)[32], uint32_t (&w)[16], unsigned long long c2, unsigned long long nb2,
+                                      unsigned long long (&sum)[2]) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        float x, y;
+        unpack2(fma2(pack2(r[2 * e], r[2 * e + 1]), c2, nb2), x, y);
+        x = ex2(x);
+        y = ex2(y);
+        sum[e & 1] = add2(sum[e & 1], pack2(__float_as_uint(x), __float_as_uint(y)));
+        w[e] = Half<kBf16>::pack(x, y);
+    }
+}
+
+// Softmax of one score tile by one warp, a row per thread; `valid` of the 128
+// tokens exist.  Writes the row's probabilities over the scores (as many 16s of
+// them as the products will take in).
+//
+// kWide: every score in registers, all of it unrolled, for units of two tiles,
+// where eight warps run through the same instructions.  Otherwise 32 columns
+// at a time, twice: with few rows one warp has them all, and a long unrolled
+// run of its own is bound by the instruction fetch (3,000 to 4,500 cycles a
+// tile against 1,300).
+template <bool kBf16, int D, bool kWide>
+__device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, int valid, bool first, bool used, float c, Row& row) {
     unsigned long long sum[2] = {0, 0};
-    // 32 columns at a time: 16 words of probabilities
+    const unsigned long long c2 = pack2(__float_as_uint(c), __float_as_uint(c));
+    float top = kNegInf, f;
+    if constexpr (kWide) {
+        uint32_t r[4][32];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        uint32_t w[16];
+        for (int b = 0; b < 4; ++b) tc::tmem_ld32(s_col + b * 32, r[b]);
+        tc::wait_ld();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            float x, y;
-            unpack2(fma2(pack2(r[b][2 * e], r[b][2 * e + 1]), c2, nb2), x, y);
-            x = ex2(x);
-            y = ex2(y);
-            sum[e & 1] = add2(sum[e & 1], pack2(__float_as_uint(x), __float_as_uint(y)));
-            w[e] = H::pack(x, y);
+        for (int b = 0; b < 4; ++b) tc::tie(r[b]);
+        if (valid < kKTile) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b) mask32(r[b], valid - b * 32);
         }
-        tc::tmem_st16(s_col + b * 16, w);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) top = max32(r[b], top);
+        if (raise<kBf16>(row, top, first, used, c, f)) rescale<D>(o_col, f);
+        const unsigned long long nb2 = pack2(__float_as_uint(-row.base), __float_as_uint(-row.base));
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            uint32_t w[16];
+            exp32<kBf16>(r[b], w, c2, nb2, sum);
+            tc::tmem_st16(s_col + b * 16, w);
+        }
+    } else {
+        const int chunks = valid < kKTile ? (valid + 31) >> 5 : 4;
+#pragma unroll 1
+        for (int b = 0; b < chunks; ++b) {
+            uint32_t r[32];
+            tc::tmem_ld32(s_col + b * 32, r);
+            tc::wait_ld();
+            tc::tie(r);
+            mask32(r, valid - b * 32);
+            top = max32(r, top);
+        }
+        if (raise<kBf16>(row, top, first, used, c, f)) rescale<D>(o_col, f);
+        const unsigned long long nb2 = pack2(__float_as_uint(-row.base), __float_as_uint(-row.base));
+        // a chunk's probabilities take the columns of scores that have been read
+#pragma unroll 1
+        for (int b = 0; b < chunks; ++b) {
+            uint32_t r[32], w[16];
+            tc::tmem_ld32(s_col + b * 32, r);
+            tc::wait_ld();
+            tc::tie(r);
+            mask32(r, valid - b * 32);
+            exp32<kBf16>(r, w, c2, nb2, sum);
+            tc::tmem_st16(s_col + b * 16, w);
+        }
     }
     float x, y;
     unpack2(add2(sum[0], sum[1]), x, y);
@@ -447,10 +539,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) unsigned char smem[];
     Ctl* ctl = reinterpret_cast<Ctl*>(smem + C::kCtl);
     unsigned char* ring = smem + 2 * C::kTileBytes;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(kFull, tid >> 5, 0);  // the same for the warp, as the compiler sees
     asm volatile("griddepcontrol.launch_dependents;");  // the join waits for this grid's end by itself
     const unsigned long long limit = p.timeout_ns;
-    Runs runs;
+    Runs runs[2];  // of prefixes, of groups
     if (!plan_run(p, ctl, runs)) return;
 
     if (tid == 0) {
@@ -524,7 +617,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (live) {
                     tc::fence_after();
-                    softmax_tile<kBf16, D>(s_col, o_col, x.left - i * kKTile, i == first, c, st);
+                    if (two) softmax_tile<kBf16, D, true>(s_col, o_col, x.left - i * kKTile, i == first, row < valid_rows, c, st);
+                    else softmax_tile<kBf16, D, false>(s_col, o_col, x.left - i * kKTile, i == first, row < valid_rows, c, st);
                     tc::fence_before();
                     __syncwarp();
                 }
@@ -546,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::fence_after();
                 if (store) p.sc.part_ml[part + row] = make_float2(st.m == kNegInf ? kNegInf : st.base, st.l);
                 float4* dst = reinterpret_cast<float4*>(p.sc.part_o) + part_chunk<D>(part, x.part_stride, row, 0);
-#pragma unroll
+#pragma unroll 1
                 for (int b = 0; b < D / 32; ++b) {
                     uint32_t o[32];
                     tc::tmem_ld32(o_col + b * 32, o);
@@ -576,15 +670,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             walk.deal = ctl->deal_first;
             walk.deal_end = ctl->deal_last + 1;
             walk.round = walk.dealt = 0;
-            walk.pos = walk.end = 0;
-            if ((int)blockIdx.x < runs.blocks) {
-                walk.pos = runs.start(blockIdx.x);
-                walk.end = runs.start(blockIdx.x + 1);
+            walk.start = ctl->start;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const bool any = (int)blockIdx.x < runs[k].blocks;
+                walk.begin[k] = any ? runs[k].start(blockIdx.x) : 0;
+                walk.finish[k] = any ? runs[k].start(blockIdx.x + 1) : 0;
             }
-            walk.off = ctl->start_off;
-            walk.seg = ctl->start_seg;
-            walk.units = ctl->start_units;
-            walk.s = ctl->start;
+            walk.enter(0);
             auto fetch = [&](const CUtensorMap* map, int n, int fy, int fh, int fp) {
                 const uint32_t slot = it % C::kSlots;
                 if (!tc::warp_wait(&ctl->empty[slot], (it / C::kSlots & 1u) ^ 1u, limit, abort)) return false;
@@ -633,156 +726,155 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t i = it > C::kSlots ? it - C::kSlots : 0; i < it; ++i)
                 tc::mbar_wait(&ctl->full[i % C::kSlots], i / C::kSlots & 1u, limit, &none);
         } else if (warp <= 2) {
-            // ---- the products of tensor tile s, issued by one thread; the other tile's run while this thread waits and commits
-            if (lane == 0) {
-                constexpr uint32_t kIdescS = tc::make_idesc(kBf16, false, kQTile, kKTile), kIdescO = tc::make_idesc(kBf16, true, kQTile, D);
-                constexpr uint32_t kTileStep = C::kTileBytes >> 4;
-                const int s = warp - 1;
-                const uint64_t q_desc = tc::make_desc(tc::smem_addr(smem), 16, 1024);
-                const uint64_t k_desc = tc::make_desc(tc::smem_addr(ring), 16, 1024), v_desc = tc::make_desc(tc::smem_addr(ring), kKTile * 128, 1024);
-                const uint32_t s_t = tmem + kColS + s * kColStep, o_t = tmem + kColO + s * kColStep;
-                uint64_t *s_full = &ctl->s_full[s], *p_ready = &ctl->p_ready[s], *pv_done = &ctl->pv_done[s], *o_free = &ctl->o_free[s];
-                uint32_t q_pos = 0, pos = 0, slot = 0, phase = 0, p_phase = 0, o_phase = 1, clean_phase = 0;  // pos, slot, phase: the next ring position
-                uint32_t batch = 0;
-                int turn = 0;  // whose the next tile of a one-tile unit is
-                auto wait = [&](uint64_t* bar, uint32_t parity) { return tc::mbar_wait(bar, parity, limit, abort); };
-                auto advance = [&]() {
-                    ++pos;
-                    if (++slot == C::kSlots) slot = 0, phase ^= 1u;
-                };
-                // A position's fill.  In units of one tile this thread passes over the other's tiles, so it may look at a slot
-                // before the fill ahead of its own has ended, and the parity of that older phase would let it through: it
-                // first waits until its own fill is under way (which the older one's release comes before).
-                auto wait_fill = [&](uint32_t at, uint32_t fill_slot, uint32_t fill_phase, bool two) {
-                    return (two || tc::wait_count(&ctl->issued, at, limit, abort)) && wait(&ctl->full[fill_slot], fill_phase);
-                };
-                // A slot comes free after two arrivals.  In units of two tiles thread 1, the last to use it, makes one as soon
-                // as its products are in, and warpgroup 0 the other when it sees the scores that followed thread 0's; in
-                // units of one tile the only user makes both.
-                auto release = [&](uint64_t* bar, bool two) {
-                    if (!two || s == 1) tc::commit(bar);
-                    if (!two) tc::commit(bar);
-                };
-                // In units of two tiles the threads take turns with the tensor core: P V and the next Q K^T of one tile, then of
-                // the other.  Left alone the two fall into step: both warpgroups in softmax, then both tiles' products, each
-                // idle during the other.
-                auto take_turn = [&]() { return tc::wait_count(&ctl->batches[s ^ 1], batch - (s ^ 1), limit, abort); };
-                auto pass_turn = [&]() { tc::store_release(&ctl->batches[s], ++batch); };
-                auto scores = [&](uint64_t a, uint32_t k_slot) {  // S = Q K^T
-                    const uint64_t b = k_desc + k_slot * kTileStep;
+            // ---- the products of tensor tile s; the other tile's run while this warp waits and commits.  The whole warp
+            // walks through, and one lane is elected for each instruction: descriptors stay in uniform registers, and 16
+            // products are issued in 650 cycles (in a branch of one lane: 1,240 beside two busy softmax warps).
+            constexpr uint32_t kIdescS = tc::make_idesc(kBf16, false, kQTile, kKTile), kIdescO = tc::make_idesc(kBf16, true, kQTile, D);
+            constexpr uint32_t kTileStep = C::kTileBytes >> 4;
+            const uint32_t one = tc::elect_one();
+            const int s = warp - 1;
+            const uint64_t q_desc = tc::make_desc(tc::smem_addr(smem), 16, 1024);
+            const uint64_t k_desc = tc::make_desc(tc::smem_addr(ring), 16, 1024), v_desc = tc::make_desc(tc::smem_addr(ring), kKTile * 128, 1024);
+            const uint32_t tm = __shfl_sync(kFull, tmem, 0), s_t = tm + kColS + s * kColStep, o_t = tm + kColO + s * kColStep;
+            uint64_t *s_full = &ctl->s_full[s], *p_ready = &ctl->p_ready[s], *pv_done = &ctl->pv_done[s], *o_free = &ctl->o_free[s];
+            uint32_t q_pos = 0, pos = 0, slot = 0, phase = 0, p_phase = 0, o_phase = 1, clean_phase = 0;  // pos, slot, phase: the next ring position
+            uint32_t batch = 0;
+            int turn = 0;  // whose the next tile of a one-tile unit is
+            auto wait = [&](uint64_t* bar, uint32_t parity) { return tc::warp_wait(bar, parity, limit, abort); };
+            auto advance = [&]() {
+                ++pos;
+                if (++slot == C::kSlots) slot = 0, phase ^= 1u;
+            };
+            // A position's fill.  In units of one tile this warp passes over the other's tiles, so it may look at a slot before
+            // the fill ahead of its own has ended, and the parity of that older phase would let it through: it first waits
+            // until its own fill is under way (which the older one's release comes before).
+            auto wait_fill = [&](uint32_t at, uint32_t fill_slot, uint32_t fill_phase, bool two) {
+                return (two || __all_sync(kFull, tc::wait_count(&ctl->issued, at, limit, abort))) && wait(&ctl->full[fill_slot], fill_phase);
+            };
+            // A slot comes free after two arrivals.  In units of two tiles warp 2, the last to use it, makes one as soon as its
+            // products are in, and warpgroup 0 the other when it sees the scores that followed warp 1's; in units of one
+            // tile the only user makes both.
+            auto release = [&](uint64_t* bar, bool two) {
+                if (!two || s == 1) tc::commit(bar, one);
+                if (!two) tc::commit(bar, one);
+            };
+            // In units of two tiles the warps take turns with the tensor core: P V and the next Q K^T of one tile, then of the
+            // other.  Left alone the two fall into step: both warpgroups in softmax, then both tiles' products, each idle
+            // during the other.
+            auto take_turn = [&]() { return (bool)__all_sync(kFull, tc::wait_count(&ctl->batches[s ^ 1], batch - (s ^ 1), limit, abort)); };
+            auto pass_turn = [&]() {
+                ++batch;
+                if (one) tc::store_release(&ctl->batches[s], batch);
+            };
+            auto scores = [&](uint64_t a, uint32_t k_slot) {  // S = Q K^T
+                const uint64_t b = k_desc + k_slot * kTileStep;
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint64_t o = (uint64_t)(((k / 4) * (kKTile * 128) + (k % 4) * 32) >> 4);
-                        tc::mma_ss(s_t, a + o, b + o, kIdescS, k > 0);
-                    }
-                };
-                // what O += P V needs besides P: V's fill, with the slots past the length zeroed (they hold anything, and 0 * v
-                // has to stay 0), and before a piece's first product the accumulator read
-                auto ready = [&](uint32_t v_pos, uint32_t v_slot, uint32_t v_phase, int have, bool first, bool two) {
-                    if (!wait_fill(v_pos, v_slot, v_phase, two)) return false;
-                    if ((have & 15) != 0 && have < kKTile) {  // the rows that the last 16 of V take in
-                        if (!two || s == 0) {
-                            unsigned char* v = ring + v_slot * C::kTileBytes;
-                            for (int r = have; r < ((have + 15) & ~15); ++r)
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint64_t o = (uint64_t)(((k / 4) * (kKTile * 128) + (k % 4) * 32) >> 4);
+                    tc::mma_ss(s_t, a + o, b + o, kIdescS, k > 0, one);
+                }
+            };
+            // what O += P V needs besides P: V's fill, with the slots past the length zeroed (they hold anything, and 0 * v
+            // has to stay 0), and before a piece's first product the accumulator read
+            auto ready = [&](uint32_t v_pos, uint32_t v_slot, uint32_t v_phase, int have, bool first, bool two) {
+                if (!wait_fill(v_pos, v_slot, v_phase, two)) return false;
+                if ((have & 15) != 0 && have < kKTile) {  // the rows that the last 16 of V take in
+                    if (!two || s == 0) {
+                        unsigned char* v = ring + v_slot * C::kTileBytes;
+                        for (int r = have + (lane >> 3); r < ((have + 15) & ~15); r += 4)
 #pragma unroll
-                                for (int h = 0; h < D / 8; ++h)
-                                    *reinterpret_cast<uint4*>(v + (h >> 3) * (kKTile * 128) + r * 128 + (h & 7) * 16) = make_uint4(0, 0, 0, 0);
-                            tc::fence_async_shared();
-                            if (two) tc::mbar_arrive(&ctl->clean);
-                        } else {
-                            if (!wait(&ctl->clean, clean_phase)) return false;
-                            clean_phase ^= 1u;
-                        }
-                    }
-                    if (first) {
-                        if (!wait(o_free, o_phase)) return false;
-                        o_phase ^= 1u;
-                    }
-                    return true;
-                };
-                auto values = [&](uint64_t b, int have, bool first) {  // O += P V
-                    if (have > kKTile - 16) {
-#pragma unroll
-                        for (int k = 0; k < kKTile / 16; ++k) tc::mma_ts(o_t, s_t + k * 8, b + (uint64_t)(k * 2048 >> 4), kIdescO, k > 0 || !first);
+                            for (int h = 0; h < D / 64; ++h)
+                                *reinterpret_cast<uint4*>(v + h * (kKTile * 128) + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        tc::fence_async_shared();
+                        __syncwarp();
+                        if (two && one) tc::mbar_arrive(&ctl->clean);
                     } else {
-                        for (int k = 0; k < (have + 15) >> 4; ++k) tc::mma_ts(o_t, s_t + k * 8, b + (uint64_t)(k * 2048 >> 4), kIdescO, k > 0 || !first);
+                        if (!wait(&ctl->clean, clean_phase)) return false;
+                        clean_phase ^= 1u;
                     }
-                };
-                while (ok) {
-                    const uint32_t pi = n_piece % kPieces;
-                    ok = wait(&ctl->piece_full[pi], n_piece / kPieces & 1u);
-                    if (!ok) break;
-                    x = ctl->piece[pi];
-                    tc::mbar_arrive(&ctl->piece_empty[pi]);
-                    ++n_piece;
-                    if (x.rows == 0) break;
-                    const bool two = x.rows > p.rows_per_tile;
-                    // Both threads see every fill of every query buffer and both free it, used or not: neither gets a phase ahead.
-                    const uint32_t q = q_pos + (two ? s : 0);
-                    ok = wait(&ctl->q_full[q_pos & 1u], q_pos >> 1 & 1u) && (!two || wait(&ctl->q_full[(q_pos + 1) & 1u], (q_pos + 1) >> 1 & 1u));
-                    const uint64_t a = q_desc + (q & 1u) * kTileStep;
-                    int left = x.left;
-                    if (two || turn == s || x.tiles > 1) {
-                        // this thread's tiles: all of them, or every other one
-                        const int step = two ? 1 : 2, skip = two || turn == s ? 0 : 1;
-                        if (skip) advance(), advance(), left -= kKTile;
-                        uint32_t k_slot = slot;
-                        ok = wait_fill(pos, slot, phase, two) && (!two || take_turn());
-                        if (ok) {
-                            tc::fence_after();
-                            scores(a, k_slot);
-                            if (two) pass_turn();
-                            tc::commit(s_full);
-                            release(&ctl->empty[k_slot], two);
-                        }
-                        for (int i = skip; ok && i < x.tiles; i += step, left -= step * kKTile) {
-                            advance();
-                            const uint32_t v_pos = pos, v_slot = slot, v_phase = phase;
-                            advance();
-                            const bool last = i + step >= x.tiles;
-                            if (!two && i + 1 < x.tiles) advance(), advance();
-                            k_slot = slot;
-                            ok = ready(v_pos, v_slot, v_phase, left, i == skip, two);
-                            ok = ok && (!two || last || wait_fill(pos, slot, phase, two));
-                            ok = ok && wait(p_ready, p_phase);
-                            p_phase ^= 1u;
-                            ok = ok && (!two || take_turn());
+                }
+                if (first) {
+                    if (!wait(o_free, o_phase)) return false;
+                    o_phase ^= 1u;
+                }
+                return true;
+            };
+            auto values = [&](uint32_t v_slot, int have, bool first) {  // O += P V
+                const uint64_t b = v_desc + v_slot * kTileStep;
+                if (have > kKTile - 16) {
+#pragma unroll
+                    for (int k = 0; k < kKTile / 16; ++k) tc::mma_ts(o_t, s_t + k * 8, b + (uint64_t)(k * 2048 >> 4), kIdescO, k > 0 || !first, one);
+                } else {
+#pragma unroll 1
+                    for (int k = 0; k < (have + 15) >> 4; ++k) tc::mma_ts(o_t, s_t + k * 8, b + (uint64_t)(k * 2048 >> 4), kIdescO, k > 0 || !first, one);
+                }
+            };
+            while (ok && next_piece()) {
+                const int tiles = __shfl_sync(kFull, x.tiles, 0);
+                const bool two = __shfl_sync(kFull, x.rows, 0) > p.rows_per_tile;
+                // Both warps see every fill of every query buffer and both free it, used or not: neither gets a phase ahead.
+                const uint32_t q = q_pos + (two ? s : 0);
+                ok = wait(&ctl->q_full[q_pos & 1u], q_pos >> 1 & 1u) && (!two || wait(&ctl->q_full[(q_pos + 1) & 1u], (q_pos + 1) >> 1 & 1u));
+                const uint64_t a = q_desc + (q & 1u) * kTileStep;
+                int left = __shfl_sync(kFull, x.left, 0);
+                if (two || turn == s || tiles > 1) {
+                    // this warp's tiles: all of them, or every other one
+                    const int step = two ? 1 : 2, skip = two || turn == s ? 0 : 1;
+                    if (skip) advance(), advance(), left -= kKTile;
+                    uint32_t k_slot = slot;
+                    ok = ok && wait_fill(pos, slot, phase, two) && (!two || take_turn());
+                    if (ok) {
+                        tc::fence_after();
+                        scores(a, k_slot);
+                        if (two) pass_turn();
+                        tc::commit(s_full, one);
+                        release(&ctl->empty[k_slot], two);
+                    }
+                    for (int i = skip; ok && i < tiles; i += step, left -= step * kKTile) {
+                        advance();
+                        const uint32_t v_pos = pos, v_slot = slot, v_phase = phase;
+                        advance();
+                        const bool last = i + step >= tiles;
+                        if (!two && i + 1 < tiles) advance(), advance();
+                        k_slot = slot;
+                        ok = ready(v_pos, v_slot, v_phase, left, i == skip, two) && (!two || last || wait_fill(pos, slot, phase, two)) &&
+                             wait(p_ready, p_phase) && (!two || take_turn());
+                        p_phase ^= 1u;
+                        if (!ok) break;
+                        tc::fence_after();
+                        values(v_slot, left, i == skip);
+                        if (two) {
+                            // P V and the next Q K^T without a pause
+                            if (!last) scores(a, k_slot);
+                            pass_turn();
+                            tc::commit(last ? pv_done : s_full, one);
+                            release(&ctl->empty[v_slot], two);
+                            if (!last) release(&ctl->empty[k_slot], two);
+                        } else {
+                            if (last) tc::commit(pv_done, one);
+                            release(&ctl->empty[v_slot], two);
+                            if (last) break;
+                            ok = wait_fill(pos, slot, phase, two);
                             if (!ok) break;
                             tc::fence_after();
-                            values(v_desc + v_slot * kTileStep, left, i == skip);
-                            if (two) {
-                                // P V and the next Q K^T without a pause
-                                if (!last) scores(a, k_slot);
-                                pass_turn();
-                                tc::commit(last ? pv_done : s_full);
-                                release(&ctl->empty[v_slot], two);
-                                if (!last) release(&ctl->empty[k_slot], two);
-                            } else {
-                                if (last) tc::commit(pv_done);
-                                release(&ctl->empty[v_slot], two);
-                                if (last) break;
-                                ok = wait_fill(pos, slot, phase, two);
-                                if (!ok) break;
-                                tc::fence_after();
-                                scores(a, k_slot);
-                                tc::commit(s_full);
-                                release(&ctl->empty[k_slot], two);
-                            }
+                            scores(a, k_slot);
+                            tc::commit(s_full, one);
+                            release(&ctl->empty[k_slot], two);
                         }
-                    } else {
-                        advance(), advance();
                     }
-                    if (!two) turn ^= x.tiles & 1;
-                    if (ok) {
-                        tc::commit(&ctl->q_free[q & 1u]);
-                        if (two) tc::mbar_arrive(&ctl->q_free[(q + 1) & 1u]);
-                    }
-                    q_pos += two ? 2 : 1;
+                } else {
+                    advance(), advance();
                 }
-                int none = 0;  // no product outlives the block
-                tc::commit(&ctl->drain);
-                tc::mbar_wait(&ctl->drain, 0, limit, &none);
+                if (!two) turn ^= tiles & 1;
+                if (ok) {
+                    tc::commit(&ctl->q_free[q & 1u], one);
+                    if (two && one) tc::mbar_arrive(&ctl->q_free[(q + 1) & 1u]);
+                }
+                q_pos += two ? 2 : 1;
             }
+            int none = 0;  // no product outlives the block
+            tc::commit(&ctl->drain, one);
+            tc::mbar_wait(&ctl->drain, 0, limit, &none);
             __syncwarp();
         } else {
             // ---- query tiles into shared memory, ahead of the products
@@ -797,14 +889,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int valid = rows * p.share;
                     constexpr int kChunks = D / 8;
                     const T* src = reinterpret_cast<const T*>(p.q) + (long long)(x.row + j * p.rows_per_tile) * p.q_stride + (long long)x.kvh * p.share * D;
-                    // straight into shared memory, all in flight; rows past the last are zeros
+                    // straight into shared memory, all in flight; rows past the last hold anything and reach nothing
                     const uint32_t at0 = tc::smem_addr(smem + b * C::kTileBytes);
-                    for (int i = lane; i < kQTile * kChunks; i += 32) {
+                    for (int i = lane; i < valid * kChunks; i += 32) {
                         const int row = i / kChunks, ch = i % kChunks;
-                        const int per = row < valid ? (row * p.share_inv) >> 16 : 0, head = row < valid ? row - per * p.share : 0;
+                        const int per = (row * p.share_inv) >> 16, head = row - per * p.share;
                         const T* from = src + per * p.q_stride + head * D + ch * 8;
                         const uint32_t at = at0 + (ch >> 3) * (kQTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
-                        tc::copy16(at, from, row < valid ? 16 : 0);
+                        tc::copy16(at, from);
                     }
                     tc::copies_done();
                     tc::fence_async_shared();
@@ -822,16 +914,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// D / 32 consecutive lanes of a head, as stored.
+template <int D>
+struct Words {
+    using W = uint2;
+    static __device__ __forceinline__ W zero() { return make_uint2(0u, 0u); }
+};
+template <>
+struct Words<64> {
+    using W = uint32_t;
+    static __device__ __forceinline__ W zero() { return 0u; }
+};
+
+template <int D>
+__device__ __forceinline__ typename Words<D>::W load_words(const void* base, long long elem) {
+    return *reinterpret_cast<const typename Words<D>::W*>(reinterpret_cast<const unsigned short*>(base) + elem);
+}
+
 template <bool kBf16, int D>
-__device__ __forceinline__ void load_lane(const void* base, long long elem, float (&x)[D / 32]) {
+__device__ __forceinline__ void widen(const typename Words<D>::W& w, float (&x)[D / 32]) {
     using H = Half<kBf16>;
-    const typename H::T* s = reinterpret_cast<const typename H::T*>(base) + elem;
     if constexpr (D == 128) {
-        const uint2 w = *reinterpret_cast<const uint2*>(s);
         const float2 a = H::unpack(w.x), b = H::unpack(w.y);
         x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
     } else {
-        const float2 a = H::unpack(*reinterpret_cast<const uint32_t*>(s));
+        const float2 a = H::unpack(w);
         x[0] = a.x, x[1] = a.y;
     }
 }
@@ -866,164 +973,207 @@ __device__ __forceinline__ void load_part(const float* parts, long long base, in
     }
 }
 
-constexpr int kBatch = 2;      // parts or tokens in flight per warp and head
-constexpr int kJoinHeads = 4;  // query heads of one key-value head per warp: its keys and values are loaded once for them
+constexpr int kBatchTokens = 4; // own tokens in flight per warp
 
-// Joins the parts of one segment for the unit rows of query heads `head` ..
-// head + n - 1 of the segment's row `rel`; warp `sub` of `warps` takes every
-// warps-th part.
-template <int D>
-__device__ __forceinline__ void join_parts(const AttendParams& p, Acc<D> (&a)[kJoinHeads], int n, int seg, int rel, int head, int lane,
-                                           int sub, int warps, const Runs& runs) {
+// Where the parts of a row's heads lie, for one segment.
+struct Parts {
+    int seg, unit, tile, row, cap, sets;  // sets: parts per piece
+    int tiles, cost, left;                // of the unit; units of the segment before it that are not dealt out (-1: it is)
+    long long span;
+    int count;
+    long long slot;
+};
+
+// What the call's inputs alone say, for the unit rows of query heads `head` ..
+// of the segment's row `rel`.
+__device__ __forceinline__ Parts locate(const AttendParams& p, int seg, int rel, int head) {
+    Parts x;
     const Seg s = load_seg(p, seg);
-    if (s.tiles == 0) return;
-    const bool prefix = seg < p.P;
-    const int rt = p.rows_per_tile, u = rel / (2 * rt), left = s.n - u * 2 * rt;
-    const bool two = left > rt;
-    const int in = rel - u * 2 * rt, kvh = head / p.share, tile = two && in >= rt ? 1 : 0;
-    const int sets = two ? 1 : 2;  // a unit of one tile: a part of each warpgroup
-    const int row = (in - tile * rt) * p.share + head - kvh * p.share;
-    const int unit = kvh * s.units + u;
-    const int2 slots = p.sc.seg_units[seg];
-    long long slot;  // of the unit's first piece
+    x.seg = seg;
+    x.tiles = s.tiles;
+    x.span = s.span();
+    x.cost = s.cost;
+    const int rt = p.rows_per_tile, u = rel / (2 * rt), in = rel - u * 2 * rt, kvh = head / p.share;
+    const bool two = s.n - u * 2 * rt > rt;
+    x.tile = two && in >= rt ? 1 : 0;
+    x.sets = two ? 1 : 2;  // a unit of one tile: a part of each warpgroup
+    x.row = (in - x.tile * rt) * p.share + head - kvh * p.share;
+    x.unit = kvh * s.units + u;
+    x.left = x.unit < s.dealt ? -1 : x.unit - s.dealt;
+    x.cap = seg < p.P ? kQTile : p.sc.group_rows;
+    x.count = 0;
+    x.slot = 0;
+    return x;
+}
+
+// The rest, from the offsets that the attention kernel left.
+__device__ __forceinline__ void place(const AttendParams& p, Parts& x, const Runs& runs, unsigned long long tiles, int2 slots) {
     int pieces = 1;
-    if (unit < s.dealt) {
-        slot = (long long)slots.y + unit;
+    if (x.left < 0) {
+        x.slot = (long long)slots.y + x.unit;
     } else {
         // the blocks whose runs hold the unit's first and last tile
-        const unsigned long long begin = p.sc.seg_tiles[seg] + (unsigned long long)(unit - s.dealt) * s.span() + kUnitCost;
+        const unsigned long long begin = tiles + (unsigned long long)(x.left * x.span + kUnitCost);
         const int c0 = runs.block_of(begin);
-        pieces = runs.block_of(begin + s.tiles - 1) - c0 + 1;
-        slot = (long long)slots.x + (unit - s.dealt) + c0;
+        pieces = runs.block_of(begin + (unsigned long long)(x.tiles - 1) * x.cost) - c0 + 1;
+        x.slot = (long long)slots.x + x.left + c0;
     }
-    const int count = pieces * sets, cap = prefix ? kQTile : p.sc.group_rows;
-    for (int k0 = sub; k0 < count; k0 += warps * kBatch) {
-        float2 ml[kBatch][kJoinHeads];
-        float v[kBatch][kJoinHeads][D / 32];
+    x.count = pieces * x.sets;
+}
+
+// Joins the parts of n heads; warp `sub` of `warps` takes every warps-th part.
+template <int D, int kHeads, int kBatchParts>  // parts in flight per warp and head
+__device__ __forceinline__ void join_parts(const AttendParams& p, Acc<D> (&a)[kHeads], int n, const Parts& x, int lane, int sub, int warps) {
+    for (int k0 = sub; k0 < x.count; k0 += warps * kBatchParts) {
+        float2 ml[kBatchParts][kHeads];
+        float v[kBatchParts][kHeads][D / 32];
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
+        for (int b = 0; b < kBatchParts; ++b) {
             const int k = k0 + b * warps;
-            const long long base = k < count ? part_row(p, prefix, slot + (two ? k : k >> 1), two ? tile : k & 1) : -1;
+            const long long base =
+                k < x.count ? part_row(p, x.seg < p.P, x.slot + (x.sets == 1 ? k : k >> 1), x.sets == 1 ? x.tile : k & 1) : -1;
 #pragma unroll
-            for (int h = 0; h < kJoinHeads; ++h) {
+            for (int h = 0; h < kHeads; ++h) {
                 ml[b][h] = make_float2(kNegInf, 0.0f);
 #pragma unroll
                 for (int e = 0; e < D / 32; ++e) v[b][h][e] = 0.0f;
                 if (base >= 0 && h < n) {
-                    ml[b][h] = p.sc.part_ml[base + row + h];
-                    load_part<D>(p.sc.part_o, base, cap, row + h, lane, v[b][h]);
+                    ml[b][h] = p.sc.part_ml[base + x.row + h];
+                    load_part<D>(p.sc.part_o, base, x.cap, x.row + h, lane, v[b][h]);
                 }
             }
         }
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b)
+        for (int b = 0; b < kBatchParts; ++b)
 #pragma unroll
-            for (int h = 0; h < kJoinHeads; ++h)
+            for (int h = 0; h < kHeads; ++h)
                 if (ml[b][h].x != kNegInf || ml[b][h].y != 0.0f) a[h].add(ml[b][h].x, ml[b][h].y, v[b][h]);  // else nothing was written
     }
 }
 
-// kSub warps per row and kJoinHeads query heads: the round's own tokens that
+// kSub warps per row and kHeads query heads of one key-value head (its keys and
+// values are loaded once for them): the round's own tokens that
 // the row sees, then the parts of the row's prefix and of its group's committed
 // tokens.
-template <bool kBf16, int D, int kSub>
-__global__ void __launch_bounds__(kJoinThreads) lp_attend_join_kernel(const AttendParams p) {
+template <bool kBf16, int D, int kSub, int kHeads>
+__global__ void __launch_bounds__(kJoinThreads, kHeads == 1 ? 4 : 2) lp_attend_join_kernel(const AttendParams p) {
+    constexpr int kBatchParts = kHeads == 1 ? 4 : 2;
     using H = Half<kBf16>;
     using T = typename H::T;
     constexpr int kE = D / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % kSub;
-    const int chunks = (p.share + kJoinHeads - 1) / kJoinHeads;
+    const int chunks = (p.share + kHeads - 1) / kHeads;
     const int row = blockIdx.x, chunk = blockIdx.y * (kJoinWarps / kSub) + warp / kSub;
-    const int kvh = chunk / chunks, first = (chunk - kvh * chunks) * kJoinHeads, head = kvh * p.share + first;
-    const int n = p.share - first < kJoinHeads ? p.share - first : kJoinHeads;  // this warp's heads
+    const int kvh = chunk / chunks, first = (chunk - kvh * chunks) * kHeads, head = kvh * p.share + first;
+    const int n = p.share - first < kHeads ? p.share - first : kHeads;  // this warp's heads
     const int g = block_find_group(p.indptr, p.G, row);
     bool mine = g >= 0 && g < p.G && kvh < p.kv_heads;
     mine = mine && row >= __ldg(&p.indptr[g]) && row < __ldg(&p.indptr[g + 1]);  // else two entries claim the row
-    Acc<D> a[kJoinHeads];
+    Acc<D> a[kHeads];
 #pragma unroll
-    for (int h = 0; h < kJoinHeads; ++h) a[h].clear();
+    for (int h = 0; h < kHeads; ++h) a[h].clear();
     Group grp = {0, 0, 0, false};
     if (mine) grp = load_group(p, g);
+    Parts own, pre;
+    own.tiles = pre.tiles = 0;
     if (grp.n > 0) {
-        float q[kJoinHeads][kE];
-#pragma unroll
-        for (int h = 0; h < kJoinHeads; ++h) {
-#pragma unroll
-            for (int e = 0; e < kE; ++e) q[h][e] = 0.0f;
-            if (h < n) load_lane<kBf16, D>(p.q, row * p.q_stride + (long long)(head + h) * D + lane * kE, q[h]);
-        }
-        const float c = p.scale * kLog2e;
-        const int* table = p.tables + (long long)g * p.max_pages;
-        const int j = row - grp.r0;
-        const unsigned mask = p.row_masks != nullptr ? __ldg(&p.row_masks[row]) : (2u << j) - 1u;
-        for (int i0 = sub; i0 < grp.n; i0 += kSub * kBatch) {
-            float k[kBatch][kE], v[kBatch][kE], s[kBatch][kJoinHeads];
-            bool sees[kBatch];
-#pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-                const int i = i0 + b * kSub;
-                sees[b] = i < grp.n && (mask >> i & 1u);
-#pragma unroll
-                for (int e = 0; e < kE; ++e) k[b][e] = v[b][e] = 0.0f;
-                if (sees[b]) {
-                    const int t = grp.len + i;
-                    const int page = __ldg(&table[t >> p.page_shift]);
-                    if (page >= 0 && page < p.num_pages) {
-                        const long long at =
-                            (((((long long)page * p.kv_heads + kvh) << p.page_shift) + (t & ((1 << p.page_shift) - 1))) * D) + lane * kE;
-                        load_lane<kBf16, D>(p.k_cache, at, k[b]);
-                        load_lane<kBf16, D>(p.v_cache, at, v[b]);
-                    } else if (lane == 0) {
-                        atomicOr(p.status, kStatusBadPage);
-                    }
-                }
-            }
-#pragma unroll
-            for (int b = 0; b < kBatch; ++b)
-#pragma unroll
-                for (int h = 0; h < kJoinHeads; ++h) {
-                    s[b][h] = 0.0f;
-#pragma unroll
-                    for (int e = 0; e < kE; ++e) s[b][h] = fmaf(q[h][e], k[b][e], s[b][h]);
-                }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-                for (int b = 0; b < kBatch; ++b)
-#pragma unroll
-                    for (int h = 0; h < kJoinHeads; ++h) s[b][h] += __shfl_xor_sync(kFull, s[b][h], o);
-#pragma unroll
-            for (int b = 0; b < kBatch; ++b)
-#pragma unroll
-                for (int h = 0; h < kJoinHeads; ++h)
-                    if (sees[b] && h < n) a[h].add(s[b][h] * c, 1.0f, v[b]);
-        }
-    }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (grp.n > 0) {
-        const Runs runs = make_runs(p.sc.seg_tiles[p.P + p.G], p.grid);
+        own = locate(p, p.P + g, row - grp.r0, head);
         for (int i = 0; i < p.P; ++i) {
             const Prefix x = load_prefix(p, i);
             if (x.bad || g < x.g0 || g >= x.g1) continue;
-            join_parts<D>(p, a, n, i, row - x.r0, head, lane, sub, kSub, runs);
+            pre = locate(p, i, row - x.r0, head);
             break;
         }
-        join_parts<D>(p, a, n, p.P + g, row - grp.r0, head, lane, sub, kSub, runs);
+        // the round's own tokens, four at a time: a lane's four (two) lanes of the head from each
+        typename Words<D>::W qw[kHeads];
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h) qw[h] = load_words<D>(p.q, row * p.q_stride + (long long)(head + (h < n ? h : 0)) * D + lane * kE);
+        const float c = p.scale * kLog2e;
+        const int j = row - grp.r0;
+        const unsigned mask = p.row_masks != nullptr ? __ldg(&p.row_masks[row]) : (2u << j) - 1u;
+        int page = 0;  // lane i: of token i
+        if (lane < grp.n) page = __ldg(&p.tables[(long long)g * p.max_pages + ((grp.len + lane) >> p.page_shift)]);
+        unsigned todo = mask & (grp.n < 32 ? (1u << grp.n) - 1u : kFull);
+        const unsigned here = __ballot_sync(kFull, page >= 0 && page < p.num_pages);
+        if (lane == 0 && (todo & ~here) != 0u) atomicOr(p.status, kStatusBadPage);
+        for (int skip = 0; todo != 0u;) {
+            typename Words<D>::W kw[kBatchTokens], vw[kBatchTokens];
+            bool sees[kBatchTokens];
+#pragma unroll
+            for (int b = 0; b < kBatchTokens; ++b) {
+                // the next seen token whose turn is this warp's
+                int i = __ffs(todo) - 1;
+                while (kSub > 1 && i >= 0 && skip++ % kSub != sub) todo &= todo - 1u, i = __ffs(todo) - 1;
+                sees[b] = i >= 0;
+                if (sees[b]) todo &= todo - 1u;
+                const int t = grp.len + (sees[b] ? i : 0), pg = __shfl_sync(kFull, page, sees[b] ? i : 0);
+                kw[b] = vw[b] = Words<D>::zero();
+                if (sees[b] && (here >> i & 1u)) {
+                    const long long at =
+                        (((((long long)pg * p.kv_heads + kvh) << p.page_shift) + (t & ((1 << p.page_shift) - 1))) * D) + lane * kE;
+                    kw[b] = load_words<D>(p.k_cache, at);
+                    vw[b] = load_words<D>(p.v_cache, at);
+                }
+            }
+            float s[kBatchTokens][kHeads];
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h) {
+                float q[kE];
+                widen<kBf16, D>(qw[h], q);
+#pragma unroll
+                for (int b = 0; b < kBatchTokens; ++b) {
+                    float k[kE];
+                    widen<kBf16, D>(kw[b], k);
+                    s[b][h] = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) s[b][h] = fmaf(q[e], k[e], s[b][h]);
+                }
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+                for (int b = 0; b < kBatchTokens; ++b)
+#pragma unroll
+                    for (int h = 0; h < kHeads; ++h) s[b][h] += __shfl_xor_sync(kFull, s[b][h], o);
+#pragma unroll
+            for (int b = 0; b < kBatchTokens; ++b) {
+                float v[kE];
+                widen<kBf16, D>(vw[b], v);
+#pragma unroll
+                for (int h = 0; h < kHeads; ++h)
+                    if (sees[b]) a[h].add(s[b][h] * c, 1.0f, v);
+            }
+        }
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (own.tiles > 0 || pre.tiles > 0) {
+        const unsigned long long pre_total = p.sc.seg_tiles[p.P + p.G], own_total = p.sc.seg_tiles[p.P + p.G + 1];
+        const unsigned long long own_tiles = own.tiles > 0 ? p.sc.seg_tiles[own.seg] : 0, pre_tiles = pre.tiles > 0 ? p.sc.seg_tiles[pre.seg] : 0;
+        const int2 own_slots = own.tiles > 0 ? p.sc.seg_units[own.seg] : make_int2(0, 0);
+        const int2 pre_slots = pre.tiles > 0 ? p.sc.seg_units[pre.seg] : make_int2(0, 0);
+        if (own.tiles > 0) {
+            place(p, own, make_runs(own_total, p.grid, 1), own_tiles, own_slots);
+            join_parts<D, kHeads, kBatchParts>(p, a, n, own, lane, sub, kSub);
+        }
+        if (pre.tiles > 0) {
+            place(p, pre, make_runs(pre_total, p.grid, 0), pre_tiles, pre_slots);
+            join_parts<D, kHeads, kBatchParts>(p, a, n, pre, lane, sub, kSub);
+        }
     }
     if constexpr (kSub > 1) {  // the warps' sums, in the order of the warps
-        __shared__ float4 part[kJoinWarps][kJoinHeads][32];
-        __shared__ float2 part_ml[kJoinWarps][kJoinHeads];
+        __shared__ float4 part[kJoinWarps][kHeads][32];
+        __shared__ float2 part_ml[kJoinWarps][kHeads];
 #pragma unroll
-        for (int h = 0; h < kJoinHeads; ++h) {
+        for (int h = 0; h < kHeads; ++h) {
             part[warp][h][lane] = make_float4(a[h].o[0], a[h].o[1], kE > 2 ? a[h].o[kE - 2] : 0.0f, kE > 2 ? a[h].o[kE - 1] : 0.0f);
             if (lane == 0) part_ml[warp][h] = make_float2(a[h].m, a[h].l);
         }
         __syncthreads();
         if (sub != 0) return;
-#pragma unroll
+#pragma unroll 1
         for (int w = 1; w < kSub; ++w)
 #pragma unroll
-            for (int h = 0; h < kJoinHeads; ++h) {
+            for (int h = 0; h < kHeads; ++h) {
                 const float4 o = part[warp + w][h][lane];
                 const float2 ml = part_ml[warp + w][h];
                 float v[kE];
@@ -1034,7 +1184,7 @@ __global__ void __launch_bounds__(kJoinThreads) lp_attend_join_kernel(const Atte
     }
     if (!mine) return;
 #pragma unroll
-    for (int h = 0; h < kJoinHeads; ++h) {
+    for (int h = 0; h < kHeads; ++h) {
         if (h >= n) break;
         const float inv = a[h].l > 0.0f ? 1.0f / a[h].l : (a[h].l == 0.0f ? 0.0f : a[h].l);
         T* dst = reinterpret_cast<T*>(p.out) + row * p.out_stride + (long long)(head + h) * D + lane * kE;
@@ -1065,10 +1215,11 @@ cudaError_t launch(const AttendParams& p, const CUtensorMap& k_map, const CUtens
     lp_attend_kernel<kBf16, D><<<p.grid, kThreads, smem_bytes<D>(), stream>>>(p, k_map, v_map);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    // few rows: several warps share a row's parts
-    const int chunks = (p.share + kJoinHeads - 1) / kJoinHeads * p.kv_heads;
-    const long long tasks = (long long)p.rows * chunks;
-    const int sub = tasks <= 4 * p.grid ? 8 : (tasks <= 16 * p.grid ? 2 : 1);
+    // Few rows: a warp per head, several for its parts (a short call waits on one chain of loads after another); many:
+    // four heads per warp, for more loads in flight beside them.
+    const long long heads = (long long)p.rows * p.q_heads;
+    const int sub = heads <= 8 * p.grid ? 8 : (heads <= 16 * p.grid ? 2 : 1), per = sub > 1 ? 1 : 4;
+    const int chunks = (p.share + per - 1) / per * p.kv_heads;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1078,9 +1229,9 @@ cudaError_t launch(const AttendParams& p, const CUtensorMap& k_map, const CUtens
     lc.stream = stream;
     lc.attrs = attr;
     lc.numAttrs = 1;
-    if (sub == 8) return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 8>, p);
-    if (sub == 2) return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 2>, p);
-    return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 1>, p);
+    if (sub == 8) return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 8, 1>, p);
+    if (sub == 2) return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 2, 1>, p);
+    return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 1, 4>, p);
 }
 
 }  // namespace

@@ -82,7 +82,7 @@ Layout layout_of(const lp_attn_desc* d, int grid) {
     const size_t part_rows = 2 * ((size_t)L.prefix_slots * lp::kQTile + (size_t)L.group_slots * (size_t)L.group_rows);
     size_t off = 0;
     L.seg_tiles = off;
-    off = lp::align_up(off + (segs + 1) * 8);
+    off = lp::align_up(off + (segs + 2) * 8);
     L.seg_units = off;
     off = lp::align_up(off + segs * 8);
     L.part_ml = off;

@@ -38,7 +38,8 @@ constexpr int kKTile = 128;    // tokens of one tile
 // a unit is at most two tiles of its query rows for one key-value head; a
 // piece is the run of a unit's token tiles that one block takes.
 struct AttendScratch {
-    unsigned long long* seg_tiles;  // [P + G + 1] tiles before the segment, of units that are not dealt out whole
+    unsigned long long* seg_tiles;  // [P + G + 2] cost of the tiles before the segment, among prefixes or among groups,
+                                    // of units that are not dealt out whole; then both totals
     int2* seg_units;                // [P + G] slots before it, of those units and of those that are
     float* part_o;                  // pieces of prefixes, then of groups: unnormalised results [2][rows][D]
     float2* part_ml;                // (maximum in base 2, sum) [2][rows]
