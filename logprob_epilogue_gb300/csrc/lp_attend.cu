@@ -286,7 +286,7 @@ constexpr int kPieceReaders = 11; // warps that read each: two of the products, 
 struct Ctl {
     uint64_t full[10], empty[10], piece_full[kPieces], piece_empty[kPieces];
     Piece piece[kPieces];
-    uint64_t q_full[2], q_free[2], s_full[2], p_ready[2], pv_done[2], o_free[2], clean, drain;
+    uint64_t q_full[2], q_free[2], s_full[2], p_ready[2], pv_done[2], o_free[2], q_grant, clean, drain;
     unsigned long long sum[kWarps][3];
     int sum_dealt[kWarps], deal_first, deal_last;
     Start start[2];
@@ -441,93 +441,63 @@ __device__ __forceinline__ float max32(const uint32_t (&r)[32], float top) {
     return fmaxf(a, b);
 }
 
-__device__ __forceinline__ void mask32(uint32_t (&r)[32], int valid) {
-    if (valid < 32) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-            if (e >= valid) r[e] = __float_as_uint(kNegInf);
-    }
-}
-
-// 32 scores to 16 words of probabilities, and their sums in pairs.
-template <bool kBf16>
-__device__ __forceinline__ void exp32(const uint32_t (&r)[32], uint32_t (&w)[16], unsigned long long c2, unsigned long long nb2,
-                                      unsigned long long (&sum)[2]) {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        float x, y;
-        unpack2(fma2(pack2(r[2 * e], r[2 * e + 1]), c2, nb2), x, y);
-        x = ex2(x);
-        y = ex2(y);
-        sum[e & 1] = add2(sum[e & 1], pack2(__float_as_uint(x), __float_as_uint(y)));
-        w[e] = Half<kBf16>::pack(x, y);
-    }
-}
-
 // Softmax of one score tile by one warp, a row per thread; `valid` of the 128
-// tokens exist.  Writes the row's probabilities over the scores (as many 16s of
-// them as the products will take in).
-//
-// kWide: every score in registers, all of it unrolled, for units of two tiles,
-// where eight warps run through the same instructions.  Otherwise 32 columns
-// at a time, twice: with few rows one warp has them all, and a long unrolled
-// run of its own is bound by the instruction fetch (3,000 to 4,500 cycles a
-// tile against 1,300).
-template <bool kBf16, int D, bool kWide>
+// tokens exist.  Writes the row's probabilities over the scores.
+template <bool kBf16, int D>
 __device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, int valid, bool first, bool used, float c, Row& row) {
-    unsigned long long sum[2] = {0, 0};
-    const unsigned long long c2 = pack2(__float_as_uint(c), __float_as_uint(c));
+    uint32_t r[4][32];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) tc::tmem_ld32(s_col + b * 32, r[b]);
+    tc::wait_ld();
+#pragma unroll
+    for (int b = 0; b < 4; ++b) tc::tie(r[b]);
+    if (valid < kKTile) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if (b * 32 + e >= valid) r[b][e] = __float_as_uint(kNegInf);
+    }
     float top = kNegInf, f;
-    if constexpr (kWide) {
-        uint32_t r[4][32];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) tc::tmem_ld32(s_col + b * 32, r[b]);
-        tc::wait_ld();
+    for (int b = 0; b < 4; ++b) top = max32(r[b], top);
+    if (raise<kBf16>(row, top, first, used, c, f)) rescale<D>(o_col, f);
+    const unsigned long long c2 = pack2(__float_as_uint(c), __float_as_uint(c));
+    const unsigned long long nb2 = pack2(__float_as_uint(-row.base), __float_as_uint(-row.base));
+    unsigned long long sum[2] = {0, 0};
 #pragma unroll
-        for (int b = 0; b < 4; ++b) tc::tie(r[b]);
-        if (valid < kKTile) {
+    for (int b = 0; b < 4; ++b) {  // 32 scores to 16 words of probabilities
+        uint32_t w[16];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) mask32(r[b], valid - b * 32);
+        for (int e = 0; e < 16; ++e) {
+            float x, y;
+            unpack2(fma2(pack2(r[b][2 * e], r[b][2 * e + 1]), c2, nb2), x, y);
+            x = ex2(x);
+            y = ex2(y);
+            sum[e & 1] = add2(sum[e & 1], pack2(__float_as_uint(x), __float_as_uint(y)));
+            w[e] = Half<kBf16>::pack(x, y);
         }
-#pragma unroll
-        for (int b = 0; b < 4; ++b) top = max32(r[b], top);
-        if (raise<kBf16>(row, top, first, used, c, f)) rescale<D>(o_col, f);
-        const unsigned long long nb2 = pack2(__float_as_uint(-row.base), __float_as_uint(-row.base));
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            uint32_t w[16];
-            exp32<kBf16>(r[b], w, c2, nb2, sum);
-            tc::tmem_st16(s_col + b * 16, w);
-        }
-    } else {
-        const int chunks = valid < kKTile ? (valid + 31) >> 5 : 4;
-#pragma unroll 1
-        for (int b = 0; b < chunks; ++b) {
-            uint32_t r[32];
-            tc::tmem_ld32(s_col + b * 32, r);
-            tc::wait_ld();
-            tc::tie(r);
-            mask32(r, valid - b * 32);
-            top = max32(r, top);
-        }
-        if (raise<kBf16>(row, top, first, used, c, f)) rescale<D>(o_col, f);
-        const unsigned long long nb2 = pack2(__float_as_uint(-row.base), __float_as_uint(-row.base));
-        // a chunk's probabilities take the columns of scores that have been read
-#pragma unroll 1
-        for (int b = 0; b < chunks; ++b) {
-            uint32_t r[32], w[16];
-            tc::tmem_ld32(s_col + b * 32, r);
-            tc::wait_ld();
-            tc::tie(r);
-            mask32(r, valid - b * 32);
-            exp32<kBf16>(r, w, c2, nb2, sum);
-            tc::tmem_st16(s_col + b * 16, w);
-        }
+        tc::tmem_st16(s_col + b * 16, w);
     }
     float x, y;
     unpack2(add2(sum[0], sum[1]), x, y);
     row.l += x + y;
     tc::wait_st();
+}
+
+// The rows' heads into a query tile (128-byte swizzle) by `n` threads, visible
+// to the tensor core.  Tile rows past the last hold anything and reach nothing.
+template <typename T, int D>
+__device__ __forceinline__ void load_queries(const AttendParams& p, int row0, int rows, int kvh, uint32_t dst, int t, int n) {
+    constexpr int kChunks = D / 8;
+    const T* src = reinterpret_cast<const T*>(p.q) + (long long)row0 * p.q_stride + (long long)kvh * p.share * D;
+    for (int i = t; i < rows * p.share * kChunks; i += n) {
+        const int row = i / kChunks, ch = i % kChunks;
+        const int per = (row * p.share_inv) >> 16, head = row - per * p.share;
+        tc::copy16(dst + (ch >> 3) * (kQTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4), src + per * p.q_stride + head * D + ch * 8);
+    }
+    tc::copies_done();
+    tc::fence_async_shared();
 }
 
 template <bool kBf16, int D>
@@ -549,10 +519,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < C::kSlots; ++i) tc::mbar_init(&ctl->full[i], 1), tc::mbar_init(&ctl->empty[i], 2);
         tc::mbar_init(&ctl->clean, 1);
+        tc::mbar_init(&ctl->q_grant, 1);
         tc::mbar_init(&ctl->drain, 2);
         for (int i = 0; i < kPieces; ++i) tc::mbar_init(&ctl->piece_full[i], 1), tc::mbar_init(&ctl->piece_empty[i], kPieceReaders);
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&ctl->q_full[i], 1);
+            tc::mbar_init(&ctl->q_full[i], 4);
             tc::mbar_init(&ctl->q_free[i], 2);
             tc::mbar_init(&ctl->s_full[i], 1);
             tc::mbar_init(&ctl->p_ready[i], 4);
@@ -597,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)quarter << 21;
         const uint32_t s_col = tmem + lanes + kColS + wg * kColStep, o_col = tmem + lanes + kColO + wg * kColStep;
         const float c = p.scale * kLog2e;
-        uint32_t s_phase = 0, pv_phase = 0, tile = 0;  // tile: tiles of the run before the piece
+        uint32_t s_phase = 0, pv_phase = 0, q_pos = 0, grant = 0, tile = 0;  // tile: tiles of the run before the piece
         int turn = 0;
         while (ok && next_piece()) {
             const bool two = x.rows > p.rows_per_tile;
@@ -606,6 +577,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool live = quarter * 32 < valid_rows;  // any row of this warp
             const int first = two ? 0 : wg ^ turn, stride = two ? 1 : 2;
             if (!two) turn ^= n & 1;
+            if (two) {
+                ok = tc::warp_wait(&ctl->q_grant, grant, limit, abort);  // both buffers are free
+                if (!ok) break;
+                grant ^= 1u;
+                const uint32_t b = (q_pos + wg) & 1u;
+                load_queries<T, D>(p, x.row + wg * rt, wg == 0 ? rt : x.rows - rt, x.kvh, tc::smem_addr(smem + b * C::kTileBytes), tid & 127, 128);
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&ctl->q_full[b], 1);
+            }
+            q_pos += two ? 2 : 1;
             Row st = {kNegInf, 0.0f, 0.0f};
             for (int i = first; i < n; i += stride) {
                 ok = tc::warp_wait(&ctl->s_full[wg], s_phase, limit, abort);
@@ -617,8 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (live) {
                     tc::fence_after();
-                    if (two) softmax_tile<kBf16, D, true>(s_col, o_col, x.left - i * kKTile, i == first, row < valid_rows, c, st);
-                    else softmax_tile<kBf16, D, false>(s_col, o_col, x.left - i * kKTile, i == first, row < valid_rows, c, st);
+                    softmax_tile<kBf16, D>(s_col, o_col, x.left - i * kKTile, i == first, row < valid_rows, c, st);
                     tc::fence_before();
                     __syncwarp();
                 }
@@ -877,32 +857,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mbar_wait(&ctl->drain, 0, limit, &none);
             __syncwarp();
         } else {
-            // ---- query tiles into shared memory, ahead of the products
+            // ---- the queries of one-tile units, ahead of the products
             uint32_t q_pos = 0;
             while (ok && next_piece()) {
+                // this warp sees every buffer come free, in order; the softmax warpgroups load the tiles of two-tile units themselves
                 const bool two = x.rows > p.rows_per_tile;
-                for (int j = 0; ok && j <= (two ? 1 : 0); ++j, ++q_pos) {
-                    const uint32_t b = q_pos & 1u;
-                    ok = tc::warp_wait(&ctl->q_free[b], (q_pos >> 1 & 1u) ^ 1u, limit, abort);
-                    if (!ok) break;
-                    const int rows = two ? (j == 0 ? p.rows_per_tile : x.rows - p.rows_per_tile) : x.rows;
-                    const int valid = rows * p.share;
-                    constexpr int kChunks = D / 8;
-                    const T* src = reinterpret_cast<const T*>(p.q) + (long long)(x.row + j * p.rows_per_tile) * p.q_stride + (long long)x.kvh * p.share * D;
-                    // straight into shared memory, all in flight; rows past the last hold anything and reach nothing
-                    const uint32_t at0 = tc::smem_addr(smem + b * C::kTileBytes);
-                    for (int i = lane; i < valid * kChunks; i += 32) {
-                        const int row = i / kChunks, ch = i % kChunks;
-                        const int per = (row * p.share_inv) >> 16, head = row - per * p.share;
-                        const T* from = src + per * p.q_stride + head * D + ch * 8;
-                        const uint32_t at = at0 + (ch >> 3) * (kQTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
-                        tc::copy16(at, from);
-                    }
-                    tc::copies_done();
-                    tc::fence_async_shared();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&ctl->q_full[b]);
+                for (int j = 0; ok && j <= (two ? 1 : 0); ++j)
+                    ok = tc::warp_wait(&ctl->q_free[(q_pos + j) & 1u], ((q_pos + j) >> 1 & 1u) ^ 1u, limit, abort);
+                if (!ok) break;
+                if (two) {
+                    if (lane == 0) tc::mbar_arrive(&ctl->q_grant);
+                    q_pos += 2;
+                    continue;
                 }
+                const uint32_t b = q_pos & 1u;
+                load_queries<T, D>(p, x.row, x.rows, x.kvh, tc::smem_addr(smem + b * C::kTileBytes), lane, 32);
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&ctl->q_full[b], 4);
+                ++q_pos;
             }
         }
     }
