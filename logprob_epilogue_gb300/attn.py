@@ -4,6 +4,7 @@ marshalling only; see ``include/lp_epilogue.h`` for the contract)."""
 from __future__ import annotations
 
 import ctypes
+import struct
 
 from . import LP_BF16, LP_F16, PLAN_DEBUG_FORCE_TIMEOUT, _check, lib
 
@@ -52,6 +53,14 @@ def attn_scratch_bytes(**desc_kw) -> int:
     return int(lib().lp_attn_scratch_bytes(ctypes.byref(make_attn_desc(**desc_kw))))
 
 
+# The io structures as one native pack each: a call sets every field at once (field by field through ctypes takes longer
+# than the kernel of a small call).
+_ROPE = "PPPPqqqqPPPPPffiiii"
+_PACK_ROPE = struct.Struct("@" + _ROPE + "0P")
+_PACK_APPEND = struct.Struct("@" + _ROPE + "PqPPPPPi0P")
+_PACK_ATTEND = struct.Struct("@PqPPPPPPPPPPqPPfiii0P")
+
+
 class AttnPlan:
     """Attention operators of a verify forward on one device: the head norms and
     position rotation (``norm_rope``), the append of a round's keys and values
@@ -62,19 +71,25 @@ class AttnPlan:
     group's committed tokens and is changed by none of the calls: after the
     epilogue, ``lens += accepted + 1`` commits the round.  Every call only
     enqueues on ``stream`` (default: torch's current stream) and ORs its status
-    bits into ``status`` without resetting it."""
+    bits into ``status`` without resetting it.  Like a ``Plan``, one plan serves
+    one stream, and one thread, at a time."""
 
     def __init__(self, **desc_kw):
         import torch
-        self.desc = make_attn_desc(**desc_kw)
-        self.device = int(self.desc.device)
-        self._dtype = torch.bfloat16 if self.desc.dtype == LP_BF16 else torch.float16
+        self.desc = d = make_attn_desc(**desc_kw)
+        self.device = int(d.device)
+        self._dtype = torch.bfloat16 if d.dtype == LP_BF16 else torch.float16
+        self._i32, self._f32 = torch.int32, torch.float32
         self._h = None
         h = ctypes.c_void_p()
-        _check(lib().lp_attn_create(ctypes.byref(h), ctypes.byref(self.desc)), "lp_attn_create")
+        _check(lib().lp_attn_create(ctypes.byref(h), ctypes.byref(d)), "lp_attn_create")
         self._h = h
-        self._i32, self._f32 = torch.int32, torch.float32
-        self._current = torch.cuda.current_stream
+        self._current = torch._C._cuda_getCurrentRawStream
+        self._io = ctypes.create_string_buffer(max(_PACK_ROPE.size, _PACK_APPEND.size, _PACK_ATTEND.size))
+        self._at = ctypes.addressof(self._io)
+        self._q_heads, self._kv_heads, self._dim = int(d.q_heads), int(d.kv_heads), int(d.head_dim)
+        self._cache_shape = (int(d.num_pages), int(d.kv_heads), int(d.page_size), int(d.head_dim))
+        self._norm_rope, self._append, self._attend = lib().lp_norm_rope, lib().lp_kv_append, lib().lp_attend
 
     def close(self) -> None:
         if getattr(self, "_h", None) is not None:
@@ -89,64 +104,67 @@ class AttnPlan:
 
     def _stream(self, stream):
         if stream is None:
-            return self._current(self.device).cuda_stream
+            return self._current(self.device)
         return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
-    def _heads(self, name, x, rows, heads):
+    def _rows(self, name, x, rows, heads):
         """A [rows, heads, head_dim] tensor with dense heads: (pointer, row stride)."""
-        d = self.desc.head_dim
-        if x.dtype != self._dtype or x.device.index != self.device or not x.is_cuda:
+        d = self._dim
+        if x is None:
+            raise ValueError(f"{name}: missing")
+        if x.dtype is not self._dtype or x.get_device() != self.device:
             raise ValueError(f"{name}: expected {self._dtype} on CUDA device {self.device}")
         if x.shape != (rows, heads, d):
             raise ValueError(f"{name}: expected shape [{rows}, {heads}, {d}], got {list(x.shape)}")
-        s = x.stride()
-        if (heads > 1 and s[1] != d) or s[2] != 1:
+        s, t, u = x.stride()
+        if (t != d and heads > 1) or u != 1:
             raise ValueError(f"{name}: the heads of a row must be dense")
-        return x.data_ptr(), s[0] if rows > 1 else heads * d
+        return x.data_ptr(), s if rows > 1 else heads * d
 
-    def _flat(self, name, x, dtype, shape=None, numel=0):
-        """A contiguous tensor of a type and a shape (or a least number of elements); None passes."""
+    def _flat(self, name, x, dtype, numel):
+        """Pointer of a contiguous tensor of a type and at least so many elements; 0 for None."""
         if x is None:
-            return None
-        if x.dtype != dtype or x.device.index != self.device or not x.is_cuda or not x.is_contiguous():
+            return 0
+        if x.dtype is not dtype or x.get_device() != self.device or not x.is_contiguous():
             raise ValueError(f"{name}: expected contiguous {dtype} on CUDA device {self.device}")
-        if shape is not None and x.shape != shape or x.numel() < numel:
-            raise ValueError(f"{name}: expected {list(shape) if shape is not None else f'at least {numel} elements'}, got {list(x.shape)}")
+        if x.numel() < numel:
+            raise ValueError(f"{name}: expected at least {numel} elements, got {list(x.shape)}")
         return x.data_ptr()
 
+    def _shaped(self, name, x, dtype, shape):
+        """Pointer of a contiguous tensor of a type and a shape; 0 for None."""
+        if x is not None and x.shape != shape:
+            raise ValueError(f"{name}: expected shape {list(shape)}, got {list(x.shape)}")
+        return self._flat(name, x, dtype, 0)
+
     def _status(self, x):
-        if x.element_size() != 4 or x.numel() < 1 or not x.is_cuda or x.device.index != self.device:
+        if x.element_size() != 4 or x.numel() < 1 or x.get_device() != self.device:
             raise ValueError(f"status: expected one 32-bit word on CUDA device {self.device}")
         return x.data_ptr()
 
-    def _caches(self, k_cache, v_cache):
-        d = self.desc
-        shape = (d.num_pages, d.kv_heads, d.page_size, d.head_dim)
-        return (self._flat("k_cache", k_cache, self._dtype, shape), self._flat("v_cache", v_cache, self._dtype, shape))
-
     def _rope(self, q, k, q_out, k_out, q_weight, k_weight, eps, weight_offset, cos_sin, interleaved, positions, status):
-        d = self.desc
-        if q is None and k is None:
-            raise ValueError("norm_rope: neither q nor k")
-        rows = int((k if q is None else q).shape[0])
-        io = RopeIO()
+        """The fields of lp_rope_io, in order, and the rows."""
+        qp = qs = qo = qos = kp = ks = ko = kos = 0
         if q is not None:
-            io.q, io.q_stride = self._heads("q", q, rows, d.q_heads)
-            io.q_out, io.q_out_stride = self._heads("q_out", q_out, rows, d.q_heads)
+            rows = q.shape[0]
+            qp, qs = self._rows("q", q, rows, self._q_heads)
+            qo, qos = self._rows("q_out", q_out, rows, self._q_heads)
+        elif k is None:
+            raise ValueError("norm_rope: neither q nor k")
+        else:
+            rows = k.shape[0]
         if k is not None:
-            io.k, io.k_stride = self._heads("k", k, rows, d.kv_heads)
+            kp, ks = self._rows("k", k, rows, self._kv_heads)
             if k_out is not None:
-                io.k_out, io.k_out_stride = self._heads("k_out", k_out, rows, d.kv_heads)
-        io.q_weight = self._flat("q_weight", q_weight, self._dtype, (d.head_dim,))
-        io.k_weight = self._flat("k_weight", k_weight, self._dtype, (d.head_dim,))
+                ko, kos = self._rows("k_out", k_out, rows, self._kv_heads)
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin: expected [positions, rot_dim]")
-        io.cos_sin = self._flat("cos_sin", cos_sin, self._f32)
-        io.max_positions, io.rot_dim = cos_sin.shape
-        io.positions = self._flat("positions", positions, self._i32, None, rows)
-        io.status = self._status(status)
-        io.eps, io.weight_offset, io.interleaved, io.rows = eps, weight_offset, int(bool(interleaved)), rows
-        return io
+        table, rot = cos_sin.shape
+        return rows, (qp, kp, qo, ko, qs, ks, qos, kos,
+                      0 if q_weight is None else self._shaped("q_weight", q_weight, self._dtype, (self._dim,)),
+                      0 if k_weight is None else self._shaped("k_weight", k_weight, self._dtype, (self._dim,)),
+                      self._flat("cos_sin", cos_sin, self._f32, 0), self._flat("positions", positions, self._i32, rows),
+                      self._status(status), eps, weight_offset, table, rot, 1 if interleaved else 0, rows)
 
     def norm_rope(self, *, cos_sin, positions, status, q=None, k=None, q_out=None, k_out=None, q_weight=None,
                   k_weight=None, eps=1e-6, weight_offset=0.0, interleaved=False, stream=None) -> None:
@@ -154,8 +172,11 @@ class AttnPlan:
         ``q`` [rows, q_heads, head_dim] and ``k`` [rows, kv_heads, head_dim].
         ``cos_sin`` is float32 [positions, rot_dim]: the cosines of the rot_dim / 2
         angles, then their sines.  Rows with a negative position are skipped."""
-        io = self._rope(q, k, q_out, k_out, q_weight, k_weight, eps, weight_offset, cos_sin, interleaved, positions, status)
-        _check(lib().lp_norm_rope(self._h, ctypes.byref(io), self._stream(stream)), "lp_norm_rope")
+        _, rope = self._rope(q, k, q_out, k_out, q_weight, k_weight, eps, weight_offset, cos_sin, interleaved, positions, status)
+        _PACK_ROPE.pack_into(self._io, 0, *rope)
+        rc = self._norm_rope(self._h, self._at, self._stream(stream))
+        if rc:
+            _check(rc, "lp_norm_rope")
 
     def append(self, *, k, v, k_cache, v_cache, group_indptr, lens, block_tables, cos_sin, positions, status, q=None,
                q_out=None, k_out=None, q_weight=None, k_weight=None, eps=1e-6, weight_offset=0.0, interleaved=False,
@@ -163,17 +184,17 @@ class AttnPlan:
         """``norm_rope``, with the keys and values of row j of group g written to
         token ``lens[g] + j`` of the paged caches (``block_tables`` int32 [groups,
         max_pages]); ``k_out`` is optional."""
-        d = self.desc
-        io = AppendIO()
-        io.rope = self._rope(q, k, q_out, k_out, q_weight, k_weight, eps, weight_offset, cos_sin, interleaved, positions, status)
-        io.v, io.v_stride = self._heads("v", v, io.rope.rows, d.kv_heads)
+        rows, rope = self._rope(q, k, q_out, k_out, q_weight, k_weight, eps, weight_offset, cos_sin, interleaved, positions, status)
+        vp, vs = self._rows("v", v, rows, self._kv_heads)
         groups = group_indptr.numel() - 1
-        io.group_indptr = self._flat("group_indptr", group_indptr, self._i32, None, 1)
-        io.lens = self._flat("lens", lens, self._i32, None, groups)
-        io.block_tables = self._flat("block_tables", block_tables, self._i32, (groups, d.max_pages))
-        io.k_cache, io.v_cache = self._caches(k_cache, v_cache)
-        io.groups = groups
-        _check(lib().lp_kv_append(self._h, ctypes.byref(io), self._stream(stream)), "lp_kv_append")
+        _PACK_APPEND.pack_into(
+            self._io, 0, *rope, vp, vs, self._flat("group_indptr", group_indptr, self._i32, 1), self._flat("lens", lens, self._i32, groups),
+            self._shaped("block_tables", block_tables, self._i32, (groups, self.desc.max_pages)),
+            self._shaped("k_cache", k_cache, self._dtype, self._cache_shape), self._shaped("v_cache", v_cache, self._dtype, self._cache_shape),
+            groups)
+        rc = self._append(self._h, self._at, self._stream(stream))
+        if rc:
+            _check(rc, "lp_kv_append")
 
     def attend(self, *, q, k_cache, v_cache, group_indptr, lens, block_tables, out, status, lse_out=None, row_masks=None,
                prefix_indptr=None, prefix_lens=None, prefix_tables=None, scale=None, stream=None) -> None:
@@ -182,25 +203,24 @@ class AttnPlan:
         the prefix that serves their group (``prefix_indptr`` int32 [prefixes + 1]
         over groups, ``prefix_lens`` [prefixes], ``prefix_tables`` [prefixes,
         max_prefix_pages]).  ``lse_out`` is float32 [rows, q_heads]."""
-        d = self.desc
-        io = AttendIO()
-        rows = int(q.shape[0])
-        io.q, io.q_stride = self._heads("q", q, rows, d.q_heads)
-        io.out, io.out_stride = self._heads("out", out, rows, d.q_heads)
-        io.k_cache, io.v_cache = self._caches(k_cache, v_cache)
+        i32 = self._i32
+        rows = q.shape[0]
+        qp, qs = self._rows("q", q, rows, self._q_heads)
+        op, os_ = self._rows("out", out, rows, self._q_heads)
         groups = group_indptr.numel() - 1
-        io.group_indptr = self._flat("group_indptr", group_indptr, self._i32, None, 1)
-        io.lens = self._flat("lens", lens, self._i32, None, groups)
-        io.block_tables = self._flat("block_tables", block_tables, self._i32, (groups, d.max_pages))
-        io.row_masks = self._flat("row_masks", row_masks, self._i32, None, rows)
+        prefixes = pi = pl = pt = 0
         if prefix_lens is not None:
-            n = prefix_lens.numel()
-            io.prefix_indptr = self._flat("prefix_indptr", prefix_indptr, self._i32, (n + 1,))
-            io.prefix_lens = self._flat("prefix_lens", prefix_lens, self._i32)
-            io.prefix_tables = self._flat("prefix_tables", prefix_tables, self._i32, (n, d.max_prefix_pages))
-            io.prefixes = n
-        io.lse_out = self._flat("lse_out", lse_out, self._f32, (rows, d.q_heads))
-        io.status = self._status(status)
-        io.scale = d.head_dim ** -0.5 if scale is None else scale
-        io.rows, io.groups = rows, groups
-        _check(lib().lp_attend(self._h, ctypes.byref(io), self._stream(stream)), "lp_attend")
+            prefixes = prefix_lens.numel()
+            pi = self._flat("prefix_indptr", prefix_indptr, i32, prefixes + 1)
+            pl = self._flat("prefix_lens", prefix_lens, i32, 0)
+            pt = self._shaped("prefix_tables", prefix_tables, i32, (prefixes, self.desc.max_prefix_pages))
+        _PACK_ATTEND.pack_into(
+            self._io, 0, qp, qs, self._shaped("k_cache", k_cache, self._dtype, self._cache_shape),
+            self._shaped("v_cache", v_cache, self._dtype, self._cache_shape), self._flat("group_indptr", group_indptr, i32, 1),
+            self._flat("lens", lens, i32, groups), self._shaped("block_tables", block_tables, i32, (groups, self.desc.max_pages)),
+            self._flat("row_masks", row_masks, i32, rows), pi, pl, pt, op, os_,
+            self._shaped("lse_out", lse_out, self._f32, (rows, self._q_heads)), self._status(status),
+            self._dim ** -0.5 if scale is None else scale, rows, groups, prefixes)
+        rc = self._attend(self._h, self._at, self._stream(stream))
+        if rc:
+            _check(rc, "lp_attend")

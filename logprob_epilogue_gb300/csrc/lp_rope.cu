@@ -4,15 +4,22 @@
 //
 // Per head x of D lanes: y = x * rsqrt(mean(x^2) + eps) * (offset + w), then
 // each pair (a, b) of the first `rot` lanes becomes (a cos - b sin, b cos + a
-// sin), in FP32, with the one rounding at the store.
+// sin), in FP32, with the one rounding at the store.  With the weights folded
+// into the rotation a lane is
+//   y = rs * (x * (cos (offset + w)) + x' * (+-sin (offset + w'))),
+// x' the pair's other lane: two products per lane, the factors the same for
+// every head of a row.
 //
-// D / 8 threads hold a head, eight consecutive lanes (one 16-byte word) each:
-// the mean square is a shuffle reduction among them, the partner of a rotated
-// lane (rot / 2 lanes away, a multiple of 8) sits at the same place of another
-// thread's word, so the rotation is one more shuffle and no shared memory is
-// needed.  A task is one row and four heads: four loads in flight per thread,
-// and the row's cos and sin are loaded once for the four.  Bound: bytes in and
-// out.
+// D / 8 threads hold a head, eight consecutive lanes (one 16-byte word) each.
+// The mean square is a shuffle reduction among them; the other lane of a
+// half-split pair (rot / 2 lanes away, a multiple of 8) sits at the same place
+// of another thread's word, so it comes with four shuffles of the words as
+// loaded.  A task is one row and up to four heads of one of q, k and v: four
+// loads in flight per thread before anything is waited for, the row's factors
+// formed once for the four.  No shared memory.
+//
+// Bound: bytes in and out, and close behind them the instructions (about 75
+// per word).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -25,75 +32,59 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kRopeThreads = 256;
 constexpr int kHeads = 4;  // heads per task
 
+__host__ __device__ constexpr int chunks_of(int heads) { return (heads + kHeads - 1) / kHeads; }
+
+template <bool kBf16>
+__device__ __forceinline__ void widen8(const uint4& w, float (&x)[8]) {
+    using H = Half<kBf16>;
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 f = H::unpack(a[j]);
+        x[2 * j] = f.x;
+        x[2 * j + 1] = f.y;
+    }
+}
+
 template <bool kBf16, int D, bool kAppend>
 __global__ void __launch_bounds__(kRopeThreads) lp_rope_kernel(RopeParams p) {
     using H = Half<kBf16>;
     using T = typename H::T;
-    constexpr int kLanes = D / 8;                     // threads per head
-    constexpr int kTasks = kRopeThreads / kLanes;     // tasks per block
-    const int lane = threadIdx.x % kLanes;
-    const int heads = p.q_heads + (kAppend ? 2 : 1) * p.kv_heads;
-    const int per_row = (heads + kHeads - 1) / kHeads;
-    const long long first = (long long)blockIdx.x * kTasks;
-    const long long task = first + threadIdx.x / kLanes;
+    constexpr int kLanes = D / 8;                  // threads per head
+    constexpr int kTasks = kRopeThreads / kLanes;  // tasks per block
+    const int lane = threadIdx.x % kLanes, e0 = lane * 8;
+    const int cq = chunks_of(p.q_heads), ck = chunks_of(p.kv_heads), per_row = cq + (kAppend ? 2 : 1) * ck;
+    const unsigned first = blockIdx.x * kTasks, task = first + threadIdx.x / kLanes;
+    const unsigned at = task / per_row;
+    const bool live = at < (unsigned)p.rows;
+    const int row = live ? (int)at : 0;
+    const int c = (int)(task - at * per_row);
+    const int kind = c < cq ? 0 : (c < cq + ck ? 1 : 2);  // q, k, v
+    const int h0 = (kind == 0 ? c : (kind == 1 ? c - cq : c - cq - ck)) * kHeads;
+    const int heads = (kind == 0 ? p.q_heads : p.kv_heads) - h0, n = !live ? 0 : (heads < kHeads ? heads : kHeads);
+    const T* src = kind == 0   ? reinterpret_cast<const T*>(p.q) + row * p.q_stride
+                   : kind == 1 ? reinterpret_cast<const T*>(p.k) + row * p.k_stride
+                               : reinterpret_cast<const T*>(p.v) + row * p.v_stride;
+    src += h0 * D + e0;
+
+    // the heads' words, whatever the row's position
+    uint4 w[kHeads];
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+        w[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (i < n) w[i] = *reinterpret_cast<const uint4*>(src + i * D);
+    }
+    const int pos = live ? __ldg(&p.positions[row]) : -1;
+    const void* weight = kind == 0 ? p.q_weight : (kind == 1 ? p.k_weight : nullptr);
     int g = -1;
     if constexpr (kAppend) g = block_find_group(p.indptr, p.G, (int)(first / per_row));
-    const long long row64 = task / per_row;
-    const bool live = row64 < p.rows;
-    const int row = live ? (int)row64 : 0;
-    const int h0 = (int)(task % per_row) * kHeads;
-    const int pos = live ? __ldg(&p.positions[row]) : -1;
-    if (pos >= p.max_pos && lane == 0 && h0 == 0) atomicOr(p.status, kStatusBadPosition);
-    const bool work = live && pos >= 0 && pos < p.max_pos;
-    const int e0 = lane * 8;
+    if (pos >= p.max_pos && lane == 0 && c == 0) atomicOr(p.status, kStatusBadPosition);
+    const bool work = pos >= 0 && pos < p.max_pos;
 
-    // loads: four heads' words, then the row's cos and sin
-    uint4 w[kHeads] = {};
-    if (work) {
-#pragma unroll
-        for (int i = 0; i < kHeads; ++i) {
-            const int h = h0 + i;
-            if (h >= heads) continue;
-            const T* src;
-            if (h < p.q_heads) src = reinterpret_cast<const T*>(p.q) + row * p.q_stride + (long long)h * D;
-            else if (!kAppend || h < p.q_heads + p.kv_heads)
-                src = reinterpret_cast<const T*>(p.k) + row * p.k_stride + (long long)(h - p.q_heads) * D;
-            else
-                src = reinterpret_cast<const T*>(p.v) + row * p.v_stride + (long long)(h - p.q_heads - p.kv_heads) * D;
-            w[i] = *reinterpret_cast<const uint4*>(src + e0);
-        }
-    }
-    const int half = p.rot >> 1;
-    float cs[8], sn[8];  // y_e = x_e * cs + partner * sn
-#pragma unroll
-    for (int e = 0; e < 8; ++e) cs[e] = 1.0f, sn[e] = 0.0f;
-    if (work && e0 < p.rot) {
-        const float* t = p.cos_sin + (long long)pos * p.rot;
-        if (p.interleaved) {
-            const float4 c = __ldg(reinterpret_cast<const float4*>(t + e0 / 2));
-            const float4 s = __ldg(reinterpret_cast<const float4*>(t + half + e0 / 2));
-            const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) cs[e] = cc[e / 2], sn[e] = (e & 1) ? ss[e / 2] : -ss[e / 2];
-        } else {
-            const int i0 = e0 < half ? e0 : e0 - half;
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                const float4 c = __ldg(reinterpret_cast<const float4*>(t + i0) + v);
-                const float4 s = __ldg(reinterpret_cast<const float4*>(t + half + i0) + v);
-                const float sign = e0 < half ? -1.0f : 1.0f;
-                cs[4 * v] = c.x, cs[4 * v + 1] = c.y, cs[4 * v + 2] = c.z, cs[4 * v + 3] = c.w;
-                sn[4 * v] = sign * s.x, sn[4 * v + 1] = sign * s.y, sn[4 * v + 2] = sign * s.z, sn[4 * v + 3] = sign * s.w;
-            }
-        }
-    }
-    // the partner's thread (half-split pairs): threads past rot keep their own
-    const int mate = (p.interleaved || e0 >= p.rot) ? lane : (e0 < half ? lane + half / 8 : lane - half / 8);
-
-    // the cache slot of the row's token
-    long long slot = -1;  // (page * kv_heads) * page_size + offset, head 0
+    // the cache slot of the row's token: (page * kv_heads) * page_size + offset, head 0
+    long long slot = -1;
     if constexpr (kAppend) {
-        if (work && h0 + kHeads > p.q_heads) {
+        if (work && kind != 0) {
             if (g < 0) g = 0;
             while (g < p.G && __ldg(&p.indptr[g + 1]) <= row) ++g;
             if (g < p.G) {
@@ -114,77 +105,104 @@ __global__ void __launch_bounds__(kRopeThreads) lp_rope_kernel(RopeParams p) {
                     }
                 }
             }
+            slot += slot >= 0 ? (long long)h0 << p.page_shift : 0;
+        }
+    }
+    const long long step = (long long)D << p.page_shift;  // elements from a head's slot to the next's
+
+    // factors of a lane and of its pair's other one, the weights in them
+    const int half = p.rot >> 1;
+    const bool turn = kind != 2 && work && e0 < p.rot;
+    float fa[8], fb[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) fa[e] = 1.0f, fb[e] = 0.0f;
+    // a half-split pair's other thread (threads past rot: their own)
+    const int mate = (p.interleaved || e0 >= p.rot) ? lane : (e0 < half ? lane + half / 8 : lane - half / 8);
+    if (turn) {
+        const float* t = p.cos_sin + (long long)pos * p.rot;
+        if (p.interleaved) {
+            const float4 cc = __ldg(reinterpret_cast<const float4*>(t + e0 / 2));
+            const float4 ss = __ldg(reinterpret_cast<const float4*>(t + half + e0 / 2));
+            const float a[4] = {cc.x, cc.y, cc.z, cc.w}, b[4] = {ss.x, ss.y, ss.z, ss.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) fa[e] = a[e / 2], fb[e] = (e & 1) ? b[e / 2] : -b[e / 2];
+        } else {
+            const int i0 = e0 < half ? e0 : e0 - half;
+            const float sign = e0 < half ? -1.0f : 1.0f;
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const float4 cc = __ldg(reinterpret_cast<const float4*>(t + i0) + v);
+                const float4 ss = __ldg(reinterpret_cast<const float4*>(t + half + i0) + v);
+                fa[4 * v] = cc.x, fa[4 * v + 1] = cc.y, fa[4 * v + 2] = cc.z, fa[4 * v + 3] = cc.w;
+                fb[4 * v] = sign * ss.x, fb[4 * v + 1] = sign * ss.y, fb[4 * v + 2] = sign * ss.z, fb[4 * v + 3] = sign * ss.w;
+            }
+        }
+    }
+    if (weight != nullptr) {
+        float u[8], v[8];
+        widen8<kBf16>(__ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(weight) + e0)), u);
+        widen8<kBf16>(__ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(weight) + mate * 8)), v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            fa[e] *= p.weight_offset + u[e];
+            fb[e] *= p.weight_offset + (p.interleaved ? u[e ^ 1] : v[e]);
         }
     }
 
+    T* dst = nullptr;
+    if (kind == 0) dst = reinterpret_cast<T*>(p.q_out) + row * p.q_out_stride + h0 * D + e0;
+    else if (kind == 1 && p.k_out != nullptr) dst = reinterpret_cast<T*>(p.k_out) + row * p.k_out_stride + h0 * D + e0;
+    T* cache = nullptr;
+    if constexpr (kAppend) {
+        if (slot >= 0) cache = reinterpret_cast<T*>(kind == 1 ? p.k_cache : p.v_cache) + slot * D + e0;
+    }
+    const bool norms = p.q_weight != nullptr || p.k_weight != nullptr, turns = p.rot > 0 && !p.interleaved;  // of the call
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
-        const int h = h0 + i;
-        const bool is_q = h < p.q_heads, is_k = !is_q && h < p.q_heads + p.kv_heads;
-        const bool turn = h < heads && (is_q || is_k);
-        const void* weight = is_q ? p.q_weight : (is_k ? p.k_weight : nullptr);
-        float x[8];
-        {
-            const uint32_t a[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        float x[8], o[8];
+        widen8<kBf16>(w[i], x);
+        float rs = 1.0f;
+        if (norms) {
+            float ss = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = H::unpack(a[j]);
-                x[2 * j] = f.x;
-                x[2 * j + 1] = f.y;
+            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+            for (int s = kLanes / 2; s > 0; s >>= 1) ss += __shfl_xor_sync(kFull, ss, s, kLanes);
+            if (weight != nullptr) rs = rsqrtf(ss * (1.0f / D) + p.eps);
+        }
+        if (turns) {
+            uint4 m;
+            m.x = __shfl_sync(kFull, w[i].x, mate, kLanes);
+            m.y = __shfl_sync(kFull, w[i].y, mate, kLanes);
+            m.z = __shfl_sync(kFull, w[i].z, mate, kLanes);
+            m.w = __shfl_sync(kFull, w[i].w, mate, kLanes);
+            widen8<kBf16>(m, o);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = x[e ^ 1];
+        }
+        if (!work || i >= n) continue;
+        uint4 y = w[i];  // values go as they are
+        if (kind != 2) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float z = x[e] * fa[e];
+                x[e] = (turn ? fmaf(o[e], fb[e], z) : z) * rs;
             }
+            y.x = H::pack(x[0], x[1]);
+            y.y = H::pack(x[2], x[3]);
+            y.z = H::pack(x[4], x[5]);
+            y.w = H::pack(x[6], x[7]);
         }
-        float ss = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o, kLanes);
-        if (weight != nullptr && h < heads) {
-            const float rs = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
-            const uint4 ww = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(weight) + e0));
-            const uint32_t a[4] = {ww.x, ww.y, ww.z, ww.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = H::unpack(a[j]);
-                x[2 * j] *= rs * (p.weight_offset + f.x);
-                x[2 * j + 1] *= rs * (p.weight_offset + f.y);
-            }
-        }
-        float y[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float other = __shfl_sync(kFull, x[e], mate, kLanes);  // the thread's own lane when interleaved
-            const float partner = p.interleaved ? x[e ^ 1] : other;
-            y[e] = (turn && e0 < p.rot) ? x[e] * cs[e] + partner * sn[e] : x[e];
-        }
-        if (!work || h >= heads) continue;
-        uint4 o;
-        o.x = H::pack(y[0], y[1]);
-        o.y = H::pack(y[2], y[3]);
-        o.z = H::pack(y[4], y[5]);
-        o.w = H::pack(y[6], y[7]);
-        if (is_q) {
-            *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.q_out) + row * p.q_out_stride + (long long)h * D + e0) = o;
-        } else if (is_k) {
-            const int kh = h - p.q_heads;
-            if (p.k_out != nullptr)
-                *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.k_out) + row * p.k_out_stride + (long long)kh * D + e0) = o;
-            if constexpr (kAppend) {
-                if (slot >= 0)
-                    *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.k_cache) + (slot + ((long long)kh << p.page_shift)) * D + e0) = o;
-            }
-        } else if constexpr (kAppend) {
-            const int vh = h - p.q_heads - p.kv_heads;
-            if (slot >= 0)  // unchanged bits
-                *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.v_cache) + (slot + ((long long)vh << p.page_shift)) * D + e0) = w[i];
-        }
+        if (dst != nullptr) *reinterpret_cast<uint4*>(dst + i * D) = y;
+        if (kAppend && cache != nullptr) *reinterpret_cast<uint4*>(cache + i * step) = y;
     }
 }
 
 template <bool kBf16, int D>
 cudaError_t launch(const RopeParams& p, cudaStream_t stream) {
     const bool append = p.k_cache != nullptr;
-    const int heads = p.q_heads + (append ? 2 : 1) * p.kv_heads;
-    const long long tasks = (long long)p.rows * ((heads + kHeads - 1) / kHeads);
+    const long long tasks = (long long)p.rows * (chunks_of(p.q_heads) + (append ? 2 : 1) * chunks_of(p.kv_heads));
     constexpr int kTasks = kRopeThreads / (D / 8);
     const unsigned grid = (unsigned)((tasks + kTasks - 1) / kTasks);
     if (append) lp_rope_kernel<kBf16, D, true><<<grid, kRopeThreads, 0, stream>>>(p);

@@ -56,6 +56,7 @@ def test_struct_sizes_match_the_header(L, tmp_path):
     subprocess.run(["gcc", "-I", os.path.join(root, "include"), str(src), "-o", str(exe)], check=True)
     sizes = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
     assert sizes == [ctypes.sizeof(t) for t in (A.AttnDesc, A.RopeIO, A.AppendIO, A.AttendIO)]
+    assert sizes[1:] == [s.size for s in (A._PACK_ROPE, A._PACK_APPEND, A._PACK_ATTEND)]
 
 
 @pytest.mark.gpu
