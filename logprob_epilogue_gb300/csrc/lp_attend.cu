@@ -185,6 +185,12 @@ __device__ __forceinline__ long long part_row(const AttendParams& p, bool prefix
     return p.sc.prefix_slots * 2 * kQTile + (slot * 2 + set) * p.sc.group_rows;
 }
 
+// Where a unit that is not dealt out is entered for the join; -1 as above.
+__device__ __forceinline__ long long unit_index(const AttendParams& p, bool prefix, int unit) {
+    if (prefix) return unit < p.sc.prefix_slots ? unit : -1;
+    return unit < p.sc.group_slots ? p.sc.prefix_slots + unit : -1;
+}
+
 // A part's results lie chunk by chunk, four lanes of the head of every row
 // side by side (a warp's stores are whole lines): index of a float4, `base`
 // the part's first row and `cap` the rows it has room for.
@@ -212,7 +218,8 @@ struct Start {
 // Walks a block's pieces: its share of the units that go round whole, then its
 // run of the other prefix units' tiles, then of the groups'.
 struct Walk {
-    unsigned long long begin[2], finish[2];  // the runs
+    Runs runs[2], run;                 // of prefixes, of groups; the current
+    unsigned long long begin[2], finish[2];  // this block's
     const Start* start;
     int kind;
     int deal, deal_end, round, dealt;  // segments with units that go round; rounds dealt; units of earlier segments
@@ -221,6 +228,7 @@ struct Walk {
     Seg s;
     __device__ __forceinline__ void enter(int k) {
         kind = k;
+        run = runs[k];
         pos = begin[k], end = finish[k];
         off = start[k].off, seg = start[k].seg, units = start[k].units, s = start[k].s;
     }
@@ -273,6 +281,12 @@ struct Walk {
             const int t1 = u1 > kUnitCost ? (int)((u1 - kUnitCost + s.cost - 1) / s.cost) : 0;
             if (t1 <= t0) continue;
             fill(p, x, seg, s, s.dealt + unit, t0, t1 - t0, (long long)units + unit + cta);
+            if (t0 == 0 && (threadIdx.x & 31) == 0) {
+                // for the join: the unit's first slot and how many blocks have a piece of it
+                const unsigned long long last = off + unit * span + kUnitCost + (unsigned long long)(s.tiles - 1) * s.cost;
+                const long long at = unit_index(p, kind == 0, units + unit);
+                if (at >= 0) p.sc.units[at] = make_int2(units + unit + cta, t1 == s.tiles ? 1 : run.block_of(last) - cta + 1);
+            }
             return true;
         }
         x.rows = 0;
@@ -350,14 +364,13 @@ __device__ __forceinline__ bool plan_run(const AttendParams& p, Ctl* ctl, Runs (
             const int kind = s < p.P ? 0 : 1;
             const unsigned long long work = x.work(p), off = kind == 0 ? at0 : at1, lo = kind == 0 ? lo0 : lo1;
             const int before = (int)(kind == 0 ? (u >> 32) + all_dealt : u & 0xFFFFFFFFull);  // slots: the dealt units', then the others'
-            if (cta == 0) p.sc.seg_tiles[s] = off, p.sc.seg_units[s] = make_int2(before, d);
+            if (cta == 0) p.sc.seg_units[s] = make_int2(before, d);
             if (lo >= off && lo < off + work) ctl->start[kind].off = off, ctl->start[kind].seg = s, ctl->start[kind].units = before, ctl->start[kind].s = x;
             (kind == 0 ? at0 : at1) += work;
             u += (unsigned long long)x.left(p) << (kind == 0 ? 32 : 0);
             d += x.dealt;
         }
     }
-    if (cta == 0 && tid == 0) p.sc.seg_tiles[S] = total0, p.sc.seg_tiles[S + 1] = total1;
     return all_dealt > 0 || cta < runs[0].blocks || cta < runs[1].blocks;
 }
 
@@ -653,6 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             walk.start = ctl->start;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
+                walk.runs[k] = runs[k];
                 const bool any = (int)blockIdx.x < runs[k].blocks;
                 walk.begin[k] = any ? runs[k].start(blockIdx.x) : 0;
                 walk.finish[k] = any ? runs[k].start(blockIdx.x + 1) : 0;
@@ -886,291 +900,190 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// D / 32 consecutive lanes of a head, as stored.
-template <int D>
-struct Words {
-    using W = uint2;
-    static __device__ __forceinline__ W zero() { return make_uint2(0u, 0u); }
-};
-template <>
-struct Words<64> {
-    using W = uint32_t;
-    static __device__ __forceinline__ W zero() { return 0u; }
-};
-
-template <int D>
-__device__ __forceinline__ typename Words<D>::W load_words(const void* base, long long elem) {
-    return *reinterpret_cast<const typename Words<D>::W*>(reinterpret_cast<const unsigned short*>(base) + elem);
-}
-
-template <bool kBf16, int D>
-__device__ __forceinline__ void widen(const typename Words<D>::W& w, float (&x)[D / 32]) {
-    using H = Half<kBf16>;
-    if constexpr (D == 128) {
-        const float2 a = H::unpack(w.x), b = H::unpack(w.y);
-        x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
-    } else {
-        const float2 a = H::unpack(w);
-        x[0] = a.x, x[1] = a.y;
-    }
-}
-
-// Running softmax of one query head, D / 32 lanes of the head per thread, in base 2.
+// ---- the join
+//
+// A warp has four query heads of a row, eight threads each: a thread holds
+// D / 8 lanes of its head, as D / 64 runs of eight.  (All four heads go through
+// the same few instructions: a call's join is short, and long unrolled code is
+// fetched once and bound by that.)
 template <int D>
 struct Acc {
-    float o[D / 32], m, l;
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) o[e] = 0.0f;
-        m = kNegInf, l = 0.0f;
-    }
-    __device__ __forceinline__ void add(float s, float w, const float (&v)[D / 32]) {  // a part: maximum s, sum w, result v
+    static constexpr int kE = D / 8;
+    float o[kE], m, l;  // in base 2
+    __device__ __forceinline__ void add(float s, float w, const float (&v)[kE]) {  // a part: maximum s, sum w, result v
         const float top = fmaxf(m, s), base = top == kNegInf ? 0.0f : top;
         const float f = ex2(m - base), g = ex2(s - base);
         l = l * f + w * g;
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) o[e] = o[e] * f + g * v[e];
+        for (int e = 0; e < kE; ++e) o[e] = o[e] * f + g * v[e];
         m = top;
     }
 };
 
-template <int D>
-__device__ __forceinline__ void load_part(const float* parts, long long base, int cap, int row, int lane, float (&v)[D / 32]) {
-    if constexpr (D == 128) {
-        const float4 w = reinterpret_cast<const float4*>(parts)[part_chunk<D>(base, cap, row, lane)];
-        v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
-    } else {
-        const float2 w = reinterpret_cast<const float2*>(parts)[part_chunk<D>(base, cap, row, lane >> 1) * 2 + (lane & 1)];
-        v[0] = w.x, v[1] = w.y;
-    }
+template <bool kBf16>
+__device__ __forceinline__ void widen8(const uint4& w, float* x) {
+    using H = Half<kBf16>;
+    const float2 a = H::unpack(w.x), b = H::unpack(w.y), c = H::unpack(w.z), d = H::unpack(w.w);
+    x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y, x[4] = c.x, x[5] = c.y, x[6] = d.x, x[7] = d.y;
 }
 
-constexpr int kBatchTokens = 4; // own tokens in flight per warp
-
-// Where the parts of a row's heads lie, for one segment.
+// Where the parts of a row's head lie, for one segment.
 struct Parts {
-    int seg, unit, tile, row, cap, sets;  // sets: parts per piece
-    int tiles, cost, left;                // of the unit; units of the segment before it that are not dealt out (-1: it is)
-    long long span;
+    int row, cap, set, sets;  // row of the unit; the parts of a piece that are its: sets of them from `set` on
     int count;
     long long slot;
 };
 
-// What the call's inputs alone say, for the unit rows of query heads `head` ..
-// of the segment's row `rel`.
 __device__ __forceinline__ Parts locate(const AttendParams& p, int seg, int rel, int head) {
     Parts x;
-    const Seg s = load_seg(p, seg);
-    x.seg = seg;
-    x.tiles = s.tiles;
-    x.span = s.span();
-    x.cost = s.cost;
-    const int rt = p.rows_per_tile, u = rel / (2 * rt), in = rel - u * 2 * rt, kvh = head / p.share;
-    const bool two = s.n - u * 2 * rt > rt;
-    x.tile = two && in >= rt ? 1 : 0;
-    x.sets = two ? 1 : 2;  // a unit of one tile: a part of each warpgroup
-    x.row = (in - x.tile * rt) * p.share + head - kvh * p.share;
-    x.unit = kvh * s.units + u;
-    x.left = x.unit < s.dealt ? -1 : x.unit - s.dealt;
-    x.cap = seg < p.P ? kQTile : p.sc.group_rows;
     x.count = 0;
-    x.slot = 0;
+    const Seg s = load_seg(p, seg);
+    if (s.tiles == 0) return x;
+    const bool prefix = seg < p.P;
+    const int2 base = p.sc.seg_units[seg];
+    const int rt = p.rows_per_tile, u = rel / (2 * rt), in = rel - u * 2 * rt, kvh = head / p.share, unit = kvh * s.units + u;
+    const bool two = s.n - u * 2 * rt > rt;
+    x.set = two && in >= rt ? 1 : 0;
+    x.sets = two ? 1 : 2;  // a unit of one tile: a part of each warpgroup
+    x.row = (in - x.set * rt) * p.share + head - kvh * p.share;
+    x.cap = prefix ? kQTile : p.sc.group_rows;
+    int pieces = 1;
+    if (unit < s.dealt) {
+        x.slot = (long long)base.y + unit;
+    } else {
+        const long long at = unit_index(p, prefix, base.x + unit - s.dealt);
+        const int2 e = at >= 0 ? p.sc.units[at] : make_int2(0, 0);
+        x.slot = e.x;
+        pieces = e.y;
+    }
+    x.count = pieces * x.sets;
     return x;
 }
 
-// The rest, from the offsets that the attention kernel left.
-__device__ __forceinline__ void place(const AttendParams& p, Parts& x, const Runs& runs, unsigned long long tiles, int2 slots) {
-    int pieces = 1;
-    if (x.left < 0) {
-        x.slot = (long long)slots.y + x.unit;
-    } else {
-        // the blocks whose runs hold the unit's first and last tile
-        const unsigned long long begin = tiles + (unsigned long long)(x.left * x.span + kUnitCost);
-        const int c0 = runs.block_of(begin);
-        pieces = runs.block_of(begin + (unsigned long long)(x.tiles - 1) * x.cost) - c0 + 1;
-        x.slot = (long long)slots.x + x.left + c0;
-    }
-    x.count = pieces * x.sets;
-}
-
-// Joins the parts of n heads; warp `sub` of `warps` takes every warps-th part.
-template <int D, int kHeads, int kBatchParts>  // parts in flight per warp and head
-__device__ __forceinline__ void join_parts(const AttendParams& p, Acc<D> (&a)[kHeads], int n, const Parts& x, int lane, int sub, int warps) {
-    for (int k0 = sub; k0 < x.count; k0 += warps * kBatchParts) {
-        float2 ml[kBatchParts][kHeads];
-        float v[kBatchParts][kHeads][D / 32];
-#pragma unroll
-        for (int b = 0; b < kBatchParts; ++b) {
-            const int k = k0 + b * warps;
-            const long long base =
-                k < x.count ? part_row(p, x.seg < p.P, x.slot + (x.sets == 1 ? k : k >> 1), x.sets == 1 ? x.tile : k & 1) : -1;
-#pragma unroll
-            for (int h = 0; h < kHeads; ++h) {
-                ml[b][h] = make_float2(kNegInf, 0.0f);
-#pragma unroll
-                for (int e = 0; e < D / 32; ++e) v[b][h][e] = 0.0f;
-                if (base >= 0 && h < n) {
-                    ml[b][h] = p.sc.part_ml[base + x.row + h];
-                    load_part<D>(p.sc.part_o, base, x.cap, x.row + h, lane, v[b][h]);
-                }
-            }
-        }
-#pragma unroll
-        for (int b = 0; b < kBatchParts; ++b)
-#pragma unroll
-            for (int h = 0; h < kHeads; ++h)
-                if (ml[b][h].x != kNegInf || ml[b][h].y != 0.0f) a[h].add(ml[b][h].x, ml[b][h].y, v[b][h]);  // else nothing was written
-    }
-}
-
-// kSub warps per row and kHeads query heads of one key-value head (its keys and
-// values are loaded once for them): the round's own tokens that
-// the row sees, then the parts of the row's prefix and of its group's committed
-// tokens.
-template <bool kBf16, int D, int kSub, int kHeads>
-__global__ void __launch_bounds__(kJoinThreads, kHeads == 1 ? 4 : 2) lp_attend_join_kernel(const AttendParams p) {
-    constexpr int kBatchParts = kHeads == 1 ? 4 : 2;
+// kSub warps per row and four heads: the round's own tokens that the row sees,
+// then the parts of the row's prefix and of its group's committed tokens.
+template <bool kBf16, int D, int kSub>
+__global__ void __launch_bounds__(kJoinThreads, kSub == 1 ? 3 : 2) lp_attend_join_kernel(const AttendParams p) {
     using H = Half<kBf16>;
     using T = typename H::T;
-    constexpr int kE = D / 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % kSub;
-    const int chunks = (p.share + kHeads - 1) / kHeads;
-    const int row = blockIdx.x, chunk = blockIdx.y * (kJoinWarps / kSub) + warp / kSub;
-    const int kvh = chunk / chunks, first = (chunk - kvh * chunks) * kHeads, head = kvh * p.share + first;
-    const int n = p.share - first < kHeads ? p.share - first : kHeads;  // this warp's heads
+    constexpr int kE = D / 8, kRuns = D / 64, kBatch = kSub > 1 ? 4 : 2;  // parts in flight per thread
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % kSub, l = lane & 7;
+    const int row = blockIdx.x, head = (blockIdx.y * (kJoinWarps / kSub) + warp / kSub) * 4 + (lane >> 3);
     const int g = block_find_group(p.indptr, p.G, row);
-    bool mine = g >= 0 && g < p.G && kvh < p.kv_heads;
+    bool mine = g >= 0 && g < p.G;
     mine = mine && row >= __ldg(&p.indptr[g]) && row < __ldg(&p.indptr[g + 1]);  // else two entries claim the row
-    Acc<D> a[kHeads];
-#pragma unroll
-    for (int h = 0; h < kHeads; ++h) a[h].clear();
+    const bool exists = mine && head < p.q_heads;
     Group grp = {0, 0, 0, false};
     if (mine) grp = load_group(p, g);
-    Parts own, pre;
-    own.tiles = pre.tiles = 0;
-    if (grp.n > 0) {
-        own = locate(p, p.P + g, row - grp.r0, head);
-        for (int i = 0; i < p.P; ++i) {
-            const Prefix x = load_prefix(p, i);
-            if (x.bad || g < x.g0 || g >= x.g1) continue;
-            pre = locate(p, i, row - x.r0, head);
-            break;
-        }
-        // the round's own tokens, four at a time: a lane's four (two) lanes of the head from each
-        typename Words<D>::W qw[kHeads];
+    Acc<D> a;
 #pragma unroll
-        for (int h = 0; h < kHeads; ++h) qw[h] = load_words<D>(p.q, row * p.q_stride + (long long)(head + (h < n ? h : 0)) * D + lane * kE);
+    for (int e = 0; e < kE; ++e) a.o[e] = 0.0f;
+    a.m = kNegInf, a.l = 0.0f;
+    const int kvh = exists ? head / p.share : 0;
+    if (grp.n > 0) {
+        float q[kE];
+#pragma unroll
+        for (int r = 0; r < kRuns; ++r)
+            widen8<kBf16>(*reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.q) + row * p.q_stride +
+                                                          (long long)(exists ? head : 0) * D + r * 64 + l * 8), q + r * 8);
         const float c = p.scale * kLog2e;
         const int j = row - grp.r0;
         const unsigned mask = p.row_masks != nullptr ? __ldg(&p.row_masks[row]) : (2u << j) - 1u;
         int page = 0;  // lane i: of token i
         if (lane < grp.n) page = __ldg(&p.tables[(long long)g * p.max_pages + ((grp.len + lane) >> p.page_shift)]);
-        unsigned todo = mask & (grp.n < 32 ? (1u << grp.n) - 1u : kFull);
         const unsigned here = __ballot_sync(kFull, page >= 0 && page < p.num_pages);
+        unsigned todo = mask & (grp.n < 32 ? (1u << grp.n) - 1u : kFull);
         if (lane == 0 && (todo & ~here) != 0u) atomicOr(p.status, kStatusBadPage);
-        for (int skip = 0; todo != 0u;) {
-            typename Words<D>::W kw[kBatchTokens], vw[kBatchTokens];
-            bool sees[kBatchTokens];
+#pragma unroll 1
+        for (int turn = 0; todo != 0u; todo &= todo - 1u, ++turn) {
+            if (kSub > 1 && turn % kSub != sub) continue;
+            const int i = __ffs(todo) - 1, t = grp.len + i;
+            const long long pg = __shfl_sync(kFull, page, i);
+            float k[kE], v[kE];
 #pragma unroll
-            for (int b = 0; b < kBatchTokens; ++b) {
-                // the next seen token whose turn is this warp's
-                int i = __ffs(todo) - 1;
-                while (kSub > 1 && i >= 0 && skip++ % kSub != sub) todo &= todo - 1u, i = __ffs(todo) - 1;
-                sees[b] = i >= 0;
-                if (sees[b]) todo &= todo - 1u;
-                const int t = grp.len + (sees[b] ? i : 0), pg = __shfl_sync(kFull, page, sees[b] ? i : 0);
-                kw[b] = vw[b] = Words<D>::zero();
-                if (sees[b] && (here >> i & 1u)) {
-                    const long long at =
-                        (((((long long)pg * p.kv_heads + kvh) << p.page_shift) + (t & ((1 << p.page_shift) - 1))) * D) + lane * kE;
-                    kw[b] = load_words<D>(p.k_cache, at);
-                    vw[b] = load_words<D>(p.v_cache, at);
+            for (int e = 0; e < kE; ++e) k[e] = v[e] = 0.0f;
+            if (here >> i & 1u) {
+                const long long at = ((((pg * p.kv_heads + kvh) << p.page_shift) + (t & ((1 << p.page_shift) - 1))) * D) + l * 8;
+#pragma unroll
+                for (int r = 0; r < kRuns; ++r) {
+                    widen8<kBf16>(*reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.k_cache) + at + r * 64), k + r * 8);
+                    widen8<kBf16>(*reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.v_cache) + at + r * 64), v + r * 8);
                 }
             }
-            float s[kBatchTokens][kHeads];
+            float s = 0.0f;
 #pragma unroll
-            for (int h = 0; h < kHeads; ++h) {
-                float q[kE];
-                widen<kBf16, D>(qw[h], q);
+            for (int e = 0; e < kE; ++e) s = fmaf(q[e], k[e], s);
 #pragma unroll
-                for (int b = 0; b < kBatchTokens; ++b) {
-                    float k[kE];
-                    widen<kBf16, D>(kw[b], k);
-                    s[b][h] = 0.0f;
-#pragma unroll
-                    for (int e = 0; e < kE; ++e) s[b][h] = fmaf(q[e], k[e], s[b][h]);
-                }
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-                for (int b = 0; b < kBatchTokens; ++b)
-#pragma unroll
-                    for (int h = 0; h < kHeads; ++h) s[b][h] += __shfl_xor_sync(kFull, s[b][h], o);
-#pragma unroll
-            for (int b = 0; b < kBatchTokens; ++b) {
-                float v[kE];
-                widen<kBf16, D>(vw[b], v);
-#pragma unroll
-                for (int h = 0; h < kHeads; ++h)
-                    if (sees[b]) a[h].add(s[b][h] * c, 1.0f, v);
-            }
+            for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+            a.add(s * c, 1.0f, v);
         }
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (own.tiles > 0 || pre.tiles > 0) {
-        const unsigned long long pre_total = p.sc.seg_tiles[p.P + p.G], own_total = p.sc.seg_tiles[p.P + p.G + 1];
-        const unsigned long long own_tiles = own.tiles > 0 ? p.sc.seg_tiles[own.seg] : 0, pre_tiles = pre.tiles > 0 ? p.sc.seg_tiles[pre.seg] : 0;
-        const int2 own_slots = own.tiles > 0 ? p.sc.seg_units[own.seg] : make_int2(0, 0);
-        const int2 pre_slots = pre.tiles > 0 ? p.sc.seg_units[pre.seg] : make_int2(0, 0);
-        if (own.tiles > 0) {
-            place(p, own, make_runs(own_total, p.grid, 1), own_tiles, own_slots);
-            join_parts<D, kHeads, kBatchParts>(p, a, n, own, lane, sub, kSub);
-        }
-        if (pre.tiles > 0) {
-            place(p, pre, make_runs(pre_total, p.grid, 0), pre_tiles, pre_slots);
-            join_parts<D, kHeads, kBatchParts>(p, a, n, pre, lane, sub, kSub);
+    if (grp.n > 0) {
+#pragma unroll 1
+        for (int i = 0; i <= p.P; ++i) {  // the row's prefix, then its group
+            int seg = p.P + g, first = grp.r0;
+            if (i < p.P) {
+                const Prefix x = load_prefix(p, i);
+                if (x.bad || g < x.g0 || g >= x.g1) continue;
+                seg = i, first = x.r0;
+                i = p.P - 1;  // the first that serves it
+            }
+            const Parts x = locate(p, seg, row - first, exists ? head : 0);
+            const bool prefix = seg < p.P;
+#pragma unroll 1
+            for (int k0 = sub; __any_sync(kFull, k0 < x.count); k0 += kSub * kBatch) {
+                float2 ml[kBatch];
+                float v[kBatch][kE];
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                    const int k = k0 + b * kSub;
+                    const long long base = k < x.count ? part_row(p, prefix, x.slot + (x.sets == 1 ? k : k >> 1), x.sets == 1 ? x.set : k & 1) : -1;
+                    ml[b] = base >= 0 ? p.sc.part_ml[base + x.row] : make_float2(kNegInf, 0.0f);
+                    const float4* src = reinterpret_cast<const float4*>(p.sc.part_o) + part_chunk<D>(base >= 0 ? base : 0, x.cap, x.row, 2 * l);
+#pragma unroll
+                    for (int r = 0; r < kRuns * 2; ++r) {
+                        float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (base >= 0) w = src[(r / 2 * 16 + (r & 1)) * x.cap];
+                        v[b][4 * r] = w.x, v[b][4 * r + 1] = w.y, v[b][4 * r + 2] = w.z, v[b][4 * r + 3] = w.w;
+                    }
+                }
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b)
+                    if (ml[b].x != kNegInf || ml[b].y != 0.0f) a.add(ml[b].x, ml[b].y, v[b]);  // else nothing was written
+            }
         }
     }
     if constexpr (kSub > 1) {  // the warps' sums, in the order of the warps
-        __shared__ float4 part[kJoinWarps][kHeads][32];
-        __shared__ float2 part_ml[kJoinWarps][kHeads];
+        __shared__ float part[kJoinWarps][kE][32];
+        __shared__ float2 part_ml[kJoinWarps][32];
 #pragma unroll
-        for (int h = 0; h < kHeads; ++h) {
-            part[warp][h][lane] = make_float4(a[h].o[0], a[h].o[1], kE > 2 ? a[h].o[kE - 2] : 0.0f, kE > 2 ? a[h].o[kE - 1] : 0.0f);
-            if (lane == 0) part_ml[warp][h] = make_float2(a[h].m, a[h].l);
-        }
+        for (int e = 0; e < kE; ++e) part[warp][e][lane] = a.o[e];
+        part_ml[warp][lane] = make_float2(a.m, a.l);
         __syncthreads();
         if (sub != 0) return;
 #pragma unroll 1
-        for (int w = 1; w < kSub; ++w)
+        for (int w = 1; w < kSub; ++w) {
+            const float2 ml = part_ml[warp + w][lane];
+            float v[kE];
 #pragma unroll
-            for (int h = 0; h < kHeads; ++h) {
-                const float4 o = part[warp + w][h][lane];
-                const float2 ml = part_ml[warp + w][h];
-                float v[kE];
-                v[0] = o.x, v[1] = o.y;
-                if constexpr (kE > 2) v[2] = o.z, v[3] = o.w;
-                if (ml.x != kNegInf || ml.y != 0.0f) a[h].add(ml.x, ml.y, v);
-            }
-    }
-    if (!mine) return;
-#pragma unroll
-    for (int h = 0; h < kHeads; ++h) {
-        if (h >= n) break;
-        const float inv = a[h].l > 0.0f ? 1.0f / a[h].l : (a[h].l == 0.0f ? 0.0f : a[h].l);
-        T* dst = reinterpret_cast<T*>(p.out) + row * p.out_stride + (long long)(head + h) * D + lane * kE;
-        if constexpr (D == 128) {
-            uint2 w;
-            w.x = H::pack(a[h].o[0] * inv, a[h].o[1] * inv);
-            w.y = H::pack(a[h].o[2] * inv, a[h].o[3] * inv);
-            *reinterpret_cast<uint2*>(dst) = w;
-        } else {
-            *reinterpret_cast<uint32_t*>(dst) = H::pack(a[h].o[0] * inv, a[h].o[1] * inv);
+            for (int e = 0; e < kE; ++e) v[e] = part[warp + w][e][lane];
+            if (ml.x != kNegInf || ml.y != 0.0f) a.add(ml.x, ml.y, v);
         }
-        if (p.lse_out != nullptr && lane == 0)
-            p.lse_out[(long long)row * p.q_heads + head + h] = a[h].l == 0.0f ? kNegInf : a[h].m * kLn2 + logf(a[h].l);
     }
+    if (!exists) return;
+    const float inv = a.l > 0.0f ? 1.0f / a.l : (a.l == 0.0f ? 0.0f : a.l);
+    T* dst = reinterpret_cast<T*>(p.out) + row * p.out_stride + (long long)head * D + l * 8;
+#pragma unroll
+    for (int r = 0; r < kRuns; ++r) {
+        uint4 w;
+        w.x = H::pack(a.o[r * 8] * inv, a.o[r * 8 + 1] * inv);
+        w.y = H::pack(a.o[r * 8 + 2] * inv, a.o[r * 8 + 3] * inv);
+        w.z = H::pack(a.o[r * 8 + 4] * inv, a.o[r * 8 + 5] * inv);
+        w.w = H::pack(a.o[r * 8 + 6] * inv, a.o[r * 8 + 7] * inv);
+        *reinterpret_cast<uint4*>(dst + r * 64) = w;
+    }
+    if (p.lse_out != nullptr && l == 0) p.lse_out[(long long)row * p.q_heads + head] = a.l == 0.0f ? kNegInf : a.m * kLn2 + logf(a.l);
 }
 
 template <int D>
@@ -1187,11 +1100,10 @@ cudaError_t launch(const AttendParams& p, const CUtensorMap& k_map, const CUtens
     lp_attend_kernel<kBf16, D><<<p.grid, kThreads, smem_bytes<D>(), stream>>>(p, k_map, v_map);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    // Few rows: a warp per head, several for its parts (a short call waits on one chain of loads after another); many:
-    // four heads per warp, for more loads in flight beside them.
-    const long long heads = (long long)p.rows * p.q_heads;
-    const int sub = heads <= 8 * p.grid ? 8 : (heads <= 16 * p.grid ? 2 : 1), per = sub > 1 ? 1 : 4;
-    const int chunks = (p.share + per - 1) / per * p.kv_heads;
+    // few rows: several warps share a row's parts
+    const int chunks = (p.q_heads + 3) / 4;
+    const long long warps = (long long)p.rows * chunks;
+    const int sub = warps <= 4 * p.grid ? 8 : (warps <= 16 * p.grid ? 2 : 1);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1201,9 +1113,9 @@ cudaError_t launch(const AttendParams& p, const CUtensorMap& k_map, const CUtens
     lc.stream = stream;
     lc.attrs = attr;
     lc.numAttrs = 1;
-    if (sub == 8) return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 8, 1>, p);
-    if (sub == 2) return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 2, 1>, p);
-    return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 1, 4>, p);
+    if (sub == 8) return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 8>, p);
+    if (sub == 2) return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 2>, p);
+    return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 1>, p);
 }
 
 }  // namespace

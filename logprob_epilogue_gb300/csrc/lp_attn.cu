@@ -64,7 +64,7 @@ int check_desc(const lp_attn_desc* d) {
 }
 
 struct Layout {
-    size_t seg_tiles, seg_units, part_o, part_ml, total;
+    size_t seg_units, units, part_o, part_ml, total;
     long long prefix_slots, group_slots;
     int group_rows;
 };
@@ -81,10 +81,10 @@ Layout layout_of(const lp_attn_desc* d, int grid) {
     const size_t segs = (size_t)d->max_prefixes + (size_t)d->max_groups;
     const size_t part_rows = 2 * ((size_t)L.prefix_slots * lp::kQTile + (size_t)L.group_slots * (size_t)L.group_rows);
     size_t off = 0;
-    L.seg_tiles = off;
-    off = lp::align_up(off + (segs + 2) * 8);
     L.seg_units = off;
     off = lp::align_up(off + segs * 8);
+    L.units = off;
+    off = lp::align_up(off + (size_t)(L.prefix_slots + L.group_slots) * 8);
     L.part_ml = off;
     off = lp::align_up(off + part_rows * 8);
     L.part_o = off;
@@ -210,8 +210,8 @@ int lp_attn_create(lp_attn_t* out, const lp_attn_desc* desc) {
         delete plan;
         return cuda_fail(e);
     }
-    plan->sc.seg_tiles = reinterpret_cast<unsigned long long*>(plan->scratch + L.seg_tiles);
     plan->sc.seg_units = reinterpret_cast<int2*>(plan->scratch + L.seg_units);
+    plan->sc.units = reinterpret_cast<int2*>(plan->scratch + L.units);
     plan->sc.part_ml = reinterpret_cast<float2*>(plan->scratch + L.part_ml);
     plan->sc.part_o = reinterpret_cast<float*>(plan->scratch + L.part_o);
     plan->sc.prefix_slots = L.prefix_slots;

@@ -38,9 +38,9 @@ constexpr int kKTile = 128;    // tokens of one tile
 // a unit is at most two tiles of its query rows for one key-value head; a
 // piece is the run of a unit's token tiles that one block takes.
 struct AttendScratch {
-    unsigned long long* seg_tiles;  // [P + G + 2] cost of the tiles before the segment, among prefixes or among groups,
-                                    // of units that are not dealt out whole; then both totals
-    int2* seg_units;                // [P + G] slots before it, of those units and of those that are
+    int2* seg_units;                // [P + G] units before the segment, of those that are cut into pieces and of those that
+                                    // go round the blocks whole
+    int2* units;                    // of prefixes, then of groups: a cut unit's first slot and its pieces
     float* part_o;                  // pieces of prefixes, then of groups: unnormalised results [2][rows][D]
     float2* part_ml;                // (maximum in base 2, sum) [2][rows]
     long long prefix_slots, group_slots;
