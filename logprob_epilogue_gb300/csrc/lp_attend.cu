@@ -40,6 +40,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "lp_attn.h"
 #include "lp_tc.h"
 
@@ -54,6 +56,10 @@ constexpr int kThreads = 384;
 constexpr int kWarps = kThreads / 32;
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
+// Tokens of a tile whose probabilities are announced before the others', so that
+// their part of P V runs under the rest of the softmax (2,048 rows behind 32,768
+// tokens: 810 us; 32 tokens 851, 96 838, all at once 876).
+constexpr int kEarly = 64;
 constexpr float kRescale = 8.0f;  // growth of the maximum (log2) that moves it
 // What a run is measured in: a token tile of a one-tile unit is 2, of a two-tile
 // unit 3, and every unit 4 more (its queries, first loads and results).  No run
@@ -300,7 +306,7 @@ constexpr int kPieceReaders = 11; // warps that read each: two of the products, 
 struct Ctl {
     uint64_t full[10], empty[10], piece_full[kPieces], piece_empty[kPieces];
     Piece piece[kPieces];
-    uint64_t q_full[2], q_free[2], s_full[2], p_ready[2], pv_done[2], o_free[2], q_grant, clean, drain;
+    uint64_t q_full[2], q_free[2], s_full[2], p_early[2], p_ready[2], pv_done[2], o_free[2], q_grant, clean, drain;
     unsigned long long sum[kWarps][3];
     int sum_dealt[kWarps], deal_first, deal_last;
     Start start[2];
@@ -454,23 +460,34 @@ __device__ __forceinline__ float max32(const uint32_t (&r)[32], float top) {
     return fmaxf(a, b);
 }
 
+// The scores of tokens from `valid` on to -infinity, in tensor memory: short
+// code, since a call comes here once per unit (see the loop below).
+__device__ __forceinline__ void mask_scores(uint32_t s_col, int valid) {
+#pragma unroll 1
+    for (int b = valid & ~15; b < kKTile; b += 16) {
+        uint32_t r[16];
+        tc::tmem_ld16(s_col + b, r);
+        tc::wait_ld();
+        tc::tie(r);
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            if (b + e >= valid) r[e] = __float_as_uint(kNegInf);
+        tc::tmem_st16(s_col + b, r);
+    }
+    tc::wait_st();
+}
+
 // Softmax of one score tile by one warp, a row per thread; `valid` of the 128
 // tokens exist.  Writes the row's probabilities over the scores.
 template <bool kBf16, int D>
-__device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, int valid, bool first, bool used, float c, Row& row) {
+__device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, int valid, bool first, bool used, float c, Row& row, uint64_t* early) {
+    if (valid < kKTile) mask_scores(s_col, valid);
     uint32_t r[4][32];
 #pragma unroll
     for (int b = 0; b < 4; ++b) tc::tmem_ld32(s_col + b * 32, r[b]);
     tc::wait_ld();
 #pragma unroll
     for (int b = 0; b < 4; ++b) tc::tie(r[b]);
-    if (valid < kKTile) {
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-                if (b * 32 + e >= valid) r[b][e] = __float_as_uint(kNegInf);
-    }
     float top = kNegInf, f;
 #pragma unroll
     for (int b = 0; b < 4; ++b) top = max32(r[b], top);
@@ -491,6 +508,12 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, int
             w[e] = Half<kBf16>::pack(x, y);
         }
         tc::tmem_st16(s_col + b * 16, w);
+        if (b == kEarly / 32 - 1) {  // the products of the tile's first tokens may begin
+            tc::wait_st();
+            tc::fence_before();
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) tc::mbar_arrive(early);
+        }
     }
     float x, y;
     unpack2(add2(sum[0], sum[1]), x, y);
@@ -498,16 +521,26 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, int
     tc::wait_st();
 }
 
+// Where the second warpgroup's copy of a one-tile unit's rows begins in the
+// query tile: half of a tile that is at most half full is free, and there the
+// rows are in tensor memory lanes of other warps, on other schedulers, than the
+// first warpgroup's.
+__device__ __forceinline__ int second_at(int rows) { return rows <= kQTile / 2 ? kQTile / 2 : 0; }
+
 // The rows' heads into a query tile (128-byte swizzle) by `n` threads, visible
-// to the tensor core.  Tile rows past the last hold anything and reach nothing.
+// to the tensor core; `again` > 0: a second time from that tile row on.  Tile
+// rows without a query hold anything and reach nothing.
 template <typename T, int D>
-__device__ __forceinline__ void load_queries(const AttendParams& p, int row0, int rows, int kvh, uint32_t dst, int t, int n) {
+__device__ __forceinline__ void load_queries(const AttendParams& p, int row0, int rows, int kvh, uint32_t dst, int again, int t, int n) {
     constexpr int kChunks = D / 8;
     const T* src = reinterpret_cast<const T*>(p.q) + (long long)row0 * p.q_stride + (long long)kvh * p.share * D;
     for (int i = t; i < rows * p.share * kChunks; i += n) {
         const int row = i / kChunks, ch = i % kChunks;
         const int per = (row * p.share_inv) >> 16, head = row - per * p.share;
-        tc::copy16(dst + (ch >> 3) * (kQTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4), src + per * p.q_stride + head * D + ch * 8);
+        const uint32_t at = dst + (ch >> 3) * (kQTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+        const T* from = src + per * p.q_stride + head * D + ch * 8;
+        tc::copy16(at, from);
+        if (again > 0) tc::copy16(at + again * 128, from);
     }
     tc::copies_done();
     tc::fence_async_shared();
@@ -539,6 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mbar_init(&ctl->q_full[i], 4);
             tc::mbar_init(&ctl->q_free[i], 2);
             tc::mbar_init(&ctl->s_full[i], 1);
+            tc::mbar_init(&ctl->p_early[i], 4);
             tc::mbar_init(&ctl->p_ready[i], 4);
             tc::mbar_init(&ctl->pv_done[i], 1);
             tc::mbar_init(&ctl->o_free[i], 4);
@@ -585,9 +619,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         int turn = 0;
         while (ok && next_piece()) {
             const bool two = x.rows > p.rows_per_tile;
-            const int n = x.tiles, rt = p.rows_per_tile, row = quarter * 32 + lane;  // row of the query tile
+            const int n = x.tiles, rt = p.rows_per_tile;
             const int valid_rows = (two ? (wg == 0 ? rt : x.rows - rt) : x.rows) * p.share;
-            const bool live = quarter * 32 < valid_rows;  // any row of this warp
+            const int row0 = quarter * 32 - (wg == 1 && !two ? second_at(valid_rows) : 0), row = row0 + lane;  // of the query tile
+            const bool live = row0 >= 0 && row0 < valid_rows, used = live && row < valid_rows;  // any row of this warp; this row
             const int first = two ? 0 : wg ^ turn, stride = two ? 1 : 2;
             if (!two) turn ^= n & 1;
             if (two) {
@@ -595,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 grant ^= 1u;
                 const uint32_t b = (q_pos + wg) & 1u;
-                load_queries<T, D>(p, x.row + wg * rt, wg == 0 ? rt : x.rows - rt, x.kvh, tc::smem_addr(smem + b * C::kTileBytes), tid & 127, 128);
+                load_queries<T, D>(p, x.row + wg * rt, wg == 0 ? rt : x.rows - rt, x.kvh, tc::smem_addr(smem + b * C::kTileBytes), 0, tid & 127, 128);
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&ctl->q_full[b], 1);
             }
@@ -611,16 +646,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (live) {
                     tc::fence_after();
-                    softmax_tile<kBf16, D>(s_col, o_col, x.left - i * kKTile, i == first, row < valid_rows, c, st);
+                    softmax_tile<kBf16, D>(s_col, o_col, x.left - i * kKTile, i == first, used, c, st, &ctl->p_early[wg]);
                     tc::fence_before();
                     __syncwarp();
+                } else if (lane == 0) {
+                    tc::mbar_arrive(&ctl->p_early[wg]);
                 }
                 if (lane == 0) tc::mbar_arrive(&ctl->p_ready[wg]);
             }
             tile += n;
             if (!ok) break;
             const long long part = x.part + wg * x.part_stride;
-            const bool store = row < valid_rows && x.part >= 0;
+            const bool store = used && x.part >= 0;
             if (first >= n) {  // no tile of this piece was this warpgroup's
                 if (store) p.sc.part_ml[part + row] = make_float2(kNegInf, 0.0f);
                 continue;
@@ -730,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t q_desc = tc::make_desc(tc::smem_addr(smem), 16, 1024);
             const uint64_t k_desc = tc::make_desc(tc::smem_addr(ring), 16, 1024), v_desc = tc::make_desc(tc::smem_addr(ring), kKTile * 128, 1024);
             const uint32_t tm = __shfl_sync(kFull, tmem, 0), s_t = tm + kColS + s * kColStep, o_t = tm + kColO + s * kColStep;
-            uint64_t *s_full = &ctl->s_full[s], *p_ready = &ctl->p_ready[s], *pv_done = &ctl->pv_done[s], *o_free = &ctl->o_free[s];
+            uint64_t *s_full = &ctl->s_full[s], *p_early = &ctl->p_early[s], *p_ready = &ctl->p_ready[s], *pv_done = &ctl->pv_done[s], *o_free = &ctl->o_free[s];
             uint32_t q_pos = 0, pos = 0, slot = 0, phase = 0, p_phase = 0, o_phase = 1, clean_phase = 0;  // pos, slot, phase: the next ring position
             uint32_t batch = 0;
             int turn = 0;  // whose the next tile of a one-tile unit is
@@ -793,14 +830,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 return true;
             };
-            auto values = [&](uint32_t v_slot, int have, bool first) {  // O += P V
+            auto values = [&](uint32_t v_slot, int have, bool first, auto early) {  // O += P V, of the tile's first tokens or of the rest
+                constexpr bool kFirst = decltype(early)::value;
+                constexpr int kFrom = kFirst ? 0 : kEarly / 16, kTo = kFirst ? kEarly / 16 : kKTile / 16;
                 const uint64_t b = v_desc + v_slot * kTileStep;
-                if (have > kKTile - 16) {
+                if (have > kTo * 16 - 16) {
 #pragma unroll
-                    for (int k = 0; k < kKTile / 16; ++k) tc::mma_ts(o_t, s_t + k * 8, b + (uint64_t)(k * 2048 >> 4), kIdescO, k > 0 || !first, one);
+                    for (int k = kFrom; k < kTo; ++k) tc::mma_ts(o_t, s_t + k * 8, b + (uint64_t)(k * 2048 >> 4), kIdescO, k > 0 || !first, one);
                 } else {
 #pragma unroll 1
-                    for (int k = 0; k < (have + 15) >> 4; ++k) tc::mma_ts(o_t, s_t + k * 8, b + (uint64_t)(k * 2048 >> 4), kIdescO, k > 0 || !first, one);
+                    for (int k = kFrom; k < (have + 15) >> 4; ++k) tc::mma_ts(o_t, s_t + k * 8, b + (uint64_t)(k * 2048 >> 4), kIdescO, k > 0 || !first, one);
                 }
             };
             while (ok && next_piece()) {
@@ -832,11 +871,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!two && i + 1 < tiles) advance(), advance();
                         k_slot = slot;
                         ok = ready(v_pos, v_slot, v_phase, left, i == skip, two) && (!two || last || wait_fill(pos, slot, phase, two)) &&
-                             wait(p_ready, p_phase) && (!two || take_turn());
+                             wait(p_early, p_phase) && (!two || take_turn());
+                        if (!ok) break;
+                        tc::fence_after();
+                        values(v_slot, left, i == skip, std::true_type());
+                        ok = wait(p_ready, p_phase);
                         p_phase ^= 1u;
                         if (!ok) break;
                         tc::fence_after();
-                        values(v_slot, left, i == skip);
+                        values(v_slot, left, i == skip, std::false_type());
                         if (two) {
                             // P V and the next Q K^T without a pause
                             if (!last) scores(a, k_slot);
@@ -885,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     continue;
                 }
                 const uint32_t b = q_pos & 1u;
-                load_queries<T, D>(p, x.row, x.rows, x.kvh, tc::smem_addr(smem + b * C::kTileBytes), lane, 32);
+                load_queries<T, D>(p, x.row, x.rows, x.kvh, tc::smem_addr(smem + b * C::kTileBytes), second_at(x.rows * p.share), lane, 32);
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&ctl->q_full[b], 4);
                 ++q_pos;
