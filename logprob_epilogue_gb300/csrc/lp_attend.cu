@@ -970,46 +970,52 @@ __device__ __forceinline__ void widen8(const uint4& w, float* x) {
     x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y, x[4] = c.x, x[5] = c.y, x[6] = d.x, x[7] = d.y;
 }
 
-// Where the parts of a row's head lie, for one segment.
+// The parts of a row's head from one segment: what the call's arguments say,
+// and after the main kernel what its tables say.
 struct Parts {
+    int seg, unit, dealt;     // seg: -1 for none; of all heads' units
     int row, cap, set, sets;  // row of the unit; the parts of a piece that are its: sets of them from `set` on
     int count;
     long long slot;
-};
-
-__device__ __forceinline__ Parts locate(const AttendParams& p, int seg, int rel, int head) {
-    Parts x;
-    x.count = 0;
-    const Seg s = load_seg(p, seg);
-    if (s.tiles == 0) return x;
-    const bool prefix = seg < p.P;
-    const int2 base = p.sc.seg_units[seg];
-    const int rt = p.rows_per_tile, u = rel / (2 * rt), in = rel - u * 2 * rt, kvh = head / p.share, unit = kvh * s.units + u;
-    const bool two = s.n - u * 2 * rt > rt;
-    x.set = two && in >= rt ? 1 : 0;
-    x.sets = two ? 1 : 2;  // a unit of one tile: a part of each warpgroup
-    x.row = (in - x.set * rt) * p.share + head - kvh * p.share;
-    x.cap = prefix ? kQTile : p.sc.group_rows;
-    int pieces = 1;
-    if (unit < s.dealt) {
-        x.slot = (long long)base.y + unit;
-    } else {
-        const long long at = unit_index(p, prefix, base.x + unit - s.dealt);
-        const int2 e = at >= 0 ? p.sc.units[at] : make_int2(0, 0);
-        x.slot = e.x;
-        pieces = e.y;
+    __device__ __forceinline__ void find(const AttendParams& p, int segment, int rel, int head) {
+        seg = -1;
+        if (segment < 0) return;
+        const Seg s = load_seg(p, segment);
+        if (s.tiles == 0) return;
+        seg = segment;
+        const int rt = p.rows_per_tile, u = rel / (2 * rt), in = rel - u * 2 * rt, kvh = head / p.share;
+        const bool two = s.n - u * 2 * rt > rt;
+        unit = kvh * s.units + u;
+        dealt = s.dealt;
+        set = two && in >= rt ? 1 : 0;
+        sets = two ? 1 : 2;  // a unit of one tile: a part of each warpgroup
+        row = (in - set * rt) * p.share + head - kvh * p.share;
+        cap = segment < p.P ? kQTile : p.sc.group_rows;
     }
-    x.count = pieces * x.sets;
-    return x;
-}
+    __device__ __forceinline__ int2 first_slots(const AttendParams& p) const { return seg >= 0 ? p.sc.seg_units[seg] : make_int2(0, 0); }
+    __device__ __forceinline__ void locate(const AttendParams& p, int2 base) {
+        slot = (long long)base.y + unit;
+        int pieces = seg >= 0 ? 1 : 0;
+        if (pieces != 0 && unit >= dealt) {
+            const long long at = unit_index(p, seg < p.P, base.x + unit - dealt);
+            const int2 e = at >= 0 ? p.sc.units[at] : make_int2(0, 0);
+            slot = e.x;
+            pieces = e.y;
+        }
+        count = pieces * sets;
+    }
+    __device__ __forceinline__ long long part(const AttendParams& p, int k) const {
+        return part_row(p, seg < p.P, slot + (sets == 1 ? k : k >> 1), sets == 1 ? set : k & 1);
+    }
+};
 
 // kSub warps per row and four heads: the round's own tokens that the row sees,
 // then the parts of the row's prefix and of its group's committed tokens.
 template <bool kBf16, int D, int kSub>
-__global__ void __launch_bounds__(kJoinThreads, kSub == 1 ? 3 : 2) lp_attend_join_kernel(const AttendParams p) {
+__global__ void __launch_bounds__(kJoinThreads, kSub > 2 ? 2 : 3) lp_attend_join_kernel(const AttendParams p) {
     using H = Half<kBf16>;
     using T = typename H::T;
-    constexpr int kE = D / 8, kRuns = D / 64, kBatch = kSub > 1 ? 4 : 2;  // parts in flight per thread
+    constexpr int kE = D / 8, kRuns = D / 64, kBatch = kSub > 2 ? 4 : 2;  // parts in flight per thread
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % kSub, l = lane & 7;
     const int row = blockIdx.x, head = (blockIdx.y * (kJoinWarps / kSub) + warp / kSub) * 4 + (lane >> 3);
     const int g = block_find_group(p.indptr, p.G, row);
@@ -1061,41 +1067,42 @@ __global__ void __launch_bounds__(kJoinThreads, kSub == 1 ? 3 : 2) lp_attend_joi
             a.add(s * c, 1.0f, v);
         }
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    Parts shared, own;  // of the first prefix that serves the row, of its group's committed tokens
+    int prefix = -1, first = 0;
     if (grp.n > 0) {
+        for (int i = 0; i < p.P && prefix < 0; ++i) {
+            const Prefix x = load_prefix(p, i);
+            if (!x.bad && g >= x.g0 && g < x.g1) prefix = i, first = x.r0;
+        }
+    }
+    shared.find(p, prefix, row - first, exists ? head : 0);
+    own.find(p, grp.n > 0 ? p.P + g : -1, row - grp.r0, exists ? head : 0);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int2 shared_at = shared.first_slots(p), own_at = own.first_slots(p);
+    shared.locate(p, shared_at);
+    own.locate(p, own_at);
 #pragma unroll 1
-        for (int i = 0; i <= p.P; ++i) {  // the row's prefix, then its group
-            int seg = p.P + g, first = grp.r0;
-            if (i < p.P) {
-                const Prefix x = load_prefix(p, i);
-                if (x.bad || g < x.g0 || g >= x.g1) continue;
-                seg = i, first = x.r0;
-                i = p.P - 1;  // the first that serves it
-            }
-            const Parts x = locate(p, seg, row - first, exists ? head : 0);
-            const bool prefix = seg < p.P;
-#pragma unroll 1
-            for (int k0 = sub; __any_sync(kFull, k0 < x.count); k0 += kSub * kBatch) {
-                float2 ml[kBatch];
-                float v[kBatch][kE];
+    for (int k0 = sub; __any_sync(kFull, k0 < shared.count + own.count); k0 += kSub * kBatch) {
+        float2 ml[kBatch];
+        float v[kBatch][kE];
 #pragma unroll
-                for (int b = 0; b < kBatch; ++b) {
-                    const int k = k0 + b * kSub;
-                    const long long base = k < x.count ? part_row(p, prefix, x.slot + (x.sets == 1 ? k : k >> 1), x.sets == 1 ? x.set : k & 1) : -1;
-                    ml[b] = base >= 0 ? p.sc.part_ml[base + x.row] : make_float2(kNegInf, 0.0f);
-                    const float4* src = reinterpret_cast<const float4*>(p.sc.part_o) + part_chunk<D>(base >= 0 ? base : 0, x.cap, x.row, 2 * l);
+        for (int b = 0; b < kBatch; ++b) {
+            const int k = k0 + b * kSub;
+            const bool is_own = k >= shared.count;
+            const int row_at = is_own ? own.row : shared.row, cap = is_own ? own.cap : shared.cap;
+            const long long base = k >= shared.count + own.count ? -1 : (is_own ? own.part(p, k - shared.count) : shared.part(p, k));
+            ml[b] = base >= 0 ? p.sc.part_ml[base + row_at] : make_float2(kNegInf, 0.0f);
+            const float4* src = reinterpret_cast<const float4*>(p.sc.part_o) + part_chunk<D>(base >= 0 ? base : 0, cap, row_at, 2 * l);
 #pragma unroll
-                    for (int r = 0; r < kRuns * 2; ++r) {
-                        float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        if (base >= 0) w = src[(r / 2 * 16 + (r & 1)) * x.cap];
-                        v[b][4 * r] = w.x, v[b][4 * r + 1] = w.y, v[b][4 * r + 2] = w.z, v[b][4 * r + 3] = w.w;
-                    }
-                }
-#pragma unroll
-                for (int b = 0; b < kBatch; ++b)
-                    if (ml[b].x != kNegInf || ml[b].y != 0.0f) a.add(ml[b].x, ml[b].y, v[b]);  // else nothing was written
+            for (int r = 0; r < kRuns * 2; ++r) {
+                float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (base >= 0) w = src[(r / 2 * 16 + (r & 1)) * cap];
+                v[b][4 * r] = w.x, v[b][4 * r + 1] = w.y, v[b][4 * r + 2] = w.z, v[b][4 * r + 3] = w.w;
             }
         }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+            if (ml[b].x != kNegInf || ml[b].y != 0.0f) a.add(ml[b].x, ml[b].y, v[b]);  // else nothing was written
     }
     if constexpr (kSub > 1) {  // the warps' sums, in the order of the warps
         __shared__ float part[kJoinWarps][kE][32];
@@ -1146,7 +1153,7 @@ cudaError_t launch(const AttendParams& p, const CUtensorMap& k_map, const CUtens
     // few rows: several warps share a row's parts
     const int chunks = (p.q_heads + 3) / 4;
     const long long warps = (long long)p.rows * chunks;
-    const int sub = warps <= 4 * p.grid ? 8 : (warps <= 16 * p.grid ? 2 : 1);
+    const int sub = warps <= 2 * p.grid ? 8 : (warps <= 4 * p.grid ? 4 : (warps <= 16 * p.grid ? 2 : 1));
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1157,6 +1164,7 @@ cudaError_t launch(const AttendParams& p, const CUtensorMap& k_map, const CUtens
     lc.attrs = attr;
     lc.numAttrs = 1;
     if (sub == 8) return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 8>, p);
+    if (sub == 4) return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 4>, p);
     if (sub == 2) return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 2>, p);
     return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 1>, p);
 }
