@@ -109,6 +109,9 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
 }
 
 // Waits for this thread's copies.
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Orders this thread's shared-memory writes before later TMA and tensor-core accesses.
