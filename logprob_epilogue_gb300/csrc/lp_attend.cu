@@ -559,33 +559,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = __shfl_sync(kFull, tid >> 5, 0);  // the same for the warp, as the compiler sees
     asm volatile("griddepcontrol.launch_dependents;");  // the join waits for this grid's end by itself
     const unsigned long long limit = p.timeout_ns;
-    Runs runs[2];  // of prefixes, of groups
-    if (!plan_run(p, ctl, runs)) return;
-
-    if (tid == 0) {
-        for (int i = 0; i < C::kSlots; ++i) tc::mbar_init(&ctl->full[i], 1), tc::mbar_init(&ctl->empty[i], 2);
-        tc::mbar_init(&ctl->clean, 1);
-        tc::mbar_init(&ctl->q_grant, 1);
-        tc::mbar_init(&ctl->drain, 2);
-        for (int i = 0; i < kPieces; ++i) tc::mbar_init(&ctl->piece_full[i], 1), tc::mbar_init(&ctl->piece_empty[i], kPieceReaders);
-        for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&ctl->q_full[i], 4);
-            tc::mbar_init(&ctl->q_free[i], 2);
-            tc::mbar_init(&ctl->s_full[i], 1);
-            tc::mbar_init(&ctl->p_early[i], 4);
-            tc::mbar_init(&ctl->p_ready[i], 4);
-            tc::mbar_init(&ctl->pv_done[i], 1);
-            tc::mbar_init(&ctl->o_free[i], 4);
+    // barriers and tensor memory while the other warps look through the segments
+    if (warp == kWarps - 1) {
+        if (lane < C::kSlots) tc::mbar_init(&ctl->full[lane], 1), tc::mbar_init(&ctl->empty[lane], 2);
+        if (lane < kPieces) tc::mbar_init(&ctl->piece_full[lane], 1), tc::mbar_init(&ctl->piece_empty[lane], kPieceReaders);
+        if (lane < 2) {
+            tc::mbar_init(&ctl->q_full[lane], 4);
+            tc::mbar_init(&ctl->q_free[lane], 2);
+            tc::mbar_init(&ctl->s_full[lane], 1);
+            tc::mbar_init(&ctl->p_early[lane], 4);
+            tc::mbar_init(&ctl->p_ready[lane], 4);
+            tc::mbar_init(&ctl->pv_done[lane], 1);
+            tc::mbar_init(&ctl->o_free[lane], 4);
+            ctl->batches[lane] = 0;
         }
-        ctl->abort = 0;
-        ctl->issued = ctl->batches[0] = ctl->batches[1] = 0;
+        if (lane == 0) {
+            tc::mbar_init(&ctl->clean, 1);
+            tc::mbar_init(&ctl->q_grant, 1);
+            tc::mbar_init(&ctl->drain, 2);
+            ctl->abort = 0;
+            ctl->issued = 0;
+        }
         tc::fence_async_shared();
     }
     if (warp == 2) tc::tmem_alloc(&ctl->tmem, kTmemCols);
+    Runs runs[2];  // of prefixes, of groups
+    const bool any = plan_run(p, ctl, runs);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = ctl->tmem;
+    if (!any) {
+        if (warp == 2) tc::tmem_dealloc(tmem, kTmemCols);
+        return;
+    }
     volatile int* abort = &ctl->abort;
     // test hook: nothing arrives on `drain` before the end, so this wait runs out
     if (p.force_timeout) tc::warp_wait(&ctl->drain, 0, limit, abort);
