@@ -1064,39 +1064,38 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
         const unsigned here = __ballot_sync(kFull, page >= 0 && page < p.num_pages);
         unsigned todo = mask & (grp.n < 32 ? (1u << grp.n) - 1u : kFull);
         if (lane == 0 && (todo & ~here) != 0u) atomicOr(p.status, kStatusBadPage);
-        int turn = 0;
-        while (todo != 0u) {
-            int n = 0;
+        if (kSub > 1) todo &= kFull / ((1u << kSub) - 1u) << sub;  // every kSub-th is this warp's
+        const int n = __popc(todo);
 #pragma unroll 1
-            for (; todo != 0u && n < kRound; todo &= todo - 1u, ++turn) {
-                if (kSub > 1 && turn % kSub != sub) continue;
+        for (int j = 0, slot = 0; j < n + kRound - 1; ++j) {
+            if (j < n) {
                 const int i = __ffs(todo) - 1, t = grp.len + i;
+                todo &= todo - 1u;
                 const long long pg = __shfl_sync(kFull, page, i);
                 const long long at = ((((pg * p.kv_heads + kvh) << p.page_shift) + (t & ((1 << p.page_shift) - 1))) * D) + l * 8;
 #pragma unroll
                 for (int r = 0; r < kRuns; ++r) {
                     if (here >> i & 1u) {
-                        tc::copy16(tc::smem_addr(&staged(n, r)), reinterpret_cast<const T*>(p.k_cache) + at + r * 64);
-                        tc::copy16(tc::smem_addr(&staged(n, kRuns + r)), reinterpret_cast<const T*>(p.v_cache) + at + r * 64);
+                        tc::copy16(tc::smem_addr(&staged(slot, r)), reinterpret_cast<const T*>(p.k_cache) + at + r * 64);
+                        tc::copy16(tc::smem_addr(&staged(slot, kRuns + r)), reinterpret_cast<const T*>(p.v_cache) + at + r * 64);
                     } else {
-                        staged(n, r) = staged(n, kRuns + r) = make_uint4(0, 0, 0, 0);
+                        staged(slot, r) = staged(slot, kRuns + r) = make_uint4(0, 0, 0, 0);
                     }
                 }
-                ++n;
             }
-            tc::copies_done();
-#pragma unroll 1
-            for (int b = 0; b < n; ++b) {
-                float k[kE], v[kE];
+            tc::copies_commit();
+            slot = slot == kRound - 1 ? 0 : slot + 1;
+            if (j < kRound - 1) continue;
+            tc::copies_wait<kRound - 1>();  // slot: of the oldest
+            float k[kE], v[kE];
 #pragma unroll
-                for (int r = 0; r < kRuns; ++r) widen8<kBf16>(staged(b, r), k + r * 8), widen8<kBf16>(staged(b, kRuns + r), v + r * 8);
-                float s = 0.0f;
+            for (int r = 0; r < kRuns; ++r) widen8<kBf16>(staged(slot, r), k + r * 8), widen8<kBf16>(staged(slot, kRuns + r), v + r * 8);
+            float s = 0.0f;
 #pragma unroll
-                for (int e = 0; e < kE; ++e) s = fmaf(q[e], k[e], s);
+            for (int e = 0; e < kE; ++e) s = fmaf(q[e], k[e], s);
 #pragma unroll
-                for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-                a.add(s * c, 1.0f, v);
-            }
+            for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+            a.add(s * c, 1.0f, v);
         }
     }
     Parts shared, own;  // of the first prefix that serves the row, of its group's committed tokens
@@ -1113,37 +1112,36 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
     const int2 shared_at = shared.first_slots(p), own_at = own.first_slots(p);
     shared.locate(p, shared_at);
     own.locate(p, own_at);
-    const int count = shared.count + own.count;
-    for (int k0 = sub; k0 < count; k0 += kSub * kRound) {
-        const int n = min(kRound, (count - k0 + kSub - 1) / kSub);
+    const int count = shared.count + own.count, n = count > sub ? (count - sub + kSub - 1) / kSub : 0;
 #pragma unroll 1
-        for (int b = 0; b < n; ++b) {
-            const int k = k0 + b * kSub;
+    for (int j = 0, slot = 0; j < n + kRound - 1; ++j) {
+        if (j < n) {
+            const int k = sub + j * kSub;
             const bool is_own = k >= shared.count;
             const int row_at = is_own ? own.row : shared.row, cap = is_own ? own.cap : shared.cap;
             const long long base = is_own ? own.part(p, k - shared.count) : shared.part(p, k);
             if (base < 0) {
-                stage_ml[b * kJoinThreads] = make_float2(kNegInf, 0.0f);
-                continue;
-            }
-            tc::copy8(tc::smem_addr(&stage_ml[b * kJoinThreads]), p.sc.part_ml + base + row_at);
-            const float4* src = reinterpret_cast<const float4*>(p.sc.part_o) + part_chunk<D>(base, cap, row_at, 2 * l);
+                stage_ml[slot * kJoinThreads] = make_float2(kNegInf, 0.0f);
+            } else {
+                tc::copy8(tc::smem_addr(&stage_ml[slot * kJoinThreads]), p.sc.part_ml + base + row_at);
+                const float4* src = reinterpret_cast<const float4*>(p.sc.part_o) + part_chunk<D>(base, cap, row_at, 2 * l);
 #pragma unroll
-            for (int r = 0; r < kRuns * 2; ++r) tc::copy16(tc::smem_addr(&staged(b, r)), src + (r / 2 * 16 + (r & 1)) * cap);
-        }
-        tc::copies_done();
-#pragma unroll 1
-        for (int b = 0; b < n; ++b) {
-            const float2 ml = stage_ml[b * kJoinThreads];
-            if (ml.x == kNegInf && ml.y == 0.0f) continue;  // nothing was written
-            float v[kE];
-#pragma unroll
-            for (int r = 0; r < kRuns * 2; ++r) {
-                const uint4 w = staged(b, r);
-                v[4 * r] = __uint_as_float(w.x), v[4 * r + 1] = __uint_as_float(w.y), v[4 * r + 2] = __uint_as_float(w.z), v[4 * r + 3] = __uint_as_float(w.w);
+                for (int r = 0; r < kRuns * 2; ++r) tc::copy16(tc::smem_addr(&staged(slot, r)), src + (r / 2 * 16 + (r & 1)) * cap);
             }
-            a.add(ml.x, ml.y, v);
         }
+        tc::copies_commit();
+        slot = slot == kRound - 1 ? 0 : slot + 1;
+        if (j < kRound - 1) continue;
+        tc::copies_wait<kRound - 1>();
+        const float2 ml = stage_ml[slot * kJoinThreads];
+        if (ml.x == kNegInf && ml.y == 0.0f) continue;  // nothing was written
+        float v[kE];
+#pragma unroll
+        for (int r = 0; r < kRuns * 2; ++r) {
+            const uint4 w = staged(slot, r);
+            v[4 * r] = __uint_as_float(w.x), v[4 * r + 1] = __uint_as_float(w.y), v[4 * r + 2] = __uint_as_float(w.z), v[4 * r + 3] = __uint_as_float(w.w);
+        }
+        a.add(ml.x, ml.y, v);
     }
     if constexpr (kSub > 1) {  // the warps' sums, in the order of the warps
         float* part = reinterpret_cast<float*>(smem);  // [e][thread]; then the maxima and sums
