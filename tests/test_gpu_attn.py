@@ -1,6 +1,7 @@
 """The attention operators on the GPU against their 64-bit reference."""
 import ctypes
 import math
+import os
 
 import numpy as np
 import pytest
@@ -599,3 +600,24 @@ def test_attend_reports_a_wait_that_runs_out():
     _, _, st = c.run(c.plan(debug_force_timeout=True, timeout_ns=2_000_000))
     assert st == lpe.STATUS_TIMEOUT
     c.check()
+
+
+@pytest.mark.parametrize("hq,n", [(3, 21), (4, 16), (5, 13), (12, 8), (5, 25), (8, 16)])
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f16", 64)])
+def test_attend_query_tiles_about_half_and_quite_full(dtype, d, hq, n):
+    """63, 64, 65, 96, 125 and 128 (row, head) pairs of a group, at one token tile, two and several."""
+    Case(dtype=dtype, d=d, hq=hq, hk=1, n=[n] * 4, lens=[1, 129, 700, 300], page=32).check()
+
+
+def test_the_example_decodes_like_its_plain_form():
+    """Every emitted token has the largest logit of the plain form, to rounding: logits of magnitude at most 6 are rounded to
+    BF16 (2^-8 of it between two), their inputs and the hidden row before them to 2^-9 each, with sums of random signs."""
+    import importlib.util
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "verify_rounds.py")
+    spec = importlib.util.spec_from_file_location("verify_rounds", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    emitted, accepted, worst = example.main()
+    assert worst <= 0.1
+    assert all(len(e) == 1 + sum(a[g] + 1 for a in accepted) for g, e in enumerate(emitted))
+    assert any(a > 0 for r in accepted for a in r)
