@@ -28,14 +28,29 @@
 // unit of one tile gives its even token tiles to one warpgroup and its odd ones
 // to the other, each with its own maximum, sum and accumulator.
 //
-// Block: warp 0 fetches pages by TMA into a ring, warp 1 issues the MMAs,
-// warps 4-7 and 8-11 are two softmax warpgroups, one row per thread.
+// Block (one per SM, 12 warps): warp 0 splits the work and fetches pages by TMA
+// into a ring of K and V tiles (160 KiB); warps 1 and 2 issue the products, each
+// of one tensor tile; warp 3 loads the queries of one-tile units; warps 4-7 and
+// 8-11 are two softmax warpgroups, one row per thread.
 //   S_i = Q_i K^T    128 x 128, shared x shared -> tensor memory
 //   softmax: S_i to registers, P_i (the plan's type) back over S_i
-//   O_i += P_i V     tensor memory x shared -> tensor memory
+//   O_i += P_i V     tensor memory x shared -> tensor memory, the first 64
+//                    tokens' part while the softmax of the others runs
 // While one warpgroup works on its S the tensor core runs the other's
 // products.  The running maximum moves only when it grows by more than 2^8
 // (then O and the sum are rescaled), so most tiles touch O not at all.
+// P is rounded to the plan's type (the products take nothing wider); S, the
+// maxima, the sums, O and the parts are 32 bits.
+//
+// What bounds it, by size (BF16, heads of 128, 32 over 8, in a CUDA graph):
+// - bandwidth, where few rows share a token: 128 groups of 4 rows at contexts up
+//   to 8,192 take 347 us, 6.5 TB/s of keys and values;
+// - the tensor core, where many rows share a prefix: of 2,048 rows behind 32,768
+//   tokens the prefix's part takes 590 us, 1.86 PFLOP/s (2,670 cycles a pair of
+//   token tiles, the products alone 2,048).  The whole call takes 796 us: the
+//   groups' own tokens (0.5 GB) 105, the parts' join 70, the rest 30;
+// - latency, in short calls: one row at 4,095 tokens takes 19 us: the launch and
+//   the split 3, the first scores 2.5, two token tiles 4, the join 8.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -61,10 +76,10 @@ constexpr int kJoinWarps = kJoinThreads / 32;
 // tokens: 810 us; 32 tokens 851, 96 838, all at once 876).
 constexpr int kEarly = 64;
 constexpr float kRescale = 8.0f;  // growth of the maximum (log2) that moves it
-// What a run is measured in: a token tile of a one-tile unit is 2, of a two-tile
-// unit 3, and every unit 4 more (its queries, first loads and results).  No run
-// is shorter than a tile, nor one of prefixes than four (every run of a unit
-// leaves a part for the join to read).
+// What a run is measured in, by the times of each: a token tile of a one-tile
+// unit is 2, of a two-tile unit 3, and every unit 4 more (its queries, first
+// loads and results).  No run is shorter than a tile, nor one of prefixes than
+// four (every run of a unit leaves a part for the join to read).
 constexpr int kTileCost = 2, kPairCost = 3, kUnitCost = 4;
 constexpr int kLeastPrefix = 4 * kPairCost, kLeastGroup = kPairCost;
 // Registers: the softmax warpgroups hold 128 scores per thread.  The split's
