@@ -968,7 +968,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---- the join
 //
 // A warp has four query heads of a row, eight threads each: a thread holds
-// D / 8 lanes of its head, as D / 64 runs of eight.  What it reads (keys and
+// D / 8 lanes of its head, as D / 64 runs of eight.  Neighbouring threads have
+// neighbouring heads, which lie side by side in a part: an asynchronous copy
+// writes shared memory by runs that are contiguous on both sides (with a head's
+// threads side by side instead, one thread at a time: eight times the writes).  What it reads (keys and
 // values of the round's own tokens, then parts) comes by asynchronous copies
 // into shared memory of its own, several at a time, and is taken up by short
 // loops: a call's join runs once through its code, and unrolled loads and sums
@@ -1047,13 +1050,14 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
     using H = Half<kBf16>;
     using T = typename H::T;
     constexpr int kE = D / 8, kRuns = D / 64, kRound = join_round(kSub);
-    // what is on its way to a thread, 16 bytes of every thread side by side; only the thread itself reads it
+    // what is on its way to a warp, 16 bytes of every thread side by side
     extern __shared__ __align__(16) unsigned char smem[];
     uint4* stage = reinterpret_cast<uint4*>(smem) + threadIdx.x;
     float2* stage_ml = reinterpret_cast<float2*>(smem + kRound * 2 * kRuns * kJoinThreads * 16) + threadIdx.x;
+    auto place = [](int h, int c) { return h * 8 + (c ^ 2 * h); };
     auto staged = [&](int b, int c) -> uint4& { return stage[(b * 2 * kRuns + c) * kJoinThreads]; };
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % kSub, l = lane & 7;
-    const int row = blockIdx.x, head = (blockIdx.y * (kJoinWarps / kSub) + warp / kSub) * 4 + (lane >> 3);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % kSub, l = lane >> 2;
+    const int row = blockIdx.x, head = (blockIdx.y * (kJoinWarps / kSub) + warp / kSub) * 4 + (lane & 3);
     const int g = block_find_group(p.indptr, p.G, row);
     bool mine = g >= 0 && g < p.G;
     mine = mine && row >= __ldg(&p.indptr[g]) && row < __ldg(&p.indptr[g + 1]);  // else two entries claim the row
@@ -1064,7 +1068,6 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
 #pragma unroll
     for (int e = 0; e < kE; ++e) a.o[e] = 0.0f;
     a.m = kNegInf, a.l = 0.0f;
-    const int kvh = exists ? head / p.share : 0;
     if (grp.n > 0) {
         float q[kE];
 #pragma unroll
@@ -1081,20 +1084,25 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
         if (lane == 0 && (todo & ~here) != 0u) atomicOr(p.status, kStatusBadPage);
         if (kSub > 1) todo &= kFull / ((1u << kSub) - 1u) << sub;  // every kSub-th is this warp's
         const int n = __popc(todo);
+        // Keys and values lie side by side along a head, so here neighbouring threads copy along a head (to the places of the
+        // threads that read them, turned so that a read meets every bank once).
+        const int copy_head = head - (lane & 3) + (lane >> 3), copy_kvh = copy_head < p.q_heads ? copy_head / p.share : 0;
+        const int copy_to = place(lane >> 3, lane & 7) - lane, read_at = place(lane & 3, l) - lane;
 #pragma unroll 1
         for (int j = 0, slot = 0; j < n + kRound - 1; ++j) {
+            __syncwarp();
             if (j < n) {
                 const int i = __ffs(todo) - 1, t = grp.len + i;
                 todo &= todo - 1u;
                 const long long pg = __shfl_sync(kFull, page, i);
-                const long long at = ((((pg * p.kv_heads + kvh) << p.page_shift) + (t & ((1 << p.page_shift) - 1))) * D) + l * 8;
+                const long long at = ((((pg * p.kv_heads + copy_kvh) << p.page_shift) + (t & ((1 << p.page_shift) - 1))) * D) + (lane & 7) * 8;
 #pragma unroll
                 for (int r = 0; r < kRuns; ++r) {
                     if (here >> i & 1u) {
-                        tc::copy16(tc::smem_addr(&staged(slot, r)), reinterpret_cast<const T*>(p.k_cache) + at + r * 64);
-                        tc::copy16(tc::smem_addr(&staged(slot, kRuns + r)), reinterpret_cast<const T*>(p.v_cache) + at + r * 64);
+                        tc::copy16(tc::smem_addr(&staged(slot, r) + copy_to), reinterpret_cast<const T*>(p.k_cache) + at + r * 64);
+                        tc::copy16(tc::smem_addr(&staged(slot, kRuns + r) + copy_to), reinterpret_cast<const T*>(p.v_cache) + at + r * 64);
                     } else {
-                        staged(slot, r) = staged(slot, kRuns + r) = make_uint4(0, 0, 0, 0);
+                        (&staged(slot, r))[copy_to] = (&staged(slot, kRuns + r))[copy_to] = make_uint4(0, 0, 0, 0);
                     }
                 }
             }
@@ -1102,14 +1110,15 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
             slot = slot == kRound - 1 ? 0 : slot + 1;
             if (j < kRound - 1) continue;
             tc::copies_wait<kRound - 1>();  // slot: of the oldest
+            __syncwarp();
             float k[kE], v[kE];
 #pragma unroll
-            for (int r = 0; r < kRuns; ++r) widen8<kBf16>(staged(slot, r), k + r * 8), widen8<kBf16>(staged(slot, kRuns + r), v + r * 8);
+            for (int r = 0; r < kRuns; ++r) widen8<kBf16>((&staged(slot, r))[read_at], k + r * 8), widen8<kBf16>((&staged(slot, kRuns + r))[read_at], v + r * 8);
             float s = 0.0f;
 #pragma unroll
             for (int e = 0; e < kE; ++e) s = fmaf(q[e], k[e], s);
 #pragma unroll
-            for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+            for (int o = 16; o > 2; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
             a.add(s * c, 1.0f, v);
         }
     }
@@ -1123,6 +1132,7 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
     }
     shared.find(p, prefix, row - first, exists ? head : 0);
     own.find(p, grp.n > 0 ? p.P + g : -1, row - grp.r0, exists ? head : 0);
+    __syncwarp();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int2 shared_at = shared.first_slots(p), own_at = own.first_slots(p);
     shared.locate(p, shared_at);
