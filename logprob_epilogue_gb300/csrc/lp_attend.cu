@@ -790,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t k_desc = tc::make_desc(tc::smem_addr(ring), 16, 1024), v_desc = tc::make_desc(tc::smem_addr(ring), kKTile * 128, 1024);
             const uint32_t tm = __shfl_sync(kFull, tmem, 0), s_t = tm + kColS + s * kColStep, o_t = tm + kColO + s * kColStep;
             uint64_t *s_full = &ctl->s_full[s], *p_early = &ctl->p_early[s], *p_ready = &ctl->p_ready[s], *pv_done = &ctl->pv_done[s], *o_free = &ctl->o_free[s];
-            uint32_t q_pos = 0, pos = 0, slot = 0, phase = 0, p_phase = 0, o_phase = 1, clean_phase = 0;  // pos, slot, phase: the next ring position
+            uint32_t q_pos = 0, pos = 0, slot = 0, phase = 0, early_phase = 0, p_phase = 0, o_phase = 1, clean_phase = 0;  // pos, slot, phase: the next ring position
             uint32_t batch = 0;
             int turn = 0;  // whose the next tile of a one-tile unit is
             auto wait = [&](uint64_t* bar, uint32_t parity) { return tc::warp_wait(bar, parity, limit, abort); };
@@ -872,57 +872,74 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = wait(&ctl->q_full[q_pos & 1u], q_pos >> 1 & 1u) && (!two || wait(&ctl->q_full[(q_pos + 1) & 1u], (q_pos + 1) >> 1 & 1u));
                 const uint64_t a = q_desc + (q & 1u) * kTileStep;
                 int left = __shfl_sync(kFull, x.left, 0);
-                if (two || turn == s || tiles > 1) {
-                    // this warp's tiles: all of them, or every other one
-                    const int step = two ? 1 : 2, skip = two || turn == s ? 0 : 1;
-                    if (skip) advance(), advance(), left -= kKTile;
+                if (two) {
                     uint32_t k_slot = slot;
-                    ok = ok && wait_fill(pos, slot, phase, two) && (!two || take_turn());
+                    ok = ok && wait_fill(pos, slot, phase, true) && take_turn();
                     if (ok) {
                         tc::fence_after();
                         scores(a, k_slot);
-                        if (two) pass_turn();
+                        pass_turn();
                         tc::commit(s_full, one);
-                        release(&ctl->empty[k_slot], two);
+                        release(&ctl->empty[k_slot], true);
                     }
-                    for (int i = skip; ok && i < tiles; i += step, left -= step * kKTile) {
+                    for (int i = 0; ok && i < tiles; ++i, left -= kKTile) {
                         advance();
                         const uint32_t v_pos = pos, v_slot = slot, v_phase = phase;
                         advance();
-                        const bool last = i + step >= tiles;
-                        if (!two && i + 1 < tiles) advance(), advance();
+                        const bool last = i + 1 == tiles;
                         k_slot = slot;
-                        ok = ready(v_pos, v_slot, v_phase, left, i == skip, two) && (!two || last || wait_fill(pos, slot, phase, two)) &&
-                             wait(p_early, p_phase) && (!two || take_turn());
+                        ok = ready(v_pos, v_slot, v_phase, left, i == 0, true) && (last || wait_fill(pos, slot, phase, true)) &&
+                             wait(p_early, early_phase) && take_turn();
+                        early_phase ^= 1u;
                         if (!ok) break;
                         tc::fence_after();
-                        values(v_slot, left, i == skip, std::true_type());
+                        values(v_slot, left, i == 0, std::true_type());
                         ok = wait(p_ready, p_phase);
                         p_phase ^= 1u;
                         if (!ok) break;
                         tc::fence_after();
-                        values(v_slot, left, i == skip, std::false_type());
-                        if (two) {
-                            // P V and the next Q K^T without a pause
-                            if (!last) scores(a, k_slot);
-                            pass_turn();
-                            tc::commit(last ? pv_done : s_full, one);
-                            release(&ctl->empty[v_slot], two);
-                            if (!last) release(&ctl->empty[k_slot], two);
-                        } else {
-                            if (last) tc::commit(pv_done, one);
-                            release(&ctl->empty[v_slot], two);
-                            if (last) break;
-                            ok = wait_fill(pos, slot, phase, two);
-                            if (!ok) break;
-                            tc::fence_after();
-                            scores(a, k_slot);
-                            tc::commit(s_full, one);
-                            release(&ctl->empty[k_slot], two);
-                        }
+                        values(v_slot, left, i == 0, std::false_type());
+                        // P V and the next Q K^T without a pause
+                        if (!last) scores(a, k_slot);
+                        pass_turn();
+                        tc::commit(last ? pv_done : s_full, one);
+                        release(&ctl->empty[v_slot], true);
+                        if (!last) release(&ctl->empty[k_slot], true);
                     }
                 } else {
-                    advance(), advance();
+                    // every other tile is this warp's
+                    const uint32_t base = pos;
+                    const int mine = turn == s ? 0 : 1;
+                    auto score = [&](int t) {
+                        const uint32_t at = base + 2 * t, k_slot = at % C::kSlots;
+                        if (!wait_fill(at, k_slot, at / C::kSlots & 1u, false)) return false;
+                        tc::fence_after();
+                        scores(a, k_slot);
+                        tc::commit(s_full, one);
+                        release(&ctl->empty[k_slot], false);
+                        return true;
+                    };
+                    if (mine < tiles) ok = ok && score(mine);
+                    for (int t = mine; ok && t < tiles; t += 2) {
+                        const uint32_t v_pos = base + 2 * t + 1, v_slot = v_pos % C::kSlots;
+                        const int have = left - t * kKTile;
+                        ok = ready(v_pos, v_slot, v_pos / C::kSlots & 1u, have, t == mine, false) && wait(p_early, early_phase);
+                        early_phase ^= 1u;
+                        if (!ok) break;
+                        tc::fence_after();
+                        values(v_slot, have, t == mine, std::true_type());
+                        ok = wait(p_ready, p_phase);
+                        p_phase ^= 1u;
+                        if (!ok) break;
+                        tc::fence_after();
+                        values(v_slot, have, t == mine, std::false_type());
+                        const bool last = t + 2 >= tiles;
+                        if (last) tc::commit(pv_done, one);
+                        release(&ctl->empty[v_slot], false);
+                        if (!last) ok = score(t + 2);
+                    }
+                    pos = base + 2 * tiles;
+                    slot = pos % C::kSlots, phase = pos / C::kSlots & 1u;
                 }
                 if (!two) turn ^= tiles & 1;
                 if (ok) {
