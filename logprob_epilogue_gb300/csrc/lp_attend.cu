@@ -24,7 +24,7 @@
 // another.  Before that, a prefix with more units than blocks deals them out
 // whole, one to every block at a time: the blocks of a head then go through
 // its tokens side by side, and a tile that one of them fetched is still in L2
-// for the others.  A unit of two query tiles reads each K and V tile once for both; a
+// for the others (2,048 rows behind 32,768 tokens: 762 us against 870).  A unit of two query tiles reads each K and V tile once for both; a
 // unit of one tile gives its even token tiles to one warpgroup and its odd ones
 // to the other, each with its own maximum, sum and accumulator.
 //
@@ -44,13 +44,13 @@
 //
 // What bounds it, by size (BF16, heads of 128, 32 over 8, in a CUDA graph):
 // - bandwidth, where few rows share a token: 128 groups of 4 rows at contexts up
-//   to 8,192 take 347 us, 6.5 TB/s of keys and values;
+//   to 8,192 take 345 us, 6.5 TB/s of keys and values;
 // - the tensor core, where many rows share a prefix: of 2,048 rows behind 32,768
-//   tokens the prefix's part takes 590 us, 1.86 PFLOP/s (2,670 cycles a pair of
-//   token tiles, the products alone 2,048).  The whole call takes 796 us: the
-//   groups' own tokens (0.5 GB) 105, the parts' join 70, the rest 30;
-// - latency, in short calls: one row at 4,095 tokens takes 19 us: the launch and
-//   the split 3, the first scores 2.5, two token tiles 4, the join 8.
+//   tokens the prefix's part takes 595 us, 1.85 PFLOP/s (2,700 cycles a pair of
+//   token tiles, the products alone 2,048).  The whole call takes 760 us: then
+//   come the groups' own tokens (0.5 GB) in 125, and the parts' join in 40;
+// - latency, in short calls: one row at 4,095 tokens takes 15.5 us: the launch and
+//   the split 3, the first scores 2.5, two token tiles 4, the join 5.5.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -73,7 +73,7 @@ constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 // Tokens of a tile whose probabilities are announced before the others', so that
 // their part of P V runs under the rest of the softmax (2,048 rows behind 32,768
-// tokens: 810 us; 32 tokens 851, 96 838, all at once 876).
+// tokens: 762 us; 32 tokens 785, 96 790, all at once 809).
 constexpr int kEarly = 64;
 constexpr float kRescale = 8.0f;  // growth of the maximum (log2) that moves it
 // What a run is measured in, by the times of each: a token tile of a one-tile
@@ -539,7 +539,8 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, int
 // Where the second warpgroup's copy of a one-tile unit's rows begins in the
 // query tile: half of a tile that is at most half full is free, and there the
 // rows are in tensor memory lanes of other warps, on other schedulers, than the
-// first warpgroup's.
+// first warpgroup's (four groups past 100,000 tokens: 48.7 us against 52.9, trees
+// of drafts 43.6 against 44.6).
 __device__ __forceinline__ int second_at(int rows) { return rows <= kQTile / 2 ? kQTile / 2 : 0; }
 
 // The rows' heads into a query tile (128-byte swizzle) by `n` threads, visible
