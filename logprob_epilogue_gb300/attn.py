@@ -88,6 +88,7 @@ class AttnPlan:
         self._io = ctypes.create_string_buffer(max(_PACK_ROPE.size, _PACK_APPEND.size, _PACK_ATTEND.size))
         self._at = ctypes.addressof(self._io)
         self._q_heads, self._kv_heads, self._dim = int(d.q_heads), int(d.kv_heads), int(d.head_dim)
+        self._one_head = (self._dim,)
         self._cache_shape = (int(d.num_pages), int(d.kv_heads), int(d.page_size), int(d.head_dim))
         self._norm_rope, self._append, self._attend = lib().lp_norm_rope, lib().lp_kv_append, lib().lp_attend
 
@@ -107,35 +108,39 @@ class AttnPlan:
             return self._current(self.device)
         return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
-    def _rows(self, name, x, rows, heads):
-        """A [rows, heads, head_dim] tensor with dense heads: (pointer, row stride)."""
-        d = self._dim
+    def _rows(self, name, x, want):
+        """A tensor of shape ``want``, [rows, heads, head_dim], with dense heads: (pointer, row stride)."""
+        if x is not None and x.dtype is self._dtype and x.shape == want and x.get_device() == self.device:
+            s, t, u = x.stride()
+            rows, heads, d = want
+            if u == 1 and (t == d or heads == 1):
+                return x.data_ptr(), s if rows > 1 else heads * d
+            raise ValueError(f"{name}: the heads of a row must be dense")
         if x is None:
             raise ValueError(f"{name}: missing")
         if x.dtype is not self._dtype or x.get_device() != self.device:
             raise ValueError(f"{name}: expected {self._dtype} on CUDA device {self.device}")
-        if x.shape != (rows, heads, d):
-            raise ValueError(f"{name}: expected shape [{rows}, {heads}, {d}], got {list(x.shape)}")
-        s, t, u = x.stride()
-        if (t != d and heads > 1) or u != 1:
-            raise ValueError(f"{name}: the heads of a row must be dense")
-        return x.data_ptr(), s if rows > 1 else heads * d
+        raise ValueError(f"{name}: expected shape {list(want)}, got {list(x.shape)}")
 
     def _flat(self, name, x, dtype, numel):
         """Pointer of a contiguous tensor of a type and at least so many elements; 0 for None."""
         if x is None:
             return 0
-        if x.dtype is not dtype or x.get_device() != self.device or not x.is_contiguous():
-            raise ValueError(f"{name}: expected contiguous {dtype} on CUDA device {self.device}")
-        if x.numel() < numel:
+        if x.dtype is dtype and x.get_device() == self.device and x.is_contiguous():
+            if x.numel() >= numel:
+                return x.data_ptr()
             raise ValueError(f"{name}: expected at least {numel} elements, got {list(x.shape)}")
-        return x.data_ptr()
+        raise ValueError(f"{name}: expected contiguous {dtype} on CUDA device {self.device}")
 
     def _shaped(self, name, x, dtype, shape):
         """Pointer of a contiguous tensor of a type and a shape; 0 for None."""
-        if x is not None and x.shape != shape:
+        if x is None:
+            return 0
+        if x.shape != shape:
             raise ValueError(f"{name}: expected shape {list(shape)}, got {list(x.shape)}")
-        return self._flat(name, x, dtype, 0)
+        if x.dtype is dtype and x.get_device() == self.device and x.is_contiguous():
+            return x.data_ptr()
+        raise ValueError(f"{name}: expected contiguous {dtype} on CUDA device {self.device}")
 
     def _status(self, x):
         if x.element_size() != 4 or x.numel() < 1 or x.get_device() != self.device:
@@ -147,22 +152,24 @@ class AttnPlan:
         qp = qs = qo = qos = kp = ks = ko = kos = 0
         if q is not None:
             rows = q.shape[0]
-            qp, qs = self._rows("q", q, rows, self._q_heads)
-            qo, qos = self._rows("q_out", q_out, rows, self._q_heads)
+            want = (rows, self._q_heads, self._dim)
+            qp, qs = self._rows("q", q, want)
+            qo, qos = self._rows("q_out", q_out, want)
         elif k is None:
             raise ValueError("norm_rope: neither q nor k")
         else:
             rows = k.shape[0]
         if k is not None:
-            kp, ks = self._rows("k", k, rows, self._kv_heads)
+            want = (rows, self._kv_heads, self._dim)
+            kp, ks = self._rows("k", k, want)
             if k_out is not None:
-                ko, kos = self._rows("k_out", k_out, rows, self._kv_heads)
+                ko, kos = self._rows("k_out", k_out, want)
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin: expected [positions, rot_dim]")
         table, rot = cos_sin.shape
         return rows, (qp, kp, qo, ko, qs, ks, qos, kos,
-                      0 if q_weight is None else self._shaped("q_weight", q_weight, self._dtype, (self._dim,)),
-                      0 if k_weight is None else self._shaped("k_weight", k_weight, self._dtype, (self._dim,)),
+                      self._shaped("q_weight", q_weight, self._dtype, self._one_head),
+                      self._shaped("k_weight", k_weight, self._dtype, self._one_head),
                       self._flat("cos_sin", cos_sin, self._f32, 0), self._flat("positions", positions, self._i32, rows),
                       self._status(status), eps, weight_offset, table, rot, 1 if interleaved else 0, rows)
 
@@ -185,7 +192,7 @@ class AttnPlan:
         token ``lens[g] + j`` of the paged caches (``block_tables`` int32 [groups,
         max_pages]); ``k_out`` is optional."""
         rows, rope = self._rope(q, k, q_out, k_out, q_weight, k_weight, eps, weight_offset, cos_sin, interleaved, positions, status)
-        vp, vs = self._rows("v", v, rows, self._kv_heads)
+        vp, vs = self._rows("v", v, (rows, self._kv_heads, self._dim))
         groups = group_indptr.numel() - 1
         _PACK_APPEND.pack_into(
             self._io, 0, *rope, vp, vs, self._flat("group_indptr", group_indptr, self._i32, 1), self._flat("lens", lens, self._i32, groups),
@@ -205,8 +212,9 @@ class AttnPlan:
         max_prefix_pages]).  ``lse_out`` is float32 [rows, q_heads]."""
         i32 = self._i32
         rows = q.shape[0]
-        qp, qs = self._rows("q", q, rows, self._q_heads)
-        op, os_ = self._rows("out", out, rows, self._q_heads)
+        want = (rows, self._q_heads, self._dim)
+        qp, qs = self._rows("q", q, want)
+        op, os_ = self._rows("out", out, want)
         groups = group_indptr.numel() - 1
         prefixes = pi = pl = pt = 0
         if prefix_lens is not None:
