@@ -103,6 +103,10 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// The call's vectors are read with ordinary loads: the kernels are resident
+// before the kernel that writes them has ended, and a read-only load might be
+// moved ahead of the wait for that.
+
 // One verify group: its rows and committed tokens.  n = 0: idle or malformed.
 struct Group {
     int r0, n, len;
@@ -111,9 +115,9 @@ struct Group {
 
 __device__ __forceinline__ Group load_group(const AttendParams& p, int g) {
     Group x;
-    const int r0 = __ldg(&p.indptr[g]), r1 = __ldg(&p.indptr[g + 1]);
+    const int r0 = p.indptr[g], r1 = p.indptr[g + 1];
     x.r0 = r0;
-    x.len = __ldg(&p.lens[g]);
+    x.len = p.lens[g];
     const long long n = (long long)r1 - r0;
     x.bad = r0 < 0 || r1 > p.rows || n < 0 || n > p.max_group_rows ||
             (x.len >= 0 && (long long)x.len + n > ((long long)p.max_pages << p.page_shift));
@@ -129,14 +133,14 @@ struct Prefix {
 
 __device__ __forceinline__ Prefix load_prefix(const AttendParams& p, int i) {
     Prefix x;
-    x.g0 = __ldg(&p.prefix_indptr[i]);
-    x.g1 = __ldg(&p.prefix_indptr[i + 1]);
-    x.len = __ldg(&p.prefix_lens[i]);
+    x.g0 = p.prefix_indptr[i];
+    x.g1 = p.prefix_indptr[i + 1];
+    x.len = p.prefix_lens[i];
     x.bad = x.g0 < 0 || x.g1 < x.g0 || x.g1 > p.G || x.len < 0 ||
             (long long)x.len > ((long long)p.max_prefix_pages << p.page_shift);
     x.r0 = x.n = 0;
     if (!x.bad) {
-        const int r0 = __ldg(&p.indptr[x.g0]), r1 = __ldg(&p.indptr[x.g1]);
+        const int r0 = p.indptr[x.g0], r1 = p.indptr[x.g1];
         x.bad = r0 < 0 || r1 < r0 || r1 > p.rows;
         if (!x.bad) x.r0 = r0, x.n = r1 - r0;
     }
@@ -573,9 +577,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     unsigned char* ring = smem + 2 * C::kTileBytes;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(kFull, tid >> 5, 0);  // the same for the warp, as the compiler sees
-    asm volatile("griddepcontrol.launch_dependents;");  // the join waits for this grid's end by itself
     const unsigned long long limit = p.timeout_ns;
-    // barriers and tensor memory while the other warps look through the segments
+    // barriers and tensor memory, before or while the other warps look through the segments
     if (warp == kWarps - 1) {
         if (lane < C::kSlots) tc::mbar_init(&ctl->full[lane], 1), tc::mbar_init(&ctl->empty[lane], 2);
         if (lane < kPieces) tc::mbar_init(&ctl->piece_full[lane], 1), tc::mbar_init(&ctl->piece_empty[lane], kPieceReaders);
@@ -599,6 +602,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_async_shared();
     }
     if (warp == 2) tc::tmem_alloc(&ctl->tmem, kTmemCols);
+    if (tid == 0) tc::prefetch_map(&k_map), tc::prefetch_map(&v_map);
+    // so far nothing of what earlier kernels write; the join may start once that is there, and waits for this grid's end by itself
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
     Runs runs[2];  // of prefixes, of groups
     const bool any = plan_run(p, ctl, runs);
     tc::fence_before();
@@ -747,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             auto page_of = [&](int i) {
                 const long long at = walk.token + i * kKTile + tok;
-                return i < x.tiles && i * kKTile + tok < x.left ? __ldg(&walk.table[at >> p.page_shift]) : -1;
+                return i < x.tiles && i * kKTile + tok < x.left ? walk.table[at >> p.page_shift] : -1;
             };
             for (bool more = ok; ok && more;) {
                 more = walk.next(p, x);
@@ -1078,7 +1085,7 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
     const int row = blockIdx.x, head = (blockIdx.y * (kJoinWarps / kSub) + warp / kSub) * 4 + (lane & 3);
     const int g = block_find_group(p.indptr, p.G, row);
     bool mine = g >= 0 && g < p.G;
-    mine = mine && row >= __ldg(&p.indptr[g]) && row < __ldg(&p.indptr[g + 1]);  // else two entries claim the row
+    mine = mine && row >= p.indptr[g] && row < p.indptr[g + 1];  // else two entries claim the row
     const bool exists = mine && head < p.q_heads;
     Group grp = {0, 0, 0, false};
     if (mine) grp = load_group(p, g);
@@ -1094,9 +1101,9 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
                                                           (long long)(exists ? head : 0) * D + r * 64 + l * 8), q + r * 8);
         const float c = p.scale * kLog2e;
         const int j = row - grp.r0;
-        const unsigned mask = p.row_masks != nullptr ? __ldg(&p.row_masks[row]) : (2u << j) - 1u;
+        const unsigned mask = p.row_masks != nullptr ? p.row_masks[row] : (2u << j) - 1u;
         int page = 0;  // lane i: of token i
-        if (lane < grp.n) page = __ldg(&p.tables[(long long)g * p.max_pages + ((grp.len + lane) >> p.page_shift)]);
+        if (lane < grp.n) page = p.tables[(long long)g * p.max_pages + ((grp.len + lane) >> p.page_shift)];
         const unsigned here = __ballot_sync(kFull, page >= 0 && page < p.num_pages);
         unsigned todo = mask & (grp.n < 32 ? (1u << grp.n) - 1u : kFull);
         if (lane == 0 && (todo & ~here) != 0u) atomicOr(p.status, kStatusBadPage);
@@ -1236,8 +1243,18 @@ cudaError_t prepare() {
 
 template <bool kBf16, int D>
 cudaError_t launch(const AttendParams& p, const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream) {
-    lp_attend_kernel<kBf16, D><<<p.grid, kThreads, smem_bytes<D>(), stream>>>(p, k_map, v_map);
-    cudaError_t e = cudaGetLastError();
+    // Both kernels are launched while the one before still runs, and wait for its end before they read what it writes.
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)p.grid);
+    lc.blockDim = dim3(kThreads);
+    lc.dynamicSmemBytes = smem_bytes<D>();
+    lc.stream = stream;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&lc, lp_attend_kernel<kBf16, D>, p, k_map, v_map);
     if (e != cudaSuccess) return e;
     // the most warps per row with which all blocks are resident at once: one row takes 15.5 us (one warp: 24.7), trees of
     // drafts 43.6 (one: 46.3, eight: 60), 2,048 rows behind a prefix 765 (eight: 1,015)
@@ -1245,16 +1262,9 @@ cudaError_t launch(const AttendParams& p, const CUtensorMap& k_map, const CUtens
     int sub = 8;
     auto per_row = [&]() { return (chunks * sub + kJoinWarps - 1) / kJoinWarps; };  // blocks
     while (sub > 1 && per_row() * (long long)p.rows > join_blocks(sub) * p.grid) sub /= 2;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3((unsigned)p.rows, (unsigned)per_row());
     lc.blockDim = dim3(kJoinThreads);
     lc.dynamicSmemBytes = join_bytes<D>(sub);
-    lc.stream = stream;
-    lc.attrs = attr;
-    lc.numAttrs = 1;
     if (sub == 8) return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 8>, p);
     if (sub == 4) return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 4>, p);
     if (sub == 2) return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 2>, p);

@@ -114,7 +114,7 @@ __device__ __forceinline__ int block_find_group(const int* indptr, int G, int ro
     int n = 0;
     for (int b = 0; b <= G; b += blockDim.x) {
         const int i = b + (int)threadIdx.x;
-        n += __syncthreads_count(i <= G && __ldg(&indptr[i <= G ? i : G]) <= row);
+        n += __syncthreads_count(i <= G && indptr[i <= G ? i : G] <= row);
     }
     return n - 1;
 }
