@@ -20,8 +20,8 @@
 //
 // Bound: bytes in and out, and close behind them the instructions (about 75
 // per word).  16,411 rows of 32 + 8 + 8 heads of 128 lanes, BF16, into a cache:
-// 82 us, 5.8 TB/s; 8,191 rows of 24 + 4 heads of 64 lanes, F16: 13.4 us, 4.5
-// TB/s; one row into a cache: 3.5 us.
+// 82 us, 5.8 TB/s; 8,191 rows of 24 + 4 heads of 64 lanes, F16: 13.0 us, 4.6
+// TB/s; one row into a cache: 3.2 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -68,6 +68,10 @@ __global__ void __launch_bounds__(kRopeThreads, kHeads == 8 ? 6 : 8) lp_rope_ker
                                : reinterpret_cast<const T*>(p.v) + row * p.v_stride;
     src += h0 * D + e0;
 
+    // Resident before the kernel ahead has ended: nothing is read before this wait, and with ordinary loads, since read-only
+    // ones might be moved ahead of it.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
     // the heads' words, whatever the row's position
     uint4 w[kHeads];
 #pragma unroll
@@ -75,7 +79,7 @@ __global__ void __launch_bounds__(kRopeThreads, kHeads == 8 ? 6 : 8) lp_rope_ker
         w[i] = make_uint4(0u, 0u, 0u, 0u);
         if (i < n) w[i] = __ldcs(reinterpret_cast<const uint4*>(src + i * D));
     }
-    const int pos = live ? __ldg(&p.positions[row]) : -1;
+    const int pos = live ? p.positions[row] : -1;
     const void* weight = kind == 0 ? p.q_weight : (kind == 1 ? p.k_weight : nullptr);
     int g = -1;
     if constexpr (kAppend) g = block_find_group(p.indptr, p.G, (int)(first / per_row));
@@ -87,9 +91,9 @@ __global__ void __launch_bounds__(kRopeThreads, kHeads == 8 ? 6 : 8) lp_rope_ker
     if constexpr (kAppend) {
         if (work && kind != 0) {
             if (g < 0) g = 0;
-            while (g < p.G && __ldg(&p.indptr[g + 1]) <= row) ++g;
+            while (g < p.G && p.indptr[g + 1] <= row) ++g;
             if (g < p.G) {
-                const int r0 = __ldg(&p.indptr[g]), r1 = __ldg(&p.indptr[g + 1]), len = __ldg(&p.lens[g]);
+                const int r0 = p.indptr[g], r1 = p.indptr[g + 1], len = p.lens[g];
                 if (row >= r0 && len >= 0) {
                     const long long t = (long long)len + (row - r0);
                     const bool fits = r0 >= 0 && r1 <= p.rows &&
@@ -97,7 +101,7 @@ __global__ void __launch_bounds__(kRopeThreads, kHeads == 8 ? 6 : 8) lp_rope_ker
                     if (!fits) {
                         if (lane == 0) atomicOr(p.status, kStatusAttnBadGroup);
                     } else {
-                        const int page = __ldg(&p.tables[(long long)g * p.max_pages + (t >> p.page_shift)]);
+                        const int page = p.tables[(long long)g * p.max_pages + (t >> p.page_shift)];
                         if (page < 0 || page >= p.num_pages) {
                             if (lane == 0) atomicOr(p.status, kStatusBadPage);
                         } else {
@@ -122,8 +126,8 @@ __global__ void __launch_bounds__(kRopeThreads, kHeads == 8 ? 6 : 8) lp_rope_ker
     if (turn) {
         const float* t = p.cos_sin + (long long)pos * p.rot;
         if (p.interleaved) {
-            const float4 cc = __ldg(reinterpret_cast<const float4*>(t + e0 / 2));
-            const float4 ss = __ldg(reinterpret_cast<const float4*>(t + half + e0 / 2));
+            const float4 cc = *reinterpret_cast<const float4*>(t + e0 / 2);
+            const float4 ss = *reinterpret_cast<const float4*>(t + half + e0 / 2);
             const float a[4] = {cc.x, cc.y, cc.z, cc.w}, b[4] = {ss.x, ss.y, ss.z, ss.w};
 #pragma unroll
             for (int e = 0; e < 8; ++e) fa[e] = a[e / 2], fb[e] = (e & 1) ? b[e / 2] : -b[e / 2];
@@ -132,8 +136,8 @@ __global__ void __launch_bounds__(kRopeThreads, kHeads == 8 ? 6 : 8) lp_rope_ker
             const float sign = e0 < half ? -1.0f : 1.0f;
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
-                const float4 cc = __ldg(reinterpret_cast<const float4*>(t + i0) + v);
-                const float4 ss = __ldg(reinterpret_cast<const float4*>(t + half + i0) + v);
+                const float4 cc = reinterpret_cast<const float4*>(t + i0)[v];
+                const float4 ss = reinterpret_cast<const float4*>(t + half + i0)[v];
                 fa[4 * v] = cc.x, fa[4 * v + 1] = cc.y, fa[4 * v + 2] = cc.z, fa[4 * v + 3] = cc.w;
                 fb[4 * v] = sign * ss.x, fb[4 * v + 1] = sign * ss.y, fb[4 * v + 2] = sign * ss.z, fb[4 * v + 3] = sign * ss.w;
             }
@@ -141,8 +145,8 @@ __global__ void __launch_bounds__(kRopeThreads, kHeads == 8 ? 6 : 8) lp_rope_ker
     }
     if (weight != nullptr) {
         float u[8], v[8];
-        widen8<kBf16>(__ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(weight) + e0)), u);
-        widen8<kBf16>(__ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(weight) + mate * 8)), v);
+        widen8<kBf16>(*reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(weight) + e0), u);
+        widen8<kBf16>(*reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(weight) + mate * 8), v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             fa[e] *= p.weight_offset + u[e];
@@ -206,15 +210,23 @@ cudaError_t launch(const RopeParams& p, cudaStream_t stream) {
     const long long tasks = (long long)p.rows * (chunks_of(p.q_heads, kHeads) + (append ? 2 : 1) * chunks_of(p.kv_heads, kHeads));
     constexpr int kTasks = kRopeThreads / (D / 8);
     const unsigned grid = (unsigned)((tasks + kTasks - 1) / kTasks);
-    if (append) lp_rope_kernel<kBf16, D, true, kHeads><<<grid, kRopeThreads, 0, stream>>>(p);
-    else lp_rope_kernel<kBf16, D, false, kHeads><<<grid, kRopeThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(grid);
+    lc.blockDim = dim3(kRopeThreads);
+    lc.stream = stream;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return append ? cudaLaunchKernelEx(&lc, lp_rope_kernel<kBf16, D, true, kHeads>, p)
+                  : cudaLaunchKernelEx(&lc, lp_rope_kernel<kBf16, D, false, kHeads>, p);
 }
 
 // Eight heads per task spread a row's factors further, but leave a short call
 // fewer threads and a long chain of its own: with 128 lanes, 16,411 rows of 48
-// heads take 82 us against 90, 512 rows 5.7 us against 4.9; with 64 lanes 8,191
-// rows of 28 heads take 15.1 us against 13.4.
+// heads take 82 us against 89, 512 rows 5.2 us against 4.3; with 64 lanes 8,191
+// rows of 28 heads take 14.8 us against 13.0.
 constexpr long long kManyHeads = 1 << 18;
 
 template <bool kBf16>

@@ -621,3 +621,40 @@ def test_the_example_decodes_like_its_plain_form():
     assert worst <= 0.1
     assert all(len(e) == 1 + sum(a[g] + 1 for a in accepted) for g, e in enumerate(emitted))
     assert any(a > 0 for r in accepted for a in r)
+
+
+def test_calls_back_to_back_see_what_the_stream_wrote_before_them():
+    """Rows, lengths and caches that a kernel writes just ahead of each call, without a pause: the same bits as with one."""
+    import torch
+    gen = generator(23)
+    hq, hk, d, page, groups, rows_g, width = 8, 2, 128, 16, 24, 3, 10
+    rows, pages = groups * rows_g, groups * width
+    plan = plan_of(max_rows=rows, max_groups=groups, q_heads=hq, kv_heads=hk, head_dim=d, page_size=page, num_pages=pages,
+                   max_pages=width, max_group_rows=rows_g)
+    tables, indptr = i32(np.random.RandomState(3).permutation(pages).reshape(groups, width)), i32(np.arange(groups + 1) * rows_g)
+    source = rand(gen, 12, rows, hq + 2 * hk, d, dtype="bf16")
+    starts = torch.randint(-1, page * width - rows_g, (12, groups), generator=gen, device=dev(), dtype=torch.int32)
+
+    def run(pause):
+        wait = torch.cuda.synchronize if pause else (lambda: None)
+        kc, vc = (torch.zeros(pages, hk, page, d, dtype=torch.bfloat16, device=dev()) for _ in range(2))
+        x, lens, st, outs = torch.empty_like(source[0]), torch.empty_like(starts[0]), status_word(), []
+        qo, out, pos = torch.empty_like(x[:, :hq]), torch.empty_like(x[:, :hq]), torch.empty(rows, dtype=torch.int32, device=dev())
+        cs = table(d)
+        wait()
+        for i in range(12):
+            x.copy_(source[i])
+            lens.copy_(starts[i])
+            torch.add(lens.clamp(min=0)[:, None], torch.arange(rows_g, device=dev(), dtype=torch.int32), out=pos.view(groups, rows_g))
+            wait()
+            q, k, v = x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:]
+            plan.append(q=q, k=k, v=v, q_out=qo, cos_sin=cs, positions=pos, group_indptr=indptr, lens=lens, block_tables=tables,
+                        k_cache=kc, v_cache=vc, status=st)
+            wait()
+            plan.attend(q=qo, k_cache=kc, v_cache=vc, group_indptr=indptr, lens=lens, block_tables=tables, out=out, status=st)
+            wait()
+            outs.append(out.clone())
+        torch.cuda.synchronize()
+        assert int(st[0]) == 0
+        return torch.stack(outs)
+    assert torch.equal(run(False), run(True))
