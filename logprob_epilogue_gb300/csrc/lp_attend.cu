@@ -24,9 +24,10 @@
 // another.  Before that, a prefix with more units than blocks deals them out
 // whole, one to every block at a time: the blocks of a head then go through
 // its tokens side by side, and a tile that one of them fetched is still in L2
-// for the others (2,048 rows behind 32,768 tokens: 762 us against 870).  A unit of two query tiles reads each K and V tile once for both; a
-// unit of one tile gives its even token tiles to one warpgroup and its odd ones
-// to the other, each with its own maximum, sum and accumulator.
+// for the others (2,048 rows behind 32,768 tokens: 762 us against 870).  A unit
+// of two query tiles reads each K and V tile once for both; a unit of one tile
+// gives its even token tiles to one warpgroup and its odd ones to the other,
+// each with its own maximum, sum and accumulator.
 //
 // Block (one per SM, 12 warps): warp 0 splits the work and fetches pages by TMA
 // into a ring of K and V tiles (160 KiB); warps 1 and 2 issue the products, each
@@ -44,13 +45,13 @@
 //
 // What bounds it, by size (BF16, heads of 128, 32 over 8, in a CUDA graph):
 // - bandwidth, where few rows share a token: 128 groups of 4 rows at contexts up
-//   to 8,192 take 345 us, 6.5 TB/s of keys and values;
+//   to 8,192 take 342 us, 6.6 TB/s of keys and values;
 // - the tensor core, where many rows share a prefix: of 2,048 rows behind 32,768
 //   tokens the prefix's part takes 595 us, 1.85 PFLOP/s (2,700 cycles a pair of
-//   token tiles, the products alone 2,048).  The whole call takes 760 us: then
-//   come the groups' own tokens (0.5 GB) in 125, and the parts' join in 40;
-// - latency, in short calls: one row at 4,095 tokens takes 15.5 us: the launch and
-//   the split 3, the first scores 2.5, two token tiles 4, the join 5.5.
+//   token tiles, the products alone 2,048).  The whole call takes 746 us: then
+//   come the groups' own tokens (0.5 GB) in 110, and the parts' join in 40;
+// - latency, in short calls: one row at 4,095 tokens takes 15.1 us: the launch and
+//   the split 2.5, the first scores 2.5, two token tiles 4, the join 5.5.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
