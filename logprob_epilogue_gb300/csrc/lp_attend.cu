@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(kFull, tid >> 5, 0);  // the same for the warp, as the compiler sees
     const unsigned long long limit = p.timeout_ns;
-    // barriers and tensor memory, before or while the other warps look through the segments
+    // the barriers, while the kernel ahead still runs
     if (warp == kWarps - 1) {
         if (lane < C::kSlots) tc::mbar_init(&ctl->full[lane], 1), tc::mbar_init(&ctl->empty[lane], 2);
         if (lane < kPieces) tc::mbar_init(&ctl->piece_full[lane], 1), tc::mbar_init(&ctl->piece_empty[lane], kPieceReaders);
@@ -602,11 +602,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc::fence_async_shared();
     }
-    if (warp == 2) tc::tmem_alloc(&ctl->tmem, kTmemCols);
     if (tid == 0) tc::prefetch_map(&k_map), tc::prefetch_map(&v_map);
     // so far nothing of what earlier kernels write; the join may start once that is there, and waits for this grid's end by itself
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
+    if (warp == 2) tc::tmem_alloc(&ctl->tmem, kTmemCols);  // not held while waiting: the kernel ahead may need it to end
     Runs runs[2];  // of prefixes, of groups
     const bool any = plan_run(p, ctl, runs);
     tc::fence_before();
