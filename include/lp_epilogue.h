@@ -550,7 +550,9 @@ int lp_kv_append(lp_attn_t plan, const lp_append_io* io, void* stream);
  * an idle or malformed group, gets out 0 and lse -inf; rows outside every
  * group are not written.  A malformed group (LP_STATUS_BAD_GROUP) has rows out
  * of range, more than max_group_rows of them, or tokens past max_pages pages;
- * rows that two entries of group_indptr claim are not written.
+ * rows that two entries of group_indptr claim are not written.  A call whose
+ * waits ran out (LP_STATUS_TIMEOUT) gives every row of its groups out 0 and
+ * lse -inf.
  * Prefix p serves groups prefix_indptr[p] .. prefix_indptr[p+1]-1 and holds
  * prefix_lens[p] tokens in the pages prefix_tables[p]. */
 typedef struct {

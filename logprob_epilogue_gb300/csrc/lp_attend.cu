@@ -614,6 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_after();
     const uint32_t tmem = ctl->tmem;
     if (!any) {
+        if (tid == 0) p.sc.gave_up[blockIdx.x] = 0;
         if (warp == 2) tc::tmem_dealloc(tmem, kTmemCols);
         return;
     }
@@ -984,7 +985,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncthreads();
-    if (tid == 0 && *abort != 0) atomicOr(p.status, kStatusAttnTimeout);
+    if (tid == 0) {
+        p.sc.gave_up[blockIdx.x] = *abort;
+        if (*abort != 0) atomicOr(p.status, kStatusAttnTimeout);
+    }
     if (warp == 2) {
         tc::fence_after();
         tc::tmem_dealloc(tmem, kTmemCols);
@@ -1054,7 +1058,7 @@ struct Parts {
             const long long at = unit_index(p, seg < p.P, base.x + unit - dealt);
             const int2 e = at >= 0 ? p.sc.units[at] : make_int2(0, 0);
             slot = e.x;
-            pieces = e.y;
+            pieces = entry_pieces(e.x, e.y, seg < p.P ? p.sc.prefix_slots : p.sc.group_slots, p.grid);
         }
         count = pieces * sets;
     }
@@ -1160,7 +1164,13 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
     own.find(p, grp.n > 0 ? p.P + g : -1, row - grp.r0, exists ? head : 0);
     __syncwarp();
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // A block's waits ran out: it left its entries and parts as they were, and no row has a result.  With few blocks the
+    // answer is put together at the end, when the loads have long come in (one row: 15.3 us; here: 15.6); with many it costs
+    // nothing here.
+    int gave_up = 0;
+    for (int b = threadIdx.x; b < p.grid; b += kJoinThreads) gave_up |= p.sc.gave_up[b];
     const int2 shared_at = shared.first_slots(p), own_at = own.first_slots(p);
+    if constexpr (kSub == 1) gave_up = __syncthreads_or(gave_up);
     shared.locate(p, shared_at);
     own.locate(p, own_at);
     const int count = shared.count + own.count, n = count > sub ? (count - sub + kSub - 1) / kSub : 0;
@@ -1197,7 +1207,7 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
     if constexpr (kSub > 1) {  // the warps' sums, in the order of the warps
         float* part = reinterpret_cast<float*>(smem);  // [e][thread]; then the maxima and sums
         float2* part_ml = reinterpret_cast<float2*>(part + kE * kJoinThreads);
-        __syncthreads();
+        gave_up = __syncthreads_or(gave_up);
 #pragma unroll
         for (int e = 0; e < kE; ++e) part[e * kJoinThreads + threadIdx.x] = a.o[e];
         part_ml[threadIdx.x] = make_float2(a.m, a.l);
@@ -1213,6 +1223,11 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
         }
     }
     if (!exists) return;
+    if (gave_up != 0) {
+#pragma unroll
+        for (int e = 0; e < kE; ++e) a.o[e] = 0.0f;
+        a.m = kNegInf, a.l = 0.0f;
+    }
     const float inv = a.l > 0.0f ? 1.0f / a.l : (a.l == 0.0f ? 0.0f : a.l);
     T* dst = reinterpret_cast<T*>(p.out) + row * p.out_stride + (long long)head * D + l * 8;
 #pragma unroll

@@ -64,7 +64,7 @@ int check_desc(const lp_attn_desc* d) {
 }
 
 struct Layout {
-    size_t seg_units, units, part_o, part_ml, total;
+    size_t seg_units, units, gave_up, part_o, part_ml, total;  // the tables come first
     long long prefix_slots, group_slots;
     int group_rows;
 };
@@ -85,6 +85,8 @@ Layout layout_of(const lp_attn_desc* d, int grid) {
     off = lp::align_up(off + segs * 8);
     L.units = off;
     off = lp::align_up(off + (size_t)(L.prefix_slots + L.group_slots) * 8);
+    L.gave_up = off;
+    off = lp::align_up(off + (size_t)grid * 4);
     L.part_ml = off;
     off = lp::align_up(off + part_rows * 8);
     L.part_o = off;
@@ -204,14 +206,19 @@ int lp_attn_create(lp_attn_t* out, const lp_attn_desc* desc) {
         plan->encode = reinterpret_cast<EncodeTiled>(fn);
         L = layout_of(desc, plan->grid);
         e = cudaMalloc(&plan->scratch, L.total);
+        // a table entry that no call has written names no part
+        if (e == cudaSuccess) e = cudaMemset(plan->scratch, 0, L.part_ml);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);
     }
     if (e != cudaSuccess) {
         (void)cudaGetLastError();
+        cudaFree(plan->scratch);
         delete plan;
         return cuda_fail(e);
     }
     plan->sc.seg_units = reinterpret_cast<int2*>(plan->scratch + L.seg_units);
     plan->sc.units = reinterpret_cast<int2*>(plan->scratch + L.units);
+    plan->sc.gave_up = reinterpret_cast<int*>(plan->scratch + L.gave_up);
     plan->sc.part_ml = reinterpret_cast<float2*>(plan->scratch + L.part_ml);
     plan->sc.part_o = reinterpret_cast<float*>(plan->scratch + L.part_o);
     plan->sc.prefix_slots = L.prefix_slots;

@@ -41,6 +41,7 @@ struct AttendScratch {
     int2* seg_units;                // [P + G] units before the segment, of those that are cut into pieces and of those that
                                     // go round the blocks whole
     int2* units;                    // of prefixes, then of groups: a cut unit's first slot and its pieces
+    int* gave_up;                   // [grid] the block's waits ran out in the last call
     float* part_o;                  // pieces of prefixes, then of groups: unnormalised results [2][rows][D]
     float2* part_ml;                // (maximum in base 2, sum) [2][rows]
     long long prefix_slots, group_slots;
@@ -69,6 +70,17 @@ struct AttendParams {
     unsigned long long timeout_ns;
     int force_timeout;
 };
+
+// The pieces of a cut unit as the join may take them from its entry (first
+// slot, pieces): as many as there can be, in slots that exist.  Whatever an
+// entry holds, the join's loop ends and stays inside the scratch.
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline int entry_pieces(int first_slot, int pieces, long long slots, int grid) {
+    const bool sound = pieces >= 1 && pieces <= grid && first_slot >= 0 && (long long)first_slot + pieces <= slots;
+    return sound ? pieces : 0;
+}
 
 // Token columns of a box of the caches' tensor maps: a page, or a tile of it.
 inline int cache_box_rows(int page_size) { return page_size < kKTile ? page_size : kKTile; }

@@ -59,6 +59,27 @@ def test_struct_sizes_match_the_header(L, tmp_path):
     assert sizes[1:] == [s.size for s in (A._PACK_ROPE, A._PACK_APPEND, A._PACK_ATTEND)]
 
 
+def test_a_table_entry_names_only_parts_that_exist(tmp_path):
+    """What the join takes from an entry (a unit's first slot and its pieces), whatever the entry holds: no pieces, or at most
+    one per block, in slots of the region."""
+    import os
+    import subprocess
+    src = tmp_path / "e.cpp"
+    src.write_text('#include <cstdio>\n#include "lp_attn.h"\nint main() { int s, n, g; long long slots;\n'
+                   '    while (std::scanf("%d %d %lld %d", &s, &n, &slots, &g) == 4) std::printf("%d\\n", lp::entry_pieces(s, n, slots, g)); }\n')
+    exe = tmp_path / "e"
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    cuda = os.path.dirname(os.path.dirname(B._nvcc()))
+    subprocess.run(["g++", "-std=c++17", "-I", os.path.join(root, "logprob_epilogue_gb300", "csrc"), "-I", os.path.join(cuda, "include"),
+                    str(src), "-o", str(exe)], check=True)
+    slots, grid = 1000, 152
+    words = [0, 1, 2, 151, 152, 153, 847, 848, 849, 998, 999, 1000, 1001, 0x3F800000, 0x7FFFFFFF, -1, -2, -0x80000000]
+    cases = [(s, n) for s in words for n in words]
+    text = "".join(f"{s} {n} {slots} {grid}\n" for s, n in cases)
+    got = [int(x) for x in subprocess.run([str(exe)], input=text, capture_output=True, text=True, check=True).stdout.split()]
+    assert got == [n if 1 <= n <= grid and 0 <= s and s + n <= slots else 0 for s, n in cases]
+
+
 @pytest.mark.gpu
 class TestRefusals:
     """Argument errors of the three calls (a plan needs a device)."""

@@ -658,3 +658,27 @@ def test_calls_back_to_back_see_what_the_stream_wrote_before_them():
         assert int(st[0]) == 0
         return torch.stack(outs)
     assert torch.equal(run(False), run(True))
+
+
+def test_a_call_that_gave_up_gives_zeros():
+    """Waits that run out, twice on one plan and after calls that left their parts in its scratch: the status, 0 and -inf for
+    every row of a group, rows of no group untouched, in about the plan's limit; then another plan gets the right result."""
+    import time
+    import torch
+    import logprob_epilogue_gb300 as lpe
+    for c in (Case(n=[2, 3], lens=[300, 40], prefixes=[150], pad_rows=2), Case(n=[3] * 70, lens=[7 * i for i in range(70)], pad_rows=1),
+              Case(n=[1], lens=[5000], hq=8, hk=1, d=64, dtype="f16")):
+        good, good_lse, st = c.run()  # and its parts stay behind in the memory that the next plan may get
+        assert st == 0
+        rows = c.indptr[-1]
+        plan = c.plan(debug_force_timeout=True, timeout_ns=2_000_000)
+        for _ in range(2):
+            began = time.perf_counter()
+            out, lse, st = c.run(plan)
+            assert time.perf_counter() - began < 5.0
+            assert st == lpe.STATUS_TIMEOUT
+            assert bool((out[:rows] == 0).all()) and bool((lse[:rows] == -math.inf).all())
+            assert bool((out[rows:] == 7.0).all()) and bool((lse[rows:] == 7.0).all())
+        plan.close()
+        out, lse, st = c.run()
+        assert st == 0 and torch.equal(out[:rows], good[:rows]) and torch.equal(lse[:rows], good_lse[:rows])
