@@ -1088,9 +1088,8 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
     auto staged = [&](int b, int c) -> uint4& { return stage[(b * 2 * kRuns + c) * kJoinThreads]; };
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % kSub, l = lane >> 2;
     const int row = blockIdx.x, head = (blockIdx.y * (kJoinWarps / kSub) + warp / kSub) * 4 + (lane & 3);
-    const int g = block_find_group(p.indptr, p.G, row);
-    bool mine = g >= 0 && g < p.G;
-    mine = mine && row >= p.indptr[g] && row < p.indptr[g + 1];  // else two entries claim the row
+    const int g = block_group_of(p.indptr, p.G, row);
+    const bool mine = g >= 0;
     const bool exists = mine && head < p.q_heads;
     Group grp = {0, 0, 0, false};
     if (mine) grp = load_group(p, g);

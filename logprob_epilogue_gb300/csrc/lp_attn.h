@@ -119,6 +119,22 @@ struct Half<false> {
     }
 };
 
+// The group that `row` belongs to; -1 where no group claims it, or several do
+// (indptr then does not ascend).  All threads of the block take part and get
+// the answer.
+__device__ __forceinline__ int block_group_of(const int* indptr, int G, int row) {
+    __shared__ int found;
+    int n = 0;
+    for (int b = 0; b < G; b += blockDim.x) {
+        const int i = b + (int)threadIdx.x;
+        const int lo = i < G ? indptr[i] : 0, hi = i < G ? indptr[i + 1] : 0;
+        const bool claims = lo <= row && row < hi;
+        if (claims) found = i;
+        n += __syncthreads_count(claims);
+    }
+    return n == 1 ? found : -1;
+}
+
 // The number of entries of indptr[0..G] that are <= row, less one: the group
 // of `row` when indptr ascends (the caller checks the answer).  All threads of
 // the block take part and get the answer.

@@ -682,3 +682,50 @@ def test_a_call_that_gave_up_gives_zeros():
         plan.close()
         out, lse, st = c.run()
         assert st == 0 and torch.equal(out[:rows], good[:rows]) and torch.equal(lse[:rows], good_lse[:rows])
+
+
+def rows_by_the_header(c, indptr, lens, max_group_rows):
+    """What the header says of each row under an indptr of any order: None (no group claims it, or two do), or the rows'
+    group, -1 for a malformed or idle one."""
+    of = []
+    for row in range(c.rows):
+        claims = [g for g in range(len(lens)) if indptr[g] <= row < indptr[g + 1]]
+        if len(claims) != 1:
+            of.append(None)
+            continue
+        g = claims[0]
+        n = indptr[g + 1] - indptr[g]
+        bad = indptr[g] < 0 or indptr[g + 1] > c.rows or n > max_group_rows or lens[g] + n > c.tables.shape[1] * c.page
+        of.append(-1 if bad or lens[g] < 0 else g)
+    return of
+
+
+def check_by_the_header(c, indptr, lens, out, lse, served):
+    """Rows of sound groups as the reference has them (with the prefix for groups in `served`), of others 0, the rest unwritten."""
+    of = rows_by_the_header(c, indptr, lens, c.max_group_rows)
+    sound = sorted({g for g in of if g is not None and g >= 0})
+    for g in sound:
+        at = [row for row, x in enumerate(of) if x == g]
+        only = [l if i == g else -1 for i, l in enumerate(lens)]
+        kw = dict(prefix_indptr=[g, g + 1], prefix_lens=c.prefix_lens, prefix_tables=c.prefix_tables) if g in served else {}
+        R.check_attend(out, lse, R.attend(c.q, c.kc, c.vc, indptr, only, c.tables, scale=c.scale, **kw), c.dtype, at)
+    for row, x in enumerate(of):
+        if x is None:
+            assert bool((out[row] == 7.0).all()) and bool((lse[row] == 7.0).all()), row
+        elif x < 0:
+            assert bool((out[row] == 0).all()) and bool((lse[row] == -math.inf).all()), row
+    return of
+
+
+@pytest.mark.parametrize("indptr", [
+    [0, 12, 24, 36, 49], [-2, 12, 24, 36, 48], [0, 12, 24, 2147483647, 48], [0, 9, 3, 8, 5], [0, 5, 2, 7, 8], [20, 2, 14, 3, 9],
+    [48, 0, 12, 24, 36], [12, 12, 0, 0, 12], [40, 30, 20, 10, 0], [0, 13, 14, 16, 28],
+])
+def test_attend_rows_of_an_indptr_of_any_order(indptr):
+    """A row goes to the one group that claims it; with two claimants, or none, it is not written."""
+    import logprob_epilogue_gb300 as lpe
+    lens = [20, 131, 40, 0]
+    c = Case(n=[12] * 4, lens=lens, hq=6, hk=2, max_group_rows=12)
+    out, lse, st = c.run(group_indptr=i32(indptr))
+    assert st == lpe.STATUS_BAD_GROUP
+    check_by_the_header(c, indptr, lens, out, lse, served=())
