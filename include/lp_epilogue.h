@@ -554,7 +554,9 @@ int lp_kv_append(lp_attn_t plan, const lp_append_io* io, void* stream);
  * waits ran out (LP_STATUS_TIMEOUT) gives every row of its groups out 0 and
  * lse -inf.
  * Prefix p serves groups prefix_indptr[p] .. prefix_indptr[p+1]-1 and holds
- * prefix_lens[p] tokens in the pages prefix_tables[p]. */
+ * prefix_lens[p] tokens in the pages prefix_tables[p].  Where group_indptr does
+ * not ascend (LP_STATUS_BAD_GROUP), it serves those of them whose rows lie in
+ * group_indptr[prefix_indptr[p]] .. group_indptr[prefix_indptr[p+1]]-1. */
 typedef struct {
     const void* q;                 /* [rows, q_heads, head_dim] */
     int64_t q_stride;

@@ -1151,12 +1151,14 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
             a.add(s * c, 1.0f, v);
         }
     }
-    Parts shared, own;  // of the first prefix that serves the row, of its group's committed tokens
+    // Of the first prefix that serves the row, of its group's committed tokens.  A prefix has parts for the rows from its first
+    // group's to its last's: a group whose rows lie elsewhere (group_indptr then does not ascend) is not served.
+    Parts shared, own;
     int prefix = -1, first = 0;
     if (grp.n > 0) {
         for (int i = 0; i < p.P && prefix < 0; ++i) {
             const Prefix x = load_prefix(p, i);
-            if (!x.bad && g >= x.g0 && g < x.g1) prefix = i, first = x.r0;
+            if (!x.bad && g >= x.g0 && g < x.g1 && grp.r0 >= x.r0 && grp.r0 + grp.n <= x.r0 + x.n) prefix = i, first = x.r0;
         }
     }
     shared.find(p, prefix, row - first, exists ? head : 0);

@@ -729,3 +729,27 @@ def test_attend_rows_of_an_indptr_of_any_order(indptr):
     out, lse, st = c.run(group_indptr=i32(indptr))
     assert st == lpe.STATUS_BAD_GROUP
     check_by_the_header(c, indptr, lens, out, lse, served=())
+
+
+@pytest.mark.parametrize("indptr,served", [
+    ([128, 0, 32, 64, 96, 128, 10], (1, 6)), ([0, 9, 3, 8, 5], (0, 4)), ([9, 2, 8, 5], (1, 3)), ([20, 2, 14, 3, 9, 16], (1, 5)),
+    ([40, 0, 4, 8, 64, 10], (1, 5)), ([12, 24, 0, 12, 36], (0, 4)), ([0, 12, 24, 36, 200], (0, 4)),
+])
+def test_attend_prefix_over_an_indptr_of_any_order(indptr, served):
+    """A prefix serves the groups whose rows lie between its first group's and its last's; nothing else is read for a row."""
+    import torch
+    import logprob_epilogue_gb300 as lpe
+    groups = len(indptr) - 1
+    lens = [20, 131, 40, 0, 7, 300][:groups]
+    c = Case(n=[32] * groups, lens=lens, hq=6, hk=2, prefixes=[200], prefix_indptr=served)
+    lo, hi = indptr[served[0]], indptr[served[1]]
+    sound = 0 <= lo <= hi <= c.rows
+    inside = [g for g in range(*served) if sound and lo <= indptr[g] <= indptr[g + 1] <= hi]
+    plan = c.plan()
+    c.run(plan)  # parts of other rows and lengths stay behind in the scratch
+    out, lse, st = c.run(plan, group_indptr=i32(indptr))
+    assert st & lpe.STATUS_BAD_GROUP and not st & ~(lpe.STATUS_BAD_GROUP | lpe.STATUS_BAD_PREFIX)
+    assert bool(st & lpe.STATUS_BAD_PREFIX) == (not sound)
+    check_by_the_header(c, indptr, lens, out, lse, served=inside)
+    again = c.run(plan, group_indptr=i32(indptr))
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
