@@ -526,7 +526,9 @@ int lp_norm_rope(lp_attn_t plan, const lp_rope_io* io, void* stream);
  * rope.k_out may be NULL (keys to the cache only).  Rows outside every group
  * and rows of idle groups reach q_out and k_out but no cache; so do the rows
  * of a malformed group (LP_STATUS_BAD_GROUP: rows out of range, or tokens past
- * max_pages pages).  No two rows may name the same slot. */
+ * max_pages pages), and where group_indptr does not ascend (LP_STATUS_BAD_GROUP)
+ * rows that two of its entries claim.  A row that lp_norm_rope skips is not
+ * written to the caches either.  No two rows may name the same slot. */
 typedef struct {
     lp_rope_io rope;
     const void* v;               /* [rows, kv_heads, head_dim] */

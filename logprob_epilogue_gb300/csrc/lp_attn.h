@@ -136,14 +136,18 @@ __device__ __forceinline__ int block_group_of(const int* indptr, int G, int row)
 }
 
 // The number of entries of indptr[0..G] that are <= row, less one: the group
-// of `row` when indptr ascends (the caller checks the answer).  All threads of
-// the block take part and get the answer.
-__device__ __forceinline__ int block_find_group(const int* indptr, int G, int row) {
+// of `row` when indptr ascends (the caller checks the answer); and whether it
+// ascends.  All threads of the block take part and get the answers.
+__device__ __forceinline__ int block_find_group(const int* indptr, int G, int row, bool& ascends) {
     int n = 0;
+    bool falls = false;
     for (int b = 0; b <= G; b += blockDim.x) {
         const int i = b + (int)threadIdx.x;
-        n += __syncthreads_count(i <= G && indptr[i <= G ? i : G] <= row);
+        const int at = indptr[i <= G ? i : G], next = indptr[i < G ? i + 1 : G];
+        falls |= next < at;
+        n += __syncthreads_count(i <= G && at <= row);
     }
+    ascends = __syncthreads_or(falls) == 0;
     return n - 1;
 }
 #endif

@@ -82,7 +82,11 @@ __global__ void __launch_bounds__(kRopeThreads, kHeads == 8 ? 6 : 8) lp_rope_ker
     const int pos = live ? p.positions[row] : -1;
     const void* weight = kind == 0 ? p.q_weight : (kind == 1 ? p.k_weight : nullptr);
     int g = -1;
-    if constexpr (kAppend) g = block_find_group(p.indptr, p.G, (int)(first / per_row));
+    bool ascends = true;
+    if constexpr (kAppend) {
+        g = block_find_group(p.indptr, p.G, (int)(first / per_row), ascends);
+        if (!ascends && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.status, kStatusAttnBadGroup);
+    }
     if (pos >= p.max_pos && lane == 0 && c == 0) atomicOr(p.status, kStatusBadPosition);
     const bool work = pos >= 0 && pos < p.max_pos;
 
@@ -90,12 +94,19 @@ __global__ void __launch_bounds__(kRopeThreads, kHeads == 8 ? 6 : 8) lp_rope_ker
     long long slot = -1;
     if constexpr (kAppend) {
         if (work && kind != 0) {
-            if (g < 0) g = 0;
-            while (g < p.G && p.indptr[g + 1] <= row) ++g;
+            if (ascends) {
+                if (g < 0) g = 0;
+                while (g < p.G && p.indptr[g + 1] <= row) ++g;
+            } else {  // the one group that claims the row
+                int claims = 0;
+                for (int i = 0; i < p.G; ++i)
+                    if (p.indptr[i] <= row && row < p.indptr[i + 1]) ++claims, g = i;
+                if (claims != 1) g = p.G;
+            }
             if (g < p.G) {
                 const int r0 = p.indptr[g], r1 = p.indptr[g + 1], len = p.lens[g];
                 if (row >= r0 && len >= 0) {
-                    const long long t = (long long)len + (row - r0);
+                    const long long t = (long long)len + row - r0;
                     const bool fits = r0 >= 0 && r1 <= p.rows &&
                                       (long long)len + (r1 - r0) <= ((long long)p.max_pages << p.page_shift);
                     if (!fits) {

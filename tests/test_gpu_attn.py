@@ -753,3 +753,40 @@ def test_attend_prefix_over_an_indptr_of_any_order(indptr, served):
     check_by_the_header(c, indptr, lens, out, lse, served=inside)
     again = c.run(plan, group_indptr=i32(indptr))
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("indptr,lens", [
+    ([6, 2, 8], [0, 0]), ([0, 4, 4, 8], [3, 0, 20]), ([0, 9, 3, 8, 5], [1, 2, 30, 0]), ([20, 2, 14, 3, 9], [0, 17, 5, 9]),
+    ([40, 30, 20, 10, 0], [0, 0, 0, 0]), ([24, 0, 8, 8, 16], [5, 6, -1, 7]), ([0, 24, 12, 30, 40], [0, 5, 3, 1]),
+    ([0, 8, 16, 23], [41, 33, -1]), ([-2147483648, 2147483647, 3, 9], [0, 0, 0]),
+])
+@pytest.mark.parametrize("hk", [1, 20])
+def test_append_puts_every_row_where_the_header_says(indptr, lens, hk):
+    """Group vectors of any order: a row reaches the slot of the one sound group that claims it, and nothing else is written."""
+    import torch
+    import logprob_epilogue_gb300 as lpe
+    rows, page, width, groups = 24, 16, 3, len(lens)
+    gen = generator(rows)
+    k, v = (rand(gen, rows, hk, 64, dtype="bf16") for _ in range(2))
+    pages = groups * width + 2
+    tables = np.random.RandomState(hk).permutation(pages)[:groups * width].reshape(groups, width)
+    kc, vc = (torch.full((pages, hk, page, 64), 7.0, dtype=torch.bfloat16, device=dev()) for _ in range(2))
+    want_k, want_v = kc.clone(), vc.clone()
+    bad = any(a > b for a, b in zip(indptr, indptr[1:]))
+    for row in range(rows):
+        claims = [g for g in range(groups) if indptr[g] <= row < indptr[g + 1]]
+        if len(claims) != 1 or lens[claims[0]] < 0:
+            continue
+        g = claims[0]
+        if indptr[g] < 0 or indptr[g + 1] > rows or lens[g] + indptr[g + 1] - indptr[g] > width * page:
+            bad = True
+            continue
+        t = lens[g] + row - indptr[g]
+        want_k[int(tables[g, t // page]), :, t % page], want_v[int(tables[g, t // page]), :, t % page] = k[row], v[row]
+    st = status_word()
+    plan = plan_of(max_rows=rows, max_groups=groups, q_heads=hk, kv_heads=hk, head_dim=64, num_pages=pages, max_pages=width)
+    plan.append(k=k, v=v, cos_sin=table(0), positions=i32([0] * rows), group_indptr=i32(indptr), lens=i32(lens), block_tables=i32(tables),
+                k_cache=kc, v_cache=vc, status=st)
+    torch.cuda.synchronize()
+    assert int(st[0]) == (lpe.STATUS_BAD_GROUP if bad else 0)
+    assert torch.equal(kc, want_k) and torch.equal(vc, want_v)
