@@ -13,6 +13,10 @@ prompt.  Each round verifies k drafts per request:
      tokens stay in the cache, past the length: nothing reads them there, and
      the next round writes over them.
 
+The batch has a slot without a request, as a captured batch has: its rows go
+through every call, its length stays negative, and its old page table, which
+names pages that other requests hold by now, is not written through.
+
 The drafts are what followed the same token the last time, so they are accepted
 as soon as the decoding repeats itself.  Run it on a GB300:
 
@@ -76,17 +80,19 @@ class Target:
         return (x + o.flatten(1) @ self.out.double()) @ self.head.double()
 
 
-def decode(target, prompt, firsts, rounds=24, drafts=3, page=16):
-    """Decodes from each of ``firsts`` behind ``prompt``: the emitted tokens of each request and the rounds' accepted drafts."""
+def decode(target, prompt, firsts, rounds=24, drafts=3, page=16, idle=1):
+    """Decodes from each of ``firsts`` behind ``prompt``, with ``idle`` slots of the batch free: the emitted tokens of each
+    request, the rounds' accepted drafts, and the slots' committed lengths."""
     dev = torch.device("cuda", torch.cuda.current_device())
     i32 = lambda x: torch.as_tensor(x, dtype=torch.int32, device=dev)  # noqa: E731
-    groups, rows_of, m = len(firsts), drafts + 1, len(prompt)
+    requests, groups, rows_of, m = len(firsts), len(firsts) + idle, drafts + 1, len(prompt)
     rows, prompt_pages = groups * rows_of, -(-m // page)
     max_pages = max(prompt_pages, -(-(rounds * rows_of) // page) + 1)
     num_pages = groups * max_pages + prompt_pages
     shape = (num_pages, target.kv_heads, page, target.head_dim)
     k_cache, v_cache = (torch.zeros(shape, dtype=torch.bfloat16, device=dev) for _ in range(2))
     tables = i32(torch.arange(groups * max_pages).view(groups, max_pages))
+    tables[requests:] = tables[0].clone()  # what a request that has left held belongs to another now
     prompt_table = i32([[groups * max_pages + i for i in range(prompt_pages)]])
     status = torch.zeros(1, dtype=torch.int32, device=dev)
     attention = lpe.AttnPlan(max_rows=rows, max_groups=groups, q_heads=target.q_heads, kv_heads=target.kv_heads,
@@ -103,7 +109,7 @@ def decode(target, prompt, firsts, rounds=24, drafts=3, page=16):
     _, _, k, v = target.heads(torch.as_tensor(prompt, device=dev))
     filler.append(k=k, v=v, group_indptr=i32([0, m]), lens=i32([0]), block_tables=prompt_table, positions=i32(range(m)), **rope, **common)
 
-    indptr, lens = i32([g * rows_of for g in range(groups + 1)]), i32([0] * groups)
+    indptr, lens = i32([g * rows_of for g in range(groups + 1)]), i32([0] * requests + [-1] * idle)
     epilogue_io = dict(group_indptr=indptr, sampled_tokens=i32([-1] * groups), requested=i32([1] * groups), top_k=i32([5] * groups),
                        token_ids=i32([[-1] * lpe.MAX_IDS] * groups), id_counts=i32([0] * groups),
                        records=i32([[0] * lpe.RECORD_WORDS] * rows), accepted=i32([0] * groups), emitted_tokens=i32([0] * rows),
@@ -112,13 +118,14 @@ def decode(target, prompt, firsts, rounds=24, drafts=3, page=16):
     emitted, followed, accepted_of = [[t] for t in firsts], {}, []
     for _ in range(rounds):
         block = []
-        for g in range(groups):
+        for g in range(requests):
             block.append(emitted[g][-1])
             for _ in range(drafts):
                 block.append(followed.get(block[-1], 0))
+        block += [0] * (idle * rows_of)
         tokens = torch.tensor(block, device=dev)
         x, q, k, v = target.heads(tokens)
-        positions = (m + lens[:, None] + torch.arange(rows_of, dtype=torch.int32, device=dev)).flatten()
+        positions = (m + lens.clamp(min=0)[:, None] + torch.arange(rows_of, dtype=torch.int32, device=dev)).flatten()
         attention.append(q=q, k=k, v=v, q_out=q_out, group_indptr=indptr, lens=lens, block_tables=tables, positions=positions,
                          **rope, **common)
         attention.attend(q=q_out, out=out, group_indptr=indptr, lens=lens, block_tables=tables, prefix_indptr=i32([0, groups]),
@@ -126,8 +133,8 @@ def decode(target, prompt, firsts, rounds=24, drafts=3, page=16):
         draft_tokens = i32([block[r + 1] if (r + 1) % rows_of else -1 for r in range(rows)])
         epilogue.bind(logits=target.logits(x, out), draft_tokens=draft_tokens, **epilogue_io)
         epilogue.run()
-        lens += epilogue_io["accepted"] + 1
-        accepted, new = epilogue_io["accepted"].tolist(), epilogue_io["emitted_tokens"].view(groups, rows_of).tolist()
+        lens += torch.where(lens < 0, 0, epilogue_io["accepted"] + 1)
+        accepted, new = epilogue_io["accepted"][:requests].tolist(), epilogue_io["emitted_tokens"].view(groups, rows_of).tolist()
         for g, a in enumerate(accepted):
             for t in new[g][:a + 1]:
                 followed[emitted[g][-1]] = t
@@ -138,7 +145,17 @@ def decode(target, prompt, firsts, rounds=24, drafts=3, page=16):
             raise RuntimeError(f"{name}: status {int(word):#x}")
     for plan in (attention, filler, epilogue):
         plan.close()
-    return emitted, accepted_of
+    return emitted, accepted_of, lens.tolist()
+
+
+def shortfall(target, prompt, emitted):
+    """How far an emitted token's logit lies below the largest of the plain form, at most."""
+    worst = 0.0
+    for e in emitted:
+        logits = target.plain_logits(torch.tensor(prompt + e[:-1], device="cuda"))[len(prompt):]
+        chosen = logits.gather(1, torch.tensor(e[1:], device="cuda")[:, None])[:, 0]
+        worst = max(worst, float((logits.max(1).values - chosen).max()))
+    return worst
 
 
 def main():
@@ -146,14 +163,10 @@ def main():
         raise SystemExit("this example needs a CUDA device")
     target = Target()
     prompt = torch.randint(0, target.vocab, (100,), generator=torch.Generator().manual_seed(1)).tolist()
-    emitted, accepted = decode(target, prompt, firsts=list(range(8)))
+    emitted, accepted, _ = decode(target, prompt, firsts=list(range(8)))
     tokens = sum(len(e) - 1 for e in emitted)
     print(f"{len(emitted)} requests, {len(accepted)} rounds: {tokens} tokens, {sum(map(sum, accepted))} of them accepted drafts")
-    worst = 0.0
-    for e in emitted:
-        logits = target.plain_logits(torch.tensor(prompt + e[:-1], device="cuda"))[len(prompt):]
-        chosen = logits.gather(1, torch.tensor(e[1:], device="cuda")[:, None])[:, 0]
-        worst = max(worst, float((logits.max(1).values - chosen).max()))
+    worst = shortfall(target, prompt, emitted)
     print(f"an emitted token's logit lies at most {worst:.3f} below the largest of the plain form in 64 bits")
     return emitted, accepted, worst
 

@@ -436,10 +436,13 @@ int lp_run_static(const lp_plan_desc* desc, const lp_io* io, void* stream);
  * State.  Group g owns rows group_indptr[g] .. group_indptr[g+1]-1, as in
  * lp_bind.  lens[g] counts its committed tokens; row j of the group is token
  * lens[g] + j.  lp_kv_append writes those tokens and lp_attend reads them;
- * neither changes lens.  After the epilogue the caller commits the round with
- * lens[g] += accepted[g] + 1: tokens past lens are never read as committed,
- * and the next append overwrites them.  lens[g] < 0 marks an idle group (a
- * slot of a captured batch without a request).
+ * neither changes lens.  lens[g] < 0 marks an idle group (a slot of a captured
+ * batch without a request; it may still own rows).  After the epilogue the
+ * caller commits the round with lens[g] += accepted[g] + 1 where lens[g] >= 0:
+ * tokens past lens are never read as committed, and the next append overwrites
+ * them.  The epilogue knows nothing of lens and accepts for an idle group's
+ * rows as for any others: its lens stays as it is, or the next append would
+ * write through the slot's old page table.
  *
  * Cache.  k_cache and v_cache are [num_pages, kv_heads, page_size, head_dim]
  * each; token t of group g is slot t % page_size of page

@@ -68,11 +68,12 @@ class AttnPlan:
     it (``attend``).
 
     Caches are [num_pages, kv_heads, page_size, head_dim].  ``lens`` counts each
-    group's committed tokens and is changed by none of the calls: after the
-    epilogue, ``lens += accepted + 1`` commits the round.  Every call only
-    enqueues on ``stream`` (default: torch's current stream) and ORs its status
-    bits into ``status`` without resetting it.  Like a ``Plan``, one plan serves
-    one stream, and one thread, at a time."""
+    group's committed tokens, negative for an idle group, and is changed by none
+    of the calls: after the epilogue, ``lens += torch.where(lens < 0, 0, accepted
+    + 1)`` commits the round.  Every call only enqueues on ``stream`` (default:
+    torch's current stream) and ORs its status bits into ``status`` without
+    resetting it.  Like a ``Plan``, one plan serves one stream, and one thread,
+    at a time."""
 
     def __init__(self, **desc_kw):
         import torch

@@ -790,3 +790,18 @@ def test_append_puts_every_row_where_the_header_says(indptr, lens, hk):
     torch.cuda.synchronize()
     assert int(st[0]) == (lpe.STATUS_BAD_GROUP if bad else 0)
     assert torch.equal(kc, want_k) and torch.equal(vc, want_v)
+
+
+def test_an_idle_slot_stays_idle_through_rounds():
+    """The example's batch with free slots: their lengths stay negative whatever the epilogue accepts for their rows, and the
+    requests, whose pages the free slots' old tables name, decode as the plain form does (the bound of the test above)."""
+    import importlib.util
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "verify_rounds.py")
+    spec = importlib.util.spec_from_file_location("verify_rounds", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    target, prompt, firsts = example.Target(), list(range(3, 40)), [5, 6, 7]
+    for idle in (0, 1, 5):
+        emitted, accepted, lens = example.decode(target, prompt, firsts, rounds=8, idle=idle)
+        assert lens == [sum(a[g] + 1 for a in accepted) for g in range(3)] + [-1] * idle
+        assert example.shortfall(target, prompt, emitted) <= 0.1
