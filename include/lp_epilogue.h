@@ -442,7 +442,11 @@ int lp_run_static(const lp_plan_desc* desc, const lp_io* io, void* stream);
  * tokens past lens are never read as committed, and the next append overwrites
  * them.  The epilogue knows nothing of lens and accepts for an idle group's
  * rows as for any others: its lens stays as it is, or the next append would
- * write through the slot's old page table.
+ * write through the slot's old page table.  That rule is for chains of drafts,
+ * which are what the epilogue accepts.  Of a tree (row_masks) the accepted
+ * branch need not be the group's first rows: whoever accepts it appends the
+ * keys and values of its rows again, in the branch's order and at the same
+ * lens, and then adds their number to lens.
  *
  * Cache.  k_cache and v_cache are [num_pages, kv_heads, page_size, head_dim]
  * each; token t of group g is slot t % page_size of page

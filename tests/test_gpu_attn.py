@@ -805,3 +805,53 @@ def test_an_idle_slot_stays_idle_through_rounds():
         emitted, accepted, lens = example.decode(target, prompt, firsts, rounds=8, idle=idle)
         assert lens == [sum(a[g] + 1 for a in accepted) for g in range(3)] + [-1] * idle
         assert example.shortfall(target, prompt, emitted) <= 0.1
+
+
+def test_a_branch_of_a_tree_is_committed_by_appending_it_again():
+    """Rows 0, 2 and 5 of a tree are accepted: appended again at the same lengths, the cache holds what a chain of the three
+    leaves there, and the next round attends to it."""
+    import torch
+    gen = generator(31)
+    hq, hk, d, page, width, n = 8, 2, 128, 16, 6, 7
+    starts, branch = [0, 13, 30], [0, 2, 5]
+    groups = len(starts)
+    rows, pages = groups * n, groups * width
+    plan = plan_of(max_rows=rows, max_groups=groups, q_heads=hq, kv_heads=hk, head_dim=d, page_size=page, num_pages=pages,
+                   max_pages=width, max_group_rows=n)
+    order = np.random.RandomState(4).permutation(pages).reshape(groups, width)
+    tables, st, cs = i32(order), status_word(), table(d)
+    kc, vc = (rand(gen, pages, hk, page, d, dtype="bf16") for _ in range(2))
+    chain_k, chain_v = kc.clone(), vc.clone()
+    qkv = rand(gen, rows, hq + 2 * hk, d, dtype="bf16")
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]
+    parents, depth, masks = [None, 0, 0, 1, 2, 2, 4], [0], [1]
+    for j in range(1, n):
+        depth.append(depth[parents[j]] + 1)
+        masks.append(masks[parents[j]] | 1 << j)
+    assert masks[5] == 1 << 0 | 1 << 2 | 1 << 5
+    lens = i32(starts)
+    pos = i32([s + depth[j] for s in starts for j in range(n)])
+    common = dict(status=st, block_tables=tables)
+    indptr = i32(np.arange(groups + 1) * n)
+    plan.append(k=k, v=v, k_cache=kc, v_cache=vc, positions=pos, group_indptr=indptr, lens=lens, cos_sin=cs, **common)
+    out, lse = torch.empty(rows, hq, d, dtype=torch.bfloat16, device=dev()), torch.empty(rows, hq, device=dev())
+    plan.attend(q=q, k_cache=kc, v_cache=vc, group_indptr=indptr, lens=lens, row_masks=i32(masks * groups), out=out, lse_out=lse, **common)
+    ref = R.attend(q, kc, vc, indptr.tolist(), starts, order, scale=d ** -0.5, masks=masks * groups)
+    R.check_attend(out, lse, ref, "bf16")
+    # the branch again, and the same three rows as a chain in caches of their own
+    at = torch.tensor([g * n + j for g in range(groups) for j in branch], device=dev())
+    three = i32(np.arange(groups + 1) * len(branch))
+    for a, b in ((kc, vc), (chain_k, chain_v)):
+        plan.append(k=k[at], v=v[at], k_cache=a, v_cache=b, positions=pos[at].contiguous(), group_indptr=three, lens=lens, cos_sin=cs, **common)
+    lens += len(branch)
+    for g, s in enumerate(starts):
+        for t in range(s + len(branch)):
+            slot = (int(order[g, t // page]), slice(None), t % page)
+            assert torch.equal(kc[slot], chain_k[slot]) and torch.equal(vc[slot], chain_v[slot])
+    nxt = rand(gen, groups, hq + 2 * hk, d, dtype="bf16")
+    one = i32(np.arange(groups + 1))
+    plan.append(k=nxt[:, hq:hq + hk], v=nxt[:, hq + hk:], k_cache=kc, v_cache=vc, positions=lens, group_indptr=one, lens=lens, cos_sin=cs, **common)
+    plan.attend(q=nxt[:, :hq], k_cache=kc, v_cache=vc, group_indptr=one, lens=lens, out=out[:groups], lse_out=lse[:groups], **common)
+    ref = R.attend(nxt[:, :hq], kc, vc, one.tolist(), lens.tolist(), order, scale=d ** -0.5)
+    R.check_attend(out[:groups], lse[:groups], ref, "bf16")
+    assert int(st[0]) == 0
