@@ -855,3 +855,49 @@ def test_a_branch_of_a_tree_is_committed_by_appending_it_again():
     ref = R.attend(nxt[:, :hq], kc, vc, one.tolist(), lens.tolist(), order, scale=d ** -0.5)
     R.check_attend(out[:groups], lse[:groups], ref, "bf16")
     assert int(st[0]) == 0
+
+
+# ---- long calls: 2^18 (row, head) pairs and more of 128 lanes are taken eight heads at a time
+
+
+@pytest.mark.parametrize("dtype,hq,hk,rows,rot,inter,norm,layout", [
+    ("bf16", 15, 3, 14564, 128, False, True, "fused"),     # chunks of 8 and 7 heads, and of 3
+    ("bf16", 15, 3, 14563, 128, False, True, "fused"),     # one row short of it
+    ("f16", 20, 5, 10486, 64, True, True, "dense"),
+    ("f16", 15, 3, 16385, 112, False, False, "inplace"),
+    ("bf16", 24, 1, 10497, 48, True, True, "inplace"),
+    ("f16", 8, 8, 16391, 0, False, True, "dense"),
+])
+def test_norm_rope_long_calls(dtype, hq, hk, rows, rot, inter, norm, layout):
+    test_norm_rope(dtype, 128, hq, hk, rows, rot, inter, norm, 1.0 if norm else 0.0, layout)
+
+
+def test_norm_rope_long_calls_of_queries_alone_with_padding():
+    """12 heads, four past the last chunk's; every third row is padding, and the last rows lie past the table."""
+    import torch
+    import logprob_epilogue_gb300 as lpe
+    rows, hq, gen = 21847, 12, generator(17)
+    q = rand(gen, rows, hq, 128, dtype="f16")
+    w = (0.3 * rand(gen, 128, dtype="f16")).half()
+    pos = torch.randint(0, 600, (rows,), generator=gen, device=dev(), dtype=torch.int32)
+    pos[::3] = -1
+    pos[-2:] = 600
+    out, st, cs = torch.full_like(q, 7.0), status_word(), table(128)
+    plan_of(max_rows=rows, q_heads=hq, kv_heads=3, dtype="f16").norm_rope(q=q, q_out=out, q_weight=w, weight_offset=1.0, cos_sin=cs, positions=pos, status=st)
+    torch.cuda.synchronize()
+    assert int(st[0]) == lpe.STATUS_BAD_POSITION
+    live = (pos >= 0) & (pos < 600)
+    ref, mag = R.heads(q, w, cs, pos, eps=1e-6, offset=1.0, interleaved=False)
+    R.check_heads(out[live], ref[live], mag[live], "f16")
+    assert bool((out[~live] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype,hq,hk,page,n,lens,with_q,k_out,norm", [
+    ("bf16", 15, 3, 64, [9000, 0, 1, 5561], [100, 5, 63, 0], True, False, True),
+    ("bf16", 15, 3, 64, [9000, 0, 1, 5560], [100, 5, 63, 0], True, False, True),    # one row short of it
+    ("f16", 20, 5, 16, [5001, 2003, 11, 3470], [0, -1, 17, 255], True, True, True),
+    ("f16", 16, 16, 256, [8192, 8190], [1, 300], False, True, False),               # keys and values alone
+    ("bf16", 12, 12, 8, [4] * 2731, [i % 90 - 1 for i in range(2731)], True, False, False),
+])
+def test_append_long_calls(dtype, hq, hk, page, n, lens, with_q, k_out, norm):
+    test_append(dtype, 128, hq, hk, page, n, lens, with_q, k_out, norm)
