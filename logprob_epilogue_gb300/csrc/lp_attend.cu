@@ -1035,13 +1035,13 @@ struct Parts {
     int row, cap, set, sets;  // row of the unit; the parts of a piece that are its: sets of them from `set` on
     int count;
     long long slot;
-    __device__ __forceinline__ void find(const AttendParams& p, int segment, int rel, int head) {
+    __device__ __forceinline__ void find(const AttendParams& p, int segment, int of, int head) {  // of: the row
         seg = -1;
         if (segment < 0) return;
         const Seg s = load_seg(p, segment);
         if (s.tiles == 0) return;
         seg = segment;
-        const int rt = p.rows_per_tile, u = rel / (2 * rt), in = rel - u * 2 * rt, kvh = head / p.share;
+        const int rt = p.rows_per_tile, rel = of - s.r0, u = rel / (2 * rt), in = rel - u * 2 * rt, kvh = head / p.share;
         const bool two = s.n - u * 2 * rt > rt;
         unit = kvh * s.units + u;
         dealt = s.dealt;
@@ -1088,7 +1088,9 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
     auto staged = [&](int b, int c) -> uint4& { return stage[(b * 2 * kRuns + c) * kJoinThreads]; };
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % kSub, l = lane >> 2;
     const int row = blockIdx.x, head = (blockIdx.y * (kJoinWarps / kSub) + warp / kSub) * 4 + (lane & 3);
-    const int g = block_group_of(p.indptr, p.G, row);
+    __shared__ int served_by;  // the prefix of the row
+    if (threadIdx.x == 0) served_by = p.P;
+    const int g = block_group_of(p.indptr, p.G, row);  // (a barrier)
     const bool mine = g >= 0;
     const bool exists = mine && head < p.q_heads;
     Group grp = {0, 0, 0, false};
@@ -1154,15 +1156,19 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
     // Of the first prefix that serves the row, of its group's committed tokens.  A prefix has parts for the rows from its first
     // group's to its last's: a group whose rows lie elsewhere (group_indptr then does not ascend) is not served.
     Parts shared, own;
-    int prefix = -1, first = 0;
-    if (grp.n > 0) {
-        for (int i = 0; i < p.P && prefix < 0; ++i) {
+    if (p.P > 0 && grp.n > 0) {  // the same for the block, whose threads look through the prefixes side by side
+        for (int i = threadIdx.x; i < p.P; i += kJoinThreads) {
+            if (p.prefix_indptr[i] > g || p.prefix_indptr[i + 1] <= g) continue;
             const Prefix x = load_prefix(p, i);
-            if (!x.bad && g >= x.g0 && g < x.g1 && grp.r0 >= x.r0 && grp.r0 + grp.n <= x.r0 + x.n) prefix = i, first = x.r0;
+            if (!x.bad && grp.r0 >= x.r0 && grp.r0 + grp.n <= x.r0 + x.n) {
+                atomicMin(&served_by, i);
+                break;
+            }
         }
+        __syncthreads();
     }
-    shared.find(p, prefix, row - first, exists ? head : 0);
-    own.find(p, grp.n > 0 ? p.P + g : -1, row - grp.r0, exists ? head : 0);
+    shared.find(p, grp.n > 0 && served_by < p.P ? served_by : -1, row, exists ? head : 0);
+    own.find(p, grp.n > 0 ? p.P + g : -1, row, exists ? head : 0);
     __syncwarp();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // A block's waits ran out: it left its entries and parts as they were, and no row has a result.  With few blocks the

@@ -901,3 +901,57 @@ def test_norm_rope_long_calls_of_queries_alone_with_padding():
 ])
 def test_append_long_calls(dtype, hq, hk, page, n, lens, with_q, k_out, norm):
     test_append(dtype, 128, hq, hk, page, n, lens, with_q, k_out, norm)
+
+
+# ---- many prefixes
+
+
+def test_attend_hundreds_of_prefixes():
+    """700 prefixes over 40 groups, most of them over none; groups before, between and behind them have none."""
+    r = np.random.RandomState(8)
+    groups, count = 40, 700
+    lens = [int(x) for x in r.randint(-1, 200, groups)]
+    ends = np.sort(r.randint(3, 36, count + 1))
+    c = Case(n=[1 + i % 3 for i in range(groups)], lens=lens, prefixes=[int(x) for x in r.randint(0, 150, count)], prefix_indptr=[int(x) for x in ends],
+             hq=6, hk=2, max_group_rows=3)
+    c.check()
+
+
+def test_attend_takes_the_first_sound_prefix():
+    """Prefixes that overlap (their group ranges do not ascend): the lowest index that covers the group serves it."""
+    import torch
+    import logprob_epilogue_gb300 as lpe
+    many = 300
+    c = Case(n=[2] * 4, lens=[5, 130, 0, 64], prefixes=[40, 90, 20] + [16] * (many - 3), prefix_indptr=[1, 3, 0, 4] + [0] * (many - 3))
+    out, lse, st = c.run()
+    assert st == lpe.STATUS_BAD_PREFIX  # the descents
+    # prefix 0 covers groups 1 and 2, prefix 1 none (3 to 0), prefix 2 all four
+    for first, end, i in ((1, 3, 0), (0, 1, 2), (3, 4, 2)):
+        only = [l if first <= g < end else -1 for g, l in enumerate(c.lens)]
+        ref = R.attend(c.q, c.kc, c.vc, c.indptr, only, c.tables, scale=c.scale, prefix_indptr=[first, end], prefix_lens=[c.prefix_lens[i]],
+                       prefix_tables=c.prefix_tables[i:i + 1])
+        R.check_attend(out, lse, ref, c.dtype, slice(c.indptr[first], c.indptr[end]))
+
+
+def test_attend_with_many_prefixes_takes_no_more_than_a_few():
+    """4,096 prefixes of which one serves groups: within five times the call with that one (looked through one after another
+    they took 22 times as long, side by side 1.4)."""
+    import torch
+    groups, took = 256, []
+    for count in (1, 4096):
+        c = Case(n=[4] * groups, lens=[150] * groups, prefixes=[100], prefix_indptr=[0, groups // 2], hq=32, hk=8, page=64, max_group_rows=4)
+        c.prefix_lens, c.prefix_indptr = [100] + [0] * (count - 1), [0] + [groups // 2] * count
+        c.prefix_tables = np.concatenate([c.prefix_tables, np.full((count - 1, c.prefix_tables.shape[1]), -1)])
+        plan, t = c.plan(), c.tensors()
+        out, st, best = torch.empty_like(c.q), status_word(), math.inf
+        for _ in range(8):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(4):
+                plan.attend(**t, out=out, status=st)
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        assert int(st[0]) == 0
+        took.append(best)
+    assert took[1] < 5 * took[0], took
