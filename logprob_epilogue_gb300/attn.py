@@ -59,6 +59,7 @@ _ROPE = "PPPPqqqqPPPPPffiiii"
 _PACK_ROPE = struct.Struct("@" + _ROPE + "0P")
 _PACK_APPEND = struct.Struct("@" + _ROPE + "PqPPPPPi0P")
 _PACK_ATTEND = struct.Struct("@PqPPPPPPPPPPqPPfiii0P")
+_ANY_POSITION = 2 ** 31 - 1  # max_positions of a call without a table
 
 
 class AttnPlan:
@@ -144,9 +145,14 @@ class AttnPlan:
         raise ValueError(f"{name}: expected contiguous {dtype} on CUDA device {self.device}")
 
     def _status(self, x):
-        if x.element_size() != 4 or x.numel() < 1 or x.get_device() != self.device:
+        if x is None or x.element_size() != 4 or x.numel() < 1 or x.get_device() != self.device:
             raise ValueError(f"status: expected one 32-bit word on CUDA device {self.device}")
         return x.data_ptr()
+
+    def _groups(self, group_indptr):
+        if group_indptr is None:
+            raise ValueError("group_indptr: missing")
+        return group_indptr.numel() - 1
 
     def _rope(self, q, k, q_out, k_out, q_weight, k_weight, eps, weight_offset, cos_sin, interleaved, positions, status):
         """The fields of lp_rope_io, in order, and the rows."""
@@ -157,7 +163,7 @@ class AttnPlan:
             qp, qs = self._rows("q", q, want)
             qo, qos = self._rows("q_out", q_out, want)
         elif k is None:
-            raise ValueError("norm_rope: neither q nor k")
+            raise ValueError("neither q nor k")
         else:
             rows = k.shape[0]
         if k is not None:
@@ -165,28 +171,32 @@ class AttnPlan:
             kp, ks = self._rows("k", k, want)
             if k_out is not None:
                 ko, kos = self._rows("k_out", k_out, want)
-        if cos_sin.dim() != 2:
+        if cos_sin is None:
+            table, rot = _ANY_POSITION, 0
+        elif cos_sin.dim() != 2:
             raise ValueError("cos_sin: expected [positions, rot_dim]")
-        table, rot = cos_sin.shape
+        else:
+            table, rot = cos_sin.shape
         return rows, (qp, kp, qo, ko, qs, ks, qos, kos,
                       self._shaped("q_weight", q_weight, self._dtype, self._one_head),
                       self._shaped("k_weight", k_weight, self._dtype, self._one_head),
                       self._flat("cos_sin", cos_sin, self._f32, 0), self._flat("positions", positions, self._i32, rows),
                       self._status(status), eps, weight_offset, table, rot, 1 if interleaved else 0, rows)
 
-    def norm_rope(self, *, cos_sin, positions, status, q=None, k=None, q_out=None, k_out=None, q_weight=None,
+    def norm_rope(self, *, positions, status, cos_sin=None, q=None, k=None, q_out=None, k_out=None, q_weight=None,
                   k_weight=None, eps=1e-6, weight_offset=0.0, interleaved=False, stream=None) -> None:
         """RMS norm (where a weight is given) and position rotation of each head of
         ``q`` [rows, q_heads, head_dim] and ``k`` [rows, kv_heads, head_dim].
         ``cos_sin`` is float32 [positions, rot_dim]: the cosines of the rot_dim / 2
-        angles, then their sines.  Rows with a negative position are skipped."""
+        angles, then their sines; without one nothing is rotated and any position
+        below 2^31 - 1 will do.  Rows with a negative position are skipped."""
         _, rope = self._rope(q, k, q_out, k_out, q_weight, k_weight, eps, weight_offset, cos_sin, interleaved, positions, status)
         _PACK_ROPE.pack_into(self._io, 0, *rope)
         rc = self._norm_rope(self._h, self._at, self._stream(stream))
         if rc:
             _check(rc, "lp_norm_rope")
 
-    def append(self, *, k, v, k_cache, v_cache, group_indptr, lens, block_tables, cos_sin, positions, status, q=None,
+    def append(self, *, k, v, k_cache, v_cache, group_indptr, lens, block_tables, positions, status, cos_sin=None, q=None,
                q_out=None, k_out=None, q_weight=None, k_weight=None, eps=1e-6, weight_offset=0.0, interleaved=False,
                stream=None) -> None:
         """``norm_rope``, with the keys and values of row j of group g written to
@@ -194,7 +204,7 @@ class AttnPlan:
         max_pages]); ``k_out`` is optional."""
         rows, rope = self._rope(q, k, q_out, k_out, q_weight, k_weight, eps, weight_offset, cos_sin, interleaved, positions, status)
         vp, vs = self._rows("v", v, (rows, self._kv_heads, self._dim))
-        groups = group_indptr.numel() - 1
+        groups = self._groups(group_indptr)
         _PACK_APPEND.pack_into(
             self._io, 0, *rope, vp, vs, self._flat("group_indptr", group_indptr, self._i32, 1), self._flat("lens", lens, self._i32, groups),
             self._shaped("block_tables", block_tables, self._i32, (groups, self.desc.max_pages)),
@@ -212,11 +222,13 @@ class AttnPlan:
         over groups, ``prefix_lens`` [prefixes], ``prefix_tables`` [prefixes,
         max_prefix_pages]).  ``lse_out`` is float32 [rows, q_heads]."""
         i32 = self._i32
+        if q is None:
+            raise ValueError("q: missing")
         rows = q.shape[0]
         want = (rows, self._q_heads, self._dim)
         qp, qs = self._rows("q", q, want)
         op, os_ = self._rows("out", out, want)
-        groups = group_indptr.numel() - 1
+        groups = self._groups(group_indptr)
         prefixes = pi = pl = pt = 0
         if prefix_lens is not None:
             prefixes = prefix_lens.numel()

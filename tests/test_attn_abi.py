@@ -157,3 +157,32 @@ class TestRefusals:
             with pytest.raises(ValueError):
                 p.norm_rope(**{**ok, **kw})
         torch.cuda.synchronize()
+
+    def test_python_takes_no_table_and_names_what_is_missing(self):
+        import torch
+        p = self.plan()
+        dev = torch.device("cuda", 0)
+        z = lambda *s, dtype=torch.bfloat16: torch.zeros(*s, dtype=dtype, device=dev)  # noqa: E731
+        i = lambda *s: z(*s, dtype=torch.int32)  # noqa: E731
+        q, k = torch.randn(4, 8, 128, device=dev).bfloat16(), torch.randn(4, 2, 128, device=dev).bfloat16()
+        out, st, pos = z(4, 8, 128), i(1), torch.tensor([0, 5, 1 << 30, -1], dtype=torch.int32, device=dev)
+        out[3] = 7.0
+        p.norm_rope(q=q, q_out=out, positions=pos, status=st)  # no table: nothing is rotated
+        assert torch.equal(out[:3], q[:3]) and bool((out[3] == 7.0).all())
+        kc, vc = z(100, 2, 16, 128), z(100, 2, 16, 128)
+        batch = dict(k_cache=kc, v_cache=vc, group_indptr=torch.tensor([0, 4], dtype=torch.int32, device=dev), lens=i(1), block_tables=i(1, 10), status=st)
+        append = dict(batch, k=k, v=k, positions=pos)
+        p.append(**append)
+        torch.cuda.synchronize()
+        assert torch.equal(kc[0, :, :3].transpose(0, 1), k[:3]) and torch.equal(vc[0, :, :3].transpose(0, 1), k[:3]) and int(st[0]) == 0
+        assert not bool(kc[0, :, 3:].any()) and not bool(vc[0, :, 3:].any())  # the row that is skipped, too
+        attend = dict(batch, q=q, out=out)
+        p.attend(**attend)
+        for call, args, names in ((p.append, append, ("status", "group_indptr", "v")), (p.attend, attend, ("status", "group_indptr", "q", "out")),
+                                  (p.norm_rope, dict(q=q, q_out=out, positions=pos, status=st), ("status", "q_out"))):
+            for name in names:
+                with pytest.raises(ValueError, match=name):
+                    call(**{**args, name: None})
+        with pytest.raises(ValueError, match="neither q nor k"):
+            p.append(**{**append, "k": None})
+        torch.cuda.synchronize()
