@@ -38,8 +38,10 @@
 //   O_i += P_i V     tensor memory x shared -> tensor memory, the first 64
 //                    tokens' part while the softmax of the others runs
 // While one warpgroup works on its S the tensor core runs the other's
-// products.  The running maximum moves only when it grows by more than 2^8
-// (then O and the sum are rescaled), so most tiles touch O not at all.
+// products.  Each row keeps a running maximum and sum (the online softmax of
+// Milakov and Gimelshein, 2018); after a published refinement of it the maximum
+// moves only when it grows by more than 2^8 (then O and the sum are rescaled),
+// so most tiles touch O not at all.
 // P is rounded to the plan's type (the products take nothing wider); S, the
 // maxima, the sums, O and the parts are 32 bits.
 //
@@ -1075,6 +1077,15 @@ constexpr int join_bytes(int sub) { return join_round(sub) * kJoinThreads * (D /
 
 // kSub warps per row and four heads: the round's own tokens that the row sees,
 // then the parts of the row's prefix and of its group's committed tokens.
+//
+// What comes before the wait reads only what kernels ahead of the main one
+// wrote (queries, lengths, tables, masks, the caches), and may: this kernel
+// starts once every block of the main kernel has let it, which each does after
+// its own wait for those kernels' end.  Parts and tables of the scratch are the
+// main kernel's own and are read after the wait for it.
+//
+// With heads of 128 the forms of one and two warps per row spill 28 bytes a
+// thread (F16: 36) at the 64 registers that four blocks per SM leave.
 template <bool kBf16, int D, int kSub>
 __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_join_kernel(const AttendParams p) {
     using H = Half<kBf16>;
