@@ -47,12 +47,12 @@
 //
 // What bounds it, by size (BF16, heads of 128, 32 over 8, in a CUDA graph):
 // - bandwidth, where few rows share a token: 128 groups of 4 rows at contexts up
-//   to 8,192 take 342 us, 6.6 TB/s of keys and values;
+//   to 8,192 take 344 us, 6.5 TB/s of keys and values;
 // - the tensor core, where many rows share a prefix: of 2,048 rows behind 32,768
 //   tokens the prefix's part takes 595 us, 1.85 PFLOP/s (2,700 cycles a pair of
-//   token tiles, the products alone 2,048).  The whole call takes 746 us: then
+//   token tiles, the products alone 2,048).  The whole call takes 750 us: then
 //   come the groups' own tokens (0.5 GB) in 110, and the parts' join in 40;
-// - latency, in short calls: one row at 4,095 tokens takes 15.1 us: the launch and
+// - latency, in short calls: one row at 4,095 tokens takes 15.0 us: the launch and
 //   the split 2.5, the first scores 2.5, two token tiles 4, the join 5.5.
 #include <cuda.h>
 #include <cuda_runtime.h>

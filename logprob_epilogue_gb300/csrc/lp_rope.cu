@@ -20,7 +20,7 @@
 //
 // Bound: bytes in and out, and close behind them the instructions (about 75
 // per word).  16,411 rows of 32 + 8 + 8 heads of 128 lanes, BF16, into a cache:
-// 82 us, 5.8 TB/s; 8,191 rows of 24 + 4 heads of 64 lanes, F16: 13.0 us, 4.6
+// 79 us, 6.0 TB/s; 8,191 rows of 24 + 4 heads of 64 lanes, F16: 13.0 us, 4.6
 // TB/s; one row into a cache: 3.2 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -236,7 +236,7 @@ cudaError_t launch(const RopeParams& p, cudaStream_t stream) {
 
 // Eight heads per task spread a row's factors further, but leave a short call
 // fewer threads and a long chain of its own: with 128 lanes, 16,411 rows of 48
-// heads take 82 us against 89, 512 rows 5.2 us against 4.3; with 64 lanes 8,191
+// heads take 79 us against 82, 512 rows 5.0 us against 4.4; with 64 lanes 8,191
 // rows of 28 heads take 14.8 us against 13.0.
 constexpr long long kManyHeads = 1 << 18;
 
