@@ -482,8 +482,9 @@ typedef struct {
     int32_t device;
     int64_t num_pages;        /* pages of each cache (>= 1) */
     uint32_t flags;           /* LP_PLAN_DEBUG_FORCE_TIMEOUT or 0 */
-    int64_t timeout_ns;       /* limit of each device-side wait (LP_STATUS_TIMEOUT); 0 = 1 s.  Some of lp_attend's
-                               * waits last as long as a block's work: longer than the call itself takes */
+    int64_t timeout_ns;       /* limit of each device-side wait (LP_STATUS_TIMEOUT); 0 = 1 s.  Some waits of
+                               * lp_attend last as long as a block works on one segment: keep the limit above the
+                               * time of a call */
 } lp_attn_desc;
 
 typedef struct lp_attn_s* lp_attn_t;
