@@ -112,6 +112,7 @@ enum {
 #define LP_STATUS_BAD_POSITION 0x40u /* lp_norm_rope, lp_kv_append: a position past the rotation table: row skipped */
 #define LP_STATUS_BAD_PAGE 0x80u     /* a page id outside [0, num_pages): not written, read as zeros */
 #define LP_STATUS_BAD_PREFIX 0x100u  /* lp_attend: a malformed prefix: taken as absent */
+#define LP_STATUS_NO_PAGES 0x200u    /* lp_kv_reserve: the free pages ran out: the groups left over sit the round out */
 
 /* Plan flags. */
 #define LP_PLAN_HOST_STAGING 0x1u     /* also allocate device staging so lp_run_host can be used */
@@ -119,6 +120,7 @@ enum {
 #define LP_PLAN_VOCAB_SHARDS 0x4u     /* also allocate the exchange buffers of lp_run_sharded */
 #define LP_PLAN_DEBUG_FORCE_TIMEOUT 0x100u /* test hook: every bounded wait runs out (no reads) */
 #define LP_PLAN_DEBUG_TRACE 0x200u    /* record a device timeline of each run (see lp_debug_trace) */
+#define LP_ATTN_KV4 0x400u            /* attention plans: the caches are held in 4 bits (lp_kv_append4, lp_attend4) */
 
 typedef struct {
     int32_t max_rows;     /* capacity: rows per run (>= 1) */
@@ -481,7 +483,7 @@ typedef struct {
     int32_t dtype;            /* LP_BF16 or LP_F16: q, k, v, caches, out and norm weights */
     int32_t device;
     int64_t num_pages;        /* pages of each cache (>= 1) */
-    uint32_t flags;           /* LP_PLAN_DEBUG_FORCE_TIMEOUT or 0 */
+    uint32_t flags;           /* LP_PLAN_DEBUG_FORCE_TIMEOUT, LP_ATTN_KV4, or 0 */
     int64_t timeout_ns;       /* limit of each device-side wait (LP_STATUS_TIMEOUT); 0 = 1 s.  Some waits of
                                * lp_attend last as long as a block works on one segment: keep the limit above the
                                * time of a call */
@@ -591,6 +593,117 @@ typedef struct {
 } lp_attend_io;
 
 int lp_attend(lp_attn_t plan, const lp_attend_io* io, void* stream);
+
+/* ---- Pages of a round ----
+ *
+ * lp_kv_reserve lays a round out on the device: which rows each group owns,
+ * the pages that they need beyond those that the group holds, and every row's
+ * position and slot.  It serves plans of either kind of cache.
+ *
+ * lens[g] counts group g's committed tokens (negative: idle), counts[g] the
+ * rows of the round, held[g] the entries of block_tables[g] that are pages of
+ * its own.  free_pages is a ring of `ring` entries; queue = {head, tail}: the
+ * free pages are entries head % ring .. (tail - 1) % ring, oldest first, and
+ * both numbers only grow.
+ *   group_indptr   the sums of counts: group g owns the next counts[g] rows.
+ *   pages          a group needs ceil((lens + counts) / page_size) pages in all.
+ *                  The groups, in order, take those they lack from the head of
+ *                  the queue into block_tables[g][held[g]..].  From the first
+ *                  one on that the rest of the queue does not cover, groups that
+ *                  lack pages get none (LP_STATUS_NO_PAGES).
+ *   idle groups    the pages they hold join the tail in the order of the groups
+ *                  and of their tables; the groups of this call get none of them.
+ *   round_lens     the lens of the round's other calls: lens[g], or -1 for a
+ *                  group without its pages, which so sits the round out.
+ *   held_out, queue_out  held and queue after the call.  They may be held and
+ *                  queue themselves; where they are not, the call can be made
+ *                  again with the same outcome (its writes to block_tables and
+ *                  free_pages are the same ones).
+ *   positions      starts[g] + lens[g] + j for row j of group g (starts NULL: 0;
+ *                  a shared prefix's tokens, say); -1 for rows of idle groups,
+ *                  of groups that sit out, and past the last group, up to `rows`
+ *                  (a captured batch's padding).
+ *   slots          the row's slot: page * page_size + offset; -1 likewise.
+ * A malformed group sits out, and gets no pages (LP_STATUS_BAD_GROUP): a
+ * negative count (taken as 0), more tokens than max_pages pages, held outside
+ * 0..max_pages (that stays as it is, of an idle group too), rows past `rows`
+ * (group_indptr ends at `rows` then).  A queue that holds less than nothing, or more than
+ * `ring`, gives and takes no page (LP_STATUS_BAD_PAGE); nor does a full one take
+ * any.  A slot whose page is outside [0, num_pages) is -1 (LP_STATUS_BAD_PAGE),
+ * a position past 2^31 - 1 too (LP_STATUS_BAD_POSITION).  round_lens must not be
+ * lens, nor may other outputs overlap inputs. */
+typedef struct {
+    const int32_t* lens;     /* [groups] */
+    const int32_t* counts;   /* [groups] */
+    const int32_t* starts;   /* [groups] or NULL */
+    const int32_t* held;     /* [groups] */
+    const int64_t* queue;    /* [2] */
+    int32_t* free_pages;     /* [ring] */
+    int32_t* block_tables;   /* [groups, max_pages] */
+    int32_t* group_indptr;   /* [groups + 1] */
+    int32_t* round_lens;     /* [groups] */
+    int32_t* held_out;       /* [groups] */
+    int64_t* queue_out;      /* [2] */
+    int32_t* positions;      /* [rows] */
+    int64_t* slots;          /* [rows] or NULL */
+    uint32_t* status;        /* [1] */
+    int32_t rows;
+    int32_t groups;
+    int32_t ring;            /* >= 1 */
+} lp_reserve_io;
+
+int lp_kv_reserve(lp_attn_t plan, const lp_reserve_io* io, void* stream);
+
+/* ---- A cache in 4 bits ----
+ *
+ * A plan with LP_ATTN_KV4 takes these calls in place of lp_kv_append and
+ * lp_attend (which answer LP_ESTATE, as these do on other plans).  Its caches
+ * are [num_pages, kv_heads, page_size, head_dim / 2] bytes, lanes 2i (low half)
+ * and 2i + 1 of a head in byte i, each an e2m1 number (0, 0.5, 1, 1.5, 2, 3, 4,
+ * 6 and their negatives), with scales [num_pages, kv_heads, page_size,
+ * head_dim / 16], one e4m3 byte for 16 consecutive lanes:
+ *   value = code * scale * factor,
+ * factor a number of the caller's for the whole cache.  State, pages, groups
+ * and status are those of the calls above.
+ *
+ * lp_kv_append4 is lp_kv_append, the rows' keys (rounded to the plan's type as
+ * k_out has them) and values going to the cache in 4 bits.  Of 16 lanes x:
+ *   scale = the e4m3 number nearest to max |x| / (6 factor), at most 448,
+ *   code  = the e2m1 number nearest to x / (scale factor), at most 6 (0 where
+ *           the scale is 0), the sign that of x,
+ * ties to even, both rounded from the exact quotient: so factor is a power of
+ * two.  A NaN or an infinity among the 16 makes the scale NaN, and with it all of
+ * them.  k_held and v_held, where given, receive the values that the codes stand
+ * for, in the plan's type (exact, but where factor takes them out of its range),
+ * of every row that k_out would be written for. */
+typedef struct {
+    lp_append_io append;   /* k_cache, v_cache: the codes */
+    void* k_scales;
+    void* v_scales;
+    void* k_held;          /* [rows, kv_heads, head_dim] or NULL */
+    void* v_held;          /* the same */
+    int64_t k_held_stride, v_held_stride;
+    float k_factor;        /* a power of two, 2^-60 .. 2^60 */
+    float v_factor;
+} lp_append4_io;
+
+int lp_kv_append4(lp_attn_t plan, const lp_append4_io* io, void* stream);
+
+/* lp_attend over such a cache: its formula, statuses and zeros, with k and v the
+ * values that the cache stands for (any factor > 0).  A page out of range reads
+ * as zeros.  The products take values and probabilities of 16 bits, in which
+ * a code times its scale is exact; BF16 queries are first multiplied by a power
+ * of two per row and head that brings their largest lane near 2^14 (undone in the
+ * scores): a lane under 2^-28 of that largest one loses bits. */
+typedef struct {
+    lp_attend_io attend;   /* k_cache, v_cache: the codes */
+    const void* k_scales;
+    const void* v_scales;
+    float k_factor;        /* > 0 */
+    float v_factor;        /* > 0 */
+} lp_attend4_io;
+
+int lp_attend4(lp_attn_t plan, const lp_attend4_io* io, void* stream);
 
 /* Message of an LP_E* code. */
 const char* lp_strerror(int code);

@@ -33,11 +33,13 @@ STATUS_BAD_TEMPERATURE = 0x20
 STATUS_BAD_POSITION = 0x40
 STATUS_BAD_PAGE = 0x80
 STATUS_BAD_PREFIX = 0x100
+STATUS_NO_PAGES = 0x200
 PLAN_HOST_STAGING = 0x1
 PLAN_READ_AHEAD = 0x2
 PLAN_VOCAB_SHARDS = 0x4
 PLAN_DEBUG_FORCE_TIMEOUT = 0x100
 PLAN_DEBUG_TRACE = 0x200
+ATTN_KV4 = 0x400
 
 ERRORS = {0: "LP_OK", -1: "LP_EINVAL", -2: "LP_ESHAPE", -3: "LP_EALIGN", -4: "LP_ECAPACITY",
           -5: "LP_EDTYPE", -6: "LP_ECUDA", -7: "LP_ESTATE", -8: "LP_ESCRATCH"}
@@ -49,7 +51,7 @@ EXPORTS = ("lp_plan_create", "lp_plan_destroy", "lp_plan_scratch_bytes", "lp_bin
            "lp_plan_tiles_per_row", "lp_run_static", "lp_score", "lp_bind_clip", "lp_debug_occupy",
            "lp_chain_verify", "lp_run_sharded",
            "lp_attn_create", "lp_attn_destroy", "lp_attn_scratch_bytes", "lp_norm_rope", "lp_kv_append", "lp_attend",
-           "lp_strerror", "lp_last_cuda_error")
+           "lp_kv_reserve", "lp_kv_append4", "lp_attend4", "lp_strerror", "lp_last_cuda_error")
 
 
 class PlanDesc(ctypes.Structure):
@@ -159,7 +161,7 @@ def lib() -> ctypes.CDLL:
         L.lp_attn_destroy.argtypes = [P]
         L.lp_attn_scratch_bytes.argtypes = [P]
         L.lp_attn_scratch_bytes.restype = ctypes.c_size_t
-        for name in ("lp_norm_rope", "lp_kv_append", "lp_attend"):
+        for name in ("lp_norm_rope", "lp_kv_append", "lp_attend", "lp_kv_reserve", "lp_kv_append4", "lp_attend4"):
             getattr(L, name).argtypes = [P, P, P]
         L.lp_strerror.argtypes = [ctypes.c_int]
         L.lp_strerror.restype = ctypes.c_char_p

@@ -23,6 +23,8 @@ struct lp_attn_s {
     int grid;
     unsigned char* scratch;
     lp::AttendScratch sc;
+    lp::Reserved* reserved;  // scratch of lp_kv_reserve
+    long long* ends;
     EncodeTiled encode;
 };
 
@@ -35,7 +37,7 @@ using lp::DeviceGuard;
 static_assert(lp::kAttnMaxGroupRows == LP_ATTN_MAX_GROUP_ROWS, "row mask bits");
 static_assert(lp::kStatusAttnBadGroup == LP_STATUS_BAD_GROUP && lp::kStatusAttnTimeout == LP_STATUS_TIMEOUT &&
                   lp::kStatusBadPosition == LP_STATUS_BAD_POSITION && lp::kStatusBadPage == LP_STATUS_BAD_PAGE &&
-                  lp::kStatusBadPrefix == LP_STATUS_BAD_PREFIX,
+                  lp::kStatusBadPrefix == LP_STATUS_BAD_PREFIX && lp::kStatusNoPages == LP_STATUS_NO_PAGES,
               "status bits");
 
 int page_shift_of(int page_size) {
@@ -59,12 +61,12 @@ int check_desc(const lp_attn_desc* d) {
     // token indexes are 32-bit (page ids and slots are combined in 64 bits)
     if (((int64_t)d->max_pages + 1) * d->page_size > 0x3FFFFFFF) return LP_ECAPACITY;
     if (((int64_t)d->max_prefix_pages + 1) * d->page_size > 0x3FFFFFFF) return LP_ECAPACITY;
-    if ((d->flags & ~(uint32_t)LP_PLAN_DEBUG_FORCE_TIMEOUT) != 0 || d->timeout_ns < 0) return LP_EINVAL;
+    if ((d->flags & ~(uint32_t)(LP_PLAN_DEBUG_FORCE_TIMEOUT | LP_ATTN_KV4)) != 0 || d->timeout_ns < 0) return LP_EINVAL;
     return LP_OK;
 }
 
 struct Layout {
-    size_t seg_units, units, gave_up, part_o, part_ml, total;  // the tables come first
+    size_t seg_units, units, gave_up, part_o, part_ml, reserved, ends, total;  // the tables come first
     long long prefix_slots, group_slots;
     int group_rows;
 };
@@ -91,6 +93,10 @@ Layout layout_of(const lp_attn_desc* d, int grid) {
     off = lp::align_up(off + part_rows * 8);
     L.part_o = off;
     off = lp::align_up(off + part_rows * (size_t)d->head_dim * 4);
+    L.reserved = off;
+    off = lp::align_up(off + (size_t)d->max_groups * sizeof(lp::Reserved));
+    L.ends = off;
+    off = lp::align_up(off + 16);
     L.total = off;
     return L;
 }
@@ -170,6 +176,50 @@ lp::RopeParams rope_params(const lp_attn_s* plan, const lp_rope_io& io) {
     return p;
 }
 
+int check_append(const lp_attn_s* plan, const lp_append_io* io) {
+    const lp_attn_desc& d = plan->d;
+    int rc = check_rope(plan, &io->rope, true);
+    if (rc != LP_OK) return rc;
+    if (io->groups < 0 || io->groups > d.max_groups) return LP_ESHAPE;
+    if (io->rope.rows == 0) return LP_OK;
+    if ((rc = check_rows(plan, io->v, io->v_stride, d.kv_heads)) != LP_OK) return rc;
+    if (!io->k_cache || !io->v_cache || !io->group_indptr) return LP_EINVAL;
+    if (io->groups > 0 && (!io->lens || !io->block_tables)) return LP_EINVAL;
+    if (!aligned(io->k_cache, 16) || !aligned(io->v_cache, 16)) return LP_EALIGN;
+    if (!aligned(io->group_indptr, 4) || !aligned(io->lens, 4) || !aligned(io->block_tables, 4)) return LP_EALIGN;
+    return LP_OK;
+}
+
+lp::RopeParams append_params(const lp_attn_s* plan, const lp_append_io& io) {
+    lp::RopeParams p = rope_params(plan, io.rope);
+    p.v = io.v;
+    p.v_stride = io.v_stride;
+    p.indptr = io.group_indptr;
+    p.lens = io.lens;
+    p.tables = io.block_tables;
+    p.k_cache = io.k_cache;
+    p.v_cache = io.v_cache;
+    p.G = io.groups;
+    p.max_pages = plan->d.max_pages;
+    p.page_shift = plan->page_shift;
+    p.num_pages = plan->d.num_pages;
+    return p;
+}
+
+// Whether the plan's caches are held in 4 bits.
+bool four_bits(const lp_attn_s* plan) { return (plan->d.flags & LP_ATTN_KV4) != 0; }
+
+int check_scales(const void* k_scales, const void* v_scales) {
+    if (!k_scales || !v_scales) return LP_EINVAL;
+    return aligned(k_scales, 16) && aligned(v_scales, 16) ? LP_OK : LP_EALIGN;
+}
+
+// A factor of lp_kv_append4: its quotients are exact only then.
+bool power_of_two(float f) {
+    int e;
+    return std::isfinite(f) && std::frexp(f, &e) == 0.5f && e >= -59 && e <= 61;
+}
+
 }  // namespace
 
 extern "C" {
@@ -221,6 +271,8 @@ int lp_attn_create(lp_attn_t* out, const lp_attn_desc* desc) {
     plan->sc.gave_up = reinterpret_cast<int*>(plan->scratch + L.gave_up);
     plan->sc.part_ml = reinterpret_cast<float2*>(plan->scratch + L.part_ml);
     plan->sc.part_o = reinterpret_cast<float*>(plan->scratch + L.part_o);
+    plan->reserved = reinterpret_cast<lp::Reserved*>(plan->scratch + L.reserved);
+    plan->ends = reinterpret_cast<long long*>(plan->scratch + L.ends);
     plan->sc.prefix_slots = L.prefix_slots;
     plan->sc.group_slots = L.group_slots;
     plan->sc.group_rows = L.group_rows;
@@ -250,36 +302,85 @@ int lp_norm_rope(lp_attn_t plan, const lp_rope_io* io, void* stream) {
 
 int lp_kv_append(lp_attn_t plan, const lp_append_io* io, void* stream) {
     if (!plan || !io) return LP_EINVAL;
+    if (four_bits(plan)) return LP_ESTATE;
+    int rc;
+    if ((rc = check_append(plan, io)) != LP_OK || io->rope.rows == 0) return rc;
+    DeviceGuard guard(plan->d.device);
+    if (!guard.ok) return cuda_fail(cudaGetLastError());
+    const cudaError_t e = lp::launch_rope(append_params(plan, *io), plan->d.dtype, plan->d.head_dim, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? LP_OK : cuda_fail(e);
+}
+
+int lp_kv_append4(lp_attn_t plan, const lp_append4_io* io, void* stream) {
+    if (!plan || !io) return LP_EINVAL;
+    if (!four_bits(plan)) return LP_ESTATE;
+    int rc;
+    if (!power_of_two(io->k_factor) || !power_of_two(io->v_factor)) return LP_EINVAL;
+    if ((rc = check_append(plan, &io->append)) != LP_OK || io->append.rope.rows == 0) return rc;
+    if ((rc = check_scales(io->k_scales, io->v_scales)) != LP_OK) return rc;
+    const int heads = plan->d.kv_heads;
+    if (io->k_held && (rc = check_rows(plan, io->k_held, io->k_held_stride, heads)) != LP_OK) return rc;
+    if (io->v_held && (rc = check_rows(plan, io->v_held, io->v_held_stride, heads)) != LP_OK) return rc;
+    DeviceGuard guard(plan->d.device);
+    if (!guard.ok) return cuda_fail(cudaGetLastError());
+    lp::RopeParams p = append_params(plan, io->append);
+    p.k_scales = static_cast<unsigned char*>(io->k_scales);
+    p.v_scales = static_cast<unsigned char*>(io->v_scales);
+    p.k_held = io->k_held;
+    p.v_held = io->v_held;
+    p.k_held_stride = io->k_held_stride;
+    p.v_held_stride = io->v_held_stride;
+    p.k_factor = io->k_factor;
+    p.v_factor = io->v_factor;
+    const cudaError_t e = lp::launch_rope(p, plan->d.dtype, plan->d.head_dim, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? LP_OK : cuda_fail(e);
+}
+
+int lp_kv_reserve(lp_attn_t plan, const lp_reserve_io* io, void* stream) {
+    if (!plan || !io) return LP_EINVAL;
     const lp_attn_desc& d = plan->d;
-    int rc = check_rope(plan, &io->rope, true);
-    if (rc != LP_OK) return rc;
-    if (io->groups < 0 || io->groups > d.max_groups) return LP_ESHAPE;
-    if (io->rope.rows == 0) return LP_OK;
-    if ((rc = check_rows(plan, io->v, io->v_stride, d.kv_heads)) != LP_OK) return rc;
-    if (!io->k_cache || !io->v_cache || !io->group_indptr) return LP_EINVAL;
-    if (io->groups > 0 && (!io->lens || !io->block_tables)) return LP_EINVAL;
-    if (!aligned(io->k_cache, 16) || !aligned(io->v_cache, 16)) return LP_EALIGN;
-    if (!aligned(io->group_indptr, 4) || !aligned(io->lens, 4) || !aligned(io->block_tables, 4)) return LP_EALIGN;
+    if (io->rows < 0 || io->rows > d.max_rows || io->groups < 0 || io->groups > d.max_groups || io->ring < 1) return LP_ESHAPE;
+    if (!io->queue || !io->queue_out || !io->group_indptr || !io->status || !io->free_pages) return LP_EINVAL;
+    if (io->groups > 0 && (!io->lens || !io->counts || !io->held || !io->block_tables || !io->round_lens || !io->held_out)) return LP_EINVAL;
+    if (io->rows > 0 && !io->positions) return LP_EINVAL;
+    if (io->groups > 0 && io->round_lens == io->lens) return LP_EINVAL;
+    const void* w4[] = {io->lens, io->counts, io->starts, io->held, io->free_pages, io->block_tables, io->group_indptr, io->round_lens,
+                        io->held_out, io->positions, io->status};
+    for (const void* q : w4)
+        if (!aligned(q, 4)) return LP_EALIGN;
+    if (!aligned(io->queue, 8) || !aligned(io->queue_out, 8) || !aligned(io->slots, 8)) return LP_EALIGN;
     DeviceGuard guard(d.device);
     if (!guard.ok) return cuda_fail(cudaGetLastError());
-    lp::RopeParams p = rope_params(plan, io->rope);
-    p.v = io->v;
-    p.v_stride = io->v_stride;
-    p.indptr = io->group_indptr;
+    lp::ReserveParams p{};
     p.lens = io->lens;
+    p.counts = io->counts;
+    p.starts = io->starts;
+    p.held = io->held;
+    p.queue = reinterpret_cast<const long long*>(io->queue);
+    p.free_pages = io->free_pages;
     p.tables = io->block_tables;
-    p.k_cache = io->k_cache;
-    p.v_cache = io->v_cache;
+    p.indptr = io->group_indptr;
+    p.round_lens = io->round_lens;
+    p.held_out = io->held_out;
+    p.queue_out = reinterpret_cast<long long*>(io->queue_out);
+    p.positions = io->positions;
+    p.slots = reinterpret_cast<long long*>(io->slots);
+    p.status = io->status;
+    p.rows = io->rows;
     p.G = io->groups;
+    p.ring = io->ring;
     p.max_pages = d.max_pages;
     p.page_shift = plan->page_shift;
     p.num_pages = d.num_pages;
-    const cudaError_t e = lp::launch_rope(p, d.dtype, d.head_dim, static_cast<cudaStream_t>(stream));
+    p.groups = plan->reserved;
+    p.ends = plan->ends;
+    const cudaError_t e = lp::launch_reserve(p, plan->grid, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? LP_OK : cuda_fail(e);
 }
 
 int lp_attend(lp_attn_t plan, const lp_attend_io* io, void* stream) {
     if (!plan || !io) return LP_EINVAL;
+    if (four_bits(plan)) return LP_ESTATE;
     const lp_attn_desc& d = plan->d;
     if (io->rows < 0 || io->rows > d.max_rows || io->groups < 0 || io->groups > d.max_groups) return LP_ESHAPE;
     if (io->prefixes < 0 || io->prefixes > d.max_prefixes) return LP_ESHAPE;
@@ -337,6 +438,10 @@ int lp_attend(lp_attn_t plan, const lp_attend_io* io, void* stream) {
         return cuda_fail(cudaErrorInvalidValue);
     const cudaError_t e = lp::launch_attend(p, k_map, v_map, d.dtype, d.head_dim, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? LP_OK : cuda_fail(e);
+}
+
+int lp_attend4(lp_attn_t plan, const lp_attend4_io* io, void* stream) {
+    return LP_EINVAL;
 }
 
 }  // extern "C"

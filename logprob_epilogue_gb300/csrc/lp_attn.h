@@ -11,7 +11,8 @@ namespace lp {
 
 constexpr int kAttnMaxGroupRows = 32;
 constexpr unsigned kStatusAttnBadGroup = 0x8u, kStatusAttnTimeout = 0x10u, kStatusBadPosition = 0x40u,
-                   kStatusBadPage = 0x80u, kStatusBadPrefix = 0x100u;
+                   kStatusBadPage = 0x80u, kStatusBadPrefix = 0x100u, kStatusNoPages = 0x200u;
+constexpr int kBlock4 = 16;  // lanes that share a scale in a cache of 4 bits
 
 struct RopeParams {
     const void *q, *k, *v;                 // [rows, heads, D]; v: append only
@@ -29,6 +30,34 @@ struct RopeParams {
     void *k_cache, *v_cache;
     int G, max_pages, page_shift;
     long long num_pages;
+    // append in 4 bits (k_scales != nullptr); k_cache, v_cache: the codes
+    unsigned char *k_scales, *v_scales;
+    void *k_held, *v_held;                 // [rows, kv_heads, D] or null
+    long long k_held_stride, v_held_stride;
+    float k_factor, v_factor;              // powers of two
+};
+
+// A group as lp_kv_reserve's first part leaves it for the second.
+struct Reserved {
+    int first;   // entries of the ring before the group's new pages (of those that it gives back, when idle)
+    int held;    // pages before the call
+    int change;  // new pages; -1 - n: idle, gives n back
+    int lens;    // of the round
+};
+
+struct ReserveParams {
+    const int *lens, *counts, *starts, *held;
+    const long long* queue;
+    int *free_pages, *tables;
+    int *indptr, *round_lens, *held_out;
+    long long* queue_out;
+    int* positions;
+    long long* slots;
+    unsigned int* status;
+    int rows, G, ring, max_pages, page_shift;
+    long long num_pages;
+    Reserved* groups;      // [max_groups] scratch
+    long long* ends;       // [2] scratch: head and tail of the queue before the call
 };
 
 constexpr int kQTile = 128;    // query rows (row, head) of one tensor-core tile
@@ -85,6 +114,7 @@ inline int entry_pieces(int first_slot, int pieces, long long slots, int grid) {
 // Token columns of a box of the caches' tensor maps: a page, or a tile of it.
 inline int cache_box_rows(int page_size) { return page_size < kKTile ? page_size : kKTile; }
 
+cudaError_t launch_reserve(const ReserveParams& p, int grid, cudaStream_t stream);
 cudaError_t launch_rope(const RopeParams& p, int dtype, int head_dim, cudaStream_t stream);
 cudaError_t prepare_attend(int dtype, int head_dim);  // once per plan: kernel attributes
 cudaError_t launch_attend(const AttendParams& p, const CUtensorMap& k_map, const CUtensorMap& v_map, int dtype,

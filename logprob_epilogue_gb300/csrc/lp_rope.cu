@@ -47,8 +47,73 @@ __device__ __forceinline__ void widen8(const uint4& w, float (&x)[8]) {
     }
 }
 
-template <bool kBf16, int D, bool kAppend, int kHeads>  // heads per task
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Eight lanes in 4 bits, their block's scale, and the values they stand for.
+struct Four {
+    uint32_t codes;
+    unsigned char scale;
+    uint4 held;
+};
+
+// The scale and the codes are those of the exact quotients.  A tie of the scale
+// lies at max |x| = 6 m factor with m of five bits, a tie of a code at |x| = b
+// scale factor with b of three: products of at most 7 bits that FP32 holds, and
+// max |x| or |x|, of at most 11 bits itself, is one of them or at least 2^-11
+// away from it (relative).  The scale's quotient is divided with one rounding,
+// which is exact at a tie and crosses none elsewhere.  A lane's is a product
+// with the reciprocal, off by at most 2^-22; rounding that to 2^-15 brings it
+// back to a tie that it stands for and takes it over none.
+template <bool kBf16>
+__device__ __forceinline__ Four four_bits(const uint4& y, float factor) {
+    using H = Half<kBf16>;
+    constexpr float kInf = __builtin_huge_valf();
+    float x[8];
+    widen8<kBf16>(y, x);
+    float top = fabsf(x[0]);
+#pragma unroll
+    for (int e = 1; e < 8; ++e) top = max_nan(top, fabsf(x[e]));
+    top = max_nan(top, __shfl_xor_sync(kFull, top, 1));
+    if (top == kInf) top = __int_as_float(0x7FFFFFFF);  // an infinity has no scale: NaN for the block
+    const float inv = 1.0f / factor;                    // exact
+    uint16_t pair;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(pair) : "f"(0.0f), "f"(__fdiv_rn(top * inv, 6.0f)));
+    uint32_t wide;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(wide) : "h"(pair));
+    const float scale = Half<false>::unpack(wide).x;
+    const float r = scale > 0.0f ? __frcp_rn(scale) * inv : 0.0f;
+    Four f;
+    f.scale = (unsigned char)(pair & 0xFFu);
+    f.codes = 0;
+    uint32_t held[4];
+    const float unit = scale * factor;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float q[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) q[k] = __uint_as_float((__float_as_uint(x[2 * e + k] * r) + 0x80u) & ~0xFFu);
+        uint32_t code, two;
+        asm("{\n\t.reg .b8 c;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %2, %3;\n\tcvt.u32.u8 %0, c;\n\tcvt.rn.f16x2.e2m1x2 %1, c;\n\t}"
+            : "=r"(code), "=r"(two)
+            : "f"(q[1]), "f"(q[0]));
+        f.codes |= code << (8 * e);
+        const float2 v = Half<false>::unpack(two);
+        held[e] = H::pack(v.x * unit, v.y * unit);
+    }
+    f.held = make_uint4(held[0], held[1], held[2], held[3]);
+    return f;
+}
+
+// Where keys and values go.
+enum Cache { kNone, kHalf, kFour };
+
+template <bool kBf16, int D, Cache kCache, int kHeads>  // heads per task
 __global__ void __launch_bounds__(kRopeThreads, kHeads == 8 ? 6 : 8) lp_rope_kernel(RopeParams p) {
+    constexpr bool kAppend = kCache != kNone;
     using H = Half<kBf16>;
     using T = typename H::T;
     constexpr int kLanes = D / 8;                  // threads per head
@@ -169,9 +234,22 @@ __global__ void __launch_bounds__(kRopeThreads, kHeads == 8 ? 6 : 8) lp_rope_ker
     if (kind == 0) dst = reinterpret_cast<T*>(p.q_out) + row * p.q_out_stride + h0 * D + e0;
     else if (kind == 1 && p.k_out != nullptr) dst = reinterpret_cast<T*>(p.k_out) + row * p.k_out_stride + h0 * D + e0;
     T* cache = nullptr;
-    if constexpr (kAppend) {
+    if constexpr (kCache == kHalf) {
         if (slot >= 0) cache = reinterpret_cast<T*>(kind == 1 ? p.k_cache : p.v_cache) + slot * D + e0;
     }
+    unsigned char *codes = nullptr, *scales = nullptr;
+    T* held = nullptr;
+    float factor = 1.0f;
+    if constexpr (kCache == kFour) {
+        if (slot >= 0) {
+            codes = static_cast<unsigned char*>(kind == 1 ? p.k_cache : p.v_cache) + slot * (D / 2) + e0 / 2;
+            scales = (kind == 1 ? p.k_scales : p.v_scales) + slot * (D / kBlock4) + e0 / kBlock4;
+        }
+        factor = kind == 1 ? p.k_factor : p.v_factor;
+        if (kind == 1 && p.k_held != nullptr) held = reinterpret_cast<T*>(p.k_held) + row * p.k_held_stride + h0 * D + e0;
+        if (kind == 2 && p.v_held != nullptr) held = reinterpret_cast<T*>(p.v_held) + row * p.v_held_stride + h0 * D + e0;
+    }
+    const bool stores = kCache == kFour && __any_sync(kFull, kind != 0);  // of the warp: a block's lanes lie in two threads
     const bool norms = p.q_weight != nullptr || p.k_weight != nullptr, turns = p.rot > 0 && !p.interleaved;  // of the call
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
@@ -197,7 +275,9 @@ __global__ void __launch_bounds__(kRopeThreads, kHeads == 8 ? 6 : 8) lp_rope_ker
 #pragma unroll
             for (int e = 0; e < 8; ++e) o[e] = x[e ^ 1];
         }
-        if (!work || i >= n) continue;
+        if constexpr (kCache != kFour) {
+            if (!work || i >= n) continue;
+        }
         uint4 y = w[i];  // values go as they are
         if (kind != 2) {
 #pragma unroll
@@ -210,8 +290,18 @@ __global__ void __launch_bounds__(kRopeThreads, kHeads == 8 ? 6 : 8) lp_rope_ker
             y.z = H::pack(x[4], x[5]);
             y.w = H::pack(x[6], x[7]);
         }
+        if constexpr (kCache == kFour) {
+            Four f = {};
+            if (stores) f = four_bits<kBf16>(y, factor);
+            if (!work || i >= n) continue;
+            if (codes != nullptr) {
+                *reinterpret_cast<uint32_t*>(codes + i * (step / 2)) = f.codes;
+                if ((lane & 1) == 0) scales[i * (step / kBlock4)] = f.scale;
+            }
+            if (held != nullptr) __stcs(reinterpret_cast<uint4*>(held + i * D), f.held);
+        }
         if (dst != nullptr) __stcs(reinterpret_cast<uint4*>(dst + i * D), y);
-        if (kAppend && cache != nullptr) *reinterpret_cast<uint4*>(cache + i * step) = y;
+        if (kCache == kHalf && cache != nullptr) *reinterpret_cast<uint4*>(cache + i * step) = y;
     }
 }
 
@@ -230,8 +320,9 @@ cudaError_t launch(const RopeParams& p, cudaStream_t stream) {
     lc.stream = stream;
     lc.attrs = attr;
     lc.numAttrs = 1;
-    return append ? cudaLaunchKernelEx(&lc, lp_rope_kernel<kBf16, D, true, kHeads>, p)
-                  : cudaLaunchKernelEx(&lc, lp_rope_kernel<kBf16, D, false, kHeads>, p);
+    if (p.k_scales != nullptr) return cudaLaunchKernelEx(&lc, lp_rope_kernel<kBf16, D, kFour, kHeads>, p);
+    return append ? cudaLaunchKernelEx(&lc, lp_rope_kernel<kBf16, D, kHalf, kHeads>, p)
+                  : cudaLaunchKernelEx(&lc, lp_rope_kernel<kBf16, D, kNone, kHeads>, p);
 }
 
 // Eight heads per task spread a row's factors further, but leave a short call
