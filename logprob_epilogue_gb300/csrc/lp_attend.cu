@@ -60,31 +60,18 @@
 
 #include <type_traits>
 
-#include "lp_attn.h"
+#include "lp_join.h"
+#include "lp_split.h"
 #include "lp_tc.h"
 
 namespace lp {
 namespace {
 
-constexpr unsigned kFull = 0xffffffffu;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNegInf = -__builtin_huge_valf();
-constexpr int kThreads = 384;
-constexpr int kWarps = kThreads / 32;
-constexpr int kJoinThreads = 256;
-constexpr int kJoinWarps = kJoinThreads / 32;
 // Tokens of a tile whose probabilities are announced before the others', so that
 // their part of P V runs under the rest of the softmax (2,048 rows behind 32,768
 // tokens: 762 us; 32 tokens 785, 96 790, all at once 809).
 constexpr int kEarly = 64;
 constexpr float kRescale = 8.0f;  // growth of the maximum (log2) that moves it
-// What a run is measured in, by the times of each: a token tile of a one-tile
-// unit is 2, of a two-tile unit 3, and every unit 4 more (its queries, first
-// loads and results).  No run is shorter than a tile, nor one of prefixes than
-// four (every run of a unit leaves a part for the join to read).
-constexpr int kTileCost = 2, kPairCost = 3, kUnitCost = 4;
-constexpr int kLeastPrefix = 4 * kPairCost, kLeastGroup = kPairCost;
 // Registers: the softmax warpgroups hold 128 scores per thread.  The split's
 // sum is what the block is launched with, 384 x 168.
 constexpr int kRegsLaunch = 168, kRegsSoftmax = 200, kRegsOther = 104;
@@ -100,307 +87,16 @@ struct Cfg {
     static constexpr int kCtl = (2 + kSlots) * kTileBytes;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// The call's vectors are read with ordinary loads: the kernels are resident
-// before the kernel that writes them has ended, and a read-only load might be
-// moved ahead of the wait for that.
-
-// One verify group: its rows and committed tokens.  n = 0: idle or malformed.
-struct Group {
-    int r0, n, len;
-    bool bad;
-};
-
-__device__ __forceinline__ Group load_group(const AttendParams& p, int g) {
-    Group x;
-    const int r0 = p.indptr[g], r1 = p.indptr[g + 1];
-    x.r0 = r0;
-    x.len = p.lens[g];
-    const long long n = (long long)r1 - r0;
-    x.bad = r0 < 0 || r1 > p.rows || n < 0 || n > p.max_group_rows ||
-            (x.len >= 0 && (long long)x.len + n > ((long long)p.max_pages << p.page_shift));
-    x.n = x.bad || x.len < 0 ? 0 : (int)n;
-    return x;
-}
-
-// Prefix i: its groups, their rows, its tokens.  n = 0: none, or malformed.
-struct Prefix {
-    int g0, g1, r0, n, len;
-    bool bad;
-};
-
-__device__ __forceinline__ Prefix load_prefix(const AttendParams& p, int i) {
-    Prefix x;
-    x.g0 = p.prefix_indptr[i];
-    x.g1 = p.prefix_indptr[i + 1];
-    x.len = p.prefix_lens[i];
-    x.bad = x.g0 < 0 || x.g1 < x.g0 || x.g1 > p.G || x.len < 0 ||
-            (long long)x.len > ((long long)p.max_prefix_pages << p.page_shift);
-    x.r0 = x.n = 0;
-    if (!x.bad) {
-        const int r0 = p.indptr[x.g0], r1 = p.indptr[x.g1];
-        x.bad = r0 < 0 || r1 < r0 || r1 > p.rows;
-        if (!x.bad) x.r0 = r0, x.n = r1 - r0;
-    }
-    return x;
-}
-
-// Segment s: prefixes 0..P-1, then the groups' committed tokens.
-struct Seg {
-    int r0, n, len;
-    int tiles, units;  // token tiles; units per key-value head; tiles = 0: no work
-    int dealt;         // of all heads' units, those that go round the blocks whole
-    bool bad;
-    __device__ __forceinline__ int left(const AttendParams& p) const { return tiles > 0 ? units * p.kv_heads - dealt : 0; }
-    int cost;          // of a token tile
-    __device__ __forceinline__ long long span() const { return (long long)tiles * cost + kUnitCost; }  // of a unit in a run
-    __device__ __forceinline__ unsigned long long work(const AttendParams& p) const { return (unsigned long long)(span() * left(p)); }
-};
-
-__device__ __forceinline__ Seg load_seg(const AttendParams& p, int s) {
-    Seg x;
-    if (s < p.P) {
-        const Prefix f = load_prefix(p, s);
-        x.r0 = f.r0, x.n = f.n, x.len = f.len, x.bad = f.bad;
-    } else {
-        const Group f = load_group(p, s - p.P);
-        x.r0 = f.r0, x.n = f.n, x.len = f.len, x.bad = f.bad;
-    }
-    x.units = (x.n + 2 * p.rows_per_tile - 1) / (2 * p.rows_per_tile);
-    x.tiles = x.n > 0 ? (x.len + kKTile - 1) / kKTile : 0;
-    x.cost = x.n > p.rows_per_tile ? kPairCost : kTileCost;
-    x.dealt = s < p.P && x.tiles > 0 ? x.units * p.kv_heads / p.grid * p.grid : 0;
-    return x;
-}
-
-// The units' cost, `total` in all, cut into one run per block: blocks
-// 0..more-1 take per + 1, the others per.
-struct Runs {
-    unsigned long long total, per;
-    int blocks, more;
-    __device__ __forceinline__ unsigned long long start(int c) const { return per * c + (c < more ? c : more); }
-    __device__ __forceinline__ int block_of(unsigned long long t) const {
-        const unsigned long long big = (per + 1) * more;
-        return t < big ? (int)quotient(t, per + 1) : more + (int)quotient(t - big, per);
-    }
-    static __device__ __forceinline__ unsigned long long quotient(unsigned long long a, unsigned long long b) {
-        return ((a | b) >> 32) == 0 ? (unsigned)a / (unsigned)b : a / b;  // the 64-bit division is slow
-    }
-};
-
-__device__ __forceinline__ Runs make_runs(unsigned long long total, int grid, int kind) {
-    Runs r;
-    r.total = total;
-    // a run as long as a tile holds the start of one, wherever it lies among a unit's tiles
-    const unsigned long long most = Runs::quotient(total, kind == 0 ? kLeastPrefix : kLeastGroup);
-    r.blocks = most < (unsigned long long)grid ? (int)most : grid;
-    if (r.blocks == 0 && total > 0) r.blocks = 1;
-    r.per = r.blocks > 0 ? Runs::quotient(total, r.blocks) : 0;
-    r.more = (int)(total - r.per * r.blocks);
-    return r;
-}
-
-// Index of row 0 of a piece's part (tile or warpgroup `set`); -1: past the
-// scratch (only overlapping prefixes can ask for that).
-__device__ __forceinline__ long long part_row(const AttendParams& p, bool prefix, long long slot, int set) {
-    if (prefix) return slot < p.sc.prefix_slots ? (slot * 2 + set) * kQTile : -1;
-    if (slot >= p.sc.group_slots) return -1;
-    return p.sc.prefix_slots * 2 * kQTile + (slot * 2 + set) * p.sc.group_rows;
-}
-
-// Where a unit that is not dealt out is entered for the join; -1 as above.
-__device__ __forceinline__ long long unit_index(const AttendParams& p, bool prefix, int unit) {
-    if (prefix) return unit < p.sc.prefix_slots ? unit : -1;
-    return unit < p.sc.group_slots ? p.sc.prefix_slots + unit : -1;
-}
-
-// A part's results lie chunk by chunk, four lanes of the head of every row
-// side by side (a warp's stores are whole lines): index of a float4, `base`
-// the part's first row and `cap` the rows it has room for.
-template <int D>
-__device__ __forceinline__ long long part_chunk(long long base, int cap, int row, int chunk) {
-    return base * (D / 4) + (long long)chunk * cap + row;
-}
-
-// A block's share of one unit.
-struct Piece {
-    int row, rows;      // first row and rows of the unit; rows = 0: the run is done
-    int kvh, tiles;
-    int left;           // tokens from its first tile to the segment's end
-    int part_stride;    // rows between the parts of its two tiles (or warpgroups)
-    long long part;     // row 0 of its first part; -1: past the scratch (only overlapping prefixes can ask for that)
-};
-
-// Where a block's run begins: its first segment, the tiles and units before it.
-struct Start {
-    unsigned long long off;
-    int seg, units;
-    Seg s;
-};
-
-// Walks a block's pieces: its share of the units that go round whole, then its
-// run of the other prefix units' tiles, then of the groups'.
-struct Walk {
-    Runs runs[2], run;                 // of prefixes, of groups; the current
-    unsigned long long begin[2], finish[2];  // this block's
-    const Start* start;
-    int kind;
-    int deal, deal_end, round, dealt;  // segments with units that go round; rounds dealt; units of earlier segments
-    unsigned long long pos, end, off;  // off: tiles before the segment
-    int seg, units, cta;               // units: the segment's first slot less cta
-    Seg s;
-    __device__ __forceinline__ void enter(int k) {
-        kind = k;
-        run = runs[k];
-        pos = begin[k], end = finish[k];
-        off = start[k].off, seg = start[k].seg, units = start[k].units, s = start[k].s;
-    }
-    const int* table;                  // pages of the piece, and its first token
-    long long token;
-    __device__ __forceinline__ void fill(const AttendParams& p, Piece& x, int sg, const Seg& y, int unit, int t0, int tiles, long long slot) {
-        const bool prefix = sg < p.P;
-        x.tiles = tiles;
-        x.kvh = unit / y.units;
-        const int first = (unit - x.kvh * y.units) * 2 * p.rows_per_tile;
-        x.row = y.r0 + first;
-        x.rows = y.n - first < 2 * p.rows_per_tile ? y.n - first : 2 * p.rows_per_tile;
-        x.left = y.len - t0 * kKTile;
-        table = prefix ? p.prefix_tables + (long long)sg * p.max_prefix_pages : p.tables + (long long)(sg - p.P) * p.max_pages;
-        token = (long long)t0 * kKTile;
-        x.part = part_row(p, prefix, slot, 0);
-        x.part_stride = prefix ? kQTile : p.sc.group_rows;
-    }
-    __device__ __forceinline__ bool next(const AttendParams& p, Piece& x) {
-        while (deal < deal_end) {
-            const Seg y = load_seg(p, deal);
-            const int unit = round * p.grid + cta;
-            if (unit < y.dealt) {
-                ++round;
-                fill(p, x, deal, y, unit, 0, y.tiles, dealt + unit);
-                return true;
-            }
-            dealt += y.dealt;
-            ++deal;
-            round = 0;
-        }
-        while (pos < end || kind == 0) {
-            if (pos >= end) {
-                enter(1);
-                continue;
-            }
-            const unsigned long long work = s.work(p);
-            if (pos >= off + work) {
-                off += work;
-                units += s.left(p);
-                s = load_seg(p, ++seg);
-                continue;
-            }
-            // the unit's cost lies before its tiles, and a tile belongs to the run that its start lies in
-            const unsigned long long rel = pos - off, rest = end - pos, span = s.span();
-            const int unit = (int)Runs::quotient(rel, span);
-            const long long u0 = (long long)(rel - unit * span), u1 = rest < span - u0 ? u0 + (long long)rest : (long long)span;
-            pos += u1 - u0;
-            const int t0 = u0 > kUnitCost ? (int)((u0 - kUnitCost + s.cost - 1) / s.cost) : 0;
-            const int t1 = u1 > kUnitCost ? (int)((u1 - kUnitCost + s.cost - 1) / s.cost) : 0;
-            if (t1 <= t0) continue;
-            fill(p, x, seg, s, s.dealt + unit, t0, t1 - t0, (long long)units + unit + cta);
-            if (t0 == 0 && (threadIdx.x & 31) == 0) {
-                // for the join: the unit's first slot and how many blocks have a piece of it
-                const unsigned long long last = off + unit * span + kUnitCost + (unsigned long long)(s.tiles - 1) * s.cost;
-                const long long at = unit_index(p, kind == 0, units + unit);
-                if (at >= 0) p.sc.units[at] = make_int2(units + unit + cta, t1 == s.tiles ? 1 : run.block_of(last) - cta + 1);
-            }
-            return true;
-        }
-        x.rows = 0;
-        return false;
-    }
-};
-
 constexpr int kPieces = 8;        // pieces the fetching warp may be ahead
 constexpr int kPieceReaders = 11; // warps that read each: two of the products, one that loads queries, eight of softmax
 
-struct Ctl {
+struct Ctl : PlanCtl<Pairs> {
     uint64_t full[10], empty[10], piece_full[kPieces], piece_empty[kPieces];
     Piece piece[kPieces];
     uint64_t q_full[2], q_free[2], s_full[2], p_early[2], p_ready[2], pv_done[2], o_free[2], q_grant, clean, drain;
-    unsigned long long sum[kWarps][3];
-    int sum_dealt[kWarps], deal_first, deal_last;
-    Start start[2];
     uint32_t tmem, issued, batches[2];  // ring fills under way or done; see take_turn
     int abort;
 };
-
-// The call's tiles and units: every thread sums its share of the segments,
-// the block scans the sums, and the thread that holds the block's first tile
-// names its segment.  Block 0 leaves the offsets for the join.  False: the
-// block has no work.
-__device__ __forceinline__ bool plan_run(const AttendParams& p, Ctl* ctl, Runs (&runs)[2]) {
-    const int S = p.P + p.G, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (S + kThreads - 1) / kThreads;
-    const int s0 = tid * per < S ? tid * per : S, s1 = s0 + per < S ? s0 + per : S;
-    // of prefixes and of groups; units: slots of units that do not go round, of prefixes in the high half
-    unsigned long long cost0 = 0, cost1 = 0, units = 0;
-    int dealt = 0, first = S, last = -1;
-    for (int s = s0; s < s1; ++s) {
-        const Seg x = load_seg(p, s);
-        (s < p.P ? cost0 : cost1) += x.work(p);
-        units += (unsigned long long)x.left(p) << (s < p.P ? 32 : 0);
-        dealt += x.dealt;
-        if (x.dealt > 0) {
-            if (last < 0) first = s;
-            last = s;
-        }
-        if (x.bad && blockIdx.x == 0) atomicOr(p.status, s < p.P ? kStatusBadPrefix : kStatusAttnBadGroup);
-    }
-    unsigned long long i0 = cost0, i1 = cost1, iu = units;
-    int id = dealt;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long a = __shfl_up_sync(kFull, i0, o), b = __shfl_up_sync(kFull, i1, o), c = __shfl_up_sync(kFull, iu, o);
-        const int d = __shfl_up_sync(kFull, id, o);
-        if (lane >= o) i0 += a, i1 += b, iu += c, id += d;
-    }
-    if (lane == 31) ctl->sum[warp][0] = i0, ctl->sum[warp][1] = i1, ctl->sum[warp][2] = iu, ctl->sum_dealt[warp] = id;
-    if (tid == 0) ctl->deal_first = S, ctl->deal_last = -1;
-    __syncthreads();
-    if (last >= 0) atomicMin(&ctl->deal_first, first), atomicMax(&ctl->deal_last, last);
-    unsigned long long b0 = 0, b1 = 0, bu = 0, total0 = 0, total1 = 0;
-    int bd = 0, all_dealt = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w == warp) b0 = total0, b1 = total1, bd = all_dealt;
-        if (w < warp) bu += ctl->sum[w][2];
-        total0 += ctl->sum[w][0];
-        total1 += ctl->sum[w][1];
-        all_dealt += ctl->sum_dealt[w];
-    }
-    unsigned long long at0 = b0 + i0 - cost0, at1 = b1 + i1 - cost1, u = bu + iu - units;
-    int d = bd + id - dealt;
-    runs[0] = make_runs(total0, gridDim.x, 0);
-    runs[1] = make_runs(total1, gridDim.x, 1);
-    const int cta = blockIdx.x;
-    const unsigned long long lo0 = cta < runs[0].blocks ? runs[0].start(cta) : ~0ull, lo1 = cta < runs[1].blocks ? runs[1].start(cta) : ~0ull;
-    if (cta == 0 || (lo0 >= at0 && lo0 < at0 + cost0) || (lo1 >= at1 && lo1 < at1 + cost1)) {
-        for (int s = s0; s < s1; ++s) {
-            const Seg x = load_seg(p, s);
-            const int kind = s < p.P ? 0 : 1;
-            const unsigned long long work = x.work(p), off = kind == 0 ? at0 : at1, lo = kind == 0 ? lo0 : lo1;
-            const int before = (int)(kind == 0 ? (u >> 32) + all_dealt : u & 0xFFFFFFFFull);  // slots: the dealt units', then the others'
-            if (cta == 0) p.sc.seg_units[s] = make_int2(before, d);
-            if (lo >= off && lo < off + work) ctl->start[kind].off = off, ctl->start[kind].seg = s, ctl->start[kind].units = before, ctl->start[kind].s = x;
-            (kind == 0 ? at0 : at1) += work;
-            u += (unsigned long long)x.left(p) << (kind == 0 ? 32 : 0);
-            d += x.dealt;
-        }
-    }
-    return all_dealt > 0 || cta < runs[0].blocks || cta < runs[1].blocks;
-}
 
 __device__ __forceinline__ unsigned long long pack2(uint32_t a, uint32_t b) {
     unsigned long long r;
@@ -610,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.launch_dependents;");
     if (warp == 2) tc::tmem_alloc(&ctl->tmem, kTmemCols);  // not held while waiting: the kernel ahead may need it to end
     Runs runs[2];  // of prefixes, of groups
-    const bool any = plan_run(p, ctl, runs);
+    const bool any = plan_run<Pairs>(p, ctl, runs);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -729,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr int kHalves = D / 64;
             const int step = p.page_shift < 7 ? 1 << p.page_shift : kKTile;  // tokens per box
             const int tok = lane / kHalves * step, half = lane % kHalves;
-            Walk walk;
+            Walk<Pairs> walk;
             walk.cta = blockIdx.x;
             walk.deal = ctl->deal_first;
             walk.deal_end = ctl->deal_last + 1;
@@ -997,269 +693,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// ---- the join
-//
-// A warp has four query heads of a row, eight threads each: a thread holds
-// D / 8 lanes of its head, as D / 64 runs of eight.  What it reads (keys and
-// values of the round's own tokens, then parts) comes by asynchronous copies
-// into shared memory, several at a time, and is taken up by short loops: a
-// call's join runs once through its code, and unrolled loads and sums are bound
-// by the fetch of their instructions (188 rows of 40 heads: 74.5 us against 67
-// for the whole call).  Neighbouring threads have neighbouring heads, which lie
-// side by side in a part: a copy writes shared memory by runs that are
-// contiguous on both sides, and with a head's threads side by side took 31
-// writes per instruction (one row at 4,095 tokens: 19.2 us against 15.6).
-template <int D>
-struct Acc {
-    static constexpr int kE = D / 8;
-    float o[kE], m, l;  // in base 2
-    __device__ __forceinline__ void add(float s, float w, const float (&v)[kE]) {  // a part: maximum s, sum w, result v
-        const float top = fmaxf(m, s), base = top == kNegInf ? 0.0f : top;
-        const float f = ex2(m - base), g = ex2(s - base);
-        l = l * f + w * g;
-#pragma unroll
-        for (int e = 0; e < kE; ++e) o[e] = o[e] * f + g * v[e];
-        m = top;
-    }
-};
-
-template <bool kBf16>
-__device__ __forceinline__ void widen8(const uint4& w, float* x) {
-    using H = Half<kBf16>;
-    const float2 a = H::unpack(w.x), b = H::unpack(w.y), c = H::unpack(w.z), d = H::unpack(w.w);
-    x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y, x[4] = c.x, x[5] = c.y, x[6] = d.x, x[7] = d.y;
-}
-
-// The parts of a row's head from one segment: what the call's arguments say,
-// and after the main kernel what its tables say.
-struct Parts {
-    int seg, unit, dealt;     // seg: -1 for none; of all heads' units
-    int row, cap, set, sets;  // row of the unit; the parts of a piece that are its: sets of them from `set` on
-    int count;
-    long long slot;
-    __device__ __forceinline__ void find(const AttendParams& p, int segment, int of, int head) {  // of: the row
-        seg = -1;
-        if (segment < 0) return;
-        const Seg s = load_seg(p, segment);
-        if (s.tiles == 0) return;
-        seg = segment;
-        const int rt = p.rows_per_tile, rel = of - s.r0, u = rel / (2 * rt), in = rel - u * 2 * rt, kvh = head / p.share;
-        const bool two = s.n - u * 2 * rt > rt;
-        unit = kvh * s.units + u;
-        dealt = s.dealt;
-        set = two && in >= rt ? 1 : 0;
-        sets = two ? 1 : 2;  // a unit of one tile: a part of each warpgroup
-        row = (in - set * rt) * p.share + head - kvh * p.share;
-        cap = segment < p.P ? kQTile : p.sc.group_rows;
-    }
-    __device__ __forceinline__ int2 first_slots(const AttendParams& p) const { return seg >= 0 ? p.sc.seg_units[seg] : make_int2(0, 0); }
-    __device__ __forceinline__ void locate(const AttendParams& p, int2 base) {
-        slot = (long long)base.y + unit;
-        int pieces = seg >= 0 ? 1 : 0;
-        if (pieces != 0 && unit >= dealt) {
-            const long long at = unit_index(p, seg < p.P, base.x + unit - dealt);
-            const int2 e = at >= 0 ? p.sc.units[at] : make_int2(0, 0);
-            slot = e.x;
-            pieces = entry_pieces(e.x, e.y, seg < p.P ? p.sc.prefix_slots : p.sc.group_slots, p.grid);
-        }
-        count = pieces * sets;
-    }
-    __device__ __forceinline__ long long part(const AttendParams& p, int k) const {
-        return part_row(p, seg < p.P, slot + (sets == 1 ? k : k >> 1), sets == 1 ? set : k & 1);
-    }
-};
-
-// Tokens or parts on their way to a thread at a time.
-__host__ __device__ constexpr int join_round(int sub) { return sub > 2 ? 6 : 3; }
-__host__ __device__ constexpr int join_blocks(int sub) { return sub > 2 ? 2 : 4; }  // per SM
-template <int D>
-constexpr int join_bytes(int sub) { return join_round(sub) * kJoinThreads * (D / 32 * 16 + 8); }
-
-// kSub warps per row and four heads: the round's own tokens that the row sees,
-// then the parts of the row's prefix and of its group's committed tokens.
-//
-// What comes before the wait reads only what kernels ahead of the main one
-// wrote (queries, lengths, tables, masks, the caches), and may: this kernel
-// starts once every block of the main kernel has let it, which each does after
-// its own wait for those kernels' end.  Parts and tables of the scratch are the
-// main kernel's own and are read after the wait for it.
-//
-// With heads of 128 the forms of one and two warps per row spill 28 bytes a
-// thread (F16: 36) at the 64 registers that four blocks per SM leave.
-template <bool kBf16, int D, int kSub>
-__global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_join_kernel(const AttendParams p) {
-    using H = Half<kBf16>;
-    using T = typename H::T;
-    constexpr int kE = D / 8, kRuns = D / 64, kRound = join_round(kSub);
-    // what is on its way to a warp, 16 bytes of every thread side by side
-    extern __shared__ __align__(16) unsigned char smem[];
-    uint4* stage = reinterpret_cast<uint4*>(smem) + threadIdx.x;
-    float2* stage_ml = reinterpret_cast<float2*>(smem + kRound * 2 * kRuns * kJoinThreads * 16) + threadIdx.x;
-    auto place = [](int h, int c) { return h * 8 + (c ^ 2 * h); };
-    auto staged = [&](int b, int c) -> uint4& { return stage[(b * 2 * kRuns + c) * kJoinThreads]; };
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % kSub, l = lane >> 2;
-    const int row = blockIdx.x, head = (blockIdx.y * (kJoinWarps / kSub) + warp / kSub) * 4 + (lane & 3);
-    __shared__ int served_by;  // the prefix of the row
-    if (threadIdx.x == 0) served_by = p.P;
-    const int g = block_group_of(p.indptr, p.G, row);  // (a barrier)
-    const bool mine = g >= 0;
-    const bool exists = mine && head < p.q_heads;
-    Group grp = {0, 0, 0, false};
-    if (mine) grp = load_group(p, g);
-    Acc<D> a;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) a.o[e] = 0.0f;
-    a.m = kNegInf, a.l = 0.0f;
-    if (grp.n > 0) {
-        float q[kE];
-#pragma unroll
-        for (int r = 0; r < kRuns; ++r)
-            widen8<kBf16>(*reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.q) + row * p.q_stride +
-                                                          (long long)(exists ? head : 0) * D + r * 64 + l * 8), q + r * 8);
-        const float c = p.scale * kLog2e;
-        const int j = row - grp.r0;
-        const unsigned mask = p.row_masks != nullptr ? p.row_masks[row] : (2u << j) - 1u;
-        int page = 0;  // lane i: of token i
-        if (lane < grp.n) page = p.tables[(long long)g * p.max_pages + ((grp.len + lane) >> p.page_shift)];
-        const unsigned here = __ballot_sync(kFull, page >= 0 && page < p.num_pages);
-        unsigned todo = mask & (grp.n < 32 ? (1u << grp.n) - 1u : kFull);
-        if (lane == 0 && (todo & ~here) != 0u) atomicOr(p.status, kStatusBadPage);
-        if (kSub > 1) todo &= kFull / ((1u << kSub) - 1u) << sub;  // every kSub-th is this warp's
-        const int n = __popc(todo);
-        // Keys and values lie side by side along a head, so here neighbouring threads copy along a head (to the places of the
-        // threads that read them, turned so that a read meets every bank once).
-        const int copy_head = head - (lane & 3) + (lane >> 3), copy_kvh = copy_head < p.q_heads ? copy_head / p.share : 0;
-        const int copy_to = place(lane >> 3, lane & 7) - lane, read_at = place(lane & 3, l) - lane;
-#pragma unroll 1
-        for (int j = 0, slot = 0; j < n + kRound - 1; ++j) {
-            __syncwarp();
-            if (j < n) {
-                const int i = __ffs(todo) - 1, t = grp.len + i;
-                todo &= todo - 1u;
-                const long long pg = __shfl_sync(kFull, page, i);
-                const long long at = ((((pg * p.kv_heads + copy_kvh) << p.page_shift) + (t & ((1 << p.page_shift) - 1))) * D) + (lane & 7) * 8;
-#pragma unroll
-                for (int r = 0; r < kRuns; ++r) {
-                    if (here >> i & 1u) {
-                        tc::copy16(tc::smem_addr(&staged(slot, r) + copy_to), reinterpret_cast<const T*>(p.k_cache) + at + r * 64);
-                        tc::copy16(tc::smem_addr(&staged(slot, kRuns + r) + copy_to), reinterpret_cast<const T*>(p.v_cache) + at + r * 64);
-                    } else {
-                        (&staged(slot, r))[copy_to] = (&staged(slot, kRuns + r))[copy_to] = make_uint4(0, 0, 0, 0);
-                    }
-                }
-            }
-            tc::copies_commit();
-            slot = slot == kRound - 1 ? 0 : slot + 1;
-            if (j < kRound - 1) continue;
-            tc::copies_wait<kRound - 1>();  // slot: of the oldest
-            __syncwarp();
-            float k[kE], v[kE];
-#pragma unroll
-            for (int r = 0; r < kRuns; ++r) widen8<kBf16>((&staged(slot, r))[read_at], k + r * 8), widen8<kBf16>((&staged(slot, kRuns + r))[read_at], v + r * 8);
-            float s = 0.0f;
-#pragma unroll
-            for (int e = 0; e < kE; ++e) s = fmaf(q[e], k[e], s);
-#pragma unroll
-            for (int o = 16; o > 2; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-            a.add(s * c, 1.0f, v);
-        }
-    }
-    // Of the first prefix that serves the row, of its group's committed tokens.  A prefix has parts for the rows from its first
-    // group's to its last's: a group whose rows lie elsewhere (group_indptr then does not ascend) is not served.
-    Parts shared, own;
-    if (p.P > 0 && grp.n > 0) {  // the same for the block, whose threads look through the prefixes side by side
-        for (int i = threadIdx.x; i < p.P; i += kJoinThreads) {
-            if (p.prefix_indptr[i] > g || p.prefix_indptr[i + 1] <= g) continue;
-            const Prefix x = load_prefix(p, i);
-            if (!x.bad && grp.r0 >= x.r0 && grp.r0 + grp.n <= x.r0 + x.n) {
-                atomicMin(&served_by, i);
-                break;
-            }
-        }
-        __syncthreads();
-    }
-    shared.find(p, grp.n > 0 && served_by < p.P ? served_by : -1, row, exists ? head : 0);
-    own.find(p, grp.n > 0 ? p.P + g : -1, row, exists ? head : 0);
-    __syncwarp();
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    // A block's waits ran out: it left its entries and parts as they were, and no row has a result.  With few blocks the
-    // answer is put together at the end, when the loads have long come in (one row: 15.3 us; here: 15.6); with many it costs
-    // nothing here.
-    int gave_up = 0;
-    for (int b = threadIdx.x; b < p.grid; b += kJoinThreads) gave_up |= p.sc.gave_up[b];
-    const int2 shared_at = shared.first_slots(p), own_at = own.first_slots(p);
-    if constexpr (kSub == 1) gave_up = __syncthreads_or(gave_up);
-    shared.locate(p, shared_at);
-    own.locate(p, own_at);
-    const int count = shared.count + own.count, n = count > sub ? (count - sub + kSub - 1) / kSub : 0;
-#pragma unroll 1
-    for (int j = 0, slot = 0; j < n + kRound - 1; ++j) {
-        if (j < n) {
-            const int k = sub + j * kSub;
-            const bool is_own = k >= shared.count;
-            const int row_at = is_own ? own.row : shared.row, cap = is_own ? own.cap : shared.cap;
-            const long long base = is_own ? own.part(p, k - shared.count) : shared.part(p, k);
-            if (base < 0) {
-                stage_ml[slot * kJoinThreads] = make_float2(kNegInf, 0.0f);
-            } else {
-                tc::copy8(tc::smem_addr(&stage_ml[slot * kJoinThreads]), p.sc.part_ml + base + row_at);
-                const float4* src = reinterpret_cast<const float4*>(p.sc.part_o) + part_chunk<D>(base, cap, row_at, 2 * l);
-#pragma unroll
-                for (int r = 0; r < kRuns * 2; ++r) tc::copy16(tc::smem_addr(&staged(slot, r)), src + (r / 2 * 16 + (r & 1)) * cap);
-            }
-        }
-        tc::copies_commit();
-        slot = slot == kRound - 1 ? 0 : slot + 1;
-        if (j < kRound - 1) continue;
-        tc::copies_wait<kRound - 1>();
-        const float2 ml = stage_ml[slot * kJoinThreads];
-        if (ml.x == kNegInf && ml.y == 0.0f) continue;  // nothing was written
-        float v[kE];
-#pragma unroll
-        for (int r = 0; r < kRuns * 2; ++r) {
-            const uint4 w = staged(slot, r);
-            v[4 * r] = __uint_as_float(w.x), v[4 * r + 1] = __uint_as_float(w.y), v[4 * r + 2] = __uint_as_float(w.z), v[4 * r + 3] = __uint_as_float(w.w);
-        }
-        a.add(ml.x, ml.y, v);
-    }
-    if constexpr (kSub > 1) {  // the warps' sums, in the order of the warps
-        float* part = reinterpret_cast<float*>(smem);  // [e][thread]; then the maxima and sums
-        float2* part_ml = reinterpret_cast<float2*>(part + kE * kJoinThreads);
-        gave_up = __syncthreads_or(gave_up);
-#pragma unroll
-        for (int e = 0; e < kE; ++e) part[e * kJoinThreads + threadIdx.x] = a.o[e];
-        part_ml[threadIdx.x] = make_float2(a.m, a.l);
-        __syncthreads();
-        if (sub != 0) return;
-#pragma unroll 1
-        for (int w = 1; w < kSub; ++w) {
-            const float2 ml = part_ml[threadIdx.x + w * 32];
-            float v[kE];
-#pragma unroll
-            for (int e = 0; e < kE; ++e) v[e] = part[e * kJoinThreads + threadIdx.x + w * 32];
-            if (ml.x != kNegInf || ml.y != 0.0f) a.add(ml.x, ml.y, v);
-        }
-    }
-    if (!exists) return;
-    if (gave_up != 0) {
-#pragma unroll
-        for (int e = 0; e < kE; ++e) a.o[e] = 0.0f;
-        a.m = kNegInf, a.l = 0.0f;
-    }
-    const float inv = a.l > 0.0f ? 1.0f / a.l : (a.l == 0.0f ? 0.0f : a.l);
-    T* dst = reinterpret_cast<T*>(p.out) + row * p.out_stride + (long long)head * D + l * 8;
-#pragma unroll
-    for (int r = 0; r < kRuns; ++r) {
-        uint4 w;
-        w.x = H::pack(a.o[r * 8] * inv, a.o[r * 8 + 1] * inv);
-        w.y = H::pack(a.o[r * 8 + 2] * inv, a.o[r * 8 + 3] * inv);
-        w.z = H::pack(a.o[r * 8 + 4] * inv, a.o[r * 8 + 5] * inv);
-        w.w = H::pack(a.o[r * 8 + 6] * inv, a.o[r * 8 + 7] * inv);
-        *reinterpret_cast<uint4*>(dst + r * 64) = w;
-    }
-    if (p.lse_out != nullptr && l == 0) p.lse_out[(long long)row * p.q_heads + head] = a.l == 0.0f ? kNegInf : a.m * kLn2 + logf(a.l);
-}
-
 template <int D>
 constexpr int smem_bytes() { return Cfg<D>::kCtl + (int)sizeof(Ctl); }
 
@@ -1268,11 +701,7 @@ cudaError_t prepare() {
     static_assert(smem_bytes<D>() <= 232448, "shared memory");
     const cudaFuncAttribute most = cudaFuncAttributeMaxDynamicSharedMemorySize;
     cudaError_t e = cudaFuncSetAttribute(lp_attend_kernel<kBf16, D>, most, smem_bytes<D>());
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(lp_attend_join_kernel<kBf16, D, 8>, most, join_bytes<D>(8));
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(lp_attend_join_kernel<kBf16, D, 4>, most, join_bytes<D>(4));
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(lp_attend_join_kernel<kBf16, D, 2>, most, join_bytes<D>(2));
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(lp_attend_join_kernel<kBf16, D, 1>, most, join_bytes<D>(1));
-    return e;
+    return e == cudaSuccess ? prepare_join<kBf16, D, Pairs, false>() : e;
 }
 
 template <bool kBf16, int D>
@@ -1290,19 +719,7 @@ cudaError_t launch(const AttendParams& p, const CUtensorMap& k_map, const CUtens
     lc.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&lc, lp_attend_kernel<kBf16, D>, p, k_map, v_map);
     if (e != cudaSuccess) return e;
-    // the most warps per row with which all blocks are resident at once: one row takes 15.5 us (one warp: 24.7), trees of
-    // drafts 43.6 (one: 46.3, eight: 60), 2,048 rows behind a prefix 765 (eight: 1,015)
-    const int chunks = (p.q_heads + 3) / 4;
-    int sub = 8;
-    auto per_row = [&]() { return (chunks * sub + kJoinWarps - 1) / kJoinWarps; };  // blocks
-    while (sub > 1 && per_row() * (long long)p.rows > join_blocks(sub) * p.grid) sub /= 2;
-    lc.gridDim = dim3((unsigned)p.rows, (unsigned)per_row());
-    lc.blockDim = dim3(kJoinThreads);
-    lc.dynamicSmemBytes = join_bytes<D>(sub);
-    if (sub == 8) return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 8>, p);
-    if (sub == 4) return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 4>, p);
-    if (sub == 2) return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 2>, p);
-    return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 1>, p);
+    return launch_join<kBf16, D, Pairs, false>(p, lc);
 }
 
 }  // namespace

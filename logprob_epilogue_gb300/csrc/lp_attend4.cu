@@ -1,0 +1,503 @@
+// lp_attend4.cu -- sm_103a kernel of lp_attend4: attention of verify rows over
+// a paged cache held in 4 bits.
+//
+// The sums, their parts and the split of the work are those of lp_attend (see
+// lp_split.h and lp_join.h): prefixes and committed tokens here, the round's
+// own tokens in the join.  Here a token and head is D / 2 bytes of codes and
+// D / 16 of scales, 0.28 of the bytes of 16 bits, and what has to keep up with
+// them is the way from codes to products.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "lp_join.h"
+#include "lp_split.h"
+#include "lp_tc.h"
+
+namespace lp {
+namespace {
+
+constexpr float kRescale = 8.0f;  // growth of the maximum (log2) that moves it
+// Probabilities are lifted by 2^6 (at most 2^14 then): F16 keeps those above 2^-30 of the largest.
+constexpr float kBias = 6.0f;
+constexpr int kWorkers = 8;       // warps that multiply
+constexpr int kMergers = 3;       // warps that add up the workers' results
+constexpr int kStep = 16;         // tokens of a step
+// Registers: the split's sum is what the block is launched with, 384 x 168.
+constexpr int kRegsLaunch = 168, kRegsWorker = 200, kRegsOther = 104;
+static_assert(2 * kRegsWorker + kRegsOther <= 3 * kRegsLaunch, "register split");
+
+template <int D>
+struct Cfg4 {
+    static constexpr int kCodes = kKTile * D / 2, kScales = kKTile * D / kBlock4;
+    static constexpr int kStage = 2 * (kCodes + kScales);  // K and V of a tile: codes, then scales
+    static constexpr int kStages = 8 * 128 / D;            // 144 KiB
+    static constexpr int kMerge = kStages * kStage;        // the workers' results: 16 rows each
+    static constexpr int kCtl = kMerge + kWorkers * 16 * D * 4;
+};
+
+constexpr int kPieces = 8;                          // pieces the fetching warp may be ahead
+constexpr int kPieceReaders = kWorkers + kMergers;  // warps that read each
+
+struct Ctl4 : PlanCtl<Fragments> {
+    uint64_t full[16], empty[16], piece_full[kPieces], piece_empty[kPieces];
+    Piece piece[kPieces];
+    uint64_t merge_full, merge_empty, drain;
+    float2 ml[kWorkers][16];
+    int abort;
+};
+
+// D += A B, 16 x 8 x 16, F16 with FP32 sums.
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The four bytes of a word, two codes each, to pairs of F16.
+__device__ __forceinline__ void widen_codes(uint32_t w, uint32_t (&h)[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\tcvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+
+// Two scale bytes to a pair of F16.
+__device__ __forceinline__ uint32_t widen_scales(uint32_t two) {
+    uint32_t h;
+    asm("{\n\t.reg .b16 s, t;\n\tmov.b32 {s, t}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, s;\n\t}" : "=r"(h) : "r"(two));
+    return h;
+}
+
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t lop_select(uint32_t a, uint32_t b, uint32_t mask) { return (a & mask) | (b & ~mask); }
+
+// A worker's rows: two per thread, lane / 4 and eight further.
+template <int D>
+struct Rows {
+    uint32_t q[2][D / 8];        // lanes lane % 4 * D / 4 .. of each, as pairs of F16
+    float o[D / 8][4];           // fragment j: lanes (D / 8) (2t) + j and (D / 8) (2t + 1) + j of the first row, then of the second
+    float c[2], m[2], base[2], limit[2], l[2];
+};
+
+// The queries of fragment `mt` of a unit.
+template <bool kBf16, int D>
+__device__ __forceinline__ void load_rows(const AttendParams& p, const Piece& x, int mt, Rows<D>& r) {
+    using T = typename Half<kBf16>::T;
+    const int lane = threadIdx.x & 31, t = lane & 3;
+    uint4 w[2][D / 32];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int row = mt * 16 + (lane >> 2) + 8 * h;
+        const int per = (row * p.share_inv) >> 16, head = row - per * p.share;
+        const T* src = reinterpret_cast<const T*>(p.q) + (long long)(x.row + per) * p.q_stride + (long long)(x.kvh * p.share + head) * D + t * (D / 4);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+            w[h][i] = row < x.rows * p.share ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float unit = 1.0f;
+        if constexpr (kBf16) {
+            // to F16 by a power of two that brings the row's largest lane to [2^14, 2^15)
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const uint32_t a[4] = {w[h][i].x, w[h][i].y, w[h][i].z, w[h][i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = Half<true>::unpack(a[e]);
+                    top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                }
+            }
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+            const int field = (int)(__float_as_uint(top) >> 23);
+            int up = 141 - field;
+            up = up > 126 ? 126 : up;
+            if (field == 255 || top == 0.0f) up = 0;
+            const float lift = __uint_as_float((uint32_t)(up + 127) << 23);
+            unit = __uint_as_float((uint32_t)(127 - up) << 23);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const uint32_t a[4] = {w[h][i].x, w[h][i].y, w[h][i].z, w[h][i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = Half<true>::unpack(a[e]);
+                    r.q[h][i * 4 + e] = Half<false>::pack(f.x * lift, f.y * lift);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) r.q[h][i * 4] = w[h][i].x, r.q[h][i * 4 + 1] = w[h][i].y, r.q[h][i * 4 + 2] = w[h][i].z, r.q[h][i * 4 + 3] = w[h][i].w;
+        }
+        // finite and above 0, so that a masked score stays -infinity and one of 0 stays 0
+        r.c[h] = fminf(fmaxf(p.scale * kLog2e * p.k_factor * unit, 0x1p-126f), 0x1p127f);
+        r.m[h] = r.limit[h] = kNegInf;
+        r.base[h] = r.l[h] = 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j) r.o[j][0] = r.o[j][1] = r.o[j][2] = r.o[j][3] = 0.0f;
+}
+
+// Sixteen tokens from `at` on of a stage, `have` of whose tokens exist.
+//
+// Column c of eight scores is token (c >> 1) + 4 (c & 1) of its eight, so that
+// the values that a thread multiplies (columns 2t and 2t + 1) are tokens t and t
+// + 4, and the four t of a load lie side by side.
+template <int D>
+__device__ __forceinline__ void step(const unsigned char* stage, int at, int have, Rows<D>& r) {
+    using C = Cfg4<D>;
+    constexpr int kK = D / 32, kV = D / 64;  // words of a thread: of a key, of a value
+    const int lane = threadIdx.x & 31, t = lane & 3, g = lane >> 2;
+    const unsigned char* ks = stage + 2 * C::kCodes;
+    const unsigned char* vs = ks + C::kScales;
+
+    // scores
+    float s[2][4];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        const int token = at + b * 8 + (g >> 1) + 4 * (g & 1);
+        uint32_t w[kK], e[kK / 2];
+        if constexpr (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(stage + token * (D / 2) + t * 16);
+            w[0] = x.x, w[1] = x.y, w[kK - 2] = x.z, w[kK - 1] = x.w;
+            const uint32_t two = widen_scales(*reinterpret_cast<const uint16_t*>(ks + token * (D / 16) + t * 2));
+            e[0] = __byte_perm(two, 0, 0x1010);
+            e[kK / 2 - 1] = __byte_perm(two, 0, 0x3232);
+        } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(stage + token * (D / 2) + t * 8);
+            w[0] = x.x, w[1] = x.y;
+            e[0] = __byte_perm(widen_scales(ks[token * (D / 16) + t]), 0, 0x1010);
+        }
+        s[b][0] = s[b][1] = s[b][2] = s[b][3] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kK; ++i) {
+            uint32_t h[4];
+            widen_codes(w[i], h);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int k = 2 * i + u;  // product
+                mma(s[b], r.q[0][2 * k], r.q[1][2 * k], r.q[0][2 * k + 1], r.q[1][2 * k + 1], mul2(h[2 * u], e[i / 2]), mul2(h[2 * u + 1], e[i / 2]));
+            }
+        }
+    }
+    const bool ragged = at + kStep > have;
+    if (ragged) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (at + b * 8 + t + 4 * (i & 1) >= have) s[b][i] = kNegInf;
+    }
+
+    // The rows' maxima: what they stand at holds until a score is 2^kRescale above it.
+    float top[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) top[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+    if (__any_sync(kFull, top[0] > r.limit[0] || top[1] > r.limit[1])) {
+        float f[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 1));
+            top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 2));
+            f[h] = 1.0f;
+            if (top[h] > r.limit[h]) {
+                const float next = top[h] * r.c[h] - kBias;
+                if (r.m[h] != kNegInf) f[h] = ex2(r.base[h] - next);
+                r.m[h] = top[h];
+                r.base[h] = next;
+                r.limit[h] = top[h] + kRescale / r.c[h];
+                r.l[h] *= f[h];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) r.o[j][0] *= f[0], r.o[j][1] *= f[0], r.o[j][2] *= f[1], r.o[j][3] *= f[1];
+    }
+    uint32_t a[4];  // probabilities
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float x = ex2(fmaf(s[b][2 * h], r.c[h], -r.base[h])), y = ex2(fmaf(s[b][2 * h + 1], r.c[h], -r.base[h]));
+            r.l[h] += x + y;
+            a[2 * b + h] = Half<false>::pack(x, y);
+        }
+
+    // values: two tokens' codes side by side
+    uint32_t e[2], w[2][2][kV];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        uint32_t scale[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int token = at + b * 8 + t + 4 * u;
+            scale[u] = vs[token * (D / 16) + (D == 128 ? g : g >> 1)];
+            if (ragged && token >= have) scale[u] = 0u;  // what lies there may be NaN, and 0 * v has to stay 0
+            if constexpr (D == 128) {
+                const uint2 x = *reinterpret_cast<const uint2*>(stage + C::kCodes + token * (D / 2) + g * 8);
+                w[b][u][0] = x.x, w[b][u][kV - 1] = x.y;
+            } else {
+                w[b][u][0] = *reinterpret_cast<const uint32_t*>(stage + C::kCodes + token * (D / 2) + g * 4);
+            }
+        }
+        e[b] = widen_scales(scale[0] | scale[1] << 8);
+    }
+#pragma unroll
+    for (int i = 0; i < kV; ++i)
+#pragma unroll
+        for (int odd = 0; odd < 2; ++odd) {
+            uint32_t h[2][4];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const uint32_t x = w[b][0][i], y = w[b][1][i];
+                widen_codes(odd ? lop_select(x >> 4, y, 0x0F0F0F0Fu) : lop_select(x, y << 4, 0x0F0F0F0Fu), h[b]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                mma(r.o[i * 8 + 2 * j + odd], a[0], a[1], a[2], a[3], mul2(h[0][j], e[0]), mul2(h[1][j], e[1]));
+        }
+}
+
+template <bool kBf16, int D>
+__global__ void __launch_bounds__(kThreads, 1) lp_attend4_kernel(const AttendParams p) {
+    using C = Cfg4<D>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    Ctl4* ctl = reinterpret_cast<Ctl4*>(smem + C::kCtl);
+    float4* merge = reinterpret_cast<float4*>(smem + C::kMerge);  // [worker][chunk][lane]
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(kFull, tid >> 5, 0);  // the same for the warp, as the compiler sees
+    const unsigned long long limit = p.timeout_ns;
+    if (warp == kWarps - 1) {  // while the kernel ahead still runs
+        if (lane < C::kStages) tc::mbar_init(&ctl->full[lane], 1), tc::mbar_init(&ctl->empty[lane], kWorkers);
+        if (lane < kPieces) tc::mbar_init(&ctl->piece_full[lane], 1), tc::mbar_init(&ctl->piece_empty[lane], kPieceReaders);
+        if (lane == 0) {
+            tc::mbar_init(&ctl->merge_full, kWorkers);
+            tc::mbar_init(&ctl->merge_empty, kMergers);
+            tc::mbar_init(&ctl->drain, 1);
+            ctl->abort = 0;
+        }
+        tc::fence_async_shared();
+    }
+    // so far nothing of what earlier kernels write; the join may start once that is there, and waits for this grid's end by itself
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    Runs runs[2];  // of prefixes, of groups
+    const bool any = plan_run<Fragments>(p, ctl, runs);
+    __syncthreads();
+    if (!any) {
+        if (tid == 0) p.sc.gave_up[blockIdx.x] = 0;
+        return;
+    }
+    volatile int* abort = &ctl->abort;
+    // test hook: nothing arrives on `drain`, so this wait runs out
+    if (p.force_timeout) tc::warp_wait(&ctl->drain, 0, limit, abort);
+
+    Piece x;
+    bool ok = !p.force_timeout;
+    uint32_t n_piece = 0, it = 0;  // it: stages
+    // the next piece, from the fetching warp; false at the end of the run
+    auto next_piece = [&]() {
+        const uint32_t i = n_piece % kPieces;
+        ok = tc::warp_wait(&ctl->piece_full[i], n_piece / kPieces & 1u, limit, abort);
+        if (!ok) return false;
+        x = ctl->piece[i];
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&ctl->piece_empty[i]);
+        ++n_piece;
+        return x.rows > 0;
+    };
+
+    if (warp >= 4) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsWorker));
+        // ---- products: fragment mt of the unit's rows, every slices-th step of the tokens
+        const int worker = warp - 4;
+        uint32_t merged = 0;
+        while (ok && next_piece()) {
+            const int fragments = (x.rows * p.share + 15) >> 4, mt = worker % fragments, slice = worker / fragments;
+            const int slices = (kWorkers - mt + fragments - 1) / fragments;
+            Rows<D> r;
+            load_rows<kBf16, D>(p, x, mt, r);
+            for (int i = 0; ok && i < x.tiles; ++i, ++it) {
+                const uint32_t at = it % C::kStages;
+                ok = tc::warp_wait(&ctl->full[at], it / C::kStages & 1u, limit, abort);
+                if (!ok) break;
+                const int left = x.left - i * kKTile, have = left < kKTile ? left : kKTile;
+                for (int s = slice * kStep; s < have; s += slices * kStep) step<D>(smem + at * C::kStage, s, have, r);
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&ctl->empty[at]);
+            }
+            if (!ok) break;
+            ok = tc::warp_wait(&ctl->merge_empty, (merged & 1u) ^ 1u, limit, abort);
+            if (!ok) break;
+            ++merged;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                r.l[h] += __shfl_xor_sync(kFull, r.l[h], 1);
+                r.l[h] += __shfl_xor_sync(kFull, r.l[h], 2);
+                if ((lane & 3) == 0) ctl->ml[worker][(lane >> 2) + 8 * h] = make_float2(r.m[h] == kNegInf ? kNegInf : r.base[h], r.l[h]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j)
+                        merge[(worker * (D / 8) + (2 * h + e) * (D / 32) + j) * 32 + lane] =
+                            make_float4(r.o[4 * j][2 * h + e], r.o[4 * j + 1][2 * h + e], r.o[4 * j + 2][2 * h + e], r.o[4 * j + 3][2 * h + e]);
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&ctl->merge_full);
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        if (warp == 0) {
+            // ---- pages into the ring: lanes 0-15 the keys, 16-31 the values, a page (or a tile of one) each
+            const int step = p.page_shift < 7 ? 1 << p.page_shift : kKTile;  // tokens per copy
+            const int box = lane & 15, tok = box * step, half = lane >> 4;
+            const unsigned char* codes = static_cast<const unsigned char*>(half == 0 ? p.k_cache : p.v_cache);
+            const unsigned char* scales = half == 0 ? p.k_scales : p.v_scales;
+            Walk<Fragments> walk;
+            walk.cta = blockIdx.x;
+            walk.deal = ctl->deal_first;
+            walk.deal_end = ctl->deal_last + 1;
+            walk.round = walk.dealt = 0;
+            walk.start = ctl->start;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                walk.runs[k] = runs[k];
+                const bool any = (int)blockIdx.x < runs[k].blocks;
+                walk.begin[k] = any ? runs[k].start(blockIdx.x) : 0;
+                walk.finish[k] = any ? runs[k].start(blockIdx.x + 1) : 0;
+            }
+            walk.enter(0);
+            auto page_of = [&](int i) {
+                const long long at = walk.token + i * kKTile + tok;
+                return i < x.tiles && i * kKTile + tok < x.left ? walk.table[at >> p.page_shift] : -1;
+            };
+            for (bool more = ok; ok && more;) {
+                more = walk.next(p, x);
+                const uint32_t pi = n_piece % kPieces;
+                ok = tc::warp_wait(&ctl->piece_empty[pi], (n_piece / kPieces & 1u) ^ 1u, limit, abort);
+                if (!ok) break;
+                if (lane == 0) {
+                    ctl->piece[pi] = x;
+                    tc::mbar_arrive(&ctl->piece_full[pi]);
+                }
+                ++n_piece;
+                if (!more) break;
+                // the pages of the next tile are read before this tile's waits
+                int next_page = page_of(0);
+                for (int i = 0; ok && i < x.tiles; ++i) {
+                    const int left = x.left - i * kKTile, valid = left < kKTile ? left : kKTile;
+                    const int boxes = (valid + step - 1) / step;
+                    const int y = (int)((walk.token + i * kKTile + tok) & ((1 << p.page_shift) - 1));
+                    const int page = next_page;
+                    next_page = page_of(i + 1);
+                    const uint32_t at = it % C::kStages;
+                    ok = tc::warp_wait(&ctl->empty[at], (it / C::kStages & 1u) ^ 1u, limit, abort);
+                    if (!ok) break;
+                    const uint32_t to = tc::smem_addr(smem + at * C::kStage);
+                    const bool copies = box < boxes, good = page >= 0 && page < p.num_pages;
+                    const unsigned got = __ballot_sync(kFull, copies && good);
+                    if (copies && !good) {  // a page that does not exist reads as zeros
+                        atomicOr(p.status, kStatusBadPage);
+                        uint4* z = reinterpret_cast<uint4*>(smem + at * C::kStage + 2 * C::kCodes + half * C::kScales + tok * (D / kBlock4));
+                        for (int k = 0; k < step * (D / kBlock4) / 16; ++k) z[k] = make_uint4(0u, 0u, 0u, 0u);
+                        tc::fence_async_shared();
+                    }
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_expect(&ctl->full[at], (uint32_t)__popc(got) * step * (D / 2 + D / kBlock4));
+                    __syncwarp();
+                    if (copies && good) {
+                        const long long slot = (((long long)page * p.kv_heads + x.kvh) << p.page_shift) + y;
+                        tc::bulk_load(to + half * C::kCodes + tok * (D / 2), codes + slot * (D / 2), step * (D / 2), &ctl->full[at]);
+                        tc::bulk_load(to + 2 * C::kCodes + half * C::kScales + tok * (D / kBlock4), scales + slot * (D / kBlock4), step * (D / kBlock4), &ctl->full[at]);
+                    }
+                    ++it;
+                }
+            }
+            // no copy outlives the block, whatever its readers did
+            int none = 0;
+            for (uint32_t i = it > C::kStages ? it - C::kStages : 0; i < it; ++i)
+                tc::mbar_wait(&ctl->full[i % C::kStages], i / C::kStages & 1u, limit, &none);
+        } else {
+            // ---- the workers' results of a piece, added up
+            uint32_t merged = 0;
+            while (ok && next_piece()) {
+                ok = tc::warp_wait(&ctl->merge_full, merged & 1u, limit, abort);
+                if (!ok) break;
+                ++merged;
+                const int rows = x.rows * p.share, fragments = (rows + 15) >> 4;
+                for (int i = (warp - 1) * 32 + lane; i < fragments * (D / 8) * 32 && x.part >= 0; i += kMergers * 32) {
+                    const int mt = i / (D / 8 * 32), chunk = i / 32 % (D / 8), h = chunk / (D / 16), e = chunk / (D / 32) & 1, j = chunk % (D / 32);
+                    const int in = (lane >> 2) + 8 * h, row = mt * 16 + in;
+                    if (row >= rows) continue;
+                    float top = kNegInf, l = 0.0f;
+                    for (int w = mt; w < kWorkers; w += fragments) top = fmaxf(top, ctl->ml[w][in].x);
+                    const float from = top == kNegInf ? 0.0f : top;
+                    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    for (int w = mt; w < kWorkers; w += fragments) {
+                        const float2 ml = ctl->ml[w][in];
+                        if (ml.x == kNegInf && ml.y == 0.0f) continue;  // saw nothing
+                        const float f = ex2(ml.x - from);
+                        const float4 v = merge[(w * (D / 8) + chunk) * 32 + lane];
+                        l = fmaf(ml.y, f, l);
+                        o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+                    }
+                    if (chunk % (D / 16) == 0 && (lane & 3) == 0) p.sc.part_ml[x.part + row] = make_float2(top, l);
+                    reinterpret_cast<float4*>(p.sc.part_o)[part_chunk<D>(x.part, x.part_stride, row, (D / 32) * (2 * (lane & 3) + e) + j)] = o;
+                }
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&ctl->merge_empty);
+            }
+        }
+    }
+    __syncthreads();
+    if (tid == 0) {
+        p.sc.gave_up[blockIdx.x] = *abort;
+        if (*abort != 0) atomicOr(p.status, kStatusAttnTimeout);
+    }
+}
+
+template <int D>
+constexpr int smem_bytes4() { return Cfg4<D>::kCtl + (int)sizeof(Ctl4); }
+
+template <bool kBf16, int D>
+cudaError_t prepare4() {
+    static_assert(smem_bytes4<D>() <= 232448, "shared memory");
+    const cudaError_t e = cudaFuncSetAttribute(lp_attend4_kernel<kBf16, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes4<D>());
+    return e == cudaSuccess ? prepare_join<kBf16, D, Fragments, true>() : e;
+}
+
+template <bool kBf16, int D>
+cudaError_t launch4(const AttendParams& p, cudaStream_t stream) {
+    // Both kernels are launched while the one before still runs, and wait for its end before they read what it writes.
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)p.grid);
+    lc.blockDim = dim3(kThreads);
+    lc.dynamicSmemBytes = smem_bytes4<D>();
+    lc.stream = stream;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&lc, lp_attend4_kernel<kBf16, D>, p);
+    return e == cudaSuccess ? launch_join<kBf16, D, Fragments, true>(p, lc) : e;
+}
+
+}  // namespace
+
+cudaError_t prepare_attend4(int dtype, int head_dim) {
+    if (dtype == 1) return head_dim == 128 ? prepare4<true, 128>() : prepare4<true, 64>();
+    return head_dim == 128 ? prepare4<false, 128>() : prepare4<false, 64>();
+}
+
+cudaError_t launch_attend4(const AttendParams& p, int dtype, int head_dim, cudaStream_t stream) {
+    if (dtype == 1) return head_dim == 128 ? launch4<true, 128>(p, stream) : launch4<true, 64>(p, stream);
+    return head_dim == 128 ? launch4<false, 128>(p, stream) : launch4<false, 64>(p, stream);
+}
+
+}  // namespace lp

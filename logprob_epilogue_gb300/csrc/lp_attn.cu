@@ -75,13 +75,15 @@ struct Layout {
 Layout layout_of(const lp_attn_desc* d, int grid) {
     Layout L{};
     const int share = d->q_heads / d->kv_heads, per_tile = lp::kQTile / share;
-    const long long group_units = (long long)d->max_groups * ((d->max_group_rows + 2 * per_tile - 1) / (2 * per_tile));
-    const long long prefix_units = d->max_prefixes == 0 ? 0 : d->max_rows / (2 * per_tile) + d->max_prefixes;
+    // tiles of a unit, parts of a piece: two; of the kernel over 4 bits, one
+    const int sets = (d->flags & LP_ATTN_KV4) != 0 ? 1 : 2;
+    const long long group_units = (long long)d->max_groups * ((d->max_group_rows + sets * per_tile - 1) / (sets * per_tile));
+    const long long prefix_units = d->max_prefixes == 0 ? 0 : d->max_rows / (sets * per_tile) + d->max_prefixes;
     L.group_rows = (d->max_group_rows < per_tile ? d->max_group_rows : per_tile) * share;
     L.group_slots = group_units * d->kv_heads + grid;
     L.prefix_slots = d->max_prefixes == 0 ? 0 : prefix_units * d->kv_heads + grid;
     const size_t segs = (size_t)d->max_prefixes + (size_t)d->max_groups;
-    const size_t part_rows = 2 * ((size_t)L.prefix_slots * lp::kQTile + (size_t)L.group_slots * (size_t)L.group_rows);
+    const size_t part_rows = sets * ((size_t)L.prefix_slots * lp::kQTile + (size_t)L.group_slots * (size_t)L.group_rows);
     size_t off = 0;
     L.seg_units = off;
     off = lp::align_up(off + segs * 8);
@@ -220,6 +222,69 @@ bool power_of_two(float f) {
     return std::isfinite(f) && std::frexp(f, &e) == 0.5f && e >= -59 && e <= 61;
 }
 
+
+// Neither rows nor groups: a call that does nothing.
+bool nothing_to_attend(const lp_attend_io& io) { return io.rows == 0 || io.groups == 0; }
+
+int check_attend(const lp_attn_s* plan, const lp_attend_io* io) {
+    const lp_attn_desc& d = plan->d;
+    if (io->rows < 0 || io->rows > d.max_rows || io->groups < 0 || io->groups > d.max_groups) return LP_ESHAPE;
+    if (io->prefixes < 0 || io->prefixes > d.max_prefixes) return LP_ESHAPE;
+    if (!io->status || !(io->scale > 0.0f) || !std::isfinite(io->scale)) return LP_EINVAL;
+    if (!aligned(io->status, 4)) return LP_EALIGN;
+    if (nothing_to_attend(*io)) return LP_OK;
+    int rc;
+    if ((rc = check_rows(plan, io->q, io->q_stride, d.q_heads)) != LP_OK) return rc;
+    if ((rc = check_rows(plan, io->out, io->out_stride, d.q_heads)) != LP_OK) return rc;
+    if (!io->k_cache || !io->v_cache || !io->group_indptr || !io->lens || !io->block_tables) return LP_EINVAL;
+    if (io->prefixes > 0 && (!io->prefix_indptr || !io->prefix_lens || !io->prefix_tables)) return LP_EINVAL;
+    if (!aligned(io->k_cache, 16) || !aligned(io->v_cache, 16)) return LP_EALIGN;
+    const void* w4[] = {io->group_indptr, io->lens, io->block_tables, io->row_masks, io->prefix_indptr,
+                        io->prefix_lens, io->prefix_tables, io->lse_out};
+    for (const void* q : w4)
+        if (!aligned(q, 4)) return LP_EALIGN;
+    return LP_OK;
+}
+
+lp::AttendParams attend_params(const lp_attn_s* plan, const lp_attend_io* io) {
+    const lp_attn_desc& d = plan->d;
+    lp::AttendParams p{};
+    p.q = io->q;
+    p.q_stride = io->q_stride;
+    p.out_stride = io->out_stride;
+    p.k_cache = io->k_cache;
+    p.v_cache = io->v_cache;
+    p.indptr = io->group_indptr;
+    p.lens = io->lens;
+    p.tables = io->block_tables;
+    p.row_masks = io->row_masks;
+    p.prefix_indptr = io->prefix_indptr;
+    p.prefix_lens = io->prefix_lens;
+    p.prefix_tables = io->prefix_tables;
+    p.out = io->out;
+    p.lse_out = io->lse_out;
+    p.status = io->status;
+    p.scale = io->scale;
+    p.rows = io->rows;
+    p.G = io->groups;
+    p.P = io->prefixes;
+    p.q_heads = d.q_heads;
+    p.kv_heads = d.kv_heads;
+    p.share = d.q_heads / d.kv_heads;
+    p.max_group_rows = d.max_group_rows;
+    p.max_pages = d.max_pages;
+    p.max_prefix_pages = d.max_prefix_pages;
+    p.page_shift = plan->page_shift;
+    p.num_pages = d.num_pages;
+    p.rows_per_tile = lp::kQTile / p.share;
+    p.share_inv = (65536 + p.share - 1) / p.share;
+    p.grid = plan->grid;
+    p.sc = plan->sc;
+    p.timeout_ns = (unsigned long long)(d.timeout_ns > 0 ? d.timeout_ns : lp::kDefaultTimeoutNs);
+    p.force_timeout = (d.flags & LP_PLAN_DEBUG_FORCE_TIMEOUT) != 0;
+    return p;
+}
+
 }  // namespace
 
 extern "C" {
@@ -250,7 +315,7 @@ int lp_attn_create(lp_attn_t* out, const lp_attn_desc* desc) {
     cudaError_t e = cudaDeviceGetAttribute(&plan->grid, cudaDevAttrMultiProcessorCount, desc->device);
     if (e == cudaSuccess) e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
     if (e == cudaSuccess && (found != cudaDriverEntryPointSuccess || !fn)) e = cudaErrorNotSupported;
-    if (e == cudaSuccess) e = lp::prepare_attend(desc->dtype, desc->head_dim);
+    if (e == cudaSuccess) e = four_bits(plan) ? lp::prepare_attend4(desc->dtype, desc->head_dim) : lp::prepare_attend(desc->dtype, desc->head_dim);
     Layout L{};
     if (e == cudaSuccess) {
         plan->encode = reinterpret_cast<EncodeTiled>(fn);
@@ -381,67 +446,34 @@ int lp_kv_reserve(lp_attn_t plan, const lp_reserve_io* io, void* stream) {
 int lp_attend(lp_attn_t plan, const lp_attend_io* io, void* stream) {
     if (!plan || !io) return LP_EINVAL;
     if (four_bits(plan)) return LP_ESTATE;
-    const lp_attn_desc& d = plan->d;
-    if (io->rows < 0 || io->rows > d.max_rows || io->groups < 0 || io->groups > d.max_groups) return LP_ESHAPE;
-    if (io->prefixes < 0 || io->prefixes > d.max_prefixes) return LP_ESHAPE;
-    if (!io->status || !(io->scale > 0.0f) || !std::isfinite(io->scale)) return LP_EINVAL;
-    if (!aligned(io->status, 4)) return LP_EALIGN;
-    if (io->rows == 0 || io->groups == 0) return LP_OK;
-    int rc;
-    if ((rc = check_rows(plan, io->q, io->q_stride, d.q_heads)) != LP_OK) return rc;
-    if ((rc = check_rows(plan, io->out, io->out_stride, d.q_heads)) != LP_OK) return rc;
-    if (!io->k_cache || !io->v_cache || !io->group_indptr || !io->lens || !io->block_tables) return LP_EINVAL;
-    if (io->prefixes > 0 && (!io->prefix_indptr || !io->prefix_lens || !io->prefix_tables)) return LP_EINVAL;
-    if (!aligned(io->k_cache, 16) || !aligned(io->v_cache, 16)) return LP_EALIGN;
-    const void* w4[] = {io->group_indptr, io->lens, io->block_tables, io->row_masks, io->prefix_indptr,
-                        io->prefix_lens, io->prefix_tables, io->lse_out};
-    for (const void* q : w4)
-        if (!aligned(q, 4)) return LP_EALIGN;
-    DeviceGuard guard(d.device);
+    const int rc = check_attend(plan, io);
+    if (rc != LP_OK || nothing_to_attend(*io)) return rc;
+    DeviceGuard guard(plan->d.device);
     if (!guard.ok) return cuda_fail(cudaGetLastError());
-    lp::AttendParams p{};
-    p.q = io->q;
-    p.q_stride = io->q_stride;
-    p.out_stride = io->out_stride;
-    p.k_cache = io->k_cache;
-    p.v_cache = io->v_cache;
-    p.indptr = io->group_indptr;
-    p.lens = io->lens;
-    p.tables = io->block_tables;
-    p.row_masks = io->row_masks;
-    p.prefix_indptr = io->prefix_indptr;
-    p.prefix_lens = io->prefix_lens;
-    p.prefix_tables = io->prefix_tables;
-    p.out = io->out;
-    p.lse_out = io->lse_out;
-    p.status = io->status;
-    p.scale = io->scale;
-    p.rows = io->rows;
-    p.G = io->groups;
-    p.P = io->prefixes;
-    p.q_heads = d.q_heads;
-    p.kv_heads = d.kv_heads;
-    p.share = d.q_heads / d.kv_heads;
-    p.max_group_rows = d.max_group_rows;
-    p.max_pages = d.max_pages;
-    p.max_prefix_pages = d.max_prefix_pages;
-    p.page_shift = plan->page_shift;
-    p.num_pages = d.num_pages;
-    p.rows_per_tile = lp::kQTile / p.share;
-    p.share_inv = (65536 + p.share - 1) / p.share;
-    p.grid = plan->grid;
-    p.sc = plan->sc;
-    p.timeout_ns = (unsigned long long)(d.timeout_ns > 0 ? d.timeout_ns : lp::kDefaultTimeoutNs);
-    p.force_timeout = (d.flags & LP_PLAN_DEBUG_FORCE_TIMEOUT) != 0;
     CUtensorMap k_map, v_map;
     if (!encode_cache(plan, &k_map, io->k_cache) || !encode_cache(plan, &v_map, io->v_cache))
         return cuda_fail(cudaErrorInvalidValue);
-    const cudaError_t e = lp::launch_attend(p, k_map, v_map, d.dtype, d.head_dim, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = lp::launch_attend(attend_params(plan, io), k_map, v_map, plan->d.dtype, plan->d.head_dim,
+                                            static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? LP_OK : cuda_fail(e);
 }
 
 int lp_attend4(lp_attn_t plan, const lp_attend4_io* io, void* stream) {
-    return LP_EINVAL;
+    if (!plan || !io) return LP_EINVAL;
+    if (!four_bits(plan)) return LP_ESTATE;
+    if (!(io->k_factor > 0.0f) || !(io->v_factor > 0.0f) || !std::isfinite(io->k_factor) || !std::isfinite(io->v_factor)) return LP_EINVAL;
+    int rc = check_attend(plan, &io->attend);
+    if (rc != LP_OK || nothing_to_attend(io->attend)) return rc;
+    if ((rc = check_scales(io->k_scales, io->v_scales)) != LP_OK) return rc;
+    DeviceGuard guard(plan->d.device);
+    if (!guard.ok) return cuda_fail(cudaGetLastError());
+    lp::AttendParams p = attend_params(plan, &io->attend);
+    p.k_scales = static_cast<const unsigned char*>(io->k_scales);
+    p.v_scales = static_cast<const unsigned char*>(io->v_scales);
+    p.k_factor = io->k_factor;
+    p.v_factor = io->v_factor;
+    const cudaError_t e = lp::launch_attend4(p, plan->d.dtype, plan->d.head_dim, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? LP_OK : cuda_fail(e);
 }
 
 }  // extern "C"

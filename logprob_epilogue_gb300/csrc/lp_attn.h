@@ -98,6 +98,9 @@ struct AttendParams {
     AttendScratch sc;
     unsigned long long timeout_ns;
     int force_timeout;
+    // a cache of 4 bits; k_cache, v_cache: the codes
+    const unsigned char *k_scales, *v_scales;
+    float k_factor, v_factor;
 };
 
 // The pieces of a cut unit as the join may take them from its entry (first
@@ -117,6 +120,8 @@ inline int cache_box_rows(int page_size) { return page_size < kKTile ? page_size
 cudaError_t launch_reserve(const ReserveParams& p, int grid, cudaStream_t stream);
 cudaError_t launch_rope(const RopeParams& p, int dtype, int head_dim, cudaStream_t stream);
 cudaError_t prepare_attend(int dtype, int head_dim);  // once per plan: kernel attributes
+cudaError_t prepare_attend4(int dtype, int head_dim);
+cudaError_t launch_attend4(const AttendParams& p, int dtype, int head_dim, cudaStream_t stream);
 cudaError_t launch_attend(const AttendParams& p, const CUtensorMap& k_map, const CUtensorMap& v_map, int dtype,
                           int head_dim, cudaStream_t stream);
 

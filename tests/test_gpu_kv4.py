@@ -5,7 +5,7 @@ import pytest
 
 import attn_ref as R
 import kv4_ref as K
-from test_gpu_attn import batch, dev, generator, i32, plan_of, rand, status_word, table
+from test_gpu_attn import EDGES, Case, batch, dev, generator, i32, plan_of, rand, status_word, table
 
 pytestmark = pytest.mark.gpu
 
@@ -372,3 +372,400 @@ def test_append4_twice_and_captured_is_the_same():
         assert torch.equal(x[at, :, off], f[at, :, off])
         w[at, :, off] = f[at, :, off]
         assert torch.equal(x, w)
+
+
+# ---- attention
+#
+# The bounds are those of attend (see attn_ref), whose terms cover this kernel's: a query is exact in F16 after its power of two
+# (a lane under 2^-28 of the row's largest is off by 2^-39 of that), a code times its scale is exact, and a probability is
+# rounded to F16, 2^-11 of it or 2^-31 of the largest.
+
+
+class Case4(Case):
+    """A Case over a cache in 4 bits: its keys and values quantised, with NaN scales in slots that nothing owns."""
+
+    def __init__(self, factors=(1.0, 1.0), **kw):
+        super().__init__(**kw)
+        self.factors = factors
+        self.raw = [self.kc, self.vc]
+        self.quantise()
+
+    def quantise(self, seed=3):
+        """Codes and scales of the raw caches; kc and vc become what these stand for, in 64 bits."""
+        import torch
+        self.codes, self.scales, stand = [], [], []
+        for raw, f in zip(self.raw, self.factors):
+            codes, scales = K.quantise_rows(raw, f)
+            junk = torch.randint(0, 16, codes.shape, generator=generator(seed), device=dev(), dtype=torch.int32).to(torch.uint8)
+            codes = K.pack(torch.where(codes == 255, junk, codes))
+            self.codes.append(codes), self.scales.append(scales), stand.append(K.values(codes, scales, f))
+        self.kc, self.vc = stand
+
+    def plan(self, **kw):
+        return super().plan(kv_bits=4, **kw)
+
+    def tensors(self):
+        import torch
+        t = super().tensors()
+        t.update(k_cache=self.codes[0], v_cache=self.codes[1], k_scales=self.scales[0].view(torch.float8_e4m3fn),
+                 v_scales=self.scales[1].view(torch.float8_e4m3fn), k_factor=self.factors[0], v_factor=self.factors[1])
+        return t
+
+    def run(self, plan=None, stream=None, **more):
+        import torch
+        out = torch.full((self.rows, self.hq, self.d), 7.0, dtype=R.DTYPE[self.dtype], device=dev())
+        lse = torch.full((self.rows, self.hq), 7.0, device=dev())
+        st = status_word()
+        plan = plan or self.plan()
+        plan.attend4(**{**self.tensors(), **more}, out=out, lse_out=lse, status=st, stream=stream)
+        torch.cuda.synchronize()
+        return out, lse, int(st[0])
+
+
+@pytest.mark.parametrize("dtype,d,hq,hk,page", [
+    ("bf16", 128, 4, 1, 16), ("f16", 64, 6, 2, 8), ("bf16", 64, 2, 2, 256), ("f16", 128, 12, 1, 64), ("bf16", 128, 10, 2, 128),
+    ("f16", 128, 5, 1, 32), ("bf16", 64, 128, 1, 64), ("bf16", 128, 8, 1, 8),
+])
+def test_attend4_lengths(dtype, d, hq, hk, page):
+    """Every length about a page's and a tile's end, groups of one to five rows, unused slots NaN."""
+    n = [1 + i % 5 for i in range(len(EDGES))]
+    Case4(dtype=dtype, d=d, hq=hq, hk=hk, page=page, n=n, lens=EDGES, pad_rows=2).check()
+
+
+@pytest.mark.parametrize("prefix", [1, 7, 64, 127, 128, 129, 300, 1025])
+@pytest.mark.parametrize("dtype,d,hq,hk,page,n,lens", [
+    ("bf16", 128, 4, 1, 16, [1], [0]),
+    ("bf16", 128, 8, 2, 64, [4] * 11, [0, 1, 2, 130, 5, 64, 9, 31, 256, 77, 3]),
+    ("f16", 64, 3, 3, 32, [32, 1, 9, 31, 32], [5, 0, 700, 1, 128]),
+    ("f16", 128, 24, 2, 8, [16, 16, 16], [1, 0, 140]),
+])
+def test_attend4_shared_prefix(prefix, dtype, d, hq, hk, page, n, lens):
+    Case4(dtype=dtype, d=d, hq=hq, hk=hk, page=page, n=n, lens=lens, prefixes=[prefix]).check()
+
+
+@pytest.mark.parametrize("hq,n", [(1, 1), (1, 15), (4, 4), (1, 17), (8, 4), (3, 11), (4, 12), (3, 21), (4, 16), (5, 13), (12, 8), (5, 25), (8, 16), (12, 32)])
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f16", 64)])
+def test_attend4_query_rows(dtype, d, hq, n):
+    """From one (row, head) pair of a group to three units of them, about every number of fragments; one token tile, two and several."""
+    Case4(dtype=dtype, d=d, hq=hq, hk=1, n=[n] * 4, lens=[1, 129, 700, 300], page=32).check()
+
+
+@pytest.mark.parametrize("factors", [(2.0 ** -8, 2.0 ** 5), (3.0, 0.7), (2.0 ** 20, 2.0 ** -20)])
+def test_attend4_factors(factors):
+    c = Case4(n=[2, 3], lens=[300, 40], prefixes=[150])
+    c.factors = factors  # what the same codes stand for under others
+    c.kc, c.vc = (K.values(x, s, f) for x, s, f in zip(c.codes, c.scales, factors))
+    c.scale /= factors[0]
+    c.check()
+
+
+def test_attend4_several_prefixes_and_groups_without_one():
+    n = [2, 3, 1, 4, 1, 1, 5, 2, 2]
+    lens = [10, 0, 300, 5, -1, 129, 0, 64, 1]
+    Case4(n=n, lens=lens, prefixes=[200, 5, 400], prefix_indptr=[1, 3, 3, 8], hq=6, hk=3).check()
+    Case4(n=n, lens=lens, prefixes=[200, 0], prefix_indptr=[0, 4, 9], hq=6, hk=3, dtype="f16", d=64).check()
+
+
+def test_attend4_many_rows_behind_a_prefix():
+    n = [1 + i % 8 for i in range(66)]
+    lens = [(37 * i) % 150 - 1 for i in range(66)]
+    Case4(n=n, lens=lens, prefixes=[517], hq=10, hk=2).check()
+    Case4(n=n, lens=lens, prefixes=[517], hq=10, hk=2, d=64, dtype="f16", page=64).check()
+
+
+def test_attend4_more_units_than_blocks():
+    n = [20, 31, 7, 32, 32, 28, 12]
+    Case4(n=n, lens=[0, 140, -1, 3, 0, 128, 9], prefixes=[260, 129], prefix_indptr=[0, 5, 7], hq=32 * 12, hk=32, d=64).check()
+    Case4(n=n, lens=[0, 140, -1, 3, 0, 128, 9], prefixes=[140], hq=16 * 40, hk=16, dtype="f16").check()
+
+
+def test_attend4_trees_and_empty_rows():
+    r = np.random.RandomState(0)
+    n, lens = [7, 32, 1, 16, 3], [0, 50, 0, 131, 0]
+    masks = []
+    for m in n:
+        rows = [1]
+        for j in range(1, m):
+            rows.append(rows[r.randint(j)] | 1 << j)
+        masks += rows
+    masks[3] = 0                 # no context, no row: nothing to see
+    masks[39] = 0                # a single row that does not see itself
+    masks[8] = 0xFFFFFFFF        # rows after its own, too
+    masks[-1] = 0xFFFFFFF8       # bits past the group's rows name nothing
+    c = Case4(n=n, lens=lens, masks=masks)
+    out, lse = c.check()
+    for row in (3, 39, c.rows - 1):
+        assert bool((out[row] == 0).all()) and bool((lse[row] == -np.inf).all())
+    Case4(n=n, lens=lens, masks=masks, prefixes=[33], d=64).check()
+
+
+def test_attend4_idle_and_malformed_groups():
+    import logprob_epilogue_gb300 as lpe
+    c = Case4(n=[2, 3, 2, 1], lens=[20, -1, 40, -7], prefixes=[30])
+    out, lse = c.check()
+    assert bool((out[2:5] == 0).all()) and bool((lse[2:5] == -np.inf).all())
+    ref = c.ref()
+    good = list(range(0, 2)) + [7]
+    out, lse, st = c.run(lens=i32([20, -1, c.tables.shape[1] * c.page - 1, -7]))  # more tokens than the table holds
+    assert st == lpe.STATUS_BAD_GROUP
+    assert bool((out[5:7] == 0).all()) and bool((lse[5:7] == -np.inf).all())
+    R.check_attend(out, lse, ref, c.dtype, good)
+    small = Case4(n=[2, 3, 2, 1], lens=[20, -1, 40, -7], prefixes=[30], max_group_rows=2)
+    out, lse, st = small.run(lens=i32([20, 3, 40, -7]))
+    assert st == lpe.STATUS_BAD_GROUP and bool((out[2:5] == 0).all())
+    R.check_attend(out, lse, ref, c.dtype, good)
+    for indptr in ([0, 2, 5, 7, 9], [-2, 2, 5, 7, 8], [0, 5, 2, 7, 8], [0, 2, 5, 2147483647, 8]):
+        _, _, st = c.run(group_indptr=i32(indptr))
+        assert st & lpe.STATUS_BAD_GROUP, indptr
+    alone = R.attend(c.q, c.kc, c.vc, c.indptr, c.lens, c.tables, scale=c.scale)
+    for bad in (dict(prefix_indptr=i32([0, 5])), dict(prefix_indptr=i32([3, 2])), dict(prefix_indptr=i32([-1, 4])),
+                dict(prefix_lens=i32([-1])), dict(prefix_lens=i32([c.prefix_tables.shape[1] * c.page + 1]))):
+        out, lse, st = c.run(**bad)
+        assert st == lpe.STATUS_BAD_PREFIX, bad
+        R.check_attend(out, lse, alone, c.dtype, slice(0, c.rows))
+
+
+@pytest.mark.parametrize("page", [16, 256])
+def test_attend4_pages_out_of_range_read_as_zeros(page):
+    import logprob_epilogue_gb300 as lpe
+    c = Case4(n=[1, 2], lens=[40, 300], page=page, fill=0.0)
+    at = 300 // page
+    for i in {0, at}:
+        for bad in (-1, -2147483648, c.pages, 2147483647):
+            tab = c.tables.copy()
+            tab[1, i] = bad
+            out, lse, st = c.run(block_tables=i32(tab))
+            assert st == lpe.STATUS_BAD_PAGE
+            kc, vc = c.kc.clone(), c.vc.clone()
+            kc[int(c.tables[1, i])] = 0
+            vc[int(c.tables[1, i])] = 0
+            R.check_attend(out, lse, R.attend(c.q, kc, vc, c.indptr, c.lens, c.tables, scale=c.scale), c.dtype)
+
+
+def test_attend4_what_is_not_finite_stays_with_the_rows_that_see_it():
+    import torch
+    c = Case4(n=[4, 4], lens=[200, 129], hq=4, hk=2)
+    clean, clean_lse = c.check()
+    t = 203  # the last draft of group 0: only row 3 sees it
+    page, off = int(c.tables[0, t // c.page]), t % c.page
+    for scales in c.scales:
+        keep = scales[page, :, off].clone()
+        scales[page, :, off] = 0x7F
+        out, lse, st = c.run()
+        scales[page, :, off] = keep
+        rows = [0, 1, 2, 4, 5, 6, 7]
+        assert st == 0 and torch.equal(out[rows], clean[rows]) and torch.equal(lse[rows], clean_lse[rows])
+        assert not bool(out[3].isfinite().all())
+    # a committed token of group 0: its rows, and no others
+    page, off = int(c.tables[0, 60 // c.page]), 60 % c.page
+    for scales in c.scales:
+        keep = scales[page, :, off].clone()
+        scales[page, :, off] = 0xFF
+        out, lse, st = c.run()
+        scales[page, :, off] = keep
+        assert st == 0 and torch.equal(out[4:], clean[4:]) and not bool(out[:4].isfinite().all(-1).any())
+    # a query that is not finite: its head of its row
+    for bad in (float("nan"), float("inf")):
+        keep = c.q[1, 2, 7].clone()
+        c.q[1, 2, 7] = bad
+        out, lse, st = c.run()
+        c.q[1, 2, 7] = keep
+        rest = torch.ones(c.rows, c.hq, dtype=torch.bool, device=dev())
+        rest[1, 2] = False
+        assert st == 0 and torch.equal(out[rest], clean[rest]) and torch.equal(lse[rest], clean_lse[rest])
+        assert not bool(out[1, 2].isfinite().all())
+
+
+@pytest.mark.parametrize("size", [2.0 ** -120, 2.0 ** -30, 2.0 ** 20, 2.0 ** 100])
+def test_attend4_queries_of_any_size(size):
+    """BF16 queries far outside F16's range, with a scale that brings their scores back."""
+    c = Case4(n=[3, 2], lens=[200, 40], prefixes=[20])
+    c.q = (c.q.float() * size).bfloat16()
+    c.q[0, 0, 3] = 2.0 ** -100 * size if size > 1 else 0.0
+    c.q[2] = 0.0
+    c.scale /= size
+    c.check()
+
+
+def test_attend4_extreme_scores():
+    """Scores of magnitude 1e3, rising and falling along the context: the running maximum moves often."""
+    import torch
+    c = Case4(n=[3, 1], lens=[900, 513], hq=4, hk=1, width=0.0)
+    c.q = torch.full_like(c.q, 8.0)
+    t = torch.arange(903, device=dev())
+    for g, count in ((0, 903), (1, 514)):
+        at, off = torch.from_numpy(c.tables[g]).to(dev())[t[:count] // c.page], t[:count] % c.page
+        ramp = (t[:count].float() - 300.0) * (1 if g == 0 else -1) / 64.0
+        c.raw[0][at, :, off] = ramp[:, None, None].expand(count, 1, 128).to(c.raw[0].dtype)
+    c.quantise()
+    c.check()
+
+
+def test_attend4_offsets_past_32_bits():
+    """Codes past 2^32 bytes, the batch in the cache's last pages."""
+    import torch
+    if torch.cuda.get_device_properties(0).total_memory < 60e9:
+        pytest.skip("needs a large card")
+    pages, hk, page, d = 70_000, 4, 256, 128
+    small = Case4(n=[1, 3], lens=[300, 77], hq=4, hk=hk, page=page, prefixes=[200])
+    big = [torch.zeros(pages, hk, page, x.shape[-1], dtype=torch.uint8, device=dev()) for x in (*small.codes, *small.scales)]
+    for x, y in zip(big, (*small.codes, *small.scales)):
+        x[pages - small.pages:] = y
+    up = lambda tab: i32(np.where(tab >= 0, tab + pages - small.pages, -1))  # noqa: E731
+    e4m3 = torch.float8_e4m3fn
+    assert big[0].numel() > 2 ** 32
+    plan = plan_of(max_rows=4, max_groups=2, q_heads=4, kv_heads=hk, page_size=page, num_pages=pages, max_pages=small.tables.shape[1], max_prefixes=1,
+                   max_prefix_pages=small.prefix_tables.shape[1], kv_bits=4)
+    moved = dict(k_cache=big[0], v_cache=big[1], k_scales=big[2].view(e4m3), v_scales=big[3].view(e4m3), block_tables=up(small.tables))
+    out, lse, st = small.run(plan, **moved, prefix_tables=up(small.prefix_tables))
+    assert st == 0
+    R.check_attend(out, lse, small.ref(), small.dtype)
+    # and the append that reaches them
+    k, v = (rand(generator(5), 4, hk, d, dtype="bf16") for _ in range(2))
+    st = status_word()
+    plan.append4(k=k, v=v, positions=i32([0] * 4), group_indptr=i32(small.indptr), lens=i32(small.lens), status=st, **moved)
+    t = small.lens[1] + 2
+    at = int(small.tables[1, t // page]) + pages - small.pages
+    for x, codes, scales in ((k, big[0], big[2]), (v, big[1], big[3])):
+        want = K.quantise_rows(x[-1])
+        assert torch.equal(codes[at, :, t % page], K.pack(want[0])) and torch.equal(scales[at, :, t % page], want[1])
+
+
+def test_attend4_strided_tensors_other_streams_and_graphs():
+    import torch
+    c = Case4(n=[4, 2, 1], lens=[100, 333, 0], prefixes=[150])
+    ref = c.ref()
+    wide = torch.zeros(c.rows, (c.hq + 3) * c.d, dtype=c.q.dtype, device=dev())
+    wide[:, c.d:(c.hq + 1) * c.d] = c.q.flatten(1)
+    q = wide[:, c.d:(c.hq + 1) * c.d].unflatten(1, (c.hq, c.d))
+    outs = torch.full((c.rows, (c.hq + 1) * c.d), 7.0, dtype=c.q.dtype, device=dev())
+    out = outs[:, :c.hq * c.d].unflatten(1, (c.hq, c.d))
+    plan, st, t = c.plan(), status_word(), c.tensors()
+    t["q"] = q
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    plan.attend4(**t, out=out, status=st, stream=side)
+    side.synchronize()
+    R.check_attend(out, None, ref, c.dtype)
+    assert bool((outs[:, c.hq * c.d:] == 7.0).all())
+    # captured once, replayed on new lengths
+    lse = torch.zeros(c.rows, c.hq, device=dev())
+    t["q"] = c.q
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plan.attend4(**t, out=out, lse_out=lse, status=st)
+    for lens in ([100, 333, 0], [3, -1, 0], [0, 0, 0], [100, 12, 0]):
+        t["lens"].copy_(i32(lens))
+        c.lens = lens
+        for g, l in enumerate(lens):
+            for j in range(c.n[g] if l >= 0 else 0):
+                at, off = int(c.tables[g, (l + j) // c.page]), (l + j) % c.page
+                c.raw[0][at, :, off], c.raw[1][at, :, off] = 0.25 * (j + 1), 0.5 * j
+        was = [*c.codes, *c.scales]
+        c.quantise()
+        for x, y in zip(was, (*c.codes, *c.scales)):  # the tensors that the graph reads
+            x.copy_(y)
+        c.codes, c.scales = was[:2], was[2:]
+        graph.replay()
+        torch.cuda.synchronize()
+        R.check_attend(out, lse, c.ref(), c.dtype)
+    assert int(st[0]) == 0
+
+
+def test_attend4_repeats_bit_for_bit_after_other_calls():
+    import torch
+    a = Case4(n=[4] * 30, lens=[(97 * i) % 500 for i in range(30)], prefixes=[700])
+    plan = a.plan()
+    first = a.run(plan)
+    for lens in ([0] * 30, [-1] * 29 + [3], [min(l, 31 * i % 300) for i, l in enumerate(a.lens)]):  # within the groups' pages
+        out, lse, st = a.run(plan, lens=i32(lens), prefix_lens=i32([lens[-1]]))
+        assert st == 0
+    again = a.run(plan)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_attend4_zero_rows_and_zero_groups():
+    import torch
+    c = Case4(n=[1], lens=[5])
+    plan = c.plan()
+    empty = torch.empty(0, c.hq, c.d, dtype=c.q.dtype, device=dev())
+    t = c.tensors()
+    t["q"] = empty
+    t["group_indptr"], t["lens"], t["block_tables"] = i32([0]), i32([]), i32(np.zeros((0, c.tables.shape[1])))
+    plan.attend4(**t, out=empty, status=status_word())
+    t["q"] = c.q
+    out = torch.full_like(c.q, 7.0)
+    plan.attend4(**t, out=out, status=status_word())
+    torch.cuda.synchronize()
+    assert bool((out == 7.0).all())
+
+
+def test_a_call_of_attend4_that_gave_up_gives_zeros():
+    """Waits that run out: the status, 0 and -inf for every row of a group, and the next plan gets the right result."""
+    import time
+    import torch
+    import logprob_epilogue_gb300 as lpe
+    for c in (Case4(n=[2, 3], lens=[300, 40], prefixes=[150], pad_rows=2), Case4(n=[1], lens=[5000], hq=8, hk=1, d=64, dtype="f16")):
+        good, good_lse, st = c.run()
+        assert st == 0
+        rows = c.indptr[-1]
+        plan = c.plan(debug_force_timeout=True, timeout_ns=2_000_000)
+        for _ in range(2):
+            began = time.perf_counter()
+            out, lse, st = c.run(plan)
+            assert time.perf_counter() - began < 5.0
+            assert st == lpe.STATUS_TIMEOUT
+            assert bool((out[:rows] == 0).all()) and bool((lse[:rows] == -np.inf).all())
+            assert bool((out[rows:] == 7.0).all()) and bool((lse[rows:] == 7.0).all())
+        plan.close()
+        out, lse, st = c.run()
+        assert st == 0 and torch.equal(out[:rows], good[:rows]) and torch.equal(lse[:rows], good_lse[:rows])
+
+
+# ---- a round
+
+
+def test_rounds_of_reserve_append4_attend4_commit():
+    """Rounds of requests that come, grow and leave: pages reserved, keys and values appended, attention, commit."""
+    import torch
+    gen = generator(11)
+    hq, hk, d, page, groups, rows_g, width = 8, 2, 128, 16, 6, 4, 9
+    rows, pages = groups * rows_g, 45
+    plan = plan_of(max_rows=rows, max_groups=groups, q_heads=hq, kv_heads=hk, head_dim=d, page_size=page, num_pages=pages,
+                   max_pages=width, max_group_rows=rows_g, max_prefixes=1, max_prefix_pages=5, kv_bits=4)
+    order = np.random.RandomState(1).permutation(pages)
+    ptab, free = order[:5].reshape(1, 5), i32(order[5:])
+    kc, vc, ks, vs = four_caches(pages, hk, page, d)
+    e4m3 = torch.float8_e4m3fn
+    ks, vs = (x.bitwise_and(0x37).view(e4m3) for x in (ks, vs))  # finite, as the prefix's are
+    lens, held, tables = i32([0, 0, 0, 0, 0, -1]), i32([0] * groups), i32(np.full((groups, width), -1))
+    queue, st, cs = torch.tensor([0, pages - 5], dtype=torch.int64, device=dev()), status_word(), table(d)
+    indptr, round_lens, pos = i32([0] * (groups + 1)), i32([0] * groups), i32([0] * rows)
+    caches = dict(k_cache=kc, v_cache=vc, k_scales=ks, v_scales=vs)
+    for step in range(7):
+        counts = i32([(g + step) % rows_g + 1 for g in range(groups)])
+        qkv = rand(gen, rows, (hq + 2 * hk) * d, dtype="bf16")
+        q, k, v = (qkv[:, a * d:b * d].unflatten(1, (b - a, d)) for a, b in ((0, hq), (hq, hq + hk), (hq + hk, hq + 2 * hk)))
+        qo, out = (torch.full((rows, hq, d), 7.0, dtype=torch.bfloat16, device=dev()) for _ in range(2))
+        lse, kh = torch.empty(rows, hq, device=dev()), torch.full((rows, hk, d), 7.0, dtype=torch.bfloat16, device=dev())
+        plan.reserve(lens=lens, counts=counts, held=held, queue=queue, free_pages=free, block_tables=tables, group_indptr=indptr,
+                     round_lens=round_lens, held_out=held, queue_out=queue, positions=pos, starts=i32([70] * groups), status=st)
+        batch_of = dict(group_indptr=indptr, lens=round_lens, block_tables=tables, status=st, **caches)
+        plan.append4(q=q, k=k, v=v, q_out=qo, cos_sin=cs, positions=pos, k_held=kh, **batch_of)
+        plan.attend4(q=qo, out=out, lse_out=lse, prefix_indptr=i32([0, groups]), prefix_lens=i32([70]), prefix_tables=i32(ptab), **batch_of)
+        ref = R.attend(qo, K.values(kc, ks), K.values(vc, vs), indptr.tolist(), round_lens.tolist(), tables.cpu().numpy(), scale=d ** -0.5,
+                       prefix_indptr=[0, groups], prefix_lens=[70], prefix_tables=ptab)
+        n = int(indptr[-1])
+        R.check_attend(out, lse, ref, "bf16", slice(0, n))
+        assert bool((out[n:] == 7.0).all()) and bool((kh[n:] == 7.0).all()) and bool((pos[n:] == -1).all())
+        # the appended keys are the rotated ones, in 4 bits
+        g = 3
+        row, t = int(indptr[g]), int(lens[g])
+        if int(round_lens[g]) >= 0:
+            at = K.values(kc, ks)[int(tables[g, t // page]), :, t % page]
+            assert torch.equal(kh[row].double(), at) and int(pos[row]) == 70 + t
+        accepted = torch.minimum(counts, i32([1, 4, 2, 3, 1, 2]))
+        lens = torch.where(round_lens >= 0, lens + accepted, lens).int()
+        if step == 3:
+            lens[1], lens[5] = -1, 0  # one leaves, one comes
+    assert int(st[0]) == 0
