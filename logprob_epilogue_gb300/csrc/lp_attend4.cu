@@ -20,7 +20,7 @@ constexpr float kRescale = 8.0f;  // growth of the maximum (log2) that moves it
 // Probabilities are lifted by 2^6 (at most 2^14 then): F16 keeps those above 2^-30 of the largest.
 constexpr float kBias = 6.0f;
 constexpr int kWorkers = 8;       // warps that multiply
-constexpr int kMergers = 3;       // warps that add up the workers' results
+constexpr int kFetchers = 4;      // warps that bring pages, a quarter of a tile's tokens each
 constexpr int kStep = 16;         // tokens of a step
 // Registers: the split's sum is what the block is launched with, 384 x 168.
 constexpr int kRegsLaunch = 168, kRegsWorker = 200, kRegsOther = 104;
@@ -35,20 +35,27 @@ struct Cfg4 {
     static constexpr int kCtl = kMerge + kWorkers * 16 * D * 4;
 };
 
-constexpr int kPieces = 8;                          // pieces the fetching warp may be ahead
-constexpr int kPieceReaders = kWorkers + kMergers;  // warps that read each
+constexpr int kPieces = 8;                               // pieces the planning warp may be ahead
+constexpr int kPieceReaders = kWorkers + kFetchers - 1;  // warps that read each
+
+// Where the tokens of a piece lie.
+struct Pages {
+    const int* table;
+    long long token;  // the first
+};
 
 struct Ctl4 : PlanCtl<Fragments> {
     uint64_t full[16], empty[16], piece_full[kPieces], piece_empty[kPieces];
     Piece piece[kPieces];
-    uint64_t merge_full, merge_empty, drain;
+    Pages pages[kPieces];
+    uint64_t merge_full, merge_done, drain;
     float2 ml[kWorkers][16];
     int abort;
 };
 
 // D += A B, 16 x 8 x 16, F16 with FP32 sums.
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -144,58 +151,96 @@ __device__ __forceinline__ void load_rows(const AttendParams& p, const Piece& x,
     for (int j = 0; j < D / 8; ++j) r.o[j][0] = r.o[j][1] = r.o[j][2] = r.o[j][3] = 0.0f;
 }
 
-// Sixteen tokens from `at` on of a stage, `have` of whose tokens exist.
+// A step is sixteen tokens from `at` on of a stage, `have` of whose tokens exist.
 //
 // Column c of eight scores is token (c >> 1) + 4 (c & 1) of its eight, so that
 // the values that a thread multiplies (columns 2t and 2t + 1) are tokens t and t
 // + 4, and the four t of a load lie side by side.
-template <int D>
-__device__ __forceinline__ void step(const unsigned char* stage, int at, int have, Rows<D>& r) {
+
+// The products of one step's values and of another's scores: a product of either
+// kind in turn, since a score's follow on one another.  kScores: s of the step at
+// token `next`; kValues: the probabilities `a` times the values at token `at`.
+template <int D, bool kScores, bool kValues>
+__device__ __forceinline__ void products(const unsigned char* stage, int next, float (&s)[2][4], int at, int have, const uint32_t (&a)[4], Rows<D>& r) {
     using C = Cfg4<D>;
-    constexpr int kK = D / 32, kV = D / 64;  // words of a thread: of a key, of a value
+    constexpr int kK = D / 32, kV = D / 64;  // words of a thread's part of a key, of a value
     const int lane = threadIdx.x & 31, t = lane & 3, g = lane >> 2;
     const unsigned char* ks = stage + 2 * C::kCodes;
     const unsigned char* vs = ks + C::kScales;
-
-    // scores
-    float s[2][4];
+    uint32_t kw[2][kK], ke[2][kK / 2], vw[2][2][kV], ve[2];
+    if constexpr (kScores) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-        const int token = at + b * 8 + (g >> 1) + 4 * (g & 1);
-        uint32_t w[kK], e[kK / 2];
-        if constexpr (D == 128) {
-            const uint4 x = *reinterpret_cast<const uint4*>(stage + token * (D / 2) + t * 16);
-            w[0] = x.x, w[1] = x.y, w[kK - 2] = x.z, w[kK - 1] = x.w;
-            const uint32_t two = widen_scales(*reinterpret_cast<const uint16_t*>(ks + token * (D / 16) + t * 2));
-            e[0] = __byte_perm(two, 0, 0x1010);
-            e[kK / 2 - 1] = __byte_perm(two, 0, 0x3232);
-        } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(stage + token * (D / 2) + t * 8);
-            w[0] = x.x, w[1] = x.y;
-            e[0] = __byte_perm(widen_scales(ks[token * (D / 16) + t]), 0, 0x1010);
+        for (int b = 0; b < 2; ++b) {
+            const int token = next + b * 8 + (g >> 1) + 4 * (g & 1);
+            if constexpr (D == 128) {
+                const uint4 x = *reinterpret_cast<const uint4*>(stage + token * (D / 2) + t * 16);
+                kw[b][0] = x.x, kw[b][1] = x.y, kw[b][kK - 2] = x.z, kw[b][kK - 1] = x.w;
+                const uint32_t two = widen_scales(*reinterpret_cast<const uint16_t*>(ks + token * (D / 16) + t * 2));
+                ke[b][0] = __byte_perm(two, 0, 0x1010);
+                ke[b][kK / 2 - 1] = __byte_perm(two, 0, 0x3232);
+            } else {
+                const uint2 x = *reinterpret_cast<const uint2*>(stage + token * (D / 2) + t * 8);
+                kw[b][0] = x.x, kw[b][1] = x.y;
+                ke[b][0] = __byte_perm(widen_scales(ks[token * (D / 16) + t]), 0, 0x1010);
+            }
+            s[b][0] = s[b][1] = s[b][2] = s[b][3] = 0.0f;
         }
-        s[b][0] = s[b][1] = s[b][2] = s[b][3] = 0.0f;
+    }
+    if constexpr (kValues) {
 #pragma unroll
-        for (int i = 0; i < kK; ++i) {
-            uint32_t h[4];
-            widen_codes(w[i], h);
+        for (int b = 0; b < 2; ++b) {
+            uint32_t scale[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const int k = 2 * i + u;  // product
-                mma(s[b], r.q[0][2 * k], r.q[1][2 * k], r.q[0][2 * k + 1], r.q[1][2 * k + 1], mul2(h[2 * u], e[i / 2]), mul2(h[2 * u + 1], e[i / 2]));
+                const int token = at + b * 8 + t + 4 * u;
+                scale[u] = vs[token * (D / 16) + (D == 128 ? g : g >> 1)];
+                if (token >= have) scale[u] = 0u;  // what lies there may be NaN, and 0 * v has to stay 0
+                if constexpr (D == 128) {
+                    const uint2 x = *reinterpret_cast<const uint2*>(stage + C::kCodes + token * (D / 2) + g * 8);
+                    vw[b][u][0] = x.x, vw[b][u][kV - 1] = x.y;
+                } else {
+                    vw[b][u][0] = *reinterpret_cast<const uint32_t*>(stage + C::kCodes + token * (D / 2) + g * 4);
+                }
             }
+            ve[b] = widen_scales(scale[0] | scale[1] << 8);
         }
     }
-    const bool ragged = at + kStep > have;
-    if (ragged) {
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+    for (int i = 0; i < kK; ++i) {
+        uint32_t kh[2][4], vh[2][4];
+        if constexpr (kScores) widen_codes(kw[0][i], kh[0]), widen_codes(kw[1][i], kh[1]);
+        if constexpr (kValues) {
+            // two tokens' codes side by side
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (at + b * 8 + t + 4 * (i & 1) >= have) s[b][i] = kNegInf;
+            for (int b = 0; b < 2; ++b) {
+                const uint32_t x = vw[b][0][i / 2], y = vw[b][1][i / 2];
+                widen_codes(i & 1 ? lop_select(x >> 4, y, 0x0F0F0F0Fu) : lop_select(x, y << 4, 0x0F0F0F0Fu), vh[b]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (kScores) {
+                const int b = j & 1, u = j >> 1, k = 2 * i + u;
+                mma(s[b], r.q[0][2 * k], r.q[1][2 * k], r.q[0][2 * k + 1], r.q[1][2 * k + 1], mul2(kh[b][2 * u], ke[b][i / 2]), mul2(kh[b][2 * u + 1], ke[b][i / 2]));
+            }
+            if constexpr (kValues)
+                mma(r.o[i / 2 * 8 + 2 * j + (i & 1)], a[0], a[1], a[2], a[3], mul2(vh[0][j], ve[0]), mul2(vh[1][j], ve[1]));
+        }
     }
+}
 
-    // The rows' maxima: what they stand at holds until a score is 2^kRescale above it.
+__device__ __forceinline__ void mask_scores(int at, int have, float (&s)[2][4]) {
+    if (at + kStep <= have) return;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (at + b * 8 + (int)(threadIdx.x & 3) + 4 * (i & 1) >= have) s[b][i] = kNegInf;
+}
+
+// The rows' maxima: what they stand at holds until a score is 2^kRescale above it.
+template <int D>
+__device__ __forceinline__ void raise(const float (&s)[2][4], Rows<D>& r) {
     float top[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) top[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
@@ -218,7 +263,11 @@ __device__ __forceinline__ void step(const unsigned char* stage, int at, int hav
 #pragma unroll
         for (int j = 0; j < D / 8; ++j) r.o[j][0] *= f[0], r.o[j][1] *= f[0], r.o[j][2] *= f[1], r.o[j][3] *= f[1];
     }
-    uint32_t a[4];  // probabilities
+}
+
+// A step's probabilities.
+template <int D>
+__device__ __forceinline__ void probabilities(const float (&s)[2][4], Rows<D>& r, uint32_t (&a)[4]) {
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -227,40 +276,50 @@ __device__ __forceinline__ void step(const unsigned char* stage, int at, int hav
             r.l[h] += x + y;
             a[2 * b + h] = Half<false>::pack(x, y);
         }
+}
 
-    // values: two tokens' codes side by side
-    uint32_t e[2], w[2][2][kV];
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-        uint32_t scale[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int token = at + b * 8 + t + 4 * u;
-            scale[u] = vs[token * (D / 16) + (D == 128 ? g : g >> 1)];
-            if (ragged && token >= have) scale[u] = 0u;  // what lies there may be NaN, and 0 * v has to stay 0
-            if constexpr (D == 128) {
-                const uint2 x = *reinterpret_cast<const uint2*>(stage + C::kCodes + token * (D / 2) + g * 8);
-                w[b][u][0] = x.x, w[b][u][kV - 1] = x.y;
-            } else {
-                w[b][u][0] = *reinterpret_cast<const uint32_t*>(stage + C::kCodes + token * (D / 2) + g * 4);
-            }
-        }
-        e[b] = widen_scales(scale[0] | scale[1] << 8);
+// Steps from token `at` to `end` of a stage: a step's values beside the next one's scores, so that the tensor core has
+// work while a warp waits for either.
+template <int D>
+__device__ __forceinline__ void steps(const unsigned char* stage, int at, int end, int have, Rows<D>& r) {
+    float s[2][4];
+    uint32_t a[4] = {0u, 0u, 0u, 0u};
+    products<D, true, false>(stage, at, s, 0, 0, a, r);
+#pragma unroll 1
+    for (;; at += kStep) {
+        mask_scores(at, have, s);
+        raise<D>(s, r);
+        probabilities<D>(s, r, a);
+        if (at + kStep >= end) break;
+        products<D, true, true>(stage, at + kStep, s, at, have, a, r);
     }
-#pragma unroll
-    for (int i = 0; i < kV; ++i)
-#pragma unroll
-        for (int odd = 0; odd < 2; ++odd) {
-            uint32_t h[2][4];
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const uint32_t x = w[b][0][i], y = w[b][1][i];
-                widen_codes(odd ? lop_select(x >> 4, y, 0x0F0F0F0Fu) : lop_select(x, y << 4, 0x0F0F0F0Fu), h[b]);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                mma(r.o[i * 8 + 2 * j + odd], a[0], a[1], a[2], a[3], mul2(h[0][j], e[0]), mul2(h[1][j], e[1]));
+    products<D, false, true>(stage, 0, s, at, have, a, r);
+}
+
+// The workers' results of a piece, fragment by fragment of the rows: each thread
+// adds up what the workers of a fragment have of four lanes of a row.
+template <int D>
+__device__ __forceinline__ void merge_piece(const AttendParams& p, const Piece& x, const Ctl4* ctl, const float4* merge, int worker, int fragments) {
+    const int lane = threadIdx.x & 31, rows = x.rows * p.share;
+    for (int i = worker; i < fragments * (D / 8) && x.part >= 0; i += kWorkers) {
+        const int mt = i / (D / 8), chunk = i % (D / 8), h = chunk / (D / 16), e = chunk / (D / 32) & 1, j = chunk % (D / 32);
+        const int in = (lane >> 2) + 8 * h, row = mt * 16 + in;
+        if (row >= rows) continue;
+        float top = kNegInf, l = 0.0f;
+        for (int w = mt; w < kWorkers; w += fragments) top = fmaxf(top, ctl->ml[w][in].x);
+        const float from = top == kNegInf ? 0.0f : top;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int w = mt; w < kWorkers; w += fragments) {
+            const float2 ml = ctl->ml[w][in];
+            if (ml.x == kNegInf && ml.y == 0.0f) continue;  // saw nothing
+            const float f = ex2(ml.x - from);
+            const float4 v = merge[(w * (D / 8) + chunk) * 32 + lane];
+            l = fmaf(ml.y, f, l);
+            o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
         }
+        if (chunk % (D / 16) == 0 && (lane & 3) == 0) p.sc.part_ml[x.part + row] = make_float2(top, l);
+        reinterpret_cast<float4*>(p.sc.part_o)[part_chunk<D>(x.part, x.part_stride, row, (D / 32) * (2 * (lane & 3) + e) + j)] = o;
+    }
 }
 
 template <bool kBf16, int D>
@@ -273,11 +332,11 @@ __global__ void __launch_bounds__(kThreads, 1) lp_attend4_kernel(const AttendPar
     const int warp = __shfl_sync(kFull, tid >> 5, 0);  // the same for the warp, as the compiler sees
     const unsigned long long limit = p.timeout_ns;
     if (warp == kWarps - 1) {  // while the kernel ahead still runs
-        if (lane < C::kStages) tc::mbar_init(&ctl->full[lane], 1), tc::mbar_init(&ctl->empty[lane], kWorkers);
+        if (lane < C::kStages) tc::mbar_init(&ctl->full[lane], kFetchers * 32), tc::mbar_init(&ctl->empty[lane], kWorkers);
         if (lane < kPieces) tc::mbar_init(&ctl->piece_full[lane], 1), tc::mbar_init(&ctl->piece_empty[lane], kPieceReaders);
         if (lane == 0) {
             tc::mbar_init(&ctl->merge_full, kWorkers);
-            tc::mbar_init(&ctl->merge_empty, kMergers);
+            tc::mbar_init(&ctl->merge_done, kWorkers);
             tc::mbar_init(&ctl->drain, 1);
             ctl->abort = 0;
         }
@@ -300,12 +359,13 @@ __global__ void __launch_bounds__(kThreads, 1) lp_attend4_kernel(const AttendPar
     Piece x;
     bool ok = !p.force_timeout;
     uint32_t n_piece = 0, it = 0;  // it: stages
-    // the next piece, from the fetching warp; false at the end of the run
-    auto next_piece = [&]() {
+    // the next piece, from the planning warp; false at the end of the run
+    auto next_piece = [&](Pages* pages) {
         const uint32_t i = n_piece % kPieces;
         ok = tc::warp_wait(&ctl->piece_full[i], n_piece / kPieces & 1u, limit, abort);
         if (!ok) return false;
         x = ctl->piece[i];
+        if (pages != nullptr) *pages = ctl->pages[i];
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&ctl->piece_empty[i]);
         ++n_piece;
@@ -314,27 +374,29 @@ __global__ void __launch_bounds__(kThreads, 1) lp_attend4_kernel(const AttendPar
 
     if (warp >= 4) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsWorker));
-        // ---- products: fragment mt of the unit's rows, every slices-th step of the tokens
+        // ---- products: fragment mt of the unit's rows, every slices-th chunk of the tokens
         const int worker = warp - 4;
         uint32_t merged = 0;
-        while (ok && next_piece()) {
+        while (ok && next_piece(nullptr)) {
             const int fragments = (x.rows * p.share + 15) >> 4, mt = worker % fragments, slice = worker / fragments;
             const int slices = (kWorkers - mt + fragments - 1) / fragments;
             Rows<D> r;
             load_rows<kBf16, D>(p, x, mt, r);
+            // tokens that a worker takes in a row: long ones keep the products close, short ones give every worker some
+            const int chunk = x.tiles * 2 >= slices ? 64 : (x.tiles * 4 >= slices ? 32 : 16);
+            int s = slice * chunk;  // the next, in its tile
             for (int i = 0; ok && i < x.tiles; ++i, ++it) {
                 const uint32_t at = it % C::kStages;
                 ok = tc::warp_wait(&ctl->full[at], it / C::kStages & 1u, limit, abort);
                 if (!ok) break;
                 const int left = x.left - i * kKTile, have = left < kKTile ? left : kKTile;
-                for (int s = slice * kStep; s < have; s += slices * kStep) step<D>(smem + at * C::kStage, s, have, r);
+                for (; s < have; s += slices * chunk) steps<D>(smem + at * C::kStage, s, s + chunk < have ? s + chunk : have, have, r);
+                s -= kKTile;
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&ctl->empty[at]);
             }
+            ok = ok && tc::warp_wait(&ctl->merge_done, (merged & 1u) ^ 1u, limit, abort);  // the piece before is read
             if (!ok) break;
-            ok = tc::warp_wait(&ctl->merge_empty, (merged & 1u) ^ 1u, limit, abort);
-            if (!ok) break;
-            ++merged;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 r.l[h] += __shfl_xor_sync(kFull, r.l[h], 1);
@@ -349,16 +411,35 @@ __global__ void __launch_bounds__(kThreads, 1) lp_attend4_kernel(const AttendPar
             }
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&ctl->merge_full);
+            ok = tc::warp_wait(&ctl->merge_full, merged & 1u, limit, abort);
+            if (!ok) break;
+            ++merged;
+            merge_piece<D>(p, x, ctl, merge, worker, fragments);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&ctl->merge_done);
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        // ---- pages into the ring: 32 tokens of each tile, a token's page per lane.  Warp 0 plans, a piece ahead.
+        Walk<Fragments> walk;
+        Pages from = {nullptr, 0}, ahead = from;
+        Piece y;
+        auto plan_piece = [&]() {  // into y and `ahead`, and to the other warps
+            const bool more = walk.next(p, y);
+            ahead.table = walk.table, ahead.token = walk.token;
+            const uint32_t i = n_piece % kPieces;
+            ok = tc::warp_wait(&ctl->piece_empty[i], (n_piece / kPieces & 1u) ^ 1u, limit, abort);
+            if (!ok) return false;
+            if (lane == 0) {
+                ctl->piece[i] = y;
+                ctl->pages[i] = ahead;
+                tc::mbar_arrive(&ctl->piece_full[i]);
+            }
+            ++n_piece;
+            return more;
+        };
+        bool more = false;
         if (warp == 0) {
-            // ---- pages into the ring: lanes 0-15 the keys, 16-31 the values, a page (or a tile of one) each
-            const int step = p.page_shift < 7 ? 1 << p.page_shift : kKTile;  // tokens per copy
-            const int box = lane & 15, tok = box * step, half = lane >> 4;
-            const unsigned char* codes = static_cast<const unsigned char*>(half == 0 ? p.k_cache : p.v_cache);
-            const unsigned char* scales = half == 0 ? p.k_scales : p.v_scales;
-            Walk<Fragments> walk;
             walk.cta = blockIdx.x;
             walk.deal = ctl->deal_first;
             walk.deal_end = ctl->deal_last + 1;
@@ -372,87 +453,56 @@ __global__ void __launch_bounds__(kThreads, 1) lp_attend4_kernel(const AttendPar
                 walk.finish[k] = any ? runs[k].start(blockIdx.x + 1) : 0;
             }
             walk.enter(0);
-            auto page_of = [&](int i) {
-                const long long at = walk.token + i * kKTile + tok;
-                return i < x.tiles && i * kKTile + tok < x.left ? walk.table[at >> p.page_shift] : -1;
-            };
-            for (bool more = ok; ok && more;) {
-                more = walk.next(p, x);
-                const uint32_t pi = n_piece % kPieces;
-                ok = tc::warp_wait(&ctl->piece_empty[pi], (n_piece / kPieces & 1u) ^ 1u, limit, abort);
-                if (!ok) break;
-                if (lane == 0) {
-                    ctl->piece[pi] = x;
-                    tc::mbar_arrive(&ctl->piece_full[pi]);
-                }
-                ++n_piece;
+            more = ok && plan_piece();
+        }
+        const int mask = (1 << p.page_shift) - 1, quarter = warp * 32;
+        while (ok) {
+            if (warp == 0) {
                 if (!more) break;
-                // the pages of the next tile are read before this tile's waits
-                int next_page = page_of(0);
-                for (int i = 0; ok && i < x.tiles; ++i) {
-                    const int left = x.left - i * kKTile, valid = left < kKTile ? left : kKTile;
-                    const int boxes = (valid + step - 1) / step;
-                    const int y = (int)((walk.token + i * kKTile + tok) & ((1 << p.page_shift) - 1));
-                    const int page = next_page;
-                    next_page = page_of(i + 1);
-                    const uint32_t at = it % C::kStages;
-                    ok = tc::warp_wait(&ctl->empty[at], (it / C::kStages & 1u) ^ 1u, limit, abort);
-                    if (!ok) break;
-                    const uint32_t to = tc::smem_addr(smem + at * C::kStage);
-                    const bool copies = box < boxes, good = page >= 0 && page < p.num_pages;
-                    const unsigned got = __ballot_sync(kFull, copies && good);
-                    if (copies && !good) {  // a page that does not exist reads as zeros
-                        atomicOr(p.status, kStatusBadPage);
-                        uint4* z = reinterpret_cast<uint4*>(smem + at * C::kStage + 2 * C::kCodes + half * C::kScales + tok * (D / kBlock4));
-                        for (int k = 0; k < step * (D / kBlock4) / 16; ++k) z[k] = make_uint4(0u, 0u, 0u, 0u);
-                        tc::fence_async_shared();
-                    }
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_expect(&ctl->full[at], (uint32_t)__popc(got) * step * (D / 2 + D / kBlock4));
-                    __syncwarp();
-                    if (copies && good) {
-                        const long long slot = (((long long)page * p.kv_heads + x.kvh) << p.page_shift) + y;
-                        tc::bulk_load(to + half * C::kCodes + tok * (D / 2), codes + slot * (D / 2), step * (D / 2), &ctl->full[at]);
-                        tc::bulk_load(to + 2 * C::kCodes + half * C::kScales + tok * (D / kBlock4), scales + slot * (D / kBlock4), step * (D / kBlock4), &ctl->full[at]);
-                    }
-                    ++it;
-                }
-            }
-            // no copy outlives the block, whatever its readers did
-            int none = 0;
-            for (uint32_t i = it > C::kStages ? it - C::kStages : 0; i < it; ++i)
-                tc::mbar_wait(&ctl->full[i % C::kStages], i / C::kStages & 1u, limit, &none);
-        } else {
-            // ---- the workers' results of a piece, added up
-            uint32_t merged = 0;
-            while (ok && next_piece()) {
-                ok = tc::warp_wait(&ctl->merge_full, merged & 1u, limit, abort);
+                x = y, from = ahead;
+                more = plan_piece();
                 if (!ok) break;
-                ++merged;
-                const int rows = x.rows * p.share, fragments = (rows + 15) >> 4;
-                for (int i = (warp - 1) * 32 + lane; i < fragments * (D / 8) * 32 && x.part >= 0; i += kMergers * 32) {
-                    const int mt = i / (D / 8 * 32), chunk = i / 32 % (D / 8), h = chunk / (D / 16), e = chunk / (D / 32) & 1, j = chunk % (D / 32);
-                    const int in = (lane >> 2) + 8 * h, row = mt * 16 + in;
-                    if (row >= rows) continue;
-                    float top = kNegInf, l = 0.0f;
-                    for (int w = mt; w < kWorkers; w += fragments) top = fmaxf(top, ctl->ml[w][in].x);
-                    const float from = top == kNegInf ? 0.0f : top;
-                    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    for (int w = mt; w < kWorkers; w += fragments) {
-                        const float2 ml = ctl->ml[w][in];
-                        if (ml.x == kNegInf && ml.y == 0.0f) continue;  // saw nothing
-                        const float f = ex2(ml.x - from);
-                        const float4 v = merge[(w * (D / 8) + chunk) * 32 + lane];
-                        l = fmaf(ml.y, f, l);
-                        o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
-                    }
-                    if (chunk % (D / 16) == 0 && (lane & 3) == 0) p.sc.part_ml[x.part + row] = make_float2(top, l);
-                    reinterpret_cast<float4*>(p.sc.part_o)[part_chunk<D>(x.part, x.part_stride, row, (D / 32) * (2 * (lane & 3) + e) + j)] = o;
+            } else if (!next_piece(&from)) {
+                break;
+            }
+            auto page_of = [&](int i) {
+                const int t = i * kKTile + quarter + lane;
+                return i < x.tiles && t < x.left ? from.table[(from.token + t) >> p.page_shift] : -1;
+            };
+            int next_page = page_of(0);  // a tile's pages are read before the waits of the one before
+            for (int i = 0; i < x.tiles; ++i, ++it) {
+                const int page = next_page, t = i * kKTile + quarter + lane;
+                next_page = page_of(i + 1);
+                const uint32_t at = it % C::kStages;
+                ok = tc::warp_wait(&ctl->empty[at], (it / C::kStages & 1u) ^ 1u, limit, abort);
+                if (!ok) break;
+                const bool exists = t < x.left, good = page >= 0 && page < p.num_pages;
+                if (exists && !good) atomicOr(p.status, kStatusBadPage);  // such a page reads as zeros
+                const long long slot = exists && good ? (((long long)page * p.kv_heads + x.kvh) << p.page_shift) + ((from.token + t) & mask) : -1;
+                const uint32_t to = tc::smem_addr(smem + at * C::kStage);
+                constexpr int kPer = D / 32, kAtOnce = 32 / kPer;  // 16-byte parts of a token's codes; tokens of an instruction
+#pragma unroll
+                for (int j = 0; j < 32 / kAtOnce; ++j) {
+                    const int token = j * kAtOnce + lane / kPer;
+                    const long long from_slot = __shfl_sync(kFull, slot, token);
+                    const long long byte = (from_slot < 0 ? 0 : from_slot) * (D / 2) + lane % kPer * 16;
+                    const uint32_t dst = to + (quarter + token) * (D / 2) + lane % kPer * 16;
+                    tc::copy16_or_zeros(dst, static_cast<const unsigned char*>(p.k_cache) + byte, from_slot >= 0);
+                    tc::copy16_or_zeros(dst + C::kCodes, static_cast<const unsigned char*>(p.v_cache) + byte, from_slot >= 0);
                 }
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&ctl->merge_empty);
+                {
+                    // scales: 16 bytes are those of 256 / D tokens (of one page), lanes 0-15 of keys, 16-31 of values
+                    constexpr int kTokens = 256 / D, kLanes = 32 / kTokens;
+                    const int l = lane & 15, token = l * kTokens & 31;
+                    const long long from_slot = __shfl_sync(kFull, slot, token);
+                    const unsigned char* src = (lane < 16 ? p.k_scales : p.v_scales) + (from_slot < 0 ? 0 : from_slot) * (D / kBlock4);
+                    const uint32_t dst = to + 2 * C::kCodes + (lane < 16 ? 0 : C::kScales) + (quarter + token) * (D / kBlock4);
+                    if (l < kLanes) tc::copy16_or_zeros(dst, src, from_slot >= 0);
+                }
+                tc::copies_arrive(&ctl->full[at]);
             }
         }
+        tc::copies_done();  // no copy outlives the block, whatever its readers did
     }
     __syncthreads();
     if (tid == 0) {
