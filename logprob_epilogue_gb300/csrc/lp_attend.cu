@@ -72,30 +72,50 @@ namespace {
 // tokens: 762 us; 32 tokens 785, 96 790, all at once 809).
 constexpr int kEarly = 64;
 constexpr float kRescale = 8.0f;  // growth of the maximum (log2) that moves it
-// Registers: the softmax warpgroups hold 128 scores per thread.  The split's
-// sum is what the block is launched with, 384 x 168.
-constexpr int kRegsLaunch = 168, kRegsSoftmax = 200, kRegsOther = 104;
-static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * kRegsLaunch, "register split");
+// Of a block.  Registers: the softmax warpgroups hold 128 scores per thread.  The
+// split's sum is what the block is launched with (384 x 168, 512 x 128).
+template <bool kFour>
+struct Block {
+    static constexpr int kThreads = kFour ? 512 : 384, kWarps = kThreads / 32;
+    static constexpr int kRegsLaunch = kFour ? 128 : 168, kRegsSoftmax = kFour ? 184 : 200, kRegsOther = kFour ? 72 : 104;
+    static constexpr int kPieceReaders = kFour ? 15 : 11;  // two warps of the products, one that loads queries, eight of softmax, four that expand
+    static_assert(2 * kRegsSoftmax + (kFour ? 2 : 1) * kRegsOther <= kThreads / 128 * kRegsLaunch, "register split");
+};
 
 // Tensor memory columns: two score tiles, two accumulators.
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256, kColStep = 128;
 
-template <int D>
+template <int D, bool kFour>
 struct Cfg {
-    static constexpr int kTileBytes = kKTile * D * 2;     // one K, V or Q tile
-    static constexpr int kSlots = 5 * 128 / D;            // ring of K and V tiles: 160 KiB
-    static constexpr int kCtl = (2 + kSlots) * kTileBytes;
+    static constexpr int kTileBytes = kKTile * D * 2;                // one K, V or Q tile
+    static constexpr int kSlots = (kFour ? 4 : 5) * 128 / D;         // ring of K and V tiles: 160 KiB (4 bits: 128)
+    static constexpr int kEntries = 3;                               // 4 bits: a warp's ring of K and V codes and scales,
+    static constexpr int kEntry = 32 * (D / 2 + D / kBlock4);        // 32 tokens each
+    static constexpr int kCodes = (2 + kSlots) * kTileBytes;
+    static constexpr int kCtl = kCodes + (kFour ? 4 * kEntries * kEntry : 0);
 };
 
 constexpr int kPieces = 8;        // pieces the fetching warp may be ahead
-constexpr int kPieceReaders = 11; // warps that read each: two of the products, one that loads queries, eight of softmax
 
-struct Ctl : PlanCtl<Pairs> {
+// Where the tokens of a piece lie.
+struct Pages {
+    const int* table;
+    long long token;  // the first
+};
+
+template <bool kFour>
+using RuleOf = std::conditional_t<kFour, Pairs4, Pairs>;
+
+template <bool kFour>
+struct Ctl : PlanCtl<RuleOf<kFour>> {
     uint64_t full[10], empty[10], piece_full[kPieces], piece_empty[kPieces];
     Piece piece[kPieces];
     uint64_t q_full[2], q_free[2], s_full[2], p_early[2], p_ready[2], pv_done[2], o_free[2], q_grant, clean, drain;
     uint32_t tmem, issued, batches[2];  // ring fills under way or done; see take_turn
     int abort;
+    // 4 bits: of the pieces; what a tile's row of queries was divided by, of the last four pieces
+    Pages pages[kFour ? kPieces : 1];
+    float unit[kFour ? 4 : 1][2][kFour ? kQTile : 1];
 };
 
 __device__ __forceinline__ unsigned long long pack2(uint32_t a, uint32_t b) {
@@ -265,22 +285,185 @@ __device__ __forceinline__ void load_queries(const AttendParams& p, int row0, in
     tc::fence_async_shared();
 }
 
-template <bool kBf16, int D>
-__global__ void __launch_bounds__(kThreads, 1)
-    lp_attend_kernel(const AttendParams p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
-    using H = Half<kBf16>;
-    using T = typename H::T;
-    using C = Cfg<D>;
+// The power of two that brings a row's largest lane, `top`, to [2^14, 2^15) and
+// what undoes it (1 for rows of zeros, infinities or NaN).
+__device__ __forceinline__ float2 lift_of(float top) {
+    const int field = (int)(__float_as_uint(top) >> 23);
+    int up = 141 - field;
+    up = up > 126 ? 126 : up;
+    if (field == 255 || top == 0.0f) up = 0;
+    return make_float2(__uint_as_float((uint32_t)(up + 127) << 23), __uint_as_float((uint32_t)(127 - up) << 23));
+}
+
+// The same from BF16 to F16, each row by its power of two; D / 8 threads have a
+// row, `n` a multiple of 32.  unit[row]: what undoes it.
+template <int D>
+__device__ __forceinline__ void lift_queries(const AttendParams& p, int row0, int rows, int kvh, uint32_t dst, int again, float* unit, int t, int n) {
+    constexpr int kChunks = D / 8, kAtOnce = 4;
+    const int ch = t % kChunks, total = rows * p.share, step = n / kChunks;
+    const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.q) + (long long)row0 * p.q_stride + (long long)kvh * p.share * D + ch * 8;
+    for (int base = 0; base < total; base += kAtOnce * step) {
+        uint4 w[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int row = base + k * step + t / kChunks, per = (row * p.share_inv) >> 16, head = row - per * p.share;
+            w[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < total) w[k] = *reinterpret_cast<const uint4*>(src + per * p.q_stride + head * D);
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int row = base + k * step + t / kChunks;
+            float x[8];
+            widen8<true>(w[k], x);
+            float top = fabsf(x[0]);
+#pragma unroll
+            for (int e = 1; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
+#pragma unroll
+            for (int o = kChunks / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+            if (row >= total) continue;
+            const float2 lift = lift_of(top);
+            if (ch == 0) unit[row] = lift.y;
+            const uint4 y = make_uint4(Half<false>::pack(x[0] * lift.x, x[1] * lift.x), Half<false>::pack(x[2] * lift.x, x[3] * lift.x),
+                                       Half<false>::pack(x[4] * lift.x, x[5] * lift.x), Half<false>::pack(x[6] * lift.x, x[7] * lift.x));
+            const uint32_t at = dst + (ch >> 3) * (kQTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+            tc::store16(at, y);
+            if (again > 0) tc::store16(at + again * 128, y);
+        }
+    }
+    tc::fence_async_shared();
+}
+
+// A cache in 4 bits into the ring of K and V tiles, by four warps: 32 tokens of
+// each tile are a warp's, from their pages (a token's per lane) by way of a ring of
+// its own to F16 in the places where the tensor core reads them.
+template <int D>
+__device__ __forceinline__ void expand(const AttendParams& p, unsigned char* smem, Ctl<true>* ctl, int quarter, bool ok, unsigned long long limit) {
+    using C = Cfg<D, true>;
+    constexpr int kParts = D / 32, kAtOnce = 32 / kParts;  // 16-byte parts of a token's codes; tokens of an instruction
+    volatile int* abort = &ctl->abort;
+    const int lane = threadIdx.x & 31, mask = (1 << p.page_shift) - 1;
+    unsigned char* entries = smem + C::kCodes + quarter * (C::kEntries * C::kEntry);
+    // a token's parts are turned, so that the lanes that read a part of eight tokens meet every bank once
+    auto place = [](int token, int part) { return token * (D / 2) + (part ^ (D == 128 ? token >> 1 & 3 : token >> 2 & 1)) * 16; };
+
+    // what is fetched: the piece, its tile, the slot of this lane's token; whether the keys of the tile are under way
+    Piece x = {};
+    Pages from = {nullptr, 0};
+    uint32_t n_piece = 0, fetched = 0, done = 0;
+    int tile = 0, next_page = -1;
+    long long slot = -1;
+    bool more = true, keys = false;
+    auto page_of = [&](int i) {
+        const int t = i * kKTile + quarter * 32 + lane;
+        return i < x.tiles && t < x.left ? from.table[(from.token + t) >> p.page_shift] : -1;
+    };
+    auto fetch = [&]() {  // the next entry; false at the end of the run
+        if (!keys) {
+            while (tile >= x.tiles) {
+                const uint32_t i = n_piece % kPieces;
+                ok = tc::warp_wait(&ctl->piece_full[i], n_piece / kPieces & 1u, limit, abort);
+                if (!ok) return false;
+                x = ctl->piece[i];
+                from = ctl->pages[i];
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&ctl->piece_empty[i]);
+                ++n_piece;
+                if (x.rows == 0) return false;
+                tile = 0;
+                next_page = page_of(0);
+            }
+            const int page = next_page, t = tile * kKTile + quarter * 32 + lane;
+            next_page = page_of(++tile);  // before the waits of this one
+            const bool exists = t < x.left, good = page >= 0 && page < p.num_pages;
+            if (exists && !good) atomicOr(p.status, kStatusBadPage);  // such a page reads as zeros
+            slot = exists && good ? (((long long)page * p.kv_heads + x.kvh) << p.page_shift) + ((from.token + t) & mask) : -1;
+        }
+        keys = !keys;
+        const unsigned char* codes = static_cast<const unsigned char*>(keys ? p.k_cache : p.v_cache);
+        const uint32_t to = tc::smem_addr(entries + fetched % C::kEntries * C::kEntry);
+#pragma unroll
+        for (int j = 0; j < 32 / kAtOnce; ++j) {
+            const int token = j * kAtOnce + lane / kParts, part = lane % kParts;
+            const long long at = __shfl_sync(kFull, slot, token);
+            tc::copy16_or_zeros(to + place(token, part), codes + (at < 0 ? 0 : at) * (D / 2) + part * 16, at >= 0);
+        }
+        tc::copy_or_zeros<D / kBlock4>(to + 16 * D + lane * (D / kBlock4), (keys ? p.k_scales : p.v_scales) + (slot < 0 ? 0 : slot) * (D / kBlock4), slot >= 0);
+        ++fetched;
+        return true;
+    };
+    while (ok) {
+        while (more && fetched - done < C::kEntries) {
+            more = fetch();
+            tc::copies_commit();
+        }
+        if (!ok || done == fetched) break;
+        const uint32_t ahead = fetched - done - 1 + (more ? 0 : 1);  // groups after the oldest (the last one is empty)
+        if (ahead >= 2) tc::copies_wait<2>();
+        else if (ahead == 1) tc::copies_wait<1>();
+        else tc::copies_wait<0>();
+        __syncwarp();
+        const uint32_t at = done % C::kSlots;
+        ok = tc::warp_wait(&ctl->empty[at], (done / C::kSlots & 1u) ^ 1u, limit, abort);
+        if (!ok) break;
+        if (quarter == 0 && lane == 0) tc::store_release(&ctl->issued, done + 1);
+        const unsigned char* entry = entries + done % C::kEntries * C::kEntry;
+        uint32_t e[D / 16];
+        {
+            uint32_t s[D / 64];
+            if constexpr (D == 128) {
+                const uint2 w = *reinterpret_cast<const uint2*>(entry + 16 * D + lane * 8);
+                s[0] = w.x, s[D / 64 - 1] = w.y;
+            } else {
+                s[0] = *reinterpret_cast<const uint32_t*>(entry + 16 * D + lane * 4);
+            }
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                uint32_t a, b;
+                asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}" : "=r"(a), "=r"(b) : "r"(s[i]));
+                e[4 * i] = __byte_perm(a, 0, 0x1010), e[4 * i + 1] = __byte_perm(a, 0, 0x3232);
+                e[4 * i + 2] = __byte_perm(b, 0, 0x1010), e[4 * i + 3] = __byte_perm(b, 0, 0x3232);
+            }
+        }
+        const int row = quarter * 32 + lane;
+        const uint32_t to = tc::smem_addr(smem + 2 * C::kTileBytes + at * C::kTileBytes) + row * 128;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            const uint4 w = *reinterpret_cast<const uint4*>(entry + place(lane, i));
+            const uint32_t codes[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int ch = i * 4 + k;
+                uint32_t h[4];
+                widen_codes(codes[k], h);
+                tc::store16(to + (ch >> 3) * (kKTile * 128) + (((ch & 7) ^ (row & 7)) << 4),
+                            make_uint4(mul2(h[0], e[ch / 2]), mul2(h[1], e[ch / 2]), mul2(h[2], e[ch / 2]), mul2(h[3], e[ch / 2])));
+            }
+        }
+        tc::fence_async_shared();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&ctl->full[at]);
+        ++done;
+    }
+    tc::copies_done();  // no copy outlives the block, whatever its readers did
+}
+
+// kFour: the caches are in 4 bits, and the products F16 whatever the plan's type.
+template <bool kBf16, int D, bool kFour>
+__device__ __forceinline__ void attend(const AttendParams& p, const CUtensorMap* k_map, const CUtensorMap* v_map) {
+    using T = typename Half<kBf16>::T;
+    using C = Cfg<D, kFour>;
+    using B = Block<kFour>;
+    constexpr bool kWide = kBf16 && !kFour;  // type of the products
     extern __shared__ __align__(1024) unsigned char smem[];
-    Ctl* ctl = reinterpret_cast<Ctl*>(smem + C::kCtl);
+    Ctl<kFour>* ctl = reinterpret_cast<Ctl<kFour>*>(smem + C::kCtl);
     unsigned char* ring = smem + 2 * C::kTileBytes;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(kFull, tid >> 5, 0);  // the same for the warp, as the compiler sees
     const unsigned long long limit = p.timeout_ns;
     // the barriers, while the kernel ahead still runs
-    if (warp == kWarps - 1) {
-        if (lane < C::kSlots) tc::mbar_init(&ctl->full[lane], 1), tc::mbar_init(&ctl->empty[lane], 2);
-        if (lane < kPieces) tc::mbar_init(&ctl->piece_full[lane], 1), tc::mbar_init(&ctl->piece_empty[lane], kPieceReaders);
+    if (warp == B::kWarps - 1) {
+        if (lane < C::kSlots) tc::mbar_init(&ctl->full[lane], kFour ? 4 : 1), tc::mbar_init(&ctl->empty[lane], 2);
+        if (lane < kPieces) tc::mbar_init(&ctl->piece_full[lane], 1), tc::mbar_init(&ctl->piece_empty[lane], B::kPieceReaders);
         if (lane < 2) {
             tc::mbar_init(&ctl->q_full[lane], 4);
             tc::mbar_init(&ctl->q_free[lane], 2);
@@ -300,13 +483,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc::fence_async_shared();
     }
-    if (tid == 0) tc::prefetch_map(&k_map), tc::prefetch_map(&v_map);
+    if (!kFour && tid == 0) tc::prefetch_map(k_map), tc::prefetch_map(v_map);
     // so far nothing of what earlier kernels write; the join may start once that is there, and waits for this grid's end by itself
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     if (warp == 2) tc::tmem_alloc(&ctl->tmem, kTmemCols);  // not held while waiting: the kernel ahead may need it to end
     Runs runs[2];  // of prefixes, of groups
-    const bool any = plan_run<Pairs>(p, ctl, runs);
+    const bool any = plan_run<RuleOf<kFour>>(p, ctl, runs);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -338,13 +521,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0;  // ring position: a tile's K, then its V
 
     // Each role sets its registers inside its own branch: code that both counts reach is held to the smaller.
-    if (warp >= 4) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    if (warp >= 4 && warp < 12) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(B::kRegsSoftmax));
         // ---- softmax
         const int wg = (warp - 4) >> 2, quarter = warp & 3;  // tensor tile; lanes 32 * quarter of tensor memory
         const uint32_t lanes = (uint32_t)quarter << 21;
         const uint32_t s_col = tmem + lanes + kColS + wg * kColStep, o_col = tmem + lanes + kColO + wg * kColStep;
-        const float c = p.scale * kLog2e;
+        float c = p.scale * kLog2e * (kFour ? p.k_factor : 1.0f);
         uint32_t s_phase = 0, pv_phase = 0, q_pos = 0, grant = 0, tile = 0;  // tile: tiles of the run before the piece
         int turn = 0;
         while (ok && next_piece()) {
@@ -360,7 +543,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 grant ^= 1u;
                 const uint32_t b = (q_pos + wg) & 1u;
-                load_queries<T, D>(p, x.row + wg * rt, wg == 0 ? rt : x.rows - rt, x.kvh, tc::smem_addr(smem + b * C::kTileBytes), 0, tid & 127, 128);
+                const int first_row = x.row + wg * rt, rows = wg == 0 ? rt : x.rows - rt;
+                const uint32_t to = tc::smem_addr(smem + b * C::kTileBytes);
+                if constexpr (kFour && kBf16)
+                    lift_queries<D>(p, first_row, rows, x.kvh, to, 0, ctl->unit[(n_piece - 1) & 3u][wg], tid & 127, 128);
+                else
+                    load_queries<T, D>(p, first_row, rows, x.kvh, to, 0, tid & 127, 128);
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&ctl->q_full[b], 1);
             }
@@ -376,7 +564,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (live) {
                     tc::fence_after();
-                    softmax_tile<kBf16, D>(s_col, o_col, x.left - i * kKTile, i == first, used, c, st, &ctl->p_early[wg]);
+                    if constexpr (kFour && kBf16) {
+                        // finite and above 0, so that a masked score stays -infinity and one of 0 stays 0
+                        if (i == first && used)
+                            c = fminf(fmaxf(p.scale * kLog2e * p.k_factor * ctl->unit[(n_piece - 1) & 3u][two ? wg : 0][row], 0x1p-126f), 0x1p127f);
+                    }
+                    softmax_tile<kWide, D>(s_col, o_col, x.left - i * kKTile, i == first, used, c, st, &ctl->p_early[wg]);
                     tc::fence_before();
                     __syncwarp();
                 } else if (lane == 0) {
@@ -418,14 +611,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (lane == 0) tc::mbar_arrive(&ctl->o_free[wg]);
         }
+    } else if (kFour && warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(B::kRegsOther));
+        if constexpr (kFour) expand<D>(p, smem, ctl, warp - 12, ok, limit);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(B::kRegsOther));
         if (warp == 0) {
             // ---- pages into the ring
             constexpr int kHalves = D / 64;
             const int step = p.page_shift < 7 ? 1 << p.page_shift : kKTile;  // tokens per box
             const int tok = lane / kHalves * step, half = lane % kHalves;
-            Walk<Pairs> walk;
+            Walk<RuleOf<kFour>> walk;
             walk.cta = blockIdx.x;
             walk.deal = ctl->deal_first;
             walk.deal_end = ctl->deal_last + 1;
@@ -463,10 +659,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 if (lane == 0) {
                     ctl->piece[pi] = x;
+                    if constexpr (kFour) ctl->pages[pi] = Pages{walk.table, walk.token};
                     tc::mbar_arrive(&ctl->piece_full[pi]);
                 }
                 ++n_piece;
                 if (!more) break;
+                if (kFour) continue;  // the expanding warps fetch
                 // the pages of the next tile are read before this tile's waits
                 int next_page = page_of(0);
                 for (int i = 0; ok && i < x.tiles; ++i) {
@@ -479,18 +677,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         page = (int)p.num_pages;  // outside the map: zeros
                         atomicOr(p.status, kStatusBadPage);
                     }
-                    ok = fetch(&k_map, boxes, y, kvh, page) && fetch(&v_map, boxes, y, kvh, page);
+                    ok = fetch(k_map, boxes, y, kvh, page) && fetch(v_map, boxes, y, kvh, page);
                 }
             }
             // no copy outlives the block, whatever its readers did
             int none = 0;
-            for (uint32_t i = it > C::kSlots ? it - C::kSlots : 0; i < it; ++i)
+            for (uint32_t i = it > C::kSlots ? it - C::kSlots : 0; !kFour && i < it; ++i)
                 tc::mbar_wait(&ctl->full[i % C::kSlots], i / C::kSlots & 1u, limit, &none);
         } else if (warp <= 2) {
             // ---- the products of tensor tile s; the other tile's run while this warp waits and commits.  The whole warp
             // walks through, and one lane is elected for each instruction: descriptors stay in uniform registers, and 16
             // products are issued in 650 cycles (in a branch of one lane: 1,240 beside two busy softmax warps).
-            constexpr uint32_t kIdescS = tc::make_idesc(kBf16, false, kQTile, kKTile), kIdescO = tc::make_idesc(kBf16, true, kQTile, D);
+            constexpr uint32_t kIdescS = tc::make_idesc(kWide, false, kQTile, kKTile), kIdescO = tc::make_idesc(kWide, true, kQTile, D);
             constexpr uint32_t kTileStep = C::kTileBytes >> 4;
             const uint32_t one = tc::elect_one();
             const int s = warp - 1;
@@ -539,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // has to stay 0), and before a piece's first product the accumulator read
             auto ready = [&](uint32_t v_pos, uint32_t v_slot, uint32_t v_phase, int have, bool first, bool two) {
                 if (!wait_fill(v_pos, v_slot, v_phase, two)) return false;
-                if ((have & 15) != 0 && have < kKTile) {  // the rows that the last 16 of V take in
+                if (!kFour && (have & 15) != 0 && have < kKTile) {  // the rows that the last 16 of V take in
                     if (!two || s == 0) {
                         unsigned char* v = ring + v_slot * C::kTileBytes;
                         for (int r = have + (lane >> 3); r < ((have + 15) & ~15); r += 4)
@@ -675,7 +873,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     continue;
                 }
                 const uint32_t b = q_pos & 1u;
-                load_queries<T, D>(p, x.row, x.rows, x.kvh, tc::smem_addr(smem + b * C::kTileBytes), second_at(x.rows * p.share), lane, 32);
+                if constexpr (kFour && kBf16)
+                    lift_queries<D>(p, x.row, x.rows, x.kvh, tc::smem_addr(smem + b * C::kTileBytes), second_at(x.rows * p.share),
+                                    ctl->unit[(n_piece - 1) & 3u][0], lane, 32);
+                else
+                    load_queries<T, D>(p, x.row, x.rows, x.kvh, tc::smem_addr(smem + b * C::kTileBytes), second_at(x.rows * p.share), lane, 32);
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&ctl->q_full[b], 4);
                 ++q_pos;
@@ -693,15 +895,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D>
-constexpr int smem_bytes() { return Cfg<D>::kCtl + (int)sizeof(Ctl); }
+template <bool kBf16, int D>
+__global__ void __launch_bounds__(Block<false>::kThreads, 1)
+    lp_attend_kernel(const AttendParams p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+    attend<kBf16, D, false>(p, &k_map, &v_map);
+}
+
+template <bool kBf16, int D>
+__global__ void __launch_bounds__(Block<true>::kThreads, 1) lp_attend4_pairs_kernel(const AttendParams p) {
+    attend<kBf16, D, true>(p, nullptr, nullptr);
+}
+
+template <int D, bool kFour>
+constexpr int smem_bytes() { return Cfg<D, kFour>::kCtl + (int)sizeof(Ctl<kFour>); }
 
 template <bool kBf16, int D>
 cudaError_t prepare() {
-    static_assert(smem_bytes<D>() <= 232448, "shared memory");
+    static_assert(smem_bytes<D, false>() <= 232448, "shared memory");
     const cudaFuncAttribute most = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    cudaError_t e = cudaFuncSetAttribute(lp_attend_kernel<kBf16, D>, most, smem_bytes<D>());
-    return e == cudaSuccess ? prepare_join<kBf16, D, Pairs, false>() : e;
+    cudaError_t e = cudaFuncSetAttribute(lp_attend_kernel<kBf16, D>, most, smem_bytes<D, false>());
+    return e == cudaSuccess ? prepare_join<kBf16, D, false>() : e;
 }
 
 template <bool kBf16, int D>
@@ -712,17 +925,40 @@ cudaError_t launch(const AttendParams& p, const CUtensorMap& k_map, const CUtens
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3((unsigned)p.grid);
-    lc.blockDim = dim3(kThreads);
-    lc.dynamicSmemBytes = smem_bytes<D>();
+    lc.blockDim = dim3(Block<false>::kThreads);
+    lc.dynamicSmemBytes = smem_bytes<D, false>();
     lc.stream = stream;
     lc.attrs = attr;
     lc.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&lc, lp_attend_kernel<kBf16, D>, p, k_map, v_map);
     if (e != cudaSuccess) return e;
-    return launch_join<kBf16, D, Pairs, false>(p, lc);
+    return launch_join<kBf16, D, false>(p, lc);
+}
+
+template <bool kBf16, int D>
+cudaError_t prepare_pairs4() {
+    static_assert(smem_bytes<D, true>() <= 232448, "shared memory");
+    return cudaFuncSetAttribute(lp_attend4_pairs_kernel<kBf16, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D, true>());
+}
+
+template <bool kBf16, int D>
+cudaError_t launch_pairs4(const AttendParams& p, cudaLaunchConfig_t lc) {
+    lc.blockDim = dim3(Block<true>::kThreads);
+    lc.dynamicSmemBytes = smem_bytes<D, true>();
+    return cudaLaunchKernelEx(&lc, lp_attend4_pairs_kernel<kBf16, D>, p);
 }
 
 }  // namespace
+
+cudaError_t prepare_attend4_pairs(int dtype, int head_dim) {
+    if (dtype == 1) return head_dim == 128 ? prepare_pairs4<true, 128>() : prepare_pairs4<true, 64>();
+    return head_dim == 128 ? prepare_pairs4<false, 128>() : prepare_pairs4<false, 64>();
+}
+
+cudaError_t launch_attend4_pairs(const AttendParams& p, int dtype, int head_dim, const cudaLaunchConfig_t& lc) {
+    if (dtype == 1) return head_dim == 128 ? launch_pairs4<true, 128>(p, lc) : launch_pairs4<true, 64>(p, lc);
+    return head_dim == 128 ? launch_pairs4<false, 128>(p, lc) : launch_pairs4<false, 64>(p, lc);
+}
 
 cudaError_t prepare_attend(int dtype, int head_dim) {
     if (dtype == 1) return head_dim == 128 ? prepare<true, 128>() : prepare<true, 64>();

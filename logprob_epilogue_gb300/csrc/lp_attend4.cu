@@ -60,27 +60,6 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The four bytes of a word, two codes each, to pairs of F16.
-__device__ __forceinline__ void widen_codes(uint32_t w, uint32_t (&h)[4]) {
-    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\tcvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-        : "r"(w));
-}
-
-// Two scale bytes to a pair of F16.
-__device__ __forceinline__ uint32_t widen_scales(uint32_t two) {
-    uint32_t h;
-    asm("{\n\t.reg .b16 s, t;\n\tmov.b32 {s, t}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, s;\n\t}" : "=r"(h) : "r"(two));
-    return h;
-}
-
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
 __device__ __forceinline__ uint32_t lop_select(uint32_t a, uint32_t b, uint32_t mask) { return (a & mask) | (b & ~mask); }
 
 // A worker's rows: two per thread, lane / 4 and eight further.
@@ -317,8 +296,8 @@ __device__ __forceinline__ void merge_piece(const AttendParams& p, const Piece& 
             l = fmaf(ml.y, f, l);
             o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
         }
-        if (chunk % (D / 16) == 0 && (lane & 3) == 0) p.sc.part_ml[x.part + row] = make_float2(top, l);
-        reinterpret_cast<float4*>(p.sc.part_o)[part_chunk<D>(x.part, x.part_stride, row, (D / 32) * (2 * (lane & 3) + e) + j)] = o;
+        if (chunk % (D / 16) == 0 && (lane & 3) == 0) p.fragments.part_ml[x.part + row] = make_float2(top, l);
+        reinterpret_cast<float4*>(p.fragments.part_o)[part_chunk<D>(x.part, x.part_stride, row, (D / 32) * (2 * (lane & 3) + e) + j)] = o;
     }
 }
 
@@ -349,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) lp_attend4_kernel(const AttendPar
     const bool any = plan_run<Fragments>(p, ctl, runs);
     __syncthreads();
     if (!any) {
-        if (tid == 0) p.sc.gave_up[blockIdx.x] = 0;
+        if (tid == 0) p.fragments.gave_up[blockIdx.x] = 0;
         return;
     }
     volatile int* abort = &ctl->abort;
@@ -506,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) lp_attend4_kernel(const AttendPar
     }
     __syncthreads();
     if (tid == 0) {
-        p.sc.gave_up[blockIdx.x] = *abort;
+        p.fragments.gave_up[blockIdx.x] = *abort;
         if (*abort != 0) atomicOr(p.status, kStatusAttnTimeout);
     }
 }
@@ -518,12 +497,12 @@ template <bool kBf16, int D>
 cudaError_t prepare4() {
     static_assert(smem_bytes4<D>() <= 232448, "shared memory");
     const cudaError_t e = cudaFuncSetAttribute(lp_attend4_kernel<kBf16, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes4<D>());
-    return e == cudaSuccess ? prepare_join<kBf16, D, Fragments, true>() : e;
+    return e == cudaSuccess ? prepare_join<kBf16, D, true>() : e;
 }
 
 template <bool kBf16, int D>
 cudaError_t launch4(const AttendParams& p, cudaStream_t stream) {
-    // Both kernels are launched while the one before still runs, and wait for its end before they read what it writes.
+    // Each kernel is launched while the one before still runs, and waits for its end before it reads what that writes.
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -534,13 +513,22 @@ cudaError_t launch4(const AttendParams& p, cudaStream_t stream) {
     lc.stream = stream;
     lc.attrs = attr;
     lc.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&lc, lp_attend4_kernel<kBf16, D>, p);
-    return e == cudaSuccess ? launch_join<kBf16, D, Fragments, true>(p, lc) : e;
+    cudaError_t e = cudaSuccess;
+    if (runs_fragments(p)) e = cudaLaunchKernelEx(&lc, lp_attend4_kernel<kBf16, D>, p);
+    if (e == cudaSuccess && runs_pairs(p)) e = launch_attend4_pairs(p, kBf16 ? 1 : 2, D, lc);
+    return e == cudaSuccess ? launch_join<kBf16, D, true>(p, lc) : e;
 }
 
 }  // namespace
 
+int pick_wide(const AttendParams& p) {
+    const bool groups = (long long)p.rows * p.share > 32LL * p.G;
+    return (p.P > 0 ? kWidePrefixes : 0) | (groups ? kWideGroups : 0);
+}
+
 cudaError_t prepare_attend4(int dtype, int head_dim) {
+    const cudaError_t e = prepare_attend4_pairs(dtype, head_dim);
+    if (e != cudaSuccess) return e;
     if (dtype == 1) return head_dim == 128 ? prepare4<true, 128>() : prepare4<true, 64>();
     return head_dim == 128 ? prepare4<false, 128>() : prepare4<false, 64>();
 }

@@ -22,7 +22,7 @@ struct lp_attn_s {
     int page_shift;
     int grid;
     unsigned char* scratch;
-    lp::AttendScratch sc;
+    lp::AttendScratch sc, fragments;
     lp::Reserved* reserved;  // scratch of lp_kv_reserve
     long long* ends;
     EncodeTiled encode;
@@ -66,41 +66,70 @@ int check_desc(const lp_attn_desc* d) {
 }
 
 struct Layout {
-    size_t seg_units, units, gave_up, part_o, part_ml, reserved, ends, total;  // the tables come first
+    size_t seg_units, units, gave_up, part_ml, part_o;  // the tables come first
     long long prefix_slots, group_slots;
     int group_rows;
 };
 
+struct Scratch {
+    Layout pairs, fragments;      // fragments: of a plan over 4 bits
+    size_t tables, reserved, ends, total;  // tables: bytes of all the tables, which come first
+};
+
 // Pieces of a kind: every unit starts one and every block boundary one more.
-Layout layout_of(const lp_attn_desc* d, int grid) {
-    Layout L{};
+// sets: tiles of a unit, and parts of a piece.
+void lay_tables(Layout& L, const lp_attn_desc* d, int grid, int sets, size_t& off) {
     const int share = d->q_heads / d->kv_heads, per_tile = lp::kQTile / share;
-    // tiles of a unit, parts of a piece: two; of the kernel over 4 bits, one
-    const int sets = (d->flags & LP_ATTN_KV4) != 0 ? 1 : 2;
     const long long group_units = (long long)d->max_groups * ((d->max_group_rows + sets * per_tile - 1) / (sets * per_tile));
     const long long prefix_units = d->max_prefixes == 0 ? 0 : d->max_rows / (sets * per_tile) + d->max_prefixes;
     L.group_rows = (d->max_group_rows < per_tile ? d->max_group_rows : per_tile) * share;
     L.group_slots = group_units * d->kv_heads + grid;
     L.prefix_slots = d->max_prefixes == 0 ? 0 : prefix_units * d->kv_heads + grid;
     const size_t segs = (size_t)d->max_prefixes + (size_t)d->max_groups;
-    const size_t part_rows = sets * ((size_t)L.prefix_slots * lp::kQTile + (size_t)L.group_slots * (size_t)L.group_rows);
-    size_t off = 0;
     L.seg_units = off;
     off = lp::align_up(off + segs * 8);
     L.units = off;
     off = lp::align_up(off + (size_t)(L.prefix_slots + L.group_slots) * 8);
     L.gave_up = off;
     off = lp::align_up(off + (size_t)grid * 4);
+}
+
+void lay_parts(Layout& L, const lp_attn_desc* d, int sets, size_t& off) {
+    const size_t part_rows = sets * ((size_t)L.prefix_slots * lp::kQTile + (size_t)L.group_slots * (size_t)L.group_rows);
     L.part_ml = off;
     off = lp::align_up(off + part_rows * 8);
     L.part_o = off;
     off = lp::align_up(off + part_rows * (size_t)d->head_dim * 4);
-    L.reserved = off;
+}
+
+Scratch scratch_of(const lp_attn_desc* d, int grid) {
+    Scratch s{};
+    const bool four = (d->flags & LP_ATTN_KV4) != 0;
+    size_t off = 0;
+    lay_tables(s.pairs, d, grid, 2, off);
+    if (four) lay_tables(s.fragments, d, grid, 1, off);
+    s.tables = off;
+    lay_parts(s.pairs, d, 2, off);
+    if (four) lay_parts(s.fragments, d, 1, off);
+    s.reserved = off;
     off = lp::align_up(off + (size_t)d->max_groups * sizeof(lp::Reserved));
-    L.ends = off;
+    s.ends = off;
     off = lp::align_up(off + 16);
-    L.total = off;
-    return L;
+    s.total = off;
+    return s;
+}
+
+lp::AttendScratch place(const Layout& L, unsigned char* base) {
+    lp::AttendScratch sc;
+    sc.seg_units = reinterpret_cast<int2*>(base + L.seg_units);
+    sc.units = reinterpret_cast<int2*>(base + L.units);
+    sc.gave_up = reinterpret_cast<int*>(base + L.gave_up);
+    sc.part_ml = reinterpret_cast<float2*>(base + L.part_ml);
+    sc.part_o = reinterpret_cast<float*>(base + L.part_o);
+    sc.prefix_slots = L.prefix_slots;
+    sc.group_slots = L.group_slots;
+    sc.group_rows = L.group_rows;
+    return sc;
 }
 
 // The 4-D map of a cache: lanes, slots of a page, heads, pages; boxes of 64
@@ -296,7 +325,7 @@ size_t lp_attn_scratch_bytes(const lp_attn_desc* desc) {
         (void)cudaGetLastError();
         sms = 152;  // no such device here: a GB300's
     }
-    return layout_of(desc, sms).total;
+    return scratch_of(desc, sms).total;
 }
 
 int lp_attn_create(lp_attn_t* out, const lp_attn_desc* desc) {
@@ -316,13 +345,13 @@ int lp_attn_create(lp_attn_t* out, const lp_attn_desc* desc) {
     if (e == cudaSuccess) e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
     if (e == cudaSuccess && (found != cudaDriverEntryPointSuccess || !fn)) e = cudaErrorNotSupported;
     if (e == cudaSuccess) e = four_bits(plan) ? lp::prepare_attend4(desc->dtype, desc->head_dim) : lp::prepare_attend(desc->dtype, desc->head_dim);
-    Layout L{};
+    Scratch s{};
     if (e == cudaSuccess) {
         plan->encode = reinterpret_cast<EncodeTiled>(fn);
-        L = layout_of(desc, plan->grid);
-        e = cudaMalloc(&plan->scratch, L.total);
+        s = scratch_of(desc, plan->grid);
+        e = cudaMalloc(&plan->scratch, s.total);
         // a table entry that no call has written names no part
-        if (e == cudaSuccess) e = cudaMemset(plan->scratch, 0, L.part_ml);
+        if (e == cudaSuccess) e = cudaMemset(plan->scratch, 0, s.tables);
         if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);
     }
     if (e != cudaSuccess) {
@@ -331,16 +360,10 @@ int lp_attn_create(lp_attn_t* out, const lp_attn_desc* desc) {
         delete plan;
         return cuda_fail(e);
     }
-    plan->sc.seg_units = reinterpret_cast<int2*>(plan->scratch + L.seg_units);
-    plan->sc.units = reinterpret_cast<int2*>(plan->scratch + L.units);
-    plan->sc.gave_up = reinterpret_cast<int*>(plan->scratch + L.gave_up);
-    plan->sc.part_ml = reinterpret_cast<float2*>(plan->scratch + L.part_ml);
-    plan->sc.part_o = reinterpret_cast<float*>(plan->scratch + L.part_o);
-    plan->reserved = reinterpret_cast<lp::Reserved*>(plan->scratch + L.reserved);
-    plan->ends = reinterpret_cast<long long*>(plan->scratch + L.ends);
-    plan->sc.prefix_slots = L.prefix_slots;
-    plan->sc.group_slots = L.group_slots;
-    plan->sc.group_rows = L.group_rows;
+    plan->sc = place(s.pairs, plan->scratch);
+    if (four_bits(plan)) plan->fragments = place(s.fragments, plan->scratch);
+    plan->reserved = reinterpret_cast<lp::Reserved*>(plan->scratch + s.reserved);
+    plan->ends = reinterpret_cast<long long*>(plan->scratch + s.ends);
     *out = plan;
     return LP_OK;
 }
@@ -472,6 +495,8 @@ int lp_attend4(lp_attn_t plan, const lp_attend4_io* io, void* stream) {
     p.v_scales = static_cast<const unsigned char*>(io->v_scales);
     p.k_factor = io->k_factor;
     p.v_factor = io->v_factor;
+    p.fragments = plan->fragments;
+    p.wide = lp::pick_wide(p);
     const cudaError_t e = lp::launch_attend4(p, plan->d.dtype, plan->d.head_dim, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? LP_OK : cuda_fail(e);
 }

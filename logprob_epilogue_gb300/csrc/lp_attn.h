@@ -101,7 +101,21 @@ struct AttendParams {
     // a cache of 4 bits; k_cache, v_cache: the codes
     const unsigned char *k_scales, *v_scales;
     float k_factor, v_factor;
+    int wide;              // segments whose units are pairs of tiles: kWidePrefixes, kWideGroups; the others' are fragments
+    AttendScratch fragments;  // of those
 };
+
+constexpr int kWidePrefixes = 1, kWideGroups = 2;
+
+// Whether a call over 4 bits has segments of either kind.
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline bool runs_pairs(const AttendParams& p) { return (p.wide & kWideGroups) != 0 || (p.P > 0 && (p.wide & kWidePrefixes) != 0); }
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline bool runs_fragments(const AttendParams& p) { return (p.wide & kWideGroups) == 0 || (p.P > 0 && (p.wide & kWidePrefixes) == 0); }
 
 // The pieces of a cut unit as the join may take them from its entry (first
 // slot, pieces): as many as there can be, in slots that exist.  Whatever an
@@ -120,6 +134,9 @@ inline int cache_box_rows(int page_size) { return page_size < kKTile ? page_size
 cudaError_t launch_reserve(const ReserveParams& p, int grid, cudaStream_t stream);
 cudaError_t launch_rope(const RopeParams& p, int dtype, int head_dim, cudaStream_t stream);
 cudaError_t prepare_attend(int dtype, int head_dim);  // once per plan: kernel attributes
+int pick_wide(const AttendParams& p);  // AttendParams::wide
+cudaError_t prepare_attend4_pairs(int dtype, int head_dim);
+cudaError_t launch_attend4_pairs(const AttendParams& p, int dtype, int head_dim, const cudaLaunchConfig_t& lc);
 cudaError_t prepare_attend4(int dtype, int head_dim);
 cudaError_t launch_attend4(const AttendParams& p, int dtype, int head_dim, cudaStream_t stream);
 cudaError_t launch_attend(const AttendParams& p, const CUtensorMap& k_map, const CUtensorMap& v_map, int dtype,
@@ -153,6 +170,27 @@ struct Half<false> {
         return *reinterpret_cast<const uint32_t*>(&h);
     }
 };
+
+// Caches in 4 bits: the four bytes of a word, two codes each, to pairs of F16.
+__device__ __forceinline__ void widen_codes(uint32_t w, uint32_t (&h)[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\tcvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+
+// Two scale bytes to a pair of F16.
+__device__ __forceinline__ uint32_t widen_scales(uint32_t two) {
+    uint32_t h;
+    asm("{\n\t.reg .b16 s, t;\n\tmov.b32 {s, t}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, s;\n\t}" : "=r"(h) : "r"(two));
+    return h;
+}
+
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 
 // The group that `row` belongs to; -1 where no group claims it, or several do
 // (indptr then does not ascend).  All threads of the block take part and get

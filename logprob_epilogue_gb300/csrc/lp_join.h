@@ -62,15 +62,15 @@ __device__ __forceinline__ void widen_four(uint32_t codes, uint32_t scale, float
 
 // The parts of a row's head from one segment: what the call's arguments say,
 // and after the main kernel what its tables say.
-template <class Rule>
+template <bool kFour>
 struct Parts {
     int seg, unit, dealt;     // seg: -1 for none; of all heads' units
     int row, cap, set, sets;  // row of the unit; the parts of a piece that are its: sets of them from `set` on
     int count;
     long long slot;
-    __device__ __forceinline__ void find(const AttendParams& p, int segment, int of, int head) {  // of: the row
-        seg = -1;
-        if (segment < 0) return;
+    bool pairs;               // units of pairs of tiles
+    template <class Rule>
+    __device__ __forceinline__ void find_by(const AttendParams& p, int segment, int of, int head) {
         const Seg<Rule> s = load_seg<Rule>(p, segment);
         if (s.tiles == 0) return;
         seg = segment;
@@ -81,22 +81,39 @@ struct Parts {
         set = two && in >= rt ? 1 : 0;
         sets = two ? 1 : Rule::kSets;  // a unit of one tile: a part of each warpgroup
         row = (in - set * rt) * p.share + head - kvh * p.share;
-        cap = segment < p.P ? kQTile : p.sc.group_rows;
+        cap = segment < p.P ? kQTile : Rule::scratch(p).group_rows;
     }
-    __device__ __forceinline__ int2 first_slots(const AttendParams& p) const { return seg >= 0 ? p.sc.seg_units[seg] : make_int2(0, 0); }
+    __device__ __forceinline__ void find(const AttendParams& p, int segment, int of, int head) {  // of: the row
+        seg = -1;
+        pairs = true;
+        if (segment < 0) return;
+        if constexpr (kFour) {
+            pairs = Pairs4::takes(p, segment < p.P);
+            if (pairs) find_by<Pairs4>(p, segment, of, head);
+            else find_by<Fragments>(p, segment, of, head);
+        } else {
+            find_by<Pairs>(p, segment, of, head);
+        }
+    }
+    __device__ __forceinline__ const AttendScratch& scratch(const AttendParams& p) const { return kFour && !pairs ? p.fragments : p.sc; }
+    __device__ __forceinline__ int2 first_slots(const AttendParams& p) const { return seg >= 0 ? scratch(p).seg_units[seg] : make_int2(0, 0); }
     __device__ __forceinline__ void locate(const AttendParams& p, int2 base) {
+        const AttendScratch& sc = scratch(p);
         slot = (long long)base.y + unit;
         int pieces = seg >= 0 ? 1 : 0;
         if (pieces != 0 && unit >= dealt) {
-            const long long at = unit_index(p, seg < p.P, base.x + unit - dealt);
-            const int2 e = at >= 0 ? p.sc.units[at] : make_int2(0, 0);
+            const long long at = unit_index(sc, seg < p.P, base.x + unit - dealt);
+            const int2 e = at >= 0 ? sc.units[at] : make_int2(0, 0);
             slot = e.x;
-            pieces = entry_pieces(e.x, e.y, seg < p.P ? p.sc.prefix_slots : p.sc.group_slots, p.grid);
+            pieces = entry_pieces(e.x, e.y, seg < p.P ? sc.prefix_slots : sc.group_slots, p.grid);
         }
         count = pieces * sets;
     }
     __device__ __forceinline__ long long part(const AttendParams& p, int k) const {
-        return part_row<Rule>(p, seg < p.P, slot + (sets == 1 ? k : k >> 1), sets == 1 ? set : k & 1);
+        const long long at = slot + (sets == 1 ? k : k >> 1);
+        const int s = sets == 1 ? set : k & 1;
+        if (kFour && !pairs) return part_row<Fragments>(p, seg < p.P, at, s);
+        return part_row<Pairs>(p, seg < p.P, at, s);
     }
 };
 
@@ -117,7 +134,7 @@ constexpr int join_bytes(int sub) { return join_round(sub) * kJoinThreads * (D /
 //
 // With heads of 128 the forms of one and two warps per row spill 28 bytes a
 // thread (F16: 36) at the 64 registers that four blocks per SM leave.
-template <bool kBf16, int D, int kSub, class Rule, bool kFour>
+template <bool kBf16, int D, int kSub, bool kFour>
 __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_join_kernel(const AttendParams p) {
     using H = Half<kBf16>;
     using T = typename H::T;
@@ -238,7 +255,7 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
     }
     // Of the first prefix that serves the row, of its group's committed tokens.  A prefix has parts for the rows from its first
     // group's to its last's: a group whose rows lie elsewhere (group_indptr then does not ascend) is not served.
-    Parts<Rule> shared, own;
+    Parts<kFour> shared, own;
     if (p.P > 0 && grp.n > 0) {  // the same for the block, whose threads look through the prefixes side by side
         for (int i = threadIdx.x; i < p.P; i += kJoinThreads) {
             if (p.prefix_indptr[i] > g || p.prefix_indptr[i + 1] <= g) continue;
@@ -258,7 +275,14 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
     // answer is put together at the end, when the loads have long come in (one row: 15.3 us; here: 15.6); with many it costs
     // nothing here.
     int gave_up = 0;
-    for (int b = threadIdx.x; b < p.grid; b += kJoinThreads) gave_up |= p.sc.gave_up[b];
+    for (int b = threadIdx.x; b < p.grid; b += kJoinThreads) {
+        if constexpr (kFour) {
+            if (runs_pairs(p)) gave_up |= p.sc.gave_up[b];
+            if (runs_fragments(p)) gave_up |= p.fragments.gave_up[b];
+        } else {
+            gave_up |= p.sc.gave_up[b];
+        }
+    }
     const int2 shared_at = shared.first_slots(p), own_at = own.first_slots(p);
     if constexpr (kSub == 1) gave_up = __syncthreads_or(gave_up);
     shared.locate(p, shared_at);
@@ -271,11 +295,12 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
             const bool is_own = k >= shared.count;
             const int row_at = is_own ? own.row : shared.row, cap = is_own ? own.cap : shared.cap;
             const long long base = is_own ? own.part(p, k - shared.count) : shared.part(p, k);
+            const AttendScratch& sc = is_own ? own.scratch(p) : shared.scratch(p);
             if (base < 0) {
                 stage_ml[slot * kJoinThreads] = make_float2(kNegInf, 0.0f);
             } else {
-                tc::copy8(tc::smem_addr(&stage_ml[slot * kJoinThreads]), p.sc.part_ml + base + row_at);
-                const float4* src = reinterpret_cast<const float4*>(p.sc.part_o) + part_chunk<D>(base, cap, row_at, 2 * l);
+                tc::copy8(tc::smem_addr(&stage_ml[slot * kJoinThreads]), sc.part_ml + base + row_at);
+                const float4* src = reinterpret_cast<const float4*>(sc.part_o) + part_chunk<D>(base, cap, row_at, 2 * l);
 #pragma unroll
                 for (int r = 0; r < kRuns * 2; ++r) tc::copy16(tc::smem_addr(&staged(slot, r)), src + (r / 2 * 16 + (r & 1)) * cap);
             }
@@ -333,18 +358,18 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
     if (p.lse_out != nullptr && l == 0) p.lse_out[(long long)row * p.q_heads + head] = a.l == 0.0f ? kNegInf : a.m * kLn2 + logf(a.l);
 }
 
-template <bool kBf16, int D, class Rule, bool kFour>
+template <bool kBf16, int D, bool kFour>
 cudaError_t prepare_join() {
     const cudaFuncAttribute most = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    cudaError_t e = cudaFuncSetAttribute(lp_attend_join_kernel<kBf16, D, 8, Rule, kFour>, most, join_bytes<D>(8));
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(lp_attend_join_kernel<kBf16, D, 4, Rule, kFour>, most, join_bytes<D>(4));
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(lp_attend_join_kernel<kBf16, D, 2, Rule, kFour>, most, join_bytes<D>(2));
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(lp_attend_join_kernel<kBf16, D, 1, Rule, kFour>, most, join_bytes<D>(1));
+    cudaError_t e = cudaFuncSetAttribute(lp_attend_join_kernel<kBf16, D, 8, kFour>, most, join_bytes<D>(8));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(lp_attend_join_kernel<kBf16, D, 4, kFour>, most, join_bytes<D>(4));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(lp_attend_join_kernel<kBf16, D, 2, kFour>, most, join_bytes<D>(2));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(lp_attend_join_kernel<kBf16, D, 1, kFour>, most, join_bytes<D>(1));
     return e;
 }
 
 // `lc`: the main kernel's launch, whose stream and attributes the join's has too.
-template <bool kBf16, int D, class Rule, bool kFour>
+template <bool kBf16, int D, bool kFour>
 cudaError_t launch_join(const AttendParams& p, cudaLaunchConfig_t lc) {
     // the most warps per row with which all blocks are resident at once: one row takes 15.5 us (one warp: 24.7), trees of
     // drafts 43.6 (one: 46.3, eight: 60), 2,048 rows behind a prefix 765 (eight: 1,015)
@@ -355,10 +380,10 @@ cudaError_t launch_join(const AttendParams& p, cudaLaunchConfig_t lc) {
     lc.gridDim = dim3((unsigned)p.rows, (unsigned)per_row());
     lc.blockDim = dim3(kJoinThreads);
     lc.dynamicSmemBytes = join_bytes<D>(sub);
-    if (sub == 8) return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 8, Rule, kFour>, p);
-    if (sub == 4) return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 4, Rule, kFour>, p);
-    if (sub == 2) return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 2, Rule, kFour>, p);
-    return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 1, Rule, kFour>, p);
+    if (sub == 8) return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 8, kFour>, p);
+    if (sub == 4) return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 4, kFour>, p);
+    if (sub == 2) return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 2, kFour>, p);
+    return cudaLaunchKernelEx(&lc, lp_attend_join_kernel<kBf16, D, 1, kFour>, p);
 }
 
 }  // namespace lp

@@ -15,7 +15,7 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_huge_valf();
-constexpr int kThreads = 384;  // of a block that plans
+constexpr int kThreads = 384;  // of a block that sum up its plan (it may have more)
 constexpr int kWarps = kThreads / 32;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -33,6 +33,13 @@ struct Pairs {
     static constexpr int kMostCost = kPairCost;  // of a tile
     static __device__ __forceinline__ int unit_rows(const AttendParams& p) { return 2 * p.rows_per_tile; }
     static __device__ __forceinline__ int cost(const AttendParams& p, int n) { return n > p.rows_per_tile ? kPairCost : kTileCost; }
+    static __device__ __forceinline__ const AttendScratch& scratch(const AttendParams& p) { return p.sc; }
+    static __device__ __forceinline__ bool takes(const AttendParams&, bool) { return true; }
+};
+
+// The same for a cache in 4 bits, of the segments that they are chosen for.
+struct Pairs4 : Pairs {
+    static __device__ __forceinline__ bool takes(const AttendParams& p, bool prefix) { return (p.wide & (prefix ? kWidePrefixes : kWideGroups)) != 0; }
 };
 
 // Units of one tile of 128 query rows at most, in fragments of 16 rows: a piece
@@ -47,6 +54,8 @@ struct Fragments {
         const int rows = (n < p.rows_per_tile ? n : p.rows_per_tile) * p.share, products = (rows + 15) / 16 * 2;
         return products > 3 ? products : 3;
     }
+    static __device__ __forceinline__ const AttendScratch& scratch(const AttendParams& p) { return p.fragments; }
+    static __device__ __forceinline__ bool takes(const AttendParams& p, bool prefix) { return !Pairs4::takes(p, prefix); }
 };
 
 // The call's vectors are read with ordinary loads: the kernels are resident
@@ -117,7 +126,7 @@ __device__ __forceinline__ Seg<Rule> load_seg(const AttendParams& p, int s) {
         x.r0 = f.r0, x.n = f.n, x.len = f.len, x.bad = f.bad;
     }
     x.units = (x.n + Rule::unit_rows(p) - 1) / Rule::unit_rows(p);
-    x.tiles = x.n > 0 ? (x.len + kKTile - 1) / kKTile : 0;
+    x.tiles = x.n > 0 && Rule::takes(p, s < p.P) ? (x.len + kKTile - 1) / kKTile : 0;
     x.cost = Rule::cost(p, x.n);
     x.dealt = s < p.P && x.tiles > 0 ? x.units * p.kv_heads / p.grid * p.grid : 0;
     return x;
@@ -156,15 +165,16 @@ __device__ __forceinline__ Runs make_runs(unsigned long long total, int grid, in
 // scratch (only overlapping prefixes can ask for that).
 template <class Rule>
 __device__ __forceinline__ long long part_row(const AttendParams& p, bool prefix, long long slot, int set) {
-    if (prefix) return slot < p.sc.prefix_slots ? (slot * Rule::kSets + set) * kQTile : -1;
-    if (slot >= p.sc.group_slots) return -1;
-    return p.sc.prefix_slots * Rule::kSets * kQTile + (slot * Rule::kSets + set) * p.sc.group_rows;
+    const AttendScratch& sc = Rule::scratch(p);
+    if (prefix) return slot < sc.prefix_slots ? (slot * Rule::kSets + set) * kQTile : -1;
+    if (slot >= sc.group_slots) return -1;
+    return sc.prefix_slots * Rule::kSets * kQTile + (slot * Rule::kSets + set) * sc.group_rows;
 }
 
 // Where a unit that is not dealt out is entered for the join; -1 as above.
-__device__ __forceinline__ long long unit_index(const AttendParams& p, bool prefix, int unit) {
-    if (prefix) return unit < p.sc.prefix_slots ? unit : -1;
-    return unit < p.sc.group_slots ? p.sc.prefix_slots + unit : -1;
+__device__ __forceinline__ long long unit_index(const AttendScratch& sc, bool prefix, int unit) {
+    if (prefix) return unit < sc.prefix_slots ? unit : -1;
+    return unit < sc.group_slots ? sc.prefix_slots + unit : -1;
 }
 
 // A part's results lie chunk by chunk, four lanes of the head of every row
@@ -223,7 +233,7 @@ struct Walk {
         table = prefix ? p.prefix_tables + (long long)sg * p.max_prefix_pages : p.tables + (long long)(sg - p.P) * p.max_pages;
         token = (long long)t0 * kKTile;
         x.part = part_row<Rule>(p, prefix, slot, 0);
-        x.part_stride = prefix ? kQTile : p.sc.group_rows;
+        x.part_stride = prefix ? kQTile : Rule::scratch(p).group_rows;
     }
     __device__ __forceinline__ bool next(const AttendParams& p, Piece& x) {
         while (deal < deal_end) {
@@ -262,8 +272,8 @@ struct Walk {
             if (t0 == 0 && (threadIdx.x & 31) == 0) {
                 // for the join: the unit's first slot and how many blocks have a piece of it
                 const unsigned long long last = off + unit * span + Rule::kUnitCost + (unsigned long long)(s.tiles - 1) * s.cost;
-                const long long at = unit_index(p, kind == 0, units + unit);
-                if (at >= 0) p.sc.units[at] = make_int2(units + unit + cta, t1 == s.tiles ? 1 : run.block_of(last) - cta + 1);
+                const long long at = unit_index(Rule::scratch(p), kind == 0, units + unit);
+                if (at >= 0) Rule::scratch(p).units[at] = make_int2(units + unit + cta, t1 == s.tiles ? 1 : run.block_of(last) - cta + 1);
             }
             return true;
         }
@@ -312,7 +322,7 @@ __device__ __forceinline__ bool plan_run(const AttendParams& p, PlanCtl<Rule>* c
         const int d = __shfl_up_sync(kFull, id, o);
         if (lane >= o) i0 += a, i1 += b, iu += c, id += d;
     }
-    if (lane == 31) ctl->sum[warp][0] = i0, ctl->sum[warp][1] = i1, ctl->sum[warp][2] = iu, ctl->sum_dealt[warp] = id;
+    if (lane == 31 && warp < kWarps) ctl->sum[warp][0] = i0, ctl->sum[warp][1] = i1, ctl->sum[warp][2] = iu, ctl->sum_dealt[warp] = id;
     if (tid == 0) ctl->deal_first = S, ctl->deal_last = -1;
     if (Rule::kMostCost == 0) {
         if (tid == 0) ctl->most_cost[0] = ctl->most_cost[1] = 1;
@@ -347,7 +357,7 @@ __device__ __forceinline__ bool plan_run(const AttendParams& p, PlanCtl<Rule>* c
             const int kind = s < p.P ? 0 : 1;
             const unsigned long long work = x.work(p), off = kind == 0 ? at0 : at1, lo = kind == 0 ? lo0 : lo1;
             const int before = (int)(kind == 0 ? (u >> 32) + all_dealt : u & 0xFFFFFFFFull);  // slots: the dealt units', then the others'
-            if (cta == 0) p.sc.seg_units[s] = make_int2(before, d);
+            if (cta == 0) Rule::scratch(p).seg_units[s] = make_int2(before, d);
             if (lo >= off && lo < off + work) ctl->start[kind].off = off, ctl->start[kind].seg = s, ctl->start[kind].units = before, ctl->start[kind].s = x;
             (kind == 0 ? at0 : at1) += work;
             u += (unsigned long long)x.left(p) << (kind == 0 ? 32 : 0);

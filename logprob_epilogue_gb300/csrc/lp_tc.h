@@ -113,6 +113,16 @@ __device__ __forceinline__ void copy16_or_zeros(uint32_t dst, const void* src, b
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16u : 0u) : "memory");
 }
 
+// The same for 4 or 8 bytes.
+template <int kBytes>
+__device__ __forceinline__ void copy_or_zeros(uint32_t dst, const void* src, bool read) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(read ? (uint32_t)kBytes : 0u) : "memory");
+}
+
+__device__ __forceinline__ void store16(uint32_t dst, const uint4& w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+}
+
 // This thread arrives once its copies so far are in.
 __device__ __forceinline__ void copies_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");

@@ -23,8 +23,7 @@ def L():
 def test_null_arguments_and_descriptors(L):
     for f in (L.lp_kv_reserve, L.lp_kv_append4, L.lp_attend4):
         assert f(None, None, None) == EINVAL
-    four = A.attn_scratch_bytes(**BASE, kv_bits=4)
-    assert 0 < four <= A.attn_scratch_bytes(**BASE)  # one part per piece in place of two
+    assert A.attn_scratch_bytes(**BASE, kv_bits=4) > A.attn_scratch_bytes(**BASE) > 0  # parts of either kernel
     with pytest.raises(ValueError, match="kv_bits"):
         A.make_attn_desc(**BASE, kv_bits=8)
     d = A.make_attn_desc(**BASE)
