@@ -285,17 +285,7 @@ __device__ __forceinline__ void load_queries(const AttendParams& p, int row0, in
     tc::fence_async_shared();
 }
 
-// The power of two that brings a row's largest lane, `top`, to [2^14, 2^15) and
-// what undoes it (1 for rows of zeros, infinities or NaN).
-__device__ __forceinline__ float2 lift_of(float top) {
-    const int field = (int)(__float_as_uint(top) >> 23);
-    int up = 141 - field;
-    up = up > 126 ? 126 : up;
-    if (field == 255 || top == 0.0f) up = 0;
-    return make_float2(__uint_as_float((uint32_t)(up + 127) << 23), __uint_as_float((uint32_t)(127 - up) << 23));
-}
-
-// The same from BF16 to F16, each row by its power of two; D / 8 threads have a
+// The same from BF16 to F16, each row by a power of two of its own; D / 8 threads have a
 // row, `n` a multiple of 32.  unit[row]: what undoes it.
 template <int D>
 __device__ __forceinline__ void lift_queries(const AttendParams& p, int row0, int rows, int kvh, uint32_t dst, int again, float* unit, int t, int n) {

@@ -61,6 +61,7 @@ struct ReserveParams {
 };
 
 constexpr int kQTile = 128;    // query rows (row, head) of one tensor-core tile
+constexpr int kUnitRows = 32;  // of a unit whose rows are the products' columns
 constexpr int kKTile = 128;    // tokens of one tile
 
 // Scratch of lp_attend.  A segment is a prefix or a group's committed tokens;
@@ -74,7 +75,7 @@ struct AttendScratch {
     float* part_o;                  // pieces of prefixes, then of groups: unnormalised results [2][rows][D]
     float2* part_ml;                // (maximum in base 2, sum) [2][rows]
     long long prefix_slots, group_slots;
-    int group_rows;                 // rows per tile in a group slot (prefix slots: kQTile)
+    int prefix_rows, group_rows;    // rows per tile in a prefix slot and in a group slot
 };
 
 struct AttendParams {
@@ -101,8 +102,9 @@ struct AttendParams {
     // a cache of 4 bits; k_cache, v_cache: the codes
     const unsigned char *k_scales, *v_scales;
     float k_factor, v_factor;
-    int wide;              // segments whose units are pairs of tiles: kWidePrefixes, kWideGroups; the others' are fragments
-    AttendScratch fragments;  // of those
+    int wide;              // segments whose units are pairs of tiles: kWidePrefixes, kWideGroups; the others' are columns
+    AttendScratch columns;  // of those
+    int rows_per_unit;        // of those: kUnitRows / share (0: only pairs)
 };
 
 constexpr int kWidePrefixes = 1, kWideGroups = 2;
@@ -115,7 +117,7 @@ inline bool runs_pairs(const AttendParams& p) { return (p.wide & kWideGroups) !=
 #ifdef __CUDACC__
 __host__ __device__
 #endif
-inline bool runs_fragments(const AttendParams& p) { return (p.wide & kWideGroups) == 0 || (p.P > 0 && (p.wide & kWidePrefixes) == 0); }
+inline bool runs_columns(const AttendParams& p) { return (p.wide & kWideGroups) == 0 || (p.P > 0 && (p.wide & kWidePrefixes) == 0); }
 
 // The pieces of a cut unit as the join may take them from its entry (first
 // slot, pieces): as many as there can be, in slots that exist.  Whatever an
@@ -138,7 +140,8 @@ int pick_wide(const AttendParams& p);  // AttendParams::wide
 cudaError_t prepare_attend4_pairs(int dtype, int head_dim);
 cudaError_t launch_attend4_pairs(const AttendParams& p, int dtype, int head_dim, const cudaLaunchConfig_t& lc);
 cudaError_t prepare_attend4(int dtype, int head_dim);
-cudaError_t launch_attend4(const AttendParams& p, int dtype, int head_dim, cudaStream_t stream);
+cudaError_t launch_attend4(const AttendParams& p, const CUtensorMap& k_map, const CUtensorMap& v_map, int dtype, int head_dim,
+                           cudaStream_t stream);
 cudaError_t launch_attend(const AttendParams& p, const CUtensorMap& k_map, const CUtensorMap& v_map, int dtype,
                           int head_dim, cudaStream_t stream);
 
@@ -190,6 +193,16 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
+}
+
+// The power of two that brings a row's largest lane, `top`, to [2^14, 2^15) and
+// what undoes it (1 for rows of zeros, infinities or NaN).
+__device__ __forceinline__ float2 lift_of(float top) {
+    const int field = (int)(__float_as_uint(top) >> 23);
+    int up = 141 - field;
+    up = up > 126 ? 126 : up;
+    if (field == 255 || top == 0.0f) up = 0;
+    return make_float2(__uint_as_float((uint32_t)(up + 127) << 23), __uint_as_float((uint32_t)(127 - up) << 23));
 }
 
 // The group that `row` belongs to; -1 where no group claims it, or several do

@@ -42,19 +42,14 @@ struct Pairs4 : Pairs {
     static __device__ __forceinline__ bool takes(const AttendParams& p, bool prefix) { return (p.wide & (prefix ? kWidePrefixes : kWideGroups)) != 0; }
 };
 
-// Units of one tile of 128 query rows at most, in fragments of 16 rows: a piece
-// leaves one part.  In times of 256 cycles of a multiprocessor: a token tile's
-// keys and values come in 3, its products take 2 for every fragment, and every
-// unit has 8 more (its queries, the join of its warps).
-struct Fragments {
-    static constexpr int kSets = 1, kUnitCost = 8;
-    static constexpr int kMostCost = 0;  // of a tile: as the call's units have it
-    static __device__ __forceinline__ int unit_rows(const AttendParams& p) { return p.rows_per_tile; }
-    static __device__ __forceinline__ int cost(const AttendParams& p, int n) {
-        const int rows = (n < p.rows_per_tile ? n : p.rows_per_tile) * p.share, products = (rows + 15) / 16 * 2;
-        return products > 3 ? products : 3;
-    }
-    static __device__ __forceinline__ const AttendScratch& scratch(const AttendParams& p) { return p.fragments; }
+// Units of at most kUnitRows query rows, whose tiles' products have the tokens as
+// rows, for calls with as few heads for a key-value head: a piece leaves one part.
+// A token tile costs 3, and every unit 6 more.
+struct Columns {
+    static constexpr int kSets = 1, kUnitCost = 6, kMostCost = 3;
+    static __device__ __forceinline__ int unit_rows(const AttendParams& p) { return p.rows_per_unit; }
+    static __device__ __forceinline__ int cost(const AttendParams&, int) { return kMostCost; }
+    static __device__ __forceinline__ const AttendScratch& scratch(const AttendParams& p) { return p.columns; }
     static __device__ __forceinline__ bool takes(const AttendParams& p, bool prefix) { return !Pairs4::takes(p, prefix); }
 };
 
@@ -166,9 +161,9 @@ __device__ __forceinline__ Runs make_runs(unsigned long long total, int grid, in
 template <class Rule>
 __device__ __forceinline__ long long part_row(const AttendParams& p, bool prefix, long long slot, int set) {
     const AttendScratch& sc = Rule::scratch(p);
-    if (prefix) return slot < sc.prefix_slots ? (slot * Rule::kSets + set) * kQTile : -1;
+    if (prefix) return slot < sc.prefix_slots ? (slot * Rule::kSets + set) * sc.prefix_rows : -1;
     if (slot >= sc.group_slots) return -1;
-    return sc.prefix_slots * Rule::kSets * kQTile + (slot * Rule::kSets + set) * sc.group_rows;
+    return sc.prefix_slots * Rule::kSets * sc.prefix_rows + (slot * Rule::kSets + set) * sc.group_rows;
 }
 
 // Where a unit that is not dealt out is entered for the join; -1 as above.
@@ -233,7 +228,7 @@ struct Walk {
         table = prefix ? p.prefix_tables + (long long)sg * p.max_prefix_pages : p.tables + (long long)(sg - p.P) * p.max_pages;
         token = (long long)t0 * kKTile;
         x.part = part_row<Rule>(p, prefix, slot, 0);
-        x.part_stride = prefix ? kQTile : Rule::scratch(p).group_rows;
+        x.part_stride = prefix ? Rule::scratch(p).prefix_rows : Rule::scratch(p).group_rows;
     }
     __device__ __forceinline__ bool next(const AttendParams& p, Piece& x) {
         while (deal < deal_end) {
@@ -286,7 +281,7 @@ struct Walk {
 template <class Rule>
 struct PlanCtl {
     unsigned long long sum[kWarps][3];
-    int sum_dealt[kWarps], most_cost[2], deal_first, deal_last;
+    int sum_dealt[kWarps], deal_first, deal_last;
     Start<Rule> start[2];
 };
 
@@ -301,13 +296,12 @@ __device__ __forceinline__ bool plan_run(const AttendParams& p, PlanCtl<Rule>* c
     const int s0 = tid * per < S ? tid * per : S, s1 = s0 + per < S ? s0 + per : S;
     // of prefixes and of groups; units: slots of units that do not go round, of prefixes in the high half
     unsigned long long cost0 = 0, cost1 = 0, units = 0;
-    int dealt = 0, first = S, last = -1, cost[2] = {1, 1};
+    int dealt = 0, first = S, last = -1;
     for (int s = s0; s < s1; ++s) {
         const Seg<Rule> x = load_seg<Rule>(p, s);
         (s < p.P ? cost0 : cost1) += x.work(p);
         units += (unsigned long long)x.left(p) << (s < p.P ? 32 : 0);
         dealt += x.dealt;
-        if (Rule::kMostCost == 0 && x.tiles > 0) cost[s < p.P ? 0 : 1] = max(cost[s < p.P ? 0 : 1], x.cost);
         if (x.dealt > 0) {
             if (last < 0) first = s;
             last = s;
@@ -324,15 +318,6 @@ __device__ __forceinline__ bool plan_run(const AttendParams& p, PlanCtl<Rule>* c
     }
     if (lane == 31 && warp < kWarps) ctl->sum[warp][0] = i0, ctl->sum[warp][1] = i1, ctl->sum[warp][2] = iu, ctl->sum_dealt[warp] = id;
     if (tid == 0) ctl->deal_first = S, ctl->deal_last = -1;
-    if (Rule::kMostCost == 0) {
-        if (tid == 0) ctl->most_cost[0] = ctl->most_cost[1] = 1;
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int most = __reduce_max_sync(kFull, cost[k]);
-            if (lane == 0 && most > 1) atomicMax(&ctl->most_cost[k], most);
-        }
-    }
     __syncthreads();
     if (last >= 0) atomicMin(&ctl->deal_first, first), atomicMax(&ctl->deal_last, last);
     unsigned long long b0 = 0, b1 = 0, bu = 0, total0 = 0, total1 = 0;
@@ -347,8 +332,8 @@ __device__ __forceinline__ bool plan_run(const AttendParams& p, PlanCtl<Rule>* c
     }
     unsigned long long at0 = b0 + i0 - cost0, at1 = b1 + i1 - cost1, u = bu + iu - units;
     int d = bd + id - dealt;
-    runs[0] = make_runs(total0, gridDim.x, 0, Rule::kMostCost == 0 ? ctl->most_cost[0] : Rule::kMostCost);
-    runs[1] = make_runs(total1, gridDim.x, 1, Rule::kMostCost == 0 ? ctl->most_cost[1] : Rule::kMostCost);
+    runs[0] = make_runs(total0, gridDim.x, 0, Rule::kMostCost);
+    runs[1] = make_runs(total1, gridDim.x, 1, Rule::kMostCost);
     const int cta = blockIdx.x;
     const unsigned long long lo0 = cta < runs[0].blocks ? runs[0].start(cta) : ~0ull, lo1 = cta < runs[1].blocks ? runs[1].start(cta) : ~0ull;
     if (cta == 0 || (lo0 >= at0 && lo0 < at0 + cost0) || (lo1 >= at1 && lo1 < at1 + cost1)) {
