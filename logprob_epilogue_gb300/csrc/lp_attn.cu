@@ -77,12 +77,11 @@ struct Scratch {
 };
 
 // Pieces of a kind: every unit starts one and every block boundary one more.
-// sets: tiles of a unit, and parts of a piece.
-// tile: query rows of one.
-void lay_tables(Layout& L, const lp_attn_desc* d, int grid, int sets, int tile, size_t& off) {
+// tiles: of a unit, of `tile` query rows each.
+void lay_tables(Layout& L, const lp_attn_desc* d, int grid, int tiles, int tile, size_t& off) {
     const int share = d->q_heads / d->kv_heads, per_tile = tile / share;
-    const long long group_units = (long long)d->max_groups * ((d->max_group_rows + sets * per_tile - 1) / (sets * per_tile));
-    const long long prefix_units = d->max_prefixes == 0 ? 0 : d->max_rows / (sets * per_tile) + d->max_prefixes;
+    const long long group_units = (long long)d->max_groups * ((d->max_group_rows + tiles * per_tile - 1) / (tiles * per_tile));
+    const long long prefix_units = d->max_prefixes == 0 ? 0 : d->max_rows / (tiles * per_tile) + d->max_prefixes;
     L.prefix_rows = tile;
     L.group_rows = (d->max_group_rows < per_tile ? d->max_group_rows : per_tile) * share;
     L.group_slots = group_units * d->kv_heads + grid;
@@ -96,8 +95,9 @@ void lay_tables(Layout& L, const lp_attn_desc* d, int grid, int sets, int tile, 
     off = lp::align_up(off + (size_t)grid * 4);
 }
 
-void lay_parts(Layout& L, const lp_attn_desc* d, int sets, size_t& off) {
-    const size_t part_rows = sets * ((size_t)L.prefix_slots * (size_t)L.prefix_rows + (size_t)L.group_slots * (size_t)L.group_rows);
+// Two parts of a piece.
+void lay_parts(Layout& L, const lp_attn_desc* d, size_t& off) {
+    const size_t part_rows = 2 * ((size_t)L.prefix_slots * (size_t)L.prefix_rows + (size_t)L.group_slots * (size_t)L.group_rows);
     L.part_ml = off;
     off = lp::align_up(off + part_rows * 8);
     L.part_o = off;
@@ -111,8 +111,8 @@ Scratch scratch_of(const lp_attn_desc* d, int grid) {
     lay_tables(s.pairs, d, grid, 2, lp::kQTile, off);
     if (four) lay_tables(s.columns, d, grid, 1, lp::kUnitRows, off);
     s.tables = off;
-    lay_parts(s.pairs, d, 2, off);
-    if (four) lay_parts(s.columns, d, 1, off);
+    lay_parts(s.pairs, d, off);
+    if (four) lay_parts(s.columns, d, off);
     s.reserved = off;
     off = lp::align_up(off + (size_t)d->max_groups * sizeof(lp::Reserved));
     s.ends = off;
@@ -151,13 +151,13 @@ bool encode_cache(const lp_attn_s* plan, CUtensorMap* map, const void* cache) {
 }
 
 // The same of codes in 4 bits: a token's D / 2 bytes (its parts turned, see the
-// kernel) by as many tokens as a warp fetches of a page.
+// kernel) by a page's tokens, or a tile's.
 bool encode_codes(const lp_attn_s* plan, CUtensorMap* map, const void* codes) {
     const lp_attn_desc& d = plan->d;
     const cuuint64_t row = (cuuint64_t)d.head_dim / 2;
     const cuuint64_t dims[4] = {row, (cuuint64_t)d.page_size, (cuuint64_t)d.kv_heads, (cuuint64_t)d.num_pages};
     const cuuint64_t strides[3] = {row, row * d.page_size, row * d.page_size * d.kv_heads};
-    const cuuint32_t box[4] = {(cuuint32_t)row, (cuuint32_t)(d.page_size < 32 ? d.page_size : 32), 1, 1};
+    const cuuint32_t box[4] = {(cuuint32_t)row, (cuuint32_t)lp::cache_box_rows(d.page_size), 1, 1};
     const cuuint32_t step[4] = {1, 1, 1, 1};
     return plan->encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(codes), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         d.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

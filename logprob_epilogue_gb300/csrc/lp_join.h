@@ -75,11 +75,11 @@ struct Parts {
         if (s.tiles == 0) return;
         seg = segment;
         const int rt = p.rows_per_tile, unit_rows = Rule::unit_rows(p), rel = of - s.r0, u = rel / unit_rows, in = rel - u * unit_rows, kvh = head / p.share;
-        const bool two = Rule::kSets == 2 && s.n - u * unit_rows > rt;
+        const bool two = Rule::kPairs && s.n - u * unit_rows > rt;
         unit = kvh * s.units + u;
         dealt = s.dealt;
         set = two && in >= rt ? 1 : 0;
-        sets = two ? 1 : Rule::kSets;  // a unit of one tile: a part of each warpgroup
+        sets = two ? 1 : Rule::kSets;  // a unit of one tile: a part of each warpgroup (or stream)
         row = (in - set * rt) * p.share + head - kvh * p.share;
         cap = segment < p.P ? Rule::scratch(p).prefix_rows : Rule::scratch(p).group_rows;
     }

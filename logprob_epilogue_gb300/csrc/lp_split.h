@@ -24,11 +24,18 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // Units of up to two tiles of 128 query rows: a piece leaves a part for each
 // tile, or for each warpgroup where the unit is one tile.  What a run is
 // measured in, by the times of each: a token tile of a one-tile unit is 2, of a
 // two-tile unit 3, and every unit 4 more (its queries, first loads and results).
 struct Pairs {
+    static constexpr bool kPairs = true;
     static constexpr int kSets = 2, kTileCost = 2, kPairCost = 3, kUnitCost = 4;
     static constexpr int kMostCost = kPairCost;  // of a tile
     static __device__ __forceinline__ int unit_rows(const AttendParams& p) { return 2 * p.rows_per_tile; }
@@ -43,10 +50,11 @@ struct Pairs4 : Pairs {
 };
 
 // Units of at most kUnitRows query rows, whose tiles' products have the tokens as
-// rows, for calls with as few heads for a key-value head: a piece leaves one part.
-// A token tile costs 3, and every unit 6 more.
+// rows, for calls with as few heads for a key-value head: a piece leaves a part of its
+// even tiles and one of its odd ones.  A token tile costs 3, and every unit 6 more.
 struct Columns {
-    static constexpr int kSets = 1, kUnitCost = 6, kMostCost = 3;
+    static constexpr bool kPairs = false;
+    static constexpr int kSets = 2, kUnitCost = 6, kMostCost = 3;
     static __device__ __forceinline__ int unit_rows(const AttendParams& p) { return p.rows_per_unit; }
     static __device__ __forceinline__ int cost(const AttendParams&, int) { return kMostCost; }
     static __device__ __forceinline__ const AttendScratch& scratch(const AttendParams& p) { return p.columns; }

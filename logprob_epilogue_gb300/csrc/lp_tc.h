@@ -68,6 +68,14 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsign
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit, abort));
 }
 
+// Two of them, looked at side by side (each by all lanes: a barrier is one warp's
+// business at a time).
+__device__ __forceinline__ bool warp_wait2(uint64_t* a, uint32_t parity_a, uint64_t* b, uint32_t parity_b, unsigned long long limit, volatile int* abort) {
+    const bool first = mbar_try_wait(a, parity_a), second = mbar_try_wait(b, parity_b);
+    if (__all_sync(0xffffffffu, first && second)) return true;
+    return __all_sync(0xffffffffu, mbar_wait(a, parity_a, limit, abort) && mbar_wait(b, parity_b, limit, abort));
+}
+
 // A counter in shared memory that one thread raises: waits until it is past
 // `n` (differences modulo 2^32).  False as for mbar_wait.
 __device__ __forceinline__ void store_release(uint32_t* at, uint32_t v) {
