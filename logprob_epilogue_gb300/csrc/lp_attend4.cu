@@ -89,8 +89,8 @@ struct Ctl4 : PlanCtl<Columns> {
     int abort;
 };
 
-// The queries of a unit by a warp, rows past its last zeros, in the places where the
-// tensor core reads them (128-byte swizzle).  BF16 becomes F16 by a power of two for
+// The queries of a unit by a warp, rows past its last up to sixteen zeros, in the
+// places where the tensor core reads them (128-byte swizzle).  BF16 becomes F16 by a power of two for
 // each row; D / 8 threads have a row.
 template <bool kBf16, int D>
 __device__ __forceinline__ void lay_queries(const AttendParams& p, const Piece& x, uint32_t to, float* unit) {
@@ -99,7 +99,7 @@ __device__ __forceinline__ void lay_queries(const AttendParams& p, const Piece& 
     const int lane = threadIdx.x & 31, ch = lane % kChunks, rows = x.rows * p.share;
     const T* src = reinterpret_cast<const T*>(p.q) + (long long)x.row * p.q_stride + (long long)x.kvh * p.share * D + ch * 8;
 #pragma unroll 1
-    for (int base = 0; base < kUnitRows; base += kTurns * kAtOnce) {
+    for (int base = 0; base < ((rows + 15) & ~15); base += kTurns * kAtOnce) {
         uint4 w[kTurns];
 #pragma unroll
         for (int k = 0; k < kTurns; ++k) {
@@ -111,17 +111,21 @@ __device__ __forceinline__ void lay_queries(const AttendParams& p, const Piece& 
         for (int k = 0; k < kTurns; ++k) {
             const int row = base + k * kAtOnce + lane / kChunks;
             if constexpr (kBf16) {
-                float q[8];
-                widen8<true>(w[k], q);
-                float top = fabsf(q[0]);
+                // the largest magnitude: that of BF16 is its order as an integer without the sign
+                const uint32_t m = 0x7FFF7FFFu;
+                uint32_t top = __vmaxu2(__vmaxu2(w[k].x & m, w[k].y & m), __vmaxu2(w[k].z & m, w[k].w & m));
 #pragma unroll
-                for (int e = 1; e < 8; ++e) top = fmaxf(top, fabsf(q[e]));
-#pragma unroll
-                for (int o = kChunks / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-                const float2 lift = lift_of(top);
+                for (int o = kChunks / 2; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(kFull, top, o));
+                const uint32_t most = top >> 16 > (top & 0xFFFFu) ? top & 0xFFFF0000u : top << 16;
+                const float2 lift = lift_of(__uint_as_float(most));
                 if (ch == 0) unit[row] = lift.y;
-                w[k] = make_uint4(Half<false>::pack(q[0] * lift.x, q[1] * lift.x), Half<false>::pack(q[2] * lift.x, q[3] * lift.x),
-                                  Half<false>::pack(q[4] * lift.x, q[5] * lift.x), Half<false>::pack(q[6] * lift.x, q[7] * lift.x));
+                uint32_t a[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 q = Half<true>::unpack(a[e]);
+                    a[e] = Half<false>::pack(q.x * lift.x, q.y * lift.x);
+                }
+                w[k] = make_uint4(a[0], a[1], a[2], a[3]);
             } else if (ch == 0) {
                 unit[row] = 1.0f;
             }
@@ -131,31 +135,23 @@ __device__ __forceinline__ void lay_queries(const AttendParams& p, const Piece& 
     tc::fence_async_shared();
 }
 
-// The scales of a thread's token, each as a pair of F16; zeros where `zero`.
+// A sixteenth of a tile's way to F16: 32 lanes of a thread's token.  The copies turn
+// a token's parts of 16 bytes (64- or 32-byte swizzle), so that the threads that read a
+// part of eight tokens meet every bank once.
 template <int D>
-__device__ __forceinline__ void token_scales(const unsigned char* scales, int token, bool zero, uint32_t (&e)[D / 16]) {
-    uint32_t s[D / 64];
-    if constexpr (D == 128) {
-        const uint2 w = *reinterpret_cast<const uint2*>(scales + token * 8);
-        s[0] = w.x, s[D / 64 - 1] = w.y;
-    } else {
-        s[0] = *reinterpret_cast<const uint32_t*>(scales + token * 4);
-    }
+__device__ __forceinline__ void expand_part(const unsigned char* codes, const unsigned char* scales, int token, int part, bool exists, uint32_t (&h)[16]) {
+    const uint4 w = *reinterpret_cast<const uint4*>(codes + token * (D / 2) + (part ^ (D == 128 ? token >> 1 & 3 : token >> 2 & 1)) * 16);
+    uint32_t two = *reinterpret_cast<const uint16_t*>(scales + token * (D / kBlock4) + part * 2);
+    if (!exists) two = 0u;
+    two = widen_scales(two);
+    const uint32_t e[2] = {__byte_perm(two, 0, 0x1010), __byte_perm(two, 0, 0x3232)}, c[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-        if (zero) s[i] = 0u;
-        const uint32_t a = widen_scales(s[i]), b = widen_scales(s[i] >> 16);
-        e[4 * i] = __byte_perm(a, 0, 0x1010), e[4 * i + 1] = __byte_perm(a, 0, 0x3232);
-        e[4 * i + 2] = __byte_perm(b, 0, 0x1010), e[4 * i + 3] = __byte_perm(b, 0, 0x3232);
+    for (int j = 0; j < 4; ++j) {
+        uint32_t v[4];
+        widen_codes(c[j], v);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) h[j * 4 + q] = mul2(v[q], e[j >> 1]);
     }
-}
-
-// Sixteen bytes of a thread's token, 32 codes.  The copies turn a token's parts (64-
-// or 32-byte swizzle), so that the lanes that read a part of eight tokens meet every
-// bank once.
-template <int D>
-__device__ __forceinline__ uint4 token_codes(const unsigned char* codes, int token, int part) {
-    return *reinterpret_cast<const uint4*>(codes + token * (D / 2) + (part ^ (D == 128 ? token >> 1 & 3 : token >> 2 & 1)) * 16);
 }
 
 template <bool kBf16, int D>
@@ -417,64 +413,78 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
         }
     } else if (warp >= kFirstExpand) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsExpand));
-        // ---- codes to F16: 32 tokens of the stream's tiles
+        // ---- codes to F16: 32 tokens of the stream's tiles.  A tile's keys go before the values of the one before, whose
+        // place may still be in use.
         const int stream = (warp - kFirstExpand) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t keys = tmem + ((uint32_t)quarter << 21) + kColK + stream * (D / 2);
         const uint32_t values = tc::smem_addr(smem + stream * C::kValues) + row * 128;
-        uint32_t use = 0, slot = 0, phase = 0;  // the stream's tiles; of its ring
-        while (ok && next_piece()) {
-            for (int i = stream; i < x.tiles; i += 2, ++use) {
-                const int have = x.left - i * kKTile;  // tokens of the tile
-                const unsigned char* tile = smem + C::kAtRing + (stream * C::kRing + slot) * C::kBytes;
-                if (!wait2(&ctl->tile_full[stream][slot], phase, &ctl->k_empty[stream], (use & 1u) ^ 1u)) break;
-                tc::fence_after();
-                {
-                    uint32_t e[D / 16];
-                    token_scales<D>(tile + 2 * C::kCodes, row, false, e);
-#pragma unroll
-                    for (int h = 0; h < D / 64; ++h) {
-                        uint32_t k[32];
-#pragma unroll
-                        for (int part = 0; part < 2; ++part) {
-                            const uint4 w = token_codes<D>(tile, row, 2 * h + part);
-                            const uint32_t codes[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                uint32_t v[4];
-                                widen_codes(codes[j], v);
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) k[part * 16 + j * 4 + q] = mul2(v[q], e[h * 4 + part * 2 + (j >> 1)]);
-                            }
-                        }
-                        tc::tmem_st32(keys + h * 32, k);
-                    }
-                    tc::wait_st();
-                    tc::fence_before();
-                }
-                arrive(&ctl->k_full[stream]);
-                if (!wait(&ctl->v_empty[stream], (use & 1u) ^ 1u)) break;
-                {
-                    uint32_t e[D / 16];
-                    token_scales<D>(tile + 2 * C::kCodes + C::kScales, row, row >= have, e);  // what lies past the tokens may be NaN, and 0 * v has to stay 0
-#pragma unroll
-                    for (int part = 0; part < D / 32; ++part) {
-                        const uint4 w = token_codes<D>(tile + C::kCodes, row, part);
-                        const uint32_t codes[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int ch = part * 4 + j;
-                            uint32_t v[4];
-                            widen_codes(codes[j], v);
-                            tc::store16(values + (ch >> 3) * (kKTile * 128) + (((ch & 7) ^ (row & 7)) << 4),
-                                        make_uint4(mul2(v[0], e[ch / 2]), mul2(v[1], e[ch / 2]), mul2(v[2], e[ch / 2]), mul2(v[3], e[ch / 2])));
-                        }
-                    }
-                    tc::fence_async_shared();
-                }
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&ctl->tile_empty[stream][slot]), tc::mbar_arrive(&ctl->v_full[stream]);
-                if (++slot == C::kRing) slot = 0, phase ^= 1u;
+        const unsigned char* ring = smem + C::kAtRing + stream * C::kRing * C::kBytes;
+        uint32_t use_k = 0, slot = 0, phase = 0;  // the stream's tiles; of its ring
+        uint32_t use_v = 0, v_slot = 0;
+        int pending = 0;  // tokens of the tile whose values are left
+        auto expand_keys = [&]() {
+            const unsigned char* tile = ring + slot * C::kBytes;
+            if (!wait2(&ctl->tile_full[stream][slot], phase, &ctl->k_empty[stream], (use_k & 1u) ^ 1u)) return false;
+            tc::fence_after();
+            // (short code in loops: with many warps at many places, unrolled loops wait for their instructions)
+#pragma unroll 1
+            for (int part = 0; part < D / 32; ++part) {
+                uint32_t h[16];
+                expand_part<D>(tile, tile + 2 * C::kCodes, row, part, true, h);
+                tc::tmem_st16(keys + part * 16, h);
             }
+            tc::wait_st();
+            tc::fence_before();
+            arrive(&ctl->k_full[stream]);
+            ++use_k;
+            if (++slot == C::kRing) slot = 0, phase ^= 1u;
+            return true;
+        };
+        auto expand_values = [&]() {
+            const unsigned char* tile = ring + v_slot * C::kBytes + C::kCodes;
+            if (!wait(&ctl->v_empty[stream], (use_v & 1u) ^ 1u)) return false;
+#pragma unroll 1
+            for (int part = 0; part < D / 32; ++part) {
+                uint32_t h[16];
+                expand_part<D>(tile, tile + C::kCodes + C::kScales, row, part, row < pending, h);  // what lies past the tokens may be NaN, and 0 * v has to stay 0
+                const uint32_t to = values + (part >> 1) * (kKTile * 128);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) tc::store16(to + ((((part & 1) * 4 + j) ^ (row & 7)) << 4), make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]));
+            }
+            tc::fence_async_shared();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&ctl->tile_empty[stream][v_slot]), tc::mbar_arrive(&ctl->v_full[stream]);
+            ++use_v;
+            if (++v_slot == C::kRing) v_slot = 0;
+            pending = 0;
+            return true;
+        };
+        // One place for each, so that neither's code comes twice: an iteration takes a tile's keys, or the next piece, and then
+        // the values that are due.
+        int i = 0;
+        x.tiles = 0;
+        for (bool more = ok; more || pending > 0;) {
+            bool due = pending > 0;
+            int have = 0;
+            if (i < x.tiles) {
+                have = x.left - i * kKTile;
+                i += 2;
+                if (!expand_keys()) break;
+            } else if (more) {
+                // The next piece, where it is known: the values left may be what the others wait for.
+                const uint32_t at = n_piece % kPieces;
+                if (due && !__all_sync(kFull, tc::mbar_try_wait(&ctl->piece_full[at], n_piece / kPieces & 1u))) {
+                    // they first
+                } else {
+                    more = next_piece();
+                    if (!ok) break;
+                    if (!more) x.tiles = 0;
+                    i = stream;
+                    if (i < x.tiles) continue;
+                }
+            }
+            if (due && !expand_values()) break;
+            if (have > 0) pending = have;
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
@@ -608,7 +618,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
                     if (!wait2(&ctl->k_full[stream], use_k & 1u, &ctl->s_empty[stream], (use_k & 1u) ^ 1u)) return false;
                     ++use_k;
                     tc::fence_after();
-#pragma unroll
+#pragma unroll 2
                     for (int k = 0; k < D / 16; ++k)
                         tc::mma_ts(score, keys + k * 8, q + (uint64_t)(((k / 4) * (kUnitRows * 128) + (k % 4) * 32) >> 4), idesc_s, k > 0, one);
                     tc::commit(&ctl->s_full[stream], one);
@@ -623,14 +633,10 @@ __global__ void __launch_bounds__(kBlockThreads, 1)
                     ++use_v;
                     if (i == stream && !wait(&ctl->o_free[stream], (use_o++ & 1u) ^ 1u)) break;
                     tc::fence_after();
-                    if (have >= kKTile) {
-#pragma unroll
-                        for (int k = 0; k < kKTile / 16; ++k) tc::mma_ss(result, v + (uint64_t)(k * 2048 >> 4), pr + (uint64_t)(k * 2048 >> 4), idesc_o, k > 0 || i != stream, one);
-                    } else {
-#pragma unroll 1
-                        for (int k = 0; k < (have + 15) >> 4; ++k)
-                            tc::mma_ss(result, v + (uint64_t)(k * 2048 >> 4), pr + (uint64_t)(k * 2048 >> 4), idesc_o, k > 0 || i != stream, one);
-                    }
+                    const int steps = have < kKTile ? (have + 15) >> 4 : kKTile / 16;
+#pragma unroll 2
+                    for (int k = 0; k < steps; ++k)
+                        tc::mma_ss(result, v + (uint64_t)(k * 2048 >> 4), pr + (uint64_t)(k * 2048 >> 4), idesc_o, k > 0 || i != stream, one);
                     tc::commit(&ctl->v_empty[stream], one);
                     tc::commit(&ctl->p_empty[stream], one);
                 }
