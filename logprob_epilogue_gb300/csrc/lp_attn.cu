@@ -22,7 +22,7 @@ struct lp_attn_s {
     int page_shift;
     int grid;
     unsigned char* scratch;
-    lp::AttendScratch sc, columns;
+    lp::AttendScratch sc, fragments;
     lp::Reserved* reserved;  // scratch of lp_kv_reserve
     long long* ends;
     EncodeTiled encode;
@@ -72,7 +72,7 @@ struct Layout {
 };
 
 struct Scratch {
-    Layout pairs, columns;        // columns: of a plan over 4 bits
+    Layout pairs, fragments;        // fragments: of a plan over 4 bits
     size_t tables, reserved, ends, total;  // tables: bytes of all the tables, which come first
 };
 
@@ -95,9 +95,9 @@ void lay_tables(Layout& L, const lp_attn_desc* d, int grid, int tiles, int tile,
     off = lp::align_up(off + (size_t)grid * 4);
 }
 
-// Two parts of a piece.
-void lay_parts(Layout& L, const lp_attn_desc* d, size_t& off) {
-    const size_t part_rows = 2 * ((size_t)L.prefix_slots * (size_t)L.prefix_rows + (size_t)L.group_slots * (size_t)L.group_rows);
+// `sets` parts of a piece.
+void lay_parts(Layout& L, const lp_attn_desc* d, int sets, size_t& off) {
+    const size_t part_rows = (size_t)sets * ((size_t)L.prefix_slots * (size_t)L.prefix_rows + (size_t)L.group_slots * (size_t)L.group_rows);
     L.part_ml = off;
     off = lp::align_up(off + part_rows * 8);
     L.part_o = off;
@@ -109,10 +109,10 @@ Scratch scratch_of(const lp_attn_desc* d, int grid) {
     const bool four = (d->flags & LP_ATTN_KV4) != 0 && d->q_heads / d->kv_heads <= lp::kUnitRows;
     size_t off = 0;
     lay_tables(s.pairs, d, grid, 2, lp::kQTile, off);
-    if (four) lay_tables(s.columns, d, grid, 1, lp::kUnitRows, off);
+    if (four) lay_tables(s.fragments, d, grid, 1, lp::kUnitRows, off);
     s.tables = off;
-    lay_parts(s.pairs, d, off);
-    if (four) lay_parts(s.columns, d, off);
+    lay_parts(s.pairs, d, 2, off);
+    if (four) lay_parts(s.fragments, d, 1, off);
     s.reserved = off;
     off = lp::align_up(off + (size_t)d->max_groups * sizeof(lp::Reserved));
     s.ends = off;
@@ -147,20 +147,6 @@ bool encode_cache(const lp_attn_s* plan, CUtensorMap* map, const void* cache) {
     return plan->encode(map, d.dtype == LP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                         const_cast<void*>(cache), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// The same of codes in 4 bits: a token's D / 2 bytes (its parts turned, see the
-// kernel) by a page's tokens, or a tile's.
-bool encode_codes(const lp_attn_s* plan, CUtensorMap* map, const void* codes) {
-    const lp_attn_desc& d = plan->d;
-    const cuuint64_t row = (cuuint64_t)d.head_dim / 2;
-    const cuuint64_t dims[4] = {row, (cuuint64_t)d.page_size, (cuuint64_t)d.kv_heads, (cuuint64_t)d.num_pages};
-    const cuuint64_t strides[3] = {row, row * d.page_size, row * d.page_size * d.kv_heads};
-    const cuuint32_t box[4] = {(cuuint32_t)row, (cuuint32_t)lp::cache_box_rows(d.page_size), 1, 1};
-    const cuuint32_t step[4] = {1, 1, 1, 1};
-    return plan->encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(codes), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        d.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -378,7 +364,7 @@ int lp_attn_create(lp_attn_t* out, const lp_attn_desc* desc) {
         return cuda_fail(e);
     }
     plan->sc = place(s.pairs, plan->scratch);
-    if (s.columns.prefix_rows > 0) plan->columns = place(s.columns, plan->scratch);
+    if (s.fragments.prefix_rows > 0) plan->fragments = place(s.fragments, plan->scratch);
     plan->reserved = reinterpret_cast<lp::Reserved*>(plan->scratch + s.reserved);
     plan->ends = reinterpret_cast<long long*>(plan->scratch + s.ends);
     *out = plan;
@@ -512,12 +498,11 @@ int lp_attend4(lp_attn_t plan, const lp_attend4_io* io, void* stream) {
     p.v_scales = static_cast<const unsigned char*>(io->v_scales);
     p.k_factor = io->k_factor;
     p.v_factor = io->v_factor;
-    p.columns = plan->columns;
+    p.fragments = plan->fragments;
     p.rows_per_unit = lp::kUnitRows / p.share;
+    p.two_cost = plan->d.head_dim == 64 ? 3 : 4;
     p.wide = lp::pick_wide(p);
-    CUtensorMap k_map, v_map;
-    if (!encode_codes(plan, &k_map, io->attend.k_cache) || !encode_codes(plan, &v_map, io->attend.v_cache)) return cuda_fail(cudaErrorInvalidValue);
-    const cudaError_t e = lp::launch_attend4(p, k_map, v_map, plan->d.dtype, plan->d.head_dim, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = lp::launch_attend4(p, plan->d.dtype, plan->d.head_dim, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? LP_OK : cuda_fail(e);
 }
 

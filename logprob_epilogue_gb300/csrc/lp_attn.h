@@ -61,7 +61,7 @@ struct ReserveParams {
 };
 
 constexpr int kQTile = 128;    // query rows (row, head) of one tensor-core tile
-constexpr int kUnitRows = 32;  // of a unit whose rows are the products' columns
+constexpr int kUnitRows = 32;  // of a unit of fragments
 constexpr int kKTile = 128;    // tokens of one tile
 
 // Scratch of lp_attend.  A segment is a prefix or a group's committed tokens;
@@ -102,8 +102,9 @@ struct AttendParams {
     // a cache of 4 bits; k_cache, v_cache: the codes
     const unsigned char *k_scales, *v_scales;
     float k_factor, v_factor;
-    int wide;              // segments whose units are pairs of tiles: kWidePrefixes, kWideGroups; the others' are columns
-    AttendScratch columns;  // of those
+    int wide;              // segments whose units are pairs of tiles: kWidePrefixes, kWideGroups; the others' are fragments
+    AttendScratch fragments;  // of those
+    int two_cost;             // of those with two fragments: of a token tile, see Fragments
     int rows_per_unit;        // of those: kUnitRows / share (0: only pairs)
 };
 
@@ -117,7 +118,7 @@ inline bool runs_pairs(const AttendParams& p) { return (p.wide & kWideGroups) !=
 #ifdef __CUDACC__
 __host__ __device__
 #endif
-inline bool runs_columns(const AttendParams& p) { return (p.wide & kWideGroups) == 0 || (p.P > 0 && (p.wide & kWidePrefixes) == 0); }
+inline bool runs_fragments(const AttendParams& p) { return (p.wide & kWideGroups) == 0 || (p.P > 0 && (p.wide & kWidePrefixes) == 0); }
 
 // The pieces of a cut unit as the join may take them from its entry (first
 // slot, pieces): as many as there can be, in slots that exist.  Whatever an
@@ -140,8 +141,7 @@ int pick_wide(const AttendParams& p);  // AttendParams::wide
 cudaError_t prepare_attend4_pairs(int dtype, int head_dim);
 cudaError_t launch_attend4_pairs(const AttendParams& p, int dtype, int head_dim, const cudaLaunchConfig_t& lc);
 cudaError_t prepare_attend4(int dtype, int head_dim);
-cudaError_t launch_attend4(const AttendParams& p, const CUtensorMap& k_map, const CUtensorMap& v_map, int dtype, int head_dim,
-                           cudaStream_t stream);
+cudaError_t launch_attend4(const AttendParams& p, int dtype, int head_dim, cudaStream_t stream);
 cudaError_t launch_attend(const AttendParams& p, const CUtensorMap& k_map, const CUtensorMap& v_map, int dtype,
                           int head_dim, cudaStream_t stream);
 

@@ -79,7 +79,7 @@ struct Parts {
         unit = kvh * s.units + u;
         dealt = s.dealt;
         set = two && in >= rt ? 1 : 0;
-        sets = two ? 1 : Rule::kSets;  // a unit of one tile: a part of each warpgroup (or stream)
+        sets = two ? 1 : Rule::kSets;  // a unit of one tile: a part of each warpgroup
         row = (in - set * rt) * p.share + head - kvh * p.share;
         cap = segment < p.P ? Rule::scratch(p).prefix_rows : Rule::scratch(p).group_rows;
     }
@@ -90,12 +90,12 @@ struct Parts {
         if constexpr (kFour) {
             pairs = Pairs4::takes(p, segment < p.P);
             if (pairs) find_by<Pairs4>(p, segment, of, head);
-            else find_by<Columns>(p, segment, of, head);
+            else find_by<Fragments>(p, segment, of, head);
         } else {
             find_by<Pairs>(p, segment, of, head);
         }
     }
-    __device__ __forceinline__ const AttendScratch& scratch(const AttendParams& p) const { return kFour && !pairs ? p.columns : p.sc; }
+    __device__ __forceinline__ const AttendScratch& scratch(const AttendParams& p) const { return kFour && !pairs ? p.fragments : p.sc; }
     __device__ __forceinline__ int2 first_slots(const AttendParams& p) const { return seg >= 0 ? scratch(p).seg_units[seg] : make_int2(0, 0); }
     __device__ __forceinline__ void locate(const AttendParams& p, int2 base) {
         const AttendScratch& sc = scratch(p);
@@ -112,7 +112,7 @@ struct Parts {
     __device__ __forceinline__ long long part(const AttendParams& p, int k) const {
         const long long at = slot + (sets == 1 ? k : k >> 1);
         const int s = sets == 1 ? set : k & 1;
-        if (kFour && !pairs) return part_row<Columns>(p, seg < p.P, at, s);
+        if (kFour && !pairs) return part_row<Fragments>(p, seg < p.P, at, s);
         return part_row<Pairs>(p, seg < p.P, at, s);
     }
 };
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
     for (int b = threadIdx.x; b < p.grid; b += kJoinThreads) {
         if constexpr (kFour) {
             if (runs_pairs(p)) gave_up |= p.sc.gave_up[b];
-            if (runs_columns(p)) gave_up |= p.columns.gave_up[b];
+            if (runs_fragments(p)) gave_up |= p.fragments.gave_up[b];
         } else {
             gave_up |= p.sc.gave_up[b];
         }

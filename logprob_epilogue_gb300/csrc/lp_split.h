@@ -49,15 +49,18 @@ struct Pairs4 : Pairs {
     static __device__ __forceinline__ bool takes(const AttendParams& p, bool prefix) { return (p.wide & (prefix ? kWidePrefixes : kWideGroups)) != 0; }
 };
 
-// Units of at most kUnitRows query rows, whose tiles' products have the tokens as
-// rows, for calls with as few heads for a key-value head: a piece leaves a part of its
-// even tiles and one of its odd ones.  A token tile costs 3, and every unit 6 more.
-struct Columns {
+// Units of at most kUnitRows query rows, one or two fragments of 16, for calls with
+// as few heads for a key-value head: a piece leaves one part.  A token tile of one
+// fragment costs 2, of two 4, or 3 where both share a worker's codes (D = 64), and
+// every unit 5 more.
+struct Fragments {
     static constexpr bool kPairs = false;
-    static constexpr int kSets = 2, kUnitCost = 6, kMostCost = 3;
+    static constexpr int kSets = 1, kUnitCost = 5, kTileCost = 2, kMostCost = 4;
     static __device__ __forceinline__ int unit_rows(const AttendParams& p) { return p.rows_per_unit; }
-    static __device__ __forceinline__ int cost(const AttendParams&, int) { return kMostCost; }
-    static __device__ __forceinline__ const AttendScratch& scratch(const AttendParams& p) { return p.columns; }
+    static __device__ __forceinline__ int cost(const AttendParams& p, int n) {
+        return (n < p.rows_per_unit ? n : p.rows_per_unit) * p.share > 16 ? p.two_cost : kTileCost;
+    }
+    static __device__ __forceinline__ const AttendScratch& scratch(const AttendParams& p) { return p.fragments; }
     static __device__ __forceinline__ bool takes(const AttendParams& p, bool prefix) { return !Pairs4::takes(p, prefix); }
 };
 

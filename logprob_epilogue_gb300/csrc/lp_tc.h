@@ -68,14 +68,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsign
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit, abort));
 }
 
-// Two of them, looked at side by side (each by all lanes: a barrier is one warp's
-// business at a time).
-__device__ __forceinline__ bool warp_wait2(uint64_t* a, uint32_t parity_a, uint64_t* b, uint32_t parity_b, unsigned long long limit, volatile int* abort) {
-    const bool first = mbar_try_wait(a, parity_a), second = mbar_try_wait(b, parity_b);
-    if (__all_sync(0xffffffffu, first && second)) return true;
-    return __all_sync(0xffffffffu, mbar_wait(a, parity_a, limit, abort) && mbar_wait(b, parity_b, limit, abort));
-}
-
 // A counter in shared memory that one thread raises: waits until it is past
 // `n` (differences modulo 2^32).  False as for mbar_wait.
 __device__ __forceinline__ void store_release(uint32_t* at, uint32_t v) {
@@ -209,8 +201,6 @@ __host__ __device__ constexpr uint32_t make_idesc(bool bf16, bool b_mn_major, in
     return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_mn_major ? 1u : 0u) << 16) |
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-
-constexpr uint32_t kAMnMajor = 1u << 15;  // of it: A's rows run along memory
 
 // D (tensor memory) = A (shared) B (shared) [+ D].
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate, uint32_t one) {
