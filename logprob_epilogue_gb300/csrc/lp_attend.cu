@@ -280,39 +280,38 @@ __device__ __forceinline__ void load_queries(const AttendParams& p, int row0, in
 }
 
 // The same from BF16 to F16, each row by a power of two of its own; D / 8 threads have a
-// row, `n` a multiple of 32.  unit[row]: what undoes it.
+// row, `n` a multiple of 32.  unit[row]: what undoes it.  All of it is under way at once,
+// then each thread changes what it fetched.
 template <int D>
 __device__ __forceinline__ void lift_queries(const AttendParams& p, int row0, int rows, int kvh, uint32_t dst, int again, float* unit, int t, int n) {
-    constexpr int kChunks = D / 8, kAtOnce = 4;
+    constexpr int kChunks = D / 8;
     const int ch = t % kChunks, total = rows * p.share, step = n / kChunks;
     const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.q) + (long long)row0 * p.q_stride + (long long)kvh * p.share * D + ch * 8;
-    for (int base = 0; base < total; base += kAtOnce * step) {
-        uint4 w[kAtOnce];
+    auto place = [&](int row) { return dst + (ch >> 3) * (kQTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4); };
+    for (int row = t / kChunks; row < total; row += step) {
+        const int per = (row * p.share_inv) >> 16, head = row - per * p.share;
+        tc::copy16(place(row), src + per * p.q_stride + head * D);
+    }
+    tc::copies_done();
+#pragma unroll 4
+    for (int base = 0; base < total; base += step) {
+        const int row = base + t / kChunks;
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (row < total) w = tc::load16(place(row));
+        // the largest magnitude: that of BF16 is its order as an integer without the sign
+        const uint32_t m = 0x7FFF7FFFu;
+        uint32_t top = __vmaxu2(__vmaxu2(w.x & m, w.y & m), __vmaxu2(w.z & m, w.w & m));
 #pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-            const int row = base + k * step + t / kChunks, per = (row * p.share_inv) >> 16, head = row - per * p.share;
-            w[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (row < total) w[k] = *reinterpret_cast<const uint4*>(src + per * p.q_stride + head * D);
-        }
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-            const int row = base + k * step + t / kChunks;
-            float x[8];
-            widen8<true>(w[k], x);
-            float top = fabsf(x[0]);
-#pragma unroll
-            for (int e = 1; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
-#pragma unroll
-            for (int o = kChunks / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-            if (row >= total) continue;
-            const float2 lift = lift_of(top);
-            if (ch == 0) unit[row] = lift.y;
-            const uint4 y = make_uint4(Half<false>::pack(x[0] * lift.x, x[1] * lift.x), Half<false>::pack(x[2] * lift.x, x[3] * lift.x),
-                                       Half<false>::pack(x[4] * lift.x, x[5] * lift.x), Half<false>::pack(x[6] * lift.x, x[7] * lift.x));
-            const uint32_t at = dst + (ch >> 3) * (kQTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
-            tc::store16(at, y);
-            if (again > 0) tc::store16(at + again * 128, y);
-        }
+        for (int o = kChunks / 2; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(kFull, top, o));
+        if (row >= total) continue;
+        const float2 lift = lift_of(__uint_as_float(top >> 16 > (top & 0xFFFFu) ? top & 0xFFFF0000u : top << 16));
+        if (ch == 0) unit[row] = lift.y;
+        float x[8];
+        widen8<true>(w, x);
+        const uint4 y = make_uint4(Half<false>::pack(x[0] * lift.x, x[1] * lift.x), Half<false>::pack(x[2] * lift.x, x[3] * lift.x),
+                                   Half<false>::pack(x[4] * lift.x, x[5] * lift.x), Half<false>::pack(x[6] * lift.x, x[7] * lift.x));
+        tc::store16(place(row), y);
+        if (again > 0) tc::store16(place(row) + again * 128, y);
     }
     tc::fence_async_shared();
 }

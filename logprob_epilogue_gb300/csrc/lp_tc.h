@@ -126,6 +126,12 @@ __device__ __forceinline__ void copy_or_zeros(uint32_t dst, const void* src, boo
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(read ? (uint32_t)kBytes : 0u) : "memory");
 }
 
+__device__ __forceinline__ uint4 load16(uint32_t src) {
+    uint4 w;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(src) : "memory");
+    return w;
+}
+
 __device__ __forceinline__ void store16(uint32_t dst, const uint4& w) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
 }
