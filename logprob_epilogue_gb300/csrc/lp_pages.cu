@@ -27,7 +27,6 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kSumThreads = 1024;
 constexpr int kFillThreads = 256;
-constexpr int kFillRows = 4 * kFillThreads;  // rows of a block of the second kernel
 
 struct Sums {
     long long rows, lack, back;
@@ -35,28 +34,43 @@ struct Sums {
 
 __device__ __forceinline__ Sums operator+(const Sums& a, const Sums& b) { return {a.rows + b.rows, a.lack + b.lack, a.back + b.back}; }
 
+// Of one group: rows (at most one more than a call may have), pages.  32 groups' sums are below 2^32.
+struct Mine {
+    unsigned rows, lack, back;
+};
+
 // Sum of the block's values before this thread's; `total`: of all.
-__device__ __forceinline__ Sums block_before(const Sums& mine, Sums& total) {
-    __shared__ Sums warps[kSumThreads / 32];
+__device__ __forceinline__ Sums block_before(const Mine& mine, Sums& total) {
+    static_assert(kSumThreads == 1024, "a warp's lane for each warp");
+    __shared__ Sums before[33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Sums x = mine;
+    Mine x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const Sums y = {__shfl_up_sync(kFull, x.rows, o), __shfl_up_sync(kFull, x.lack, o), __shfl_up_sync(kFull, x.back, o)};
-        if (lane >= o) x = x + y;
+        const Mine y = {__shfl_up_sync(kFull, x.rows, o), __shfl_up_sync(kFull, x.lack, o), __shfl_up_sync(kFull, x.back, o)};
+        if (lane >= o) x = {x.rows + y.rows, x.lack + y.lack, x.back + y.back};
     }
-    __syncthreads();  // the values of the round before are read
-    if (lane == 31) warps[warp] = x;
+    __syncthreads();  // the sums of the round before are read
+    if (lane == 31) before[warp + 1] = {x.rows, x.lack, x.back};
     __syncthreads();
-    Sums before = {0, 0, 0};
-    total = before;
-    for (int w = 0; w < kSumThreads / 32; ++w) {
-        if (w == warp) before = total;
-        total = total + warps[w];
+    if (warp == 0) {
+        Sums up = before[lane + 1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const Sums y = {__shfl_up_sync(kFull, up.rows, o), __shfl_up_sync(kFull, up.lack, o), __shfl_up_sync(kFull, up.back, o)};
+            if (lane >= o) up = up + y;
+        }
+        before[lane + 1] = up;
+        if (lane == 0) before[0] = {0, 0, 0};
     }
-    return {before.rows + x.rows - mine.rows, before.lack + x.lack - mine.lack, before.back + x.back - mine.back};
+    __syncthreads();
+    total = before[32];
+    const Sums of = before[warp];
+    return {of.rows + (x.rows - mine.rows), of.lack + (x.lack - mine.lack), of.back + (x.back - mine.back)};
 }
 
+// kSumThreads groups at a time, a thread each; the next ones' values are on their way
+// while these are summed.
 __device__ void reserve_groups(const ReserveParams& p) {
     const int tid = threadIdx.x;
     const long long head = p.queue[0], tail = p.queue[1];
@@ -69,17 +83,24 @@ __device__ void reserve_groups(const ReserveParams& p) {
     }
     __syncthreads();
     unsigned int status = sound ? 0u : kStatusBadPage;
+    long long takes = 0, returns = 0;
     Sums base = {0, 0, 0};
+    int next_len = 0, next_count = 0, next_held = 0;
+    auto load = [&](int g) {
+        if (g < p.G) next_len = p.lens[g], next_count = p.counts[g], next_held = p.held[g];
+    };
+    load(tid);
     for (int g0 = 0; g0 < p.G; g0 += kSumThreads) {
-        const int g = g0 + tid;
+        const int g = g0 + tid, len = next_len, count = next_count, held = next_held;
         const bool exists = g < p.G;
-        const int len = exists ? p.lens[g] : 0, count = exists ? p.counts[g] : 0, held = exists ? p.held[g] : 0;
-        const int n = count > 0 ? count : 0;
+        load(g + kSumThreads);
+        const int n = exists && count > 0 ? count : 0;
         const long long pages = ((long long)(len > 0 ? len : 0) + n + (1 << p.page_shift) - 1) >> p.page_shift;
         const bool holds = held >= 0 && held <= p.max_pages;
         const bool idle = len < 0;
         bool bad = exists && (count < 0 || !holds || (!idle && pages > p.max_pages));
-        Sums mine = {n, !exists || idle || bad || pages <= held ? 0 : pages - held, exists && idle && holds ? held : 0};
+        const Mine mine = {(unsigned)(n <= p.rows ? n : p.rows + 1), (unsigned)(!exists || idle || bad || pages <= held ? 0 : pages - held),
+                           (unsigned)(exists && idle && holds ? held : 0)};
         Sums total;
         const Sums at = base + block_before(mine, total);
         base = base + total;
@@ -104,20 +125,26 @@ __device__ void reserve_groups(const ReserveParams& p) {
         r.change = serves ? (int)mine.lack : (gives ? -1 - held : 0);
         r.lens = serves ? len : -1;
         p.groups[g] = r;
-        if (serves && mine.lack > 0) atomicMax(&taken, (unsigned long long)(at.lack + mine.lack));
-        if (gives) atomicMax(&returned, (unsigned long long)(at.back + mine.back));
+        if (serves && mine.lack > 0) takes = at.lack + mine.lack;  // later groups' are no less
+        if (gives) returns = at.back + mine.back;
     }
     if (status != 0) atomicOr(p.status, status);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) takes = max(takes, __shfl_xor_sync(kFull, takes, o)), returns = max(returns, __shfl_xor_sync(kFull, returns, o));
+    if ((tid & 31) == 0 && takes > 0) atomicMax(&taken, (unsigned long long)takes);
+    if ((tid & 31) == 0 && returns > 0) atomicMax(&returned, (unsigned long long)returns);
     __syncthreads();
     if (tid == 0) {
-        p.ends[0] = head, p.ends[1] = tail;
+        p.ends[0] = sound ? head % p.ring : 0, p.ends[1] = sound ? tail % p.ring : 0;
         p.queue_out[0] = head + (long long)taken;
         p.queue_out[1] = tail + (long long)returned;
     }
 }
 
-// Entry `at` past an end of the queue.
-__device__ __forceinline__ int ring_at(const ReserveParams& p, long long end, long long at) { return (int)((end + at) % p.ring); }
+// Entry `at` (below the ring's size) past an end of the queue, which is given by its entry.
+__device__ __forceinline__ int ring_at(const ReserveParams& p, long long end, long long at) {
+    return (int)(end + at < p.ring ? end + at : end + at - p.ring);
+}
 
 // Tables and queue of groups first, first + step, ..: a warp each.
 __device__ __forceinline__ void move_pages(const ReserveParams& p, long long head, long long tail, int first, int step) {
@@ -130,17 +157,43 @@ __device__ __forceinline__ void move_pages(const ReserveParams& p, long long hea
     }
 }
 
-// Positions and slots of rows first, first + step, .. below `end`.
+// The group of each lane's row, of rows that ascend: the last that starts at or
+// before it.  The warp looks for the first row's, 32 groups at a time spread over what is
+// left of them, and then over the 32 after it for all its rows; for the first row
+// that starts later yet it looks again.
+__device__ __forceinline__ int group_of(const ReserveParams& p, int row) {
+    const int lane = threadIdx.x & 31;
+    int base = 0, group = 0;
+    unsigned open = kFull;  // lanes without a group yet
+    while (open != 0) {
+        const int target = __shfl_sync(kFull, row, __ffs(open) - 1);
+        for (int over = p.G; over - base > 1;) {  // its group: one of base .. over - 1
+            const int step = (over - base + 31) / 32, mine = base + lane * step;
+            const unsigned upto = __ballot_sync(kFull, lane == 0 || (mine < over && p.indptr[mine] <= target));
+            base += (31 - __clz((int)upto)) * step;
+            over = base + step < over ? base + step : over;
+        }
+        const int next = base + 1 + lane, start = next < p.G ? p.indptr[next] : 0x7FFFFFFF;
+        int before = 0;  // starts at or before this lane's row
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            if (__shfl_sync(kFull, start, before + o - 1) <= row) before += o;
+        const bool all = __shfl_sync(kFull, start, 31) <= row;
+        if ((open >> lane & 1u) != 0 && !all) group = base + before;
+        open &= __ballot_sync(kFull, all);
+    }
+    return group;
+}
+
+// Positions and slots of rows first, first + step, .. below `end` (a warp's side by side).
 __device__ __forceinline__ void place_rows(const ReserveParams& p, long long head, long long first, long long end, int step) {
-    for (long long i = first; i < end; i += step) {
-        const int row = (int)i;
+    const int total = p.indptr[p.G];
+    for (long long i = first - (threadIdx.x & 31); i < end; i += step) {
+        const int row0 = (int)i, row = row0 + (threadIdx.x & 31);
         long long position = -1, slot = -1;
-        if (row < p.indptr[p.G]) {
-            int g = 0, over = p.G;  // the last group that starts at or before the row
-            while (over - g > 1) {
-                const int mid = (g + over) >> 1;
-                (p.indptr[mid] <= row ? g : over) = mid;
-            }
+        const int g = row0 < total ? group_of(p, row < total ? row : total - 1) : 0;
+        if (row >= end) continue;
+        if (row < total) {
             const Reserved r = p.groups[g];
             if (r.lens >= 0) {
                 const int token = r.lens + row - p.indptr[g], at = token >> p.page_shift;
@@ -177,13 +230,15 @@ __global__ void __launch_bounds__(kSumThreads) lp_reserve_kernel(const ReservePa
     }
 }
 
-__global__ void __launch_bounds__(kFillThreads) lp_reserve_fill_kernel(const ReserveParams p) {
+// The first row_blocks blocks place the rows, the others move the pages.
+__global__ void __launch_bounds__(kFillThreads) lp_reserve_fill_kernel(const ReserveParams p, int row_blocks) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const long long head = p.ends[0], tail = p.ends[1];
-    move_pages(p, head, tail, (int)((blockIdx.x * kFillThreads + threadIdx.x) >> 5), (int)(gridDim.x * (kFillThreads / 32)));
-    for (long long r0 = (long long)blockIdx.x * kFillRows; r0 < p.rows; r0 += (long long)gridDim.x * kFillRows) {
-        const long long end = r0 + kFillRows < p.rows ? r0 + kFillRows : p.rows;
-        place_rows(p, head, r0 + threadIdx.x, end, kFillThreads);
+    if ((int)blockIdx.x < row_blocks) {
+        place_rows(p, head, (long long)blockIdx.x * kFillThreads + threadIdx.x, p.rows, row_blocks * kFillThreads);
+    } else {
+        const int block = (int)blockIdx.x - row_blocks, blocks = (int)gridDim.x - row_blocks;
+        move_pages(p, head, tail, (int)((block * kFillThreads + threadIdx.x) >> 5), blocks * (kFillThreads / 32));
     }
 }
 
@@ -205,11 +260,16 @@ cudaError_t launch_reserve(const ReserveParams& p, int grid, cudaStream_t stream
     if (p.rows <= kAloneRows && p.G <= kAloneGroups) return cudaLaunchKernelEx(&lc, lp_reserve_kernel<true>, p);
     const cudaError_t e = cudaLaunchKernelEx(&lc, lp_reserve_kernel<false>, p);
     if (e != cudaSuccess) return e;
-    const long long by_rows = ((long long)p.rows + kFillRows - 1) / kFillRows, by_groups = ((long long)p.G * 32 + kFillThreads - 1) / kFillThreads;
-    const long long blocks = by_rows > by_groups ? by_rows : by_groups, most = (long long)grid * 8;
-    lc.gridDim = dim3((unsigned)(blocks < most ? (blocks > 0 ? blocks : 1) : most));
+    const long long most = (long long)grid * 8;
+    auto blocks = [&](long long threads) {
+        const long long n = (threads + kFillThreads - 1) / kFillThreads;
+        return (int)(n < most ? n : most);
+    };
+    const int row_blocks = blocks(p.rows), page_blocks = blocks((long long)p.G * 32);
+    if (row_blocks + page_blocks == 0) return cudaSuccess;
+    lc.gridDim = dim3((unsigned)(row_blocks + page_blocks));
     lc.blockDim = dim3(kFillThreads);
-    return cudaLaunchKernelEx(&lc, lp_reserve_fill_kernel, p);
+    return cudaLaunchKernelEx(&lc, lp_reserve_fill_kernel, p, row_blocks);
 }
 
 }  // namespace lp
