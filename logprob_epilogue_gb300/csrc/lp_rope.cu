@@ -60,16 +60,19 @@ struct Four {
     uint4 held;
 };
 
+// x to 2^-15 of itself, finite x.
+__device__ __forceinline__ float snap(float x) { return __uint_as_float((__float_as_uint(x) + 0x80u) & ~0xFFu); }
+
 // The scale and the codes are those of the exact quotients.  A tie of the scale
 // lies at max |x| = 6 m factor with m of five bits, a tie of a code at |x| = b
 // scale factor with b of three: products of at most 7 bits that FP32 holds, and
 // max |x| or |x|, of at most 11 bits itself, is one of them or at least 2^-11
-// away from it (relative).  The scale's quotient is divided with one rounding,
-// which is exact at a tie and crosses none elsewhere.  A lane's is a product
-// with the reciprocal, off by at most 2^-22; rounding that to 2^-15 brings it
-// back to a tie that it stands for and takes it over none.
+// away from it (relative).  Both quotients are products with a reciprocal (of 6,
+// rounded; of the scale, off by one unit in the last place at most), so off by less
+// than 2^-22; rounding them to 2^-15 brings each back to a tie that it stands
+// for and takes it over none.
 template <bool kBf16>
-__device__ __forceinline__ Four four_bits(const uint4& y, float factor) {
+__device__ __forceinline__ Four four_bits(const uint4& y, float factor, float inv, bool hold) {
     using H = Half<kBf16>;
     constexpr float kInf = __builtin_huge_valf();
     float x[8];
@@ -78,33 +81,34 @@ __device__ __forceinline__ Four four_bits(const uint4& y, float factor) {
 #pragma unroll
     for (int e = 1; e < 8; ++e) top = max_nan(top, fabsf(x[e]));
     top = max_nan(top, __shfl_xor_sync(kFull, top, 1));
-    if (top == kInf) top = __int_as_float(0x7FFFFFFF);  // an infinity has no scale: NaN for the block
-    const float inv = 1.0f / factor;                    // exact
-    uint16_t pair;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(pair) : "f"(0.0f), "f"(__fdiv_rn(top * inv, 6.0f)));
+    uint16_t pair;  // neither an infinity nor a NaN has a scale: NaN for the block
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(pair) : "f"(0.0f), "f"(top < kInf ? snap(top * inv * (1.0f / 6.0f)) : __int_as_float(0x7FFFFFFF)));
     uint32_t wide;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(wide) : "h"(pair));
     const float scale = Half<false>::unpack(wide).x;
-    const float r = scale > 0.0f ? __frcp_rn(scale) * inv : 0.0f;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(scale));
+    r = scale > 0.0f ? r * inv : 0.0f;
     Four f;
     f.scale = (unsigned char)(pair & 0xFFu);
-    f.codes = 0;
-    uint32_t held[4];
-    const float unit = scale * factor;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        float q[2];
+    for (int e = 0; e < 8; ++e) x[e] = snap(x[e] * r);
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(f.codes)
+        : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+    f.held = make_uint4(0u, 0u, 0u, 0u);
+    if (hold) {
+        uint32_t h[4];
+        widen_codes(f.codes, h);
+        const float unit = scale * factor;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) q[k] = __uint_as_float((__float_as_uint(x[2 * e + k] * r) + 0x80u) & ~0xFFu);
-        uint32_t code, two;
-        asm("{\n\t.reg .b8 c;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %2, %3;\n\tcvt.u32.u8 %0, c;\n\tcvt.rn.f16x2.e2m1x2 %1, c;\n\t}"
-            : "=r"(code), "=r"(two)
-            : "f"(q[1]), "f"(q[0]));
-        f.codes |= code << (8 * e);
-        const float2 v = Half<false>::unpack(two);
-        held[e] = H::pack(v.x * unit, v.y * unit);
+        for (int e = 0; e < 4; ++e) {
+            const float2 v = Half<false>::unpack(h[e]);
+            h[e] = H::pack(v.x * unit, v.y * unit);
+        }
+        f.held = make_uint4(h[0], h[1], h[2], h[3]);
     }
-    f.held = make_uint4(held[0], held[1], held[2], held[3]);
     return f;
 }
 
@@ -250,6 +254,8 @@ __global__ void __launch_bounds__(kRopeThreads, kHeads == 8 ? 6 : 8) lp_rope_ker
         if (kind == 2 && p.v_held != nullptr) held = reinterpret_cast<T*>(p.v_held) + row * p.v_held_stride + h0 * D + e0;
     }
     const bool stores = kCache == kFour && __any_sync(kFull, kind != 0);  // of the warp: a block's lanes lie in two threads
+    const float inv = 1.0f / factor;  // exact
+    const bool holds = p.k_held != nullptr || p.v_held != nullptr;
     const bool norms = p.q_weight != nullptr || p.k_weight != nullptr, turns = p.rot > 0 && !p.interleaved;  // of the call
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
@@ -292,7 +298,7 @@ __global__ void __launch_bounds__(kRopeThreads, kHeads == 8 ? 6 : 8) lp_rope_ker
         }
         if constexpr (kCache == kFour) {
             Four f = {};
-            if (stores) f = four_bits<kBf16>(y, factor);
+            if (stores) f = four_bits<kBf16>(y, factor, inv, holds);
             if (!work || i >= n) continue;
             if (codes != nullptr) {
                 *reinterpret_cast<uint32_t*>(codes + i * (step / 2)) = f.codes;
