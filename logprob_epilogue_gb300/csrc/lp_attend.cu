@@ -139,6 +139,8 @@ __device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigne
 // One row's running softmax: the maximum, what is subtracted in base 2, the sum.
 struct Row {
     float m, base, l;
+    float taken;  // F16 over a cache in 4 bits: the sum of the probabilities as the products take them; by it, not by l, the
+                  // results are divided, and what the rounding does to a row of few tokens cancels
 };
 
 // The maximum after scores up to `top`; f: what sums so far are worth under it.
@@ -152,7 +154,7 @@ __device__ __forceinline__ bool raise(Row& row, float top, bool first, bool used
     if (first) {
         row.m = top;
         row.base = top == kNegInf ? 0.0f : top * c - kBias;
-        row.l = 0.0f;
+        row.l = row.taken = 0.0f;
         return false;
     }
     const bool grow = used && (row.m == kNegInf ? top > row.m : top * c > row.m * c + kRescale);
@@ -162,6 +164,7 @@ __device__ __forceinline__ bool raise(Row& row, float top, bool first, bool used
         row.m = top;
         row.base = next;
         row.l *= f;
+        row.taken *= f;
     }
     return __any_sync(kFull, grow);
 }
@@ -211,7 +214,7 @@ __device__ __forceinline__ void mask_scores(uint32_t s_col, int valid) {
 
 // Softmax of one score tile by one warp, a row per thread; `valid` of the 128
 // tokens exist.  Writes the row's probabilities over the scores.
-template <bool kBf16, int D>
+template <bool kBf16, int D, bool kTaken>
 __device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, int valid, bool first, bool used, float c, Row& row, uint64_t* early) {
     if (valid < kKTile) mask_scores(s_col, valid);
     uint32_t r[4][32];
@@ -226,7 +229,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, int
     if (raise<kBf16>(row, top, first, used, c, f)) rescale<D>(o_col, f);
     const unsigned long long c2 = pack2(__float_as_uint(c), __float_as_uint(c));
     const unsigned long long nb2 = pack2(__float_as_uint(-row.base), __float_as_uint(-row.base));
-    unsigned long long sum[2] = {0, 0};
+    unsigned long long sum[2] = {0, 0}, taken[2] = {0, 0};
 #pragma unroll
     for (int b = 0; b < 4; ++b) {  // 32 scores to 16 words of probabilities
         uint32_t w[16];
@@ -238,6 +241,10 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, int
             y = ex2(y);
             sum[e & 1] = add2(sum[e & 1], pack2(__float_as_uint(x), __float_as_uint(y)));
             w[e] = Half<kBf16>::pack(x, y);
+            if constexpr (kTaken) {
+                const float2 f = Half<kBf16>::unpack(w[e]);
+                taken[e & 1] = add2(taken[e & 1], pack2(__float_as_uint(f.x), __float_as_uint(f.y)));
+            }
         }
         tc::tmem_st16(s_col + b * 16, w);
         if (b == kEarly / 32 - 1) {  // the products of the tile's first tokens may begin
@@ -250,6 +257,10 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_col, uint32_t o_col, int
     float x, y;
     unpack2(add2(sum[0], sum[1]), x, y);
     row.l += x + y;
+    if constexpr (kTaken) {
+        unpack2(add2(taken[0], taken[1]), x, y);
+        row.taken += x + y;
+    }
     tc::wait_st();
 }
 
@@ -436,7 +447,8 @@ __device__ __forceinline__ void attend(const AttendParams& p, const CUtensorMap*
     using T = typename Half<kBf16>::T;
     using C = Cfg<D, kFour>;
     using B = Block<kFour>;
-    constexpr bool kWide = kBf16 && !kFour;  // type of the products
+    constexpr bool kWide = kBf16 && !kFour;   // type of the products
+    constexpr bool kTaken = kFour && !kBf16;  // results divided by Row::taken: BF16 results are rounded by more than that gives
     extern __shared__ __align__(1024) unsigned char smem[];
     Ctl<kFour>* ctl = reinterpret_cast<Ctl<kFour>*>(smem + C::kCtl);
     unsigned char* ring = smem + 2 * C::kTileBytes;
@@ -536,7 +548,7 @@ __device__ __forceinline__ void attend(const AttendParams& p, const CUtensorMap*
                 if (lane == 0) tc::mbar_arrive(&ctl->q_full[b], 1);
             }
             q_pos += two ? 2 : 1;
-            Row st = {kNegInf, 0.0f, 0.0f};
+            Row st = {kNegInf, 0.0f, 0.0f, 0.0f};
             for (int i = first; i < n; i += stride) {
                 ok = tc::warp_wait(&ctl->s_full[wg], s_phase, limit, abort);
                 if (!ok) break;
@@ -552,7 +564,7 @@ __device__ __forceinline__ void attend(const AttendParams& p, const CUtensorMap*
                         if (i == first && used)
                             c = fminf(fmaxf(p.scale * kLog2e * p.k_factor * ctl->unit[(n_piece - 1) & 3u][two ? wg : 0][row], 0x1p-126f), 0x1p127f);
                     }
-                    softmax_tile<kWide, D>(s_col, o_col, x.left - i * kKTile, i == first, used, c, st, &ctl->p_early[wg]);
+                    softmax_tile<kWide, D, kTaken>(s_col, o_col, x.left - i * kKTile, i == first, used, c, st, &ctl->p_early[wg]);
                     tc::fence_before();
                     __syncwarp();
                 } else if (lane == 0) {
@@ -583,6 +595,11 @@ __device__ __forceinline__ void attend(const AttendParams& p, const CUtensorMap*
                     tc::wait_ld();
                     tc::tie(o);
                     if (store) {
+                        if constexpr (kTaken) {
+                            const float by = st.taken == 0.0f ? 1.0f : st.l / st.taken;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
+                        }
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
                             dst[(b * 8 + e) * x.part_stride] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),

@@ -86,6 +86,8 @@ __device__ __forceinline__ void mma0(float (&d)[4], uint32_t a0, uint32_t a1, ui
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
+constexpr uint32_t kOnes = 0x3C003C00u;  // two of F16
+
 // a where the mask is set, else b.
 __device__ __forceinline__ uint32_t select(uint32_t a, uint32_t b, uint32_t mask) { return (a & mask) | (b & ~mask); }
 
@@ -95,6 +97,9 @@ struct Rows {
     uint32_t q[kF][2][D / 8];  // lanes lane % 4 * D / 4 .. of each, as pairs of F16
     float o[kF][D / 8][4];  // fragment j: lanes (D / 8) (2t) + j and (D / 8) (2t + 1) + j of the first row, then of the second
     float c[kF][2], base[kF][2], limit[kF][2], l[kF][2];  // limit: -infinity until a score is above that
+    // the rows' sums of the probabilities as the products take them (a product with ones, so twice each): by these, not by l,
+    // the results are divided, and what the rounding does to a row of few tokens cancels
+    float taken[kF][4];
 };
 
 // The queries of a unit, by the helpers, to where a worker's thread has its part
@@ -157,6 +162,8 @@ __device__ __forceinline__ void take_rows(const AttendParams& p, const unsigned 
             r.limit[f][h] = kNegInf;
             r.base[f][h] = r.l[f][h] = 0.0f;
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r.taken[f][e] = 0.0f;
 #pragma unroll
         for (int j = 0; j < D / 8; ++j) r.o[f][j][0] = r.o[f][j][1] = r.o[f][j][2] = r.o[f][j][3] = 0.0f;
     }
@@ -224,6 +231,10 @@ __device__ __forceinline__ void products(const unsigned char* later, int next, f
         }
 #pragma unroll
         for (int b = 0; b < 2; ++b) ve[b] = widen_scales(ve[b]);
+    }
+    if constexpr (kValues) {
+#pragma unroll
+        for (int f = 0; f < kF; ++f) mma(r.taken[f], a[f][0], a[f][1], a[f][2], a[f][3], kOnes, kOnes);
     }
 #pragma unroll
     for (int i = 0; i < kK; ++i) {
@@ -300,6 +311,7 @@ __device__ __forceinline__ void raise(const float (&s)[kF][2][4], Rows<D, kF>& r
                     r.base[f][h] = next;
                     r.limit[f][h] = t + kRescale / r.c[f][h];
                     r.l[f][h] *= by[h];
+                    r.taken[f][2 * h] *= by[h];
                 }
             }
 #pragma unroll
@@ -443,12 +455,13 @@ __device__ __forceinline__ bool work_piece(const AttendParams& p, const Piece& x
             r.l[f][h] += __shfl_xor_sync(kFull, r.l[f][h], 1);
             r.l[f][h] += __shfl_xor_sync(kFull, r.l[f][h], 2);
             if ((lane & 3) == 0) ctl->ml[worker][(lane >> 2) + 8 * h] = make_float2(r.limit[f][h] == kNegInf ? kNegInf : r.base[f][h], r.l[f][h]);
+            const float by = r.taken[f][2 * h] == 0.0f ? 1.0f : r.l[f][h] / r.taken[f][2 * h];
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
                 for (int j = 0; j < D / 32; ++j)
-                    merge[((2 * h + e) * (D / 32) + j) * 32] =
-                        make_float4(r.o[f][4 * j][2 * h + e], r.o[f][4 * j + 1][2 * h + e], r.o[f][4 * j + 2][2 * h + e], r.o[f][4 * j + 3][2 * h + e]);
+                    merge[((2 * h + e) * (D / 32) + j) * 32] = make_float4(r.o[f][4 * j][2 * h + e] * by, r.o[f][4 * j + 1][2 * h + e] * by,
+                                                                           r.o[f][4 * j + 2][2 * h + e] * by, r.o[f][4 * j + 3][2 * h + e] * by);
         }
         arrive(&ctl->merge_full);
         ++line.merged;
