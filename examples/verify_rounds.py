@@ -18,12 +18,18 @@ through every call, its length stays negative, and its old page table, which
 names pages that other requests hold by now, is not written through.
 
 The drafts are what followed the same token the last time, so they are accepted
-as soon as the decoding repeats itself.  Run it on a GB300:
+as soon as the decoding repeats itself.
 
-    python examples/verify_rounds.py
+With ``kv_bits=4`` the cache is held in 4 bits (``append4``, ``attend4``), and
+``AttnPlan.reserve`` lays each round out on the device: a request takes pages from a
+queue of free ones as it grows, and the rows' positions follow from its length.
+The toy's logits then move by what 4 bits lose.  Run it on a GB300:
+
+    python examples/verify_rounds.py [--kv-bits 4]
 """
 from __future__ import annotations
 
+import argparse
 import os
 import sys
 
@@ -80,7 +86,7 @@ class Target:
         return (x + o.flatten(1) @ self.out.double()) @ self.head.double()
 
 
-def decode(target, prompt, firsts, rounds=24, drafts=3, page=16, idle=1):
+def decode(target, prompt, firsts, rounds=24, drafts=3, page=16, idle=1, kv_bits=16):
     """Decodes from each of ``firsts`` behind ``prompt``, with ``idle`` slots of the batch free: the emitted tokens of each
     request, the rounds' accepted drafts, and the slots' committed lengths."""
     dev = torch.device("cuda", torch.cuda.current_device())
@@ -89,27 +95,39 @@ def decode(target, prompt, firsts, rounds=24, drafts=3, page=16, idle=1):
     rows, prompt_pages = groups * rows_of, -(-m // page)
     max_pages = max(prompt_pages, -(-(rounds * rows_of) // page) + 1)
     num_pages = groups * max_pages + prompt_pages
-    shape = (num_pages, target.kv_heads, page, target.head_dim)
-    k_cache, v_cache = (torch.zeros(shape, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    four, shape = kv_bits == 4, (num_pages, target.kv_heads, page)
+    if four:
+        names = {"k_cache": (2, torch.uint8), "v_cache": (2, torch.uint8), "k_scales": (16, torch.float8_e4m3fn), "v_scales": (16, torch.float8_e4m3fn)}
+    else:
+        names = {"k_cache": (1, torch.bfloat16), "v_cache": (1, torch.bfloat16)}
+    caches = {name: torch.zeros(*shape, target.head_dim // lanes, dtype=dtype, device=dev) for name, (lanes, dtype) in names.items()}
     tables = i32(torch.arange(groups * max_pages).view(groups, max_pages))
     tables[requests:] = tables[0].clone()  # what a request that has left held belongs to another now
     prompt_table = i32([[groups * max_pages + i for i in range(prompt_pages)]])
     status = torch.zeros(1, dtype=torch.int32, device=dev)
     attention = lpe.AttnPlan(max_rows=rows, max_groups=groups, q_heads=target.q_heads, kv_heads=target.kv_heads,
                              head_dim=target.head_dim, page_size=page, num_pages=num_pages, max_pages=max_pages,
-                             max_group_rows=rows_of, max_prefixes=1, max_prefix_pages=prompt_pages, device=dev.index)
+                             max_group_rows=rows_of, max_prefixes=1, max_prefix_pages=prompt_pages, device=dev.index,
+                             kv_bits=kv_bits)
     epilogue = lpe.Plan(max_rows=rows, max_groups=groups, k_max=drafts, V=target.vocab, V_padded=target.vocab, dtype="bf16",
                         device=dev.index)
-    common = dict(k_cache=k_cache, v_cache=v_cache, status=status)
+    common = dict(status=status, **caches)
     rope = dict(cos_sin=target.cos_sin, q_weight=target.q_norm, k_weight=target.k_norm, eps=EPS)
 
     # the prompt's keys and values, once for all requests
     filler = lpe.AttnPlan(max_rows=m, max_groups=1, q_heads=target.q_heads, kv_heads=target.kv_heads, head_dim=target.head_dim,
-                          page_size=page, num_pages=num_pages, max_pages=prompt_pages, device=dev.index)
+                          page_size=page, num_pages=num_pages, max_pages=prompt_pages, device=dev.index, kv_bits=kv_bits)
     _, _, k, v = target.heads(torch.as_tensor(prompt, device=dev))
-    filler.append(k=k, v=v, group_indptr=i32([0, m]), lens=i32([0]), block_tables=prompt_table, positions=i32(range(m)), **rope, **common)
+    fill, append, attend = ((filler.append4, attention.append4, attention.attend4) if four else
+                            (filler.append, attention.append, attention.attend))
+    fill(k=k, v=v, group_indptr=i32([0, m]), lens=i32([0]), block_tables=prompt_table, positions=i32(range(m)), **rope, **common)
 
     indptr, lens = i32([g * rows_of for g in range(groups + 1)]), i32([0] * requests + [-1] * idle)
+    if four:  # all pages but the prompt's are free, and nobody holds any
+        tables, held, queue = i32([[-1] * max_pages] * groups), i32([0] * groups), torch.tensor([0, groups * max_pages], device=dev)
+        layout = dict(counts=i32([rows_of] * groups), starts=i32([m] * groups), held=held, held_out=held, queue=queue, queue_out=queue,
+                      free_pages=i32(range(groups * max_pages)), block_tables=tables, group_indptr=indptr, status=status,
+                      round_lens=i32([0] * groups), positions=i32([0] * rows))
     epilogue_io = dict(group_indptr=indptr, sampled_tokens=i32([-1] * groups), requested=i32([1] * groups), top_k=i32([5] * groups),
                        token_ids=i32([[-1] * lpe.MAX_IDS] * groups), id_counts=i32([0] * groups),
                        records=i32([[0] * lpe.RECORD_WORDS] * rows), accepted=i32([0] * groups), emitted_tokens=i32([0] * rows),
@@ -125,11 +143,14 @@ def decode(target, prompt, firsts, rounds=24, drafts=3, page=16, idle=1):
         block += [0] * (idle * rows_of)
         tokens = torch.tensor(block, device=dev)
         x, q, k, v = target.heads(tokens)
-        positions = (m + lens.clamp(min=0)[:, None] + torch.arange(rows_of, dtype=torch.int32, device=dev)).flatten()
-        attention.append(q=q, k=k, v=v, q_out=q_out, group_indptr=indptr, lens=lens, block_tables=tables, positions=positions,
-                         **rope, **common)
-        attention.attend(q=q_out, out=out, group_indptr=indptr, lens=lens, block_tables=tables, prefix_indptr=i32([0, groups]),
-                         prefix_lens=i32([m]), prefix_tables=prompt_table, **common)
+        if four:
+            attention.reserve(lens=lens, **layout)
+            positions, round_lens = layout["positions"], layout["round_lens"]
+        else:
+            positions, round_lens = (m + lens.clamp(min=0)[:, None] + torch.arange(rows_of, dtype=torch.int32, device=dev)).flatten(), lens
+        append(q=q, k=k, v=v, q_out=q_out, group_indptr=indptr, lens=round_lens, block_tables=tables, positions=positions, **rope, **common)
+        attend(q=q_out, out=out, group_indptr=indptr, lens=round_lens, block_tables=tables, prefix_indptr=i32([0, groups]),
+               prefix_lens=i32([m]), prefix_tables=prompt_table, **common)
         draft_tokens = i32([block[r + 1] if (r + 1) % rows_of else -1 for r in range(rows)])
         epilogue.bind(logits=target.logits(x, out), draft_tokens=draft_tokens, **epilogue_io)
         epilogue.run()
@@ -158,12 +179,12 @@ def shortfall(target, prompt, emitted):
     return worst
 
 
-def main():
+def main(kv_bits=16):
     if not torch.cuda.is_available():
         raise SystemExit("this example needs a CUDA device")
     target = Target()
     prompt = torch.randint(0, target.vocab, (100,), generator=torch.Generator().manual_seed(1)).tolist()
-    emitted, accepted, _ = decode(target, prompt, firsts=list(range(8)))
+    emitted, accepted, _ = decode(target, prompt, firsts=list(range(8)), kv_bits=kv_bits)
     tokens = sum(len(e) - 1 for e in emitted)
     print(f"{len(emitted)} requests, {len(accepted)} rounds: {tokens} tokens, {sum(map(sum, accepted))} of them accepted drafts")
     worst = shortfall(target, prompt, emitted)
@@ -172,4 +193,6 @@ def main():
 
 
 if __name__ == "__main__":
-    main()
+    parser = argparse.ArgumentParser(description="Speculative rounds of a toy target.")
+    parser.add_argument("--kv-bits", type=int, choices=(4, 16), default=16, help="bits of a cached key or value")
+    main(parser.parse_args().kv_bits)

@@ -769,3 +769,18 @@ def test_rounds_of_reserve_append4_attend4_commit():
         if step == 3:
             lens[1], lens[5] = -1, 0  # one leaves, one comes
     assert int(st[0]) == 0
+
+
+def test_the_example_decodes_over_a_cache_in_4_bits():
+    """It runs, every request grows by what was accepted, and free slots stay free."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "verify_rounds.py")
+    spec = importlib.util.spec_from_file_location("verify_rounds", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    target, prompt, firsts = example.Target(), list(range(3, 40)), [5, 6, 7]
+    for idle in (0, 1, 5):
+        emitted, accepted, lens = example.decode(target, prompt, firsts, rounds=8, idle=idle, kv_bits=4)
+        assert lens == [sum(a[g] + 1 for a in accepted) for g in range(3)] + [-1] * idle
+        assert all(len(e) == 1 + n for e, n in zip(emitted, lens))
