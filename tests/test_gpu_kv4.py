@@ -784,3 +784,60 @@ def test_the_example_decodes_over_a_cache_in_4_bits():
         emitted, accepted, lens = example.decode(target, prompt, firsts, rounds=8, idle=idle, kv_bits=4)
         assert lens == [sum(a[g] + 1 for a in accepted) for g in range(3)] + [-1] * idle
         assert all(len(e) == 1 + n for e, n in zip(emitted, lens))
+
+
+@pytest.mark.parametrize("groups", [900, 5000])
+def test_reserve_rows_among_groups_without_any(groups):
+    """Long runs of groups without rows before, between and after those that have some: neighbouring rows lie thousands of groups apart."""
+    r = np.random.RandomState(groups)
+    counts = np.zeros(groups, np.int64)
+    some = np.sort(r.choice(groups, 40, replace=False))
+    counts[some] = r.randint(1, 3, 40)
+    counts[some[7]] = 90
+    counts[some[8]] = 33
+    lens = r.randint(0, 30, groups)
+    lens[r.choice(groups, groups // 3, replace=False)] = -1
+    counts, lens = counts.tolist(), lens.tolist()
+    both_reserve(reserve_inputs(counts, lens, 8, seed=5), 8, sum(counts) + 37)
+
+
+def test_reserve_largest_counts_and_holdings_side_by_side():
+    """Warps full of groups with the largest counts: their sums pass 32 bits, what follows sits out and what is before them does not."""
+    groups, first = 2100, 1030
+    counts, lens = [1] * first + [2 ** 31 - 1] * 70 + [2] * (groups - first - 70), [3 + g % 9 for g in range(groups)]
+    x = reserve_inputs([1] * groups, lens, 8, seed=1, extra=1)
+    x["counts"] = counts
+    both_reserve(x, 8, first + 100)
+    x["held"][5] = x["held"][1200] = x["tables"].shape[1]
+    x["lens"][5] = x["lens"][1200] = -1  # idle groups with full tables
+    x["tables"][5] = x["tables"][1200] = np.arange(x["tables"].shape[1])
+    both_reserve(x, 8, first + 100)
+
+
+@pytest.mark.parametrize("dtype,d,hq", [("bf16", 64, 2), ("f16", 128, 2), ("bf16", 128, 3), ("f16", 64, 4)])
+def test_attend4_units_of_one_and_two_fragments_side_by_side(dtype, d, hq):
+    """Blocks that go through several units, of 16 rows and fewer and of more, whole ones and cut ones."""
+    r = np.random.RandomState(d + hq)
+    groups = 330
+    n, lens = r.randint(1, 32 // hq, groups).tolist(), r.randint(-1, 300, groups)
+    n[0] = 32 // hq
+    lens[r.choice(groups, 6, replace=False)] = r.randint(1000, 2500, 6)
+    Case4(dtype=dtype, d=d, hq=hq, hk=1, page=32, n=n, lens=lens.tolist()).check()
+
+
+@pytest.mark.parametrize("page", [16, 256])
+def test_attend4_pages_out_of_range_of_groups_of_many_rows(page):
+    """The same zeros where a group's rows take query tiles."""
+    import logprob_epilogue_gb300 as lpe
+    c = Case4(n=[12, 20], lens=[40, 300], page=page, fill=0.0, hq=8, hk=1)
+    at = 300 // page
+    for i in {0, at}:
+        for bad in (-1, c.pages, 2147483647):
+            tab = c.tables.copy()
+            tab[1, i] = bad
+            out, lse, st = c.run(block_tables=i32(tab))
+            assert st == lpe.STATUS_BAD_PAGE
+            kc, vc = c.kc.clone(), c.vc.clone()
+            kc[int(c.tables[1, i])] = 0
+            vc[int(c.tables[1, i])] = 0
+            R.check_attend(out, lse, R.attend(c.q, kc, vc, c.indptr, c.lens, c.tables, scale=c.scale), c.dtype)
