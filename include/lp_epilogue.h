@@ -693,8 +693,8 @@ int lp_kv_append4(lp_attn_t plan, const lp_append4_io* io, void* stream);
  * values that the cache stands for (any factor > 0).  A page out of range reads
  * as zeros.  The products take values and probabilities of 16 bits, in which
  * a code times its scale is exact; BF16 queries are first multiplied by a power
- * of two per row and head that brings their largest lane near 2^14 (undone in the
- * scores): a lane under 2^-28 of that largest one loses bits. */
+ * of two per row and head that brings their largest lane to [2^14, 2^15) (undone in
+ * the scores): a lane under 2^-28 of that largest one loses bits. */
 typedef struct {
     lp_attend_io attend;   /* k_cache, v_cache: the codes */
     const void* k_scales;

@@ -54,6 +54,15 @@
 //   come the groups' own tokens (0.5 GB) in 110, and the parts' join in 40;
 // - latency, in short calls: one row at 4,095 tokens takes 15.0 us: the launch and
 //   the split 2.5, the first scores 2.5, two token tiles 4, the join 5.5.
+//
+// Over a cache in 4 bits (lp_attend4 where many rows share a token) four more warps
+// expand codes into the ring of K and V tiles, 128 KiB then, and the products are F16.
+// They bound it: a quarter of a K or V tile takes a warp 1,540 cycles (560 to
+// convert and store it, 560 to fetch the next one's codes, the rest in waits), so the
+// prefix's part of 2,048 rows takes 800 us, 1.37 PFLOP/s.  Codes by bulk copies of warp 0 took
+// 174 us where these take 206 (19 groups of 12 rows and 16,384 tokens, pages of 256
+// tokens; 364 with pages of 16), bulk copies of each warp's own 220, loads into
+// registers one tile ahead 261; eight such warps leave the softmax too few registers.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

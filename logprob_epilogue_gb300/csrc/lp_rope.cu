@@ -22,6 +22,11 @@
 // per word).  16,411 rows of 32 + 8 + 8 heads of 128 lanes, BF16, into a cache:
 // 79 us, 6.0 TB/s; 8,191 rows of 24 + 4 heads of 64 lanes, F16: 13.0 us, 4.6
 // TB/s; one row into a cache: 3.2 us.
+//
+// Into a cache in 4 bits the instructions bound it, about 200 per word of keys and
+// values (284 with divided quotients, values as held always formed and four heads per task): 18,846 rows of 8 + 8 heads of
+// 128 lanes take 38.1 us, 4.6 TB/s with the values as held written beside the codes;
+// 512 rows 4.6 us, one row 3.1 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -285,7 +290,7 @@ __global__ void __launch_bounds__(kRopeThreads, kHeads == 8 ? 6 : 8) lp_rope_ker
             if (!work || i >= n) continue;
         }
         uint4 y = w[i];  // values go as they are
-        if (kind != 2) {
+        if (kind != 2 && (kCache != kFour || norms || p.rot > 0)) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float z = x[e] * fa[e];
@@ -334,13 +339,16 @@ cudaError_t launch(const RopeParams& p, cudaStream_t stream) {
 // Eight heads per task spread a row's factors further, but leave a short call
 // fewer threads and a long chain of its own: with 128 lanes, 16,411 rows of 48
 // heads take 79 us against 82, 512 rows 5.0 us against 4.4; with 64 lanes 8,191
-// rows of 28 heads take 14.8 us against 13.0.
+// rows of 28 heads take 14.8 us against 13.0.  In 4 bits a task's lanes cost more beside
+// its factors: 18,846 rows of 8 heads of keys take 38.1 us against 40.4, 512 rows 5.9
+// against 4.6.
 constexpr long long kManyHeads = 1 << 18;
 
 template <bool kBf16>
 cudaError_t pick(const RopeParams& p, int head_dim, cudaStream_t stream) {
     if (head_dim == 64) return launch<kBf16, 64, 4>(p, stream);
-    return (long long)p.rows * (p.q_heads + p.kv_heads) >= kManyHeads ? launch<kBf16, 128, 8>(p, stream) : launch<kBf16, 128, 4>(p, stream);
+    const long long many = p.k_scales == nullptr ? kManyHeads : kManyHeads / 2;
+    return (long long)p.rows * (p.q_heads + p.kv_heads) >= many ? launch<kBf16, 128, 8>(p, stream) : launch<kBf16, 128, 4>(p, stream);
 }
 
 }  // namespace
