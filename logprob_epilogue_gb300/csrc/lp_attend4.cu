@@ -11,7 +11,7 @@
 // tcgen05 takes has to lie in shared or tensor memory first, and with so few
 // rows the codes' way there costs more than the products that it saves (measured
 // with keys expanded into tensor memory and values into shared memory by eight
-// warps: 238 us where this takes 193, and 20.6 us for one token where this takes 15.3).
+// warps: 238 us where this takes 191, and 20.6 us for one token where this takes 14.4).
 //
 // Block (one per SM, 12 warps): warp 0 splits the work, warps 0 and 3 bring every
 // other tile of 128 tokens into a ring (144 KiB) by bulk copies, four per page;
@@ -23,7 +23,7 @@
 // sums, results and parts are 32 bits.
 //
 // What bounds it, by size (BF16, heads of 128, 32 over 8, in a CUDA graph):
-// - the workers' instructions: 128 groups of 4 rows at contexts up to 8,192 take 192
+// - the workers' instructions: 128 groups of 4 rows at contexts up to 8,192 take 191
 //   us, 3.3 TB/s of codes and scales.  A tile of one fragment takes 1,480 cycles of a
 //   block, 1,200 where the tiles are there already; at the rates of their pipes the
 //   conversions and their products with the scales take 760, and beside them the
@@ -34,8 +34,8 @@
 // - pages of few tokens: a bulk copy takes its warp about 100 cycles, so pages of
 //   8 tokens take 197 us there, 16 137, 32 113, 64 and more 109 (copies of 16 bytes a
 //   lane: 161, 159, 138, 138).
-// - latency: one row at 4,095 tokens takes 15.0 us, the launch, the split and the first
-//   pages 8, a tile or two 2, the join 5.
+// - latency: one row at 4,095 tokens takes 14.4 us, the launch, the split and the first
+//   pages 8, a tile or two 2, the join 4.5.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -130,7 +130,6 @@ lp::AttendScratch place(const Layout& L, unsigned char* base) {
     sc.part_o = reinterpret_cast<float*>(base + L.part_o);
     sc.prefix_slots = L.prefix_slots;
     sc.group_slots = L.group_slots;
-    sc.prefix_rows = L.prefix_rows;
     sc.group_rows = L.group_rows;
     return sc;
 }

@@ -75,7 +75,7 @@ struct AttendScratch {
     float* part_o;                  // pieces of prefixes, then of groups: unnormalised results [2][rows][D]
     float2* part_ml;                // (maximum in base 2, sum) [2][rows]
     long long prefix_slots, group_slots;
-    int prefix_rows, group_rows;    // rows per tile in a prefix slot and in a group slot
+    int group_rows;                 // rows per tile in a group slot
 };
 
 struct AttendParams {

@@ -38,6 +38,7 @@ struct Pairs {
     static constexpr bool kPairs = true;
     static constexpr int kSets = 2, kTileCost = 2, kPairCost = 3, kUnitCost = 4;
     static constexpr int kMostCost = kPairCost;  // of a tile
+    static constexpr int kPrefixRows = kQTile;   // of a part of a prefix
     static __device__ __forceinline__ int unit_rows(const AttendParams& p) { return 2 * p.rows_per_tile; }
     static __device__ __forceinline__ int cost(const AttendParams& p, int n) { return n > p.rows_per_tile ? kPairCost : kTileCost; }
     static __device__ __forceinline__ const AttendScratch& scratch(const AttendParams& p) { return p.sc; }
@@ -55,7 +56,7 @@ struct Pairs4 : Pairs {
 // every unit 5 more.
 struct Fragments {
     static constexpr bool kPairs = false;
-    static constexpr int kSets = 1, kUnitCost = 5, kTileCost = 2, kMostCost = 4;
+    static constexpr int kSets = 1, kUnitCost = 5, kTileCost = 2, kMostCost = 4, kPrefixRows = kUnitRows;
     static __device__ __forceinline__ int unit_rows(const AttendParams& p) { return p.rows_per_unit; }
     static __device__ __forceinline__ int cost(const AttendParams& p, int n) {
         return (n < p.rows_per_unit ? n : p.rows_per_unit) * p.share > 16 ? p.two_cost : kTileCost;
@@ -172,9 +173,9 @@ __device__ __forceinline__ Runs make_runs(unsigned long long total, int grid, in
 template <class Rule>
 __device__ __forceinline__ long long part_row(const AttendParams& p, bool prefix, long long slot, int set) {
     const AttendScratch& sc = Rule::scratch(p);
-    if (prefix) return slot < sc.prefix_slots ? (slot * Rule::kSets + set) * sc.prefix_rows : -1;
+    if (prefix) return slot < sc.prefix_slots ? (slot * Rule::kSets + set) * Rule::kPrefixRows : -1;
     if (slot >= sc.group_slots) return -1;
-    return sc.prefix_slots * Rule::kSets * sc.prefix_rows + (slot * Rule::kSets + set) * sc.group_rows;
+    return sc.prefix_slots * Rule::kSets * Rule::kPrefixRows + (slot * Rule::kSets + set) * sc.group_rows;
 }
 
 // Where a unit that is not dealt out is entered for the join; -1 as above.
@@ -239,7 +240,7 @@ struct Walk {
         table = prefix ? p.prefix_tables + (long long)sg * p.max_prefix_pages : p.tables + (long long)(sg - p.P) * p.max_pages;
         token = (long long)t0 * kKTile;
         x.part = part_row<Rule>(p, prefix, slot, 0);
-        x.part_stride = prefix ? Rule::scratch(p).prefix_rows : Rule::scratch(p).group_rows;
+        x.part_stride = prefix ? Rule::kPrefixRows : Rule::scratch(p).group_rows;
     }
     __device__ __forceinline__ bool next(const AttendParams& p, Piece& x) {
         while (deal < deal_end) {
