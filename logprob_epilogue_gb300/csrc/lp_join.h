@@ -17,8 +17,6 @@
 #include "lp_split.h"
 #include "lp_tc.h"
 
-// Unnamed: the same join with external linkage, instruction for instruction as many, took 1 to 3 us more a call (one
-// row at 4,095 tokens: 17.1 us against 15.4); the cause was not found.
 namespace lp {
 namespace {
 
@@ -142,10 +140,11 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
     using H = Half<kBf16>;
     using T = typename H::T;
     constexpr int kE = D / 8, kRuns = D / 64, kRound = join_round(kSub);
-    // what is on its way to a warp, 16 bytes of every thread side by side
-    extern __shared__ __align__(16) unsigned char smem[];
-    uint4* stage = reinterpret_cast<uint4*>(smem) + threadIdx.x;
-    float2* stage_ml = reinterpret_cast<float2*>(smem + kRound * 2 * kRuns * kJoinThreads * 16) + threadIdx.x;
+    // What is on its way to a warp, 16 bytes of every thread side by side: on lines of 128 bytes (one row at 4,095 tokens:
+    // 15.3 us; wherever the words before it end, 17.1).
+    extern __shared__ __align__(128) unsigned char join_smem[];
+    uint4* stage = reinterpret_cast<uint4*>(join_smem) + threadIdx.x;
+    float2* stage_ml = reinterpret_cast<float2*>(join_smem + kRound * 2 * kRuns * kJoinThreads * 16) + threadIdx.x;
     auto place = [](int h, int c) { return h * 8 + (c ^ 2 * h); };
     auto staged = [&](int b, int c) -> uint4& { return stage[(b * 2 * kRuns + c) * kJoinThreads]; };
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % kSub, l = lane >> 2;
@@ -323,7 +322,7 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
         a.add(ml.x, ml.y, v);
     }
     if constexpr (kSub > 1) {  // the warps' sums, in the order of the warps
-        float* part = reinterpret_cast<float*>(smem);  // [e][thread]; then the maxima and sums
+        float* part = reinterpret_cast<float*>(join_smem);  // [e][thread]; then the maxima and sums
         float2* part_ml = reinterpret_cast<float2*>(part + kE * kJoinThreads);
         gave_up = __syncthreads_or(gave_up);
 #pragma unroll
