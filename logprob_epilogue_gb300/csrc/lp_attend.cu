@@ -531,7 +531,7 @@ __device__ __forceinline__ void attend(const AttendParams& p, const CUtensorMap*
         const int wg = (warp - 4) >> 2, quarter = warp & 3;  // tensor tile; lanes 32 * quarter of tensor memory
         const uint32_t lanes = (uint32_t)quarter << 21;
         const uint32_t s_col = tmem + lanes + kColS + wg * kColStep, o_col = tmem + lanes + kColO + wg * kColStep;
-        float c = p.scale * kLog2e * (kFour ? p.k_factor : 1.0f);
+        float c = kFour ? scaled(p.score, p.score_exp) : p.scale * kLog2e;
         uint32_t s_phase = 0, pv_phase = 0, q_pos = 0, grant = 0, tile = 0;  // tile: tiles of the run before the piece
         int turn = 0;
         while (ok && next_piece()) {
@@ -569,9 +569,7 @@ __device__ __forceinline__ void attend(const AttendParams& p, const CUtensorMap*
                 if (live) {
                     tc::fence_after();
                     if constexpr (kFour && kBf16) {
-                        // finite and above 0, so that a masked score stays -infinity and one of 0 stays 0
-                        if (i == first && used)
-                            c = fminf(fmaxf(p.scale * kLog2e * p.k_factor * ctl->unit[(n_piece - 1) & 3u][two ? wg : 0][row], 0x1p-126f), 0x1p127f);
+                        if (i == first && used) c = scaled(p.score, p.score_exp + exponent_of(ctl->unit[(n_piece - 1) & 3u][two ? wg : 0][row]));
                     }
                     softmax_tile<kWide, D, kTaken>(s_col, o_col, x.left - i * kKTile, i == first, used, c, st, &ctl->p_early[wg]);
                     tc::fence_before();

@@ -175,8 +175,7 @@ __device__ __forceinline__ void take_rows(const AttendParams& p, const unsigned 
                 const uint4 w = reinterpret_cast<const uint4*>(from)[((f * 2 + h) * (D / 32) + i) * 32 + lane];
                 r.q[f][h][i * 4] = w.x, r.q[f][h][i * 4 + 1] = w.y, r.q[f][h][i * 4 + 2] = w.z, r.q[f][h][i * 4 + 3] = w.w;
             }
-            // finite and above 0, so that a masked score stays -infinity and one of 0 stays 0
-            r.c[f][h] = fminf(fmaxf(p.scale * kLog2e * p.k_factor * (kBf16 ? unit[f * 16 + h * 8 + (lane >> 2)] : 1.0f), 0x1p-126f), 0x1p127f);
+            r.c[f][h] = scaled(p.score, p.score_exp + (kBf16 ? exponent_of(unit[f * 16 + h * 8 + (lane >> 2)]) : 0));
             r.limit[f][h] = kNegInf;
             r.base[f][h] = r.l[f][h] = 0.0f;
         }

@@ -253,6 +253,13 @@ bool power_of_two(float f) {
     return std::isfinite(f) && std::frexp(f, &e) == 0.5f && e >= -59 && e <= 61;
 }
 
+// scale log2(e) factor: either product may leave FP32's range where queries bring the scores back.
+void split_score(float scale, float factor, lp::AttendParams& p) {
+    int a, b, c, d;
+    const float base2 = std::frexp(std::frexp(scale, &a) * 1.4426950408889634f, &b);
+    p.score = 2.0f * std::frexp(base2 * std::frexp(factor, &c), &d);
+    p.score_exp = a + b + c + d - 1;
+}
 
 // Neither rows nor groups: a call that does nothing.
 bool nothing_to_attend(const lp_attend_io& io) { return io.rows == 0 || io.groups == 0; }
@@ -495,7 +502,7 @@ int lp_attend4(lp_attn_t plan, const lp_attend4_io* io, void* stream) {
     lp::AttendParams p = attend_params(plan, &io->attend);
     p.k_scales = static_cast<const unsigned char*>(io->k_scales);
     p.v_scales = static_cast<const unsigned char*>(io->v_scales);
-    p.k_factor = io->k_factor;
+    split_score(io->attend.scale, io->k_factor, p);
     p.v_factor = io->v_factor;
     p.fragments = plan->fragments;
     p.rows_per_unit = lp::kUnitRows / p.share;

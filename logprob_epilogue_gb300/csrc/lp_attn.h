@@ -101,7 +101,9 @@ struct AttendParams {
     int force_timeout;
     // a cache of 4 bits; k_cache, v_cache: the codes
     const unsigned char *k_scales, *v_scales;
-    float k_factor, v_factor;
+    float score;           // scale log2(e) k_factor = score 2^score_exp, 1 <= score < 2
+    int score_exp;
+    float v_factor;
     int wide;              // segments whose units are pairs of tiles: kWidePrefixes, kWideGroups; the others' are fragments
     AttendScratch fragments;  // of those
     int two_cost;             // of those with two fragments: of a token tile, see Fragments

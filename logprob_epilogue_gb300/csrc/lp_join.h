@@ -166,7 +166,6 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
         for (int r = 0; r < kRuns; ++r)
             widen8<kBf16>(*reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.q) + row * p.q_stride +
                                                           (long long)(exists ? head : 0) * D + r * 64 + l * 8), q + r * 8);
-        const float c = p.scale * kLog2e;
         const int j = row - grp.r0;
         const unsigned mask = p.row_masks != nullptr ? p.row_masks[row] : (2u << j) - 1u;
         int page = 0;  // lane i: of token i
@@ -180,7 +179,8 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
             // A thread's lanes of a token are kRuns words of codes, each of one block, of K and of V: few enough to load two
             // tokens' at once into registers.
             const int kvh = exists ? head / p.share : 0;
-            const float ck = c * p.k_factor;
+            // in two factors: what the first one, kept to FP32's normal numbers, lacks (1, as a rule) is the second
+            const float ck = scaled(p.score, p.score_exp), more = scaled(1.0f, p.score_exp - exponent_of(ck));
 #pragma unroll 1
             for (int j = 0; j < n; j += 2) {
                 uint32_t w[2][2][kRuns], e[2][2][kRuns];
@@ -212,10 +212,11 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
                     for (int i = 0; i < kE; ++i) s = fmaf(q[i], k[i], s);
 #pragma unroll
                     for (int o = 16; o > 2; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-                    a.add(s * ck, 1.0f, v);
+                    a.add(s * ck * more, 1.0f, v);
                 }
             }
         } else {
+            const float c = p.scale * kLog2e;
             // Keys and values lie side by side along a head, so here neighbouring threads copy along a head (to the places of the
             // threads that read them, turned so that a read meets every bank once).
             const int copy_head = head - (lane & 3) + (lane >> 3), copy_kvh = copy_head < p.q_heads ? copy_head / p.share : 0;

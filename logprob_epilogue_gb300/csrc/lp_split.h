@@ -30,6 +30,16 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
+// m 2^e, 1 <= m < 2, with e kept to FP32's normal numbers: finite and above 0, so that as a factor it leaves a masked
+// score at -infinity and one of 0 at 0.
+__device__ __forceinline__ float scaled(float m, int e) {
+    e = e < -126 ? -126 : (e > 127 ? 127 : e);
+    return m * __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+// The exponent of a positive normal number.
+__device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
+
 // Units of up to two tiles of 128 query rows: a piece leaves a part for each
 // tile, or for each warpgroup where the unit is one tile.  What a run is
 // measured in, by the times of each: a token tile of a one-tile unit is 2, of a
