@@ -346,16 +346,17 @@ __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_joi
         for (int e = 0; e < kE; ++e) a.o[e] = 0.0f;
         a.m = kNegInf, a.l = 0.0f;
     }
-    float inv = a.l > 0.0f ? 1.0f / a.l : (a.l == 0.0f ? 0.0f : a.l);
-    if constexpr (kFour) inv *= p.v_factor;
+    const float inv = a.l > 0.0f ? 1.0f / a.l : (a.l == 0.0f ? 0.0f : a.l);
+    // the factor last: a small one, divided by the sum, would lose bits below FP32's normal numbers
+    auto lane_of = [&](int e) { return kFour ? a.o[e] * inv * p.v_factor : a.o[e] * inv; };
     T* dst = reinterpret_cast<T*>(p.out) + row * p.out_stride + (long long)head * D + l * 8;
 #pragma unroll
     for (int r = 0; r < kRuns; ++r) {
         uint4 w;
-        w.x = H::pack(a.o[r * 8] * inv, a.o[r * 8 + 1] * inv);
-        w.y = H::pack(a.o[r * 8 + 2] * inv, a.o[r * 8 + 3] * inv);
-        w.z = H::pack(a.o[r * 8 + 4] * inv, a.o[r * 8 + 5] * inv);
-        w.w = H::pack(a.o[r * 8 + 6] * inv, a.o[r * 8 + 7] * inv);
+        w.x = H::pack(lane_of(r * 8), lane_of(r * 8 + 1));
+        w.y = H::pack(lane_of(r * 8 + 2), lane_of(r * 8 + 3));
+        w.z = H::pack(lane_of(r * 8 + 4), lane_of(r * 8 + 5));
+        w.w = H::pack(lane_of(r * 8 + 6), lane_of(r * 8 + 7));
         *reinterpret_cast<uint4*>(dst + r * 64) = w;
     }
     if (p.lse_out != nullptr && l == 0) p.lse_out[(long long)row * p.q_heads + head] = a.l == 0.0f ? kNegInf : a.m * kLn2 + logf(a.l);

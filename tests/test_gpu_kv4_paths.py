@@ -75,3 +75,17 @@ def test_attend4_factors_that_bring_one_another_back(size, scale, factor, n, hq)
     c.scale = scale
     restate(c, factor, 1.0)
     check(c)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64)])
+@pytest.mark.parametrize("n,hq", [([2], 4), ([12], 8)])
+@pytest.mark.parametrize("factor", [2.0 ** -126, 2.0 ** -128, 2.0 ** -131, 2.0 ** 116])
+def test_attend4_values_under_a_factor_at_the_ends_of_the_range(dtype, d, n, hq, factor):
+    """Values of 2,688 factor, which BF16 holds: the factor alone, divided by the sum of 5,000 probabilities, would leave FP32's normal numbers."""
+    import torch
+    c = Case4(dtype=dtype, d=d, hq=hq, hk=1, n=n, lens=[5001])
+    c.raw[1][~c.raw[1].isnan()] = 2688.0
+    c.quantise()
+    restate(c, 1.0, factor)
+    out, _ = check(c)
+    assert torch.equal(out.double(), torch.full_like(out, 2688.0 * factor).double())
