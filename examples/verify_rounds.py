@@ -22,7 +22,8 @@ as soon as the decoding repeats itself.
 
 With ``kv_bits=4`` the cache is held in 4 bits (``append4``, ``attend4``), and
 ``AttnPlan.reserve`` lays each round out on the device: a request takes pages from a
-queue of free ones as it grows, and the rows' positions follow from its length.
+queue of free ones as it grows, and the rows' positions follow from its length.  A
+request that gets none sits the round out.
 The toy's logits then move by what 4 bits lose.  Run it on a GB300:
 
     python examples/verify_rounds.py [--kv-bits 4]
@@ -86,9 +87,10 @@ class Target:
         return (x + o.flatten(1) @ self.out.double()) @ self.head.double()
 
 
-def decode(target, prompt, firsts, rounds=24, drafts=3, page=16, idle=1, kv_bits=16):
+def decode(target, prompt, firsts, rounds=24, drafts=3, page=16, idle=1, kv_bits=16, free=None):
     """Decodes from each of ``firsts`` behind ``prompt``, with ``idle`` slots of the batch free: the emitted tokens of each
-    request, the rounds' accepted drafts, and the slots' committed lengths."""
+    request, the rounds' accepted drafts (-1: the request sat out), and the slots' committed lengths.  ``free``: pages that 4
+    bits find in the queue (as many as all slots need unless given)."""
     dev = torch.device("cuda", torch.cuda.current_device())
     i32 = lambda x: torch.as_tensor(x, dtype=torch.int32, device=dev)  # noqa: E731
     requests, groups, rows_of, m = len(firsts), len(firsts) + idle, drafts + 1, len(prompt)
@@ -124,7 +126,7 @@ def decode(target, prompt, firsts, rounds=24, drafts=3, page=16, idle=1, kv_bits
 
     indptr, lens = i32([g * rows_of for g in range(groups + 1)]), i32([0] * requests + [-1] * idle)
     if four:  # all pages but the prompt's are free, and nobody holds any
-        tables, held, queue = i32([[-1] * max_pages] * groups), i32([0] * groups), torch.tensor([0, groups * max_pages], device=dev)
+        tables, held, queue = i32([[-1] * max_pages] * groups), i32([0] * groups), torch.tensor([0, groups * max_pages if free is None else free], device=dev)
         layout = dict(counts=i32([rows_of] * groups), starts=i32([m] * groups), held=held, held_out=held, queue=queue, queue_out=queue,
                       free_pages=i32(range(groups * max_pages)), block_tables=tables, group_indptr=indptr, status=status,
                       round_lens=i32([0] * groups), positions=i32([0] * rows))
@@ -154,15 +156,16 @@ def decode(target, prompt, firsts, rounds=24, drafts=3, page=16, idle=1, kv_bits
         draft_tokens = i32([block[r + 1] if (r + 1) % rows_of else -1 for r in range(rows)])
         epilogue.bind(logits=target.logits(x, out), draft_tokens=draft_tokens, **epilogue_io)
         epilogue.run()
-        lens += torch.where(lens < 0, 0, epilogue_io["accepted"] + 1)
-        accepted, new = epilogue_io["accepted"][:requests].tolist(), epilogue_io["emitted_tokens"].view(groups, rows_of).tolist()
+        took_part = torch.where(round_lens < 0, -1, epilogue_io["accepted"])
+        lens += took_part + 1
+        accepted, new = took_part[:requests].tolist(), epilogue_io["emitted_tokens"].view(groups, rows_of).tolist()
         for g, a in enumerate(accepted):
             for t in new[g][:a + 1]:
                 followed[emitted[g][-1]] = t
                 emitted[g].append(t)
         accepted_of.append(accepted)
     for name, word in (("attention", status), ("epilogue", epilogue_io["status"])):
-        if int(word) != 0:
+        if int(word) & ~lpe.STATUS_NO_PAGES:
             raise RuntimeError(f"{name}: status {int(word):#x}")
     for plan in (attention, filler, epilogue):
         plan.close()

@@ -440,15 +440,15 @@ int lp_run_static(const lp_plan_desc* desc, const lp_io* io, void* stream);
  * lens[g] + j.  lp_kv_append writes those tokens and lp_attend reads them;
  * neither changes lens.  lens[g] < 0 marks an idle group (a slot of a captured
  * batch without a request; it may still own rows).  After the epilogue the
- * caller commits the round with lens[g] += accepted[g] + 1 where lens[g] >= 0:
- * tokens past lens are never read as committed, and the next append overwrites
- * them.  The epilogue knows nothing of lens and accepts for an idle group's
- * rows as for any others: its lens stays as it is, or the next append would
- * write through the slot's old page table.  That rule is for chains of drafts,
- * which are what the epilogue accepts.  Of a tree (row_masks) the accepted
- * branch need not be the group's first rows: whoever accepts it appends the
- * keys and values of its rows again, in the branch's order and at the same
- * lens, and then adds their number to lens.
+ * caller commits the round with lens[g] += accepted[g] + 1 where the lens that
+ * the round's calls were given is >= 0: tokens past lens are never read as
+ * committed, and the next append overwrites them.  The epilogue knows nothing
+ * of lens and accepts for an idle group's rows as for any others: its lens stays
+ * as it is, or the next append would write through the slot's old page table.
+ * That rule is for chains of drafts, which are what the epilogue accepts.  Of a
+ * tree (row_masks) the accepted branch need not be the group's first rows:
+ * whoever accepts it appends the keys and values of its rows again, in the
+ * branch's order and at the same lens, and then adds their number to lens.
  *
  * Cache.  k_cache and v_cache are [num_pages, kv_heads, page_size, head_dim]
  * each; token t of group g is slot t % page_size of page
@@ -614,7 +614,10 @@ int lp_attend(lp_attn_t plan, const lp_attend_io* io, void* stream);
  *   idle groups    the pages they hold join the tail in the order of the groups
  *                  and of their tables; the groups of this call get none of them.
  *   round_lens     the lens of the round's other calls: lens[g], or -1 for a
- *                  group without its pages, which so sits the round out.
+ *                  group without its pages, which so sits the round out.  Commit
+ *                  by it: lens[g] += accepted[g] + 1 where round_lens[g] >= 0.
+ *                  The epilogue accepts for the rows of a group that sat out as
+ *                  for any others, and what it emits for them is of no use.
  *   held_out, queue_out  held and queue after the call.  They may be held and
  *                  queue themselves; where they are not, the call can be made
  *                  again with the same outcome (its writes to block_tables and

@@ -102,7 +102,8 @@ class AttnPlan:
 
     ``lens`` counts each group's committed tokens, negative for an idle group,
     and is changed by none of the calls: after the epilogue, ``lens +=
-    torch.where(lens < 0, 0, accepted + 1)`` commits the round.  Every call only
+    torch.where(lens < 0, 0, accepted + 1)`` commits the round (``round_lens < 0``
+    after ``reserve``, whose groups without pages sit out).  Every call only
     enqueues on ``stream`` (default: torch's current stream) and ORs its status
     bits into ``status`` without resetting it.  Like a ``Plan``, one plan serves
     one stream, and one thread, at a time."""
@@ -339,7 +340,8 @@ class AttnPlan:
         ``held[g]`` of ``block_tables[g]`` from the queue of free pages (int64
         ``queue`` = [head, tail] into the ring ``free_pages``), and idle groups
         (``lens`` < 0) give theirs back.  ``round_lens`` are the lens for the
-        round's other calls (-1 where the pages ran out), ``positions`` and the
+        round's other calls and for its commit (-1 where the pages ran out: that
+        group sits the round out, and its ``lens`` stays), ``positions`` and the
         int64 ``slots`` those of every row (-1: padding); their length is the
         batch's rows.  ``held_out`` and ``queue_out`` may be ``held`` and
         ``queue``."""

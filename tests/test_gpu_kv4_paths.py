@@ -431,3 +431,33 @@ def test_reserve_long_requests_that_leave_and_come(groups):
     x["tables"] = tables
     both_reserve(x, page, sum(counts) + 3)
     both_reserve(x, page, sum(counts), inplace=True)
+
+
+def example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "verify_rounds.py")
+    spec = importlib.util.spec_from_file_location("verify_rounds", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+@pytest.mark.parametrize("free", [0, 1, 3, 4, 5])
+def test_rounds_whose_pages_run_out(free):
+    """A request without pages keeps its length and emits nothing; the others' lengths stay within the pages that they hold."""
+    e = example()
+    page, drafts, rounds = 16, 3, 24
+    emitted, accepted, lens = e.decode(e.Target(), list(range(3, 40)), [5, 6, 7], rounds=rounds, drafts=drafts, page=page, idle=1, kv_bits=4, free=free)
+    held, want, left = [0, 0, 0], [0, 0, 0], free
+    for a in accepted:
+        short = False  # groups in order; from the first that the rest does not cover, those that lack pages get none
+        for g in range(3):
+            lack = -(-(want[g] + drafts + 1) // page) - held[g]
+            short |= lack > left
+            served = lack == 0 or not short
+            assert (a[g] >= 0) == served, (a, g)
+            if served:
+                held[g], left, want[g] = held[g] + lack, left - lack, want[g] + a[g] + 1
+    assert lens == want + [-1] and any(-1 in a for a in accepted)
+    assert [len(x) for x in emitted] == [1 + n for n in want]
