@@ -19,7 +19,10 @@
 // sums 2, then two dependent reads per row).  4,099 groups of one row: 14.5 us, 11 of them
 // the one block's five times 1,024 groups (2 us each; eight consecutive groups
 // per thread took longer, 20: a block's writes then go out 32 bytes apart).  37 prompts,
-// 638,367 rows: 11.2 us, the rows' 7.7 MB beside four dependent reads.
+// 638,367 rows: 11.2 us, the rows' 7.7 MB beside four dependent reads.  A group's pages
+// are one warp's, 32 at a time, each time a read and then a write: beside 127 groups of 4
+// rows one that gives 512 pages back takes 7.9 us, 2,048 15, 8,192 45, one that takes
+// 8,192 new ones 48; 128 that give 8,192 each 170, all in one block.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -246,8 +249,12 @@ __global__ void __launch_bounds__(kFillThreads) lp_reserve_fill_kernel(const Res
     }
 }
 
-// Rows and groups of a call that one block does alone.
-constexpr int kAloneRows = 4096, kAloneGroups = 1024;
+// Rows and groups of a call that one block does alone.  A second launch costs a caller on the host 1.8 us, and in a graph it
+// gives a call's rows all multiprocessors.  Alone against with a second kernel, us in a graph: 128 groups of 4 rows 5.5 and
+// 5.9, 128 of 8 5.7 and 5.8, 128 of 16 7.0 and 6.1, 128 of 32 9.6 and 6.1; 256 of 1 5.8 and 6.0, 256 of 8 7.6 and 5.9, 512 of 1
+// 7.1 and 6.3, 1,024 of 1 11.1 and 6.8; one of 2,048 5.6 and 5.4.  From Python 7.7 to 8.0 and 9.4 to 9.7, but alone 9.7 for
+// 128 of 32 and 11.2 for 1,024 of 1.  So up to where what a graph loses is what the host gains.
+constexpr int kAloneRows = 2048, kAloneGroups = 256;
 
 }  // namespace
 

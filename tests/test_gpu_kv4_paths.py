@@ -433,6 +433,15 @@ def test_reserve_long_requests_that_leave_and_come(groups):
     both_reserve(x, page, sum(counts), inplace=True)
 
 
+@pytest.mark.parametrize("groups,rows", [(256, 2048), (257, 2048), (256, 2049), (1, 2048), (1, 2049), (257, 257)])
+def test_reserve_about_where_a_second_kernel_begins(groups, rows):
+    r = np.random.RandomState(groups + rows)
+    counts = np.bincount(r.randint(0, groups, rows), minlength=groups).tolist()
+    lens = r.randint(-1 if groups > 1 else 0, 99, groups).tolist()
+    both_reserve(reserve_inputs(counts, lens, 16, seed=rows), 16, rows)
+    both_reserve(reserve_inputs(counts, lens, 16, seed=rows, free=rows // 40), 16, rows, inplace=True)
+
+
 def example():
     import importlib.util
     import os
