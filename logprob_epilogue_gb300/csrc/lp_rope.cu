@@ -25,8 +25,10 @@
 //
 // Into a cache in 4 bits the instructions bound it, about 200 per word of keys and
 // values (284 with divided quotients, values as held always formed and four heads per task): 18,846 rows of 8 + 8 heads of
-// 128 lanes take 38.1 us, 4.6 TB/s with the values as held written beside the codes;
-// 512 rows 4.6 us, one row 3.1 us.
+// 128 lanes take 38.1 us, 4.6 TB/s with the values as held written beside the codes,
+// 32.5 without; 512 rows 4.6 us, one row 3.1 us.  A round's own call (32 query heads, norms
+// and rotation, nothing held): 512 rows 5.4 us, 18,846 108 us, 3.85 TB/s, F16 the same; with
+// heads of 64 lanes, F16, 59 us, 3.5 TB/s.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -339,16 +341,23 @@ cudaError_t launch(const RopeParams& p, cudaStream_t stream) {
 // Eight heads per task spread a row's factors further, but leave a short call
 // fewer threads and a long chain of its own: with 128 lanes, 16,411 rows of 48
 // heads take 79 us against 82, 512 rows 5.0 us against 4.4; with 64 lanes 8,191
-// rows of 28 heads take 14.8 us against 13.0.  In 4 bits a task's lanes cost more beside
-// its factors: 18,846 rows of 8 heads of keys take 38.1 us against 40.4, 512 rows 5.9
-// against 4.6.
-constexpr long long kManyHeads = 1 << 18;
+// rows of 28 heads take 14.8 us against 13.0.
+//
+// In 4 bits it is the keys' and values' lanes that cost, and beside queries eight heads
+// do not pay: with 32 query heads over 8, norms and rotation 512 rows take 6.6 us against
+// 5.4, 1,024 8.1 against 8.8, 2,048 14.1 against 14.3, 4,096 26.0 and 26.0, 18,846 109.8 against
+// 108.6.  Without queries, 8 heads of keys, rotated here: 512 rows 6.0 against 4.4, 8,192
+// 20.2 against 19.8, 9,000 21.4 against 21.7, 16,384 37.4 against 38.2, 18,846 42.9 against
+// 43.6; rotated before, values as held written: 4,096 10.7 against 10.1, 18,846 37.1 against
+// 39.4, and without these 32.4 against 36.2.
+constexpr long long kManyHeads = 1 << 18, kManyHeads4 = 72000;
 
 template <bool kBf16>
 cudaError_t pick(const RopeParams& p, int head_dim, cudaStream_t stream) {
     if (head_dim == 64) return launch<kBf16, 64, 4>(p, stream);
-    const long long many = p.k_scales == nullptr ? kManyHeads : kManyHeads / 2;
-    return (long long)p.rows * (p.q_heads + p.kv_heads) >= many ? launch<kBf16, 128, 8>(p, stream) : launch<kBf16, 128, 4>(p, stream);
+    const long long heads = (long long)p.rows * (p.q_heads + p.kv_heads);
+    const bool eight = p.k_scales == nullptr ? heads >= kManyHeads : p.q_heads == 0 && heads >= kManyHeads4;
+    return eight ? launch<kBf16, 128, 8>(p, stream) : launch<kBf16, 128, 4>(p, stream);
 }
 
 }  // namespace

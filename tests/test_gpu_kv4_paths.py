@@ -8,7 +8,7 @@ import pytest
 import attn_ref as R
 import kv4_ref as K
 from test_gpu_attn import EDGES, batch, dev, generator, i32, plan_of, rand, status_word, table
-from test_gpu_kv4 import Case4, both_reserve, four_caches, reserve_inputs
+from test_gpu_kv4 import Case4, append4, both_reserve, four_caches, reserve_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -413,6 +413,12 @@ def test_append4_keys_out_beside_what_is_not_finite(dtype, rope):
     torch.cuda.synchronize()
     assert int(st[0]) == 0 and bool(want.isnan().any())
     assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got[~want.isnan()], want[~want.isnan()])
+
+
+@pytest.mark.parametrize("dtype,hk,n,held", [("bf16", 8, [9001], True), ("f16", 3, [20_000, 1, 4100], False), ("bf16", 9, [8000], True), ("f16", 12, [5999], False)])
+def test_append4_many_keys_without_queries(dtype, hk, n, held):
+    """Eight heads per task and four, at counts of heads that are multiples of neither."""
+    append4(dtype, 128, hk, hk, 64, n, [3] * len(n), held=held, rope=False)
 
 
 @pytest.mark.parametrize("groups", [3, 1200])
