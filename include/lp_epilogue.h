@@ -565,7 +565,8 @@ int lp_kv_append(lp_attn_t plan, const lp_append_io* io, void* stream);
  * of range, more than max_group_rows of them, or tokens past max_pages pages;
  * rows that two entries of group_indptr claim are not written.  A call whose
  * waits ran out (LP_STATUS_TIMEOUT) gives every row of its groups out 0 and
- * lse -inf.
+ * lse -inf.  Scores from 2^24 on in magnitude are out of range in F16: a row that
+ * has one may come out as 0 or NaN.
  * Prefix p serves groups prefix_indptr[p] .. prefix_indptr[p+1]-1 and holds
  * prefix_lens[p] tokens in the pages prefix_tables[p].  Where group_indptr does
  * not ascend (LP_STATUS_BAD_GROUP), it serves those of them whose rows lie in
@@ -693,11 +694,14 @@ typedef struct {
 int lp_kv_append4(lp_attn_t plan, const lp_append4_io* io, void* stream);
 
 /* lp_attend over such a cache: its formula, statuses and zeros, with k and v the
- * values that the cache stands for (any factor > 0).  A page out of range reads
+ * values that the cache stands for (any factor > 0, and scale * k_factor may leave
+ * FP32's range where the queries bring the scores back).  A page out of range reads
  * as zeros.  The products take values and probabilities of 16 bits, in which
  * a code times its scale is exact; BF16 queries are first multiplied by a power
  * of two per row and head that brings their largest lane to [2^14, 2^15) (undone in
- * the scores): a lane under 2^-28 of that largest one loses bits. */
+ * the scores): a lane under 2^-28 of that largest one loses bits.  Scores from
+ * 2^24 on in magnitude are out of range: FP32 numbers as large lie whole powers
+ * of two apart, and a row that has one may come out as 0 or NaN. */
 typedef struct {
     lp_attend_io attend;   /* k_cache, v_cache: the codes */
     const void* k_scales;

@@ -23,11 +23,12 @@
 // sums, results and parts are 32 bits.
 //
 // What bounds it, by size (BF16, heads of 128, 32 over 8, in a CUDA graph):
-// - the workers' instructions: 128 groups of 4 rows at contexts up to 8,192 take 191
-//   us, 3.3 TB/s of codes and scales.  A tile of one fragment takes 1,480 cycles of a
-//   block, 1,200 where the tiles are there already; at the rates of their pipes the
-//   conversions and their products with the scales take 760, and beside them the
-//   products on the tensor core 510.  Twelve workers, with the queries in shared memory, take as long
+// - the workers' latencies, two warps per scheduler, each in turn waiting for its own
+//   conversions and products (issue slots used to 49%, no pipe to more than 35%): 128
+//   groups of 4 rows at contexts up to 8,192 take 191 us, 3.3 TB/s of codes and scales.
+//   A tile of one fragment takes 1,480 cycles of a block, 1,200 where the tiles are
+//   there already; at the rates of their pipes the conversions and their products with
+//   the scales take 760, and beside them the products on the tensor core 510.  Twelve workers, with the queries in shared memory, take as long
 //   (110 us for 19 groups of 16,384 tokens against 109), 32 tokens a step too (109).
 // - fragments: 32 rows of a unit take 192 us for those 19 groups; with D = 64 both share
 //   a worker's conversions, 98 against 70 (124 as two workers').
@@ -36,6 +37,7 @@
 //   lane: 161, 159, 138, 138).
 // - latency: one row at 4,095 tokens takes 14.4 us, the launch, the split and the first
 //   pages 8, a tile or two 2, the join 4.5.
+// A thread spills 12 bytes with D = 64 and 20 with D = 128.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -740,7 +742,11 @@ cudaError_t launch4(const AttendParams& p, cudaStream_t stream) {
 // each, us: 19 groups of 16,384 tokens and 4 rows (16 of a unit) 109 and 191, 8 rows 192
 // and 196, 12 rows 287 and 205, 16 rows 376 and 210; 608 groups of 512 tokens 201 and
 // 314, 341 and 374, 564 and 470, 737 and 621; D = 64, 19 groups: 70 and 146, 98 and 149,
-// 157 and 156, 187 and 159.  So by the rows that a prefix and a group have on average.
+// 157 and 156, 187 and 159.  So by the rows that a prefix and a group have on average,
+// padding and idle groups among them: what a call's sizes say before it runs.  Few large
+// groups among many small ones so take fragments: one of 32 rows at 16,384 tokens beside
+// 127 of one row at 1,024 takes 119 (142 by pairs), at 65,536 tokens 226 (169), eight of
+// them at 16,384 beside 120 take 386 (208).
 int pick_wide(const AttendParams& p) {
     if (p.rows_per_unit == 0) return kWidePrefixes | kWideGroups;
     const long long rows = (long long)p.rows * p.share;

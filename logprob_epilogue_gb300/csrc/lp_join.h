@@ -133,8 +133,9 @@ constexpr int join_bytes(int sub) { return join_round(sub) * kJoinThreads * (D /
 // its own wait for those kernels' end.  Parts and tables of the scratch are the
 // main kernel's own and are read after the wait for it.
 //
-// With heads of 128 the forms of one and two warps per row spill 28 bytes a
-// thread (F16: 36) at the 64 registers that four blocks per SM leave.
+// With heads of 128 the forms of one and two warps per row spill at the 64
+// registers that four blocks per SM leave: 28 bytes a thread (F16: 36), over a
+// cache in 4 bits, two tokens of whose words wait in registers, 80 (148 reloaded).
 template <bool kBf16, int D, int kSub, bool kFour>
 __global__ void __launch_bounds__(kJoinThreads, join_blocks(kSub)) lp_attend_join_kernel(const AttendParams p) {
     using H = Half<kBf16>;

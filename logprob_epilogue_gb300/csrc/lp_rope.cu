@@ -28,7 +28,7 @@
 // 128 lanes take 38.1 us, 4.6 TB/s with the values as held written beside the codes,
 // 32.5 without; 512 rows 4.6 us, one row 3.1 us.  A round's own call (32 query heads, norms
 // and rotation, nothing held): 512 rows 5.4 us, 18,846 108 us, 3.85 TB/s, F16 the same; with
-// heads of 64 lanes, F16, 59 us, 3.5 TB/s.
+// heads of 64 lanes, F16, 59 us, 3.5 TB/s.  A thread spills 28 bytes.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
